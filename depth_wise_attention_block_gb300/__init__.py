@@ -20,6 +20,10 @@ import torch
 
 from . import _native as _N
 from ._native import (  # noqa: F401
+    ATTNRES_ACT_GELU,
+    ATTNRES_ACT_GELU_TANH,
+    ATTNRES_ACT_NONE,
+    ATTNRES_ACT_SILU,
     ATTNRES_BF16,
     ATTNRES_DEFAULT_EPS,
     ATTNRES_DEVERR_WAIT_TIMEOUT,
@@ -36,6 +40,11 @@ __all__ = [
     "attnres_interblock", "attnres_interblock_workspace_size", "attnres_intrablock_step", "attnres_num_sources", "attnres_layer_sources", "attnres_block_step",
     "attnres_layer_step", "attnres_synthetic_layer", "attnres_synthetic_layer_backward", "attnres_fold",
     "attnres_aggregate_fold",
+    "attnres_linear", "attnres_linear_workspace_size", "attnres_linear_backward",
+    "attnres_linear_backward_workspace_size", "attnres_qk_norm_rope", "attnres_qk_norm_rope_backward",
+    "attnres_qk_norm_rope_backward_workspace_size", "attnres_linear_attention",
+    "attnres_linear_attention_workspace_size", "attnres_linear_attention_backward",
+    "attnres_linear_attention_backward_workspace_size", "attnres_linear_attention_step",
     "attnres_version", "AttnResState",
     "attnres_aggregate_host", "attnres_aggregate_host_workspace_size", "dtype_code", "AttnresError",
 ]
@@ -437,3 +446,316 @@ def attnres_aggregate_host(sources_host: Sequence[torch.Tensor] | torch.Tensor, 
         int(chunk_tokens), _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
         _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
     _N.check(rc, "attnres_aggregate_host")
+
+
+# ------------------------------------------------- operators of a layer body --
+
+_ACT = {"none": ATTNRES_ACT_NONE, "gelu": ATTNRES_ACT_GELU, "gelu_tanh": ATTNRES_ACT_GELU_TANH,
+        "silu": ATTNRES_ACT_SILU}
+
+
+def activation_code(activation: str) -> int:
+    try:
+        return _ACT[activation]
+    except KeyError:
+        raise ValueError(f"unknown activation {activation!r}; use one of {sorted(_ACT)}") from None
+
+
+def _rows(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype) -> tuple[int | None, int]:
+    """Pointer and row stride (elements) of a tensor whose rows (everything
+    behind the first dimension) are contiguous; None: (None, row length)."""
+    width = 1
+    for n in shape[1:]:
+        width *= n
+    if t is None:
+        return None, width
+    ptr = _dev_ptr(t, name, dtype, contiguous=False)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.is_contiguous():
+        return ptr, width
+    st, inner = t.stride(), 1
+    for n, s in zip(reversed(shape[1:]), reversed(st[1:])):
+        if n > 1 and s != inner:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        inner *= n
+    if shape[0] > 1 and st[0] < width:
+        raise ValueError(f"the rows of {name} overlap")
+    return ptr, st[0] if shape[0] > 1 else width
+
+
+def _vec(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype) -> int | None:
+    if t is None:
+        return None
+    ptr = _dev_ptr(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return ptr
+
+
+def _workspace(workspace: torch.Tensor | None, nbytes: int, device, stream) -> tuple[torch.Tensor | None, int | None, int]:
+    """The caller's workspace, or one allocated through torch for the stream
+    the call runs on (so that torch does not hand it out again while the
+    kernels use it).  (tensor to keep, pointer, bytes)."""
+    if workspace is None:
+        if nbytes <= 0:
+            return None, None, 0
+        if stream is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        else:
+            s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+            with torch.cuda.stream(s):
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        return workspace, workspace.data_ptr(), nbytes
+    return workspace, _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def _matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-d tensor")
+    return t.shape[0], t.shape[1]
+
+
+def attnres_linear_workspace_size(M: int, N: int, K: int, dtype: torch.dtype) -> int:
+    """Bytes of device workspace with which attnres_linear takes its fastest path for these sizes."""
+    return _N.check(_N.lib.attnres_linear_workspace_size(M, N, K, dtype_code(dtype)), "attnres_linear_workspace_size")
+
+
+def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: torch.Tensor | None = None,
+                   residual: torch.Tensor | None = None, activation: str = "none",
+                   workspace: torch.Tensor | None = None, dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """out = act(x w^T + bias) + residual.
+
+    x: [M, K]; w: [N, K]; out, residual: [M, N], all float32 or all bfloat16
+    (rows contiguous, w wholly); bias: [N] float32; residual may be out
+    itself.  activation: "none", "gelu", "gelu_tanh" or "silu".  workspace:
+    a device buffer of attnres_linear_workspace_size bytes (allocated here
+    through torch when None).
+    """
+    M, K = _matrix(x, "x")
+    N = _matrix(w, "w")[0]
+    dt = x.dtype
+    code = dtype_code(dt)
+    act = activation_code(activation)
+    xp, ldx = _rows(x, "x", (M, K), dt)
+    wp = _vec(w, "w", (N, K), dt)
+    op, ldo = _rows(out, "out", (M, N), dt)
+    rp, ldr = _rows(residual, "residual", (M, N), dt)
+    need = 0 if workspace is not None else attnres_linear_workspace_size(M, N, K, dt)
+    _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
+    rc = _N.lib.attnres_linear(xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32), rp, ldr, op, ldo, M, N, K, code, act,
+                               ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+    _N.check(rc, "attnres_linear")
+
+
+def attnres_linear_backward_workspace_size(M: int, N: int, K: int, dtype: torch.dtype, activation: str = "none") -> int:
+    """Bytes of device workspace attnres_linear_backward needs."""
+    return _N.check(_N.lib.attnres_linear_backward_workspace_size(M, N, K, dtype_code(dtype), activation_code(activation)),
+                    "attnres_linear_backward_workspace_size")
+
+
+def attnres_linear_backward(x: torch.Tensor, w: torch.Tensor, grad_out: torch.Tensor,
+                            grad_x: torch.Tensor | None = None, grad_w: torch.Tensor | None = None,
+                            grad_bias: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                            activation: str = "none", workspace: torch.Tensor | None = None,
+                            dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of attnres_linear with respect to x, w and bias (those not
+    None are overwritten); the residual's gradient is grad_out.  grad_x
+    [M, K], grad_w [N, K] of x's dtype, grad_bias [N] float32."""
+    M, K = _matrix(x, "x")
+    N = _matrix(w, "w")[0]
+    dt = x.dtype
+    code = dtype_code(dt)
+    act = activation_code(activation)
+    xp, ldx = _rows(x, "x", (M, K), dt)
+    wp = _vec(w, "w", (N, K), dt)
+    gp, ldg = _rows(grad_out, "grad_out", (M, N), dt)
+    need = 0 if workspace is not None else attnres_linear_backward_workspace_size(M, N, K, dt, activation)
+    _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
+    rc = _N.lib.attnres_linear_backward(
+        xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32), gp, ldg, _vec(grad_x, "grad_x", (M, K), dt),
+        _vec(grad_w, "grad_w", (N, K), dt), _vec(grad_bias, "grad_bias", (N,), torch.float32), M, N, K, code, act, ws,
+        nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+    _N.check(rc, "attnres_linear_backward")
+
+
+def _heads(t: torch.Tensor | None, name: str) -> tuple[int, int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise ValueError(f"{name} must be [T, heads, channels]")
+    return tuple(t.shape)
+
+
+def _qk_sizes(q, k):
+    """(T, D, dtype, Hq, Hk) of a q and a k, either of them None."""
+    first = q if q is not None else k
+    T, _, D = _heads(first, "q" if q is not None else "k")
+    return T, D, first.dtype, q.shape[1] if q is not None else 0, _heads(k, "k")[1] if k is not None else 0
+
+
+def _rope_args(T: int, positions, inv_freq, interleaved: bool):
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return (_vec(positions, "positions", (T,), torch.int64),
+            _vec(inv_freq, "inv_freq", (rot // 2,), torch.float32), rot, int(bool(interleaved)))
+
+
+def attnres_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
+                         k_out: torch.Tensor | None, q_gain: torch.Tensor | None = None,
+                         k_gain: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                         inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+                         eps: float = ATTNRES_DEFAULT_EPS, stream=None) -> None:
+    """RMSNorm of every head of q [T, Hq, D] and k [T, Hk, D] (either may be
+    None) with gains [D] float32 or None, and rotation of the first
+    2 len(inv_freq) channels by positions [T] int64 times inv_freq float32
+    (both None: no rotation).  Heads and channels contiguous, tokens at any
+    stride; q_out may be q and k_out k."""
+    T, D, dt, Hq, Hk = _qk_sizes(q, k)
+    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt)
+    kp, ks = _rows(k, "k", (T, Hk, D), dt)
+    qo, qos = _rows(q_out if q is not None else None, "q_out", (T, Hq, D), dt)
+    ko, kos = _rows(k_out if k is not None else None, "k_out", (T, Hk, D), dt)
+    rc = _N.lib.attnres_qk_norm_rope(qp, qs, Hq, kp, ks, Hk, T, D, dtype_code(dt), _vec(q_gain, "q_gain", (D,), torch.float32),
+                                     _vec(k_gain, "k_gain", (D,), torch.float32), float(eps), pos, freq, rot, inter,
+                                     qo, qos, ko, kos, _stream_ptr(stream))
+    _N.check(rc, "attnres_qk_norm_rope")
+
+
+def attnres_qk_norm_rope_backward_workspace_size(T: int, Hq: int, Hk: int, D: int) -> int:
+    """Bytes of device workspace the gain gradients of attnres_qk_norm_rope_backward need."""
+    return _N.check(_N.lib.attnres_qk_norm_rope_backward_workspace_size(T, Hq, Hk, D),
+                    "attnres_qk_norm_rope_backward_workspace_size")
+
+
+def attnres_qk_norm_rope_backward(q: torch.Tensor | None, k: torch.Tensor | None, grad_q_out: torch.Tensor | None,
+                                  grad_k_out: torch.Tensor | None, grad_q: torch.Tensor | None,
+                                  grad_k: torch.Tensor | None, q_gain: torch.Tensor | None = None,
+                                  k_gain: torch.Tensor | None = None, grad_q_gain: torch.Tensor | None = None,
+                                  grad_k_gain: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                                  inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+                                  eps: float = ATTNRES_DEFAULT_EPS, workspace: torch.Tensor | None = None,
+                                  stream=None) -> None:
+    """Gradients of attnres_qk_norm_rope, from the forward's inputs (q and k
+    as they were before it).  grad_q may be grad_q_out and grad_k grad_k_out;
+    the gain gradients ([D] float32) are overwritten, or skipped when None."""
+    T, D, dt, Hq, Hk = _qk_sizes(q, k)
+    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt)
+    kp, ks = _rows(k, "k", (T, Hk, D), dt)
+    gqo, gqos = _rows(grad_q_out if q is not None else None, "grad_q_out", (T, Hq, D), dt)
+    gko, gkos = _rows(grad_k_out if k is not None else None, "grad_k_out", (T, Hk, D), dt)
+    gq, gqs = _rows(grad_q if q is not None else None, "grad_q", (T, Hq, D), dt)
+    gk, gks = _rows(grad_k if k is not None else None, "grad_k", (T, Hk, D), dt)
+    dgq = _vec(grad_q_gain, "grad_q_gain", (D,), torch.float32)
+    dgk = _vec(grad_k_gain, "grad_k_gain", (D,), torch.float32)
+    need = 0
+    if workspace is None and (dgq is not None or dgk is not None):
+        need = attnres_qk_norm_rope_backward_workspace_size(T, Hq, Hk, D)
+    _keep, ws, nbytes = _workspace(workspace, need, (q if q is not None else k).device, stream)
+    rc = _N.lib.attnres_qk_norm_rope_backward(
+        qp, qs, Hq, kp, ks, Hk, T, D, dtype_code(dt), _vec(q_gain, "q_gain", (D,), torch.float32),
+        _vec(k_gain, "k_gain", (D,), torch.float32), float(eps), pos, freq, rot, inter, gqo, gqos, gko, gkos, gq, gqs,
+        gk, gks, dgq, dgk, ws, nbytes, _stream_ptr(stream))
+    _N.check(rc, "attnres_qk_norm_rope_backward")
+
+
+def _attention_args(q, k, v, log_decay, cu_seqlens):
+    T, H, Dk = _heads(q, "q")
+    Dv = _heads(v, "v")[2]
+    dt = q.dtype
+    qp, qs = _rows(q, "q", (T, H, Dk), dt)
+    kp, ks = _rows(k, "k", (T, H, Dk), dt)
+    vp, vs = _rows(v, "v", (T, H, Dv), dt)
+    if isinstance(log_decay, torch.Tensor) and log_decay.requires_grad:
+        raise ValueError("log_decay is a constant: it gets no gradient")
+    g = _vec(log_decay, "log_decay", (H,), torch.float32)
+    N = 1
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        if N < 1:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+    cu = _vec(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
+    return T, H, Dk, Dv, dt, (qp, qs, kp, ks, vp, vs, T, H, Dk, Dv, dtype_code(dt), g), cu, N
+
+
+def attnres_linear_attention_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: torch.dtype, num_seqs: int = 1) -> int:
+    """Bytes of device workspace attnres_linear_attention needs (0: none)."""
+    return _N.check(_N.lib.attnres_linear_attention_workspace_size(T, H, Dk, Dv, dtype_code(dtype), num_seqs),
+                    "attnres_linear_attention_workspace_size")
+
+
+def attnres_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                             out: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                             initial_state: torch.Tensor | None = None, final_state: torch.Tensor | None = None,
+                             scale: float | None = None, workspace: torch.Tensor | None = None,
+                             dev_err: torch.Tensor | None = None, stream=None) -> None:
+    """Causal linear attention over prompts, S_t = e^log_decay S_{t-1} + k_t v_t^T,
+    out_t = scale q_t S_t (scale None: 1/sqrt(Dk)).
+
+    q, k: [T, H, Dk]; v, out: [T, H, Dv], float32 or bfloat16, tokens at any
+    stride; log_decay: [H] float32; cu_seqlens: [num_seqs + 1] int32 on the
+    device (None: one sequence); initial_state, final_state: [num_seqs, H,
+    Dk, Dv] float32 or None, possibly the same tensor.
+    """
+    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens)
+    op, os_ = _rows(out, "out", (T, H, Dv), dt)
+    shape = (N, H, Dk, Dv)
+    s0 = _vec(initial_state, "initial_state", shape, torch.float32)
+    s1 = _vec(final_state, "final_state", shape, torch.float32)
+    need = 0 if workspace is not None else attnres_linear_attention_workspace_size(T, H, Dk, Dv, dt, N)
+    _keep, ws, nbytes = _workspace(workspace, need, q.device, stream)
+    rc = _N.lib.attnres_linear_attention(*head, cu, N, s0, s1, float(Dk ** -0.5 if scale is None else scale), op, os_,
+                                         ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+    _N.check(rc, "attnres_linear_attention")
+
+
+def attnres_linear_attention_backward_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: torch.dtype,
+                                                     num_seqs: int = 1) -> int:
+    """Bytes of device workspace attnres_linear_attention_backward needs (0: none)."""
+    return _N.check(_N.lib.attnres_linear_attention_backward_workspace_size(T, H, Dk, Dv, dtype_code(dtype), num_seqs),
+                    "attnres_linear_attention_backward_workspace_size")
+
+
+def attnres_linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                                      grad_out: torch.Tensor, grad_q: torch.Tensor, grad_k: torch.Tensor,
+                                      grad_v: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                                      initial_state: torch.Tensor | None = None,
+                                      grad_final_state: torch.Tensor | None = None,
+                                      grad_initial_state: torch.Tensor | None = None, scale: float | None = None,
+                                      workspace: torch.Tensor | None = None, dev_err: torch.Tensor | None = None,
+                                      stream=None) -> None:
+    """Gradients of attnres_linear_attention from the forward's inputs
+    (grad_q, grad_k, grad_v contiguous, of q's dtype; the states' float32)."""
+    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens)
+    gp, gs = _rows(grad_out, "grad_out", (T, H, Dv), dt)
+    shape = (N, H, Dk, Dv)
+    s0 = _vec(initial_state, "initial_state", shape, torch.float32)
+    ds1 = _vec(grad_final_state, "grad_final_state", shape, torch.float32)
+    ds0 = _vec(grad_initial_state, "grad_initial_state", shape, torch.float32)
+    need = 0 if workspace is not None else attnres_linear_attention_backward_workspace_size(T, H, Dk, Dv, dt, N)
+    _keep, ws, nbytes = _workspace(workspace, need, q.device, stream)
+    rc = _N.lib.attnres_linear_attention_backward(
+        *head, cu, N, s0, float(Dk ** -0.5 if scale is None else scale), gp, gs, ds1, _vec(grad_q, "grad_q", (T, H, Dk), dt),
+        _vec(grad_k, "grad_k", (T, H, Dk), dt), _vec(grad_v, "grad_v", (T, H, Dv), dt), ds0, ws, nbytes,
+        _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+    _N.check(rc, "attnres_linear_attention_backward")
+
+
+def attnres_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                                  state: torch.Tensor, out: torch.Tensor, slots: torch.Tensor | None = None,
+                                  scale: float | None = None, stream=None) -> None:
+    """One token per row: state [num_slots, H, Dk, Dv] float32 of slot
+    slots[b] (int32; None: b) updated in place, out [B, H, Dv] written.  A
+    slot outside the pool marks a padding row (its out row stays); rows of
+    one slot are consecutive tokens in row order."""
+    B, H, Dk, Dv, dt, head, _, _ = _attention_args(q, k, v, log_decay, None)
+    op, os_ = _rows(out, "out", (B, H, Dv), dt)
+    if not isinstance(state, torch.Tensor) or state.dim() != 4:
+        raise ValueError("state must be [num_slots, H, Dk, Dv]")
+    num_slots = state.shape[0]
+    sp = _vec(state, "state", (num_slots, H, Dk, Dv), torch.float32)
+    rc = _N.lib.attnres_linear_attention_step(*head, sp, num_slots, _vec(slots, "slots", (B,), torch.int32),
+                                              float(Dk ** -0.5 if scale is None else scale), op, os_,
+                                              _stream_ptr(stream))
+    _N.check(rc, "attnres_linear_attention_step")

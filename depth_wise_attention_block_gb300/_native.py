@@ -28,6 +28,11 @@ ATTNRES_MAX_BLOCKS = ATTNRES_MAX_SOURCES - 1
 ATTNRES_DEFAULT_EPS = 1e-5
 ATTNRES_STATE_EARLY_LOADS = 0x1
 
+ATTNRES_ACT_NONE = 0
+ATTNRES_ACT_GELU = 1
+ATTNRES_ACT_GELU_TANH = 2
+ATTNRES_ACT_SILU = 3
+
 # every function declared in include/attnres.h
 EXPORTED = (
     "attnres_aggregate",
@@ -50,6 +55,18 @@ EXPORTED = (
     "attnres_synthetic_layer",
     "attnres_synthetic_layer_backward",
     "attnres_fold",
+    "attnres_linear",
+    "attnres_linear_workspace_size",
+    "attnres_linear_backward",
+    "attnres_linear_backward_workspace_size",
+    "attnres_qk_norm_rope",
+    "attnres_qk_norm_rope_backward",
+    "attnres_qk_norm_rope_backward_workspace_size",
+    "attnres_linear_attention",
+    "attnres_linear_attention_workspace_size",
+    "attnres_linear_attention_backward",
+    "attnres_linear_attention_backward_workspace_size",
+    "attnres_linear_attention_step",
     "attnres_debug_wait_test",
     "attnres_status_string",
     "attnres_last_error",
@@ -108,6 +125,24 @@ def _load() -> ctypes.CDLL:
         "attnres_synthetic_layer": (i32, [vp, vp, vp, vp, i64, i32, i32, vp]),
         "attnres_synthetic_layer_backward": (i32, [vp, vp, vp, vp, vp, vp, i64, i32, i32, vp]),
         "attnres_fold": (i32, [vp, vp, vp, i64, i32, i32, vp]),
+        "attnres_linear": (i32, [vp, i64, vp, vp, vp, i64, vp, i64, i64, i32, i32, i32, i32, vp, i64, vp, vp]),
+        "attnres_linear_workspace_size": (i64, [i64, i32, i32, i32]),
+        "attnres_linear_backward": (i32, [vp, i64, vp, vp, vp, i64, vp, vp, vp, i64, i32, i32, i32, i32, vp, i64, vp,
+                                          vp]),
+        "attnres_linear_backward_workspace_size": (i64, [i64, i32, i32, i32, i32]),
+        "attnres_qk_norm_rope": (i32, [vp, i64, i32, vp, i64, i32, i64, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp,
+                                       i64, vp, i64, vp]),
+        "attnres_qk_norm_rope_backward": (i32, [vp, i64, i32, vp, i64, i32, i64, i32, i32, vp, vp, f32, vp, vp, i32,
+                                                i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
+        "attnres_qk_norm_rope_backward_workspace_size": (i64, [i64, i32, i32, i32]),
+        "attnres_linear_attention": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, i32, vp, vp, i32, vp, vp,
+                                           f32, vp, i64, vp, i64, vp, vp]),
+        "attnres_linear_attention_workspace_size": (i64, [i64, i32, i32, i32, i32, i32]),
+        "attnres_linear_attention_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, i32, i32, vp, vp, i32,
+                                                    vp, f32, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp, vp]),
+        "attnres_linear_attention_backward_workspace_size": (i64, [i64, i32, i32, i32, i32, i32]),
+        "attnres_linear_attention_step": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, vp, i32, vp,
+                                                f32, vp, i64, vp]),
         "attnres_debug_wait_test": (i32, [ctypes.c_uint64, i32]),
         "attnres_status_string": (ctypes.c_char_p, [i32]),
         "attnres_last_error": (ctypes.c_char_p, []),

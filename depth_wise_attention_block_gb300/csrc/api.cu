@@ -13,14 +13,14 @@
 #include <cmath>
 #include <string>
 
-#include "attnres.h"
+#include "api_common.h"
 #include "launch.h"
 
 using namespace attnres;
 
-namespace {
+namespace attnres {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 int fail(int code, const char* fmt, ...) {
   char buf[512];
@@ -41,13 +41,9 @@ int cuda_fail(cudaError_t e, const char* what) {
   return fail(ATTNRES_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
 
-bool valid_dtype(int dt) { return dt == ATTNRES_F32 || dt == ATTNRES_BF16; }
+}  // namespace attnres
 
-// Whether the byte ranges [a, a + na) and [b, b + nb) share a byte.
-bool overlaps(const void* a, int64_t na, const void* b, int64_t nb) {
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return na > 0 && nb > 0 && pa < pb + (uintptr_t)nb && pb < pa + (uintptr_t)na;
-}
+namespace {
 
 // The output r (and the weights) must not share memory with any source.
 int check_outputs_apart(const void* const* sources, int S, int64_t src_bytes, const void* out_r, int64_t r_bytes,
@@ -131,9 +127,6 @@ int check_state(const attnres_state* st) {
 
 constexpr int kMaxHostSlots = 8;  // more than 3 slots gains nothing; bounds the events made per call
 
-int64_t align256(int64_t x) { return (x + 255) & ~int64_t(255); }
-int64_t dtype_bytes(int dt) { return dt == ATTNRES_BF16 ? 2 : 4; }
-
 // Workspace: the query (d fp32), then per slot the [S, n, d] sources of a
 // chunk of n <= chunk_tokens tokens, its r and (optionally) its weights.
 struct HostLayout {
@@ -185,7 +178,7 @@ struct HostPipe {
 
 extern "C" {
 
-int attnres_version(void) { return (2 << 16) | 0; }
+int attnres_version(void) { return (2 << 16) | 1; }
 
 const char* attnres_status_string(int status) {
   switch (status) {

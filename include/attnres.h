@@ -482,6 +482,223 @@ int attnres_synthetic_layer_backward(const void* x, const float* g, const float*
 int attnres_fold(const void* prev, const void* F, void* dst, int64_t T, int d, int dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Operators of a layer body.  Between two aggregations a layer maps r_l to
+ * its output v_l; the calls below are what such a body is made of: the
+ * projections around it (attnres_linear), the norm and rotation of its heads
+ * (attnres_qk_norm_rope) and a token mixer with a state of fixed size
+ * (attnres_linear_attention).  The pages leave the body open; the formulas
+ * here define the operations.
+ *
+ * Row strides (ld*, *_stride) are in elements between consecutive rows
+ * (tokens) of a tensor whose rows are otherwise contiguous: slices of one
+ * wider buffer can be passed as they are.  A row stride is at least the
+ * row's length.
+ * ---------------------------------------------------------------------- */
+
+/* activations of attnres_linear */
+typedef enum {
+  ATTNRES_ACT_NONE = 0,
+  ATTNRES_ACT_GELU = 1,      /* z Phi(z), Phi the normal distribution function */
+  ATTNRES_ACT_GELU_TANH = 2, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  ATTNRES_ACT_SILU = 3       /* z / (1 + exp(-z)) */
+} attnres_activation;
+
+/* ------------------------------------------------------------------------
+ * attnres_linear -- matrix product with bias, activation and residual in
+ * its epilogue:
+ *   z[m,n] = sum_k x[m,k] w[n,k] + bias[n]     (fp32 accumulate)
+ *   out[m,n] = round(act(z[m,n]) + residual[m,n])
+ * x         device [M, K] of dtype, row stride ldx
+ * w         device [N, K] of dtype, contiguous
+ * bias      device [N] fp32 or NULL
+ * residual  device [M, N] of dtype, row stride ldr, or NULL; it may be out
+ *           itself (with ldr = ldo)
+ * out       device [M, N] of dtype, row stride ldo
+ * M >= 0 (0 launches nothing and accepts NULL buffers), N, K >= 1
+ * act       one of attnres_activation
+ * workspace NULL, or device scratch of workspace_bytes, 256-byte aligned,
+ *           sharing no memory with an operand (its contents on entry do not
+ *           matter).  With attnres_linear_workspace_size(...) bytes every
+ *           size and alignment runs on the tensor cores (tcgen05); without
+ *           it, bf16 operands whose rows start on 16-byte boundaries do, and
+ *           others run on the CUDA cores.  fp32 operands enter the tensor
+ *           cores as three bf16 terms each, whose six leading products keep
+ *           fp32 precision (an infinite operand gives NaN there).
+ * No output may share memory with an input (but residual, as above).
+ * Calls that overlap in time need a workspace each.
+ * ---------------------------------------------------------------------- */
+int attnres_linear(const void* x, int64_t ldx, const void* w, const float* bias, const void* residual, int64_t ldr,
+                   void* out, int64_t ldo, int64_t M, int N, int K, int dtype, int act, void* workspace,
+                   int64_t workspace_bytes, int* dev_err, void* stream);
+
+/* Bytes of workspace with which attnres_linear takes its fastest path for
+ * these sizes on the current device, whatever the operands' alignment and
+ * row strides.  Negative attnres_status on bad arguments. */
+int64_t attnres_linear_workspace_size(int64_t M, int N, int K, int dtype);
+
+/* ------------------------------------------------------------------------
+ * attnres_linear_backward -- gradients of attnres_linear, nothing kept from
+ * the forward (z is recomputed where the activation needs it):
+ *   dz = grad_out * act'(z)      (grad_out itself without an activation)
+ *   grad_x[m,k] = sum_n dz[m,n] w[n,k]
+ *   grad_w[n,k] = sum_m dz[m,n] x[m,k]
+ *   grad_bias[n] = sum_m dz[m,n]
+ * The residual's gradient is grad_out.
+ * x, w, bias, act, sizes  as in attnres_linear (bias is only read with an
+ *             activation)
+ * grad_out    device [M, N] of dtype, row stride ldg
+ * grad_x      device [M, K] of dtype, contiguous, or NULL to skip
+ * grad_w      device [N, K] of dtype, contiguous, or NULL
+ * grad_bias   device [N] fp32, or NULL
+ * workspace   device scratch of at least
+ *             attnres_linear_backward_workspace_size(...) bytes, 256-byte
+ *             aligned (required)
+ * All outputs are overwritten, with sums in a fixed order (bit-reproducible);
+ * with bf16 tensors the products grad_x and grad_w take dz rounded to bf16
+ * (grad_bias sums it in fp32).  M = 0 zeroes grad_w and grad_bias.
+ * ---------------------------------------------------------------------- */
+int attnres_linear_backward(const void* x, int64_t ldx, const void* w, const float* bias, const void* grad_out,
+                            int64_t ldg, void* grad_x, void* grad_w, float* grad_bias, int64_t M, int N, int K,
+                            int dtype, int act, void* workspace, int64_t workspace_bytes, int* dev_err,
+                            void* stream);
+
+/* Bytes of workspace attnres_linear_backward needs.  Negative
+ * attnres_status on bad arguments. */
+int64_t attnres_linear_backward_workspace_size(int64_t M, int N, int K, int dtype, int act);
+
+/* ------------------------------------------------------------------------
+ * attnres_qk_norm_rope -- RMSNorm of every head of q and k and rotation by
+ * position, in one launch.  Per token t and head row x of D channels:
+ *   y = gain * x / sqrt(mean_c x_c^2 + eps)
+ *   pair i of the first `rot` channels, (a, b) = (y_i, y_{i + rot/2}), or
+ *   (y_{2i}, y_{2i+1}) when interleaved, turns by p = positions[t] inv_freq[i]:
+ *   out_a = a cos p - b sin p,  out_b = b cos p + a sin p;
+ *   channels rot .. D-1 stay.
+ * q           device [T, Hq, D] of dtype, token stride q_stride; NULL if Hq = 0
+ * k           device [T, Hk, D] of dtype, token stride k_stride; NULL if Hk = 0
+ * q_gain, k_gain  device [D] fp32 or NULL (no gain)
+ * positions   device [T] int64 (NULL allowed when rot = 0).  The angle is
+ *             reduced before it is rounded to fp32: far positions keep the
+ *             precision of near ones.
+ * inv_freq    device [rot / 2] fp32 (NULL allowed when rot = 0)
+ * rot         even, 0 .. D
+ * q_out, k_out  device [T, H, D] of dtype with their own token strides; each
+ *             may be its input itself (same stride), and may share no other
+ *             memory with an input or output
+ * T >= 0 (0 launches nothing), D 1..1024, Hq + Hk >= 1.
+ * ---------------------------------------------------------------------- */
+int attnres_qk_norm_rope(const void* q, int64_t q_stride, int Hq, const void* k, int64_t k_stride, int Hk, int64_t T,
+                         int D, int dtype, const float* q_gain, const float* k_gain, float eps,
+                         const int64_t* positions, const float* inv_freq, int rot, int interleaved, void* q_out,
+                         int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attnres_qk_norm_rope_backward -- its gradients, from the forward's inputs.
+ * With dy the incoming gradient turned back, h = x / rho and n = gain * dy:
+ *   grad_x = (n - h mean_c(n_c h_c)) / rho,   grad_gain[c] = sum_{t,heads} dy_c h_c
+ * grad_q_out, grad_k_out  device [T, H, D] of dtype, token strides given
+ * grad_q, grad_k          device [T, H, D] of dtype, token strides given
+ *             (each may be the incoming gradient itself, same stride)
+ * grad_q_gain, grad_k_gain  device [D] fp32, overwritten, or NULL to skip;
+ *             summed in a fixed order (bit-reproducible)
+ * workspace   device scratch, 4-byte aligned, of at least
+ *             attnres_qk_norm_rope_backward_workspace_size(T, Hq, Hk, D)
+ *             bytes; may be NULL when neither gain gradient is wanted
+ * T = 0 only zeroes the gain gradients.
+ * ---------------------------------------------------------------------- */
+int attnres_qk_norm_rope_backward(const void* q, int64_t q_stride, int Hq, const void* k, int64_t k_stride, int Hk,
+                                  int64_t T, int D, int dtype, const float* q_gain, const float* k_gain, float eps,
+                                  const int64_t* positions, const float* inv_freq, int rot, int interleaved,
+                                  const void* grad_q_out, int64_t gqo_stride, const void* grad_k_out,
+                                  int64_t gko_stride, void* grad_q, int64_t gq_stride, void* grad_k,
+                                  int64_t gk_stride, float* grad_q_gain, float* grad_k_gain, void* workspace,
+                                  int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the gain gradients need on the current device. */
+int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, int D);
+
+/* ------------------------------------------------------------------------
+ * attnres_linear_attention -- causal linear attention with one decay per
+ * head, over prompts.  Each of num_seqs sequences and H heads keeps a state
+ * S [Dk, Dv], decayed by exp(log_decay[h]) before every token:
+ *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    out_t = scale q_t S_t
+ * q, k        device [T, H, Dk] of dtype, token strides given
+ * v           device [T, H, Dv] of dtype, token stride given
+ * log_decay   device [H] fp32, <= 0 (a constant of the head: it gets no
+ *             gradient)
+ * cu_seqlens  device [num_seqs + 1] int32, non-decreasing, 0 <= .. <= T:
+ *             sequence n is rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 (it may
+ *             be empty).  Rows outside every sequence are left as they are.
+ *             Values outside 0..T are clamped.  NULL: one sequence of T rows
+ *             (num_seqs = 1).
+ * initial_state device [num_seqs, H, Dk, Dv] fp32 or NULL (zero)
+ * final_state device [num_seqs, H, Dk, Dv] fp32 or NULL; it may be
+ *             initial_state itself
+ * scale       finite; 1/sqrt(Dk) is usual
+ * out         device [T, H, Dv] of dtype, token stride given
+ * workspace   device scratch of at least
+ *             attnres_linear_attention_workspace_size(...) bytes, 256-byte
+ *             aligned (NULL when that is 0)
+ * T >= 0, H 1..65535, Dk, Dv 1..256, num_seqs 1..65535 (ATTNRES_ERANGE
+ * above).  The state is held in fp32.  bf16 tensors with Dk and Dv of 64 or
+ * 128, 16-byte aligned rows, run in chunks of 128 tokens on the tensor cores
+ * (tcgen05): scores and states enter those products rounded to bf16, the
+ * state's own sums keep fp32 precision.  Other shapes run on the CUDA cores
+ * in fp32.
+ * ---------------------------------------------------------------------- */
+int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                             int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype, const float* log_decay,
+                             const int32_t* cu_seqlens, int num_seqs, const float* initial_state, float* final_state,
+                             float scale, void* out, int64_t out_stride, void* workspace, int64_t workspace_bytes,
+                             int* dev_err, void* stream);
+
+/* Bytes of workspace attnres_linear_attention needs (0: none). */
+int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs);
+
+/* ------------------------------------------------------------------------
+ * attnres_linear_attention_backward -- its gradients, from the forward's
+ * inputs (nothing is kept).  With R_t the gradient at S_t,
+ *   R_t = scale q_t do_t^T + exp(log_decay) R_{t+1}
+ *   (R of the last token: scale q do^T + grad_final_state)
+ *   grad_q_t = scale S_t do_t,  grad_k_t = R_t v_t,  grad_v_t = R_t^T k_t,
+ *   grad_initial_state = exp(log_decay) R_{first}
+ *   (grad_final_state itself for an empty sequence).
+ * grad_out    device [T, H, Dv] of dtype, token stride given
+ * grad_q, grad_k, grad_v  device, contiguous [T, H, D] of dtype; rows outside
+ *             every sequence are left as they are
+ * grad_final_state    device [num_seqs, H, Dk, Dv] fp32 or NULL (zero)
+ * grad_initial_state  the same shape or NULL; it may be grad_final_state
+ * Other arguments as in attnres_linear_attention; workspace of at least
+ * attnres_linear_attention_backward_workspace_size(...) bytes.
+ * ---------------------------------------------------------------------- */
+int attnres_linear_attention_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                      int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype,
+                                      const float* log_decay, const int32_t* cu_seqlens, int num_seqs,
+                                      const float* initial_state, float scale, const void* grad_out,
+                                      int64_t grad_out_stride, const float* grad_final_state, void* grad_q,
+                                      void* grad_k, void* grad_v, float* grad_initial_state, void* workspace,
+                                      int64_t workspace_bytes, int* dev_err, void* stream);
+
+int64_t attnres_linear_attention_backward_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs);
+
+/* ------------------------------------------------------------------------
+ * attnres_linear_attention_step -- the recurrent form for decoding: row b of
+ * the batch is one token of the sequence whose state lies in slot slots[b].
+ * q, k        device [B, H, Dk] of dtype, row strides given
+ * v, out      device [B, H, Dv] of dtype, row strides given
+ * state       device [num_slots, H, Dk, Dv] fp32, updated in place
+ * slots       device [B] int32, or NULL (row b in slot b, B <= num_slots).
+ *             A row whose slot is outside 0..num_slots-1 is padding: its out
+ *             row is left as it is.  Rows that name the same slot are
+ *             consecutive tokens of that sequence, in the order of the rows.
+ * B 0..65535 (0 launches nothing); Dk, Dv, H, log_decay, scale as above.
+ * ---------------------------------------------------------------------- */
+int attnres_linear_attention_step(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, int B, int H, int Dk, int Dv, int dtype, const float* log_decay,
+                                  float* state, int num_slots, const int32_t* slots, float scale, void* out,
+                                  int64_t out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
  * attnres_debug_wait_test -- a diagnostic with no counterpart in the pages:
  * makes the bounded waits of the ring kernels launched afterwards from this
  * process run out on a healthy GPU, so that their timeout path can be tested
