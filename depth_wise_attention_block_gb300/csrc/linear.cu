@@ -11,6 +11,7 @@
 #include "device_common.cuh"
 #include "launch.h"
 #include "linear_epilogue.cuh"
+#include "linear_tc.h"
 
 namespace attnres {
 
@@ -144,8 +145,7 @@ __global__ void __launch_bounds__(256) rowsum_kernel(const float* part, int rows
 
 int64_t align_up(int64_t x) { return (x + 255) & ~int64_t(255); }
 
-template <typename T>
-cudaError_t linear_any(const LinearArgs& a) {
+LinearEpilogue forward_epilogue(const LinearArgs& a) {
   LinearEpilogue epi{};
   epi.bias = a.bias;
   epi.res = a.residual;
@@ -153,53 +153,78 @@ cudaError_t linear_any(const LinearArgs& a) {
   epi.out = a.out;
   epi.ldo = a.ldo;
   epi.act = a.act;
-  return launch_any<T, true, true, kEpiForward>(static_cast<const T*>(a.x), a.ldx, 1, static_cast<const T*>(a.w), a.K, 1,
-                                                a.M, a.N, a.K, epi, a.stream);
+  return epi;
 }
 
-// Workspace of the backward: dz [M, N] (with an activation), then the
-// partial rows of the bias gradient (one per 32 tokens at most).
+template <typename T>
+cudaError_t linear_any(const LinearArgs& a) {
+  return launch_any<T, true, true, kEpiForward>(static_cast<const T*>(a.x), a.ldx, 1, static_cast<const T*>(a.w), a.K, 1,
+                                                a.M, a.N, a.K, forward_epilogue(a), a.stream);
+}
+
+// Workspace of the backward: dz [M, N rounded up to 8] (with an activation),
+// the partial rows of the bias gradient, and the operands' copies for the
+// tensor cores.
+int64_t dz_pitch(int N) { return ((int64_t)N + 7) / 8 * 8; }
 struct BwdLayout {
-  int64_t dz, part, total;
+  int64_t dz, part, x, w, g, total;
 };
-BwdLayout bwd_layout(int64_t M, int N, int dtype, int act) {
+BwdLayout bwd_layout(int64_t M, int N, int K, int dtype, int act) {
+  const bool bf16 = dtype == ATTNRES_BF16;
+  const int np = bf16 ? 1 : 3;
   BwdLayout L;
-  L.dz = act != ATTNRES_ACT_NONE ? align_up(M * N * (dtype == ATTNRES_BF16 ? 2 : 4)) : 0;
-  L.part = align_up((M + 31) / 32 * N * 4);
-  L.total = L.dz + L.part;
+  L.dz = act != ATTNRES_ACT_NONE ? align_up(M * dz_pitch(N) * (bf16 ? 2 : 4)) : 0;
+  // rows of 64 tokens (CUDA cores, column sums), of 32 (wide tiles), or the
+  // clusters' of few tokens (at most 2 tiles x 8 ranks x 2)
+  int64_t rows = (M + 127) / 128 * 4;
+  if (M <= 256 && rows < 32) rows = 32;
+  L.part = align_up(rows * N * 4);
+  L.x = !bf16 || K % 8 ? tc_prep_bytes(M, K, np) : 0;
+  L.w = !bf16 || K % 8 ? tc_prep_bytes(N, K, np) : 0;
+  L.g = !bf16 || (act == ATTNRES_ACT_NONE && N % 8) ? tc_prep_bytes(M, N, np) : 0;
+  L.total = L.dz + L.part + L.x + L.w + L.g;
   return L;
+}
+
+template <typename T>
+cudaError_t launch_colsum(const T* g, const LinearBwdArgs& a, float* part) {
+  const int64_t tiles = (a.M + kGT - 1) / kGT;
+  return launch_kernel(colsum_kernel<T>, dim3((a.N + 31) / 32, (unsigned)(tiles < 65535 ? tiles : 65535)), dim3(256), 0, a.stream, g,
+                       (long long)a.ldg, (int)a.M, a.N, part);
+}
+
+cudaError_t launch_rowsum(const float* part, int rows, const LinearBwdArgs& a) {
+  return launch_kernel(rowsum_kernel, dim3((a.N + 31) / 32), dim3(256), 0, a.stream, part, rows, a.N, a.grad_bias);
 }
 
 template <typename T>
 cudaError_t linear_backward_any(const LinearBwdArgs& a) {
   const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.w), *g = static_cast<const T*>(a.grad_out);
-  const BwdLayout L = bwd_layout(a.M, a.N, a.dtype, a.act);
+  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act);
   char* ws = static_cast<char*>(a.workspace);
   float* part = reinterpret_cast<float*>(ws + L.dz);
   const T* dz = g;
   long long ldz = a.ldg;
   cudaError_t e;
-  const int tiles = (int)((a.M + kGT - 1) / kGT);
   if (a.act != ATTNRES_ACT_NONE) {
     LinearEpilogue epi{};
     epi.bias = a.bias;
     epi.res = a.grad_out;
     epi.ldr = a.ldg;
     epi.out = ws;
-    epi.ldo = a.N;
+    epi.ldo = dz_pitch(a.N);
     epi.act = a.act;
     epi.part = a.grad_bias ? part : nullptr;
     e = launch_any<T, true, true, kEpiDz>(x, a.ldx, 1, w, a.K, 1, a.M, a.N, a.K, epi, a.stream);
     if (e != cudaSuccess) return e;
     dz = reinterpret_cast<const T*>(ws);
-    ldz = a.N;
+    ldz = dz_pitch(a.N);
   } else if (a.grad_bias) {
-    e = launch_kernel(colsum_kernel<T>, dim3((a.N + 31) / 32, tiles < 65535 ? tiles : 65535), dim3(256), 0, a.stream, g,
-                      (long long)a.ldg, (int)a.M, a.N, part);
+    e = launch_colsum(g, a, part);
     if (e != cudaSuccess) return e;
   }
   if (a.grad_bias) {
-    e = launch_kernel(rowsum_kernel, dim3((a.N + 31) / 32), dim3(256), 0, a.stream, (const float*)part, tiles, a.N, a.grad_bias);
+    e = launch_rowsum(part, (int)((a.M + kGT - 1) / kGT), a);
     if (e != cudaSuccess) return e;
   }
   if (a.grad_x) {
@@ -219,19 +244,129 @@ cudaError_t linear_backward_any(const LinearBwdArgs& a) {
   return cudaSuccess;
 }
 
+// fp32 products below this many multiply-adds stay on the CUDA cores: the
+// tensor cores need one more launch, which splits the operands.
+constexpr int64_t kSmallFp32 = int64_t(1) << 24;
+
+bool small_fp32(int64_t M, int N, int K, int dtype) { return dtype == ATTNRES_F32 && M * N < kSmallFp32 / K; }
+
+// Takes the next `bytes` of the workspace, or null where they do not fit.
+struct Arena {
+  char* at;
+  int64_t left;
+  void* take(int64_t bytes) {
+    if (bytes > left) return nullptr;
+    void* r = at;
+    at += bytes;
+    left -= bytes;
+    return r;
+  }
+};
+
+// On the tensor cores; *done says whether the workspace sufficed.
+cudaError_t linear_tc(const LinearArgs& a, bool* done) {
+  const bool bf16 = a.dtype == ATTNRES_BF16;
+  const int np = bf16 ? 1 : 3;
+  TcOperand op[2] = {{a.x, a.ldx, a.M, a.K, false, nullptr}, {a.w, a.K, a.N, a.K, false, nullptr}};
+  Arena ws{static_cast<char*>(a.workspace), a.workspace_bytes};
+  TcOperand prep[2];
+  int nprep = 0;
+  *done = false;
+  for (TcOperand& o : op) {
+    if (bf16 && tc_rows_ok(o.ptr, o.ld)) continue;
+    o.prep = ws.take(tc_prep_bytes(o.rows, o.cols, np));
+    if (!o.prep) return cudaSuccess;
+    prep[nprep++] = o;
+  }
+  *done = true;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e == cudaSuccess && nprep) e = launch_tc_prep(prep, nprep, np, a.stream);
+  if (e != cudaSuccess) return e;
+  return launch_tc_gemm(tc_plan(a.M, a.N, a.K, np, di.sm_count), op[0], op[1], a.M, a.N, a.K, np, kEpiForward,
+                        forward_epilogue(a), a.dev_err, a.stream);
+}
+
+cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
+  const bool bf16 = a.dtype == ATTNRES_BF16, act = a.act != ATTNRES_ACT_NONE;
+  const int np = bf16 ? 1 : 3;
+  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act);
+  Arena ws{static_cast<char*>(a.workspace), a.workspace_bytes};
+  void* dz_buf = L.dz ? ws.take(L.dz) : nullptr;
+  float* part = static_cast<float*>(ws.take(L.part));
+  TcOperand x{a.x, a.ldx, a.M, a.K, false, nullptr}, w{a.w, a.K, a.N, a.K, false, nullptr};
+  TcOperand dz{act ? dz_buf : a.grad_out, act ? dz_pitch(a.N) : a.ldg, a.M, a.N, false, nullptr};
+  const bool use_x = act || a.grad_w, use_w = act || a.grad_x, use_dz = a.grad_x || a.grad_w;
+  TcOperand prep[3];
+  int nprep = 0;
+  *done = false;
+  for (TcOperand* o : {&x, &w, &dz}) {
+    if (!(o == &x ? use_x : o == &w ? use_w : use_dz) || (bf16 && tc_rows_ok(o->ptr, o->ld))) continue;
+    o->prep = ws.take(tc_prep_bytes(o->rows, o->cols, np));
+    if (!o->prep) return cudaSuccess;
+    if (o != &dz || !act) prep[nprep++] = *o;  // dz's copy comes after dz
+  }
+  *done = true;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  for (int i = 0; i < nprep && e == cudaSuccess; i += 2) e = launch_tc_prep(prep + i, nprep - i < 2 ? 1 : 2, np, a.stream);
+  if (e != cudaSuccess) return e;
+  int part_rows = 0;
+  if (act) {
+    LinearEpilogue epi{};
+    epi.bias = a.bias;
+    epi.res = a.grad_out;
+    epi.ldr = a.ldg;
+    epi.out = dz_buf;
+    epi.ldo = dz_pitch(a.N);
+    epi.act = a.act;
+    epi.part = a.grad_bias ? part : nullptr;
+    const TcPlan plan = tc_plan(a.M, a.N, a.K, np, di.sm_count);
+    part_rows = plan.part_rows;
+    e = launch_tc_gemm(plan, x, w, a.M, a.N, a.K, np, kEpiDz, epi, a.dev_err, a.stream);
+    if (e == cudaSuccess && dz.prep) e = launch_tc_prep(&dz, 1, np, a.stream);
+  } else if (a.grad_bias) {
+    part_rows = (int)((a.M + kGT - 1) / kGT);
+    e = bf16 ? launch_colsum(static_cast<const bf16_t*>(a.grad_out), a, part) : launch_colsum(static_cast<const float*>(a.grad_out), a, part);
+  }
+  if (e == cudaSuccess && a.grad_bias) e = launch_rowsum(part, part_rows, a);
+  if (e == cudaSuccess && a.grad_x) {
+    LinearEpilogue epi{};
+    epi.out = a.grad_x;
+    epi.ldo = a.K;
+    TcOperand wt = w;
+    wt.mn = true;
+    e = launch_tc_gemm(tc_plan(a.M, a.K, a.N, np, di.sm_count), dz, wt, a.M, a.K, a.N, np, kEpiForward, epi, a.dev_err, a.stream);
+  }
+  if (e == cudaSuccess && a.grad_w) {
+    LinearEpilogue epi{};
+    epi.out = a.grad_w;
+    epi.ldo = a.K;
+    TcOperand zt = dz, xt = x;
+    zt.mn = xt.mn = true;
+    e = launch_tc_gemm(tc_plan(a.N, a.K, a.M, np, di.sm_count), zt, xt, a.N, a.K, a.M, np, kEpiForward, epi, a.dev_err, a.stream);
+  }
+  return e;
+}
+
 }  // namespace
 
 int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype) {
-  (void)M, (void)N, (void)K, (void)dtype;
-  return 0;
+  if (small_fp32(M, N, K, dtype) || (dtype == ATTNRES_BF16 && K % 8 == 0)) return 0;
+  const int np = dtype == ATTNRES_BF16 ? 1 : 3;
+  return tc_prep_bytes(M, K, np) + tc_prep_bytes(N, K, np);
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act) {
-  (void)K;
-  return bwd_layout(M, N, dtype, act).total;
+  return bwd_layout(M, N, K, dtype, act).total;
 }
 
 cudaError_t launch_linear(const LinearArgs& a) {
+  if (!small_fp32(a.M, a.N, a.K, a.dtype)) {
+    bool done;
+    const cudaError_t e = linear_tc(a, &done);
+    if (done || e != cudaSuccess) return e;
+  }
   return a.dtype == ATTNRES_BF16 ? linear_any<bf16_t>(a) : linear_any<float>(a);
 }
 
@@ -241,6 +376,11 @@ cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
     if (a.grad_w) e = cudaMemsetAsync(a.grad_w, 0, (size_t)a.N * a.K * (a.dtype == ATTNRES_BF16 ? 2 : 4), a.stream);
     if (e == cudaSuccess && a.grad_bias) e = cudaMemsetAsync(a.grad_bias, 0, (size_t)a.N * 4, a.stream);
     return e;
+  }
+  if (!small_fp32(a.M, a.N, a.K, a.dtype)) {
+    bool done;
+    const cudaError_t e = linear_backward_tc(a, &done);
+    if (done || e != cudaSuccess) return e;
   }
   return a.dtype == ATTNRES_BF16 ? linear_backward_any<bf16_t>(a) : linear_backward_any<float>(a);
 }

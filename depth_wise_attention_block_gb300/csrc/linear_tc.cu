@@ -1,0 +1,653 @@
+// The matrix products of attnres_linear and its backward on the tensor cores.
+//
+//   C(m, n) = sum_k A(m, k) B(n, k), then an epilogue (linear_epilogue.cuh)
+//
+// Operands come in by TMA, 64 steps of the contraction at a time, in the
+// 128-byte swizzle, either K-major (rows of the contraction: x, w, dz in
+// dz w) or MN-major (columns of it: w in dz w, both operands of dz^T x), so
+// that no operand is ever transposed in memory.  One thread issues
+// tcgen05.mma (M = 128 rows, fp32 accumulators in TMEM); eight warps run the
+// epilogue while the next tile's products are formed in the other half of
+// TMEM.
+//
+// Two shapes of launch:
+//  - wide: persistent CTAs over tiles of 128 x bn.  The bound is the tensor
+//    cores.
+//  - narrow (SWAP): few rows of one operand (decode).  The wide operand's
+//    rows become the 128 lanes and the few rows the columns, so the weights
+//    are read once; the contraction is split over a cluster of `ksplit` CTAs
+//    whose partial tiles are joined through distributed shared memory in rank
+//    order (no atomics, no workspace).  Two CTAs share an SM.  The bound is
+//    HBM.
+//
+// fp32 operands (NP = 3) enter as three bf16 terms each (hi + mid + lo, 24
+// bits).  The product hi hi goes to one accumulator and the five others that
+// matter (hi mid, mid hi, mid mid, hi lo, lo hi) to a second one 2^-8
+// smaller; both are drained into fp32 registers every kDrain blocks, so that
+// the tensor cores' truncating accumulation never runs over more than 256
+// steps of the contraction.
+#include <math.h>
+
+#include "attnres.h"
+#include "body.h"
+#include "launch.h"
+#include "linear_epilogue.cuh"
+#include "linear_tc.h"
+#include "tc_common.cuh"
+
+namespace attnres {
+
+namespace {
+
+constexpr int kLanes = 128;            // M of the instruction
+constexpr int kKB = 64;                // contraction steps per block: one 128-byte swizzle row
+constexpr int kThreads = 320;          // TMA warp, MMA warp, 8 epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kMaxStages = 8;
+constexpr int kDrain = 4;              // NP = 3: blocks between two drains
+constexpr int kMaxKsplit = 8;
+constexpr int kNarrowSmem = 100 * 1024;  // two CTAs per SM
+
+struct TcParams {
+  CUtensorMap ma, mb;    // lanes' operand, columns' operand
+  bool a_mn, b_mn;
+  int lanes, cols;       // size of the product along lanes and columns
+  int kblocks;
+  int bn;                // columns per tile, a multiple of 16
+  int tiles_l, tiles_c;
+  int ksplit, stages;
+  uint32_t stage_bytes, plane_a, plane_b;  // bytes of a stage, of one plane of A and of B
+  uint32_t tmem_cols, acc_cols;            // allocated columns, columns of one accumulator buffer
+  uint32_t idesc;
+  LinearEpilogue epi;
+  int* dev_err;
+  unsigned long long wait_ns;
+};
+
+// One plane of an operand's tile, block kb of the contraction, rows from r0.
+__device__ __forceinline__ void load_plane(uint32_t dst, const CUtensorMap* map, bool mn, int r0, int rows, int kb, int plane,
+                                           uint32_t bar) {
+  if (!mn) {
+    tma_load_3d(dst, map, kb * kKB, r0, plane, bar);
+  } else {
+    for (int j = 0; j < rows; j += 64) tma_load_3d(dst + j * 128, map, r0 + j, kb * kKB, plane, bar);  // 8 KB panels
+  }
+}
+
+// descriptor of the 16 contraction steps from 16 kk of a plane
+__device__ __forceinline__ uint64_t plane_desc(uint32_t addr, bool mn, int kk) {
+  return mn ? smem_desc_mn128(addr + kk * 2048, 8192) : smem_desc_k128(addr + kk * 32);
+}
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float* v);
+template <>
+__device__ __forceinline__ void load16<bf16_t>(const bf16_t* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[8 * i + 2 * j] = bf16lo(u[j]);
+      v[8 * i + 2 * j + 1] = bf16hi(u[j]);
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void load16<float>(const float* p, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p) + i);
+    v[4 * i] = w.x;
+    v[4 * i + 1] = w.y;
+    v[4 * i + 2] = w.z;
+    v[4 * i + 3] = w.w;
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float* v);
+template <>
+__device__ __forceinline__ void store16<bf16_t>(bf16_t* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                                pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+}
+template <>
+__device__ __forceinline__ void store16<float>(float* p, const float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(p)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// Sums of 16 columns over the warp's 32 lanes: lane l returns column l / 2's
+// (both lanes of a pair the same), in a fixed order, by halving exchanges.
+__device__ __forceinline__ float column_sums16(float* v, int lane) {
+#pragma unroll
+  for (int half = 8; half > 0; half >>= 1) {
+    const bool up = lane & (2 * half);
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float keep = up ? v[i + half] : v[i], give = up ? v[i] : v[i + half];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2 * half);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
+}
+
+// 16 columns n0 .. of row m (lanes: rows): values, then their columns' sums
+// over the warp (kEpiDz with partial rows).  `vec`: whole 16-byte accesses.
+template <typename T, int MODE>
+__device__ __forceinline__ void epilogue_row16(const TcParams& p, float* v, long long m, int n0, bool vec_out, bool vec_res,
+                                               int lane, int part_row) {
+  const LinearEpilogue& e = p.epi;
+  const bool row = m < p.lanes;
+  const bool full = n0 + 16 <= p.cols;
+  if (full) {
+    if (e.bias) {
+      float b[16];
+      if ((reinterpret_cast<uintptr_t>(e.bias) & 15) == 0)
+        load16<float>(e.bias + n0, b);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) b[i] = __ldg(e.bias + n0 + i);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] += b[i];
+    }
+    float r[16];
+    if (e.res) {
+      const T* src = static_cast<const T*>(e.res) + (row ? m : 0) * e.ldr + n0;
+      if (vec_res)
+        load16<T>(src, r);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) r[i] = load_elem(src + i);
+    }
+    if constexpr (MODE == kEpiDz) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = r[i] * act_slope(e.act, v[i]);
+    } else {
+      if (e.act != ATTNRES_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = act_value(e.act, v[i]);
+      }
+      if (e.res) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] += r[i];
+      }
+    }
+    if (row) {
+      T* dst = static_cast<T*>(e.out) + m * e.ldo + n0;
+      if (vec_out)
+        store16<T>(dst, v);
+      else
+#pragma unroll
+        for (int i = 0; i < 16; ++i) store_elem(dst + i, v[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      v[i] = row && n0 + i < p.cols ? epilogue_one<T, MODE>(e, m, n0 + i, v[i]) : 0.f;
+  }
+  if (MODE == kEpiDz && e.part) {
+    if (!row) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    }
+    const float s = column_sums16(v, lane);
+    const int n = n0 + lane / 2;
+    if ((lane & 1) == 0 && n < p.cols) e.part[(long long)part_row * p.cols + n] = s;
+  }
+}
+
+__device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int NP, int MODE, bool SWAP>
+__global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant__ TcParams p) {
+  using T = typename std::conditional<NP == 3, float, bf16_t>::type;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = SWAP && p.ksplit > 1 ? (int)cluster_ctarank() : 0;
+  const int ntiles = p.tiles_l * p.tiles_c;
+  const int tile0 = SWAP ? blockIdx.x / p.ksplit : blockIdx.x, tstep = SWAP ? ntiles : gridDim.x;
+  const int kb0 = (int)((long long)rank * p.kblocks / p.ksplit), kb1 = (int)((long long)(rank + 1) * p.kblocks / p.ksplit);
+  const int group = NP == 3 ? kDrain : p.kblocks;  // blocks per accumulator drain
+
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&acc_full[b]), 1);
+      mbar_init(smem_addr(&acc_empty[b]), kEpiWarps);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_base), p.tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int brows = p.b_mn ? (p.bn + 63) / 64 * 64 : p.bn;
+      int it = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+        const int l0 = tile % p.tiles_l * kLanes, c0 = tile / p.tiles_l * p.bn;
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          const int st = it % p.stages;
+          if (!mbar_wait_bounded(smem_addr(&empty[st]), ((uint32_t)(it / p.stages) & 1u) ^ 1u, p.wait_ns)) {
+            report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_addr(&full[st]), a = base + st * p.stage_bytes, b = a + NP * p.plane_a;
+          mbar_arrive_expect_tx(fb, NP * (kLanes * 128 + brows * 128));
+#pragma unroll
+          for (int pl = 0; pl < NP; ++pl) {
+            load_plane(a + pl * p.plane_a, &p.ma, p.a_mn, l0, kLanes, kb, pl, fb);
+            load_plane(b + pl * p.plane_b, &p.mb, p.b_mn, c0, brows, kb, pl, fb);
+          }
+        }
+      }
+      // the CTA never exits under a copy
+      const int armed = it < p.stages ? it : p.stages;
+      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.stages) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int it = 0, g = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+        for (int kb = kb0; kb < kb1 && ok; ++g) {
+          const int end = kb + group < kb1 ? kb + group : kb1;
+          const int buf = g & 1;
+          if (!mbar_wait_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns)) {
+            report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + buf * p.acc_cols;
+          for (const int first = kb; kb < end; ++kb, ++it) {
+            const int st = it % p.stages;
+            if (!mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)(it / p.stages) & 1u, p.wait_ns)) {
+              report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a = base + st * p.stage_bytes, b = a + NP * p.plane_a;
+#pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              const uint32_t acc = kb > first || kk > 0;
+              if constexpr (NP == 1) {
+                tc_mma_bf16(d, plane_desc(a, p.a_mn, kk), plane_desc(b, p.b_mn, kk), p.idesc, acc);
+              } else {
+                uint64_t da[3], db[3];
+#pragma unroll
+                for (int pl = 0; pl < 3; ++pl) {
+                  da[pl] = plane_desc(a + pl * p.plane_a, p.a_mn, kk);
+                  db[pl] = plane_desc(b + pl * p.plane_b, p.b_mn, kk);
+                }
+                const uint32_t d1 = d + p.acc_cols / 2;
+                tc_mma_bf16(d, da[0], db[0], p.idesc, acc);
+                tc_mma_bf16(d1, da[0], db[2], p.idesc, acc);
+                tc_mma_bf16(d1, da[2], db[0], p.idesc, 1u);
+                tc_mma_bf16(d1, da[1], db[1], p.idesc, 1u);
+                tc_mma_bf16(d1, da[0], db[1], p.idesc, 1u);
+                tc_mma_bf16(d1, da[1], db[0], p.idesc, 1u);
+              }
+            }
+            tc_commit(smem_addr(&empty[st]));
+          }
+          tc_commit(smem_addr(&acc_full[buf]));
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // warp w reads TMEM lanes 32 (w mod 4) .. + 31; two warps share a quarter
+    // and take the 16-column chunks in turn
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
+    const int nchunk = (p.bn + 15) / 16;
+    constexpr int kRegChunks = NP == 3 ? 4 : 1;  // NP = 3: bn <= 128
+    const bool vec_out = p.epi.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.out) & 15) == 0;
+    const bool vec_res = p.epi.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.res) & 15) == 0;
+    const float nan = __int_as_float(0x7fc00000);
+    bool ok = true;
+    int g = 0;
+    for (int tile = tile0; tile < ntiles; tile += tstep) {
+      const int l0 = tile % p.tiles_l * kLanes, c0 = tile / p.tiles_l * p.bn;
+      const long long m = l0 + 32 * quarter + lane;
+      float acc[kRegChunks][16];
+      if constexpr (NP == 3) {
+#pragma unroll
+        for (int c = 0; c < kRegChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c][i] = 0.f;
+      }
+      for (int kb = kb0; kb < kb1; kb += group, ++g) {
+        const int buf = g & 1;
+        if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
+          if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+          ok = false;
+        }
+        tc_fence_after();
+        const uint32_t at = lanes_at + buf * p.acc_cols;
+        if constexpr (NP == 3) {
+#pragma unroll
+          for (int c = 0; c < kRegChunks; ++c) {
+            const int ch = 2 * c + half;
+            if (ch < nchunk) {
+              uint32_t v[16], w[16];
+              tmem_ld16(at + ch * 16, v);
+              tmem_ld16(at + p.acc_cols / 2 + ch * 16, w);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[c][i] += __uint_as_float(v[i]) + __uint_as_float(w[i]);
+            }
+          }
+        } else {
+          for (int ch = half; ch < nchunk; ch += 2) {
+            uint32_t v[16];
+            tmem_ld16(at + ch * 16, v);
+            tmem_ld_wait();
+            float f[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = ok ? __uint_as_float(v[i]) : nan;
+            if constexpr (SWAP) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((ch * 16 + i) * kLanes + 32 * quarter + lane) * 4), "f"(f[i]) : "memory");
+            } else if (c0 + ch * 16 < p.cols) {
+              epilogue_row16<T, MODE>(p, f, m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&acc_empty[buf]));
+      }
+      if constexpr (NP == 3) {
+#pragma unroll
+        for (int c = 0; c < kRegChunks; ++c) {
+          const int ch = 2 * c + half;
+          if (ch < nchunk) {
+            if (!ok) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[c][i] = nan;
+            }
+            if constexpr (SWAP) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((ch * 16 + i) * kLanes + 32 * quarter + lane) * 4), "f"(acc[c][i]) : "memory");
+            } else if (c0 + ch * 16 < p.cols) {
+              epilogue_row16<T, MODE>(p, acc[c], m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+            }
+          }
+        }
+      }
+    }
+  }
+  if constexpr (SWAP) {
+    // the cluster's partial tiles [column][lane], joined in rank order; each
+    // rank takes a range of the columns
+    if (p.ksplit > 1) {
+      __syncwarp();
+      cluster_sync_all();
+    } else {
+      __syncthreads();
+    }
+    if (warp >= 2) {
+      const int e = tid - 64, row = e % kLanes, g = e / kLanes;
+      const int l0 = tile0 % p.tiles_l * kLanes, c0 = tile0 / p.tiles_l * p.bn;
+      const int cl0 = rank * p.bn / p.ksplit, cl1 = (rank + 1) * p.bn / p.ksplit;
+      const int n = l0 + row;
+      const uint32_t mine = base + row * 4;
+      uint32_t at[kMaxKsplit];
+#pragma unroll
+      for (int r = 0; r < kMaxKsplit; ++r) at[r] = r < p.ksplit && p.ksplit > 1 ? map_shared_rank(mine, r) : mine;
+      float sum = 0.f;
+      for (int c = cl0 + g; c < cl1; c += 2) {
+        float v = 0.f;
+        if (p.ksplit > 1) {
+#pragma unroll
+          for (int r = 0; r < kMaxKsplit; ++r)
+            if (r < p.ksplit) v += ld_shared_cluster(at[r] + c * kLanes * 4);
+        } else {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(mine + c * kLanes * 4) : "memory");
+        }
+        if (n < p.lanes && c0 + c < p.cols) sum += epilogue_one<T, MODE>(p.epi, c0 + c, n, v);
+      }
+      if (MODE == kEpiDz && p.epi.part && n < p.lanes)
+        p.epi.part[(long long)((tile0 / p.tiles_l * p.ksplit + rank) * 2 + g) * p.lanes + n] = sum;
+    }
+    if (p.ksplit > 1) {
+      __syncwarp();
+      cluster_sync_all();  // no CTA leaves while another reads its tile
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// ----------------------------------------------------------- operands ------
+
+// Copies of operands TMA cannot take as they are: rows on 16-byte boundaries
+// (bf16), or the three bf16 terms of fp32 values (hi = round(v), mid =
+// round(v - hi), lo = round(v - hi - mid); the subtractions are exact).
+struct PrepJob {
+  const void* src;
+  long long ld, rows;
+  int cols;
+  long long pitch;  // elements per destination row, a multiple of 8
+  bf16_t* dst;      // NP planes of rows x pitch
+};
+struct PrepParams {
+  PrepJob job[2];
+};
+
+__device__ __forceinline__ uint32_t bf16_near(float v) {
+  uint32_t b = f32_to_bf16_bits(v);
+  // a finite value that would round to infinity is cut instead
+  if ((b & 0x7fffu) == 0x7f80u && isfinite(v)) b = __float_as_uint(v) >> 16;
+  return b;
+}
+
+template <int NP>
+__global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ PrepParams p) {
+  const PrepJob& j = p.job[blockIdx.y];
+  pdl_wait();
+  pdl_trigger();
+  const long long pairs = j.pitch / 2, total = j.rows * pairs;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
+    const long long r = i / pairs;
+    const int c = (int)(i % pairs) * 2;
+    if constexpr (NP == 1) {
+      const uint16_t* s = static_cast<const uint16_t*>(j.src) + r * j.ld + c;
+      const uint32_t lo = c < j.cols ? s[0] : 0, hi = c + 1 < j.cols ? s[1] : 0;
+      reinterpret_cast<uint32_t*>(j.dst)[i] = lo | hi << 16;
+    } else {
+      const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
+      float a = c < j.cols ? s[0] : 0.f, b = c + 1 < j.cols ? s[1] : 0.f;
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        const uint32_t x = bf16_near(a), y = bf16_near(b);
+        reinterpret_cast<uint32_t*>(j.dst)[pl * total + i] = x | y << 16;
+        a -= bf16_bits_to_f32(x);
+        b -= bf16_bits_to_f32(y);
+      }
+    }
+  }
+}
+
+int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// The operand's tensor map: element (row, contraction step) at ptr[row ld +
+// step] (K-major) or ptr[step ld + row] (MN-major), `np` planes apart.
+bool operand_map(CUtensorMap* map, const void* ptr, int64_t outer, int64_t inner, int64_t ld, int np, bool mn, int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)np};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(outer * ld * 2)};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? kKB : box_rows), 1};
+  return make_tensor_map(map, ptr, 3, dims, strides, box);
+}
+
+template <int NP, int MODE>
+cudaError_t launch_mode(const TcParams& p, bool swap, int grid, int smem, int smem_max, cudaStream_t stream) {
+  if (!swap) {
+    static SmemOptIn optin;
+    const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_gemm_kernel<NP, MODE, false>), smem_max);
+    return e != cudaSuccess ? e : launch_kernel(tc_gemm_kernel<NP, MODE, false>, dim3(grid), dim3(kThreads), smem, stream, p);
+  }
+  static SmemOptIn optin;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_gemm_kernel<NP, MODE, true>), smem_max);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.ksplit;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tc_gemm_kernel<NP, MODE, true>, p);
+}
+
+}  // namespace
+
+bool tc_rows_ok(const void* ptr, int64_t ld) { return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0 && ld % 8 == 0; }
+
+int64_t tc_prep_bytes(int64_t rows, int64_t cols, int np) { return np * up(rows * up(cols, 8) * 2, 256); }
+
+TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
+  TcPlan best{};
+  const int64_t kblocks = up(K, kKB) / kKB;
+  const int bn_max = np == 3 ? 128 : 256;
+  double cost = 1e300;
+  // wide: whole waves of tiles; a block costs the tensor cores bn / 2 cycles
+  // per instruction, 4 instructions (24 with three terms), and a tile the
+  // epilogue's start-up
+  for (int bn = 64; bn <= bn_max; bn *= 2) {
+    const int64_t tiles = up(M, kLanes) / kLanes * (up(N, bn) / bn);
+    const double tile = (double)kblocks * (np == 3 ? 24 : 4) * (bn < 128 ? 64 : bn / 2) + 1500;
+    const double c = (double)((tiles + sm_count - 1) / sm_count) * tile + 1500;
+    if (c < cost) {
+      cost = c;
+      best = {false, bn, 1, 0};
+    }
+  }
+  // narrow: M's rows as columns, N's as lanes, the contraction over a
+  // cluster; the CTAs' streams share HBM (about 24 bytes per cycle and SM)
+  if (M <= 256) {
+    const int bn = M >= 128 ? 128 : (int)up(M, 16);
+    const int slots = sm_count * (np == 3 ? 1 : 2);
+    for (int ks = 1; ks <= kMaxKsplit && ks <= kblocks; ++ks) {
+      const int64_t tiles = up(N, kLanes) / kLanes * (up(M, bn) / bn);
+      const int64_t ctas = tiles * ks;
+      const int64_t waves = (ctas + slots - 1) / slots;
+      const double block = np == 3 ? 24.0 * 64 + 600 : (kLanes + bn) * 128.0 / (24.0 / 2);
+      const double c = (double)waves * ((double)((kblocks + ks - 1) / ks) * block + 2500) + 1500;
+      if (c < cost) {
+        cost = c;
+        best = {true, bn, ks, 0};
+      }
+    }
+  }
+  best.part_rows = best.swap ? (int)(up(M, best.bn) / best.bn * best.ksplit * 2) : (int)(up(M, kLanes) / 32);
+  return best;
+}
+
+cudaError_t launch_tc_prep(const TcOperand* ops, int n, int np, cudaStream_t stream) {
+  PrepParams pp{};
+  int64_t most = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t pitch = up(ops[i].cols, 8);
+    pp.job[i] = {ops[i].ptr, ops[i].ld, ops[i].rows, (int)ops[i].cols, pitch, static_cast<bf16_t*>(ops[i].prep)};
+    const int64_t c = (ops[i].rows * pitch / 2 + 255) / 256;
+    if (c > most) most = c;
+  }
+  const dim3 grid((unsigned)(most < 2432 ? most : 2432), n);
+  return np == 3 ? launch_kernel(prep_kernel<3>, grid, dim3(256), 0, stream, pp)
+                 : launch_kernel(prep_kernel<1>, grid, dim3(256), 0, stream, pp);
+}
+
+cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOperand& B, int64_t M, int N, int64_t K, int np,
+                           int mode, const LinearEpilogue& epi, int* dev_err, cudaStream_t stream) {
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const TcOperand &lo = plan.swap ? B : A, &co = plan.swap ? A : B;
+  TcParams p{};
+  auto map = [&](CUtensorMap* m, const TcOperand& o, int box) {
+    const void* ptr = o.prep ? o.prep : o.ptr;
+    const int64_t ld = o.prep ? up(o.cols, 8) : o.ld;
+    return operand_map(m, ptr, o.rows, o.cols, ld, np, o.mn, box);
+  };
+  if (!map(&p.ma, lo, kLanes) || !map(&p.mb, co, plan.bn)) return cudaErrorInvalidValue;
+  p.a_mn = lo.mn;
+  p.b_mn = co.mn;
+  p.lanes = plan.swap ? N : (int)M;
+  p.cols = plan.swap ? (int)M : N;
+  p.kblocks = (int)(up(K, kKB) / kKB);
+  p.bn = plan.bn;
+  p.tiles_l = (int)(up(p.lanes, kLanes) / kLanes);
+  p.tiles_c = (int)(up(p.cols, p.bn) / p.bn);
+  p.ksplit = plan.ksplit;
+  p.plane_a = kLanes * 128;
+  p.plane_b = (uint32_t)((p.b_mn ? up(p.bn, 64) : up(p.bn, 8)) * 128);
+  p.stage_bytes = np * (p.plane_a + p.plane_b);
+  const int nacc = np == 3 ? 2 : 1;
+  const int nbuf = plan.swap && np == 1 ? 1 : 2;
+  p.acc_cols = nacc * (uint32_t)p.bn;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < nbuf * p.acc_cols) p.tmem_cols *= 2;
+  p.idesc = tc_idesc_bf16(kLanes, p.bn, p.a_mn, p.b_mn);
+  p.epi = epi;
+  p.dev_err = dev_err;
+  p.wait_ns = wait_limit_ns();
+  // shared memory: the stages; narrow tiles also park their partial sums there
+  const int smem_max = di.max_smem_optin - 1024;  // the kernels' static shared memory fits in the rest
+  const int budget = (plan.swap && np == 1 ? kNarrowSmem : smem_max) - 1024;
+  int stages = budget / (int)p.stage_bytes;
+  if (stages > kMaxStages) stages = kMaxStages;
+  if (stages < 2) return cudaErrorInvalidValue;
+  p.stages = stages;
+  int smem = stages * (int)p.stage_bytes;
+  if (plan.swap && smem < p.bn * kLanes * 4) smem = p.bn * kLanes * 4;
+  smem += 1024;
+  const int64_t tiles = (int64_t)p.tiles_l * p.tiles_c;
+  const int64_t grid = plan.swap ? tiles * p.ksplit : (tiles < di.sm_count ? tiles : di.sm_count);
+  if (tiles > INT32_MAX / kMaxKsplit) return cudaErrorInvalidValue;
+  if (np == 3)
+    return mode == kEpiDz ? launch_mode<3, kEpiDz>(p, plan.swap, (int)grid, smem, smem_max, stream)
+                          : launch_mode<3, kEpiForward>(p, plan.swap, (int)grid, smem, smem_max, stream);
+  return mode == kEpiDz ? launch_mode<1, kEpiDz>(p, plan.swap, (int)grid, smem, smem_max, stream)
+                        : launch_mode<1, kEpiForward>(p, plan.swap, (int)grid, smem, smem_max, stream);
+}
+
+}  // namespace attnres

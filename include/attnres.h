@@ -518,12 +518,12 @@ typedef enum {
  * act       one of attnres_activation
  * workspace NULL, or device scratch of workspace_bytes, 256-byte aligned,
  *           sharing no memory with an operand (its contents on entry do not
- *           matter).  With attnres_linear_workspace_size(...) bytes every
- *           size and alignment runs on the tensor cores (tcgen05); without
- *           it, bf16 operands whose rows start on 16-byte boundaries do, and
- *           others run on the CUDA cores.  fp32 operands enter the tensor
- *           cores as three bf16 terms each, whose six leading products keep
- *           fp32 precision (an infinite operand gives NaN there).
+ *           matter).  bf16 operands whose rows start on 16-byte boundaries go
+ *           to the tensor cores (tcgen05) without one.  Others are first
+ *           copied into it: bf16 to aligned rows, fp32 as three bf16 terms
+ *           each, whose six leading products keep fp32 precision (there an
+ *           infinite operand gives NaN).  Where it is too small for that, and
+ *           for small fp32 products, the CUDA cores take the call.
  * No output may share memory with an input (but residual, as above).
  * Calls that overlap in time need a workspace each.
  * ---------------------------------------------------------------------- */
@@ -532,8 +532,8 @@ int attnres_linear(const void* x, int64_t ldx, const void* w, const float* bias,
                    int64_t workspace_bytes, int* dev_err, void* stream);
 
 /* Bytes of workspace with which attnres_linear takes its fastest path for
- * these sizes on the current device, whatever the operands' alignment and
- * row strides.  Negative attnres_status on bad arguments. */
+ * contiguous operands of these sizes (0: it needs none).  Negative
+ * attnres_status on bad arguments. */
 int64_t attnres_linear_workspace_size(int64_t M, int N, int K, int dtype);
 
 /* ------------------------------------------------------------------------
