@@ -113,7 +113,7 @@ struct LinAttnArgs {
 };
 cudaError_t launch_linear_attention(const LinAttnArgs& a);
 cudaError_t launch_linear_attention_backward(const LinAttnArgs& a);
-int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N, bool backward);
+int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N);
 
 struct LinAttnStepArgs {
   const void *q, *k, *v;

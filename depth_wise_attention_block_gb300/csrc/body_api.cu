@@ -352,7 +352,7 @@ int attnres_qk_norm_rope_backward(const void* q, int64_t q_stride, int Hq, const
 int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs) {
   const int rc = check_la_sizes(T, H, Dk, Dv, dtype, num_seqs);
   if (rc != ATTNRES_OK) return rc;
-  const int64_t n = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs, false);
+  const int64_t n = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (n < 0) return fail(ATTNRES_ECUDA, "device query");
   ok();
   return n;
@@ -361,7 +361,7 @@ int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv
 int64_t attnres_linear_attention_backward_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs) {
   const int rc = check_la_sizes(T, H, Dk, Dv, dtype, num_seqs);
   if (rc != ATTNRES_OK) return rc;
-  const int64_t n = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs, true);
+  const int64_t n = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (n < 0) return fail(ATTNRES_ECUDA, "device query");
   ok();
   return n;
@@ -391,7 +391,7 @@ int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int
     rc = check_apart(in, 6, outs, 3, in_place);
     if (rc != ATTNRES_OK) return rc;
   }
-  const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs, false);
+  const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (need < 0) return fail(ATTNRES_ECUDA, "device query");
   rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != ATTNRES_OK) return rc;
@@ -458,7 +458,7 @@ int attnres_linear_attention_backward(const void* q, int64_t q_stride, const voi
     rc = check_apart(in, 8, outs, 5, in_place);
     if (rc != ATTNRES_OK) return rc;
   }
-  const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs, true);
+  const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (need < 0) return fail(ATTNRES_ECUDA, "device query");
   rc = check_workspace(workspace, workspace_bytes, need);
   if (rc != ATTNRES_OK) return rc;

@@ -292,9 +292,8 @@ ScanArgs scan_args(const LinAttnArgs& a, const void* x, int64_t xs, const void* 
 
 }  // namespace
 
-int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N, bool backward) {
-  (void)T, (void)H, (void)Dk, (void)Dv, (void)dtype, (void)N, (void)backward;
-  return 0;
+int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N) {
+  return scan_tc_dims(Dk, Dv, dtype) ? scan_tc_workspace(T, H, Dk, Dv, N) : 0;
 }
 
 cudaError_t launch_linear_attention(const LinAttnArgs& a) {
@@ -302,33 +301,40 @@ cudaError_t launch_linear_attention(const LinAttnArgs& a) {
   s.s_in = a.s0;
   s.s_out = a.s1;
   s.p_scale = s.in_scale = a.scale;
+  if (scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(s)) return launch_scan_tc(s, a.workspace, false, a.dev_err, a.stream);
   return launch_scan(s, a.dtype, a.stream);
 }
 
 cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   const int64_t rk = (int64_t)a.H * a.Dk, rv = (int64_t)a.H * a.Dv;
-  ScanArgs s = scan_args(a, a.dout, a.dos, a.v, a.vs, a.Dv, a.k, a.ks, a.Dk, a.dq, rk);
-  s.s_in = a.s0;
-  s.transposed = true;
-  s.p_scale = s.in_scale = a.scale;
-  cudaError_t e = launch_scan(s, a.dtype, a.stream);
-  if (e != cudaSuccess) return e;
-  s = scan_args(a, a.v, a.vs, a.dout, a.dos, a.Dv, a.q, a.qs, a.Dk, a.dk, rk);
-  s.s_in = a.ds1;
-  s.transposed = true;
-  s.reverse = true;
-  s.shift = 1;
-  s.p_scale = s.up_scale = a.scale;
-  e = launch_scan(s, a.dtype, a.stream);
-  if (e != cudaSuccess) return e;
-  // last: it may write grad_initial_state over grad_final_state
-  s = scan_args(a, a.k, a.ks, a.q, a.qs, a.Dk, a.dout, a.dos, a.Dv, a.dv, rv);
-  s.s_in = a.ds1;
-  s.s_out = a.ds0;
-  s.reverse = true;
-  s.shift = 1;
-  s.p_scale = s.up_scale = a.scale;
-  return launch_scan(s, a.dtype, a.stream);
+  ScanArgs q = scan_args(a, a.dout, a.dos, a.v, a.vs, a.Dv, a.k, a.ks, a.Dk, a.dq, rk);
+  q.s_in = a.s0;
+  q.transposed = true;
+  q.p_scale = q.in_scale = a.scale;
+  ScanArgs k = scan_args(a, a.v, a.vs, a.dout, a.dos, a.Dv, a.q, a.qs, a.Dk, a.dk, rk);
+  k.s_in = a.ds1;
+  k.transposed = true;
+  k.reverse = true;
+  k.shift = 1;
+  k.p_scale = k.up_scale = a.scale;
+  ScanArgs v = scan_args(a, a.k, a.ks, a.q, a.qs, a.Dk, a.dout, a.dos, a.Dv, a.dv, rv);
+  v.s_in = a.ds1;
+  v.s_out = a.ds0;
+  v.reverse = true;
+  v.shift = 1;
+  v.p_scale = v.up_scale = a.scale;
+  // dv last: it may write grad_initial_state over grad_final_state
+  if (scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(q) && scan_tc_ok(k) && scan_tc_ok(v)) {
+    cudaError_t e = launch_scan_tc(q, a.workspace, false, a.dev_err, a.stream);
+    if (e == cudaSuccess) e = launch_scan_tc(k, a.workspace, false, a.dev_err, a.stream);
+    // the same reversed state, [Dk, Dv] in both
+    if (e == cudaSuccess) e = launch_scan_tc(v, a.workspace, true, a.dev_err, a.stream);
+    return e;
+  }
+  cudaError_t e = launch_scan(q, a.dtype, a.stream);
+  if (e == cudaSuccess) e = launch_scan(k, a.dtype, a.stream);
+  if (e == cudaSuccess) e = launch_scan(v, a.dtype, a.stream);
+  return e;
 }
 
 cudaError_t launch_linear_attention_step(const LinAttnStepArgs& a) {

@@ -1,6 +1,7 @@
 // The scan behind linear attention and its gradients (linear_attention.cu).
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace attnres {
@@ -33,9 +34,19 @@ struct ScanArgs {
   float* s_out;
   bool transposed, reverse;
   int shift;               // 1: the carried state is already decayed for the next token
+  bool wide_out;           // out's rows start on 32-byte boundaries (set by the launch)
   float p_scale, in_scale, up_scale;  // factors of the triangle, of the carried state's part, of what enters the state
 
   __host__ __device__ int state_at(int da, int dc) const { return transposed ? dc * Da + da : da * Dc + dc; }
 };
+
+// The scan on the tensor cores (linear_attention_tc.cu).
+constexpr int kScanChunk = 128;  // tokens per chunk
+bool scan_tc_dims(int Dk, int Dv, int dtype);
+bool scan_tc_ok(const ScanArgs& s);  // alignment, sizes
+int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N);
+// states_ready: the workspace holds the states before the segments already,
+// left there by a scan of the same direction, states and sums b c^T
+cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream);
 
 }  // namespace attnres
