@@ -323,8 +323,13 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   v.reverse = true;
   v.shift = 1;
   v.p_scale = v.up_scale = a.scale;
-  // dv last: it may write grad_initial_state over grad_final_state
+  // grad_initial_state may lie over grad_final_state: it is written after
+  // the last read, by dv's scan or where the segments' states are joined
   if (scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(q) && scan_tc_ok(k) && scan_tc_ok(v)) {
+    if (scan_tc_segmented(a.T, a.H, a.N)) {
+      k.s_out = a.ds0;
+      v.s_out = nullptr;
+    }
     cudaError_t e = launch_scan_tc(q, a.workspace, false, a.dev_err, a.stream);
     if (e == cudaSuccess) e = launch_scan_tc(k, a.workspace, false, a.dev_err, a.stream);
     // the same reversed state, [Dk, Dv] in both

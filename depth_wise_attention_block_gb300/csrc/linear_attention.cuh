@@ -44,9 +44,11 @@ struct ScanArgs {
 constexpr int kScanChunk = 128;  // tokens per chunk
 bool scan_tc_dims(int Dk, int Dv, int dtype);
 bool scan_tc_ok(const ScanArgs& s);  // alignment, sizes
+bool scan_tc_segmented(int64_t T, int H, int N);  // whether long sequences are cut into segments
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N);
 // states_ready: the workspace holds the states before the segments already,
-// left there by a scan of the same direction, states and sums b c^T
+// left there by a scan of the same direction, states and sums b c^T (which
+// wrote the final state, if any)
 cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream);
 
 }  // namespace attnres

@@ -7,19 +7,19 @@
 //
 // Every product is a tcgen05.mma with its accumulator in TMEM.  a, b and c
 // arrive by TMA in the 128-byte swizzle and serve K-major (a b^T, a S) or
-// MN-major (P c, the token sums) from the same tile.  Four warps turn the
+// MN-major (P c, the token sums) from the same tile.  Eight warps turn the
 // scores into P (bf16, back into TMEM as the next product's operand) and
-// write the outputs; four warps hold the state in fp32 registers (one row of
-// Da per thread), give it to the products rounded to bf16, and weigh b with
-// the decays: the weighted rows enter as three bf16 terms (24 bits), so that
-// the state keeps fp32 precision over any number of chunks; each chunk's U
-// starts from zero in TMEM and is added in fp32 round-to-nearest.
+// write the outputs; eight warps hold the state in fp32 registers (half a
+// row of Da per thread), give it to the products rounded to bf16, and weigh b
+// with the decays: the weighted rows enter as three bf16 terms (24 bits), so
+// that the state keeps fp32 precision over any number of chunks; each chunk's
+// U starts from zero in TMEM and is added in fp32 round-to-nearest.
 //
 // A reversed scan (gradients of k and v) takes the chunks from the end and
 // mirrors the mask and the powers; nothing is reordered in memory.
 //
 // Few heads and sequences do not fill the GPU.  A long sequence is then cut
-// into segments: scan_tc_kernel<STATE> forms every segment's own state (it
+// into segments: state_tc_kernel forms every segment's own state (it
 // reads b and c only), la_combine_kernel runs through the segments and
 // leaves the state before each, and the scan runs over all segments at once.
 //
@@ -39,7 +39,7 @@ namespace attnres {
 namespace {
 
 constexpr int kC = kScanChunk;         // tokens per chunk
-constexpr int kTileThreads = 320;      // 4 warps scores and outputs, 4 state, TMA, MMA
+constexpr int kTileThreads = 576;      // 8 warps scores and outputs, 8 state, TMA, MMA
 constexpr int kMaxSlots = 8;
 constexpr int kPanel = kC * 128;       // bytes of 64 channels of a tile
 
@@ -104,19 +104,19 @@ __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
                : "memory");
 }
 
-// STATE: the segments' own states only (b and c; no scores, no outputs).
-template <int DA, int DC, bool STATE>
+// TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
+// where only bf16 outputs follow from it.
+template <int DA, int DC, int TERMS>
 __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams p) {
   constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;  // bytes of a slot
-  constexpr int kTiles = STATE ? 2 : 3;                // tiles per chunk: (a,) b, c
-  constexpr int kSplitWarps = STATE ? 8 : 4;
+  constexpr int kTiles = 3;                            // tiles per chunk: a, b, c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, b_ready, u_full, u_free;
   __shared__ uint32_t tmem_base;
-  __shared__ float tab[kC], pw[kC + 2];  // p_scale l^k; l^k
+  __shared__ float tab[2 * kC], pw[kC + 2];  // p_scale l^(i - kC), 0 below; l^i
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t s_buf = base + p.slots * kTile, mid = s_buf + (STATE ? 0 : DC * DA * 2), lo = mid + kC * DA * 2;
+  const uint32_t s_buf = base + p.slots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
 
@@ -126,16 +126,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
       mbar_init(smem_addr(&empty[s]), 1);
     }
     mbar_init(smem_addr(&p_full), 1);
-    mbar_init(smem_addr(&p_ready), 4);
+    mbar_init(smem_addr(&p_ready), 8);
     mbar_init(smem_addr(&o_full), 1);
-    mbar_init(smem_addr(&o_free), 4);
-    mbar_init(smem_addr(&s_ready), 4);
-    mbar_init(smem_addr(&b_ready), kSplitWarps);
+    mbar_init(smem_addr(&o_free), 8);
+    mbar_init(smem_addr(&s_ready), 8);
+    mbar_init(smem_addr(&b_ready), 8);
     mbar_init(smem_addr(&u_full), 1);
-    mbar_init(smem_addr(&u_free), 4);
+    mbar_init(smem_addr(&u_free), 8);
     mbar_fence_init();
   }
-  if (warp == 9) tmem_alloc(smem_addr(&tmem_base), 512);
+  if (warp == 17) tmem_alloc(smem_addr(&tmem_base), 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -146,14 +146,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
   if (tid < kC + 2) {
     const float l = expf(g * (float)tid);
     pw[tid] = l;
-    if (tid < kC) tab[tid] = p.s.p_scale * l;
+    if (tid < kC) {
+      tab[tid] = 0.f;
+      tab[kC + tid] = p.s.p_scale * l;
+    }
   }
   __syncthreads();
   const bool live = !p.nsegs || seg_i < *p.nsegs;
   Segment sg{0, 0, 0, 0};
   if (live) sg = segment_of(p, seg_i);
-  const bool work = live && !(STATE && sg.last);  // nothing needs the state behind the last segment but its own scan
-  const int nchunk = work ? (sg.len + kC - 1) / kC : 0;
+  const int nchunk = live ? (sg.len + kC - 1) / kC : 0;
   const bool rev = p.s.reverse;
   // chunk n's first token and length (a reversed scan's short chunk is its last)
   auto chunk_len = [&](int n) { return sg.len - n * kC < kC ? sg.len - n * kC : kC; };
@@ -171,7 +173,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
     ok = __all_sync(0xffffffffu, ok);
   };
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (lane == 0) {
       int it = 0;
       for (int n = 0; n < nchunk && ok; ++n) {
@@ -180,9 +182,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
           const int st = it % p.slots;
           wait(&empty[st], (uint32_t)(it / p.slots) + 1u);
           if (!ok) break;
-          const int which = STATE ? k + 1 : k;
-          const int D = which == 2 ? DC : DA;
-          const CUtensorMap* m = which == 0 ? &p.ma : which == 1 ? &p.mb : &p.mc;
+          const int D = k == 2 ? DC : DA;
+          const CUtensorMap* m = k == 0 ? &p.ma : k == 1 ? &p.mb : &p.mc;
           const uint32_t fb = smem_addr(&full[st]);
           mbar_arrive_expect_tx(fb, D * kC * 2);
           for (int x = 0; x < D; x += 64) tma_load_2d(base + st * kTile + x / 64 * kPanel, m, h * D + x, t, fb);
@@ -193,258 +194,495 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
       for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.slots) & 1u);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 17) {
     if (lane == 0) {
       constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC),
                          kI4 = tc_idesc_bf16(128, DA, true, true);
-      for (int n = 0; n < nchunk && ok; ++n) {
+      auto slot = [&](int i) { return base + i % p.slots * kTile; };
+      auto wait_tile = [&](int i) { wait(&full[i % p.slots], (uint32_t)(i / p.slots)); };
+      // scores of chunk n, over those of n - 1 (whose P c is done)
+      auto scores = [&](int n) {
         const int it = n * kTiles;
-        const int sa = it % p.slots, sb = (it + kTiles - 2) % p.slots, sc = (it + kTiles - 1) % p.slots;
-        const uint32_t A = base + sa * kTile, B = base + sb * kTile, Ct = base + sc * kTile;
-        auto lap = [&](int i) { return (uint32_t)(i / p.slots); };
-        const uint32_t ph = (uint32_t)n;
-        if constexpr (!STATE) {
-          // P's columns are free once the last chunk's P c is done
-          if (n > 0) wait(&o_full, ph - 1);
-          wait(&full[sa], lap(it));
-          wait(&full[sb], lap(it + 1));
-          tc_fence_after();
+        if (n > 0) wait(&o_full, (uint32_t)n - 1u);
+        wait_tile(it);
+        wait_tile(it + 1);
+        tc_fence_after();
+        const uint64_t da = smem_desc_k128(slot(it)), db = smem_desc_k128(slot(it + 1));
 #pragma unroll
-          for (int kk = 0; kk < DA / 16; ++kk) {
-            const uint32_t off = kk / 4 * kPanel + kk % 4 * 32;
-            tc_mma_bf16(tmem + kColP, smem_desc_k128(A + off), smem_desc_k128(B + off), kI1, kk > 0);
-          }
-          tc_commit(smem_addr(&p_full));
-          wait(&s_ready, ph);
-          wait(&o_free, ph + 1);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < DA / 16; ++kk)
-            tc_mma_bf16(tmem + kColO2, smem_desc_k128(A + kk / 4 * kPanel + kk % 4 * 32),
-                        smem_desc_k128(s_buf + kk / 4 * (DC * 128) + kk % 4 * 32), kI3, kk > 0);
-          tc_commit(smem_addr(&empty[sa]));
-          wait(&full[sc], lap(it + 2));
-          // rows behind a short chunk's end are cleared with the weighted rows
-          if (chunk_len(n) < kC) wait(&b_ready, ph);
-          wait(&p_ready, ph);
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            tc_mma_bf16_ts(tmem + kColO1, tmem + kColP + kk * 8, smem_desc_mn128(Ct + kk * 2048, kPanel), kI2, kk > 0);
-          tc_commit(smem_addr(&o_full));
-        } else {
-          wait(&full[sc], lap(it + 1));
+        for (int kk = 0; kk < DA / 16; ++kk) {
+          const uint32_t off = (kk / 4 * kPanel + kk % 4 * 32) / 16;
+          tc_mma_bf16(tmem + kColP, da + off, db + off, kI1, kk > 0);
         }
+        tc_commit(smem_addr(&p_full));
+      };
+      if (nchunk > 0) scores(0);
+      for (int n = 0; n < nchunk && ok; ++n) {
+        const int it = n * kTiles, ib = it + 1, ic = it + 2;
+        const uint32_t ph = (uint32_t)n;
+        const uint64_t dc = smem_desc_mn128(slot(ic), kPanel);
+        wait(&s_ready, ph);
+        wait(&o_free, ph + 1);
+        tc_fence_after();
+        const uint64_t da = smem_desc_k128(slot(it)), ds = smem_desc_k128(s_buf);
+#pragma unroll
+        for (int kk = 0; kk < DA / 16; ++kk)
+          tc_mma_bf16(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
+        tc_commit(smem_addr(&empty[it % p.slots]));
+        wait_tile(ic);
+        // rows behind a short chunk's end are cleared with the weighted rows
+        if (chunk_len(n) < kC) wait(&b_ready, ph);
+        wait(&p_ready, ph);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kC / 16; ++kk)
+          tc_mma_bf16_ts(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
+        tc_commit(smem_addr(&o_full));
+        // the next scores before this chunk's sums: the warps that turn
+        // them into P weigh b's rows first
+        if (n + 1 < nchunk) scores(n + 1);
         wait(&b_ready, ph);
         wait(&u_free, ph + 1);
         tc_fence_after();
         // c's channels as the 128 rows (64 channels: the other 64 rows are
         // whatever lies behind, and are not read)
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          const uint32_t bt = term == 0 ? B : term == 1 ? mid : lo;
+        for (int term = 0; term < TERMS; ++term) {
+          const uint64_t dt = smem_desc_mn128(term == 0 ? slot(ib) : rest + (term - 1) * (kC * DA * 2), kPanel);
 #pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk)
-            tc_mma_bf16(tmem + kColU, smem_desc_mn128(Ct + kk * 2048, kPanel), smem_desc_mn128(bt + kk * 2048, kPanel), kI4,
-                        term > 0 || kk > 0);
+          for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
-        tc_commit(smem_addr(&empty[sb]));
-        tc_commit(smem_addr(&empty[sc]));
+        tc_commit(smem_addr(&empty[ib % p.slots]));
+        tc_commit(smem_addr(&empty[ic % p.slots]));
         tc_commit(smem_addr(&u_full));
       }
     }
     __syncwarp();
   } else {
-    const int quarter = warp & 3, row = 32 * quarter + lane;
+    // warp w reads TMEM lanes 32 (w mod 4) .. + 31; two warps of a group share
+    // a quarter, each with half of the columns
+    const int quarter = warp & 3, half = warp >> 2 & 1, row = 32 * quarter + lane;
     const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
     // b's rows times their decay, as three bf16 terms (hi over b itself)
-    auto split = [&](int n, int threads, int t0) {
+    auto split = [&](int n, int t0) {
       const int len = chunk_len(n);
-      const uint32_t B = base + (n * kTiles + kTiles - 2) % p.slots * kTile, Ct = base + (n * kTiles + kTiles - 1) % p.slots * kTile;
-#pragma unroll 2
-      for (int v = t0; v < kC * DA / 8; v += threads) {
-        const int j = (v / 8) % kC;
-        const uint32_t at = v * 16;
-        if (j < len) {
-          const float f = p.s.up_scale * pw[rev ? j + p.s.shift : len - 1 - j + p.s.shift];
-          const uint4 w = ld_shared_v4(B + at);
-          const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-          uint32_t th[4], tm[4], tl[4];
+      const uint32_t B = base + (n * kTiles + 1) % p.slots * kTile, Ct = base + (n * kTiles + 2) % p.slots * kTile;
+      // thread t0's vectors of 8 channels lie in rows t0 / 8 + kStep i of each
+      // panel, i < kBatch; a panel's are loaded before the first is stored
+      const float* fac = pw + p.s.shift + (rev ? 0 : len - 1);
+      constexpr int kStep = 256 / 8, kBatch = kC / kStep;
+      static_assert(kBatch >= 1 && kBatch * kStep == kC, "the batches cover a panel's rows once");
+#pragma unroll 1
+      for (int x = 0; x < DA / 64; ++x) {
+        const int j0 = t0 / 8;
+        const uint32_t at = x * kPanel + j0 * 128 + t0 % 8 * 16;
+        uint4 w[kBatch];
+        float f[kBatch];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = bf16lo(in[k]) * f, y = bf16hi(in[k]) * f;
-            th[k] = pack_bf16x2(x, y);
-            const float x1 = x - bf16lo(th[k]), y1 = y - bf16hi(th[k]);
-            tm[k] = pack_bf16x2(x1, y1);
-            tl[k] = pack_bf16x2(x1 - bf16lo(tm[k]), y1 - bf16hi(tm[k]));
+        for (int i = 0; i < kBatch; ++i) {
+          const int j = j0 + i * kStep;
+          w[i] = ld_shared_v4(B + at + i * kStep * 128);
+          f[i] = p.s.up_scale * (rev ? fac[j] : fac[j < len ? -j : 0]);
+          if (j >= len) w[i] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const uint32_t in[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+          const uint64_t ff = f2_pack(f[i], f[i]), zero = f2_pack(0.f, 0.f), minus = f2_pack(-1.f, -1.f);
+          uint64_t v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = f2_fma(f2_pack(bf16lo(in[k]), bf16hi(in[k])), ff, zero);
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float a, b;
+              f2_unpack(v[k], a, b);
+              h[k] = pack_bf16x2(a, b);
+              if (term + 1 < TERMS) v[k] = f2_fma(f2_pack(bf16lo(h[k]), bf16hi(h[k])), minus, v[k]);
+            }
+            st_shared_v4((term == 0 ? B : rest + (term - 1) * (kC * DA * 2)) + at + i * kStep * 128, h[0], h[1], h[2], h[3]);
           }
-          st_shared_v4(B + at, th[0], th[1], th[2], th[3]);
-          st_shared_v4(mid + at, tm[0], tm[1], tm[2], tm[3]);
-          st_shared_v4(lo + at, tl[0], tl[1], tl[2], tl[3]);
-        } else {  // behind the chunk's end: another chunk's or sequence's rows
-          st_shared_v4(B + at, 0, 0, 0, 0);
-          st_shared_v4(mid + at, 0, 0, 0, 0);
-          st_shared_v4(lo + at, 0, 0, 0, 0);
         }
       }
-      for (int v = t0 + len * 8; v < kC * 8; v += threads)
+      for (int v = t0 + len * 8; v < kC * 8; v += 256)
         for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kPanel + v * 16, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&b_ready));
     };
 
-    if (warp < 4) {
-      if constexpr (STATE) {
-        for (int n = 0; n < nchunk; ++n) {
-          if (n > 0) warp_wait(&u_full, n - 1);
-          const int i1 = n * 2;
-          warp_wait(&full[i1 % p.slots], (uint32_t)(i1 / p.slots));
-          warp_wait(&full[(i1 + 1) % p.slots], (uint32_t)((i1 + 1) / p.slots));
-          split(n, 256, tid);
-        }
-      } else {
-        for (int n = 0; n < nchunk; ++n) {
-          const int len = chunk_len(n);
-          warp_wait(&p_full, n);
-          tc_fence_after();
-#pragma unroll 2
-          for (int j0 = 0; j0 < kC; j0 += 16) {
-            uint32_t w[8];
-            // blocks that the mask leaves empty for all of the warp's rows
-            if (rev ? j0 + 15 < 32 * quarter || j0 >= len : j0 > 32 * quarter + 31) {
+    if (warp < 8) {
+      for (int n = 0; n < nchunk; ++n) {
+        const int len = chunk_len(n);
+        warp_wait(&p_full, n);
+        tc_fence_after();
+        // 16 columns at a time (a short loop: the warps of the roles share
+        // the instruction cache); each half's P lies over the first half of
+        // its own scores
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          const int j0 = half * 64 + b * 16, lo_row = 32 * quarter;
+          uint32_t w[8];
+          if (rev ? j0 + 15 < lo_row || j0 >= len : j0 > lo_row + 31) {  // empty for all of the warp's rows
 #pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = 0;
-            } else {
-              uint32_t v[16];
-              tmem_ld16(lanes_at + kColP + j0, v);
-              tmem_ld_wait();
-              float f[16];
+            for (int k = 0; k < 8; ++k) w[k] = 0;
+          } else {
+            uint32_t v[16];
+            tmem_ld16(lanes_at + kColP + j0, v);
+            // 0 where the mask is; a reversed scan's distances grow with the column
+            const float* t = tab + kC + (rev ? j0 - row : row - j0 - 15);
+            float f[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) {
-                const int j = j0 + k, d = rev ? j - row : row - j;
-                f[k] = d >= 0 && (!rev || j < len) ? __uint_as_float(v[k]) * tab[d & (kC - 1)] : 0.f;
-              }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
-            }
-            tmem_st8(lanes_at + kColP + j0 / 2, w);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&p_ready));
-
-          warp_wait(&o_full, n);
-          tc_fence_after();
-          const bool in = row < len;
-          const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
-          const float coef = in ? p.s.in_scale * pw[e] : 0.f;
-          bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(n) + row) * p.s.os + (long long)h * DC;
-#pragma unroll 2
-          for (int c0 = 0; c0 < DC; c0 += 16) {
-            uint32_t x[16], y[16];
-            tmem_ld16(lanes_at + kColO1 + c0, x);
-            tmem_ld16(lanes_at + kColO2 + c0, y);
+            for (int k = 0; k < 16; ++k) f[k] = t[k];
             tmem_ld_wait();
-            uint32_t w[8];
+            if (rev) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              w[k] = ok ? pack_bf16x2(fmaf(coef, __uint_as_float(y[2 * k]), __uint_as_float(x[2 * k])),
-                                      fmaf(coef, __uint_as_float(y[2 * k + 1]), __uint_as_float(x[2 * k + 1])))
-                        : 0x7fc07fc0u;
-            if (in) {
-              if (p.s.wide_out) {
-                st_global_v8(out + c0, w);
-              } else {
-                *reinterpret_cast<uint4*>(out + c0) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(out + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+              for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float x = f[15 - k] * __uint_as_float(v[k]), y = f[k] * __uint_as_float(v[15 - k]);
+                f[k] = x;
+                f[15 - k] = y;
               }
             }
+            if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
+              const int last = rev ? len : row + 1, first = rev ? row : 0;
+#pragma unroll
+              for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&o_free));
+          tmem_st8(lanes_at + kColP + half * 64 + b * 8, w);
         }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&p_ready));
+
+        // b's weighted rows: a b^T has read b, and the last chunk's sums
+        // have read its terms
+        if (n > 0) warp_wait(&u_full, n - 1);
+        const int ib = n * kTiles + 1;
+        warp_wait(&full[ib % p.slots], (uint32_t)(ib / p.slots));
+        if (len < kC) warp_wait(&full[(ib + 1) % p.slots], (uint32_t)((ib + 1) / p.slots));
+        split(n, tid);
+
+        warp_wait(&o_full, n);
+        tc_fence_after();
+        const bool in = row < len;
+        const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
+        const float coef = in ? p.s.in_scale * pw[e] : 0.f;
+        bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(n) + row) * p.s.os + (long long)h * DC;
+#pragma unroll 1
+        for (int c0 = half * (DC / 2); c0 < (half + 1) * (DC / 2); c0 += 32) {
+          uint32_t x[32], y[32];
+          tmem_ld16(lanes_at + kColO1 + c0, x);
+          tmem_ld16(lanes_at + kColO2 + c0, y);
+          tmem_ld16(lanes_at + kColO1 + c0 + 16, x + 16);
+          tmem_ld16(lanes_at + kColO2 + c0 + 16, y + 16);
+          tmem_ld_wait();
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k)
+            w[k] = ok ? pack_bf16x2(fmaf(coef, __uint_as_float(y[2 * k]), __uint_as_float(x[2 * k])),
+                                    fmaf(coef, __uint_as_float(y[2 * k + 1]), __uint_as_float(x[2 * k + 1])))
+                      : 0x7fc07fc0u;
+          if (in) {
+            if (p.s.wide_out) {
+              st_global_v8(out + c0, w);
+              st_global_v8(out + c0 + 16, w + 8);
+            } else {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                reinterpret_cast<uint4*>(out + c0)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&o_free));
       }
     } else {
-      // the state: thread `row` holds S[0 .. DA)[row]
-      float S[DA];
+      // the state: a thread holds S[d0 .. d0 + DH)[row]
+      constexpr int DH = DA / 2;
+      const int d0 = half * DH;
+      float S[DH];
       const long long st = ((long long)(p.seg_state ? seg_i : sg.seq) * p.s.H + h) * DA * DC;
-      const float* from = STATE ? nullptr : p.seg_state ? p.seg_state : p.s.s_in;
+      const float* from = p.seg_state ? p.seg_state : p.s.s_in;
       const bool mine = row < DC && live;
       if (from && mine) {
         if (p.s.transposed) {
 #pragma unroll
-          for (int d = 0; d < DA; d += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(from + st + (long long)row * DA + d);
+          for (int d = 0; d < DH; d += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(from + st + (long long)row * DA + d0 + d);
             S[d] = v.x, S[d + 1] = v.y, S[d + 2] = v.z, S[d + 3] = v.w;
           }
         } else {
 #pragma unroll
-          for (int d = 0; d < DA; ++d) S[d] = from[st + d * DC + row];
+          for (int d = 0; d < DH; ++d) S[d] = from[st + (d0 + d) * DC + row];
         }
       } else {
 #pragma unroll
-        for (int d = 0; d < DA; ++d) S[d] = 0.f;
+        for (int d = 0; d < DH; ++d) S[d] = 0.f;
+      }
+      // S rounded to bf16 for a S: 8 values of this thread's row, [DC rows][DA]
+      // in the 128-byte swizzle
+      auto put = [&](int d) {
+        const int at = d0 + d;
+        if (row < DC)
+          st_shared_v4(s_buf + at / 64 * (DC * 128) + row * 128 + (((at / 8) ^ row) & 7) * 16, pack_bf16x2(S[d], S[d + 1]),
+                       pack_bf16x2(S[d + 2], S[d + 3]), pack_bf16x2(S[d + 4], S[d + 5]), pack_bf16x2(S[d + 6], S[d + 7]));
+      };
+      auto put_done = [&] {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&s_ready));
+      };
+      if (nchunk > 0) {
+#pragma unroll
+        for (int d = 0; d < DH; d += 8) put(d);
+        put_done();
       }
       for (int n = 0; n < nchunk; ++n) {
-        if constexpr (!STATE) {
-          // rounded to bf16 for a S, [DC rows][DA] in the 128-byte swizzle
-          // (chunk n - 1's a S was done before its U, waited for below)
-          if (row < DC) {
-#pragma unroll
-            for (int d = 0; d < DA; d += 8)
-              st_shared_v4(s_buf + d / 64 * (DC * 128) + row * 128 + (((d / 8) ^ row) & 7) * 16, pack_bf16x2(S[d], S[d + 1]),
-                           pack_bf16x2(S[d + 2], S[d + 3]), pack_bf16x2(S[d + 4], S[d + 5]), pack_bf16x2(S[d + 6], S[d + 7]));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&s_ready));
-        }
-        const int ib = n * kTiles + kTiles - 2;
-        warp_wait(&full[ib % p.slots], (uint32_t)(ib / p.slots));
-        if (STATE || chunk_len(n) < kC) warp_wait(&full[(ib + 1) % p.slots], (uint32_t)((ib + 1) / p.slots));
-        if constexpr (!STATE) warp_wait(&p_full, n);  // a b^T has read b
-        split(n, 32 * kSplitWarps, STATE ? tid : tid - 128);
-        warp_wait(&u_full, n);
-        tc_fence_after();
         const float decay = expf(g * (float)chunk_len(n));
+        warp_wait(&u_full, n);  // and a S before it
+        tc_fence_after();
+        const bool next = n + 1 < nchunk;
 #pragma unroll
-        for (int d = 0; d < DA; d += 16) {
+        for (int d = 0; d < DH; d += 16) {
           uint32_t v[16];
-          tmem_ld16(lanes_at + kColU + d, v);
+          tmem_ld16(lanes_at + kColU + d0 + d, v);
           tmem_ld_wait();
 #pragma unroll
           for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]));
+          if (next) {
+            put(d);
+            put(d + 8);
+          }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&u_free));
+        if (next) put_done();
       }
-      // STATE: the segment's own state; the scan: behind a sequence's end
-      const bool emit = STATE ? work : live && sg.last && p.s.s_out;
-      if (emit && mine) {
-        float* to = STATE ? p.seg_state : p.s.s_out;
-        const long long at = STATE ? st : ((long long)sg.seq * p.s.H + h) * DA * DC;
+      // the state behind a sequence in one piece (segments: joined before)
+      if (mine && p.s.s_out && !p.seg_state) {
+        float* to = p.s.s_out + st;
         const float nan = __int_as_float(0x7fc00000);
         if (p.s.transposed) {
 #pragma unroll
-          for (int d = 0; d < DA; d += 4)
-            *reinterpret_cast<float4*>(to + at + (long long)row * DA + d) =
+          for (int d = 0; d < DH; d += 4)
+            *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
                 ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
         } else {
 #pragma unroll
-          for (int d = 0; d < DA; ++d) to[at + d * DC + row] = ok ? S[d] : nan;
+          for (int d = 0; d < DH; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
         }
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == 17) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Every segment's own state, sum_j l^{len-1-j} b_j c_j^T over its tokens, in
+// half chunks of 64 tokens: while the tensor cores take one half, sixteen
+// warps weigh the rows of the next (its terms have a second buffer) and add
+// the last whole chunk's sums, from one of two accumulators in TMEM, to the
+// state (a quarter of a row of DA per thread).  The bound is HBM.
+constexpr int kHalf = kC / 2;
+constexpr int kHalfPanel = kHalf * 128;  // bytes of 64 channels of a half chunk
+
+template <int DA, int DC>
+__global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_constant__ ScanTcParams p) {
+  constexpr int kTileB = kHalf * DA * 2, kStage = kHalf * (DA + DC) * 2;
+  constexpr uint32_t kColU = 128;  // columns between the accumulators
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], b_ready[2], t_free[2], u_full[2], u_free[2];
+  __shared__ uint32_t tmem_base;
+  __shared__ float pw[kC + 2];  // l^i
+  // stages (b, c), then two buffers of two terms (which an operand of 64
+  // channels reads into behind the last stage: rows of its product not used)
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + p.slots * kStage;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
+
+  if (tid == 0) {
+    for (int s = 0; s < p.slots; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&b_ready[b]), 16);
+      mbar_init(smem_addr(&t_free[b]), 1);
+      mbar_init(smem_addr(&u_full[b]), 1);
+      mbar_init(smem_addr(&u_free[b]), 16);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 17) tmem_alloc(smem_addr(&tmem_base), 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  const float g = __ldg(p.s.log_decay + h);
+  if (tid < kC + 2) pw[tid] = expf(g * (float)tid);
+  __syncthreads();
+  Segment sg{0, 0, 0, 1};
+  if (!p.nsegs || seg_i < *p.nsegs) sg = segment_of(p, seg_i);
+  const bool work = sg.len > 0 && !(sg.last && !p.s.s_out);  // a last segment's own state is part of the final one only
+  const int nchunk = work ? (sg.len + kC - 1) / kC : 0;
+  const bool rev = p.s.reverse;
+  auto chunk_len = [&](int n) { return sg.len - n * kC < kC ? sg.len - n * kC : kC; };
+  auto chunk_at = [&](int n) { return rev ? sg.first + sg.len - n * kC - chunk_len(n) : sg.first + n * kC; };
+  // halves: two per chunk, one where the last chunk has at most 64 tokens
+  const int nhalf = nchunk > 0 ? 2 * nchunk - (chunk_len(nchunk - 1) <= kHalf ? 1 : 0) : 0;
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (ok && !mbar_wait_bounded(smem_addr(bar), parity & 1u, p.wait_ns)) {
+      report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+      ok = false;
+    }
+  };
+  auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
+    wait(bar, parity);
+    ok = __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp == 16) {
+    if (lane == 0) {
+      int i = 0;
+      for (; i < nhalf; ++i) {
+        const int st = i % p.slots, t = chunk_at(i / 2) + i % 2 * kHalf;
+        wait(&empty[st], (uint32_t)(i / p.slots) + 1u);
+        if (!ok) break;
+        const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
+        mbar_arrive_expect_tx(fb, kStage);
+#pragma unroll
+        for (int x = 0; x < DA; x += 64) tma_load_2d(to + x / 64 * kHalfPanel, &p.mb, h * DA + x, t, fb);
+#pragma unroll
+        for (int x = 0; x < DC; x += 64) tma_load_2d(to + kTileB + x / 64 * kHalfPanel, &p.mc, h * DC + x, t, fb);
+      }
+      // the CTA never exits under a copy
+      const int armed = i < p.slots ? i : p.slots;
+      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((i - 1 - st) / p.slots) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 17) {
+    if (lane == 0) {
+      constexpr uint32_t kI = tc_idesc_bf16(128, DA, true, true);
+      for (int i = 0; i < nhalf && ok; ++i) {
+        const int st = i % p.slots, n = i / 2;
+        const uint32_t d = tmem + (n & 1) * kColU;
+        wait(&b_ready[i & 1], (uint32_t)(i / 2));
+        if (i % 2 == 0) wait(&u_free[n & 1], (uint32_t)(n / 2) + 1u);
+        tc_fence_after();
+        const uint64_t dc = smem_desc_mn128(base + st * kStage + kTileB, kHalfPanel);
+#pragma unroll
+        for (int term = 0; term < 3; ++term) {
+          const uint64_t dt = smem_desc_mn128(term == 0 ? base + st * kStage : rest + ((i & 1) * 2 + term - 1) * kTileB, kHalfPanel);
+#pragma unroll
+          for (int kk = 0; kk < kHalf / 16; ++kk) tc_mma_bf16(d, dc + kk * 128, dt + kk * 128, kI, i % 2 > 0 || term > 0 || kk > 0);
+        }
+        tc_commit(smem_addr(&empty[st]));
+        tc_commit(smem_addr(&t_free[i & 1]));
+        if (i % 2 == 1 || i == nhalf - 1) tc_commit(smem_addr(&u_full[n & 1]));
+      }
+    }
+    __syncwarp();
+  } else {
+    // thread: row `row` of the state, DA / 4 of its values from d0
+    constexpr int DQ = DA / 4;
+    const int row = 32 * (warp & 3) + lane, d0 = (warp >> 2) * DQ;
+    const uint32_t from = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + d0;
+    float S[DQ];
+#pragma unroll
+    for (int d = 0; d < DQ; ++d) S[d] = 0.f;
+    auto add = [&](int n) {
+      const float decay = expf(g * (float)chunk_len(n));
+      warp_wait(&u_full[n & 1], (uint32_t)(n / 2));
+      tc_fence_after();
+#pragma unroll
+      for (int d = 0; d < DQ; d += 16) {
+        uint32_t v[16];
+        tmem_ld16(from + (n & 1) * kColU + d, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&u_free[n & 1]));
+    };
+    for (int i = 0; i < nhalf; ++i) {
+      const int st = i % p.slots, len = chunk_len(i / 2), j0 = i % 2 * kHalf;  // rows j0 .. of the chunk
+      const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + (i & 1) * 2 * kTileB;
+      warp_wait(&full[st], (uint32_t)(i / p.slots));
+      warp_wait(&t_free[i & 1], (uint32_t)(i / 2) + 1u);
+      // one vector of 8 channels per thread and panel of 64: row tid / 8
+      const int j = j0 + tid / 8;
+      const float f = j < len ? p.s.up_scale * pw[p.s.shift + (rev ? j : len - 1 - j)] : 0.f;
+      uint4 w[DA / 64];
+#pragma unroll
+      for (int x = 0; x < DA / 64; ++x) {
+        w[x] = ld_shared_v4(B + x * kHalfPanel + tid * 16);
+        if (j >= len) w[x] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+      }
+#pragma unroll
+      for (int x = 0; x < DA / 64; ++x) {
+        const uint32_t at = x * kHalfPanel + tid * 16, in[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+        uint32_t th[4], tm[4], tl[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float a = bf16lo(in[k]) * f, b = bf16hi(in[k]) * f;
+          th[k] = pack_bf16x2(a, b);
+          const float a1 = a - bf16lo(th[k]), b1 = b - bf16hi(th[k]);
+          tm[k] = pack_bf16x2(a1, b1);
+          tl[k] = pack_bf16x2(a1 - bf16lo(tm[k]), b1 - bf16hi(tm[k]));
+        }
+        st_shared_v4(B + at, th[0], th[1], th[2], th[3]);
+        st_shared_v4(T + at, tm[0], tm[1], tm[2], tm[3]);
+        st_shared_v4(T + kTileB + at, tl[0], tl[1], tl[2], tl[3]);
+      }
+      if (j >= len) {
+#pragma unroll
+        for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kHalfPanel + tid * 16, 0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&b_ready[i & 1]));
+      if (i % 2 == 1 && i > 1) add(i / 2 - 1);
+    }
+    if (nchunk > 1 && nhalf % 2 == 1) add(nchunk - 2);
+    if (nchunk > 0) add(nchunk - 1);
+    if (work && row < DC) {
+      float* to = p.seg_state + ((long long)seg_i * p.s.H + h) * DA * DC;
+      const float nan = __int_as_float(0x7fc00000);
+      if (p.s.transposed) {
+#pragma unroll
+        for (int d = 0; d < DQ; d += 4)
+          *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
+              ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
+      } else {
+#pragma unroll
+        for (int d = 0; d < DQ; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 17) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -502,7 +740,7 @@ __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu
 }
 
 // Per sequence and head: the state before each segment, from the segments'
-// own states, in place (and in order).
+// own states, in place and in order, and the final state.
 __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__ ScanTcParams p, const int* first_of, int per_head) {
   const long long e = (blockIdx.x * 256LL + threadIdx.x) * 4;  // over [H][Da Dc]
   const int n = blockIdx.y;
@@ -518,15 +756,28 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
     const float* in = p.s.s_in + n * all + e;
     w = make_float4(in[0], in[1], in[2], in[3]);
   }
-  for (int s = s0; s < s1; ++s) {
-    float4* at = reinterpret_cast<float4*>(p.seg_state + s * all + e);
-    const Segment sg = segment_of(p, s);
-    float4 u = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (!sg.last) u = *at;
-    *at = w;
-    const float d = expf(g * (float)sg.len);
-    w = make_float4(fmaf(w.x, d, u.x), fmaf(w.y, d, u.y), fmaf(w.z, d, u.z), fmaf(w.w, d, u.w));
+  // four segments' states are loaded before the first of them is replaced
+  constexpr int kAhead = 4;
+  for (int s = s0; s < s1; s += kAhead) {
+    float4 u[kAhead];
+    float d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      d[i] = 1.f;
+      if (s + i < s1) {
+        const Segment sg = segment_of(p, s + i);
+        d[i] = expf(g * (float)sg.len);
+        if (sg.len > 0 && (!sg.last || p.s.s_out)) u[i] = *reinterpret_cast<const float4*>(p.seg_state + (s + i) * all + e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s + i < s1) *reinterpret_cast<float4*>(p.seg_state + (s + i) * all + e) = w;
+      w = make_float4(fmaf(w.x, d[i], u[i].x), fmaf(w.y, d[i], u[i].y), fmaf(w.z, d[i], u[i].z), fmaf(w.w, d[i], u[i].w));
+    }
   }
+  if (p.s.s_out) *reinterpret_cast<float4*>(p.s.s_out + n * all + e) = w;
 }
 
 int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -545,31 +796,50 @@ Layout layout(int64_t T, int H, int Dk, int Dv, int N, int seg_len) {
   return L;
 }
 
-template <int DA, int DC, bool STATE>
-cudaError_t launch_tile(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+template <int DA, int DC, int TERMS>
+cudaError_t launch_scan_tile(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
   constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;
-  const int fixed = (STATE ? 0 : DC * DA * 2) + 2 * kC * DA * 2 + 1024;
-  const int smem_max = di.max_smem_optin - 2560;  // barriers and power tables are static
+  const int fixed = DC * DA * 2 + (TERMS - 1) * kC * DA * 2 + 1024;
+  const int smem_max = di.max_smem_optin - 2048;  // barriers and power tables are static
   p.slots = (smem_max - fixed) / kTile;
   if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  if (p.slots < (STATE ? 2 : 3)) return cudaErrorInvalidValue;
+  if (p.slots < 4) return cudaErrorInvalidValue;
   static SmemOptIn optin;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(scan_tc_kernel<DA, DC, STATE>), smem_max);
+  const auto kern = scan_tc_kernel<DA, DC, TERMS>;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), smem_max);
   if (e != cudaSuccess) return e;
-  return launch_kernel(scan_tc_kernel<DA, DC, STATE>, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)(fixed + p.slots * kTile),
-                       stream, p);
+  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)(fixed + p.slots * kTile), stream, p);
 }
 
-template <bool STATE>
-cudaError_t launch_dims(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
-  if (p.s.Da == 128) return p.s.Dc == 128 ? launch_tile<128, 128, STATE>(p, segs, di, stream) : launch_tile<128, 64, STATE>(p, segs, di, stream);
-  return p.s.Dc == 128 ? launch_tile<64, 128, STATE>(p, segs, di, stream) : launch_tile<64, 64, STATE>(p, segs, di, stream);
+template <int TERMS>
+cudaError_t launch_scan_dims(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+  if (p.s.Da == 128)
+    return p.s.Dc == 128 ? launch_scan_tile<128, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<128, 64, TERMS>(p, segs, di, stream);
+  return p.s.Dc == 128 ? launch_scan_tile<64, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<64, 64, TERMS>(p, segs, di, stream);
 }
 
-bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_t stride) {
+template <int DA, int DC>
+cudaError_t launch_state_tile(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+  constexpr int kStage = kHalf * (DA + DC) * 2, kFixed = 4 * kHalf * DA * 2 + 1024;
+  const int smem_max = di.max_smem_optin - 2048;
+  p.slots = (smem_max - kFixed) / kStage;
+  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+  static SmemOptIn optin;
+  const auto kern = state_tc_kernel<DA, DC>;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), smem_max);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)(kFixed + p.slots * kStage), stream, p);
+}
+
+cudaError_t launch_state_dims(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+  if (p.s.Da == 128) return p.s.Dc == 128 ? launch_state_tile<128, 128>(p, segs, di, stream) : launch_state_tile<128, 64>(p, segs, di, stream);
+  return p.s.Dc == 128 ? launch_state_tile<64, 128>(p, segs, di, stream) : launch_state_tile<64, 64>(p, segs, di, stream);
+}
+
+bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_t stride, int tokens = kC) {
   const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)T};
   const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, kC};
+  const cuuint32_t box[2] = {64, (cuuint32_t)tokens};
   return make_tensor_map(m, ptr, 2, dims, strides, box);
 }
 
@@ -596,6 +866,11 @@ int scan_tc_segment(int64_t T, int H, int N, int sm_count) {
     }
   }
   return seg;
+}
+
+bool scan_tc_segmented(int64_t T, int H, int N) {
+  DeviceInfo di;
+  return device_info(&di) == cudaSuccess && scan_tc_segment(T, H, N, di.sm_count) > 0;
 }
 
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N) {
@@ -642,7 +917,10 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready
                           first_of + s.N + 1);
         if (e != cudaSuccess) return e;
       }
-      e = launch_dims<true>(p, segs, di, stream);
+      ScanTcParams ps = p;
+      if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))
+        return cudaErrorInvalidValue;
+      e = launch_state_dims(ps, segs, di, stream);
       if (e != cudaSuccess) return e;
       const int per_head = s.Da * s.Dc;
       e = launch_kernel(la_combine_kernel, dim3((unsigned)(((int64_t)s.H * per_head / 4 + 255) / 256), s.N), dim3(256), 0, stream, p,
@@ -650,7 +928,7 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready
       if (e != cudaSuccess) return e;
     }
   }
-  return launch_dims<false>(p, segs, di, stream);
+  return s.s_out && p.seg_len == 0 ? launch_scan_dims<3>(p, segs, di, stream) : launch_scan_dims<2>(p, segs, di, stream);
 }
 
 }  // namespace attnres
