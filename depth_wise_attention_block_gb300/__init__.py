@@ -461,36 +461,55 @@ def activation_code(activation: str) -> int:
         raise ValueError(f"unknown activation {activation!r}; use one of {sorted(_ACT)}") from None
 
 
-def _rows(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype) -> tuple[int | None, int]:
-    """Pointer and row stride (elements) of a tensor whose rows (everything
-    behind the first dimension) are contiguous; None: (None, row length)."""
-    width = 1
-    for n in shape[1:]:
-        width *= n
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device_of(t, name: str) -> int:
+    """The current device, on which a call's first tensor has to be."""
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0 or dev != _get_device():
+        _dev_ptr(t, name, contiguous=False)
+    return dev
+
+
+def _where(t, name: str, dtype: torch.dtype, cur: int) -> None:
+    """Say what is wrong with a tensor that is not of `dtype` on device `cur`."""
+    _dev_ptr(t, name, dtype, contiguous=False)
+    raise ValueError(f"{name} is on {t.device} but the current device is cuda:{cur}")
+
+
+def _rows(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, cur: int) -> tuple[int | None, int]:
+    """Pointer and row stride (elements) of a tensor on device `cur` whose
+    rows (everything behind the first dimension) are contiguous; None:
+    (None, row length)."""
+    width = shape[1] if len(shape) == 2 else shape[1] * shape[2]
     if t is None:
         return None, width
-    ptr = _dev_ptr(t, name, dtype, contiguous=False)
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur or t.dtype is not dtype:
+        _where(t, name, dtype, cur)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.is_contiguous():
-        return ptr, width
-    st, inner = t.stride(), 1
-    for n, s in zip(reversed(shape[1:]), reversed(st[1:])):
-        if n > 1 and s != inner:
-            raise ValueError(f"the rows of {name} must be contiguous")
-        inner *= n
+        return t.data_ptr(), width
+    st, last = t.stride(), shape[-1]
+    if (st[-1] != 1 and last > 1) or (len(shape) == 3 and st[1] != last and shape[1] > 1):
+        raise ValueError(f"the rows of {name} must be contiguous")
     if shape[0] > 1 and st[0] < width:
         raise ValueError(f"the rows of {name} overlap")
-    return ptr, st[0] if shape[0] > 1 else width
+    return t.data_ptr(), st[0] if shape[0] > 1 else width
 
 
-def _vec(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype) -> int | None:
+def _vec(t: torch.Tensor | None, name: str, shape: tuple, dtype: torch.dtype, cur: int) -> int | None:
+    """Pointer of a contiguous tensor on device `cur`."""
     if t is None:
         return None
-    ptr = _dev_ptr(t, name, dtype)
+    if not isinstance(t, torch.Tensor) or t.get_device() != cur or t.dtype is not dtype:
+        _where(t, name, dtype, cur)
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    return ptr
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _workspace(workspace: torch.Tensor | None, nbytes: int, device, stream) -> tuple[torch.Tensor | None, int | None, int]:
@@ -537,13 +556,14 @@ def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: to
     dt = x.dtype
     code = dtype_code(dt)
     act = activation_code(activation)
-    xp, ldx = _rows(x, "x", (M, K), dt)
-    wp = _vec(w, "w", (N, K), dt)
-    op, ldo = _rows(out, "out", (M, N), dt)
-    rp, ldr = _rows(residual, "residual", (M, N), dt)
+    cur = _device_of(x, "x")
+    xp, ldx = _rows(x, "x", (M, K), dt, cur)
+    wp = _vec(w, "w", (N, K), dt, cur)
+    op, ldo = _rows(out, "out", (M, N), dt, cur)
+    rp, ldr = _rows(residual, "residual", (M, N), dt, cur)
     need = 0 if workspace is not None else attnres_linear_workspace_size(M, N, K, dt)
     _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
-    rc = _N.lib.attnres_linear(xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32), rp, ldr, op, ldo, M, N, K, code, act,
+    rc = _N.lib.attnres_linear(xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), rp, ldr, op, ldo, M, N, K, code, act,
                                ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
     _N.check(rc, "attnres_linear")
 
@@ -567,14 +587,15 @@ def attnres_linear_backward(x: torch.Tensor, w: torch.Tensor, grad_out: torch.Te
     dt = x.dtype
     code = dtype_code(dt)
     act = activation_code(activation)
-    xp, ldx = _rows(x, "x", (M, K), dt)
-    wp = _vec(w, "w", (N, K), dt)
-    gp, ldg = _rows(grad_out, "grad_out", (M, N), dt)
+    cur = _device_of(x, "x")
+    xp, ldx = _rows(x, "x", (M, K), dt, cur)
+    wp = _vec(w, "w", (N, K), dt, cur)
+    gp, ldg = _rows(grad_out, "grad_out", (M, N), dt, cur)
     need = 0 if workspace is not None else attnres_linear_backward_workspace_size(M, N, K, dt, activation)
     _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
     rc = _N.lib.attnres_linear_backward(
-        xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32), gp, ldg, _vec(grad_x, "grad_x", (M, K), dt),
-        _vec(grad_w, "grad_w", (N, K), dt), _vec(grad_bias, "grad_bias", (N,), torch.float32), M, N, K, code, act, ws,
+        xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), gp, ldg, _vec(grad_x, "grad_x", (M, K), dt, cur),
+        _vec(grad_w, "grad_w", (N, K), dt, cur), _vec(grad_bias, "grad_bias", (N,), torch.float32, cur), M, N, K, code, act, ws,
         nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
     _N.check(rc, "attnres_linear_backward")
 
@@ -585,19 +606,19 @@ def _heads(t: torch.Tensor | None, name: str) -> tuple[int, int, int]:
     return tuple(t.shape)
 
 
-def _qk_sizes(q, k):
+def _qk_sizes(q, k, positions, inv_freq):
     """(T, D, dtype, Hq, Hk) of a q and a k, either of them None."""
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
     first = q if q is not None else k
     T, _, D = _heads(first, "q" if q is not None else "k")
     return T, D, first.dtype, q.shape[1] if q is not None else 0, _heads(k, "k")[1] if k is not None else 0
 
 
-def _rope_args(T: int, positions, inv_freq, interleaved: bool):
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq come together")
+def _rope_args(T: int, positions, inv_freq, interleaved: bool, cur: int):
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return (_vec(positions, "positions", (T,), torch.int64),
-            _vec(inv_freq, "inv_freq", (rot // 2,), torch.float32), rot, int(bool(interleaved)))
+    return (_vec(positions, "positions", (T,), torch.int64, cur),
+            _vec(inv_freq, "inv_freq", (rot // 2,), torch.float32, cur), rot, int(bool(interleaved)))
 
 
 def attnres_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: torch.Tensor | None,
@@ -610,14 +631,16 @@ def attnres_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: 
     2 len(inv_freq) channels by positions [T] int64 times inv_freq float32
     (both None: no rotation).  Heads and channels contiguous, tokens at any
     stride; q_out may be q and k_out k."""
-    T, D, dt, Hq, Hk = _qk_sizes(q, k)
-    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved)
-    qp, qs = _rows(q, "q", (T, Hq, D), dt)
-    kp, ks = _rows(k, "k", (T, Hk, D), dt)
-    qo, qos = _rows(q_out if q is not None else None, "q_out", (T, Hq, D), dt)
-    ko, kos = _rows(k_out if k is not None else None, "k_out", (T, Hk, D), dt)
-    rc = _N.lib.attnres_qk_norm_rope(qp, qs, Hq, kp, ks, Hk, T, D, dtype_code(dt), _vec(q_gain, "q_gain", (D,), torch.float32),
-                                     _vec(k_gain, "k_gain", (D,), torch.float32), float(eps), pos, freq, rot, inter,
+    T, D, dt, Hq, Hk = _qk_sizes(q, k, positions, inv_freq)
+    code = dtype_code(dt)
+    cur = _device_of(q if q is not None else k, "q" if q is not None else "k")
+    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved, cur)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt, cur)
+    kp, ks = _rows(k, "k", (T, Hk, D), dt, cur)
+    qo, qos = _rows(q_out if q is not None else None, "q_out", (T, Hq, D), dt, cur)
+    ko, kos = _rows(k_out if k is not None else None, "k_out", (T, Hk, D), dt, cur)
+    rc = _N.lib.attnres_qk_norm_rope(qp, qs, Hq, kp, ks, Hk, T, D, code, _vec(q_gain, "q_gain", (D,), torch.float32, cur),
+                                     _vec(k_gain, "k_gain", (D,), torch.float32, cur), float(eps), pos, freq, rot, inter,
                                      qo, qos, ko, kos, _stream_ptr(stream))
     _N.check(rc, "attnres_qk_norm_rope")
 
@@ -639,44 +662,47 @@ def attnres_qk_norm_rope_backward(q: torch.Tensor | None, k: torch.Tensor | None
     """Gradients of attnres_qk_norm_rope, from the forward's inputs (q and k
     as they were before it).  grad_q may be grad_q_out and grad_k grad_k_out;
     the gain gradients ([D] float32) are overwritten, or skipped when None."""
-    T, D, dt, Hq, Hk = _qk_sizes(q, k)
-    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved)
-    qp, qs = _rows(q, "q", (T, Hq, D), dt)
-    kp, ks = _rows(k, "k", (T, Hk, D), dt)
-    gqo, gqos = _rows(grad_q_out if q is not None else None, "grad_q_out", (T, Hq, D), dt)
-    gko, gkos = _rows(grad_k_out if k is not None else None, "grad_k_out", (T, Hk, D), dt)
-    gq, gqs = _rows(grad_q if q is not None else None, "grad_q", (T, Hq, D), dt)
-    gk, gks = _rows(grad_k if k is not None else None, "grad_k", (T, Hk, D), dt)
-    dgq = _vec(grad_q_gain, "grad_q_gain", (D,), torch.float32)
-    dgk = _vec(grad_k_gain, "grad_k_gain", (D,), torch.float32)
+    T, D, dt, Hq, Hk = _qk_sizes(q, k, positions, inv_freq)
+    code = dtype_code(dt)
+    cur = _device_of(q if q is not None else k, "q" if q is not None else "k")
+    pos, freq, rot, inter = _rope_args(T, positions, inv_freq, interleaved, cur)
+    qp, qs = _rows(q, "q", (T, Hq, D), dt, cur)
+    kp, ks = _rows(k, "k", (T, Hk, D), dt, cur)
+    gqo, gqos = _rows(grad_q_out if q is not None else None, "grad_q_out", (T, Hq, D), dt, cur)
+    gko, gkos = _rows(grad_k_out if k is not None else None, "grad_k_out", (T, Hk, D), dt, cur)
+    gq, gqs = _rows(grad_q if q is not None else None, "grad_q", (T, Hq, D), dt, cur)
+    gk, gks = _rows(grad_k if k is not None else None, "grad_k", (T, Hk, D), dt, cur)
+    dgq = _vec(grad_q_gain, "grad_q_gain", (D,), torch.float32, cur)
+    dgk = _vec(grad_k_gain, "grad_k_gain", (D,), torch.float32, cur)
     need = 0
     if workspace is None and (dgq is not None or dgk is not None):
         need = attnres_qk_norm_rope_backward_workspace_size(T, Hq, Hk, D)
     _keep, ws, nbytes = _workspace(workspace, need, (q if q is not None else k).device, stream)
     rc = _N.lib.attnres_qk_norm_rope_backward(
-        qp, qs, Hq, kp, ks, Hk, T, D, dtype_code(dt), _vec(q_gain, "q_gain", (D,), torch.float32),
-        _vec(k_gain, "k_gain", (D,), torch.float32), float(eps), pos, freq, rot, inter, gqo, gqos, gko, gkos, gq, gqs,
+        qp, qs, Hq, kp, ks, Hk, T, D, code, _vec(q_gain, "q_gain", (D,), torch.float32, cur),
+        _vec(k_gain, "k_gain", (D,), torch.float32, cur), float(eps), pos, freq, rot, inter, gqo, gqos, gko, gkos, gq, gqs,
         gk, gks, dgq, dgk, ws, nbytes, _stream_ptr(stream))
     _N.check(rc, "attnres_qk_norm_rope_backward")
 
 
-def _attention_args(q, k, v, log_decay, cu_seqlens):
+def _attention_args(q, k, v, log_decay, cu_seqlens, cur: int):
     T, H, Dk = _heads(q, "q")
     Dv = _heads(v, "v")[2]
     dt = q.dtype
-    qp, qs = _rows(q, "q", (T, H, Dk), dt)
-    kp, ks = _rows(k, "k", (T, H, Dk), dt)
-    vp, vs = _rows(v, "v", (T, H, Dv), dt)
+    code = dtype_code(dt)
+    qp, qs = _rows(q, "q", (T, H, Dk), dt, cur)
+    kp, ks = _rows(k, "k", (T, H, Dk), dt, cur)
+    vp, vs = _rows(v, "v", (T, H, Dv), dt, cur)
     if isinstance(log_decay, torch.Tensor) and log_decay.requires_grad:
         raise ValueError("log_decay is a constant: it gets no gradient")
-    g = _vec(log_decay, "log_decay", (H,), torch.float32)
+    g = _vec(log_decay, "log_decay", (H,), torch.float32, cur)
     N = 1
     if cu_seqlens is not None:
         N = cu_seqlens.numel() - 1
         if N < 1:
             raise ValueError("cu_seqlens must hold at least two offsets")
-    cu = _vec(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32)
-    return T, H, Dk, Dv, dt, (qp, qs, kp, ks, vp, vs, T, H, Dk, Dv, dtype_code(dt), g), cu, N
+    cu = _vec(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, cur)
+    return T, H, Dk, Dv, dt, (qp, qs, kp, ks, vp, vs, T, H, Dk, Dv, code, g), cu, N
 
 
 def attnres_linear_attention_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: torch.dtype, num_seqs: int = 1) -> int:
@@ -698,11 +724,12 @@ def attnres_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     device (None: one sequence); initial_state, final_state: [num_seqs, H,
     Dk, Dv] float32 or None, possibly the same tensor.
     """
-    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens)
-    op, os_ = _rows(out, "out", (T, H, Dv), dt)
+    cur = _device_of(q, "q")
+    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens, cur)
+    op, os_ = _rows(out, "out", (T, H, Dv), dt, cur)
     shape = (N, H, Dk, Dv)
-    s0 = _vec(initial_state, "initial_state", shape, torch.float32)
-    s1 = _vec(final_state, "final_state", shape, torch.float32)
+    s0 = _vec(initial_state, "initial_state", shape, torch.float32, cur)
+    s1 = _vec(final_state, "final_state", shape, torch.float32, cur)
     need = 0 if workspace is not None else attnres_linear_attention_workspace_size(T, H, Dk, Dv, dt, N)
     _keep, ws, nbytes = _workspace(workspace, need, q.device, stream)
     rc = _N.lib.attnres_linear_attention(*head, cu, N, s0, s1, float(Dk ** -0.5 if scale is None else scale), op, os_,
@@ -727,17 +754,18 @@ def attnres_linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch
                                       stream=None) -> None:
     """Gradients of attnres_linear_attention from the forward's inputs
     (grad_q, grad_k, grad_v contiguous, of q's dtype; the states' float32)."""
-    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens)
-    gp, gs = _rows(grad_out, "grad_out", (T, H, Dv), dt)
+    cur = _device_of(q, "q")
+    T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens, cur)
+    gp, gs = _rows(grad_out, "grad_out", (T, H, Dv), dt, cur)
     shape = (N, H, Dk, Dv)
-    s0 = _vec(initial_state, "initial_state", shape, torch.float32)
-    ds1 = _vec(grad_final_state, "grad_final_state", shape, torch.float32)
-    ds0 = _vec(grad_initial_state, "grad_initial_state", shape, torch.float32)
+    s0 = _vec(initial_state, "initial_state", shape, torch.float32, cur)
+    ds1 = _vec(grad_final_state, "grad_final_state", shape, torch.float32, cur)
+    ds0 = _vec(grad_initial_state, "grad_initial_state", shape, torch.float32, cur)
     need = 0 if workspace is not None else attnres_linear_attention_backward_workspace_size(T, H, Dk, Dv, dt, N)
     _keep, ws, nbytes = _workspace(workspace, need, q.device, stream)
     rc = _N.lib.attnres_linear_attention_backward(
-        *head, cu, N, s0, float(Dk ** -0.5 if scale is None else scale), gp, gs, ds1, _vec(grad_q, "grad_q", (T, H, Dk), dt),
-        _vec(grad_k, "grad_k", (T, H, Dk), dt), _vec(grad_v, "grad_v", (T, H, Dv), dt), ds0, ws, nbytes,
+        *head, cu, N, s0, float(Dk ** -0.5 if scale is None else scale), gp, gs, ds1, _vec(grad_q, "grad_q", (T, H, Dk), dt, cur),
+        _vec(grad_k, "grad_k", (T, H, Dk), dt, cur), _vec(grad_v, "grad_v", (T, H, Dv), dt, cur), ds0, ws, nbytes,
         _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
     _N.check(rc, "attnres_linear_attention_backward")
 
@@ -749,13 +777,14 @@ def attnres_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     slots[b] (int32; None: b) updated in place, out [B, H, Dv] written.  A
     slot outside the pool marks a padding row (its out row stays); rows of
     one slot are consecutive tokens in row order."""
-    B, H, Dk, Dv, dt, head, _, _ = _attention_args(q, k, v, log_decay, None)
-    op, os_ = _rows(out, "out", (B, H, Dv), dt)
+    cur = _device_of(q, "q")
+    B, H, Dk, Dv, dt, head, _, _ = _attention_args(q, k, v, log_decay, None, cur)
+    op, os_ = _rows(out, "out", (B, H, Dv), dt, cur)
     if not isinstance(state, torch.Tensor) or state.dim() != 4:
         raise ValueError("state must be [num_slots, H, Dk, Dv]")
     num_slots = state.shape[0]
-    sp = _vec(state, "state", (num_slots, H, Dk, Dv), torch.float32)
-    rc = _N.lib.attnres_linear_attention_step(*head, sp, num_slots, _vec(slots, "slots", (B,), torch.int32),
+    sp = _vec(state, "state", (num_slots, H, Dk, Dv), torch.float32, cur)
+    rc = _N.lib.attnres_linear_attention_step(*head, sp, num_slots, _vec(slots, "slots", (B,), torch.int32, cur),
                                               float(Dk ** -0.5 if scale is None else scale), op, os_,
                                               _stream_ptr(stream))
     _N.check(rc, "attnres_linear_attention_step")

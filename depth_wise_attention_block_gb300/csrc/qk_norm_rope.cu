@@ -11,7 +11,9 @@
 // and sines of the token's position are computed once per group and stay in
 // registers, the two 16-byte vectors that a lane holds of a head contain both
 // members of its pairs (no exchange between lanes but the row sums), and the
-// next head's vectors load while this one is computed.
+// vectors of the next rows are on their way (cp.async into shared memory that
+// each thread keeps to itself: four rows ahead, two in the backward, where a
+// register prefetch of one row left HBM at 57 % on 16384 tokens x 112 heads).
 //
 // Angles: p inv_freq is reduced modulo a full turn before it is rounded to
 // fp32.  inv_freq / (2 pi) is held as an unevaluated sum of two fp32 numbers
@@ -31,8 +33,8 @@ namespace attnres {
 namespace {
 
 constexpr int kQkThreads = 256;
-constexpr int kQkBlocksPerSm = 4;  // resident CTAs the grid is sized for
-constexpr int kQkMaxD = 1024;
+constexpr int kQkBlocksPerSm = 3;     // resident CTAs of the forward (2 or 4 are slower: rows in flight against registers)
+constexpr int kQkBwdBlocksPerSm = 2;  // of the backward
 
 struct QkParams {
   QkHead h[2];
@@ -82,12 +84,93 @@ __device__ __forceinline__ void rotate(float& a, float& b, float c, float s) {
   a = x;
 }
 
+// A lane's two vectors as packed fp32: X the first members of its pairs, Y
+// the second ones, two pairs to a register pair.  INTER: the pairs are
+// neighbours inside a vector (X[0 .. V/4) of vector a, the rest of b);
+// otherwise X is vector a and Y vector b.
+template <typename T, bool INTER>
+struct Pairs;
+template <bool INTER>
+struct Pairs<bf16_t, INTER> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void load(const uint4& a, const uint4& b, uint64_t* X, uint64_t* Y) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      X[i] = INTER ? f2_pack(bf16lo(w[2 * i]), bf16lo(w[2 * i + 1])) : f2_pack(bf16lo(w[i]), bf16hi(w[i]));
+      Y[i] = INTER ? f2_pack(bf16hi(w[2 * i]), bf16hi(w[2 * i + 1])) : f2_pack(bf16lo(w[4 + i]), bf16hi(w[4 + i]));
+    }
+  }
+  static __device__ __forceinline__ void store(const uint64_t* X, const uint64_t* Y, uint4* a, uint4* b) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x0, x1, y0, y1;
+      f2_unpack(X[i], x0, x1);
+      f2_unpack(Y[i], y0, y1);
+      w[INTER ? 2 * i : i] = INTER ? pack_bf16x2(x0, y0) : pack_bf16x2(x0, x1);
+      w[INTER ? 2 * i + 1 : 4 + i] = INTER ? pack_bf16x2(x1, y1) : pack_bf16x2(y0, y1);
+    }
+    *a = make_uint4(w[0], w[1], w[2], w[3]);
+    *b = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+};
+template <bool INTER>
+struct Pairs<float, INTER> {
+  static constexpr int N = 2;
+  static __device__ __forceinline__ void load(const uint4& a, const uint4& b, uint64_t* X, uint64_t* Y) {
+    auto f = [](uint32_t u) { return __uint_as_float(u); };
+    X[0] = INTER ? f2_pack(f(a.x), f(a.z)) : f2_pack(f(a.x), f(a.y));
+    Y[0] = INTER ? f2_pack(f(a.y), f(a.w)) : f2_pack(f(b.x), f(b.y));
+    X[1] = INTER ? f2_pack(f(b.x), f(b.z)) : f2_pack(f(a.z), f(a.w));
+    Y[1] = INTER ? f2_pack(f(b.y), f(b.w)) : f2_pack(f(b.z), f(b.w));
+  }
+  static __device__ __forceinline__ void store(const uint64_t* X, const uint64_t* Y, uint4* a, uint4* b) {
+    float x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f2_unpack(X[i], x[2 * i], x[2 * i + 1]);
+      f2_unpack(Y[i], y[2 * i], y[2 * i + 1]);
+    }
+    auto u = [](float v) { return __float_as_uint(v); };
+    *a = INTER ? make_uint4(u(x[0]), u(y[0]), u(x[1]), u(y[1])) : make_uint4(u(x[0]), u(x[1]), u(x[2]), u(x[3]));
+    *b = INTER ? make_uint4(u(x[2]), u(y[2]), u(x[3]), u(y[3])) : make_uint4(u(y[0]), u(y[1]), u(y[2]), u(y[3]));
+  }
+};
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// each pair (x, y) turned by (c, s)
+__device__ __forceinline__ void rotate2(uint64_t& x, uint64_t& y, uint64_t c, uint64_t s) {
+  const uint64_t minus = f2_pack(-1.f, -1.f);
+  const uint64_t ys = f2_mul(f2_mul(y, s), minus), xs = f2_mul(x, s);
+  x = f2_fma(x, c, ys);
+  y = f2_fma(y, c, xs);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+  const int bytes = in ? 16 : 0;  // none: zeros
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // INTER pairs channels (2i, 2i + 1), otherwise (i, i + rot/2).
 template <typename T, int L, bool INTER, bool BWD>
-__global__ void __launch_bounds__(kQkThreads) qk_vec_kernel(const __grid_constant__ QkParams p) {
-  constexpr int V = Vec16<T>::kElems;
+__global__ void __launch_bounds__(kQkThreads, BWD ? kQkBwdBlocksPerSm : kQkBlocksPerSm) qk_vec_kernel(const __grid_constant__ QkParams p) {
+  constexpr int V = Vec16<T>::kElems, NP = Pairs<T, INTER>::N;
   constexpr int kGroups = kQkThreads / L;
-  extern __shared__ float smem[];  // BWD: [kGroups][D]
+  constexpr int kAhead = BWD ? 2 : 4, kVecs = BWD ? 4 : 2;  // rows on their way; vectors of a row per thread
+  extern __shared__ __align__(16) float smem[];  // [kAhead][kVecs][threads] vectors; at the end, BWD: [kGroups][D]
+  // this head's gains, a vector's first members before its second ones
+  // (INTER), read again for every row: the registers go to loads in flight
+  __shared__ __align__(16) float gains[64 * V];
   const int which = blockIdx.x >= p.blocks0 ? 1 : 0;
   const QkHead& hd = p.h[which];
   const int block = blockIdx.x - (which ? p.blocks0 : 0);
@@ -113,140 +196,184 @@ __global__ void __launch_bounds__(kQkThreads) qk_vec_kernel(const __grid_constan
   pdl_wait();
   pdl_trigger();
 
-  float ga[V], gb[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) {
-    ga[e] = hd.gain && ha ? __ldg(hd.gain + va * V + e) : 1.f;
-    gb[e] = hd.gain && hb ? __ldg(hd.gain + vb * V + e) : 1.f;
-  }
-  float dga[BWD ? V : 1], dgb[BWD ? V : 1];
+  for (int c = threadIdx.x; c < p.D; c += kQkThreads)
+    gains[INTER ? c / V * V + c % 2 * (V / 2) + c % V / 2 : c] = hd.gain ? __ldg(hd.gain + c) : 1.f;
+  __syncthreads();
+  // the lane's gains in the order of X and Y (vector 0's where it has none)
+  auto gain = [&](uint64_t* GX, uint64_t* GY) {
+    const ulonglong2* ga = reinterpret_cast<const ulonglong2*>(gains + (ha ? va : 0) * V);
+    const ulonglong2* gb = reinterpret_cast<const ulonglong2*>(gains + (hb ? vb : 0) * V);
+    if constexpr (V == 8) {
+      const ulonglong2 a0 = ga[0], a1 = ga[1], b0 = gb[0], b1 = gb[1];
+      GX[0] = a0.x, GX[1] = a0.y;
+      GX[2] = INTER ? b0.x : a1.x, GX[3] = INTER ? b0.y : a1.y;
+      GY[0] = INTER ? a1.x : b0.x, GY[1] = INTER ? a1.y : b0.y;
+      GY[2] = b1.x, GY[3] = b1.y;
+    } else {
+      const ulonglong2 a0 = ga[0], b0 = gb[0];
+      GX[0] = a0.x, GX[1] = INTER ? b0.x : a0.y;
+      GY[0] = INTER ? a0.y : b0.x, GY[1] = b0.y;
+    }
+  };
+  uint64_t dgx[BWD ? NP : 1], dgy[BWD ? NP : 1];
   if constexpr (BWD) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) dga[e] = dgb[e] = 0.f;
+    for (int e = 0; e < NP; ++e) dgx[e] = dgy[e] = 0;
   }
 
   const int hc = p.hc[which];
   const int nch = (hd.H + hc - 1) / hc;
-  const T* X = static_cast<const T*>(hd.x);
+  const T* X0 = static_cast<const T*>(hd.x);
   const T* DY = static_cast<const T*>(hd.dy);
   T* O = static_cast<T*>(hd.out);
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   // the loop is uniform over a warp (its groups share the shuffles): a group
   // past the end works on nothing
   const long long stride = (long long)nblocks * kGroups;
-  const long long warp_unit = (long long)block * kGroups + (threadIdx.x / 32) * (32 / L);
-  for (long long u0 = warp_unit; u0 < p.units[which]; u0 += stride) {
+  const long long warp_unit = (long long)block * kGroups + (threadIdx.x / 32) * (32 / L), units = p.units[which];
+  struct Unit {
+    long long t;
+    int h0, h1;
+  };
+  auto unit = [&](long long u0) {
     const long long u = u0 + group % (32 / L);
-    const bool live = u < p.units[which];
-    const long long t = live ? u / nch : 0;
-    const int h0 = live ? (int)(u % nch) * hc : 0;
-    const int h1 = live ? (h0 + hc < hd.H ? h0 + hc : hd.H) : 0;
+    Unit r{0, 0, 0};
+    if (u < units) {
+      r.t = u / nch;
+      r.h0 = (int)(u % nch) * hc;
+      r.h1 = r.h0 + hc < hd.H ? r.h0 + hc : hd.H;
+    }
+    return r;
+  };
+  // the rows ahead: row `ahead_k` of unit `ahead_u`, in ring order
+  const uint32_t ring = smem_addr(smem) + threadIdx.x * 16;
+  long long ahead_u = warp_unit;
+  int ahead_k = 0, ahead_slot = 0;
+  Unit au = unit(ahead_u);
+  auto fetch = [&] {
+    if (ahead_u < units) {
+      const int h = au.h0 + ahead_k;
+      const bool in = h < au.h1;
+      const long long xo = in ? au.t * hd.xs + (long long)h * p.D : 0;
+      const uint32_t to = ring + ahead_slot * (kVecs * kQkThreads * 16);
+      cp_async16(to, X0 + xo + (ha ? va * V : 0), in && ha);
+      cp_async16(to + kQkThreads * 16, X0 + xo + (hb ? vb * V : 0), in && hb);
+      if constexpr (BWD) {
+        const long long yo = in ? au.t * hd.dys + (long long)h * p.D : 0;
+        cp_async16(to + 2 * kQkThreads * 16, DY + yo + (ha ? va * V : 0), in && ha);
+        cp_async16(to + 3 * kQkThreads * 16, DY + yo + (hb ? vb * V : 0), in && hb);
+      }
+      if (++ahead_k == hc) {
+        ahead_k = 0;
+        ahead_u += stride;
+        au = unit(ahead_u);
+      }
+      ahead_slot = ahead_slot + 1 == kAhead ? 0 : ahead_slot + 1;
+    }
+    cp_async_commit();  // a group for every row, empty or not
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch();
+  int slot = 0;
+  for (long long u0 = warp_unit; u0 < units; u0 += stride) {
+    const Unit cu = unit(u0);
+    const long long t = cu.t;
+    const int h0 = cu.h0, h1 = cu.h1;
 
-    float cs[V], sn[V];
+    // cosines and sines of the lane's 2 NP pairs, in the order of X
+    uint64_t cs[NP], sn[NP];
     if (p.rot > 0) {
       const long long pos = __ldg(p.pos + t);
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        int i;  // frequency of the lane's pair e
-        if constexpr (INTER)
-          i = e < V / 2 ? va * (V / 2) + e : vb * (V / 2) + e - V / 2;
-        else
-          i = rot_half ? lane * V + e : p.rot;
-        cs[e] = 1.f;
-        sn[e] = 0.f;
-        if (i < p.rot / 2) turn(pos, __ldg(p.freq + i), &cs[e], &sn[e]);
+      for (int e = 0; e < NP; ++e) {
+        float c[2] = {1.f, 1.f}, sv[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int pair = 2 * e + k;
+          int i;  // its frequency
+          if constexpr (INTER)
+            i = pair < NP ? va * NP + pair : vb * NP + pair - NP;
+          else
+            i = rot_half ? lane * V + pair : p.rot;
+          if (i < p.rot / 2) turn(pos, __ldg(p.freq + i), &c[k], &sv[k]);
+          if (BWD) sv[k] = -sv[k];  // gradients turn back
+        }
+        cs[e] = f2_pack(c[0], c[1]);
+        sn[e] = f2_pack(sv[0], sv[1]);
       }
     }
 
-    const T* x = X + t * hd.xs;
-    const T* dy = BWD ? DY + t * hd.dys : nullptr;
     T* o = O + t * hd.os;
-    const bool la = ha && live, lb = hb && live;
-    uint4 xa = zero, xb = zero, ya = zero, yb = zero;
-    auto load = [&](int h) {
-      const bool in = h < h1;
-      xa = in && la ? __ldcs(reinterpret_cast<const uint4*>(x + (long long)h * p.D) + va) : zero;
-      xb = in && lb ? __ldcs(reinterpret_cast<const uint4*>(x + (long long)h * p.D) + vb) : zero;
-      if constexpr (BWD) {
-        ya = in && la ? __ldcs(reinterpret_cast<const uint4*>(dy + (long long)h * p.D) + va) : zero;
-        yb = in && lb ? __ldcs(reinterpret_cast<const uint4*>(dy + (long long)h * p.D) + vb) : zero;
-      }
-    };
-    load(h0);
     for (int k = 0; k < hc; ++k) {  // the same count for every group of the warp
       const int h = h0 + k;
-      float a[V], b[V], da[BWD ? V : 1], db[BWD ? V : 1];
-      Vec16<T>::unpack(xa, a);
-      Vec16<T>::unpack(xb, b);
-      if constexpr (BWD) {
-        Vec16<T>::unpack(ya, da);
-        Vec16<T>::unpack(yb, db);
-      }
-      load(h + 1);
-      float ss = 0.f;
+      uint64_t X[NP], Y[NP], GX[NP], GY[NP], dX[BWD ? NP : 1], dY[BWD ? NP : 1];
+      cp_async_wait<kAhead - 1>();
+      const uint32_t at = ring + slot * (kVecs * kQkThreads * 16);
+      Pairs<T, INTER>::load(ld_shared_v4(at), ld_shared_v4(at + kQkThreads * 16), X, Y);
+      if constexpr (BWD) Pairs<T, INTER>::load(ld_shared_v4(at + 2 * kQkThreads * 16), ld_shared_v4(at + 3 * kQkThreads * 16), dX, dY);
+      slot = slot + 1 == kAhead ? 0 : slot + 1;
+      fetch();  // into the slot just read
+      uint64_t sq = 0;
 #pragma unroll
-      for (int e = 0; e < V; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+      for (int e = 0; e < NP; ++e) sq = f2_fma(X[e], X[e], f2_fma(Y[e], Y[e], sq));
+      const float inv = rsqrtf(group_sum<L>(f2_hsum(sq)) * p.inv_d + p.eps);
+      const uint64_t inv2 = f2_pack(inv, inv);
+      gain(GX, GY);
       if constexpr (!BWD) {
-        const float inv = 1.f / sqrtf(group_sum<L>(ss) * p.inv_d + p.eps);
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          a[e] *= inv * ga[e];
-          b[e] *= inv * gb[e];
-        }
-        if (p.rot > 0) {
-          if constexpr (INTER) {
-#pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-              rotate(a[2 * e], a[2 * e + 1], cs[e], sn[e]);
-              rotate(b[2 * e], b[2 * e + 1], cs[V / 2 + e], sn[V / 2 + e]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) rotate(a[e], b[e], cs[e], sn[e]);
-          }
+        for (int e = 0; e < NP; ++e) {
+          X[e] = f2_mul(X[e], f2_mul(GX[e], inv2));
+          Y[e] = f2_mul(Y[e], f2_mul(GY[e], inv2));
+          if (p.rot > 0) rotate2(X[e], Y[e], cs[e], sn[e]);
         }
       } else {
-        if (p.rot > 0) {
-          if constexpr (INTER) {
+        uint64_t nx = 0;  // sum n x
 #pragma unroll
-            for (int e = 0; e < V / 2; ++e) {
-              rotate(da[2 * e], da[2 * e + 1], cs[e], -sn[e]);
-              rotate(db[2 * e], db[2 * e + 1], cs[V / 2 + e], -sn[V / 2 + e]);
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) rotate(da[e], db[e], cs[e], -sn[e]);
-          }
+        for (int e = 0; e < NP; ++e) {
+          if (p.rot > 0) rotate2(dX[e], dY[e], cs[e], sn[e]);
+          nx = f2_fma(f2_mul(dX[e], GX[e]), X[e], f2_fma(f2_mul(dY[e], GY[e]), Y[e], nx));
         }
-        float nx = 0.f;  // sum n x
-#pragma unroll
-        for (int e = 0; e < V; ++e) nx = fmaf(da[e] * ga[e], a[e], fmaf(db[e] * gb[e], b[e], nx));
-        const float inv = 1.f / sqrtf(group_sum<L>(ss) * p.inv_d + p.eps);
-        const float mh = group_sum<L>(nx) * p.inv_d * inv;  // mean(n h)
+        const float mh = group_sum<L>(f2_hsum(nx)) * p.inv_d * inv;  // mean(n h)
+        const uint64_t mh2 = f2_pack(-mh, -mh);
         const bool in = h < h1;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float hx = a[e] * inv, hy = b[e] * inv;
+        for (int e = 0; e < NP; ++e) {
+          X[e] = f2_mul(X[e], inv2);
+          Y[e] = f2_mul(Y[e], inv2);
           if (in) {  // a head past the group's range holds zeros, and 0 / rho may be NaN (eps = 0)
-            dga[e] = fmaf(da[e], hx, dga[e]);
-            dgb[e] = fmaf(db[e], hy, dgb[e]);
+            dgx[e] = f2_fma(dX[e], X[e], dgx[e]);
+            dgy[e] = f2_fma(dY[e], Y[e], dgy[e]);
           }
-          a[e] = (da[e] * ga[e] - hx * mh) * inv;
-          b[e] = (db[e] * gb[e] - hy * mh) * inv;
+          X[e] = f2_mul(f2_fma(X[e], mh2, f2_mul(dX[e], GX[e])), inv2);
+          Y[e] = f2_mul(f2_fma(Y[e], mh2, f2_mul(dY[e], GY[e])), inv2);
         }
       }
       if (h < h1) {
-        if (la) __stcs(reinterpret_cast<uint4*>(o + (long long)h * p.D) + va, Vec16<T>::pack(a));
-        if (lb) __stcs(reinterpret_cast<uint4*>(o + (long long)h * p.D) + vb, Vec16<T>::pack(b));
+        uint4 oa, ob;
+        Pairs<T, INTER>::store(X, Y, &oa, &ob);
+        if (ha) __stcs(reinterpret_cast<uint4*>(o + (long long)h * p.D) + va, oa);
+        if (hb) __stcs(reinterpret_cast<uint4*>(o + (long long)h * p.D) + vb, ob);
       }
     }
   }
   if constexpr (BWD) {
+    cp_async_wait<0>();
+    __syncthreads();  // the ring is done with
     if (p.part) {  // groups in order: the sums do not depend on timing
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (ha) smem[group * p.D + va * V + e] = dga[e];
-        if (hb) smem[group * p.D + vb * V + e] = dgb[e];
+      for (int e = 0; e < NP; ++e) {
+        float x[2], y[2];
+        f2_unpack(dgx[e], x[0], x[1]);
+        f2_unpack(dgy[e], y[0], y[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int pair = 2 * e + k;
+          // the channels of pair `pair`, and whether the lane has its vector
+          const bool second = INTER && pair >= NP;
+          const int at = INTER ? (second ? vb : va) * V + 2 * (pair - (second ? NP : 0)) : va * V + pair;
+          const int bt = INTER ? at + 1 : vb * V + pair;
+          if (second ? hb : ha) smem[group * p.D + at] = x[k];
+          if (INTER ? (second ? hb : ha) : hb) smem[group * p.D + bt] = y[k];
+        }
       }
       __syncthreads();
       for (int c = threadIdx.x; c < p.D; c += kQkThreads) {
@@ -290,7 +417,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const __grid_constan
       const float v = load_elem(x + c);
       ss = fmaf(v, v, ss);
     }
-    const float inv = 1.f / sqrtf(warp_sum(ss) * p.inv_d + p.eps);
+    const float inv = rsqrtf(warp_sum(ss) * p.inv_d + p.eps);
     if (BWD) {
       for (int i = lane; i < items; i += 32) {
         const int a = i < half ? (inter ? 2 * i : i) : half + i, b = inter ? a + 1 : a + half;
@@ -361,7 +488,7 @@ __global__ void __launch_bounds__(256) qk_dgain_kernel(const float* part, int bl
 
 template <typename T, int L, bool BWD>
 cudaError_t launch_vec(const QkArgs& a, const QkParams& p, int grid) {
-  const int smem = BWD && p.part ? kQkThreads / L * p.D * 4 : 0;
+  const int smem = 8 * kQkThreads * 16;  // the ring; the gain gradients' sums need at most half of it
   return a.interleaved ? launch_kernel(qk_vec_kernel<T, L, true, BWD>, dim3(grid), dim3(kQkThreads), smem, a.stream, p)
                        : launch_kernel(qk_vec_kernel<T, L, false, BWD>, dim3(grid), dim3(kQkThreads), smem, a.stream, p);
 }
@@ -386,7 +513,7 @@ int64_t qk_backward_workspace_bytes(int64_t T, int Hq, int Hk, int D) {
   (void)T, (void)Hq, (void)Hk;
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return (int64_t)di.sm_count * kQkBlocksPerSm * D * 4;
+  return (int64_t)di.sm_count * kQkBwdBlocksPerSm * D * 4;
 }
 
 cudaError_t launch_qk_norm_rope(const QkArgs& a) {
@@ -426,20 +553,34 @@ cudaError_t launch_qk_norm_rope(const QkArgs& a) {
   p.pos = reinterpret_cast<const long long*>(a.pos);
   p.freq = a.freq;
   p.part = dgain ? a.workspace : nullptr;
-  // heads per group and pass: all of them when there are tokens enough to
-  // fill the GPU, fewer (each group then computes its angles again) when not
-  const long long slots = (long long)di.sm_count * kQkBlocksPerSm * groups;
-  const long long rows = a.T * (a.h[0].H + a.h[1].H);
-  int hc = (int)(vec ? (rows + slots - 1) / slots : 1);
-  if (hc > 16) hc = 16;
-  for (int i = 0; i < 2; ++i) {
-    const int H = a.h[i].H;
-    p.hc[i] = H < 1 ? 1 : (hc < H ? hc : H);
-    p.units[i] = H > 0 ? a.T * ((H + p.hc[i] - 1) / p.hc[i]) : 0;
+  // heads per group: few enough that every resident group has a unit, many
+  // enough that its angles (about three rows' worth of work) are shared
+  const long long cap = (long long)di.sm_count * (a.backward ? kQkBwdBlocksPerSm : kQkBlocksPerSm);
+  const long long slots = cap * groups;
+  auto plan = [&](int hc) {
+    for (int i = 0; i < 2; ++i) {
+      const int H = a.h[i].H;
+      const int parts = H < 1 ? 1 : (H + hc - 1) / hc;
+      p.hc[i] = H < 1 ? 1 : (H + parts - 1) / parts;  // as even as they come
+      p.units[i] = H > 0 ? a.T * parts : 0;
+    }
+    const int most = p.hc[0] > p.hc[1] ? p.hc[0] : p.hc[1];
+    return (p.units[0] + p.units[1] + slots - 1) / slots * (most + (a.rot > 0 ? 3 : 0));
+  };
+  int hc = 1;
+  if (vec) {
+    long long best = plan(1);
+    for (int c = 2; c <= 32; ++c) {
+      const long long cost = plan(c);
+      if (cost < best) {
+        best = cost;
+        hc = c;
+      }
+    }
   }
+  plan(hc);
   // CTAs to q and k by their share of the units, at least one each
   const long long need0 = (p.units[0] + groups - 1) / groups, need1 = (p.units[1] + groups - 1) / groups;
-  const long long cap = (long long)di.sm_count * kQkBlocksPerSm;
   long long b0 = need0, b1 = need1;
   if (b0 + b1 > cap) {
     b0 = need0 * cap / (need0 + need1);
