@@ -10,9 +10,14 @@
 // epilogue while the next tile's products are formed in the other half of
 // TMEM.
 //
-// Two shapes of launch:
-//  - wide: persistent CTAs over tiles of 128 x bn.  The bound is the tensor
-//    cores.
+// Three shapes of launch:
+//  - pairs: two CTAs of a cluster form one 256 x 256 tile
+//    (tcgen05.mma.cta_group::2): each loads 128 rows of A and 128 rows of B,
+//    half the L2 traffic per product of a 128 x 256 tile, whose 94 bytes per
+//    cycle and SM are more than L2 delivers (2048 x 7168 x 7168: 175 us with
+//    single tiles).  Persistent, the bound is the tensor cores.
+//  - wide: persistent single CTAs over tiles of 128 x bn, where there are too
+//    few 256 x 256 tiles, and for fp32 operands.
 //  - narrow (SWAP): few rows of one operand (decode).  The wide operand's
 //    rows become the 128 lanes and the few rows the columns, so the weights
 //    are read once; the contraction is split over a cluster of `ksplit` CTAs
@@ -450,6 +455,182 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
   }
 }
 
+// ------------------------------------------------------------- pairs -------
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// one arrival at `bar` of both CTAs once the MMAs issued so far are done
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+               "h"((uint16_t)3)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+
+constexpr int kPairN = 256;                              // columns of a pair's tile
+constexpr int kPairStage = 2 * kLanes * 128;             // bytes of a stage in one CTA: 128 rows of A, 128 of B
+constexpr int kPairTmem = 512;                           // two accumulators of 256 columns
+
+// Rank r of a cluster of two holds rows 128 r .. + 127 of the tile (in its
+// TMEM) and rows 128 r .. + 127 of B.  Rank 0 issues the MMAs for both; its
+// `full` barriers count the bytes of both, and its commits free the stages of
+// both.
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_constant__ TcParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ uint32_t tmem_base;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const int ntiles = p.tiles_l * p.tiles_c, tile0 = blockIdx.x / 2, tstep = gridDim.x / 2;
+
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&empty[s]), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(smem_addr(&acc_full[b]), 1);
+      mbar_init(smem_addr(&acc_empty[b]), 2 * kEpiWarps);
+    }
+    mbar_fence_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_base), kPairTmem);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // both CTAs' barriers are there
+  tc_fence_after();
+  const uint32_t tmem = tmem_base;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+        const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN + rank * kLanes;
+        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+          const int st = it % p.stages;
+          if (!mbar_wait_cluster_bounded(smem_addr(&empty[st]), ((uint32_t)(it / p.stages) & 1u) ^ 1u, p.wait_ns)) {
+            report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+            ok = false;
+            break;
+          }
+          const uint32_t fb = smem_addr(&full[st]), a = base + st * kPairStage, b = a + kPairStage / 2;
+          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kPairStage);
+          const uint32_t bar = map_shared_rank(fb, 0);
+          if (p.a_mn) {
+            tma_load_3d_pair(a, &p.ma, l0, kb * kKB, 0, bar);
+            tma_load_3d_pair(a + 8192, &p.ma, l0 + 64, kb * kKB, 0, bar);
+          } else {
+            tma_load_3d_pair(a, &p.ma, kb * kKB, l0, 0, bar);
+          }
+          if (p.b_mn) {
+            tma_load_3d_pair(b, &p.mb, c0, kb * kKB, 0, bar);
+            tma_load_3d_pair(b + 8192, &p.mb, c0 + 64, kb * kKB, 0, bar);
+          } else {
+            tma_load_3d_pair(b, &p.mb, kb * kKB, c0, 0, bar);
+          }
+        }
+      }
+      // no CTA exits under a copy: rank 0 sees the bytes of both
+      if (rank == 0) {
+        const int armed = it < p.stages ? it : p.stages;
+        for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.stages) & 1u);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      const uint32_t step = p.a_mn ? 128 : 2, stepb = p.b_mn ? 128 : 2;  // 16 contraction steps, in units of 16 bytes
+      int it = 0, g = 0;
+      bool ok = true;
+      for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++g) {
+        const int buf = g & 1;
+        if (!mbar_wait_cluster_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns)) {
+          report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * kPairN;
+        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+          const int st = it % p.stages;
+          if (!mbar_wait_cluster_bounded(smem_addr(&full[st]), (uint32_t)(it / p.stages) & 1u, p.wait_ns)) {
+            report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a = base + st * kPairStage;
+          const uint64_t da = plane_desc(a, p.a_mn, 0), db = plane_desc(a + kPairStage / 2, p.b_mn, 0);
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk) tc_mma_bf16_pair(d, da + kk * step, db + kk * stepb, p.idesc, kb > 0 || kk > 0);
+          tc_commit_pair(smem_addr(&empty[st]));
+        }
+        tc_commit_pair(smem_addr(&acc_full[buf]));
+      }
+    }
+    __syncwarp();
+  } else {
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
+    const bool vec_out = p.epi.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.out) & 15) == 0;
+    const bool vec_res = p.epi.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.res) & 15) == 0;
+    const float nan = __int_as_float(0x7fc00000);
+    bool ok = true;
+    int g = 0;
+    for (int tile = tile0; tile < ntiles; tile += tstep, ++g) {
+      const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN;
+      const long long m = l0 + 32 * quarter + lane;
+      const int buf = g & 1;
+      if (ok && !__all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
+        if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+        ok = false;
+      }
+      tc_fence_after();
+      for (int ch = half; ch < kPairN / 16; ch += 2) {
+        uint32_t v[16];
+        tmem_ld16(lanes_at + buf * kPairN + ch * 16, v);
+        tmem_ld_wait();
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = ok ? __uint_as_float(v[i]) : nan;
+        if (c0 + ch * 16 < p.cols) epilogue_row16<bf16_t, MODE>(p, f, m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(map_shared_rank(smem_addr(&acc_empty[buf]), 0));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA's shared memory or TMEM is in use by the other
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kPairTmem);
+  }
+}
+
 // ----------------------------------------------------------- operands ------
 
 // Copies of operands TMA cannot take as they are: rows on 16-byte boundaries
@@ -538,6 +719,28 @@ cudaError_t launch_mode(const TcParams& p, bool swap, int grid, int smem, int sm
   return cudaLaunchKernelEx(&cfg, tc_gemm_kernel<NP, MODE, true>, p);
 }
 
+template <int MODE>
+cudaError_t launch_pair(const TcParams& p, int grid, int smem, int smem_max, cudaStream_t stream) {
+  static SmemOptIn optin;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_pair_kernel<MODE>), smem_max);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl_enabled() ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, tc_pair_kernel<MODE>, p);
+}
+
 }  // namespace
 
 bool tc_rows_ok(const void* ptr, int64_t ld) { return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0 && ld % 8 == 0; }
@@ -549,16 +752,24 @@ TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
   const int64_t kblocks = up(K, kKB) / kKB;
   const int bn_max = np == 3 ? 128 : 256;
   double cost = 1e300;
-  // wide: whole waves of tiles; a block costs the tensor cores bn / 2 cycles
-  // per instruction, 4 instructions (24 with three terms), and a tile the
-  // epilogue's start-up
+  // whole waves of tiles, in cycles: an instruction of a single tile of 256
+  // columns takes about 250 (L2), of 128 or fewer about 130; of a pair's tile
+  // about 150; then the start and end of a tile's pipeline
   for (int bn = 64; bn <= bn_max; bn *= 2) {
     const int64_t tiles = up(M, kLanes) / kLanes * (up(N, bn) / bn);
-    const double tile = (double)kblocks * (np == 3 ? 24 : 4) * (bn < 128 ? 64 : bn / 2) + 1500;
+    const double tile = (double)kblocks * (np == 3 ? 24 * 130 : 4 * (bn == 256 ? 250 : 130)) + 1500;
     const double c = (double)((tiles + sm_count - 1) / sm_count) * tile + 1500;
     if (c < cost) {
       cost = c;
-      best = {false, bn, 1, 0};
+      best = {TcPlan::kWide, bn, 1, 0};
+    }
+  }
+  if (np == 1) {
+    const int64_t tiles = up(M, 2 * kLanes) / (2 * kLanes) * (up(N, kPairN) / kPairN);
+    const double c = (double)((tiles + sm_count / 2 - 1) / (sm_count / 2)) * ((double)kblocks * 4 * 150 + 1500) + 2500;
+    if (c < cost) {
+      cost = c;
+      best = {TcPlan::kPairs, kPairN, 1, 0};
     }
   }
   // narrow: M's rows as columns, N's as lanes, the contraction over a
@@ -574,11 +785,13 @@ TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
       const double c = (double)waves * ((double)((kblocks + ks - 1) / ks) * block + 2500) + 1500;
       if (c < cost) {
         cost = c;
-        best = {true, bn, ks, 0};
+        best = {TcPlan::kNarrow, bn, ks, 0};
       }
     }
   }
-  best.part_rows = best.swap ? (int)(up(M, best.bn) / best.bn * best.ksplit * 2) : (int)(up(M, kLanes) / 32);
+  best.part_rows = best.shape == TcPlan::kNarrow ? (int)(up(M, best.bn) / best.bn * best.ksplit * 2)
+                   : best.shape == TcPlan::kPairs ? (int)(up(M, 2 * kLanes) / 32)
+                                                  : (int)(up(M, kLanes) / 32);
   return best;
 }
 
@@ -601,28 +814,30 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  const TcOperand &lo = plan.swap ? B : A, &co = plan.swap ? A : B;
+  const bool swap = plan.shape == TcPlan::kNarrow, pairs = plan.shape == TcPlan::kPairs;
+  const TcOperand &lo = swap ? B : A, &co = swap ? A : B;
   TcParams p{};
   auto map = [&](CUtensorMap* m, const TcOperand& o, int box) {
     const void* ptr = o.prep ? o.prep : o.ptr;
     const int64_t ld = o.prep ? up(o.cols, 8) : o.ld;
     return operand_map(m, ptr, o.rows, o.cols, ld, np, o.mn, box);
   };
-  if (!map(&p.ma, lo, kLanes) || !map(&p.mb, co, plan.bn)) return cudaErrorInvalidValue;
+  if (!map(&p.ma, lo, kLanes) || !map(&p.mb, co, pairs ? kLanes : plan.bn)) return cudaErrorInvalidValue;
   p.a_mn = lo.mn;
   p.b_mn = co.mn;
-  p.lanes = plan.swap ? N : (int)M;
-  p.cols = plan.swap ? (int)M : N;
+  p.lanes = swap ? N : (int)M;
+  p.cols = swap ? (int)M : N;
   p.kblocks = (int)(up(K, kKB) / kKB);
   p.bn = plan.bn;
-  p.tiles_l = (int)(up(p.lanes, kLanes) / kLanes);
+  const int tile_l = pairs ? 2 * kLanes : kLanes;
+  p.tiles_l = (int)(up(p.lanes, tile_l) / tile_l);
   p.tiles_c = (int)(up(p.cols, p.bn) / p.bn);
   p.ksplit = plan.ksplit;
   p.plane_a = kLanes * 128;
   p.plane_b = (uint32_t)((p.b_mn ? up(p.bn, 64) : up(p.bn, 8)) * 128);
   p.stage_bytes = np * (p.plane_a + p.plane_b);
   const int nacc = np == 3 ? 2 : 1;
-  const int nbuf = plan.swap && np == 1 ? 1 : 2;
+  const int nbuf = swap && np == 1 ? 1 : 2;
   p.acc_cols = nacc * (uint32_t)p.bn;
   p.tmem_cols = 32;
   while (p.tmem_cols < nbuf * p.acc_cols) p.tmem_cols *= 2;
@@ -632,22 +847,30 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
   p.wait_ns = wait_limit_ns();
   // shared memory: the stages; narrow tiles also park their partial sums there
   const int smem_max = di.max_smem_optin - 1024;  // the kernels' static shared memory fits in the rest
-  const int budget = (plan.swap && np == 1 ? kNarrowSmem : smem_max) - 1024;
+  const int budget = (swap && np == 1 ? kNarrowSmem : smem_max) - 1024;
   int stages = budget / (int)p.stage_bytes;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages < 2) return cudaErrorInvalidValue;
   p.stages = stages;
   int smem = stages * (int)p.stage_bytes;
-  if (plan.swap && smem < p.bn * kLanes * 4) smem = p.bn * kLanes * 4;
+  if (swap && smem < p.bn * kLanes * 4) smem = p.bn * kLanes * 4;
   smem += 1024;
   const int64_t tiles = (int64_t)p.tiles_l * p.tiles_c;
-  const int64_t grid = plan.swap ? tiles * p.ksplit : (tiles < di.sm_count ? tiles : di.sm_count);
   if (tiles > INT32_MAX / kMaxKsplit) return cudaErrorInvalidValue;
+  if (pairs) {
+    p.stages = (smem_max - 1024) / kPairStage;
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.idesc = tc_idesc_bf16(2 * kLanes, kPairN, p.a_mn, p.b_mn);
+    const int64_t pr = di.sm_count / 2;
+    const int grid = (int)(2 * (tiles < pr ? tiles : pr)), smem = p.stages * kPairStage + 1024;
+    return mode == kEpiDz ? launch_pair<kEpiDz>(p, grid, smem, smem_max, stream) : launch_pair<kEpiForward>(p, grid, smem, smem_max, stream);
+  }
+  const int64_t grid = swap ? tiles * p.ksplit : (tiles < di.sm_count ? tiles : di.sm_count);
   if (np == 3)
-    return mode == kEpiDz ? launch_mode<3, kEpiDz>(p, plan.swap, (int)grid, smem, smem_max, stream)
-                          : launch_mode<3, kEpiForward>(p, plan.swap, (int)grid, smem, smem_max, stream);
-  return mode == kEpiDz ? launch_mode<1, kEpiDz>(p, plan.swap, (int)grid, smem, smem_max, stream)
-                        : launch_mode<1, kEpiForward>(p, plan.swap, (int)grid, smem, smem_max, stream);
+    return mode == kEpiDz ? launch_mode<3, kEpiDz>(p, swap, (int)grid, smem, smem_max, stream)
+                          : launch_mode<3, kEpiForward>(p, swap, (int)grid, smem, smem_max, stream);
+  return mode == kEpiDz ? launch_mode<1, kEpiDz>(p, swap, (int)grid, smem, smem_max, stream)
+                        : launch_mode<1, kEpiForward>(p, swap, (int)grid, smem, smem_max, stream);
 }
 
 }  // namespace attnres

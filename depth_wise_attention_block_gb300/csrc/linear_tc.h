@@ -21,7 +21,8 @@ struct TcOperand {
 };
 
 struct TcPlan {
-  bool swap;      // B's rows along the lanes (few rows of A)
+  enum Shape { kWide, kPairs, kNarrow };
+  Shape shape;    // narrow: B's rows along the lanes (few rows of A)
   int bn;         // columns of a tile
   int ksplit;     // CTAs of a cluster that share a tile's contraction
   int part_rows;  // partial rows of the column sums (kEpiDz)

@@ -138,6 +138,38 @@ def test_linear_backward(A, m, n, k, dt):
         _close(gb, db, (ez + (m + 16) * E * np.abs(dz)).sum(0), (act, "grad_bias"))
 
 
+@pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("m,n,k,act", [(2100, 2600, 200, "silu"), (4000, 5000, 328, "none"), (2049, 4097, 520, "gelu"),
+                                       (1030, 9000, 136, "gelu_tanh")])
+def test_linear_many_tiles(A, m, n, k, act, dt):
+    """Sizes of several waves of tiles, forward and gradients, with odd edges;
+    the fp64 statement evaluated by torch on the GPU, for its speed."""
+    x, w, b, res = _linear_inputs(m, n, k, dt, 31)
+    out, gx, gw, gb = torch.empty_like(res), torch.empty_like(x), torch.empty_like(w), torch.empty(n, device="cuda")
+    err = _err()
+    A.attnres_linear(x, w, out, bias=b, residual=res, activation=act, dev_err=err)
+    A.attnres_linear_backward(x, w, res, gx, gw, gb, bias=b, activation=act, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    X, Wt, R = x.double(), w.double(), res.double()
+    z = (X @ Wt.T + b.double()).cpu().numpy()
+    want = torch.from_numpy(B.activation(z, act)).cuda() + R
+    cz = X.abs() @ Wt.abs().T + b.double().abs()
+    u = U[dt]
+
+    def close(got, ref, bound, what):
+        e = (got.double() - ref).abs()
+        assert torch.isfinite(got).all() and (e <= bound + UNDERFLOW).all(), f"{what}: worst {(e / (bound + UNDERFLOW)).max():.3g} x bound"
+    close(out, want, u * want.abs() + 1.13 * (k + 16) * E * cz + 8 * E * (want.abs() + cz + R.abs()), "out")
+    dz = R * torch.from_numpy(B.activation_slope(z, act)).cuda()
+    ez = R.abs() * (0 if act == "none" else 1) * (1.2 * (k + 16) * E * cz + 12 * E * 1.13)
+    ezr = ez + (0 if act == "none" else u) * dz.abs()
+    dx, dw = dz @ Wt, dz.T @ X
+    close(gx, dx, u * dx.abs() + (ezr + (n + 16) * E * dz.abs()) @ Wt.abs(), "grad_x")
+    close(gw, dw, u * dw.abs() + (ezr + (m + 16) * E * dz.abs()).T @ X.abs(), "grad_w")
+    close(gb, dz.sum(0), (ez + (m + 16) * E * dz.abs()).sum(0), "grad_bias")
+
+
 def test_linear_backward_parts_and_empty(A):
     x, w, b, gy = _linear_inputs(70, 40, 24, torch.bfloat16, 3)
     full = [torch.empty_like(x), torch.empty_like(w), torch.empty(40, device="cuda")]
