@@ -69,6 +69,26 @@ struct TcParams {
   unsigned long long wait_ns;
 };
 
+// A place in the ring of stages and the parity of its lap, without the
+// divisions (the thread that issues the MMAs has 128 cycles for each).
+struct RingPos {
+  int st = 0;
+  uint32_t lap = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++st == stages) {
+      st = 0;
+      lap ^= 1u;
+    }
+  }
+};
+// waits for the last phase of every stage that a producer armed: the CTA
+// never exits under a copy (`r` is the place after the last armed one, `lap0`
+// whether it is still in the first lap)
+__device__ __forceinline__ void drain_stages(const uint64_t* full, const RingPos& r, bool lap0, int stages) {
+  for (int st = 0; st < (lap0 ? r.st : stages); ++st)
+    mbar_wait_bounded(smem_addr(&full[st]), st < r.st ? r.lap : r.lap ^ 1u);
+}
+
 // One plane of an operand's tile, block kb of the contraction, rows from r0.
 __device__ __forceinline__ void load_plane(uint32_t dst, const CUtensorMap* map, bool mn, int r0, int rows, int kb, int plane,
                                            uint32_t bar) {
@@ -247,13 +267,13 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
   if (warp == 0) {
     if (lane == 0) {
       const int brows = p.b_mn ? (p.bn + 63) / 64 * 64 : p.bn;
-      int it = 0;
-      bool ok = true;
+      RingPos r;
+      bool ok = true, lap0 = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int l0 = tile % p.tiles_l * kLanes, c0 = tile / p.tiles_l * p.bn;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int st = it % p.stages;
-          if (!mbar_wait_bounded(smem_addr(&empty[st]), ((uint32_t)(it / p.stages) & 1u) ^ 1u, p.wait_ns)) {
+        for (int kb = kb0; kb < kb1; ++kb) {
+          const int st = r.st;
+          if (!mbar_wait_bounded(smem_addr(&empty[st]), r.lap ^ 1u, p.wait_ns)) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
@@ -265,16 +285,21 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             load_plane(a + pl * p.plane_a, &p.ma, p.a_mn, l0, kLanes, kb, pl, fb);
             load_plane(b + pl * p.plane_b, &p.mb, p.b_mn, c0, brows, kb, pl, fb);
           }
+          r.next(p.stages);
+          lap0 = lap0 && r.st > 0;
         }
       }
-      // the CTA never exits under a copy
-      const int armed = it < p.stages ? it : p.stages;
-      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.stages) & 1u);
+      drain_stages(full, r, lap0, p.stages);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      int it = 0, g = 0;
+      // descriptors of the first stage; a stage, a plane and 16 steps further
+      // are additions to the address field (units of 16 bytes)
+      const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + NP * p.plane_a, p.b_mn, 0);
+      const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2, pa = p.plane_a / 16, pb = p.plane_b / 16;
+      RingPos r;
+      int g = 0;
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         for (int kb = kb0; kb < kb1 && ok; ++g) {
@@ -286,38 +311,32 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + buf * p.acc_cols;
-          for (const int first = kb; kb < end; ++kb, ++it) {
-            const int st = it % p.stages;
-            if (!mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)(it / p.stages) & 1u, p.wait_ns)) {
+          const uint32_t d = tmem + buf * p.acc_cols, d1 = d + p.acc_cols / 2;
+          uint32_t acc = 0;
+          for (; kb < end; ++kb) {
+            if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns)) {
               report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t a = base + st * p.stage_bytes, b = a + NP * p.plane_a;
+            const uint32_t at = r.st * (p.stage_bytes / 16);
+            const uint64_t da = da0 + at, db = db0 + at;
 #pragma unroll
             for (int kk = 0; kk < kKB / 16; ++kk) {
-              const uint32_t acc = kb > first || kk > 0;
-              if constexpr (NP == 1) {
-                tc_mma_bf16(d, plane_desc(a, p.a_mn, kk), plane_desc(b, p.b_mn, kk), p.idesc, acc);
-              } else {
-                uint64_t da[3], db[3];
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl) {
-                  da[pl] = plane_desc(a + pl * p.plane_a, p.a_mn, kk);
-                  db[pl] = plane_desc(b + pl * p.plane_b, p.b_mn, kk);
-                }
-                const uint32_t d1 = d + p.acc_cols / 2;
-                tc_mma_bf16(d, da[0], db[0], p.idesc, acc);
-                tc_mma_bf16(d1, da[0], db[2], p.idesc, acc);
-                tc_mma_bf16(d1, da[2], db[0], p.idesc, 1u);
-                tc_mma_bf16(d1, da[1], db[1], p.idesc, 1u);
-                tc_mma_bf16(d1, da[0], db[1], p.idesc, 1u);
-                tc_mma_bf16(d1, da[1], db[0], p.idesc, 1u);
+              const uint64_t a = da + kk * sa, b = db + kk * sb;
+              tc_mma_bf16(d, a, b, p.idesc, acc);
+              if constexpr (NP == 3) {
+                tc_mma_bf16(d1, a, b + 2 * pb, p.idesc, acc);
+                tc_mma_bf16(d1, a + 2 * pa, b, p.idesc, 1u);
+                tc_mma_bf16(d1, a + pa, b + pb, p.idesc, 1u);
+                tc_mma_bf16(d1, a, b + pb, p.idesc, 1u);
+                tc_mma_bf16(d1, a + pa, b, p.idesc, 1u);
               }
+              acc = 1;
             }
-            tc_commit(smem_addr(&empty[st]));
+            tc_commit(smem_addr(&empty[r.st]));
+            r.next(p.stages);
           }
           tc_commit(smem_addr(&acc_full[buf]));
         }
@@ -525,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
 
   if (warp == 0) {
     if (lane == 0) {
-      int it = 0;
-      bool ok = true;
+      RingPos r;
+      bool ok = true, lap0 = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN + rank * kLanes;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const int st = it % p.stages;
-          if (!mbar_wait_cluster_bounded(smem_addr(&empty[st]), ((uint32_t)(it / p.stages) & 1u) ^ 1u, p.wait_ns)) {
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          const int st = r.st;
+          if (!mbar_wait_bounded(smem_addr(&empty[st]), r.lap ^ 1u, p.wait_ns)) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
@@ -551,19 +570,20 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
           } else {
             tma_load_3d_pair(b, &p.mb, kb * kKB, c0, 0, bar);
           }
+          r.next(p.stages);
+          lap0 = lap0 && r.st > 0;
         }
       }
       // no CTA exits under a copy: rank 0 sees the bytes of both
-      if (rank == 0) {
-        const int armed = it < p.stages ? it : p.stages;
-        for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.stages) & 1u);
-      }
+      if (rank == 0) drain_stages(full, r, lap0, p.stages);
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint32_t step = p.a_mn ? 128 : 2, stepb = p.b_mn ? 128 : 2;  // 16 contraction steps, in units of 16 bytes
-      int it = 0, g = 0;
+      const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + kPairStage / 2, p.b_mn, 0);
+      const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2;  // 16 contraction steps, in units of 16 bytes
+      RingPos r;
+      int g = 0;
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++g) {
         const int buf = g & 1;
@@ -573,19 +593,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
         }
         tc_fence_after();
         const uint32_t d = tmem + buf * kPairN;
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const int st = it % p.stages;
-          if (!mbar_wait_cluster_bounded(smem_addr(&full[st]), (uint32_t)(it / p.stages) & 1u, p.wait_ns)) {
+        uint32_t acc = 0;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns)) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a = base + st * kPairStage;
-          const uint64_t da = plane_desc(a, p.a_mn, 0), db = plane_desc(a + kPairStage / 2, p.b_mn, 0);
+          const uint64_t da = da0 + r.st * (kPairStage / 16), db = db0 + r.st * (kPairStage / 16);
 #pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk) tc_mma_bf16_pair(d, da + kk * step, db + kk * stepb, p.idesc, kb > 0 || kk > 0);
-          tc_commit_pair(smem_addr(&empty[st]));
+          for (int kk = 0; kk < kKB / 16; ++kk) {
+            tc_mma_bf16_pair(d, da + kk * sa, db + kk * sb, p.idesc, acc);
+            acc = 1;
+          }
+          tc_commit_pair(smem_addr(&empty[r.st]));
+          r.next(p.stages);
         }
         tc_commit_pair(smem_addr(&acc_full[buf]));
       }
