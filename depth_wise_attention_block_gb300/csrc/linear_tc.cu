@@ -505,7 +505,11 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
 }
 
 constexpr int kPairN = 256;                              // columns of a pair's tile
-constexpr int kPairStage = 2 * kLanes * 128;             // bytes of a stage in one CTA: 128 rows of A, 128 of B
+constexpr int kPairBlock = 2 * kLanes * 128;             // bytes of a block in one CTA: 128 rows of A, 128 of B
+// Two blocks to a stage: waiting, committing and stepping on take the issuing
+// thread about 300 cycles, an instruction's issue 64 and its execution 128;
+// with one block (four instructions) to a stage the issue was the bound.
+constexpr int kPairStage = 2 * kPairBlock;
 constexpr int kPairTmem = 512;                           // two accumulators of 256 columns
 
 // Rank r of a cluster of two holds rows 128 r .. + 127 of the tile (in its
@@ -548,27 +552,31 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
       bool ok = true, lap0 = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN + rank * kLanes;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          const int st = r.st;
-          if (!mbar_wait_bounded(smem_addr(&empty[st]), r.lap ^ 1u, p.wait_ns)) {
+        for (int kb = 0; kb < p.kblocks; kb += 2) {
+          if (!mbar_wait_bounded(smem_addr(&empty[r.st]), r.lap ^ 1u, p.wait_ns)) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
           }
-          const uint32_t fb = smem_addr(&full[st]), a = base + st * kPairStage, b = a + kPairStage / 2;
-          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kPairStage);
+          const int blocks = kb + 1 < p.kblocks ? 2 : 1;
+          const uint32_t fb = smem_addr(&full[r.st]);
+          if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kPairBlock * blocks);
           const uint32_t bar = map_shared_rank(fb, 0);
-          if (p.a_mn) {
-            tma_load_3d_pair(a, &p.ma, l0, kb * kKB, 0, bar);
-            tma_load_3d_pair(a + 8192, &p.ma, l0 + 64, kb * kKB, 0, bar);
-          } else {
-            tma_load_3d_pair(a, &p.ma, kb * kKB, l0, 0, bar);
-          }
-          if (p.b_mn) {
-            tma_load_3d_pair(b, &p.mb, c0, kb * kKB, 0, bar);
-            tma_load_3d_pair(b + 8192, &p.mb, c0 + 64, kb * kKB, 0, bar);
-          } else {
-            tma_load_3d_pair(b, &p.mb, kb * kKB, c0, 0, bar);
+          for (int i = 0; i < blocks; ++i) {
+            const uint32_t a = base + r.st * kPairStage + i * kPairBlock, b = a + kPairBlock / 2;
+            const int k = (kb + i) * kKB;
+            if (p.a_mn) {
+              tma_load_3d_pair(a, &p.ma, l0, k, 0, bar);
+              tma_load_3d_pair(a + 8192, &p.ma, l0 + 64, k, 0, bar);
+            } else {
+              tma_load_3d_pair(a, &p.ma, k, l0, 0, bar);
+            }
+            if (p.b_mn) {
+              tma_load_3d_pair(b, &p.mb, c0, k, 0, bar);
+              tma_load_3d_pair(b + 8192, &p.mb, c0 + 64, k, 0, bar);
+            } else {
+              tma_load_3d_pair(b, &p.mb, k, c0, 0, bar);
+            }
           }
           r.next(p.stages);
           lap0 = lap0 && r.st > 0;
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
-      const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + kPairStage / 2, p.b_mn, 0);
+      const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + kPairBlock / 2, p.b_mn, 0);
       const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2;  // 16 contraction steps, in units of 16 bytes
       RingPos r;
       int g = 0;
@@ -594,7 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
         tc_fence_after();
         const uint32_t d = tmem + buf * kPairN;
         uint32_t acc = 0;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = 0; kb < p.kblocks; kb += 2) {
           if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns)) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
@@ -606,6 +614,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
           for (int kk = 0; kk < kKB / 16; ++kk) {
             tc_mma_bf16_pair(d, da + kk * sa, db + kk * sb, p.idesc, acc);
             acc = 1;
+          }
+          if (kb + 1 < p.kblocks) {
+#pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk)
+              tc_mma_bf16_pair(d, da + kPairBlock / 16 + kk * sa, db + kPairBlock / 16 + kk * sb, p.idesc, 1u);
           }
           tc_commit_pair(smem_addr(&empty[r.st]));
           r.next(p.stages);
