@@ -174,10 +174,9 @@ BwdLayout bwd_layout(int64_t M, int N, int K, int dtype, int act) {
   const int np = bf16 ? 1 : 3;
   BwdLayout L;
   L.dz = act != ATTNRES_ACT_NONE ? align_up(M * dz_pitch(N) * (bf16 ? 2 : 4)) : 0;
-  // rows of 64 tokens (CUDA cores, column sums), of 32 (wide tiles and pairs), or the
-  // clusters' of few tokens (at most 2 tiles x 8 ranks x 2)
-  int64_t rows = (M + 255) / 256 * 8;
-  if (M <= 256 && rows < 32) rows = 32;
+  // rows of 64 tokens (CUDA cores, column sums), of 32 (wide tiles and
+  // pairs), or the clusters' of up to 1024 tokens (16 per tile of 128)
+  const int64_t rows = M <= 1024 ? (M + 127) / 128 * 16 : (M + 255) / 256 * 8;
   L.part = align_up(rows * N * 4);
   L.x = !bf16 || K % 8 ? tc_prep_bytes(M, K, np) : 0;
   L.w = !bf16 || K % 8 ? tc_prep_bytes(N, K, np) : 0;

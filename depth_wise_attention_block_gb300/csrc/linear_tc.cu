@@ -104,40 +104,62 @@ __device__ __forceinline__ uint64_t plane_desc(uint32_t addr, bool mn, int kk) {
   return mn ? smem_desc_mn128(addr + kk * 2048, 8192) : smem_desc_k128(addr + kk * 32);
 }
 
+// 16 values of a row as they lie in memory
 template <typename T>
-__device__ __forceinline__ void load16(const T* p, float* v);
+struct Raw16;
 template <>
-__device__ __forceinline__ void load16<bf16_t>(const bf16_t* p, float* v) {
+struct Raw16<bf16_t> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const bf16_t* p, bool vec) {
+    if (vec) {
+      const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+      w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+    } else {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = bf16lo(u[j]);
-      v[8 * i + 2 * j + 1] = bf16hi(u[j]);
+      for (int i = 0; i < 8; ++i) w[i] = (uint32_t)p[2 * i].bits | (uint32_t)p[2 * i + 1].bits << 16;
     }
   }
-}
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float* v) {
+  __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 w = __ldg(reinterpret_cast<const float4*>(p) + i);
-    v[4 * i] = w.x;
-    v[4 * i + 1] = w.y;
-    v[4 * i + 2] = w.z;
-    v[4 * i + 3] = w.w;
+    for (int i = 0; i < 8; ++i) {
+      v[2 * i] = bf16lo(w[i]);
+      v[2 * i + 1] = bf16hi(w[i]);
+    }
   }
-}
+};
+template <>
+struct Raw16<float> {
+  float w[16];
+  __device__ __forceinline__ void load(const float* p, bool vec) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (vec) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+        w[4 * i] = a.x, w[4 * i + 1] = a.y, w[4 * i + 2] = a.z, w[4 * i + 3] = a.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[4 * i + j] = __ldg(p + 4 * i + j);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = w[i];
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store16(T* p, const float* v);
 template <>
 __device__ __forceinline__ void store16<bf16_t>(bf16_t* p, const float* v) {
+  uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    reinterpret_cast<uint4*>(p)[i] = make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                                pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  if ((reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+    st_global_v8(p, w);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 template <>
 __device__ __forceinline__ void store16<float>(float* p, const float* v) {
@@ -160,70 +182,64 @@ __device__ __forceinline__ float column_sums16(float* v, int lane) {
   return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 1);
 }
 
-// 16 columns n0 .. of row m (lanes: rows): values, then their columns' sums
-// over the warp (kEpiDz with partial rows).  `vec`: whole 16-byte accesses.
+// The epilogue of 16 columns n0 .. of row m (lanes: rows), and (kEpiDz with
+// partial rows) their columns' sums over the warp.  `ahead` loads the
+// residual's values, which a caller does before it waits for the product.
 template <typename T, int MODE>
-__device__ __forceinline__ void epilogue_row16(const TcParams& p, float* v, long long m, int n0, bool vec_out, bool vec_res,
-                                               int lane, int part_row) {
-  const LinearEpilogue& e = p.epi;
-  const bool row = m < p.lanes;
-  const bool full = n0 + 16 <= p.cols;
-  if (full) {
-    if (e.bias) {
-      float b[16];
-      if ((reinterpret_cast<uintptr_t>(e.bias) & 15) == 0)
-        load16<float>(e.bias + n0, b);
-      else
+struct RowEpilogue {
+  const TcParams& p;
+  bool vec_out, vec_res, vec_bias;
+  __device__ __forceinline__ explicit RowEpilogue(const TcParams& q) : p(q) {
+    vec_out = q.epi.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(q.epi.out) & 15) == 0;
+    vec_res = q.epi.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(q.epi.res) & 15) == 0;
+    vec_bias = (reinterpret_cast<uintptr_t>(q.epi.bias) & 15) == 0;
+  }
+  __device__ __forceinline__ void ahead(Raw16<T>& r, long long m, int n0) const {
+    if (p.epi.res && n0 + 16 <= p.cols)
+      r.load(static_cast<const T*>(p.epi.res) + (m < p.lanes ? m : 0) * p.epi.ldr + n0, vec_res);
+  }
+  __device__ __forceinline__ void run(float* v, const Raw16<T>& res, long long m, int n0, int lane, int part_row) const {
+    const LinearEpilogue& e = p.epi;
+    const bool row = m < p.lanes;
+    if (n0 + 16 <= p.cols) {
+      if (e.bias) {
+        Raw16<float> b;
+        b.load(e.bias + n0, vec_bias);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) b[i] = __ldg(e.bias + n0 + i);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] += b[i];
-    }
-    float r[16];
-    if (e.res) {
-      const T* src = static_cast<const T*>(e.res) + (row ? m : 0) * e.ldr + n0;
-      if (vec_res)
-        load16<T>(src, r);
-      else
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = load_elem(src + i);
-    }
-    if constexpr (MODE == kEpiDz) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = r[i] * act_slope(e.act, v[i]);
-    } else {
-      if (e.act != ATTNRES_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = act_value(e.act, v[i]);
+        for (int i = 0; i < 16; ++i) v[i] += b.w[i];
       }
+      float r[16];
       if (e.res) {
+        res.get(r);
+      } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] += r[i];
+        for (int i = 0; i < 16; ++i) r[i] = 0.f;
       }
-    }
-    if (row) {
-      T* dst = static_cast<T*>(e.out) + m * e.ldo + n0;
-      if (vec_out)
-        store16<T>(dst, v);
-      else
+      act_apply<MODE, 16>(e.act, v, r);
+      if (row) {
+        T* dst = static_cast<T*>(e.out) + m * e.ldo + n0;
+        if (vec_out) {
+          store16<T>(dst, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) store_elem(dst + i, v[i]);
-    }
-  } else {
+          for (int i = 0; i < 16; ++i) store_elem(dst + i, v[i]);
+        }
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      v[i] = row && n0 + i < p.cols ? epilogue_one<T, MODE>(e, m, n0 + i, v[i]) : 0.f;
+      for (int i = 0; i < 16; ++i) v[i] = row && n0 + i < p.cols ? epilogue_one<T, MODE>(e, m, n0 + i, v[i]) : 0.f;
+    }
+    if (MODE == kEpiDz && e.part) {
+      if (!row) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = 0.f;
+      }
+      const float s = column_sums16(v, lane);
+      const int n = n0 + lane / 2;
+      if ((lane & 1) == 0 && n < p.cols) e.part[(long long)part_row * p.cols + n] = s;
+    }
   }
-  if (MODE == kEpiDz && e.part) {
-    if (!row) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    }
-    const float s = column_sums16(v, lane);
-    const int n = n0 + lane / 2;
-    if ((lane & 1) == 0 && n < p.cols) e.part[(long long)part_row * p.cols + n] = s;
-  }
-}
+};
 
 __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   float v;
@@ -350,8 +366,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
     const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
     const int nchunk = (p.bn + 15) / 16;
     constexpr int kRegChunks = NP == 3 ? 4 : 1;  // NP = 3: bn <= 128
-    const bool vec_out = p.epi.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.out) & 15) == 0;
-    const bool vec_res = p.epi.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.res) & 15) == 0;
+    const RowEpilogue<T, MODE> epi(p);
     const float nan = __int_as_float(0x7fc00000);
     bool ok = true;
     int g = 0;
@@ -365,6 +380,8 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
 #pragma unroll
           for (int i = 0; i < 16; ++i) acc[c][i] = 0.f;
       }
+      Raw16<T> res[2];
+      if constexpr (!SWAP && NP == 1) epi.ahead(res[0], m, c0 + half * 16);
       for (int kb = kb0; kb < kb1; kb += group, ++g) {
         const int buf = g & 1;
         if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
@@ -387,9 +404,11 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             }
           }
         } else {
+#pragma unroll 2
           for (int ch = half; ch < nchunk; ch += 2) {
             uint32_t v[16];
             tmem_ld16(at + ch * 16, v);
+            if constexpr (!SWAP) epi.ahead(res[1], m, c0 + (ch + 2) * 16);
             tmem_ld_wait();
             float f[16];
 #pragma unroll
@@ -399,7 +418,8 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
               for (int i = 0; i < 16; ++i)
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((ch * 16 + i) * kLanes + 32 * quarter + lane) * 4), "f"(f[i]) : "memory");
             } else if (c0 + ch * 16 < p.cols) {
-              epilogue_row16<T, MODE>(p, f, m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+              epi.run(f, res[0], m, c0 + ch * 16, lane, l0 / 32 + quarter);
+              res[0] = res[1];
             }
           }
         }
@@ -421,7 +441,8 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
               for (int i = 0; i < 16; ++i)
                 asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + ((ch * 16 + i) * kLanes + 32 * quarter + lane) * 4), "f"(acc[c][i]) : "memory");
             } else if (c0 + ch * 16 < p.cols) {
-              epilogue_row16<T, MODE>(p, acc[c], m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+              epi.ahead(res[0], m, c0 + ch * 16);
+              epi.run(acc[c], res[0], m, c0 + ch * 16, lane, l0 / 32 + quarter);
             }
           }
         }
@@ -630,8 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
-    const bool vec_out = p.epi.ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.out) & 15) == 0;
-    const bool vec_res = p.epi.ldr % 8 == 0 && (reinterpret_cast<uintptr_t>(p.epi.res) & 15) == 0;
+    const RowEpilogue<bf16_t, MODE> epi(p);
     const float nan = __int_as_float(0x7fc00000);
     bool ok = true;
     int g = 0;
@@ -639,19 +659,24 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
       const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN;
       const long long m = l0 + 32 * quarter + lane;
       const int buf = g & 1;
+      Raw16<bf16_t> res[2];
+      epi.ahead(res[0], m, c0 + half * 16);
       if (ok && !__all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
         if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
         ok = false;
       }
       tc_fence_after();
+#pragma unroll 2
       for (int ch = half; ch < kPairN / 16; ch += 2) {
         uint32_t v[16];
         tmem_ld16(lanes_at + buf * kPairN + ch * 16, v);
+        epi.ahead(res[1], m, c0 + (ch + 2) * 16);
         tmem_ld_wait();
         float f[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = ok ? __uint_as_float(v[i]) : nan;
-        if (c0 + ch * 16 < p.cols) epilogue_row16<bf16_t, MODE>(p, f, m, c0 + ch * 16, vec_out, vec_res, lane, l0 / 32 + quarter);
+        if (c0 + ch * 16 < p.cols) epi.run(f, res[0], m, c0 + ch * 16, lane, l0 / 32 + quarter);
+        res[0] = res[1];
       }
       tc_fence_before();
       __syncwarp();
@@ -695,23 +720,25 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ PrepP
   const PrepJob& j = p.job[blockIdx.y];
   pdl_wait();
   pdl_trigger();
-  const long long pairs = j.pitch / 2, total = j.rows * pairs;
-  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < total; i += gridDim.x * 256LL) {
-    const long long r = i / pairs;
-    const int c = (int)(i % pairs) * 2;
-    if constexpr (NP == 1) {
-      const uint16_t* s = static_cast<const uint16_t*>(j.src) + r * j.ld + c;
-      const uint32_t lo = c < j.cols ? s[0] : 0, hi = c + 1 < j.cols ? s[1] : 0;
-      reinterpret_cast<uint32_t*>(j.dst)[i] = lo | hi << 16;
-    } else {
-      const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
-      float a = c < j.cols ? s[0] : 0.f, b = c + 1 < j.cols ? s[1] : 0.f;
+  const long long plane = j.rows * j.pitch;
+  for (long long r = blockIdx.x; r < j.rows; r += gridDim.x) {
+    uint32_t* dst = reinterpret_cast<uint32_t*>(j.dst + r * j.pitch);
+#pragma unroll 2
+    for (int c = threadIdx.x * 2; c < j.pitch; c += 512) {
+      if constexpr (NP == 1) {
+        const uint16_t* s = static_cast<const uint16_t*>(j.src) + r * j.ld + c;
+        const uint32_t lo = c < j.cols ? s[0] : 0, hi = c + 1 < j.cols ? s[1] : 0;
+        dst[c / 2] = lo | hi << 16;
+      } else {
+        const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
+        float a = c < j.cols ? s[0] : 0.f, b = c + 1 < j.cols ? s[1] : 0.f;
 #pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        const uint32_t x = bf16_near(a), y = bf16_near(b);
-        reinterpret_cast<uint32_t*>(j.dst)[pl * total + i] = x | y << 16;
-        a -= bf16_bits_to_f32(x);
-        b -= bf16_bits_to_f32(y);
+        for (int pl = 0; pl < 3; ++pl) {
+          const uint32_t x = bf16_near(a), y = bf16_near(b);
+          dst[(pl * plane + c) / 2] = x | y << 16;
+          a -= bf16_bits_to_f32(x);
+          b -= bf16_bits_to_f32(y);
+        }
       }
     }
   }
@@ -810,7 +837,7 @@ TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
   }
   // narrow: M's rows as columns, N's as lanes, the contraction over a
   // cluster; the CTAs' streams share HBM (about 24 bytes per cycle and SM)
-  if (M <= 256) {
+  if (M <= 1024) {
     const int bn = M >= 128 ? 128 : (int)up(M, 16);
     const int slots = sm_count * (np == 3 ? 1 : 2);
     for (int ks = 1; ks <= kMaxKsplit && ks <= kblocks; ++ks) {
@@ -837,8 +864,7 @@ cudaError_t launch_tc_prep(const TcOperand* ops, int n, int np, cudaStream_t str
   for (int i = 0; i < n; ++i) {
     const int64_t pitch = up(ops[i].cols, 8);
     pp.job[i] = {ops[i].ptr, ops[i].ld, ops[i].rows, (int)ops[i].cols, pitch, static_cast<bf16_t*>(ops[i].prep)};
-    const int64_t c = (ops[i].rows * pitch / 2 + 255) / 256;
-    if (c > most) most = c;
+    if (ops[i].rows > most) most = ops[i].rows;
   }
   const dim3 grid((unsigned)(most < 2432 ? most : 2432), n);
   return np == 3 ? launch_kernel(prep_kernel<3>, grid, dim3(256), 0, stream, pp)
