@@ -41,6 +41,28 @@ namespace {
 constexpr int kC = kScanChunk;         // tokens per chunk
 constexpr int kTileThreads = 576;      // 8 warps scores and outputs, 8 state, TMA, MMA
 constexpr int kMaxSlots = 8;
+// Dynamic shared memory of sm_103a's 227 KB per CTA beside 2 KB of barriers
+// and tables.  The rings' lengths are constants: a division by a length read
+// from a parameter costs the issuing threads more than a product.
+constexpr int kDynSmem = 232448 - 2048;
+
+// ring slots of the scan, of the states' kernel
+template <int DA, int DC, int TERMS>
+struct ScanSmem {
+  static constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;
+  static constexpr int kFixed = DC * DA * 2 + (TERMS - 1) * kC * DA * 2 + 1024;
+  static constexpr int kFit = (kDynSmem - kFixed) / kTile, kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr int kBytes = kFixed + kSlots * kTile;
+  static_assert(kSlots >= 4, "a chunk's tiles and the next chunk's first");
+};
+constexpr int kHalf = kC / 2;
+template <int DA, int DC>
+struct StateSmem {
+  static constexpr int kStage = kHalf * (DA + DC) * 2;
+  static constexpr int kFixed = 4 * kHalf * DA * 2 + 1024;
+  static constexpr int kFit = (kDynSmem - kFixed) / kStage, kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
+  static constexpr int kBytes = kFixed + kSlots * kStage;
+};
 constexpr int kPanel = kC * 128;       // bytes of 64 channels of a tile
 
 struct Segment {
@@ -54,7 +76,6 @@ struct ScanTcParams {
   const int* nsegs;
   int seg_len;           // tokens per segment (0: a sequence is one segment)
   float* seg_state;      // [segment][H][..]: STATE writes each segment's own, the scan reads the state before it
-  int slots;
   int* dev_err;
   unsigned long long wait_ns;
 };
@@ -101,7 +122,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // where only bf16 outputs follow from it.
 template <int DA, int DC, int TERMS>
 __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams p) {
-  constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;  // bytes of a slot
+  constexpr int kTile = ScanSmem<DA, DC, TERMS>::kTile, kSlots = ScanSmem<DA, DC, TERMS>::kSlots;
   constexpr int kTiles = 3;                            // tiles per chunk: a, b, c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -109,12 +130,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
   __shared__ uint32_t tmem_base;
   __shared__ float tab[2 * kC], pw[kC + 2];  // p_scale l^(i - kC), 0 below; l^i
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t s_buf = base + p.slots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
+  const uint32_t s_buf = base + kSlots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
 
   if (tid == 0) {
-    for (int s = 0; s < p.slots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 1);
     }
@@ -172,8 +193,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
       for (int n = 0; n < nchunk && ok; ++n) {
         const int t = chunk_at(n);
         for (int k = 0; k < kTiles; ++k, ++it) {
-          const int st = it % p.slots;
-          wait(&empty[st], (uint32_t)(it / p.slots) + 1u);
+          const int st = it % kSlots;
+          wait(&empty[st], (uint32_t)(it / kSlots) + 1u);
           if (!ok) break;
           const int D = k == 2 ? DC : DA;
           const CUtensorMap* m = k == 0 ? &p.ma : k == 1 ? &p.mb : &p.mc;
@@ -183,16 +204,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         }
       }
       // the CTA never exits under a copy
-      const int armed = it < p.slots ? it : p.slots;
-      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / p.slots) & 1u);
+      const int armed = it < kSlots ? it : kSlots;
+      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / kSlots) & 1u);
     }
     __syncwarp();
   } else if (warp == 17) {
     if (lane == 0) {
       constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC),
                          kI4 = tc_idesc_bf16(128, DA, true, true);
-      auto slot = [&](int i) { return base + i % p.slots * kTile; };
-      auto wait_tile = [&](int i) { wait(&full[i % p.slots], (uint32_t)(i / p.slots)); };
+      auto slot = [&](int i) { return base + i % kSlots * kTile; };
+      auto wait_tile = [&](int i) { wait(&full[i % kSlots], (uint32_t)(i / kSlots)); };
       // scores of chunk n, over those of n - 1 (whose P c is done)
       auto scores = [&](int n) {
         const int it = n * kTiles;
@@ -220,7 +241,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < DA / 16; ++kk)
           tc_mma_bf16(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
-        tc_commit(smem_addr(&empty[it % p.slots]));
+        tc_commit(smem_addr(&empty[it % kSlots]));
         wait_tile(ic);
         // rows behind a short chunk's end are cleared with the weighted rows
         if (chunk_len(n) < kC) wait(&b_ready, ph);
@@ -244,8 +265,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
-        tc_commit(smem_addr(&empty[ib % p.slots]));
-        tc_commit(smem_addr(&empty[ic % p.slots]));
+        tc_commit(smem_addr(&empty[ib % kSlots]));
+        tc_commit(smem_addr(&empty[ic % kSlots]));
         tc_commit(smem_addr(&u_full));
       }
     }
@@ -258,7 +279,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
     // b's rows times their decay, as three bf16 terms (hi over b itself)
     auto split = [&](int n, int t0) {
       const int len = chunk_len(n);
-      const uint32_t B = base + (n * kTiles + 1) % p.slots * kTile, Ct = base + (n * kTiles + 2) % p.slots * kTile;
+      const uint32_t B = base + (n * kTiles + 1) % kSlots * kTile, Ct = base + (n * kTiles + 2) % kSlots * kTile;
       // thread t0's vectors of 8 channels lie in rows t0 / 8 + kStep i of each
       // panel, i < kBatch; a panel's are loaded before the first is stored
       const float* fac = pw + p.s.shift + (rev ? 0 : len - 1);
@@ -359,8 +380,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         // have read its terms
         if (n > 0) warp_wait(&u_full, n - 1);
         const int ib = n * kTiles + 1;
-        warp_wait(&full[ib % p.slots], (uint32_t)(ib / p.slots));
-        if (len < kC) warp_wait(&full[(ib + 1) % p.slots], (uint32_t)((ib + 1) / p.slots));
+        warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
+        if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
         split(n, tid);
 
         warp_wait(&o_full, n);
@@ -490,12 +511,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
 // warps weigh the rows of the next (its terms have a second buffer) and add
 // the last whole chunk's sums, from one of two accumulators in TMEM, to the
 // state (a quarter of a row of DA per thread).  The bound is HBM.
-constexpr int kHalf = kC / 2;
 constexpr int kHalfPanel = kHalf * 128;  // bytes of 64 channels of a half chunk
 
 template <int DA, int DC>
 __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_constant__ ScanTcParams p) {
-  constexpr int kTileB = kHalf * DA * 2, kStage = kHalf * (DA + DC) * 2;
+  constexpr int kTileB = kHalf * DA * 2, kStage = StateSmem<DA, DC>::kStage, kSlots = StateSmem<DA, DC>::kSlots;
   constexpr uint32_t kColU = 128;  // columns between the accumulators
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], b_ready[2], t_free[2], u_full[2], u_free[2];
@@ -503,12 +523,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   __shared__ float pw[kC + 2];  // l^i
   // stages (b, c), then two buffers of two terms (which an operand of 64
   // channels reads into behind the last stage: rows of its product not used)
-  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + p.slots * kStage;
+  const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + kSlots * kStage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
 
   if (tid == 0) {
-    for (int s = 0; s < p.slots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 1);
     }
@@ -555,8 +575,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     if (lane == 0) {
       int i = 0;
       for (; i < nhalf; ++i) {
-        const int st = i % p.slots, t = chunk_at(i / 2) + i % 2 * kHalf;
-        wait(&empty[st], (uint32_t)(i / p.slots) + 1u);
+        const int st = i % kSlots, t = chunk_at(i / 2) + i % 2 * kHalf;
+        wait(&empty[st], (uint32_t)(i / kSlots) + 1u);
         if (!ok) break;
         const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
         mbar_arrive_expect_tx(fb, kStage);
@@ -566,15 +586,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
         for (int x = 0; x < DC; x += 64) tma_load_2d(to + kTileB + x / 64 * kHalfPanel, &p.mc, h * DC + x, t, fb);
       }
       // the CTA never exits under a copy
-      const int armed = i < p.slots ? i : p.slots;
-      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((i - 1 - st) / p.slots) & 1u);
+      const int armed = i < kSlots ? i : kSlots;
+      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((i - 1 - st) / kSlots) & 1u);
     }
     __syncwarp();
   } else if (warp == 17) {
     if (lane == 0) {
       constexpr uint32_t kI = tc_idesc_bf16(128, DA, true, true);
       for (int i = 0; i < nhalf && ok; ++i) {
-        const int st = i % p.slots, n = i / 2;
+        const int st = i % kSlots, n = i / 2;
         const uint32_t d = tmem + (n & 1) * kColU;
         wait(&b_ready[i & 1], (uint32_t)(i / 2));
         if (i % 2 == 0) wait(&u_free[n & 1], (uint32_t)(n / 2) + 1u);
@@ -617,9 +637,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
       if (lane == 0) mbar_arrive(smem_addr(&u_free[n & 1]));
     };
     for (int i = 0; i < nhalf; ++i) {
-      const int st = i % p.slots, len = chunk_len(i / 2), j0 = i % 2 * kHalf;  // rows j0 .. of the chunk
+      const int st = i % kSlots, len = chunk_len(i / 2), j0 = i % 2 * kHalf;  // rows j0 .. of the chunk
       const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + (i & 1) * 2 * kTileB;
-      warp_wait(&full[st], (uint32_t)(i / p.slots));
+      warp_wait(&full[st], (uint32_t)(i / kSlots));
       warp_wait(&t_free[i & 1], (uint32_t)(i / 2) + 1u);
       // one vector of 8 channels per thread and panel of 64: row tid / 8
       const int j = j0 + tid / 8;
@@ -790,41 +810,35 @@ Layout layout(int64_t T, int H, int Dk, int Dv, int N, int seg_len) {
 }
 
 template <int DA, int DC, int TERMS>
-cudaError_t launch_scan_tile(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
-  constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;
-  const int fixed = DC * DA * 2 + (TERMS - 1) * kC * DA * 2 + 1024;
-  const int smem_max = di.max_smem_optin - 2048;  // barriers and power tables are static
-  p.slots = (smem_max - fixed) / kTile;
-  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
-  if (p.slots < 4) return cudaErrorInvalidValue;
+cudaError_t launch_scan_tile(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+  constexpr int kBytes = ScanSmem<DA, DC, TERMS>::kBytes;
+  if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
   const auto kern = scan_tc_kernel<DA, DC, TERMS>;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), smem_max);
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)(fixed + p.slots * kTile), stream, p);
+  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)kBytes, stream, p);
 }
 
 template <int TERMS>
-cudaError_t launch_scan_dims(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+cudaError_t launch_scan_dims(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
   if (p.s.Da == 128)
     return p.s.Dc == 128 ? launch_scan_tile<128, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<128, 64, TERMS>(p, segs, di, stream);
   return p.s.Dc == 128 ? launch_scan_tile<64, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<64, 64, TERMS>(p, segs, di, stream);
 }
 
 template <int DA, int DC>
-cudaError_t launch_state_tile(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
-  constexpr int kStage = kHalf * (DA + DC) * 2, kFixed = 4 * kHalf * DA * 2 + 1024;
-  const int smem_max = di.max_smem_optin - 2048;
-  p.slots = (smem_max - kFixed) / kStage;
-  if (p.slots > kMaxSlots) p.slots = kMaxSlots;
+cudaError_t launch_state_tile(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+  constexpr int kBytes = StateSmem<DA, DC>::kBytes;
+  if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
   const auto kern = state_tc_kernel<DA, DC>;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), smem_max);
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)(kFixed + p.slots * kStage), stream, p);
+  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)kBytes, stream, p);
 }
 
-cudaError_t launch_state_dims(ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+cudaError_t launch_state_dims(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
   if (p.s.Da == 128) return p.s.Dc == 128 ? launch_state_tile<128, 128>(p, segs, di, stream) : launch_state_tile<128, 64>(p, segs, di, stream);
   return p.s.Dc == 128 ? launch_state_tile<64, 128>(p, segs, di, stream) : launch_state_tile<64, 64>(p, segs, di, stream);
 }
