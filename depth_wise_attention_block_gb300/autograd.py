@@ -1,4 +1,5 @@
-"""One layer of depth-wise attention as a differentiable torch operation.
+"""One layer of depth-wise attention, and the operators of a layer body, as
+differentiable torch operations.
 
 `aggregate(H, w)` returns r = sum_s softmax_s(w . RMSNorm(H_s)) H_s for a
 [S, T, d] stack of sources (float32 or bfloat16) and an fp32 pseudo-query
@@ -10,14 +11,30 @@ workspace.  Gradients: dH in the sources' dtype, dw in fp32 (summed over
 tokens in a fixed order, so bit-reproducible).  The incoming gradient of r
 is taken in the sources' dtype (the backward kernel reads it so): an fp32
 gradient for bf16 sources is rounded to bf16 first.
+
+`linear`, `qk_norm_rope` and `linear_attention` wrap the calls of the same
+names the same way: nothing but the inputs is kept, the backward recomputes
+what it needs, incoming gradients are taken in the tensors' dtype, and
+gradients nobody asks for are not formed.  They can be differentiated once.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import ATTNRES_DEFAULT_EPS, attnres_aggregate, attnres_aggregate_backward
+from . import (
+    ATTNRES_DEFAULT_EPS,
+    attnres_aggregate,
+    attnres_aggregate_backward,
+    attnres_linear,
+    attnres_linear_attention,
+    attnres_linear_attention_backward,
+    attnres_linear_backward,
+    attnres_qk_norm_rope,
+    attnres_qk_norm_rope_backward,
+)
 
-__all__ = ["AttnResAggregate", "aggregate"]
+__all__ = ["AttnResAggregate", "aggregate", "linear", "qk_norm_rope", "linear_attention"]
 
 
 class AttnResAggregate(torch.autograd.Function):
@@ -47,3 +64,120 @@ class AttnResAggregate(torch.autograd.Function):
 def aggregate(H: torch.Tensor, w: torch.Tensor, eps: float = ATTNRES_DEFAULT_EPS) -> torch.Tensor:
     """r = sum_s softmax_s(w . RMSNorm(H_s)) H_s, differentiable in H and w."""
     return AttnResAggregate.apply(H, w, eps)
+
+
+def _rows_contiguous(t: torch.Tensor) -> torch.Tensor:
+    """t itself where the calls take it (rows contiguous behind the first
+    dimension, in order), or a contiguous copy."""
+    inner = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n > 1 and s != inner:
+            return t.contiguous()
+        inner *= n
+    return t if t.shape[0] <= 1 or t.stride(0) >= inner else t.contiguous()
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, residual, activation):
+        x, w = _rows_contiguous(x), w.contiguous()
+        out = torch.empty((x.shape[0], w.shape[0]), dtype=x.dtype, device=x.device)
+        attnres_linear(x, w, out, bias=bias, residual=None if residual is None else _rows_contiguous(residual),
+                       activation=activation)
+        ctx.save_for_backward(x, w, bias)
+        ctx.activation = activation
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, w, bias = ctx.saved_tensors
+        need_x, need_w, need_b, need_r, _ = ctx.needs_input_grad
+        grad = _rows_contiguous(grad.to(x.dtype))
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
+        gw = torch.empty_like(w) if need_w else None
+        gb = torch.empty_like(bias) if need_b else None
+        attnres_linear_backward(x, w, grad, gx, gw, gb, bias=bias, activation=ctx.activation)
+        return gx, gw, gb, grad if need_r else None, None
+
+
+def linear(x: torch.Tensor, w: torch.Tensor, bias: torch.Tensor | None = None,
+           residual: torch.Tensor | None = None, activation: str = "none") -> torch.Tensor:
+    """activation(x w^T + bias) + residual over x's last dimension; w [N, K]
+    of x's dtype, bias [N] float32, residual of the result's shape."""
+    lead = x.shape[:-1]
+    flat = None if residual is None else residual.reshape(-1, w.shape[0])
+    return _Linear.apply(x.reshape(-1, x.shape[-1]), w, bias, flat, activation).reshape(*lead, w.shape[0])
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_gain, k_gain, positions, inv_freq, interleaved, eps):
+        q, k = _rows_contiguous(q), _rows_contiguous(k)
+        outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
+        ctx.rope = dict(positions=positions, inv_freq=inv_freq, interleaved=interleaved, eps=eps)
+        attnres_qk_norm_rope(q, k, *outs, q_gain=q_gain, k_gain=k_gain, **ctx.rope)
+        ctx.save_for_backward(q, k, q_gain, k_gain)
+        return tuple(outs)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gq, gk):
+        q, k, q_gain, k_gain = ctx.saved_tensors
+        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
+        gains = [torch.empty_like(g) if g is not None and need else None
+                 for g, need in zip((q_gain, k_gain), ctx.needs_input_grad[2:4])]
+        attnres_qk_norm_rope_backward(q, k, _rows_contiguous(gq.to(q.dtype)), _rows_contiguous(gk.to(k.dtype)), *grads,
+                                      q_gain=q_gain, k_gain=k_gain, grad_q_gain=gains[0], grad_k_gain=gains[1],
+                                      **ctx.rope)
+        return (*grads, *gains, None, None, None, None)
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: torch.Tensor | None = None,
+                 k_gain: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                 inv_freq: torch.Tensor | None = None, interleaved: bool = False,
+                 eps: float = ATTNRES_DEFAULT_EPS) -> tuple[torch.Tensor, torch.Tensor]:
+    """RMSNorm of q's and k's heads [T, heads, D] and their rotation, differentiable in q, k and the gains."""
+    return _QkNormRope.apply(q, k, q_gain, k_gain, positions, inv_freq, interleaved, eps)
+
+
+class _LinearAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, log_decay, cu_seqlens, initial_state, scale):
+        q, k, v = _rows_contiguous(q), _rows_contiguous(k), _rows_contiguous(v)
+        n = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+        out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+        if cu_seqlens is not None:
+            out.zero_()  # rows outside every sequence
+        final = torch.empty((n, q.shape[1], q.shape[2], v.shape[2]), dtype=torch.float32, device=q.device)
+        initial_state = None if initial_state is None else initial_state.contiguous()
+        attnres_linear_attention(q, k, v, log_decay, out, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                                 final_state=final, scale=scale)
+        ctx.save_for_backward(q, k, v, log_decay, cu_seqlens, initial_state)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return out, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_final):
+        q, k, v, log_decay, cu_seqlens, initial_state = ctx.saved_tensors
+        if grad_out is None:
+            grad_out = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
+        make = torch.empty if cu_seqlens is None else torch.zeros
+        grads = [make(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
+        g0 = torch.empty_like(initial_state) if initial_state is not None and ctx.needs_input_grad[5] else None
+        attnres_linear_attention_backward(q, k, v, log_decay, _rows_contiguous(grad_out.to(v.dtype)), *grads,
+                                          cu_seqlens=cu_seqlens, initial_state=initial_state,
+                                          grad_final_state=None if grad_final is None else grad_final.contiguous(),
+                                          grad_initial_state=g0, scale=ctx.scale)
+        return (*grads, None, None, g0, None)
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                     cu_seqlens: torch.Tensor | None = None, initial_state: torch.Tensor | None = None,
+                     scale: float | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(out [T, H, Dv], final states [num_seqs, H, Dk, Dv] float32) of
+    attnres_linear_attention, differentiable in q, k, v and the initial
+    states; rows outside every sequence are zero and get zero gradients."""
+    return _LinearAttention.apply(q, k, v, log_decay, cu_seqlens, initial_state, scale)

@@ -82,11 +82,20 @@ class StackForward:
     With `early_loads` the fused steps load their stored rows before the
     body before them has finished (ATTNRES_STATE_EARLY_LOADS); the results
     are the same bits.
+
+    body: what runs between the aggregations in place of the stand-in (G and
+    Sc may then be None): an object whose `issue(layer, r, F, stream)` issues
+    launches that write v_layer to F from r and write nothing of the state's
+    rows (LinearAttentionBody is one).  With early_loads its last launch has
+    to meet that flag's conditions, as every call of the library does.
     """
 
     def __init__(self, h0, W, G, Sc, num_layers: int, block_size: int, eps: float = 1e-5,
                  keep_weights: bool = True, dev_err: torch.Tensor | None = None, schedule: str = "single",
-                 two_phase_from: int = 6, early_loads: bool = True, first_layer_from_pass: bool = True):
+                 two_phase_from: int = 6, early_loads: bool = True, first_layer_from_pass: bool = True, body=None):
+        if body is None and (G is None or Sc is None):
+            raise ValueError("the stand-in body needs G and Sc")
+        self.body = body
         self.L, self.B, self.eps = num_layers, block_size, eps
         T, d = h0.shape
         self.T, self.d = T, d
@@ -141,7 +150,16 @@ class StackForward:
         q = min(n * self.B, self.L) - (n - 1) * self.B
         return n <= self.PASS_MAX_SOURCES and q <= self.PASS_MAX_QUERIES
 
+    def _issue_body(self, layer: int, stream=None) -> None:
+        """v_layer into F from r."""
+        if self.body is None:
+            attnres_synthetic_layer(self.r, self.G[layer - 1], self.Sc[layer - 1], self.F, stream=stream)
+        else:
+            self.body.issue(layer, self.r, self.F, stream)
+
     def launches_per_forward(self) -> int:
+        if self.body is not None:
+            raise ValueError("the launch count is that of the stand-in body")
         if self.schedule == "single":
             return 2 * self.L + 1
         N = -(-self.L // self.B)
@@ -165,7 +183,7 @@ class StackForward:
                     attnres_layer_step(st, self.F if l > 1 else None, self.W[l - 1], l, self.r,
                                        self.weights[l - 1] if self.weights is not None else None,
                                        dev_err=self.dev_err, stream=stream)
-                    attnres_synthetic_layer(self.r, self.G[l - 1], self.Sc[l - 1], self.F, stream=stream)
+                    self._issue_body(l, stream)
                     if on_layer is not None:
                         on_layer(l, self)
                 continue
@@ -186,7 +204,7 @@ class StackForward:
                                             self.R_inter[q], self.lse_inter[q], A[q], self.r,
                                             self.weights[layer - 1] if self.weights is not None else None,
                                             dev_err=self.dev_err, stream=stream)
-                attnres_synthetic_layer(self.r, self.G[layer - 1], self.Sc[layer - 1], self.F, stream=stream)
+                self._issue_body(layer, stream)
                 if on_layer is not None:
                     on_layer(layer, self)
         attnres_layer_step(st, self.F, self.W[L], L + 1, self.r,
@@ -205,7 +223,7 @@ class StackForward:
             attnres_layer_step(self.state, self.F if l > first else None, self.W[l - 1], l, self.r,
                                self.weights[l - 1] if self.weights is not None else None,
                                dev_err=self.dev_err, stream=stream)
-            attnres_synthetic_layer(self.r, self.G[l - 1], self.Sc[l - 1], self.F, stream=stream)
+            self._issue_body(l, stream)
             if on_layer is not None:
                 on_layer(l, self)
         if last == self.L:
@@ -262,7 +280,10 @@ class StackForward:
 
     def bytes_moved(self) -> int:
         """Minimum HBM bytes one forward must move (every source row, F row,
-        partial/b_n row read once; r, F, partial/b_n and weights written once)."""
+        partial/b_n row read once; r, F, partial/b_n and weights written once),
+        with the stand-in body."""
+        if self.body is not None:
+            raise ValueError("the byte model is that of the stand-in body")
         return stack_forward_bytes(self.T, self.d, self.state.h0.element_size(), self.L, self.B)
 
 
@@ -291,6 +312,8 @@ class StackBackward:
     """
 
     def __init__(self, fwd: StackForward):
+        if fwd.body is not None:
+            raise ValueError("StackBackward differentiates the stand-in body (see autograd for the others)")
         self.fwd = fwd
         st, T, d, B = fwd.state, fwd.T, fwd.d, fwd.B
         dt, dev = st.h0.dtype, st.h0.device
