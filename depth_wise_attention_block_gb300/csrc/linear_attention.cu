@@ -25,131 +25,241 @@ namespace attnres {
 
 namespace {
 
-constexpr int kSC = 32;        // tokens per chunk
-constexpr int kSD = 32;        // columns of c per CTA
+constexpr int kSC = 64;        // tokens per chunk
 constexpr int kSThreads = 256;
 constexpr int kSMaxD = 256;
+constexpr int kSPitchP = kSC + 4;
 
-// rows of a and b in shared memory: one word of padding against bank conflicts
-__host__ __device__ constexpr int scan_pitch(int Da) { return Da + 1; }
-__host__ constexpr int scan_smem(int Da) {
-  return (2 * kSC * scan_pitch(Da) + kSC * kSD + kSC * (kSC + 1) + Da * kSD + 2 * kSC) * 4;
+// The scan on the CUDA cores: a CTA takes a sequence, a head and NG groups of
+// 32 columns of c.  Every product runs from shared memory in register tiles,
+// four rows by 2 NG columns per thread (16 x 16 threads), four steps of its
+// contraction per 16-byte load of the rows, column pairs in packed fp32.
+// Rows lie 16 bytes further apart than their length (no bank conflicts
+// between a tile's rows).  The bound is the FMA rate, of which shared-memory
+// loads leave about half.
+__host__ __device__ constexpr int scan_rows(int Da) { return (Da + 3) / 4 * 4 + 4; }  // pitch of a and b
+__host__ constexpr int scan_smem(int Da, int NG) {
+  const int d = (Da + 63) / 64 * 64;  // the state's rows, whole tiles
+  return (2 * kSC * scan_rows(Da) + kSC * 32 * NG + kSC * kSPitchP + d * 32 * NG + kSC + 8) * 4;
 }
 
+// rows 0 .. kSC - 1 (zero from len on) of `width` channels to dst, columns up to `cols` zero-filled
 template <typename T>
+__device__ __forceinline__ void scan_load(float* dst, int pitch, const void* src, long long stride, int off, int width, int cols, int len,
+                                          const SeqRange& sr, long long i0, bool reverse, bool vec) {
+  const T* p = static_cast<const T*>(src) + off;
+  const int q = cols / 4;
+  for (int i = threadIdx.x; i < kSC * q; i += kSThreads) {
+    const int r = i / q, c = i % q * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r < len) {
+      const T* at = p + sr.row(i0 + r, reverse) * stride + c;
+      if (vec && c + 4 <= width) {
+        if constexpr (sizeof(T) == 4) {
+          v = __ldg(reinterpret_cast<const float4*>(at));
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+          v = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        }
+      } else {
+        if (c < width) v.x = load_elem(at);
+        if (c + 1 < width) v.y = load_elem(at + 1);
+        if (c + 2 < width) v.z = load_elem(at + 2);
+        if (c + 3 < width) v.w = load_elem(at + 3);
+      }
+    }
+    *reinterpret_cast<float4*>(dst + r * pitch + c) = v;
+  }
+}
+
+// acc[r][s] += sum_k A[ty + 16 r][k] B[k][32 s + 2 tx ..], k < K (a multiple of 4)
+template <int NG>
+__device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A, int pitch, const float* B, int K, int tx, int ty) {
+#pragma unroll 2
+  for (int k = 0; k < K; k += 4) {
+    float4 a[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) a[r] = *reinterpret_cast<const float4*>(A + (ty + 16 * r) * pitch + k);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint64_t b[NG];
+#pragma unroll
+      for (int s = 0; s < NG; ++s) b[s] = *reinterpret_cast<const uint64_t*>(B + (k + e) * 32 * NG + 32 * s + 2 * tx);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float x = e == 0 ? a[r].x : e == 1 ? a[r].y : e == 2 ? a[r].z : a[r].w;
+        const uint64_t xx = f2_pack(x, x);
+#pragma unroll
+        for (int s = 0; s < NG; ++s) acc[r][s] = f2_fma(xx, b[s], acc[r][s]);
+      }
+    }
+  }
+}
+
+template <typename T, int NG>
 __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_constant__ ScanArgs p) {
-  extern __shared__ float sm[];
-  const int Da = p.Da, Dc = p.Dc, pitch = scan_pitch(Da);
+  extern __shared__ __align__(16) float sm[];
+  const int Da = p.Da, Dc = p.Dc, pitch = scan_rows(Da), K = pitch - 4, Dr = (Da + 63) / 64 * 64;
+  constexpr int NC = 32 * NG;
   float* a = sm;                        // [kSC][pitch]
   float* b = a + kSC * pitch;           // [kSC][pitch]
-  float* c = b + kSC * pitch;           // [kSC][kSD]
-  float* P = c + kSC * kSD;             // [kSC][kSC + 1]
-  float* S = P + kSC * (kSC + 1);       // [Da][kSD]
-  float* pw = S + Da * kSD;             // l^0 .. l^kSC
-  const int tid = threadIdx.x;
-  const int c0 = blockIdx.x * kSD, h = blockIdx.y;
+  float* c = b + kSC * pitch;           // [kSC][NC]
+  float* P = c + kSC * NC;              // [kSC][kSPitchP]
+  float* S = P + kSC * kSPitchP;        // [Dr][NC]
+  float* pw = S + Dr * NC;              // l^0 .. l^kSC
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int c0 = blockIdx.x * NC, h = blockIdx.y, wc = Dc - c0 < NC ? Dc - c0 : NC;
   pdl_wait();
   pdl_trigger();
   const float g = p.log_decay[h];
   if (tid <= kSC) pw[tid] = expf(g * (float)tid);
-  for (int n = blockIdx.z; n < p.N; n += gridDim.z) {
-    const SeqRange sr = seq_range(p.cu, n, p.T);
-    const long long st = ((long long)n * p.H + h) * Da * Dc;
+  const int n = blockIdx.z;
+  const SeqRange sr = seq_range(p.cu, n, p.T);
+  const long long st = ((long long)n * p.H + h) * Da * Dc;
+  for (int i = tid; i < Dr * NC; i += kSThreads) {
+    const int da = i / NC, dc = c0 + i % NC;
+    S[i] = p.s_in && da < Da && dc < Dc ? p.s_in[st + p.state_at(da, dc)] : 0.f;
+  }
+  for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
+    const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
     __syncthreads();
-    for (int i = tid; i < Da * kSD; i += kSThreads) {
-      const int da = i / kSD, dc = c0 + i % kSD;
-      S[i] = p.s_in && dc < Dc ? p.s_in[st + p.state_at(da, dc)] : 0.f;
-    }
-    for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
-      const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
-      __syncthreads();
-      for (int i = tid; i < kSC * Da; i += kSThreads) {
-        const int r = i / Da, d = i % Da;
-        const long long row = sr.row(i0 + r, p.reverse);
-        a[r * pitch + d] = r < len ? load_elem(static_cast<const T*>(p.a) + row * p.as + (long long)h * Da + d) : 0.f;
-        b[r * pitch + d] = r < len ? load_elem(static_cast<const T*>(p.b) + row * p.bs + (long long)h * Da + d) : 0.f;
-      }
-      for (int i = tid; i < kSC * kSD; i += kSThreads) {
-        const int r = i / kSD, d = c0 + i % kSD;
-        const long long row = sr.row(i0 + r, p.reverse);
-        c[i] = r < len && d < Dc ? load_elem(static_cast<const T*>(p.c) + row * p.cs + (long long)h * Dc + d) : 0.f;
-      }
-      __syncthreads();
-      {  // the triangle: rows i, i + 16; columns j, j + 16
-        const int i = tid / 16, j = tid % 16;
-        float s00 = 0.f, s01 = 0.f, s10 = 0.f, s11 = 0.f;
-        for (int d = 0; d < Da; ++d) {
-          const float x0 = a[i * pitch + d], x1 = a[(i + 16) * pitch + d];
-          const float y0 = b[j * pitch + d], y1 = b[(j + 16) * pitch + d];
-          s00 = fmaf(x0, y0, s00);
-          s01 = fmaf(x0, y1, s01);
-          s10 = fmaf(x1, y0, s10);
-          s11 = fmaf(x1, y1, s11);
-        }
-        auto put = [&](int r, int q, float v) { P[r * (kSC + 1) + q] = q <= r ? v * pw[r - q] * p.p_scale : 0.f; };
-        put(i, j, s00);
-        put(i, j + 16, s01);
-        put(i + 16, j, s10);
-        put(i + 16, j + 16, s11);
-      }
-      __syncthreads();
-      {  // out rows ty, ty + 8, ..; column tx
-        const int tx = tid % 32, ty = tid / 32;
-        float in[4] = {}, from[4] = {};
-        for (int j = 0; j < kSC; ++j) {
-          const float y = c[j * kSD + tx];
+    scan_load<T>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
+    scan_load<T>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
+    scan_load<T>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
+    __syncthreads();
+    {  // the triangle: rows ty + 16 r, columns tx + 16 s, sums over even and odd channels packed
+      uint64_t acc[4][4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) in[r] = fmaf(P[(ty + 8 * r) * (kSC + 1) + j], y, in[r]);
-        }
-        for (int d = 0; d < Da; ++d) {
-          const float y = S[d * kSD + tx];
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) from[r] = fmaf(a[(ty + 8 * r) * pitch + d], y, from[r]);
-        }
+        for (int s = 0; s < 4; ++s) acc[r][s] = 0;
+      for (int k = 0; k < K; k += 4) {
+        ulonglong2 x[4], y[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const int i = ty + 8 * r;
-          if (i < len && c0 + tx < Dc)
-            store_elem(static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0 + tx,
-                       fmaf(from[r], pw[i + 1 - p.shift] * p.in_scale, in[r]));
+          x[r] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * r) * pitch + k);
+          y[r] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * r) * pitch + k);
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
       }
-      __syncthreads();
-      {  // the state: rows ty, ty + 8, ..; column tx
-        const int tx = tid % 32, ty = tid / 32;
-        float u[kSMaxD / 8];
 #pragma unroll
-        for (int r = 0; r < kSMaxD / 8; ++r) u[r] = 0.f;
-        for (int j = 0; j < len; ++j) {
-          const float y = c[j * kSD + tx] * pw[len - 1 - j + p.shift] * p.up_scale;
+      for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int r = 0; r < kSMaxD / 8; ++r)
-            if (ty + 8 * r < Da) u[r] = fmaf(b[j * pitch + ty + 8 * r], y, u[r]);
+        for (int s = 0; s < 4; ++s) {
+          const int i = ty + 16 * r, j = tx + 16 * s;
+          P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
         }
+    }
+    __syncthreads();
+    {
+      uint64_t in[4][NG], from[4][NG];
 #pragma unroll
-        for (int r = 0; r < kSMaxD / 8; ++r)
-          if (ty + 8 * r < Da) S[(ty + 8 * r) * kSD + tx] = fmaf(S[(ty + 8 * r) * kSD + tx], pw[len], u[r]);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
+      scan_mma<NG>(in, P, kSPitchP, c, (len + 3) / 4 * 4, tx, ty);
+      scan_mma<NG>(from, a, pitch, S, K, tx, ty);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = ty + 16 * r;
+        if (i < len) {
+          const float coef = pw[i + 1 - p.shift] * p.in_scale;
+          T* out = static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0;
+#pragma unroll
+          for (int s = 0; s < NG; ++s) {
+            float x0, x1, y0, y1;
+            f2_unpack(in[r][s], x0, x1);
+            f2_unpack(from[r][s], y0, y1);
+            const int d = 32 * s + 2 * tx;
+            if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
+            if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
+          }
+        }
       }
     }
     __syncthreads();
-    if (p.s_out)
-      for (int i = tid; i < Da * kSD; i += kSThreads) {
-        const int da = i / kSD, dc = c0 + i % kSD;
-        if (dc < Dc) p.s_out[st + p.state_at(da, dc)] = S[i];
+    // the state: rows d0 + 4 ty .. + 3
+    const uint64_t decay = f2_pack(pw[len], pw[len]), zero = f2_pack(0.f, 0.f);
+    for (int d0 = 0; d0 < Dr; d0 += 64) {
+      const int d = d0 + 4 * ty;
+      if (d >= K) continue;
+      uint64_t u[4][NG];
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < NG; ++s) u[r][s] = zero;
+#pragma unroll 4
+      for (int j = 0; j < len; ++j) {
+        const float f = pw[len - 1 - j + p.shift] * p.up_scale;
+        const float4 x = *reinterpret_cast<const float4*>(b + j * pitch + d);
+        const uint64_t w[4] = {f2_pack(x.x * f, x.x * f), f2_pack(x.y * f, x.y * f), f2_pack(x.z * f, x.z * f), f2_pack(x.w * f, x.w * f)};
+#pragma unroll
+        for (int s = 0; s < NG; ++s) {
+          const uint64_t y = *reinterpret_cast<const uint64_t*>(c + j * NC + 32 * s + 2 * tx);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) u[r][s] = f2_fma(w[r], y, u[r][s]);
+        }
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int s = 0; s < NG; ++s) {
+          uint64_t* at = reinterpret_cast<uint64_t*>(S + (d + r) * NC + 32 * s + 2 * tx);
+          *at = f2_fma(*at, decay, u[r][s]);
+        }
+    }
   }
+  __syncthreads();
+  if (p.s_out)
+    for (int i = tid; i < Da * NC; i += kSThreads) {
+      const int da = i / NC, dc = c0 + i % NC;
+      if (dc < Dc) p.s_out[st + p.state_at(da, dc)] = S[i];
+    }
+}
+
+template <typename T, int NG>
+cudaError_t launch_scan_any(const ScanArgs& s, cudaStream_t stream) {
+  static SmemOptIn optin;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  e = optin.ensure(reinterpret_cast<const void*>(scan_any_kernel<T, NG>));
+  if (e != cudaSuccess) return e;
+  return launch_kernel(scan_any_kernel<T, NG>, dim3((s.Dc + 32 * NG - 1) / (32 * NG), s.H, s.N), dim3(kSThreads), scan_smem(s.Da, NG), stream,
+                       s);
 }
 
 template <typename T>
-cudaError_t launch_scan_any(const ScanArgs& s, cudaStream_t stream) {
-  static SmemOptIn optin;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(scan_any_kernel<T>), scan_smem(kSMaxD));
+cudaError_t launch_scan_type(const ScanArgs& in, cudaStream_t stream) {
+  ScanArgs s = in;
+  auto vec = [](const void* p, long long stride, int D) {
+    return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0 && stride % 4 == 0 && D % 4 == 0;
+  };
+  s.vec_a = vec(s.a, s.as, s.Da);
+  s.vec_b = vec(s.b, s.bs, s.Da);
+  s.vec_c = vec(s.c, s.cs, s.Dc);
+  // as many columns per CTA as the chunk's scores are worth (every CTA of a
+  // head forms them again) and shared memory holds, but few enough for two
+  // CTAs per SM where that leaves the GPU idle
+  int ng = (s.Dc + 31) / 32;
+  if (ng > 4) ng = (ng + 1) / 2 > 4 ? 4 : (ng + 1) / 2;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  return launch_kernel(scan_any_kernel<T>, dim3((s.Dc + kSD - 1) / kSD, s.H, s.N), dim3(kSThreads), scan_smem(s.Da), stream, s);
+  while (ng > 1 && (scan_smem(s.Da, ng) > di.max_smem_optin || (int64_t)s.N * s.H * ((s.Dc + 32 * ng - 1) / (32 * ng)) < di.sm_count)) --ng;
+  switch (ng) {
+    case 1: return launch_scan_any<T, 1>(s, stream);
+    case 2: return launch_scan_any<T, 2>(s, stream);
+    case 3: return launch_scan_any<T, 3>(s, stream);
+    default: return launch_scan_any<T, 4>(s, stream);
+  }
 }
 
 cudaError_t launch_scan(const ScanArgs& s, int dtype, cudaStream_t stream) {
-  return dtype == ATTNRES_BF16 ? launch_scan_any<bf16_t>(s, stream) : launch_scan_any<float>(s, stream);
+  return dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, stream) : launch_scan_type<float>(s, stream);
 }
 
 // ------------------------------------------------------------------ step --

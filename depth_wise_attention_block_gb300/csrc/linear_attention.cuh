@@ -35,6 +35,7 @@ struct ScanArgs {
   bool transposed, reverse;
   int shift;               // 1: the carried state is already decayed for the next token
   bool wide_out;           // out's rows start on 32-byte boundaries (set by the launch)
+  bool vec_a, vec_b, vec_c;  // rows in vectors of 4 elements (set by the launch)
   float p_scale, in_scale, up_scale;  // factors of the triangle, of the carried state's part, of what enters the state
 
   __host__ __device__ int state_at(int da, int dc) const { return transposed ? dc * Da + da : da * Dc + dc; }
