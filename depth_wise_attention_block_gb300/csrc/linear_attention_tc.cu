@@ -10,10 +10,11 @@
 // MN-major (P c, the token sums) from the same tile.  Eight warps turn the
 // scores into P (bf16, back into TMEM as the next product's operand) and
 // write the outputs; eight warps hold the state in fp32 registers (half a
-// row of Da per thread), give it to the products rounded to bf16, and weigh b
-// with the decays: the weighted rows enter as three bf16 terms (24 bits), so
-// that the state keeps fp32 precision over any number of chunks; each chunk's
-// U starts from zero in TMEM and is added in fp32 round-to-nearest.
+// row of Da per thread) and give it to the products rounded to bf16; all of
+// them weigh b with the decays.  The weighted rows enter as three bf16 terms
+// (24 bits) where the state is a result, so that it keeps fp32 precision over
+// any number of chunks; each chunk's U starts from zero in TMEM and is added
+// in fp32 round-to-nearest.
 //
 // A reversed scan (gradients of k and v) takes the chunks from the end and
 // mirrors the mask and the powers; nothing is reordered in memory.
@@ -39,7 +40,8 @@ namespace attnres {
 namespace {
 
 constexpr int kC = kScanChunk;         // tokens per chunk
-constexpr int kTileThreads = 576;      // 8 warps scores and outputs, 8 state, TMA, MMA
+constexpr int kTileThreads = 576;      // the states' kernel: 16 warps of arithmetic, TMA, MMA
+constexpr int kScanThreads = 608;      // the scan: 8 warps scores and outputs, 8 state, TMA, two MMA
 constexpr int kMaxSlots = 8;
 // Dynamic shared memory of sm_103a's 227 KB per CTA beside 2 KB of barriers
 // and tables.  The rings' lengths are constants: a division by a length read
@@ -121,7 +123,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
 // where only bf16 outputs follow from it.
 template <int DA, int DC, int TERMS>
-__global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams p) {
+__global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams p) {
   constexpr int kTile = ScanSmem<DA, DC, TERMS>::kTile, kSlots = ScanSmem<DA, DC, TERMS>::kSlots;
   constexpr int kTiles = 3;                            // tiles per chunk: a, b, c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
@@ -137,14 +139,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&empty[s]), 2);  // two arrivals free a slot: each MMA warp's (c), or one warp's two (a, b)
     }
     mbar_init(smem_addr(&p_full), 1);
     mbar_init(smem_addr(&p_ready), 8);
     mbar_init(smem_addr(&o_full), 1);
     mbar_init(smem_addr(&o_free), 8);
     mbar_init(smem_addr(&s_ready), 8);
-    mbar_init(smem_addr(&b_ready), 8);
+    mbar_init(smem_addr(&b_ready), 16);
     mbar_init(smem_addr(&u_full), 1);
     mbar_init(smem_addr(&u_free), 8);
     mbar_fence_init();
@@ -210,8 +212,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
     __syncwarp();
   } else if (warp == 17) {
     if (lane == 0) {
-      constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC),
-                         kI4 = tc_idesc_bf16(128, DA, true, true);
+      constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC);
       auto slot = [&](int i) { return base + i % kSlots * kTile; };
       auto wait_tile = [&](int i) { wait(&full[i % kSlots], (uint32_t)(i / kSlots)); };
       // scores of chunk n, over those of n - 1 (whose P c is done)
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
       };
       if (nchunk > 0) scores(0);
       for (int n = 0; n < nchunk && ok; ++n) {
-        const int it = n * kTiles, ib = it + 1, ic = it + 2;
+        const int it = n * kTiles, ic = it + 2;
         const uint32_t ph = (uint32_t)n;
         const uint64_t dc = smem_desc_mn128(slot(ic), kPanel);
         wait(&s_ready, ph);
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         for (int kk = 0; kk < DA / 16; ++kk)
           tc_mma_bf16(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
         tc_commit(smem_addr(&empty[it % kSlots]));
+        tc_commit(smem_addr(&empty[it % kSlots]));
         wait_tile(ic);
         // rows behind a short chunk's end are cleared with the weighted rows
         if (chunk_len(n) < kC) wait(&b_ready, ph);
@@ -251,9 +253,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         for (int kk = 0; kk < kC / 16; ++kk)
           tc_mma_bf16_ts(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
         tc_commit(smem_addr(&o_full));
-        // the next scores before this chunk's sums: the warps that turn
-        // them into P weigh b's rows first
+        tc_commit(smem_addr(&empty[ic % kSlots]));
         if (n + 1 < nchunk) scores(n + 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 18) {
+    if (lane == 0) {
+      // a warp of its own: an instruction of 128 columns takes about as long
+      // to issue as to execute, and these products wait for other things
+      constexpr uint32_t kI4 = tc_idesc_bf16(128, DA, true, true);
+      for (int n = 0; n < nchunk && ok; ++n) {
+        const int ib = n * kTiles + 1, ic = ib + 1;
+        const uint32_t ph = (uint32_t)n, b0 = base + ib % kSlots * kTile;
+        const uint64_t dc = smem_desc_mn128(base + ic % kSlots * kTile, kPanel);
+        wait(&full[ic % kSlots], (uint32_t)(ic / kSlots));
         wait(&b_ready, ph);
         wait(&u_free, ph + 1);
         tc_fence_after();
@@ -261,13 +275,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         // whatever lies behind, and are not read)
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
-          const uint64_t dt = smem_desc_mn128(term == 0 ? slot(ib) : rest + (term - 1) * (kC * DA * 2), kPanel);
+          const uint64_t dt = smem_desc_mn128(term == 0 ? b0 : rest + (term - 1) * (kC * DA * 2), kPanel);
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
+        tc_commit(smem_addr(&u_full));
+        tc_commit(smem_addr(&empty[ib % kSlots]));
         tc_commit(smem_addr(&empty[ib % kSlots]));
         tc_commit(smem_addr(&empty[ic % kSlots]));
-        tc_commit(smem_addr(&u_full));
       }
     }
     __syncwarp();
@@ -283,7 +298,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
       // thread t0's vectors of 8 channels lie in rows t0 / 8 + kStep i of each
       // panel, i < kBatch; a panel's are loaded before the first is stored
       const float* fac = pw + p.s.shift + (rev ? 0 : len - 1);
-      constexpr int kStep = 256 / 8, kBatch = kC / kStep;
+      constexpr int kStep = 512 / 8, kBatch = kC / kStep;
       static_assert(kBatch >= 1 && kBatch * kStep == kC, "the batches cover a panel's rows once");
 #pragma unroll 1
       for (int x = 0; x < DA / 64; ++x) {
@@ -319,7 +334,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
           }
         }
       }
-      for (int v = t0 + len * 8; v < kC * 8; v += 256)
+      for (int v = t0 + len * 8; v < kC * 8; v += 512)
         for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kPanel + v * 16, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
@@ -461,8 +476,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) scan_tc_kernel(const __grid_c
         put_done();
       }
       for (int n = 0; n < nchunk; ++n) {
-        const float decay = expf(g * (float)chunk_len(n));
-        warp_wait(&u_full, n);  // and a S before it
+        // this group's half of b's weighted rows
+        const int ib = n * kTiles + 1, len = chunk_len(n);
+        warp_wait(&p_full, n);
+        warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
+        if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
+        split(n, tid);
+        const float decay = expf(g * (float)len);
+        warp_wait(&u_full, n);
+        warp_wait(&o_full, n);  // a S has read the state before
         tc_fence_after();
         const bool next = n + 1 < nchunk;
 #pragma unroll
@@ -817,7 +839,7 @@ cudaError_t launch_scan_tile(const ScanTcParams& p, int64_t segs, const DeviceIn
   const auto kern = scan_tc_kernel<DA, DC, TERMS>;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)kBytes, stream, p);
+  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kScanThreads), (size_t)kBytes, stream, p);
 }
 
 template <int TERMS>
