@@ -61,9 +61,10 @@ constexpr int kHalf = kC / 2;
 template <int DA, int DC>
 struct StateSmem {
   static constexpr int kStage = kHalf * (DA + DC) * 2;
-  static constexpr int kFixed = 4 * kHalf * DA * 2 + 1024;
+  static constexpr int kFixed = 6 * kHalf * DA * 2 + 1024;
   static constexpr int kFit = (kDynSmem - kFixed) / kStage, kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr int kBytes = kFixed + kSlots * kStage;
+  static_assert(kSlots >= 4, "a half's barrier is read before its stage's next use");
 };
 constexpr int kPanel = kC * 128;       // bytes of 64 channels of a tile
 
@@ -529,21 +530,29 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 }
 
 // Every segment's own state, sum_j l^{len-1-j} b_j c_j^T over its tokens, in
-// half chunks of 64 tokens: while the tensor cores take one half, sixteen
-// warps weigh the rows of the next (its terms have a second buffer) and add
-// the last whole chunk's sums, from one of two accumulators in TMEM, to the
-// state (a quarter of a row of DA per thread).  The bound is HBM.
+// half chunks of 64 tokens: while the tensor cores take one half, eight warps
+// weigh the rows of the next and eight others those of the one behind it
+// (each group has its buffer of terms, and its latencies fall into the
+// other's arithmetic), and all sixteen add the last whole chunk's sums, from
+// one of two accumulators in TMEM, to the state (a quarter of a row of DA per
+// thread).  The first two terms lie one
+// behind the other and form one operand of 2 DA columns with sums of their
+// own, to which the third term's are added: two instructions per 16 tokens
+// instead of three, which matters because issuing one takes as long as 128
+// columns take to execute.  One barrier per stage says that a half's products
+// are done: to the loads, to the terms' next writers and to the sums' readers.
+// The bound is HBM.
 constexpr int kHalfPanel = kHalf * 128;  // bytes of 64 channels of a half chunk
 
 template <int DA, int DC>
 __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_constant__ ScanTcParams p) {
   constexpr int kTileB = kHalf * DA * 2, kStage = StateSmem<DA, DC>::kStage, kSlots = StateSmem<DA, DC>::kSlots;
-  constexpr uint32_t kColU = 128;  // columns between the accumulators
+  constexpr uint32_t kColU = 2 * DA;  // columns between the accumulators: first terms' sums, then the others'
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], b_ready[2], t_free[2], u_full[2], u_free[2];
+  __shared__ __align__(8) uint64_t full[kMaxSlots], done[kMaxSlots], b_ready[2], u_free[2];
   __shared__ uint32_t tmem_base;
   __shared__ float pw[kC + 2];  // l^i
-  // stages (b, c), then two buffers of two terms (which an operand of 64
+  // stages (b, c), then two buffers of three terms (which an operand of 64
   // channels reads into behind the last stage: rows of its product not used)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + kSlots * kStage;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -552,17 +561,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_addr(&b_ready[b]), 16);
-      mbar_init(smem_addr(&t_free[b]), 1);
-      mbar_init(smem_addr(&u_full[b]), 1);
+      mbar_init(smem_addr(&b_ready[b]), 8);
       mbar_init(smem_addr(&u_free[b]), 16);
     }
     mbar_fence_init();
   }
-  if (warp == 17) tmem_alloc(smem_addr(&tmem_base), 256);
+  if (warp == 17) tmem_alloc(smem_addr(&tmem_base), 4 * DA);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
       int i = 0;
       for (; i < nhalf; ++i) {
         const int st = i % kSlots, t = chunk_at(i / 2) + i % 2 * kHalf;
-        wait(&empty[st], (uint32_t)(i / kSlots) + 1u);
+        wait(&done[st], (uint32_t)(i / kSlots) + 1u);
         if (!ok) break;
         const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
         mbar_arrive_expect_tx(fb, kStage);
@@ -614,23 +621,21 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     __syncwarp();
   } else if (warp == 17) {
     if (lane == 0) {
-      constexpr uint32_t kI = tc_idesc_bf16(128, DA, true, true);
+      constexpr uint32_t kI2 = tc_idesc_bf16(128, 2 * DA, true, true), kI1 = tc_idesc_bf16(128, DA, true, true);
       for (int i = 0; i < nhalf && ok; ++i) {
         const int st = i % kSlots, n = i / 2;
-        const uint32_t d = tmem + (n & 1) * kColU;
+        const uint32_t d = tmem + (n & 1) * kColU, more = i % 2;
+        const uint64_t dc = smem_desc_mn128(base + st * kStage + kTileB, kHalfPanel);
+        const uint64_t dt = smem_desc_mn128(rest + (i & 1) * 3 * kTileB, kHalfPanel);
         wait(&b_ready[i & 1], (uint32_t)(i / 2));
         if (i % 2 == 0) wait(&u_free[n & 1], (uint32_t)(n / 2) + 1u);
         tc_fence_after();
-        const uint64_t dc = smem_desc_mn128(base + st * kStage + kTileB, kHalfPanel);
 #pragma unroll
-        for (int term = 0; term < 3; ++term) {
-          const uint64_t dt = smem_desc_mn128(term == 0 ? base + st * kStage : rest + ((i & 1) * 2 + term - 1) * kTileB, kHalfPanel);
-#pragma unroll
-          for (int kk = 0; kk < kHalf / 16; ++kk) tc_mma_bf16(d, dc + kk * 128, dt + kk * 128, kI, i % 2 > 0 || term > 0 || kk > 0);
+        for (int kk = 0; kk < kHalf / 16; ++kk) {
+          tc_mma_bf16(d, dc + kk * 128, dt + kk * 128, kI2, kk > 0 ? 1u : more);
+          tc_mma_bf16(d + DA, dc + kk * 128, dt + 2 * kTileB / 16 + kk * 128, kI1, 1u);
         }
-        tc_commit(smem_addr(&empty[st]));
-        tc_commit(smem_addr(&t_free[i & 1]));
-        if (i % 2 == 1 || i == nhalf - 1) tc_commit(smem_addr(&u_full[n & 1]));
+        tc_commit(smem_addr(&done[st]));
       }
     }
     __syncwarp();
@@ -644,60 +649,71 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     for (int d = 0; d < DQ; ++d) S[d] = 0.f;
     auto add = [&](int n) {
       const float decay = expf(g * (float)chunk_len(n));
-      warp_wait(&u_full[n & 1], (uint32_t)(n / 2));
+      const int i = 2 * n + 1 < nhalf ? 2 * n + 1 : nhalf - 1;  // the chunk's last half
+      warp_wait(&done[i % kSlots], (uint32_t)(i / kSlots));
       tc_fence_after();
 #pragma unroll
       for (int d = 0; d < DQ; d += 16) {
-        uint32_t v[16];
+        uint32_t v[16], w[16];
         tmem_ld16(from + (n & 1) * kColU + d, v);
+        tmem_ld16(from + (n & 1) * kColU + DA + d, w);
         tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]));
+        for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]) + __uint_as_float(w[k]));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&u_free[n & 1]));
     };
-    for (int i = 0; i < nhalf; ++i) {
-      const int st = i % kSlots, len = chunk_len(i / 2), j0 = i % 2 * kHalf;  // rows j0 .. of the chunk
-      const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + (i & 1) * 2 * kTileB;
+    const int group = warp >> 3, tg = tid & 255;
+    for (int i = group; i < nhalf; i += 2) {
+      const int st = i % kSlots, len = chunk_len(i / 2), j0 = group * kHalf;  // rows j0 .. of the chunk
+      const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + group * 3 * kTileB;
       warp_wait(&full[st], (uint32_t)(i / kSlots));
-      warp_wait(&t_free[i & 1], (uint32_t)(i / 2) + 1u);
-      // one vector of 8 channels per thread and panel of 64: row tid / 8
-      const int j = j0 + tid / 8;
-      const float f = j < len ? p.s.up_scale * pw[p.s.shift + (rev ? j : len - 1 - j)] : 0.f;
-      uint4 w[DA / 64];
+      if (i >= 2) warp_wait(&done[(i - 2) % kSlots], (uint32_t)((i - 2) / kSlots));  // the terms' last readers
+      // vectors of 8 channels: rows tg / 8 and 32 further of every panel of 64
+      constexpr int kVecs = 2 * DA / 64;
+      float f[2];
+      uint4 w[kVecs];
 #pragma unroll
-      for (int x = 0; x < DA / 64; ++x) {
-        w[x] = ld_shared_v4(B + x * kHalfPanel + tid * 16);
-        if (j >= len) w[x] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+      for (int r = 0; r < 2; ++r) {
+        const int j = j0 + tg / 8 + 32 * r;
+        f[r] = j < len ? p.s.up_scale * pw[p.s.shift + (rev ? j : len - 1 - j)] : 0.f;
+#pragma unroll
+        for (int x = 0; x < DA / 64; ++x) {
+          const int v = r * (DA / 64) + x;
+          w[v] = ld_shared_v4(B + x * kHalfPanel + r * 4096 + tg * 16);
+          if (j >= len) w[v] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+        }
+        if (j >= len) {
+#pragma unroll
+          for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kHalfPanel + r * 4096 + tg * 16, 0, 0, 0, 0);
+        }
       }
 #pragma unroll
-      for (int x = 0; x < DA / 64; ++x) {
-        const uint32_t at = x * kHalfPanel + tid * 16, in[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+      for (int v = 0; v < kVecs; ++v) {
+        const uint32_t at = v % (DA / 64) * kHalfPanel + v / (DA / 64) * 4096 + tg * 16, in[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+        const float fv = f[v / (DA / 64)];
         uint32_t th[4], tm[4], tl[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float a = bf16lo(in[k]) * f, b = bf16hi(in[k]) * f;
+          const float a = bf16lo(in[k]) * fv, b = bf16hi(in[k]) * fv;
           th[k] = pack_bf16x2(a, b);
           const float a1 = a - bf16lo(th[k]), b1 = b - bf16hi(th[k]);
           tm[k] = pack_bf16x2(a1, b1);
           tl[k] = pack_bf16x2(a1 - bf16lo(tm[k]), b1 - bf16hi(tm[k]));
         }
-        st_shared_v4(B + at, th[0], th[1], th[2], th[3]);
-        st_shared_v4(T + at, tm[0], tm[1], tm[2], tm[3]);
-        st_shared_v4(T + kTileB + at, tl[0], tl[1], tl[2], tl[3]);
-      }
-      if (j >= len) {
-#pragma unroll
-        for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kHalfPanel + tid * 16, 0, 0, 0, 0);
+        st_shared_v4(T + at, th[0], th[1], th[2], th[3]);
+        st_shared_v4(T + kTileB + at, tm[0], tm[1], tm[2], tm[3]);
+        st_shared_v4(T + 2 * kTileB + at, tl[0], tl[1], tl[2], tl[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&b_ready[i & 1]));
-      if (i % 2 == 1 && i > 1) add(i / 2 - 1);
+      if (lane == 0) mbar_arrive(smem_addr(&b_ready[group]));
+      if (i > 1) add(i / 2 - 1);
     }
-    if (nchunk > 1 && nhalf % 2 == 1) add(nchunk - 2);
+    // a last chunk of one half left the second group one chunk behind
+    if (group == 1 && nhalf % 2 == 1 && nchunk > 1) add(nchunk - 2);
     if (nchunk > 0) add(nchunk - 1);
     if (work && row < DC) {
       float* to = p.seg_state + ((long long)seg_i * p.s.H + h) * DA * DC;
@@ -717,7 +733,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   __syncthreads();
   if (warp == 17) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 4 * DA);
   }
 }
 
