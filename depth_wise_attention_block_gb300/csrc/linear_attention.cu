@@ -27,11 +27,12 @@ namespace {
 
 constexpr int kSC = 64;        // tokens per chunk
 constexpr int kSThreads = 256;
-constexpr int kSMaxD = 256;
+constexpr int kSMaxD = 256;  // of the step's rows
 constexpr int kSPitchP = kSC + 4;
 
-// The scan on the CUDA cores: a CTA takes a sequence, a head and NG groups of
-// 32 columns of c.  Every product runs from shared memory in register tiles,
+// The scan on the CUDA cores: a CTA takes a segment, a head and NG groups of
+// 32 columns of c (STATE: the segments' own states only, without scores and
+// outputs; the combine kernel then leaves the state before each).  Every product runs from shared memory in register tiles,
 // four rows by 2 NG columns per thread (16 x 16 threads), four steps of its
 // contraction per 16-byte load of the rows, column pairs in packed fp32.
 // Rows lie 16 bytes further apart than their length (no bank conflicts
@@ -96,7 +97,7 @@ __device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A,
   }
 }
 
-template <typename T, int NG>
+template <typename T, int NG, bool STATE>
 __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_constant__ ScanArgs p) {
   extern __shared__ __align__(16) float sm[];
   const int Da = p.Da, Dc = p.Dc, pitch = scan_rows(Da), K = pitch - 4, Dr = (Da + 63) / 64 * 64;
@@ -113,74 +114,80 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
   pdl_trigger();
   const float g = p.log_decay[h];
   if (tid <= kSC) pw[tid] = expf(g * (float)tid);
-  const int n = blockIdx.z;
-  const SeqRange sr = seq_range(p.cu, n, p.T);
-  const long long st = ((long long)n * p.H + h) * Da * Dc;
+  const int seg_i = blockIdx.z;
+  if (p.nsegs && seg_i >= *p.nsegs) return;
+  const Segment sg = segment_of(p, seg_i);
+  if (STATE && (sg.len == 0 || (sg.last && !p.s_out))) return;  // a last segment's own state is part of the final one only
+  const SeqRange sr{sg.first, sg.len};
+  const long long st = ((long long)(p.seg_state ? seg_i : sg.seq) * p.H + h) * Da * Dc;
+  const float* before = STATE ? nullptr : p.seg_state ? p.seg_state : p.s_in;
   for (int i = tid; i < Dr * NC; i += kSThreads) {
     const int da = i / NC, dc = c0 + i % NC;
-    S[i] = p.s_in && da < Da && dc < Dc ? p.s_in[st + p.state_at(da, dc)] : 0.f;
+    S[i] = before && da < Da && dc < Dc ? before[st + p.state_at(da, dc)] : 0.f;
   }
   for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
     const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
     __syncthreads();
-    scan_load<T>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
+    if constexpr (!STATE) scan_load<T>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
     scan_load<T>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
     scan_load<T>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
     __syncthreads();
-    {  // the triangle: rows ty + 16 r, columns tx + 16 s, sums over even and odd channels packed
-      uint64_t acc[4][4];
+    if constexpr (!STATE) {
+      {  // the triangle: rows ty + 16 r, columns tx + 16 s, sums over even and odd channels packed
+        uint64_t acc[4][4];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) acc[r][s] = 0;
-      for (int k = 0; k < K; k += 4) {
-        ulonglong2 x[4], y[4];
+          for (int s = 0; s < 4; ++s) acc[r][s] = 0;
+        for (int k = 0; k < K; k += 4) {
+          ulonglong2 x[4], y[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * r) * pitch + k);
-          y[r] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * r) * pitch + k);
+          for (int r = 0; r < 4; ++r) {
+            x[r] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * r) * pitch + k);
+            y[r] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * r) * pitch + k);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
+          for (int s = 0; s < 4; ++s) {
+            const int i = ty + 16 * r, j = tx + 16 * s;
+            P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
+          }
       }
+      __syncthreads();
+      {
+        uint64_t in[4][NG], from[4][NG];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int i = ty + 16 * r, j = tx + 16 * s;
-          P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
-        }
-    }
-    __syncthreads();
-    {
-      uint64_t in[4][NG], from[4][NG];
+          for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
+        scan_mma<NG>(in, P, kSPitchP, c, (len + 3) / 4 * 4, tx, ty);
+        scan_mma<NG>(from, a, pitch, S, K, tx, ty);
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r) {
+          const int i = ty + 16 * r;
+          if (i < len) {
+            const float coef = pw[i + 1 - p.shift] * p.in_scale;
+            T* out = static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0;
 #pragma unroll
-        for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
-      scan_mma<NG>(in, P, kSPitchP, c, (len + 3) / 4 * 4, tx, ty);
-      scan_mma<NG>(from, a, pitch, S, K, tx, ty);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = ty + 16 * r;
-        if (i < len) {
-          const float coef = pw[i + 1 - p.shift] * p.in_scale;
-          T* out = static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0;
-#pragma unroll
-          for (int s = 0; s < NG; ++s) {
-            float x0, x1, y0, y1;
-            f2_unpack(in[r][s], x0, x1);
-            f2_unpack(from[r][s], y0, y1);
-            const int d = 32 * s + 2 * tx;
-            if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
-            if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
+            for (int s = 0; s < NG; ++s) {
+              float x0, x1, y0, y1;
+              f2_unpack(in[r][s], x0, x1);
+              f2_unpack(from[r][s], y0, y1);
+              const int d = 32 * s + 2 * tx;
+              if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
+              if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
+            }
           }
         }
       }
+      __syncthreads();
     }
-    __syncthreads();
     // the state: rows d0 + 4 ty .. + 3
     const uint64_t decay = f2_pack(pw[len], pw[len]), zero = f2_pack(0.f, 0.f);
     for (int d0 = 0; d0 < Dr; d0 += 64) {
@@ -213,27 +220,55 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
     }
   }
   __syncthreads();
-  if (p.s_out)
+  float* to = STATE ? p.seg_state : p.seg_state ? nullptr : p.s_out;  // segments: the final state is joined with the others
+  if (to)
     for (int i = tid; i < Da * NC; i += kSThreads) {
       const int da = i / NC, dc = c0 + i % NC;
-      if (dc < Dc) p.s_out[st + p.state_at(da, dc)] = S[i];
+      if (dc < Dc) to[st + p.state_at(da, dc)] = S[i];
     }
 }
 
-template <typename T, int NG>
-cudaError_t launch_scan_any(const ScanArgs& s, cudaStream_t stream) {
+template <typename T, int NG, bool STATE>
+cudaError_t launch_scan_any(const ScanArgs& s, int64_t segs, cudaStream_t stream) {
   static SmemOptIn optin;
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
+  const auto kern = scan_any_kernel<T, NG, STATE>;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  e = optin.ensure(reinterpret_cast<const void*>(scan_any_kernel<T, NG>));
-  if (e != cudaSuccess) return e;
-  return launch_kernel(scan_any_kernel<T, NG>, dim3((s.Dc + 32 * NG - 1) / (32 * NG), s.H, s.N), dim3(kSThreads), scan_smem(s.Da, NG), stream,
-                       s);
+  return launch_kernel(kern, dim3((s.Dc + 32 * NG - 1) / (32 * NG), s.H, (unsigned)segs), dim3(kSThreads), scan_smem(s.Da, NG), stream, s);
+}
+
+template <typename T, bool STATE>
+cudaError_t launch_scan_groups(const ScanArgs& s, int ng, int64_t segs, cudaStream_t stream) {
+  switch (ng) {
+    case 1: return launch_scan_any<T, 1, STATE>(s, segs, stream);
+    case 2: return launch_scan_any<T, 2, STATE>(s, segs, stream);
+    case 3: return launch_scan_any<T, 3, STATE>(s, segs, stream);
+    default: return launch_scan_any<T, 4, STATE>(s, segs, stream);
+  }
+}
+
+// Column groups per CTA: as many as the chunk's scores are worth (every CTA
+// of a head forms them again) and two CTAs' shared memory holds, or one's
+// where that is a single group.
+int scan_groups(int Da, int Dc, int smem_max) {
+  int ng = (Dc + 31) / 32;
+  if (ng > 4) ng = (ng + 1) / 2 > 4 ? 4 : (ng + 1) / 2;
+  while (ng > 2 && scan_smem(Da, ng) > smem_max / 2) --ng;
+  while (ng > 1 && scan_smem(Da, ng) > smem_max) --ng;
+  return ng;
+}
+
+// Tokens per segment on the CUDA cores.  At most 65535 segments to a grid.
+int scan_any_segment(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
+  const int ng = scan_groups(Da, Dc, di.max_smem_optin);
+  const int per_sm = 2 * scan_smem(Da, ng) + 2048 <= di.max_smem_optin ? 2 : 1;
+  int seg = seg_tokens(T, N, kSC, (int64_t)H * ((Dc + 32 * ng - 1) / (32 * ng)), per_sm * di.sm_count, 0.4);
+  if (seg > 0 && T / seg + 1 + N > 65535) seg = 0;
+  return seg;
 }
 
 template <typename T>
-cudaError_t launch_scan_type(const ScanArgs& in, cudaStream_t stream) {
+cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t workspace_bytes, bool states_ready, cudaStream_t stream) {
   ScanArgs s = in;
   auto vec = [](const void* p, long long stride, int D) {
     return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0 && stride % 4 == 0 && D % 4 == 0;
@@ -241,26 +276,141 @@ cudaError_t launch_scan_type(const ScanArgs& in, cudaStream_t stream) {
   s.vec_a = vec(s.a, s.as, s.Da);
   s.vec_b = vec(s.b, s.bs, s.Da);
   s.vec_c = vec(s.c, s.cs, s.Dc);
-  // as many columns per CTA as the chunk's scores are worth (every CTA of a
-  // head forms them again) and shared memory holds, but few enough for two
-  // CTAs per SM where that leaves the GPU idle
-  int ng = (s.Dc + 31) / 32;
-  if (ng > 4) ng = (ng + 1) / 2 > 4 ? 4 : (ng + 1) / 2;
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
-  while (ng > 1 && (scan_smem(s.Da, ng) > di.max_smem_optin || (int64_t)s.N * s.H * ((s.Dc + 32 * ng - 1) / (32 * ng)) < di.sm_count)) --ng;
-  switch (ng) {
-    case 1: return launch_scan_any<T, 1>(s, stream);
-    case 2: return launch_scan_any<T, 2>(s, stream);
-    case 3: return launch_scan_any<T, 3>(s, stream);
-    default: return launch_scan_any<T, 4>(s, stream);
+  // one cut for both orders of the two head sizes: the gradients' scans share states
+  s.seg_len = scan_any_segment(s.T, s.H, s.transposed ? s.Dc : s.Da, s.transposed ? s.Da : s.Dc, s.N, di);
+  SegLayout L = seg_layout(s.T, s.H, s.Da, s.Dc, s.N, s.seg_len);
+  if (L.total > workspace_bytes) {  // tensors that the tensor cores would have taken but for their alignment
+    s.seg_len = 0;
+    L = SegLayout{};
+  }
+  const int ng = scan_groups(s.Da, s.Dc, di.max_smem_optin);
+  int64_t segs;
+  seg_place(s, L, workspace, &segs);
+  if (s.seg_len > 0 && !states_ready) {
+    e = launch_seg_plan(s, stream);
+    if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, ng, segs, stream);
+    if (e == cudaSuccess) e = launch_seg_combine(s, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_scan_groups<T, false>(s, ng, segs, stream);
+}
+
+// The segments of a ragged batch, in order: one thread per sequence counts,
+// a prefix sum places them.
+constexpr int kPlanThreads = 1024;
+__global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu, int N, long long T, int seg_len, bool reverse, Segment* segs,
+                                                               int* first_of, int* nsegs) {
+  __shared__ int sums[32];
+  __shared__ int carry;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_wait();
+  pdl_trigger();
+  if (tid == 0) carry = 0;
+  for (int n0 = 0; n0 < N; n0 += kPlanThreads) {
+    const int n = n0 + tid;
+    SeqRange r{0, 0};
+    int cnt = 0;
+    if (n < N) {
+      r = seq_range(cu, n, T);
+      cnt = r.len > seg_len ? (int)((r.len + seg_len - 1) / seg_len) : 1;
+    }
+    int x = cnt;
+    for (int o = 1; o < 32; o *= 2) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+      int y = sums[lane];
+      for (int o = 1; o < 32; o *= 2) {
+        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+      }
+      sums[lane] = y;
+    }
+    __syncthreads();
+    const int at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
+    // offsets that decrease could ask for more segments than there are rows: none past the table
+    const long long cap = (T + seg_len - 1) / seg_len + N;
+    if (n < N) first_of[n] = (int)(at < cap ? at : cap);
+    for (int i = 0; i < cnt && at + i < cap; ++i) segs[at + i] = cut(n, r, i, seg_len, reverse);
+    const int total = sums[31];
+    __syncthreads();
+    if (tid == 0) carry += total;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    const long long cap = (T + seg_len - 1) / seg_len + N;
+    const int total = (int)(carry < cap ? carry : cap);
+    first_of[N] = total;
+    *nsegs = total;
   }
 }
 
-cudaError_t launch_scan(const ScanArgs& s, int dtype, cudaStream_t stream) {
-  return dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, stream) : launch_scan_type<float>(s, stream);
+// Per sequence and head: the state before each segment, from the segments'
+// own states, in place and in order, and the final state.  VEC floats per
+// thread of [H][Da Dc].
+template <int VEC>
+__global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__ ScanArgs p, const int* first_of, int per_head) {
+  const long long e = (blockIdx.x * 256LL + threadIdx.x) * VEC;
+  const int n = blockIdx.y;
+  pdl_wait();
+  pdl_trigger();
+  const long long all = (long long)p.H * per_head;
+  if (e >= all) return;
+  const float g = __ldg(p.log_decay + (int)(e / per_head));
+  const int s0 = first_of ? first_of[n] : 0;
+  const int s1 = first_of ? first_of[n + 1] : (int)((p.T + p.seg_len - 1) / p.seg_len);
+  float w[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) w[k] = p.s_in ? p.s_in[n * all + e + k] : 0.f;
+  // four segments' states are loaded before the first of them is replaced
+  constexpr int kAhead = 4;
+  for (int s = s0; s < s1; s += kAhead) {
+    float u[kAhead][VEC], d[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      d[i] = 1.f;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) u[i][k] = 0.f;
+      if (s + i < s1) {
+        const Segment sg = segment_of(p, s + i);
+        d[i] = expf(g * (float)sg.len);
+        const float* at = p.seg_state + (s + i) * all + e;
+        if (sg.len > 0 && (!sg.last || p.s_out)) {
+          if constexpr (VEC == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at);
+            u[i][0] = x.x, u[i][1] = x.y, u[i][2] = x.z, u[i][3] = x.w;
+          } else {
+            u[i][0] = *at;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (s + i < s1) {
+        float* at = p.seg_state + (s + i) * all + e;
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(at) = make_float4(w[0], w[1], w[2], w[3]);
+        else
+          *at = w[0];
+      }
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) w[k] = fmaf(w[k], d[i], u[i][k]);
+    }
+  }
+  if (p.s_out) {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) p.s_out[n * all + e + k] = w[k];
+  }
 }
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // ------------------------------------------------------------------ step --
 
@@ -402,17 +552,92 @@ ScanArgs scan_args(const LinAttnArgs& a, const void* x, int64_t xs, const void* 
 
 }  // namespace
 
-int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N) {
-  return scan_tc_dims(Dk, Dv, dtype) ? scan_tc_workspace(T, H, Dk, Dv, N) : 0;
+SegLayout seg_layout(int64_t T, int H, int Da, int Dc, int N, int seg_len) {
+  SegLayout L{};
+  if (seg_len == 0) return L;
+  L.segs = round_up(T, seg_len) / seg_len + N;
+  L.table = round_up(L.segs * (int64_t)sizeof(Segment), 256);
+  L.first = round_up((N + 2) * 4, 256);
+  L.states = round_up(L.segs * H * (int64_t)Da * Dc * 4, 256);
+  L.total = L.table + L.first + L.states;
+  return L;
 }
+
+void seg_place(ScanArgs& s, const SegLayout& L, void* workspace, int64_t* segs) {
+  *segs = s.N;
+  if (s.seg_len == 0) return;
+  char* ws = static_cast<char*>(workspace);
+  s.seg_state = reinterpret_cast<float*>(ws + L.table + L.first);
+  *segs = s.cu ? L.segs : round_up(s.T, s.seg_len) / s.seg_len;
+  if (s.cu) {
+    s.segs = reinterpret_cast<Segment*>(ws);
+    s.nsegs = reinterpret_cast<int*>(ws + L.table) + s.N + 1;  // behind the N + 1 first segments
+  }
+}
+
+int seg_tokens(int64_t T, int N, int chunk, int64_t per_seg, int slots, double extra) {
+  const int64_t chunks = round_up(T, chunk) / chunk;
+  const double even = (double)per_seg * (double)(chunks + N) / slots;  // chunks per slot if all were equal
+  double best = (double)(chunks > even ? chunks : even) + 2;
+  int seg = 0;
+  for (int64_t c = 2; c < chunks; c += c < 16 ? 1 : c / 8) {
+    const int64_t ctas = per_seg * (round_up(chunks, c) / c + N - 1);
+    const double cost = (double)((ctas + slots - 1) / slots) * ((double)c + 2) * (1 + extra) + 4;
+    if (cost < best) {
+      best = cost;
+      seg = (int)(c * chunk);
+    }
+  }
+  return seg;
+}
+
+cudaError_t launch_seg_plan(const ScanArgs& s, cudaStream_t stream) {
+  if (!s.segs) return cudaSuccess;
+  int* first_of = const_cast<int*>(s.nsegs) - s.N - 1;
+  return launch_kernel(la_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, s.cu, s.N, s.T, s.seg_len, s.reverse,
+                       const_cast<Segment*>(s.segs), first_of, first_of + s.N + 1);
+}
+
+cudaError_t launch_seg_combine(const ScanArgs& s, cudaStream_t stream) {
+  const int per_head = s.Da * s.Dc;
+  const int* first_of = s.segs ? s.nsegs - s.N - 1 : nullptr;
+  const int64_t all = (int64_t)s.H * per_head;
+  if (per_head % 4 == 0)
+    return launch_kernel(la_combine_kernel<4>, dim3((unsigned)((all / 4 + 255) / 256), s.N), dim3(256), 0, stream, s, first_of, per_head);
+  return launch_kernel(la_combine_kernel<1>, dim3((unsigned)((all + 255) / 256), s.N), dim3(256), 0, stream, s, first_of, per_head);
+}
+
+int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N) {
+  if (scan_tc_dims(Dk, Dv, dtype)) return scan_tc_workspace(T, H, Dk, Dv, N);
+  DeviceInfo di;
+  if (device_info(&di) != cudaSuccess) return -1;
+  return seg_layout(T, H, Dk, Dv, N, scan_any_segment(T, H, Dk, Dv, N, di)).total;
+}
+
+namespace {
+
+cudaError_t launch_scan(const LinAttnArgs& a, const ScanArgs& s, bool tc, bool states_ready) {
+  if (tc) return launch_scan_tc(s, a.workspace, states_ready, a.dev_err, a.stream);
+  return a.dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, a.workspace, a.workspace_bytes, states_ready, a.stream)
+                                 : launch_scan_type<float>(s, a.workspace, a.workspace_bytes, states_ready, a.stream);
+}
+
+// whether long sequences are cut into segments on the CUDA cores
+bool scan_any_segmented(const LinAttnArgs& a) {
+  DeviceInfo di;
+  if (device_info(&di) != cudaSuccess) return false;
+  const int seg = scan_any_segment(a.T, a.H, a.Dk, a.Dv, a.N, di);
+  return seg > 0 && seg_layout(a.T, a.H, a.Dk, a.Dv, a.N, seg).total <= a.workspace_bytes;
+}
+
+}  // namespace
 
 cudaError_t launch_linear_attention(const LinAttnArgs& a) {
   ScanArgs s = scan_args(a, a.q, a.qs, a.k, a.ks, a.Dk, a.v, a.vs, a.Dv, a.out, a.os);
   s.s_in = a.s0;
   s.s_out = a.s1;
   s.p_scale = s.in_scale = a.scale;
-  if (scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(s)) return launch_scan_tc(s, a.workspace, false, a.dev_err, a.stream);
-  return launch_scan(s, a.dtype, a.stream);
+  return launch_scan(a, s, scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(s), false);
 }
 
 cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
@@ -429,26 +654,19 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   k.p_scale = k.up_scale = a.scale;
   ScanArgs v = scan_args(a, a.k, a.ks, a.q, a.qs, a.Dk, a.dout, a.dos, a.Dv, a.dv, rv);
   v.s_in = a.ds1;
-  v.s_out = a.ds0;
   v.reverse = true;
   v.shift = 1;
   v.p_scale = v.up_scale = a.scale;
-  // grad_initial_state may lie over grad_final_state: it is written after
-  // the last read, by dv's scan or where the segments' states are joined
-  if (scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(q) && scan_tc_ok(k) && scan_tc_ok(v)) {
-    if (scan_tc_segmented(a.T, a.H, a.N)) {
-      k.s_out = a.ds0;
-      v.s_out = nullptr;
-    }
-    cudaError_t e = launch_scan_tc(q, a.workspace, false, a.dev_err, a.stream);
-    if (e == cudaSuccess) e = launch_scan_tc(k, a.workspace, false, a.dev_err, a.stream);
-    // the same reversed state, [Dk, Dv] in both
-    if (e == cudaSuccess) e = launch_scan_tc(v, a.workspace, true, a.dev_err, a.stream);
-    return e;
-  }
-  cudaError_t e = launch_scan(q, a.dtype, a.stream);
-  if (e == cudaSuccess) e = launch_scan(k, a.dtype, a.stream);
-  if (e == cudaSuccess) e = launch_scan(v, a.dtype, a.stream);
+  const bool tc = scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(q) && scan_tc_ok(k) && scan_tc_ok(v);
+  // dk and dv carry the same reversed state ([Dk, Dv] in memory for both): in
+  // segments it is formed once.  grad_initial_state may lie over
+  // grad_final_state, so it is written after the last read of that: where
+  // the segments' states are joined, or by dv's scan.
+  const bool cut = tc ? scan_tc_segmented(a.T, a.H, a.N) : scan_any_segmented(a);
+  (cut ? k : v).s_out = a.ds0;
+  cudaError_t e = launch_scan(a, q, tc, false);
+  if (e == cudaSuccess) e = launch_scan(a, k, tc, false);
+  if (e == cudaSuccess) e = launch_scan(a, v, tc, cut);
   return e;
 }
 

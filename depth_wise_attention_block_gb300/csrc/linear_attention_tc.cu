@@ -68,38 +68,12 @@ struct StateSmem {
 };
 constexpr int kPanel = kC * 128;       // bytes of 64 channels of a tile
 
-struct Segment {
-  int seq, first, len, last;  // sequence, first token, tokens, whether the sequence ends with it
-};
-
 struct ScanTcParams {
   CUtensorMap ma, mb, mc;
   ScanArgs s;
-  const Segment* segs;   // null: segment = sequence, or arithmetic over one sequence
-  const int* nsegs;
-  int seg_len;           // tokens per segment (0: a sequence is one segment)
-  float* seg_state;      // [segment][H][..]: STATE writes each segment's own, the scan reads the state before it
   int* dev_err;
   unsigned long long wait_ns;
 };
-
-// segment `i` of a sequence, in the direction of the scan
-__device__ __forceinline__ Segment cut(int n, const SeqRange& r, int i, int seg_len, bool reverse) {
-  Segment g;
-  g.seq = n;
-  const long long i0 = (long long)i * seg_len;
-  const long long len = seg_len > 0 && r.len - i0 > seg_len ? seg_len : r.len - i0;
-  g.len = (int)len;
-  g.first = (int)(reverse ? r.start + r.len - i0 - len : r.start + i0);
-  g.last = i0 + len >= r.len;
-  return g;
-}
-
-__device__ __forceinline__ Segment segment_of(const ScanTcParams& p, int i) {
-  if (p.segs) return p.segs[i];
-  if (p.s.cu) return cut(i, seq_range(p.s.cu, i, p.s.T), 0, 0, p.s.reverse);
-  return cut(0, {0, p.s.T}, i, p.seg_len, p.s.reverse);
-}
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]),
@@ -169,9 +143,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     }
   }
   __syncthreads();
-  const bool live = !p.nsegs || seg_i < *p.nsegs;
+  const bool live = !p.s.nsegs || seg_i < *p.s.nsegs;
   Segment sg{0, 0, 0, 0};
-  if (live) sg = segment_of(p, seg_i);
+  if (live) sg = segment_of(p.s, seg_i);
   const int nchunk = live ? (sg.len + kC - 1) / kC : 0;
   const bool rev = p.s.reverse;
   // chunk n's first token and length (a reversed scan's short chunk is its last)
@@ -440,8 +414,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       constexpr int DH = DA / 2;
       const int d0 = half * DH;
       float S[DH];
-      const long long st = ((long long)(p.seg_state ? seg_i : sg.seq) * p.s.H + h) * DA * DC;
-      const float* from = p.seg_state ? p.seg_state : p.s.s_in;
+      const long long st = ((long long)(p.s.seg_state ? seg_i : sg.seq) * p.s.H + h) * DA * DC;
+      const float* from = p.s.seg_state ? p.s.seg_state : p.s.s_in;
       const bool mine = row < DC && live;
       if (from && mine) {
         if (p.s.transposed) {
@@ -506,7 +480,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         if (next) put_done();
       }
       // the state behind a sequence in one piece (segments: joined before)
-      if (mine && p.s.s_out && !p.seg_state) {
+      if (mine && p.s.s_out && !p.s.seg_state) {
         float* to = p.s.s_out + st;
         const float nan = __int_as_float(0x7fc00000);
         if (p.s.transposed) {
@@ -580,7 +554,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   if (tid < kC + 2) pw[tid] = expf(g * (float)tid);
   __syncthreads();
   Segment sg{0, 0, 0, 1};
-  if (!p.nsegs || seg_i < *p.nsegs) sg = segment_of(p, seg_i);
+  if (!p.s.nsegs || seg_i < *p.s.nsegs) sg = segment_of(p.s, seg_i);
   const bool work = sg.len > 0 && !(sg.last && !p.s.s_out);  // a last segment's own state is part of the final one only
   const int nchunk = work ? (sg.len + kC - 1) / kC : 0;
   const bool rev = p.s.reverse;
@@ -716,7 +690,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     if (group == 1 && nhalf % 2 == 1 && nchunk > 1) add(nchunk - 2);
     if (nchunk > 0) add(nchunk - 1);
     if (work && row < DC) {
-      float* to = p.seg_state + ((long long)seg_i * p.s.H + h) * DA * DC;
+      float* to = p.s.seg_state + ((long long)seg_i * p.s.H + h) * DA * DC;
       const float nan = __int_as_float(0x7fc00000);
       if (p.s.transposed) {
 #pragma unroll
@@ -735,116 +709,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     tc_fence_after();
     tmem_dealloc(tmem, 4 * DA);
   }
-}
-
-// The segments of a ragged batch, in order: one thread per sequence counts,
-// a prefix sum places them.
-constexpr int kPlanThreads = 1024;
-__global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu, int N, long long T, int seg_len, bool reverse, Segment* segs,
-                                                               int* first_of, int* nsegs) {
-  __shared__ int sums[32];
-  __shared__ int carry;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_wait();
-  pdl_trigger();
-  if (tid == 0) carry = 0;
-  for (int n0 = 0; n0 < N; n0 += kPlanThreads) {
-    const int n = n0 + tid;
-    SeqRange r{0, 0};
-    int cnt = 0;
-    if (n < N) {
-      r = seq_range(cu, n, T);
-      cnt = r.len > seg_len ? (int)((r.len + seg_len - 1) / seg_len) : 1;
-    }
-    int x = cnt;
-    for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-      int y = sums[lane];
-      for (int o = 1; o < 32; o *= 2) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) y += z;
-      }
-      sums[lane] = y;
-    }
-    __syncthreads();
-    const int at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
-    // offsets that decrease could ask for more segments than there are rows: none past the table
-    const long long cap = (T + seg_len - 1) / seg_len + N;
-    if (n < N) first_of[n] = (int)(at < cap ? at : cap);
-    for (int i = 0; i < cnt && at + i < cap; ++i) segs[at + i] = cut(n, r, i, seg_len, reverse);
-    const int total = sums[31];
-    __syncthreads();
-    if (tid == 0) carry += total;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    const long long cap = (T + seg_len - 1) / seg_len + N;
-    const int total = (int)(carry < cap ? carry : cap);
-    first_of[N] = total;
-    *nsegs = total;
-  }
-}
-
-// Per sequence and head: the state before each segment, from the segments'
-// own states, in place and in order, and the final state.
-__global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__ ScanTcParams p, const int* first_of, int per_head) {
-  const long long e = (blockIdx.x * 256LL + threadIdx.x) * 4;  // over [H][Da Dc]
-  const int n = blockIdx.y;
-  pdl_wait();
-  pdl_trigger();
-  const long long all = (long long)p.s.H * per_head;
-  if (e >= all) return;
-  const float g = __ldg(p.s.log_decay + (int)(e / per_head));
-  const int s0 = first_of ? first_of[n] : 0;
-  const int s1 = first_of ? first_of[n + 1] : (int)((p.s.T + p.seg_len - 1) / p.seg_len);
-  float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (p.s.s_in) {
-    const float* in = p.s.s_in + n * all + e;
-    w = make_float4(in[0], in[1], in[2], in[3]);
-  }
-  // four segments' states are loaded before the first of them is replaced
-  constexpr int kAhead = 4;
-  for (int s = s0; s < s1; s += kAhead) {
-    float4 u[kAhead];
-    float d[kAhead];
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      d[i] = 1.f;
-      if (s + i < s1) {
-        const Segment sg = segment_of(p, s + i);
-        d[i] = expf(g * (float)sg.len);
-        if (sg.len > 0 && (!sg.last || p.s.s_out)) u[i] = *reinterpret_cast<const float4*>(p.seg_state + (s + i) * all + e);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (s + i < s1) *reinterpret_cast<float4*>(p.seg_state + (s + i) * all + e) = w;
-      w = make_float4(fmaf(w.x, d[i], u[i].x), fmaf(w.y, d[i], u[i].y), fmaf(w.z, d[i], u[i].z), fmaf(w.w, d[i], u[i].w));
-    }
-  }
-  if (p.s.s_out) *reinterpret_cast<float4*>(p.s.s_out + n * all + e) = w;
-}
-
-int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-struct Layout {
-  int64_t segs, table, first, states, total;  // segments at most; bytes
-};
-Layout layout(int64_t T, int H, int Dk, int Dv, int N, int seg_len) {
-  Layout L{};
-  if (seg_len == 0) return L;
-  L.segs = up(T, seg_len) / seg_len + N;
-  L.table = up(L.segs * (int64_t)sizeof(Segment), 256);
-  L.first = up((N + 2) * 4, 256);
-  L.states = up(L.segs * H * (int64_t)Dk * Dv * 4, 256);
-  L.total = L.table + L.first + L.states;
-  return L;
 }
 
 template <int DA, int DC, int TERMS>
@@ -892,26 +756,7 @@ bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_
 
 bool scan_tc_dims(int Dk, int Dv, int dtype) { return dtype == ATTNRES_BF16 && (Dk == 64 || Dk == 128) && (Dv == 64 || Dv == 128); }
 
-// Tokens per segment (0: every sequence in one piece), by a count of chunks:
-// a wave of segments takes their chunks and about two more to start and end;
-// the segments' own states cost half of a scan, and the launches about 4
-// chunks.  The lengths are on the device, so the longest sequence is taken
-// to be all T tokens.
-int scan_tc_segment(int64_t T, int H, int N, int sm_count) {
-  const int64_t chunks = up(T, kC) / kC;
-  const double even = (double)H * (double)(chunks + N) / sm_count;  // chunks per SM if all were equal
-  double best = (double)(chunks > even ? chunks : even) + 2;
-  int seg = 0;
-  for (int64_t c = 2; c < chunks; c += c < 16 ? 1 : c / 8) {
-    const int64_t ctas = H * (up(chunks, c) / c + N - 1);
-    const double cost = (double)((ctas + sm_count - 1) / sm_count) * ((double)c + 2) * 1.5 + 4;
-    if (cost < best) {
-      best = cost;
-      seg = (int)(c * kC);
-    }
-  }
-  return seg;
-}
+static int scan_tc_segment(int64_t T, int H, int N, int sm_count) { return seg_tokens(T, N, kC, H, sm_count, 0.5); }
 
 bool scan_tc_segmented(int64_t T, int H, int N) {
   DeviceInfo di;
@@ -921,7 +766,7 @@ bool scan_tc_segmented(int64_t T, int H, int N) {
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return layout(T, H, Dk, Dv, N, scan_tc_segment(T, H, N, di.sm_count)).total;
+  return seg_layout(T, H, Dk, Dv, N, scan_tc_segment(T, H, N, di.sm_count)).total;
 }
 
 bool scan_tc_ok(const ScanArgs& s) {
@@ -943,37 +788,20 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready
     return cudaErrorInvalidValue;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
-  p.seg_len = scan_tc_segment(s.T, s.H, s.N, di.sm_count);
-  const Layout L = layout(s.T, s.H, s.Da, s.Dc, s.N, p.seg_len);
-  int64_t segs = s.N;
-  if (p.seg_len > 0) {
-    char* ws = static_cast<char*>(workspace);
-    Segment* table = reinterpret_cast<Segment*>(ws);
-    int* first_of = reinterpret_cast<int*>(ws + L.table);  // [N + 1], then the count
-    p.seg_state = reinterpret_cast<float*>(ws + L.table + L.first);
-    segs = s.cu ? L.segs : up(s.T, p.seg_len) / p.seg_len;
-    if (s.cu) {
-      p.segs = table;
-      p.nsegs = first_of + s.N + 1;
-    }
-    if (!states_ready) {
-      if (s.cu) {
-        e = launch_kernel(la_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, s.cu, s.N, s.T, p.seg_len, s.reverse, table, first_of,
-                          first_of + s.N + 1);
-        if (e != cudaSuccess) return e;
-      }
-      ScanTcParams ps = p;
-      if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))
-        return cudaErrorInvalidValue;
-      e = launch_state_dims(ps, segs, di, stream);
-      if (e != cudaSuccess) return e;
-      const int per_head = s.Da * s.Dc;
-      e = launch_kernel(la_combine_kernel, dim3((unsigned)(((int64_t)s.H * per_head / 4 + 255) / 256), s.N), dim3(256), 0, stream, p,
-                        (const int*)(s.cu ? first_of : nullptr), per_head);
-      if (e != cudaSuccess) return e;
-    }
+  p.s.seg_len = scan_tc_segment(s.T, s.H, s.N, di.sm_count);
+  int64_t segs;
+  seg_place(p.s, seg_layout(s.T, s.H, s.Da, s.Dc, s.N, p.s.seg_len), workspace, &segs);
+  if (p.s.seg_len > 0 && !states_ready) {
+    e = launch_seg_plan(p.s, stream);
+    if (e != cudaSuccess) return e;
+    ScanTcParams ps = p;
+    if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))
+      return cudaErrorInvalidValue;
+    e = launch_state_dims(ps, segs, di, stream);
+    if (e == cudaSuccess) e = launch_seg_combine(p.s, stream);
+    if (e != cudaSuccess) return e;
   }
-  return s.s_out && p.seg_len == 0 ? launch_scan_dims<3>(p, segs, di, stream) : launch_scan_dims<2>(p, segs, di, stream);
+  return s.s_out && p.s.seg_len == 0 ? launch_scan_dims<3>(p, segs, di, stream) : launch_scan_dims<2>(p, segs, di, stream);
 }
 
 }  // namespace attnres
