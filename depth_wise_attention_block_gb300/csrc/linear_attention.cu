@@ -26,31 +26,31 @@ namespace attnres {
 namespace {
 
 constexpr int kSC = 64;        // tokens per chunk
-constexpr int kSThreads = 256;
 constexpr int kSMaxD = 256;  // of the step's rows
 constexpr int kSPitchP = kSC + 4;
 
 // The scan on the CUDA cores: a CTA takes a segment, a head and NG groups of
-// 32 columns of c (STATE: the segments' own states only, without scores and
-// outputs; the combine kernel then leaves the state before each).  Every product runs from shared memory in register tiles,
+// 32 columns of c for each of W groups of 256 threads (STATE: the segments'
+// own states only, without scores and outputs; the combine kernel then leaves
+// the state before each).  Every product runs from shared memory in register tiles,
 // four rows by 2 NG columns per thread (16 x 16 threads), four steps of its
 // contraction per 16-byte load of the rows, column pairs in packed fp32.
 // Rows lie 16 bytes further apart than their length (no bank conflicts
 // between a tile's rows).  The bound is the FMA rate, of which shared-memory
 // loads leave about half.
 __host__ __device__ constexpr int scan_rows(int Da) { return (Da + 3) / 4 * 4 + 4; }  // pitch of a and b
-__host__ constexpr int scan_smem(int Da, int NG) {
+__host__ constexpr int scan_smem(int Da, int nc) {  // nc columns of c
   const int d = (Da + 63) / 64 * 64;  // the state's rows, whole tiles
-  return (2 * kSC * scan_rows(Da) + kSC * 32 * NG + kSC * kSPitchP + d * 32 * NG + kSC + 8) * 4;
+  return (2 * kSC * scan_rows(Da) + kSC * nc + kSC * kSPitchP + d * nc + kSC + 8) * 4;
 }
 
 // rows 0 .. kSC - 1 (zero from len on) of `width` channels to dst, columns up to `cols` zero-filled
-template <typename T>
+template <typename T, int THREADS>
 __device__ __forceinline__ void scan_load(float* dst, int pitch, const void* src, long long stride, int off, int width, int cols, int len,
                                           const SeqRange& sr, long long i0, bool reverse, bool vec) {
   const T* p = static_cast<const T*>(src) + off;
   const int q = cols / 4;
-  for (int i = threadIdx.x; i < kSC * q; i += kSThreads) {
+  for (int i = threadIdx.x; i < kSC * q; i += THREADS) {
     const int r = i / q, c = i % q * 4;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r < len) {
@@ -73,8 +73,8 @@ __device__ __forceinline__ void scan_load(float* dst, int pitch, const void* src
   }
 }
 
-// acc[r][s] += sum_k A[ty + 16 r][k] B[k][32 s + 2 tx ..], k < K (a multiple of 4)
-template <int NG>
+// acc[r][s] += sum_k A[ty + 16 r][k] B[k][32 s + 2 tx ..], k < K (a multiple of 4), rows of B NC long
+template <int NG, int NC>
 __device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A, int pitch, const float* B, int K, int tx, int ty) {
 #pragma unroll 2
   for (int k = 0; k < K; k += 4) {
@@ -85,7 +85,7 @@ __device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A,
     for (int e = 0; e < 4; ++e) {
       uint64_t b[NG];
 #pragma unroll
-      for (int s = 0; s < NG; ++s) b[s] = *reinterpret_cast<const uint64_t*>(B + (k + e) * 32 * NG + 32 * s + 2 * tx);
+      for (int s = 0; s < NG; ++s) b[s] = *reinterpret_cast<const uint64_t*>(B + (k + e) * NC + 32 * s + 2 * tx);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float x = e == 0 ? a[r].x : e == 1 ? a[r].y : e == 2 ? a[r].z : a[r].w;
@@ -97,18 +97,19 @@ __device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A,
   }
 }
 
-template <typename T, int NG, bool STATE>
-__global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_constant__ ScanArgs p) {
+template <typename T, int NG, int W, bool STATE>
+__global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant__ ScanArgs p) {
   extern __shared__ __align__(16) float sm[];
   const int Da = p.Da, Dc = p.Dc, pitch = scan_rows(Da), K = pitch - 4, Dr = (Da + 63) / 64 * 64;
-  constexpr int NC = 32 * NG;
+  constexpr int NC = 32 * NG * W, kThreads = 256 * W;
   float* a = sm;                        // [kSC][pitch]
   float* b = a + kSC * pitch;           // [kSC][pitch]
   float* c = b + kSC * pitch;           // [kSC][NC]
   float* P = c + kSC * NC;              // [kSC][kSPitchP]
   float* S = P + kSC * kSPitchP;        // [Dr][NC]
   float* pw = S + Dr * NC;              // l^0 .. l^kSC
-  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16 % 16, group = tid / 256;
+  const int own = group * 32 * NG;  // the group's first column
   const int c0 = blockIdx.x * NC, h = blockIdx.y, wc = Dc - c0 < NC ? Dc - c0 : NC;
   pdl_wait();
   pdl_trigger();
@@ -121,41 +122,43 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
   const SeqRange sr{sg.first, sg.len};
   const long long st = ((long long)(p.seg_state ? seg_i : sg.seq) * p.H + h) * Da * Dc;
   const float* before = STATE ? nullptr : p.seg_state ? p.seg_state : p.s_in;
-  for (int i = tid; i < Dr * NC; i += kSThreads) {
+  for (int i = tid; i < Dr * NC; i += kThreads) {
     const int da = i / NC, dc = c0 + i % NC;
     S[i] = before && da < Da && dc < Dc ? before[st + p.state_at(da, dc)] : 0.f;
   }
   for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
     const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
     __syncthreads();
-    if constexpr (!STATE) scan_load<T>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
-    scan_load<T>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
-    scan_load<T>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
+    if constexpr (!STATE) scan_load<T, kThreads>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
+    scan_load<T, kThreads>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
+    scan_load<T, kThreads>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
     __syncthreads();
     if constexpr (!STATE) {
-      {  // the triangle: rows ty + 16 r, columns tx + 16 s, sums over even and odd channels packed
-        uint64_t acc[4][4];
+      {  // the triangle: rows ty + 16 r of the group's, columns tx + 16 s, sums over even and odd channels packed
+        constexpr int R = 4 / W;
+        const float* ag = a + group * 16 * R * pitch;
+        uint64_t acc[R][4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int s = 0; s < 4; ++s) acc[r][s] = 0;
+#pragma unroll 2
         for (int k = 0; k < K; k += 4) {
-          ulonglong2 x[4], y[4];
+          ulonglong2 x[R], y[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            x[r] = *reinterpret_cast<const ulonglong2*>(a + (ty + 16 * r) * pitch + k);
-            y[r] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * r) * pitch + k);
-          }
+          for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const ulonglong2*>(ag + (ty + 16 * r) * pitch + k);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
+          for (int s = 0; s < 4; ++s) y[s] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * s) * pitch + k);
+#pragma unroll
+          for (int r = 0; r < R; ++r)
 #pragma unroll
             for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const int i = ty + 16 * r, j = tx + 16 * s;
+            const int i = group * 16 * R + ty + 16 * r, j = tx + 16 * s;
             P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
           }
       }
@@ -166,8 +169,8 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
         for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
-        scan_mma<NG>(in, P, kSPitchP, c, (len + 3) / 4 * 4, tx, ty);
-        scan_mma<NG>(from, a, pitch, S, K, tx, ty);
+        scan_mma<NG, NC>(in, P, kSPitchP, c + own, (len + 3) / 4 * 4, tx, ty);
+        scan_mma<NG, NC>(from, a, pitch, S + own, K, tx, ty);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = ty + 16 * r;
@@ -179,7 +182,7 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
               float x0, x1, y0, y1;
               f2_unpack(in[r][s], x0, x1);
               f2_unpack(from[r][s], y0, y1);
-              const int d = 32 * s + 2 * tx;
+              const int d = own + 32 * s + 2 * tx;
               if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
               if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
             }
@@ -205,7 +208,7 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
         const uint64_t w[4] = {f2_pack(x.x * f, x.x * f), f2_pack(x.y * f, x.y * f), f2_pack(x.z * f, x.z * f), f2_pack(x.w * f, x.w * f)};
 #pragma unroll
         for (int s = 0; s < NG; ++s) {
-          const uint64_t y = *reinterpret_cast<const uint64_t*>(c + j * NC + 32 * s + 2 * tx);
+          const uint64_t y = *reinterpret_cast<const uint64_t*>(c + j * NC + own + 32 * s + 2 * tx);
 #pragma unroll
           for (int r = 0; r < 4; ++r) u[r][s] = f2_fma(w[r], y, u[r][s]);
         }
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
       for (int r = 0; r < 4; ++r)
 #pragma unroll
         for (int s = 0; s < NG; ++s) {
-          uint64_t* at = reinterpret_cast<uint64_t*>(S + (d + r) * NC + 32 * s + 2 * tx);
+          uint64_t* at = reinterpret_cast<uint64_t*>(S + (d + r) * NC + own + 32 * s + 2 * tx);
           *at = f2_fma(*at, decay, u[r][s]);
         }
     }
@@ -222,47 +225,46 @@ __global__ void __launch_bounds__(kSThreads) scan_any_kernel(const __grid_consta
   __syncthreads();
   float* to = STATE ? p.seg_state : p.seg_state ? nullptr : p.s_out;  // segments: the final state is joined with the others
   if (to)
-    for (int i = tid; i < Da * NC; i += kSThreads) {
+    for (int i = tid; i < Da * NC; i += kThreads) {
       const int da = i / NC, dc = c0 + i % NC;
       if (dc < Dc) to[st + p.state_at(da, dc)] = S[i];
     }
 }
 
-template <typename T, int NG, bool STATE>
+// Columns per CTA: all of them (every CTA of a head forms the chunk's scores
+// again) up to 128, in one group of 32, 64 or 96, or two of 64; fewer where
+// shared memory does not hold them.
+int scan_columns(int Da, int Dc, int smem_max) {
+  int nc = Dc > 96 ? 128 : (Dc + 31) / 32 * 32;
+  while (nc > 32 && scan_smem(Da, nc) > smem_max) nc -= 32;
+  return nc;
+}
+
+template <typename T, int NG, int W, bool STATE>
 cudaError_t launch_scan_any(const ScanArgs& s, int64_t segs, cudaStream_t stream) {
   static SmemOptIn optin;
-  const auto kern = scan_any_kernel<T, NG, STATE>;
+  constexpr int nc = 32 * NG * W;
+  const auto kern = scan_any_kernel<T, NG, W, STATE>;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((s.Dc + 32 * NG - 1) / (32 * NG), s.H, (unsigned)segs), dim3(kSThreads), scan_smem(s.Da, NG), stream, s);
+  return launch_kernel(kern, dim3((s.Dc + nc - 1) / nc, s.H, (unsigned)segs), dim3(256 * W), scan_smem(s.Da, nc), stream, s);
 }
 
 template <typename T, bool STATE>
-cudaError_t launch_scan_groups(const ScanArgs& s, int ng, int64_t segs, cudaStream_t stream) {
-  switch (ng) {
-    case 1: return launch_scan_any<T, 1, STATE>(s, segs, stream);
-    case 2: return launch_scan_any<T, 2, STATE>(s, segs, stream);
-    case 3: return launch_scan_any<T, 3, STATE>(s, segs, stream);
-    default: return launch_scan_any<T, 4, STATE>(s, segs, stream);
+cudaError_t launch_scan_groups(const ScanArgs& s, int nc, int64_t segs, cudaStream_t stream) {
+  switch (nc) {
+    case 32: return launch_scan_any<T, 1, 1, STATE>(s, segs, stream);
+    case 64: return launch_scan_any<T, 2, 1, STATE>(s, segs, stream);
+    case 96: return launch_scan_any<T, 3, 1, STATE>(s, segs, stream);
+    default: return launch_scan_any<T, 2, 2, STATE>(s, segs, stream);
   }
-}
-
-// Column groups per CTA: as many as the chunk's scores are worth (every CTA
-// of a head forms them again) and two CTAs' shared memory holds, or one's
-// where that is a single group.
-int scan_groups(int Da, int Dc, int smem_max) {
-  int ng = (Dc + 31) / 32;
-  if (ng > 4) ng = (ng + 1) / 2 > 4 ? 4 : (ng + 1) / 2;
-  while (ng > 2 && scan_smem(Da, ng) > smem_max / 2) --ng;
-  while (ng > 1 && scan_smem(Da, ng) > smem_max) --ng;
-  return ng;
 }
 
 // Tokens per segment on the CUDA cores.  At most 65535 segments to a grid.
 int scan_any_segment(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
-  const int ng = scan_groups(Da, Dc, di.max_smem_optin);
-  const int per_sm = 2 * scan_smem(Da, ng) + 2048 <= di.max_smem_optin ? 2 : 1;
-  int seg = seg_tokens(T, N, kSC, (int64_t)H * ((Dc + 32 * ng - 1) / (32 * ng)), per_sm * di.sm_count, 0.4);
+  const int nc = scan_columns(Da, Dc, di.max_smem_optin);
+  const int per_sm = 2 * scan_smem(Da, nc) + 2048 <= di.max_smem_optin ? 2 : 1;
+  int seg = seg_tokens(T, N, kSC, (int64_t)H * ((Dc + nc - 1) / nc), per_sm * di.sm_count, 0.4);
   if (seg > 0 && T / seg + 1 + N > 65535) seg = 0;
   return seg;
 }
@@ -286,16 +288,16 @@ cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t worksp
     s.seg_len = 0;
     L = SegLayout{};
   }
-  const int ng = scan_groups(s.Da, s.Dc, di.max_smem_optin);
+  const int nc = scan_columns(s.Da, s.Dc, di.max_smem_optin);
   int64_t segs;
   seg_place(s, L, workspace, &segs);
   if (s.seg_len > 0 && !states_ready) {
     e = launch_seg_plan(s, stream);
-    if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, ng, segs, stream);
+    if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, nc, segs, stream);
     if (e == cudaSuccess) e = launch_seg_combine(s, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_scan_groups<T, false>(s, ng, segs, stream);
+  return launch_scan_groups<T, false>(s, nc, segs, stream);
 }
 
 // The segments of a ragged batch, in order: one thread per sequence counts,
