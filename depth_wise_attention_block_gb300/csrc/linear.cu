@@ -243,11 +243,12 @@ cudaError_t linear_backward_any(const LinearBwdArgs& a) {
   return cudaSuccess;
 }
 
-// fp32 products below this many multiply-adds stay on the CUDA cores: the
-// tensor cores need one more launch, which splits the operands.
+// Short fp32 products below this many multiply-adds stay on the CUDA cores:
+// the tensor cores need one more launch, which splits the operands (about 9 us
+// together), a stage of 16 steps here about 1.2 us (100 x 100 x 100: 11 us).
 constexpr int64_t kSmallFp32 = int64_t(1) << 24;
 
-bool small_fp32(int64_t M, int N, int K, int dtype) { return dtype == ATTNRES_F32 && M * N < kSmallFp32 / K; }
+bool small_fp32(int64_t M, int N, int K, int dtype) { return dtype == ATTNRES_F32 && K <= 96 && M * N < kSmallFp32 / K; }
 
 // Takes the next `bytes` of the workspace, or null where they do not fit.
 struct Arena {
@@ -266,24 +267,25 @@ struct Arena {
 cudaError_t linear_tc(const LinearArgs& a, bool* done) {
   const bool bf16 = a.dtype == ATTNRES_BF16;
   const int np = bf16 ? 1 : 3;
+  *done = false;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const TcPlan plan = tc_plan(a.M, a.N, a.K, np, di.sm_count);
   TcOperand op[2] = {{a.x, a.ldx, a.M, a.K, false, nullptr}, {a.w, a.K, a.N, a.K, false, nullptr}};
   Arena ws{static_cast<char*>(a.workspace), a.workspace_bytes};
   TcOperand prep[2];
   int nprep = 0;
-  *done = false;
   for (TcOperand& o : op) {
-    if (bf16 && tc_rows_ok(o.ptr, o.ld)) continue;
+    if ((bf16 && tc_rows_ok(o.ptr, o.ld)) || (plan.fused && &o == &op[1])) continue;
     o.prep = ws.take(tc_prep_bytes(o.rows, o.cols, np));
     if (!o.prep) return cudaSuccess;
     prep[nprep++] = o;
   }
   *done = true;
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
-  if (e == cudaSuccess && nprep) e = launch_tc_prep(prep, nprep, np, a.stream);
+  if (nprep) e = launch_tc_prep(prep, nprep, np, a.stream);
   if (e != cudaSuccess) return e;
-  return launch_tc_gemm(tc_plan(a.M, a.N, a.K, np, di.sm_count), op[0], op[1], a.M, a.N, a.K, np, kEpiForward,
-                        forward_epilogue(a), a.dev_err, a.stream);
+  return launch_tc_gemm(plan, op[0], op[1], a.M, a.N, a.K, np, kEpiForward, forward_epilogue(a), a.dev_err, a.stream);
 }
 
 cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
@@ -295,10 +297,18 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
   float* part = static_cast<float*>(ws.take(L.part));
   TcOperand x{a.x, a.ldx, a.M, a.K, false, nullptr}, w{a.w, a.K, a.N, a.K, false, nullptr};
   TcOperand dz{act ? dz_buf : a.grad_out, act ? dz_pitch(a.N) : a.ldg, a.M, a.N, false, nullptr};
-  const bool use_x = act || a.grad_w, use_w = act || a.grad_x, use_dz = a.grad_x || a.grad_w;
+  *done = false;
+  DeviceInfo di;
+  cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  const TcPlan plan_z = tc_plan(a.M, a.N, a.K, np, di.sm_count), plan_x = tc_plan(a.M, a.K, a.N, np, di.sm_count);
+  TcPlan plan_w = tc_plan(a.N, a.K, a.M, np, di.sm_count);
+  // (dw's second operand is x, whose terms the first product needs anyway)
+  if (plan_w.fused) plan_w = tc_plan_unfused(plan_w);
+  const bool use_x = act || a.grad_w, use_dz = a.grad_x || a.grad_w;
+  const bool use_w = (act && !plan_z.fused) || (a.grad_x && !plan_x.fused);
   TcOperand prep[3];
   int nprep = 0;
-  *done = false;
   for (TcOperand* o : {&x, &w, &dz}) {
     if (!(o == &x ? use_x : o == &w ? use_w : use_dz) || (bf16 && tc_rows_ok(o->ptr, o->ld))) continue;
     o->prep = ws.take(tc_prep_bytes(o->rows, o->cols, np));
@@ -306,8 +316,6 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
     if (o != &dz || !act) prep[nprep++] = *o;  // dz's copy comes after dz
   }
   *done = true;
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
   for (int i = 0; i < nprep && e == cudaSuccess; i += 2) e = launch_tc_prep(prep + i, nprep - i < 2 ? 1 : 2, np, a.stream);
   if (e != cudaSuccess) return e;
   int part_rows = 0;
@@ -320,9 +328,8 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
     epi.ldo = dz_pitch(a.N);
     epi.act = a.act;
     epi.part = a.grad_bias ? part : nullptr;
-    const TcPlan plan = tc_plan(a.M, a.N, a.K, np, di.sm_count);
-    part_rows = plan.part_rows;
-    e = launch_tc_gemm(plan, x, w, a.M, a.N, a.K, np, kEpiDz, epi, a.dev_err, a.stream);
+    part_rows = plan_z.part_rows;
+    e = launch_tc_gemm(plan_z, x, w, a.M, a.N, a.K, np, kEpiDz, epi, a.dev_err, a.stream);
     if (e == cudaSuccess && dz.prep) e = launch_tc_prep(&dz, 1, np, a.stream);
   } else if (a.grad_bias) {
     part_rows = (int)((a.M + kGT - 1) / kGT);
@@ -335,7 +342,7 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
     epi.ldo = a.K;
     TcOperand wt = w;
     wt.mn = true;
-    e = launch_tc_gemm(tc_plan(a.M, a.K, a.N, np, di.sm_count), dz, wt, a.M, a.K, a.N, np, kEpiForward, epi, a.dev_err, a.stream);
+    e = launch_tc_gemm(plan_x, dz, wt, a.M, a.K, a.N, np, kEpiForward, epi, a.dev_err, a.stream);
   }
   if (e == cudaSuccess && a.grad_w) {
     LinearEpilogue epi{};
@@ -343,7 +350,7 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
     epi.ldo = a.K;
     TcOperand zt = dz, xt = x;
     zt.mn = xt.mn = true;
-    e = launch_tc_gemm(tc_plan(a.N, a.K, a.M, np, di.sm_count), zt, xt, a.N, a.K, a.M, np, kEpiForward, epi, a.dev_err, a.stream);
+    e = launch_tc_gemm(plan_w, zt, xt, a.N, a.K, a.M, np, kEpiForward, epi, a.dev_err, a.stream);
   }
   return e;
 }
@@ -376,7 +383,8 @@ cudaError_t launch_linear_backward(const LinearBwdArgs& a) {
     if (e == cudaSuccess && a.grad_bias) e = cudaMemsetAsync(a.grad_bias, 0, (size_t)a.N * 4, a.stream);
     return e;
   }
-  if (!small_fp32(a.M, a.N, a.K, a.dtype)) {
+  // its products run over each of the three sizes
+  if (!small_fp32(a.M, a.N, a.K, a.dtype) || a.M > 96 || a.N > 96) {
     bool done;
     const cudaError_t e = linear_backward_tc(a, &done);
     if (done || e != cudaSuccess) return e;

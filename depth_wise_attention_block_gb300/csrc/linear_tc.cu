@@ -30,7 +30,16 @@
 // matter (hi mid, mid hi, mid mid, hi lo, lo hi) to a second one 2^-8
 // smaller; both are drained into fp32 registers every kDrain blocks, so that
 // the tensor cores' truncating accumulation never runs over more than 256
-// steps of the contraction.
+// steps of the contraction.  Up to 64 columns, the terms of B lie one behind
+// the other as one operand and a term of A meets all it needs of them in one
+// instruction (three instead of six: issuing one takes about as long as 128
+// columns take to execute), each order of magnitude in columns of its own.
+// Operands are split by a kernel of their own
+// (prep_kernel) but for the wide operand of a narrow product of up to 128
+// rows: there the eight epilogue warps read it in fp32, two blocks ahead in
+// registers, and write the terms where TMA would (FUSED), since reading the
+// weights once is the bound (64 x 7168 x 7168: 191 us with the terms made in
+// memory first).
 #include <math.h>
 
 #include "attnres.h"
@@ -63,7 +72,12 @@ struct TcParams {
   int ksplit, stages;
   uint32_t stage_bytes, plane_a, plane_b;  // bytes of a stage, of one plane of A and of B
   uint32_t tmem_cols, acc_cols;            // allocated columns, columns of one accumulator buffer
-  uint32_t idesc;
+  uint32_t idesc, idesc2, idesc3;          // of one, two and three times bn columns (stacked)
+  bool stacked;
+  const float* raw;      // FUSED: the lanes' operand in fp32, row stride raw_ld
+  long long raw_ld;
+  int depth;             // steps of the contraction
+  bool raw_vec;
   LinearEpilogue epi;
   int* dev_err;
   unsigned long long wait_ns;
@@ -247,11 +261,61 @@ __device__ __forceinline__ float ld_shared_cluster(uint32_t addr) {
   return v;
 }
 
-template <int NP, int MODE, bool SWAP>
+// FUSED: thread t's four vectors of 8 fp32 values of a block of 128 lanes x 64
+// steps, K-major (lane t / 8 + 32 i, steps 8 (t mod 8) ..) or MN-major (step
+// t / 16 + 16 i, lanes 8 (t mod 16) ..), zero outside the matrix.
+__device__ __forceinline__ void fused_load(const TcParams& p, float (&v)[4][8], int l0, int kb, int t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = p.a_mn ? kb * kKB + t / 16 + 16 * i : l0 + t / 8 + 32 * i;
+    const int col = p.a_mn ? l0 + t % 16 * 8 : kb * kKB + t % 8 * 8;
+    const int rows = p.a_mn ? p.depth : p.lanes, cols = p.a_mn ? p.lanes : p.depth;
+    const float* at = p.raw + (long long)row * p.raw_ld + col;
+    if (row < rows && col + 8 <= cols && p.raw_vec) {
+      const float4 a = __ldcs(reinterpret_cast<const float4*>(at)), b = __ldcs(reinterpret_cast<const float4*>(at) + 1);
+      v[i][0] = a.x, v[i][1] = a.y, v[i][2] = a.z, v[i][3] = a.w;
+      v[i][4] = b.x, v[i][5] = b.y, v[i][6] = b.z, v[i][7] = b.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] = row < rows && col + e < cols ? __ldcs(at + e) : 0.f;
+    }
+  }
+}
+
+// Three bf16 terms of two values: the first cut (a finite value stays finite),
+// the others rounded, 2^-25 of the value left behind; the subtractions are
+// exact.
+__device__ __forceinline__ void three_terms(float x, float y, uint32_t (&w)[3]) {
+  w[0] = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+  x -= bf16lo(w[0]);
+  y -= bf16hi(w[0]);
+  w[1] = pack_bf16x2(x, y);
+  w[2] = pack_bf16x2(x - bf16lo(w[1]), y - bf16hi(w[1]));
+}
+
+// Those values' three terms into a stage's planes, in the 128-byte swizzle.
+__device__ __forceinline__ void fused_store(const TcParams& p, const float (&v)[4][8], uint32_t stage, int t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = p.a_mn ? t / 16 + 16 * i : t / 8 + 32 * i, chunk = t % 8;
+    const uint32_t at = stage + (p.a_mn ? t % 16 / 8 * 8192 : 0) + row * 128 + ((chunk ^ (row & 7)) << 4);
+    uint32_t w[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) three_terms(v[i][2 * e], v[i][2 * e + 1], w[e]);
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + pl * p.plane_a), "r"(w[0][pl]), "r"(w[1][pl]), "r"(w[2][pl]), "r"(w[3][pl])
+                   : "memory");
+  }
+}
+
+// FUSED: 0, or the lanes' operand in fp32 and tiles of up to 64 (1) or 128 (2)
+// columns, whose sums the epilogue warps hold beside the values on their way.
+template <int NP, int MODE, bool SWAP, int FUSED>
 __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant__ TcParams p) {
   using T = typename std::conditional<NP == 3, float, bf16_t>::type;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], split[FUSED ? kMaxStages : 1], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -265,6 +329,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 1);
+      if (FUSED) mbar_init(smem_addr(&split[s]), kEpiWarps);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&acc_full[b]), 1);
@@ -295,10 +360,10 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             break;
           }
           const uint32_t fb = smem_addr(&full[st]), a = base + st * p.stage_bytes, b = a + NP * p.plane_a;
-          mbar_arrive_expect_tx(fb, NP * (kLanes * 128 + brows * 128));
+          mbar_arrive_expect_tx(fb, NP * ((FUSED ? 0 : kLanes * 128) + brows * 128));
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) {
-            load_plane(a + pl * p.plane_a, &p.ma, p.a_mn, l0, kLanes, kb, pl, fb);
+            if (!FUSED) load_plane(a + pl * p.plane_a, &p.ma, p.a_mn, l0, kLanes, kb, pl, fb);
             load_plane(b + pl * p.plane_b, &p.mb, p.b_mn, c0, brows, kb, pl, fb);
           }
           r.next(p.stages);
@@ -330,7 +395,8 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
           const uint32_t d = tmem + buf * p.acc_cols, d1 = d + p.acc_cols / 2;
           uint32_t acc = 0;
           for (; kb < end; ++kb) {
-            if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns)) {
+            if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns) ||
+                (FUSED && !mbar_wait_bounded(smem_addr(&split[r.st]), r.lap, p.wait_ns))) {
               report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
               ok = false;
               break;
@@ -338,18 +404,29 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             tc_fence_after();
             const uint32_t at = r.st * (p.stage_bytes / 16);
             const uint64_t da = da0 + at, db = db0 + at;
+            if (NP == 3 && p.stacked) {
 #pragma unroll
-            for (int kk = 0; kk < kKB / 16; ++kk) {
-              const uint64_t a = da + kk * sa, b = db + kk * sb;
-              tc_mma_bf16(d, a, b, p.idesc, acc);
-              if constexpr (NP == 3) {
-                tc_mma_bf16(d1, a, b + 2 * pb, p.idesc, acc);
-                tc_mma_bf16(d1, a + 2 * pa, b, p.idesc, 1u);
-                tc_mma_bf16(d1, a + pa, b + pb, p.idesc, 1u);
-                tc_mma_bf16(d1, a, b + pb, p.idesc, 1u);
-                tc_mma_bf16(d1, a + pa, b, p.idesc, 1u);
+              for (int kk = 0; kk < kKB / 16; ++kk) {
+                const uint64_t a = da + kk * sa, b = db + kk * sb;
+                tc_mma_bf16(d, a, b, p.idesc3, acc);                    // hi (hi, mid, lo)
+                tc_mma_bf16(d + p.bn, a + pa, b, p.idesc2, 1u);         // mid (hi, mid)
+                tc_mma_bf16(d + 2 * p.bn, a + 2 * pa, b, p.idesc, 1u);  // lo hi
+                acc = 1;
               }
-              acc = 1;
+            } else {
+#pragma unroll
+              for (int kk = 0; kk < kKB / 16; ++kk) {
+                const uint64_t a = da + kk * sa, b = db + kk * sb;
+                tc_mma_bf16(d, a, b, p.idesc, acc);
+                if constexpr (NP == 3) {
+                  tc_mma_bf16(d1, a, b + 2 * pb, p.idesc, acc);
+                  tc_mma_bf16(d1, a + 2 * pa, b, p.idesc, 1u);
+                  tc_mma_bf16(d1, a + pa, b + pb, p.idesc, 1u);
+                  tc_mma_bf16(d1, a, b + pb, p.idesc, 1u);
+                  tc_mma_bf16(d1, a + pa, b, p.idesc, 1u);
+                }
+                acc = 1;
+              }
             }
             tc_commit(smem_addr(&empty[r.st]));
             r.next(p.stages);
@@ -365,7 +442,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
     const int nchunk = (p.bn + 15) / 16;
-    constexpr int kRegChunks = NP == 3 ? 4 : 1;  // NP = 3: bn <= 128
+    constexpr int kRegChunks = FUSED == 1 ? 2 : NP == 3 ? 4 : 1;  // NP = 3: bn <= 128
     const RowEpilogue<T, MODE> epi(p);
     const float nan = __int_as_float(0x7fc00000);
     bool ok = true;
@@ -382,7 +459,8 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
       }
       Raw16<T> res[2];
       if constexpr (!SWAP && NP == 1) epi.ahead(res[0], m, c0 + half * 16);
-      for (int kb = kb0; kb < kb1; kb += group, ++g) {
+      // one drain of an accumulator: into registers (NP = 3), or on its way out
+      auto drain = [&] {
         const int buf = g & 1;
         if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
           if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
@@ -397,10 +475,19 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
             if (ch < nchunk) {
               uint32_t v[16], w[16];
               tmem_ld16(at + ch * 16, v);
-              tmem_ld16(at + p.acc_cols / 2 + ch * 16, w);
+              tmem_ld16(at + (p.stacked ? p.bn : p.acc_cols / 2) + ch * 16, w);
               tmem_ld_wait();
+              float small[16];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) acc[c][i] += __uint_as_float(v[i]) + __uint_as_float(w[i]);
+              for (int i = 0; i < 16; ++i) small[i] = __uint_as_float(w[i]);
+              if (p.stacked) {
+                tmem_ld16(at + 2 * p.bn + ch * 16, w);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) small[i] += __uint_as_float(w[i]);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[c][i] += __uint_as_float(v[i]) + small[i];
             }
           }
         } else {
@@ -426,6 +513,38 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&acc_empty[buf]));
+        ++g;
+      };
+      if constexpr (FUSED) {
+        // split block after block, two of them on their way in registers; a
+        // group's sums are drained once the next group's terms are written
+        const int t = tid - 64;
+        float raw[2][4][8];
+        fused_load(p, raw[0], l0, kb0, t);
+        fused_load(p, raw[1], l0, kb0 + 1, t);
+        RingPos r;
+        for (int kb = kb0; kb < kb1; kb += 2) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int k = kb + u;
+            if (k < kb1) {
+              if (ok && !__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&empty[r.st]), r.lap ^ 1u, p.wait_ns))) {
+                if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+                ok = false;
+              }
+              fused_store(p, raw[u], base + r.st * p.stage_bytes, t);
+              if (k + 2 < kb1) fused_load(p, raw[u], l0, k + 2, t);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&split[r.st]));
+              r.next(p.stages);
+              if ((k - kb0) % kDrain == kDrain - 1 && k - kb0 >= kDrain) drain();
+            }
+          }
+        }
+        while (g * kDrain < kb1 - kb0) drain();
+      } else {
+        for (int kb = kb0; kb < kb1; kb += group) drain();
       }
       if constexpr (NP == 3) {
 #pragma unroll
@@ -695,8 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
 // ----------------------------------------------------------- operands ------
 
 // Copies of operands TMA cannot take as they are: rows on 16-byte boundaries
-// (bf16), or the three bf16 terms of fp32 values (hi = round(v), mid =
-// round(v - hi), lo = round(v - hi - mid); the subtractions are exact).
+// (bf16), or the three bf16 terms of fp32 values.
 struct PrepJob {
   const void* src;
   long long ld, rows;
@@ -707,13 +825,6 @@ struct PrepJob {
 struct PrepParams {
   PrepJob job[2];
 };
-
-__device__ __forceinline__ uint32_t bf16_near(float v) {
-  uint32_t b = f32_to_bf16_bits(v);
-  // a finite value that would round to infinity is cut instead
-  if ((b & 0x7fffu) == 0x7f80u && isfinite(v)) b = __float_as_uint(v) >> 16;
-  return b;
-}
 
 template <int NP>
 __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ PrepParams p) {
@@ -731,14 +842,10 @@ __global__ void __launch_bounds__(256) prep_kernel(const __grid_constant__ PrepP
         dst[c / 2] = lo | hi << 16;
       } else {
         const float* s = static_cast<const float*>(j.src) + r * j.ld + c;
-        float a = c < j.cols ? s[0] : 0.f, b = c + 1 < j.cols ? s[1] : 0.f;
+        uint32_t w[3];
+        three_terms(c < j.cols ? s[0] : 0.f, c + 1 < j.cols ? s[1] : 0.f, w);
 #pragma unroll
-        for (int pl = 0; pl < 3; ++pl) {
-          const uint32_t x = bf16_near(a), y = bf16_near(b);
-          dst[(pl * plane + c) / 2] = x | y << 16;
-          a -= bf16_bits_to_f32(x);
-          b -= bf16_bits_to_f32(y);
-        }
+        for (int pl = 0; pl < 3; ++pl) dst[(pl * plane + c) / 2] = w[pl];
       }
     }
   }
@@ -755,53 +862,56 @@ bool operand_map(CUtensorMap* map, const void* ptr, int64_t outer, int64_t inner
   return make_tensor_map(map, ptr, 3, dims, strides, box);
 }
 
-template <int NP, int MODE>
-cudaError_t launch_mode(const TcParams& p, bool swap, int grid, int smem, int smem_max, cudaStream_t stream) {
-  if (!swap) {
-    static SmemOptIn optin;
-    const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_gemm_kernel<NP, MODE, false>), smem_max);
-    return e != cudaSuccess ? e : launch_kernel(tc_gemm_kernel<NP, MODE, false>, dim3(grid), dim3(kThreads), smem, stream, p);
-  }
-  static SmemOptIn optin;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_gemm_kernel<NP, MODE, true>), smem_max);
-  if (e != cudaSuccess) return e;
+// A kernel's launch attributes: clusters of `cluster` CTAs (0: none), and
+// programmatic dependent launch.
+template <typename K>
+cudaError_t launch_tc(K kern, const TcParams& p, int grid, int cluster, int smem, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = p.ksplit;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  int n = 0;
+  if (cluster > 0) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = cluster;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
+  if (pdl_enabled()) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tc_gemm_kernel<NP, MODE, true>, p);
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int NP, int MODE, bool SWAP, int FUSED>
+cudaError_t launch_gemm(const TcParams& p, int grid, int smem, int smem_max, cudaStream_t stream) {
+  static SmemOptIn optin;
+  const auto kern = tc_gemm_kernel<NP, MODE, SWAP, FUSED>;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), smem_max);
+  return e != cudaSuccess ? e : launch_tc(kern, p, grid, SWAP ? p.ksplit : 0, smem, stream);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const TcParams& p, int np, bool swap, bool fused, int grid, int smem, int smem_max, cudaStream_t stream) {
+  if (np == 1)
+    return swap ? launch_gemm<1, MODE, true, 0>(p, grid, smem, smem_max, stream)
+                : launch_gemm<1, MODE, false, 0>(p, grid, smem, smem_max, stream);
+  if (fused)
+    return p.bn <= 64 ? launch_gemm<3, MODE, true, 1>(p, grid, smem, smem_max, stream) : launch_gemm<3, MODE, true, 2>(p, grid, smem, smem_max, stream);
+  return swap ? launch_gemm<3, MODE, true, 0>(p, grid, smem, smem_max, stream)
+              : launch_gemm<3, MODE, false, 0>(p, grid, smem, smem_max, stream);
 }
 
 template <int MODE>
 cudaError_t launch_pair(const TcParams& p, int grid, int smem, int smem_max, cudaStream_t stream) {
   static SmemOptIn optin;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(tc_pair_kernel<MODE>), smem_max);
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, tc_pair_kernel<MODE>, p);
+  return e != cudaSuccess ? e : launch_tc(tc_pair_kernel<MODE>, p, grid, 2, smem, stream);
 }
 
 }  // namespace
@@ -811,44 +921,68 @@ bool tc_rows_ok(const void* ptr, int64_t ld) { return (reinterpret_cast<uintptr_
 int64_t tc_prep_bytes(int64_t rows, int64_t cols, int np) { return np * up(rows * up(cols, 8) * 2, 256); }
 
 TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
+  // fp32: making the terms in memory reads 4 bytes and writes 6 per value
+  const double prep = np == 3 ? (double)(M + N) * K * 10 / 6000 : 0;
   TcPlan best{};
   const int64_t kblocks = up(K, kKB) / kKB;
   const int bn_max = np == 3 ? 128 : 256;
   double cost = 1e300;
-  // whole waves of tiles, in cycles: an instruction of a single tile of 256
-  // columns takes about 250 (L2), of 128 or fewer about 130; of a pair's tile
-  // about 150; then the start and end of a tile's pipeline
+  // All in nanoseconds.  Whole waves of tiles: an instruction of a single
+  // tile of 256 columns takes about 130 (L2), of 128 or fewer about 68, of a
+  // pair's tile 70; then the start and end of a tile's pipeline.
+  constexpr double kTileNs = 800, kLaunchNs = 800;
   for (int bn = 64; bn <= bn_max; bn *= 2) {
     const int64_t tiles = up(M, kLanes) / kLanes * (up(N, bn) / bn);
-    const double tile = (double)kblocks * (np == 3 ? 24 * 130 : 4 * (bn == 256 ? 250 : 130)) + 1500;
-    const double c = (double)((tiles + sm_count - 1) / sm_count) * tile + 1500;
+    const double tile = (double)kblocks * (np == 3 ? (bn <= 64 ? 16 : 24) * 68 : 4 * (bn == 256 ? 130 : 68)) + kTileNs;
+    const double c = (double)((tiles + sm_count - 1) / sm_count) * tile + kLaunchNs + prep;
     if (c < cost) {
       cost = c;
-      best = {TcPlan::kWide, bn, 1, 0};
+      best = {TcPlan::kWide, bn, 1, 0, false};
     }
   }
   if (np == 1) {
     const int64_t tiles = up(M, 2 * kLanes) / (2 * kLanes) * (up(N, kPairN) / kPairN);
-    const double c = (double)((tiles + sm_count / 2 - 1) / (sm_count / 2)) * ((double)kblocks * 4 * 150 + 1500) + 2500;
+    const double c = (double)((tiles + sm_count / 2 - 1) / (sm_count / 2)) * ((double)kblocks * 4 * 70 + kTileNs) + kLaunchNs + 500;
     if (c < cost) {
       cost = c;
-      best = {TcPlan::kPairs, kPairN, 1, 0};
+      best = {TcPlan::kPairs, kPairN, 1, 0, false};
     }
   }
   // narrow: M's rows as columns, N's as lanes, the contraction over a
-  // cluster; the CTAs' streams share HBM (about 24 bytes per cycle and SM)
+  // cluster.  The CTAs of a wave share HBM (6.5 bytes per ps); alone one gets
+  // about 40 bytes per ns with the 96 KB it keeps in flight (two per SM), 80
+  // with the 192 KB of fp32's terms; starting, joining and ending a wave takes
+  // about 5500.  64 x 21504 x 7168, clusters of 1, 2, 3, 5, 7: 59, 75, 62, 65,
+  // 75 us; 64 x 7168 x 7168, clusters of 2, 3, 4, 5, 8: 29, 25, 23, 22, 29 us.
   if (M <= 1024) {
     const int bn = M >= 128 ? 128 : (int)up(M, 16);
-    const int slots = sm_count * (np == 3 ? 1 : 2);
+    const int64_t slots = (int64_t)sm_count * (np == 3 ? 1 : 2);
     for (int ks = 1; ks <= kMaxKsplit && ks <= kblocks; ++ks) {
       const int64_t tiles = up(N, kLanes) / kLanes * (up(M, bn) / bn);
-      const int64_t ctas = tiles * ks;
-      const int64_t waves = (ctas + slots - 1) / slots;
-      const double block = np == 3 ? 24.0 * 64 + 600 : (kLanes + bn) * 128.0 / (24.0 / 2);
-      const double c = (double)waves * ((double)((kblocks + ks - 1) / ks) * block + 2500) + 1500;
+      const int64_t ctas = tiles * ks, blocks = (kblocks + ks - 1) / ks;
+      const double mma = (double)blocks * (np == 1 ? 4 : bn <= 64 ? 12 : 24) * 68;
+      // bytes of the lanes' operand per CTA (fused: fp32, else np terms), and
+      // the bytes per ns that a CTA alone gets
+      auto price = [&](double bytes, double rate) {
+        const double alone = (bytes + (double)blocks * np * bn * 128) / rate;
+        auto wave = [&](int64_t n) {
+          const double share = (double)n * bytes / 6500;
+          const double t = share > alone ? share : alone;
+          return (t > mma ? t : mma) + 5500;
+        };
+        return (double)(ctas / slots) * wave(slots) + (ctas % slots ? wave(ctas % slots) : 0);
+      };
+      const double c = price((double)blocks * np * kLanes * 128, np == 3 ? 80 : 40) + prep;
       if (c < cost) {
         cost = c;
-        best = {TcPlan::kNarrow, bn, ks, 0};
+        best = {TcPlan::kNarrow, bn, ks, 0, false};
+      }
+      if (np == 3 && M <= 128) {
+        const double f = price((double)blocks * kLanes * 256, 40) + (double)M * K * 10 / 6000;
+        if (f < cost) {
+          cost = f;
+          best = {TcPlan::kNarrow, bn, ks, 0, true};
+        }
       }
     }
   }
@@ -884,7 +1018,13 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
     const int64_t ld = o.prep ? up(o.cols, 8) : o.ld;
     return operand_map(m, ptr, o.rows, o.cols, ld, np, o.mn, box);
   };
-  if (!map(&p.ma, lo, kLanes) || !map(&p.mb, co, pairs ? kLanes : plan.bn)) return cudaErrorInvalidValue;
+  if ((!plan.fused && !map(&p.ma, lo, kLanes)) || !map(&p.mb, co, pairs ? kLanes : plan.bn)) return cudaErrorInvalidValue;
+  if (plan.fused) {
+    p.raw = static_cast<const float*>(lo.ptr);
+    p.raw_ld = lo.ld;
+    p.raw_vec = (reinterpret_cast<uintptr_t>(lo.ptr) & 15) == 0 && lo.ld % 4 == 0;
+  }
+  p.depth = (int)K;
   p.a_mn = lo.mn;
   p.b_mn = co.mn;
   p.lanes = swap ? N : (int)M;
@@ -898,12 +1038,17 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
   p.plane_a = kLanes * 128;
   p.plane_b = (uint32_t)((p.b_mn ? up(p.bn, 64) : up(p.bn, 8)) * 128);
   p.stage_bytes = np * (p.plane_a + p.plane_b);
-  const int nacc = np == 3 ? 2 : 1;
+  p.stacked = np == 3 && !p.b_mn && p.bn <= 64;
+  const int nacc = p.stacked ? 3 : np == 3 ? 2 : 1;
   const int nbuf = swap && np == 1 ? 1 : 2;
   p.acc_cols = nacc * (uint32_t)p.bn;
   p.tmem_cols = 32;
   while (p.tmem_cols < nbuf * p.acc_cols) p.tmem_cols *= 2;
   p.idesc = tc_idesc_bf16(kLanes, p.bn, p.a_mn, p.b_mn);
+  if (p.stacked) {
+    p.idesc2 = tc_idesc_bf16(kLanes, 2 * p.bn, p.a_mn, p.b_mn);
+    p.idesc3 = tc_idesc_bf16(kLanes, 3 * p.bn, p.a_mn, p.b_mn);
+  }
   p.epi = epi;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
@@ -928,11 +1073,8 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
     return mode == kEpiDz ? launch_pair<kEpiDz>(p, grid, smem, smem_max, stream) : launch_pair<kEpiForward>(p, grid, smem, smem_max, stream);
   }
   const int64_t grid = swap ? tiles * p.ksplit : (tiles < di.sm_count ? tiles : di.sm_count);
-  if (np == 3)
-    return mode == kEpiDz ? launch_mode<3, kEpiDz>(p, swap, (int)grid, smem, smem_max, stream)
-                          : launch_mode<3, kEpiForward>(p, swap, (int)grid, smem, smem_max, stream);
-  return mode == kEpiDz ? launch_mode<1, kEpiDz>(p, swap, (int)grid, smem, smem_max, stream)
-                        : launch_mode<1, kEpiForward>(p, swap, (int)grid, smem, smem_max, stream);
+  return mode == kEpiDz ? launch_mode<kEpiDz>(p, np, swap, plan.fused, (int)grid, smem, smem_max, stream)
+                        : launch_mode<kEpiForward>(p, np, swap, plan.fused, (int)grid, smem, smem_max, stream);
 }
 
 }  // namespace attnres

@@ -26,9 +26,14 @@ struct TcPlan {
   int bn;         // columns of a tile
   int ksplit;     // CTAs of a cluster that share a tile's contraction
   int part_rows;  // partial rows of the column sums (kEpiDz)
+  bool fused;     // fp32, narrow: B enters as it is, its terms are made on the way
 };
 // np: 1 (bf16) or 3 (fp32, three bf16 terms)
 TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count);
+inline TcPlan tc_plan_unfused(TcPlan p) {
+  p.fused = false;
+  return p;
+}
 bool tc_rows_ok(const void* ptr, int64_t ld);                     // bf16 rows TMA takes as they are
 int64_t tc_prep_bytes(int64_t rows, int64_t cols, int np);
 cudaError_t launch_tc_prep(const TcOperand* ops, int n, int np, cudaStream_t stream);  // n <= 2
