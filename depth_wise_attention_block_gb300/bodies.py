@@ -53,6 +53,9 @@ class LinearAttentionBody:
     sequences (None: one).  Decoding (decode=True): row b is the next token of
     the sequence in slot slots[b] ([T] int32; None: slot b).  Rows outside
     every sequence or slot give v = b_out.
+
+    The body's buffers and workspace belong to one forward at a time: two
+    stacks, or two captured graphs of one, that run at once need a body each.
     """
 
     def __init__(self, layers: Sequence[LinearAttentionWeights], T: int, heads: int, Dk: int, Dv: int,

@@ -12,6 +12,7 @@ using namespace attnres;
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 42;  // element offsets stay far inside int64
+constexpr int kMaxWidth = 1 << 30;               // of a projection: tiles past its end stay inside int
 
 // `rows` rows of `width` bytes, `pitch` bytes apart
 struct Rows {
@@ -50,7 +51,8 @@ int check_linear_sizes(int64_t M, int N, int K, int dtype, int act) {
   if (!valid_dtype(dtype)) return fail(ATTNRES_EDTYPE, "dtype %d", dtype);
   if (M < 0 || N < 1 || K < 1) return fail(ATTNRES_EINVAL, "M=%lld N=%d K=%d", (long long)M, N, K);
   if (M > INT32_MAX) return fail(ATTNRES_ERANGE, "M=%lld", (long long)M);
-  if (M > kMaxElems / N || M > kMaxElems / K) return fail(ATTNRES_ERANGE, "M*N or M*K too large");
+  if (N > kMaxWidth || K > kMaxWidth) return fail(ATTNRES_ERANGE, "N=%d K=%d", N, K);
+  if (M > kMaxElems / N || M > kMaxElems / K || N > kMaxElems / K) return fail(ATTNRES_ERANGE, "M*N, M*K or N*K too large");
   if (act < ATTNRES_ACT_NONE || act > ATTNRES_ACT_SILU) return fail(ATTNRES_EINVAL, "activation %d", act);
   return ATTNRES_OK;
 }
@@ -331,8 +333,8 @@ int attnres_qk_norm_rope_backward(const void* q, int64_t q_stride, int Hq, const
     }
   }
   QkArgs a{};
-  a.h[0] = {q, q_stride, grad_q_out, gqo_stride, grad_q, gq_stride, q_gain, Hq > 0 ? grad_q_gain : nullptr, Hq};
-  a.h[1] = {k, k_stride, grad_k_out, gko_stride, grad_k, gk_stride, k_gain, Hk > 0 ? grad_k_gain : nullptr, Hk};
+  a.h[0] = {q, q_stride, grad_q_out, gqo_stride, grad_q, gq_stride, q_gain, grad_q_gain, Hq};
+  a.h[1] = {k, k_stride, grad_k_out, gko_stride, grad_k, gk_stride, k_gain, grad_k_gain, Hk};
   a.T = T;
   a.D = D;
   a.dtype = dtype;
@@ -391,6 +393,7 @@ int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int
     rc = check_apart(in, 6, outs, 3, in_place);
     if (rc != ATTNRES_OK) return rc;
   }
+  if (workspace && !aligned(workspace, 256)) return fail(ATTNRES_EINVAL, "workspace is not 256-byte aligned");
   const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (need < 0) return fail(ATTNRES_ECUDA, "device query");
   rc = check_workspace(workspace, workspace_bytes, need);
@@ -416,7 +419,7 @@ int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int
   a.out = out;
   a.os = out_stride;
   a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
+  a.workspace_bytes = workspace ? workspace_bytes : 0;
   a.dev_err = dev_err;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_linear_attention(a);
@@ -458,6 +461,7 @@ int attnres_linear_attention_backward(const void* q, int64_t q_stride, const voi
     rc = check_apart(in, 8, outs, 5, in_place);
     if (rc != ATTNRES_OK) return rc;
   }
+  if (workspace && !aligned(workspace, 256)) return fail(ATTNRES_EINVAL, "workspace is not 256-byte aligned");
   const int64_t need = linear_attention_workspace_bytes(T, H, Dk, Dv, dtype, num_seqs);
   if (need < 0) return fail(ATTNRES_ECUDA, "device query");
   rc = check_workspace(workspace, workspace_bytes, need);
@@ -487,7 +491,7 @@ int attnres_linear_attention_backward(const void* q, int64_t q_stride, const voi
   a.dv = grad_v;
   a.ds0 = grad_initial_state;
   a.workspace = workspace;
-  a.workspace_bytes = workspace_bytes;
+  a.workspace_bytes = workspace ? workspace_bytes : 0;
   a.dev_err = dev_err;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_linear_attention_backward(a);

@@ -97,6 +97,18 @@ __device__ __forceinline__ void scan_mma(uint64_t (&acc)[4][NG], const float* A,
   }
 }
 
+// Row i of P c in two columns over the rows that the mask leaves alone: where
+// the product, in which a masked row counts as 0 times its values, met an
+// infinity or a NaN.
+__device__ __noinline__ uint64_t masked_pair(const float* P, const float* c, int pitch, int i) {
+  float x = 0.f, y = 0.f;
+  for (int j = 0; j <= i; ++j) {
+    x = fmaf(P[j], c[j * pitch], x);
+    y = fmaf(P[j], c[j * pitch + 1], y);
+  }
+  return f2_pack(x, y);
+}
+
 template <typename T, int NG, int W, bool STATE>
 __global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant__ ScanArgs p) {
   extern __shared__ __align__(16) float sm[];
@@ -114,7 +126,7 @@ __global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant
   pdl_wait();
   pdl_trigger();
   const float g = p.log_decay[h];
-  if (tid <= kSC) pw[tid] = expf(g * (float)tid);
+  if (tid <= kSC) pw[tid] = decay_pow(g, tid);
   const int seg_i = blockIdx.z;
   if (p.nsegs && seg_i >= *p.nsegs) return;
   const Segment sg = segment_of(p, seg_i);
@@ -171,6 +183,17 @@ __global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant
           for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
         scan_mma<NG, NC>(in, P, kSPitchP, c + own, (len + 3) / 4 * 4, tx, ty);
         scan_mma<NG, NC>(from, a, pitch, S + own, K, tx, ty);
+        uint64_t sum = 0;  // 0, or NaN where a value is not finite
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < NG; ++s) sum = f2_fma(in[r][s], 0ull, sum);
+        if (f2_hsum(sum) != 0.f) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int s = 0; s < NG; ++s) in[r][s] = masked_pair(P + (ty + 16 * r) * kSPitchP, c + own + 32 * s + 2 * tx, NC, ty + 16 * r);
+        }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = ty + 16 * r;
@@ -305,8 +328,8 @@ cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t worksp
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu, int N, long long T, int seg_len, bool reverse, Segment* segs,
                                                                int* first_of, int* nsegs) {
-  __shared__ int sums[32];
-  __shared__ int carry;
+  // 64 bits: offsets that decrease can ask for any number of segments
+  __shared__ long long sums[32], carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_wait();
   pdl_trigger();
@@ -319,28 +342,28 @@ __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu
       r = seq_range(cu, n, T);
       cnt = r.len > seg_len ? (int)((r.len + seg_len - 1) / seg_len) : 1;
     }
-    int x = cnt;
+    long long x = cnt;
     for (int o = 1; o < 32; o *= 2) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     if (warp == 0) {
-      int y = sums[lane];
+      long long y = sums[lane];
       for (int o = 1; o < 32; o *= 2) {
-        const int z = __shfl_up_sync(0xffffffffu, y, o);
+        const long long z = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) y += z;
       }
       sums[lane] = y;
     }
     __syncthreads();
-    const int at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
-    // offsets that decrease could ask for more segments than there are rows: none past the table
+    const long long at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
+    // none past the table, whatever the offsets
     const long long cap = (T + seg_len - 1) / seg_len + N;
     if (n < N) first_of[n] = (int)(at < cap ? at : cap);
     for (int i = 0; i < cnt && at + i < cap; ++i) segs[at + i] = cut(n, r, i, seg_len, reverse);
-    const int total = sums[31];
+    const long long total = sums[31];
     __syncthreads();
     if (tid == 0) carry += total;
     __syncthreads();
@@ -381,7 +404,7 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
       for (int k = 0; k < VEC; ++k) u[i][k] = 0.f;
       if (s + i < s1) {
         const Segment sg = segment_of(p, s + i);
-        d[i] = expf(g * (float)sg.len);
+        d[i] = decay_pow(g, sg.len);
         const float* at = p.seg_state + (s + i) * all + e;
         if (sg.len > 0 && (!sg.last || p.s_out)) {
           if constexpr (VEC == 4) {

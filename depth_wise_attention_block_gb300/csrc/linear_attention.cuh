@@ -21,6 +21,9 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int n, long lon
   return {s, e - s};
 }
 
+// l^n = exp(n log_decay), and l^0 = 1 for a decay that leaves nothing (-inf) too
+__device__ __forceinline__ float decay_pow(float log_decay, int n) { return n == 0 ? 1.f : expf(log_decay * (float)n); }
+
 struct Segment {
   int seq, first, len, last;  // sequence, first token, tokens, whether the sequence ends with it
 };

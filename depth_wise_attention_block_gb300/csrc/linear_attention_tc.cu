@@ -95,6 +95,38 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// The outputs of one row from the tensors in memory, over the rows that the
+// mask leaves alone, channels c0 .. c1 - 1: where the products, in which a
+// masked row counts as 0 times its values, met an infinity or a NaN.  o2: the
+// row's a S in TMEM, which a whole warp reads; `bad`: this lane's row is
+// redone; l: p_scale l^distance.
+template <int DA>
+__device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint32_t o2, long long t0, int h, int row, int len, int c0, int c1,
+                                        float coef, bool bad) {
+  for (; c0 < c1; c0 += 16) {
+    uint32_t y[16];
+    tmem_ld16(o2 + c0, y);
+    tmem_ld_wait();
+    if (!bad) continue;
+    const bf16_t* a = static_cast<const bf16_t*>(s.a) + (t0 + row) * s.as + (long long)h * DA;
+    float x[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = coef * __uint_as_float(y[k]);
+    for (int j = s.reverse ? row : 0; j < (s.reverse ? len : row + 1); ++j) {
+      const bf16_t* b = static_cast<const bf16_t*>(s.b) + (t0 + j) * s.bs + (long long)h * DA;
+      const bf16_t* c = static_cast<const bf16_t*>(s.c) + (t0 + j) * s.cs + (long long)h * s.Dc + c0;
+      float dot = 0.f;
+      for (int d = 0; d < DA; ++d) dot = fmaf(load_elem(a + d), load_elem(b + d), dot);
+      const float f = bf16lo(pack_bf16x2(dot * l[s.reverse ? j - row : row - j], 0.f));
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = fmaf(f, load_elem(c + k), x[k]);
+    }
+    bf16_t* out = static_cast<bf16_t*>(s.out) + (t0 + row) * s.os + (long long)h * s.Dc + c0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) store_elem(out + k, x[k]);
+  }
+}
+
 // TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
 // where only bf16 outputs follow from it.
 template <int DA, int DC, int TERMS>
@@ -135,7 +167,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   pdl_trigger();
   const float g = __ldg(p.s.log_decay + h);
   if (tid < kC + 2) {
-    const float l = expf(g * (float)tid);
+    const float l = decay_pow(g, tid);
     pw[tid] = l;
     if (tid < kC) {
       tab[tid] = 0.f;
@@ -380,6 +412,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
         const float coef = in ? p.s.in_scale * pw[e] : 0.f;
         bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(n) + row) * p.s.os + (long long)h * DC;
+        uint64_t sum = 0;  // 0, or NaN where a value is not finite
 #pragma unroll 1
         for (int c0 = half * (DC / 2); c0 < (half + 1) * (DC / 2); c0 += 32) {
           uint32_t x[32], y[32];
@@ -388,6 +421,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           tmem_ld16(lanes_at + kColO1 + c0 + 16, x + 16);
           tmem_ld16(lanes_at + kColO2 + c0 + 16, y + 16);
           tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) sum = f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), 0ull, sum);
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k)
@@ -405,6 +440,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             }
           }
         }
+        const bool bad = in && ok && f2_hsum(sum) != 0.f;
+        if (__any_sync(0xffffffffu, bad))
+          masked_row<DA>(p.s, tab + kC, lanes_at + kColO2, chunk_at(n), h, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_addr(&o_free));
@@ -551,7 +589,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   pdl_wait();
   pdl_trigger();
   const float g = __ldg(p.s.log_decay + h);
-  if (tid < kC + 2) pw[tid] = expf(g * (float)tid);
+  if (tid < kC + 2) pw[tid] = decay_pow(g, tid);
   __syncthreads();
   Segment sg{0, 0, 0, 1};
   if (!p.s.nsegs || seg_i < *p.s.nsegs) sg = segment_of(p.s, seg_i);

@@ -34,12 +34,11 @@
 // the other as one operand and a term of A meets all it needs of them in one
 // instruction (three instead of six: issuing one takes about as long as 128
 // columns take to execute), each order of magnitude in columns of its own.
-// Operands are split by a kernel of their own
-// (prep_kernel) but for the wide operand of a narrow product of up to 128
-// rows: there the eight epilogue warps read it in fp32, two blocks ahead in
-// registers, and write the terms where TMA would (FUSED), since reading the
-// weights once is the bound (64 x 7168 x 7168: 191 us with the terms made in
-// memory first).
+// Operands are split by a kernel of their own (prep_kernel) but for the wide
+// operand of a narrow product of up to 128 rows: there the eight epilogue
+// warps read it in fp32, two blocks ahead in registers, and write the terms
+// where TMA would (FUSED), since reading the weights once is the bound
+// (64 x 7168 x 7168: 101 us, with the terms made in memory first 191).
 #include <math.h>
 
 #include "attnres.h"
@@ -857,7 +856,8 @@ int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 // step] (K-major) or ptr[step ld + row] (MN-major), `np` planes apart.
 bool operand_map(CUtensorMap* map, const void* ptr, int64_t outer, int64_t inner, int64_t ld, int np, bool mn, int box_rows) {
   const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)np};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(outer * ld * 2)};
+  if (outer == 1) ld = up(inner, 8);  // a stride that no address depends on
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)((np == 1 ? 1 : outer) * ld * 2)};
   const cuuint32_t box[3] = {64, (cuuint32_t)(mn ? kKB : box_rows), 1};
   return make_tensor_map(map, ptr, 3, dims, strides, box);
 }
@@ -902,7 +902,8 @@ cudaError_t launch_mode(const TcParams& p, int np, bool swap, bool fused, int gr
     return swap ? launch_gemm<1, MODE, true, 0>(p, grid, smem, smem_max, stream)
                 : launch_gemm<1, MODE, false, 0>(p, grid, smem, smem_max, stream);
   if (fused)
-    return p.bn <= 64 ? launch_gemm<3, MODE, true, 1>(p, grid, smem, smem_max, stream) : launch_gemm<3, MODE, true, 2>(p, grid, smem, smem_max, stream);
+    return p.bn <= 64 ? launch_gemm<3, MODE, true, 1>(p, grid, smem, smem_max, stream)
+                      : launch_gemm<3, MODE, true, 2>(p, grid, smem, smem_max, stream);
   return swap ? launch_gemm<3, MODE, true, 0>(p, grid, smem, smem_max, stream)
               : launch_gemm<3, MODE, false, 0>(p, grid, smem, smem_max, stream);
 }

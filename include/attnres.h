@@ -514,7 +514,8 @@ typedef enum {
  * residual  device [M, N] of dtype, row stride ldr, or NULL; it may be out
  *           itself (with ldr = ldo)
  * out       device [M, N] of dtype, row stride ldo
- * M >= 0 (0 launches nothing and accepts NULL buffers), N, K >= 1
+ * M >= 0 (0 launches nothing and accepts NULL buffers), N, K 1..2^30
+ *           (ATTNRES_ERANGE above)
  * act       one of attnres_activation
  * workspace NULL, or device scratch of workspace_bytes, 256-byte aligned,
  *           sharing no memory with an operand (its contents on entry do not
@@ -624,8 +625,8 @@ int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, 
  *   S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    out_t = scale q_t S_t
  * q, k        device [T, H, Dk] of dtype, token strides given
  * v           device [T, H, Dv] of dtype, token stride given
- * log_decay   device [H] fp32, <= 0 (a constant of the head: it gets no
- *             gradient)
+ * log_decay   device [H] fp32, <= 0 (-inf: each token alone; a constant of
+ *             the head: it gets no gradient)
  * cu_seqlens  device [num_seqs + 1] int32, non-decreasing, 0 <= .. <= T:
  *             sequence n is rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 (it may
  *             be empty).  Rows outside every sequence are left as they are.
@@ -638,13 +639,16 @@ int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, 
  * out         device [T, H, Dv] of dtype, token stride given
  * workspace   device scratch of at least
  *             attnres_linear_attention_workspace_size(...) bytes, 256-byte
- *             aligned (NULL when that is 0)
+ *             aligned (NULL when that is 0).  Calls that overlap in time need
+ *             one each.
  * T >= 0, H 1..65535, Dk, Dv 1..256, num_seqs 1..65535 (ATTNRES_ERANGE
  * above).  The state is held in fp32.  bf16 tensors with Dk and Dv of 64 or
  * 128, 16-byte aligned rows, run in chunks of 128 tokens on the tensor cores
  * (tcgen05): scores and states enter those products rounded to bf16, the
- * state's own sums keep fp32 precision.  Other shapes run on the CUDA cores
- * in fp32.
+ * state's own sums keep fp32 precision.  Others run on the CUDA cores in
+ * fp32.  Long sequences are cut into segments where the batch does not fill
+ * the GPU (their states lie in the workspace).  Infinities and NaN reach the
+ * tokens behind them and no others; an infinity becomes NaN in the state.
  * ---------------------------------------------------------------------- */
 int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype, const float* log_decay,
@@ -669,7 +673,9 @@ int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv
  * grad_final_state    device [num_seqs, H, Dk, Dv] fp32 or NULL (zero)
  * grad_initial_state  the same shape or NULL; it may be grad_final_state
  * Other arguments as in attnres_linear_attention; workspace of at least
- * attnres_linear_attention_backward_workspace_size(...) bytes.
+ * attnres_linear_attention_backward_workspace_size(...) bytes.  Infinities
+ * and NaN reach grad_q of the tokens behind them, grad_k and grad_v of those
+ * before them.
  * ---------------------------------------------------------------------- */
 int attnres_linear_attention_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                       int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype,

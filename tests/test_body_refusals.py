@@ -30,6 +30,7 @@ def _linear(lib, **kw):
     (dict(act=-1), "EINVAL"), (dict(M=1 << 40), "ERANGE"), (dict(x=None), "EINVAL"), (dict(w=None), "EINVAL"),
     (dict(out=None), "EINVAL"), (dict(ldx=63), "EINVAL"), (dict(ldo=31), "EINVAL"), (dict(ldr=31), "EINVAL"),
     (dict(ldx=1 << 60), "EINVAL"), (dict(ws=WS, wsb=-1), "EINVAL"), (dict(ws=WS + 16, wsb=1024), "EINVAL"),
+    (dict(N=(1 << 30) + 1, ldo=1 << 31, ldr=1 << 31), "ERANGE"), (dict(N=1 << 30, K=1 << 30, M=1), "ERANGE"),
     (dict(out=X), "EINVAL"), (dict(out=W + 100), "EINVAL"), (dict(out=BI), "EINVAL"), (dict(out=RE + 2), "EINVAL"),
     (dict(res=OUT, ldr=40), "EINVAL"), (dict(ws=X - 256, wsb=512), "EINVAL"), (dict(ws=OUT - 256, wsb=512), "EINVAL"),
 ])
@@ -104,7 +105,7 @@ def _att(N, **kw):
     (dict(dt=2), "EDTYPE"), (dict(T=-1), "EINVAL"), (dict(H=0), "EINVAL"), (dict(Dk=0), "EINVAL"), (dict(Dv=257, vs=1 << 20), "ERANGE"),
     (dict(H=70000, qs=1 << 30), "ERANGE"), (dict(n=2), "EINVAL"), (dict(n=0), "EINVAL"), (dict(scale=float("inf")), "EINVAL"),
     (dict(qs=255), "EINVAL"), (dict(os=255), "EINVAL"), (dict(g=None), "EINVAL"), (dict(q=None), "EINVAL"), (dict(out=None), "EINVAL"),
-    (dict(T=1 << 33), "ERANGE"),
+    (dict(T=1 << 33), "ERANGE"), (dict(ws=WS + 64), "EINVAL"), (dict(ws=X), "EINVAL"),
 ])
 def test_linear_attention_refuses(N, kw, code):
     assert _att(N, **kw) == getattr(N, "ATTNRES_" + code), N.lib.attnres_last_error()

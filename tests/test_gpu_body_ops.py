@@ -291,6 +291,7 @@ ATT = [  # T, sequences, H, Dk, Dv
     (1, 1, 1, 8, 8), (5, 1, 2, 64, 64), (128, 1, 2, 128, 128), (129, 1, 3, 128, 128), (300, 4, 2, 128, 64), (257, 3, 2, 64, 128),
     (700, 9, 1, 64, 64), (1000, 1, 1, 128, 128), (200, 30, 2, 128, 128), (77, 3, 2, 96, 160), (70, 2, 1, 37, 5), (50, 2, 2, 1, 256),
     (90, 1, 1, 256, 33),
+    (2000, 1, 2, 128, 128), (4100, 5, 1, 64, 128), (3001, 3, 2, 40, 24),  # long enough to be cut into segments
 ]
 
 
@@ -413,6 +414,41 @@ def test_one_sequence_does_not_reach_another(A):
     assert torch.isnan(out2[100:200]).all() and torch.isnan(fin2[1]).all()
 
 
+@pytest.mark.parametrize("dt,D,T", [(torch.bfloat16, 128, 300), (torch.bfloat16, 64, 6000), (torch.float32, 40, 150),
+                                    (torch.bfloat16, 24, 6000)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_no_token_reaches_an_earlier_one(A, dt, D, T, bad):
+    """Infinities and NaN of a token behind: the outputs before it, and the
+    gradients that do not depend on it, are the formula's."""
+    t, H = T - 30, 2
+    q, k, v, decay, _, s0 = _att_inputs(T, 1, H, D, D, dt, 16)
+    q, k, v, do = q.clone(), k.clone(), v.clone(), _randn(_gen(17), T, H, D, dtype=dt)
+    x, do64 = [to64(a[:t]) for a in (q, k, v)], to64(do)
+    want, _ = B.linear_attention(*x, to64(decay), [0, t], to64(s0), D ** -0.5)
+    cond, _ = B.linear_attention(*[np.abs(a) for a in x], to64(decay), [0, t], np.abs(to64(s0)), D ** -0.5)
+    # dk and dv run backwards: what comes before token u does not reach them
+    u = 31
+    y = [to64(a[u:]) for a in (q, k, v)]
+    back = B.linear_attention_backward(*y, to64(decay), [0, T - u], None, D ** -0.5, do64[u:], None)
+    cback = B.linear_attention_backward(*[np.abs(a) for a in y], to64(decay), [0, T - u], None, D ** -0.5, np.abs(do64[u:]), None)
+    for a in (q, k, v):
+        a[t] = bad
+        a[t + 7, 1, 3] = -bad
+    out, fin = torch.empty_like(do), torch.empty_like(s0)
+    A.attnres_linear_attention(q, k, v, decay, out, initial_state=s0, final_state=fin)
+    _close(out[:t], want, U[dt] * np.abs(want) + _att_tol(T, D, D, dt) * cond, "out")
+    assert not torch.isfinite(out[t:, 1]).any()
+    q, k, v, _, _, _ = _att_inputs(T, 1, H, D, D, dt, 16)
+    q, k, v = q.clone(), k.clone(), v.clone()
+    for a in (q, k, v, do):
+        a[u - 1] = bad
+        a[u - 9, 1, 3] = -bad
+    grads = [torch.empty_like(do) for _ in range(3)]
+    A.attnres_linear_attention_backward(q, k, v, decay, do, *grads)
+    for got, w, c, name in zip(grads[1:], back[1:3], cback[1:3], ("dk", "dv")):
+        _close(got[u:], w, U[dt] * np.abs(w) + _att_tol(T, D, D, dt) * c, name)
+
+
 def test_a_state_survives_no_tokens(A):
     s0 = torch.randn(2, 3, 64, 64, device="cuda")
     e = torch.empty(0, 3, 64, device="cuda", dtype=torch.bfloat16)
@@ -476,6 +512,69 @@ def test_bad_offsets_are_clamped(A):
     A.attnres_linear_attention(q, k, v, decay, a, cu_seqlens=cu)
     A.attnres_linear_attention(q, k, v, decay, b, cu_seqlens=good)
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dt,T,n,H,D", [(torch.bfloat16, 300, 4, 3, 128), (torch.bfloat16, 9000, 3, 1, 64),
+                                        (torch.float32, 300, 4, 3, 40), (torch.float32, 6000, 3, 1, 24)])
+def test_a_decay_that_leaves_nothing(A, dt, T, n, H, D):
+    """log_decay = -inf is a decay of 0, which -200 rounds to in fp32: the
+    same bits, in one piece and in segments, with an empty sequence."""
+    q, k, v, _, cu, s0 = _att_inputs(T, n, H, D, D, dt, 13)
+    cu[1] = cu[2]
+    do = _randn(_gen(14), T, H, D, dtype=dt)
+    runs = []
+    for value in (-200.0, float("-inf")):
+        decay = torch.full((H,), value, device="cuda")
+        outs = [torch.empty(T, H, D, dtype=dt, device="cuda") for _ in range(4)]
+        st = [torch.empty_like(s0) for _ in range(2)]
+        A.attnres_linear_attention(q, k, v, decay, outs[0], cu_seqlens=cu, initial_state=s0, final_state=st[0])
+        A.attnres_linear_attention_backward(q, k, v, decay, do, *outs[1:], cu_seqlens=cu, initial_state=s0, grad_final_state=s0,
+                                            grad_initial_state=st[1])
+        o, pool = torch.empty(n, H, D, dtype=dt, device="cuda"), s0.clone()
+        A.attnres_linear_attention_step(q[:n], k[:n], v[:n], decay, pool, o)
+        runs.append([*outs, *st, o, pool])
+    for a, b in zip(*runs):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [64, 24])
+def test_no_workspace_is_used_where_none_is_given(A, D):
+    """A NULL workspace has no bytes whatever its size argument says, and
+    tensors off the 16-byte boundaries, for which none is asked, do without."""
+    from depth_wise_attention_block_gb300 import _native as N
+    T, H, dt = 700, 1, torch.bfloat16
+    assert A.attnres_linear_attention_workspace_size(T, H, 64, 64, dt) == 0 or D != 64
+    wide = _randn(_gen(15), T, 3 * D + 1, dtype=dt)
+    q, k, v = (wide[:, 1 + i * D:1 + (i + 1) * D].unflatten(1, (H, D)) for i in range(3))
+    decay = torch.full((H,), -0.01, device="cuda")
+    want, got = (torch.empty(T, H, D, dtype=dt, device="cuda") for _ in range(2))
+    A.attnres_linear_attention(q, k, v, decay, want)
+    need = A.attnres_linear_attention_workspace_size(T, H, D, D, dt)
+    s = 3 * D + 1
+    rc = N.lib.attnres_linear_attention(q.data_ptr(), s, k.data_ptr(), s, v.data_ptr(), s, T, H, D, D, 1, decay.data_ptr(), None, 1, None,
+                                        None, D ** -0.5, got.data_ptr(), D, None, 1 << 40, None,
+                                        torch.cuda.current_stream().cuda_stream)
+    if need > 0:
+        assert rc == N.ATTNRES_EINVAL
+    else:
+        assert rc == 0 and torch.equal(want, got)
+
+
+def test_a_stride_of_a_single_row_does_not_matter(A):
+    from depth_wise_attention_block_gb300 import _native as N
+    x, w, _, _ = _linear_inputs(1, 264, 136, torch.bfloat16, 23)
+    want, got = torch.empty(1, 264, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 264, dtype=torch.bfloat16, device="cuda")
+    A.attnres_linear(x, w, want)
+    rc = N.lib.attnres_linear(x.data_ptr(), 1 << 41, w.data_ptr(), None, None, 264, got.data_ptr(), 1 << 41, 1, 264, 136, 1, 0, None, 0,
+                              None, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and torch.equal(want, got)
+
+
+def test_gain_gradient_of_no_heads_is_zero(A):
+    q = torch.randn(5, 2, 64, device="cuda")
+    none, dg, dk = torch.empty(5, 0, 64, device="cuda"), torch.empty(64, device="cuda"), torch.full((64,), 7.0, device="cuda")
+    A.attnres_qk_norm_rope_backward(q, none, q, none, torch.empty_like(q), none, grad_q_gain=dg, grad_k_gain=dk)
+    assert not dk.any() and torch.isfinite(dg).all() and dg.any()
 
 
 # ---------------------------------------------------------------- together --
