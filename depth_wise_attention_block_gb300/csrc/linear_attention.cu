@@ -29,8 +29,9 @@ constexpr int kSC = 64;        // tokens per chunk
 constexpr int kSMaxD = 256;  // of the step's rows
 constexpr int kSPitchP = kSC + 4;
 
-// The scan on the CUDA cores: a CTA takes a segment, a head and NG groups of
-// 32 columns of c for each of W groups of 256 threads (STATE: the segments'
+// The scan on the CUDA cores: a CTA takes a sequence and head, or the pieces
+// of a range of the heads' chunks one after the other, and NG groups of
+// 32 columns of c for each of W groups of 256 threads (STATE: the pieces'
 // own states only, without scores and outputs; the combine kernel then leaves
 // the state before each).  Every product runs from shared memory in register tiles,
 // four rows by 2 NG columns per thread (16 x 16 threads), four steps of its
@@ -110,7 +111,7 @@ __device__ __noinline__ uint64_t masked_pair(const float* P, const float* c, int
 }
 
 template <typename T, int NG, int W, bool STATE>
-__global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant__ ScanArgs p) {
+__global__ void __launch_bounds__(256 * W, 2 / W) scan_any_kernel(const __grid_constant__ ScanArgs p) {
   extern __shared__ __align__(16) float sm[];
   const int Da = p.Da, Dc = p.Dc, pitch = scan_rows(Da), K = pitch - 4, Dr = (Da + 63) / 64 * 64;
   constexpr int NC = 32 * NG * W, kThreads = 256 * W;
@@ -122,136 +123,146 @@ __global__ void __launch_bounds__(256 * W) scan_any_kernel(const __grid_constant
   float* pw = S + Dr * NC;              // l^0 .. l^kSC
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16 % 16, group = tid / 256;
   const int own = group * 32 * NG;  // the group's first column
-  const int c0 = blockIdx.x * NC, h = blockIdx.y, wc = Dc - c0 < NC ? Dc - c0 : NC;
+  const int c0 = blockIdx.x * NC, wc = Dc - c0 < NC ? Dc - c0 : NC;
   pdl_wait();
   pdl_trigger();
-  const float g = p.log_decay[h];
-  if (tid <= kSC) pw[tid] = decay_pow(g, tid);
-  const int seg_i = blockIdx.z;
-  if (p.nsegs && seg_i >= *p.nsegs) return;
-  const Segment sg = segment_of(p, seg_i);
-  if (STATE && (sg.len == 0 || (sg.last && !p.s_out))) return;  // a last segment's own state is part of the final one only
-  const SeqRange sr{sg.first, sg.len};
-  const long long st = ((long long)(p.seg_state ? seg_i : sg.seq) * p.H + h) * Da * Dc;
-  const float* before = STATE ? nullptr : p.seg_state ? p.seg_state : p.s_in;
-  for (int i = tid; i < Dr * NC; i += kThreads) {
-    const int da = i / NC, dc = c0 + i % NC;
-    S[i] = before && da < Da && dc < Dc ? before[st + p.state_at(da, dc)] : 0.f;
-  }
-  for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
-    const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
-    __syncthreads();
-    if constexpr (!STATE) scan_load<T, kThreads>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
-    scan_load<T, kThreads>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
-    scan_load<T, kThreads>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
-    __syncthreads();
-    if constexpr (!STATE) {
-      {  // the triangle: rows ty + 16 r of the group's, columns tx + 16 s, sums over even and odd channels packed
-        constexpr int R = 4 / W;
-        const float* ag = a + group * 16 * R * pitch;
-        uint64_t acc[R][4];
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int s = 0; s < 4; ++s) acc[r][s] = 0;
-#pragma unroll 2
-        for (int k = 0; k < K; k += 4) {
-          ulonglong2 x[R], y[4];
-#pragma unroll
-          for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const ulonglong2*>(ag + (ty + 16 * r) * pitch + k);
-#pragma unroll
-          for (int s = 0; s < 4; ++s) y[s] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * s) * pitch + k);
+  PieceWalk walk;
+  if (p.parts > 0) walk = PieceWalk(p, blockIdx.y);
+  Piece pc;
+  for (bool first = true;; first = false) {
+    if (p.parts > 0) {
+      if (!walk.next(p, blockIdx.y, &pc)) return;
+      if (STATE && pc.last && !p.s_out) continue;  // a last piece's own state is part of the final one only
+    } else {
+      if (!first) return;
+      pc = whole_sequence(p, blockIdx.z, blockIdx.y);
+    }
+    const int h = pc.head;
+    const float g = p.log_decay[h];
+    __syncthreads();  // the piece before is done with
+    if (tid <= kSC) pw[tid] = decay_pow(g, tid);
+    const SeqRange sr{pc.first, pc.len};
+    const long long st = (p.parts > 0 ? pc.id : (long long)pc.seq * p.H + h) * Da * Dc;
+    const float* before = STATE ? nullptr : p.parts > 0 ? p.piece_state : p.s_in;
+    for (int i = tid; i < Dr * NC; i += kThreads) {
+      const int da = i / NC, dc = c0 + i % NC;
+      S[i] = before && da < Da && dc < Dc ? before[st + p.state_at(da, dc)] : 0.f;
+    }
+    for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
+      const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
+      __syncthreads();
+      if constexpr (!STATE) scan_load<T, kThreads>(a, pitch, p.a, p.as, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_a);
+      scan_load<T, kThreads>(b, pitch, p.b, p.bs, h * Da, Da, K, len, sr, i0, p.reverse, p.vec_b);
+      scan_load<T, kThreads>(c, NC, p.c, p.cs, h * Dc + c0, wc, NC, len, sr, i0, p.reverse, p.vec_c);
+      __syncthreads();
+      if constexpr (!STATE) {
+        {  // the triangle: rows ty + 16 r of the group's, columns tx + 16 s, sums over even and odd channels packed
+          constexpr int R = 4 / W;
+          const float* ag = a + group * 16 * R * pitch;
+          uint64_t acc[R][4];
 #pragma unroll
           for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
-        }
+            for (int s = 0; s < 4; ++s) acc[r][s] = 0;
+#pragma unroll 2
+          for (int k = 0; k < K; k += 4) {
+            ulonglong2 x[R], y[4];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+            for (int r = 0; r < R; ++r) x[r] = *reinterpret_cast<const ulonglong2*>(ag + (ty + 16 * r) * pitch + k);
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const int i = group * 16 * R + ty + 16 * r, j = tx + 16 * s;
-            P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
+            for (int s = 0; s < 4; ++s) y[s] = *reinterpret_cast<const ulonglong2*>(b + (tx + 16 * s) * pitch + k);
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+              for (int s = 0; s < 4; ++s) acc[r][s] = f2_fma(x[r].y, y[s].y, f2_fma(x[r].x, y[s].x, acc[r][s]));
           }
-      }
-      __syncthreads();
-      {
-        uint64_t in[4][NG], from[4][NG];
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+          for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
-        scan_mma<NG, NC>(in, P, kSPitchP, c + own, (len + 3) / 4 * 4, tx, ty);
-        scan_mma<NG, NC>(from, a, pitch, S + own, K, tx, ty);
-        uint64_t sum = 0;  // 0, or NaN where a value is not finite
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int s = 0; s < NG; ++s) sum = f2_fma(in[r][s], 0ull, sum);
-        if (f2_hsum(sum) != 0.f) {
+            for (int s = 0; s < 4; ++s) {
+              const int i = group * 16 * R + ty + 16 * r, j = tx + 16 * s;
+              P[i * kSPitchP + j] = j <= i ? f2_hsum(acc[r][s]) * pw[i - j] * p.p_scale : 0.f;
+            }
+        }
+        __syncthreads();
+        {
+          uint64_t in[4][NG], from[4][NG];
 #pragma unroll
           for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int s = 0; s < NG; ++s) in[r][s] = masked_pair(P + (ty + 16 * r) * kSPitchP, c + own + 32 * s + 2 * tx, NC, ty + 16 * r);
-        }
+            for (int s = 0; s < NG; ++s) in[r][s] = from[r][s] = 0;
+          scan_mma<NG, NC>(in, P, kSPitchP, c + own, (len + 3) / 4 * 4, tx, ty);
+          scan_mma<NG, NC>(from, a, pitch, S + own, K, tx, ty);
+          uint64_t sum = 0;  // 0, or NaN where a value is not finite
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = ty + 16 * r;
-          if (i < len) {
-            const float coef = pw[i + 1 - p.shift] * p.in_scale;
-            T* out = static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0;
+          for (int r = 0; r < 4; ++r)
 #pragma unroll
-            for (int s = 0; s < NG; ++s) {
-              float x0, x1, y0, y1;
-              f2_unpack(in[r][s], x0, x1);
-              f2_unpack(from[r][s], y0, y1);
-              const int d = own + 32 * s + 2 * tx;
-              if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
-              if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
+            for (int s = 0; s < NG; ++s) sum = f2_fma(in[r][s], 0ull, sum);
+          if (f2_hsum(sum) != 0.f) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int s = 0; s < NG; ++s) in[r][s] = masked_pair(P + (ty + 16 * r) * kSPitchP, c + own + 32 * s + 2 * tx, NC, ty + 16 * r);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int i = ty + 16 * r;
+            if (i < len) {
+              const float coef = pw[i + 1 - p.shift] * p.in_scale;
+              T* out = static_cast<T*>(p.out) + sr.row(i0 + i, p.reverse) * p.os + (long long)h * Dc + c0;
+#pragma unroll
+              for (int s = 0; s < NG; ++s) {
+                float x0, x1, y0, y1;
+                f2_unpack(in[r][s], x0, x1);
+                f2_unpack(from[r][s], y0, y1);
+                const int d = own + 32 * s + 2 * tx;
+                if (d < wc) store_elem(out + d, fmaf(y0, coef, x0));
+                if (d + 1 < wc) store_elem(out + d + 1, fmaf(y1, coef, x1));
+              }
             }
           }
         }
+        __syncthreads();
       }
-      __syncthreads();
-    }
-    // the state: rows d0 + 4 ty .. + 3
-    const uint64_t decay = f2_pack(pw[len], pw[len]), zero = f2_pack(0.f, 0.f);
-    for (int d0 = 0; d0 < Dr; d0 += 64) {
-      const int d = d0 + 4 * ty;
-      if (d >= K) continue;
-      uint64_t u[4][NG];
+      // the state: rows d0 + 4 ty .. + 3
+      const uint64_t decay = f2_pack(pw[len], pw[len]), zero = f2_pack(0.f, 0.f);
+      for (int d0 = 0; d0 < Dr; d0 += 64) {
+        const int d = d0 + 4 * ty;
+        if (d >= K) continue;
+        uint64_t u[4][NG];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int s = 0; s < NG; ++s) u[r][s] = zero;
+          for (int s = 0; s < NG; ++s) u[r][s] = zero;
 #pragma unroll 4
-      for (int j = 0; j < len; ++j) {
-        const float f = pw[len - 1 - j + p.shift] * p.up_scale;
-        const float4 x = *reinterpret_cast<const float4*>(b + j * pitch + d);
-        const uint64_t w[4] = {f2_pack(x.x * f, x.x * f), f2_pack(x.y * f, x.y * f), f2_pack(x.z * f, x.z * f), f2_pack(x.w * f, x.w * f)};
+        for (int j = 0; j < len; ++j) {
+          const float f = pw[len - 1 - j + p.shift] * p.up_scale;
+          const float4 x = *reinterpret_cast<const float4*>(b + j * pitch + d);
+          const uint64_t w[4] = {f2_pack(x.x * f, x.x * f), f2_pack(x.y * f, x.y * f), f2_pack(x.z * f, x.z * f), f2_pack(x.w * f, x.w * f)};
 #pragma unroll
-        for (int s = 0; s < NG; ++s) {
-          const uint64_t y = *reinterpret_cast<const uint64_t*>(c + j * NC + own + 32 * s + 2 * tx);
+          for (int s = 0; s < NG; ++s) {
+            const uint64_t y = *reinterpret_cast<const uint64_t*>(c + j * NC + own + 32 * s + 2 * tx);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) u[r][s] = f2_fma(w[r], y, u[r][s]);
+            for (int r = 0; r < 4; ++r) u[r][s] = f2_fma(w[r], y, u[r][s]);
+          }
         }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+          for (int s = 0; s < NG; ++s) {
+            uint64_t* at = reinterpret_cast<uint64_t*>(S + (d + r) * NC + own + 32 * s + 2 * tx);
+            *at = f2_fma(*at, decay, u[r][s]);
+          }
       }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int s = 0; s < NG; ++s) {
-          uint64_t* at = reinterpret_cast<uint64_t*>(S + (d + r) * NC + own + 32 * s + 2 * tx);
-          *at = f2_fma(*at, decay, u[r][s]);
-        }
     }
+    __syncthreads();
+    float* to = STATE ? p.piece_state : p.parts > 0 ? nullptr : p.s_out;  // pieces: the final state is joined with the others
+    if (to)
+      for (int i = tid; i < Da * NC; i += kThreads) {
+        const int da = i / NC, dc = c0 + i % NC;
+        if (dc < Dc) to[st + p.state_at(da, dc)] = S[i];
+      }
   }
-  __syncthreads();
-  float* to = STATE ? p.seg_state : p.seg_state ? nullptr : p.s_out;  // segments: the final state is joined with the others
-  if (to)
-    for (int i = tid; i < Da * NC; i += kThreads) {
-      const int da = i / NC, dc = c0 + i % NC;
-      if (dc < Dc) to[st + p.state_at(da, dc)] = S[i];
-    }
 }
 
 // Columns per CTA: all of them (every CTA of a head forms the chunk's scores
@@ -264,32 +275,33 @@ int scan_columns(int Da, int Dc, int smem_max) {
 }
 
 template <typename T, int NG, int W, bool STATE>
-cudaError_t launch_scan_any(const ScanArgs& s, int64_t segs, cudaStream_t stream) {
+cudaError_t launch_scan_any(const ScanArgs& s, cudaStream_t stream) {
   static SmemOptIn optin;
   constexpr int nc = 32 * NG * W;
   const auto kern = scan_any_kernel<T, NG, W, STATE>;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern));
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((s.Dc + nc - 1) / nc, s.H, (unsigned)segs), dim3(256 * W), scan_smem(s.Da, nc), stream, s);
+  const dim3 grid((s.Dc + nc - 1) / nc, s.parts > 0 ? s.parts * s.gang : s.H, s.parts > 0 ? 1 : s.N);
+  return launch_kernel(kern, grid, dim3(256 * W), scan_smem(s.Da, nc), stream, s);
 }
 
 template <typename T, bool STATE>
-cudaError_t launch_scan_groups(const ScanArgs& s, int nc, int64_t segs, cudaStream_t stream) {
+cudaError_t launch_scan_groups(const ScanArgs& s, int nc, cudaStream_t stream) {
   switch (nc) {
-    case 32: return launch_scan_any<T, 1, 1, STATE>(s, segs, stream);
-    case 64: return launch_scan_any<T, 2, 1, STATE>(s, segs, stream);
-    case 96: return launch_scan_any<T, 3, 1, STATE>(s, segs, stream);
-    default: return launch_scan_any<T, 2, 2, STATE>(s, segs, stream);
+    case 32: return launch_scan_any<T, 1, 1, STATE>(s, stream);
+    case 64: return launch_scan_any<T, 2, 1, STATE>(s, stream);
+    case 96: return launch_scan_any<T, 3, 1, STATE>(s, stream);
+    default: return launch_scan_any<T, 2, 2, STATE>(s, stream);
   }
 }
 
-// Tokens per segment on the CUDA cores.  At most 65535 segments to a grid.
-int scan_any_segment(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
+// Ranges on the CUDA cores: a chunk's products at the 110 FMA per ns that an
+// SM gives them, shared by the CTAs of an SM.
+Cut scan_any_cut(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
   const int nc = scan_columns(Da, Dc, di.max_smem_optin);
   const int per_sm = 2 * scan_smem(Da, nc) + 2048 <= di.max_smem_optin ? 2 : 1;
-  int seg = seg_tokens(T, N, kSC, (int64_t)H * ((Dc + nc - 1) / nc), per_sm * di.sm_count, 0.4);
-  if (seg > 0 && T / seg + 1 + N > 65535) seg = 0;
-  return seg;
+  const double chunk_ns = per_sm * (double)kSC * (kSC * (Da + nc) + 2 * Da * nc) / 110;
+  return choose_cut(T, H, Da, Dc, N, kSC, (Dc + nc - 1) / nc, per_sm * di.sm_count, 0.4, chunk_ns);
 }
 
 template <typename T>
@@ -304,44 +316,40 @@ cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t worksp
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
+  s.chunk = kSC;
   // one cut for both orders of the two head sizes: the gradients' scans share states
-  s.seg_len = scan_any_segment(s.T, s.H, s.transposed ? s.Dc : s.Da, s.transposed ? s.Da : s.Dc, s.N, di);
-  SegLayout L = seg_layout(s.T, s.H, s.Da, s.Dc, s.N, s.seg_len);
-  if (L.total > workspace_bytes) {  // tensors that the tensor cores would have taken but for their alignment
-    s.seg_len = 0;
-    L = SegLayout{};
-  }
+  const Cut cut = scan_any_cut(s.T, s.H, s.transposed ? s.Dc : s.Da, s.transposed ? s.Da : s.Dc, s.N, di);
+  const PieceLayout L = piece_layout(s.H, s.Da, s.Dc, s.N, cut);
+  s.gang = cut.gang;
+  s.parts = L.total > workspace_bytes ? 0 : cut.parts;  // tensors that the tensor cores would have taken but for their alignment
   const int nc = scan_columns(s.Da, s.Dc, di.max_smem_optin);
-  int64_t segs;
-  seg_place(s, L, workspace, &segs);
-  if (s.seg_len > 0 && !states_ready) {
-    e = launch_seg_plan(s, stream);
-    if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, nc, segs, stream);
-    if (e == cudaSuccess) e = launch_seg_combine(s, stream);
+  if (s.parts > 0) piece_place(s, L, workspace);
+  if (s.parts > 0 && !states_ready) {
+    e = launch_piece_plan(s, stream);
+    if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, nc, stream);
+    if (e == cudaSuccess) e = launch_piece_combine(s, stream);
     if (e != cudaSuccess) return e;
   }
-  return launch_scan_groups<T, false>(s, nc, segs, stream);
+  return launch_scan_groups<T, false>(s, nc, stream);
 }
 
-// The segments of a ragged batch, in order: one thread per sequence counts,
-// a prefix sum places them.
+// The tables of a ragged batch.
 constexpr int kPlanThreads = 1024;
-__global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu, int N, long long T, int seg_len, bool reverse, Segment* segs,
-                                                               int* first_of, int* nsegs) {
-  // 64 bits: offsets that decrease can ask for any number of segments
+__global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const __grid_constant__ ScanArgs p) {
+  const int N = p.N, chunk = p.chunk;
+  const int32_t* cu = p.cu;
+  const long long T = p.T;
+  int* first = const_cast<int*>(p.first);
+  // 64 bits: offsets that decrease can ask for any number of chunks
   __shared__ long long sums[32], carry;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long cap = (T + chunk - 1) / chunk + N;  // what offsets that do not decrease stay below
   pdl_wait();
   pdl_trigger();
   if (tid == 0) carry = 0;
   for (int n0 = 0; n0 < N; n0 += kPlanThreads) {
     const int n = n0 + tid;
-    SeqRange r{0, 0};
-    int cnt = 0;
-    if (n < N) {
-      r = seq_range(cu, n, T);
-      cnt = r.len > seg_len ? (int)((r.len + seg_len - 1) / seg_len) : 1;
-    }
+    const long long cnt = n < N ? (seq_range(cu, n, T).len + chunk - 1) / chunk : 0;
     long long x = cnt;
     for (int o = 1; o < 32; o *= 2) {
       const long long y = __shfl_up_sync(0xffffffffu, x, o);
@@ -359,74 +367,79 @@ __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const int32_t* cu
     }
     __syncthreads();
     const long long at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
-    // none past the table, whatever the offsets
-    const long long cap = (T + seg_len - 1) / seg_len + N;
-    if (n < N) first_of[n] = (int)(at < cap ? at : cap);
-    for (int i = 0; i < cnt && at + i < cap; ++i) segs[at + i] = cut(n, r, i, seg_len, reverse);
+    if (n < N) first[n] = (int)(at < cap ? at : cap);
     const long long total = sums[31];
     __syncthreads();
     if (tid == 0) carry += total;
     __syncthreads();
   }
-  if (tid == 0) {
-    const long long cap = (T + seg_len - 1) / seg_len + N;
-    const int total = (int)(carry < cap ? carry : cap);
-    first_of[N] = total;
-    *nsegs = total;
+  if (tid == 0) first[N] = (int)(carry < cap ? carry : cap);
+  __syncthreads();
+  const Ranges r(p);
+  for (int i = tid; i <= p.parts; i += kPlanThreads) {
+    const int u = r.begin(i), gang = r.per_head > 0 ? u / r.per_head : 0;
+    const_cast<int4*>(p.starts)[i] = make_int4(u, gang, sequence_of(first, N, u - gang * r.per_head), r.per_head);
   }
 }
 
-// Per sequence and head: the state before each segment, from the segments'
-// own states, in place and in order, and the final state.  VEC floats per
-// thread of [H][Da Dc].
+// Per sequence and head: the state before each piece, from the pieces' own
+// states, in place and in order, and the final state.  VEC floats per thread
+// of [H][Da Dc].
 template <int VEC>
-__global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__ ScanArgs p, const int* first_of, int per_head) {
+__global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__ ScanArgs p, int per_head) {
   const long long e = (blockIdx.x * 256LL + threadIdx.x) * VEC;
   const int n = blockIdx.y;
   pdl_wait();
   pdl_trigger();
   const long long all = (long long)p.H * per_head;
   if (e >= all) return;
-  const float g = __ldg(p.log_decay + (int)(e / per_head));
-  const int s0 = first_of ? first_of[n] : 0;
-  const int s1 = first_of ? first_of[n + 1] : (int)((p.T + p.seg_len - 1) / p.seg_len);
+  const int h = (int)(e / per_head);
+  const float g = __ldg(p.log_decay + h);
+  const Ranges r(p);
+  // the sequence's chunks of this head, and the ranges that have them
+  const int gang = h / p.gang, at_gang = gang * r.per_head;
+  const int u0 = at_gang + (p.first ? p.first[n] : 0), u1 = at_gang + (p.first ? p.first[n + 1] : r.per_head);
+  const int i0 = u0 < u1 ? r.owner(u0) : 0, i1 = u0 < u1 ? r.owner(u1 - 1) + 1 : 0;
+  const long long step = (long long)p.gang * per_head;  // from a piece's state to the next one's
+  float* const at0 = p.piece_state + ((long long)gang * p.N + n) * step + (h - gang * p.gang) * (long long)per_head + (e - (long long)h * per_head);
   float w[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) w[k] = p.s_in ? p.s_in[n * all + e + k] : 0.f;
-  // four segments' states are loaded before the first of them is replaced
+  // four pieces' states are loaded before the first of them is replaced
   constexpr int kAhead = 4;
-  for (int s = s0; s < s1; s += kAhead) {
+  for (int i = i0; i < i1; i += kAhead) {
     float u[kAhead][VEC], d[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      d[i] = 1.f;
+    for (int j = 0; j < kAhead; ++j) {
+      d[j] = 1.f;
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) u[i][k] = 0.f;
-      if (s + i < s1) {
-        const Segment sg = segment_of(p, s + i);
-        d[i] = decay_pow(g, sg.len);
-        const float* at = p.seg_state + (s + i) * all + e;
-        if (sg.len > 0 && (!sg.last || p.s_out)) {
+      for (int k = 0; k < VEC; ++k) u[j][k] = 0.f;
+      if (i + j < i1) {
+        const int b = r.begin(i + j) > u0 ? r.begin(i + j) : u0, f = r.begin(i + j + 1) < u1 ? r.begin(i + j + 1) : u1;
+        const Piece pc = cut_piece(p, n, h, b - u0, f - b);
+        d[j] = decay_pow(g, pc.len);
+        const float* at = at0 + (i + j) * step;
+        if (!pc.last || p.s_out) {
           if constexpr (VEC == 4) {
             const float4 x = *reinterpret_cast<const float4*>(at);
-            u[i][0] = x.x, u[i][1] = x.y, u[i][2] = x.z, u[i][3] = x.w;
+            u[j][0] = x.x, u[j][1] = x.y, u[j][2] = x.z, u[j][3] = x.w;
           } else {
-            u[i][0] = *at;
+            u[j][0] = *at;
           }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      if (s + i < s1) {
-        float* at = p.seg_state + (s + i) * all + e;
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j < i1) {
+        float* at = at0 + (i + j) * step;
         if constexpr (VEC == 4)
           *reinterpret_cast<float4*>(at) = make_float4(w[0], w[1], w[2], w[3]);
         else
           *at = w[0];
       }
 #pragma unroll
-      for (int k = 0; k < VEC; ++k) w[k] = fmaf(w[k], d[i], u[i][k]);
+      for (int k = 0; k < VEC; ++k) w[k] = fmaf(w[k], d[j], u[j][k]);
     }
   }
   if (p.s_out) {
@@ -577,66 +590,72 @@ ScanArgs scan_args(const LinAttnArgs& a, const void* x, int64_t xs, const void* 
 
 }  // namespace
 
-SegLayout seg_layout(int64_t T, int H, int Da, int Dc, int N, int seg_len) {
-  SegLayout L{};
-  if (seg_len == 0) return L;
-  L.segs = round_up(T, seg_len) / seg_len + N;
-  L.table = round_up(L.segs * (int64_t)sizeof(Segment), 256);
-  L.first = round_up((N + 2) * 4, 256);
-  L.states = round_up(L.segs * H * (int64_t)Da * Dc * 4, 256);
-  L.total = L.table + L.first + L.states;
+PieceLayout piece_layout(int H, int Da, int Dc, int N, Cut cut) {
+  PieceLayout L{};
+  if (cut.parts == 0) return L;
+  L.first = round_up((N + 1) * 4LL, 256);
+  L.starts = round_up((cut.parts + 1) * (int64_t)sizeof(int4), 256);
+  L.states = round_up(((int64_t)cut.parts * cut.gang + (int64_t)H * N) * Da * Dc * 4, 256);
+  L.total = L.first + L.starts + L.states;
   return L;
 }
 
-void seg_place(ScanArgs& s, const SegLayout& L, void* workspace, int64_t* segs) {
-  *segs = s.N;
-  if (s.seg_len == 0) return;
+void piece_place(ScanArgs& s, const PieceLayout& L, void* workspace) {
   char* ws = static_cast<char*>(workspace);
-  s.seg_state = reinterpret_cast<float*>(ws + L.table + L.first);
-  *segs = s.cu ? L.segs : round_up(s.T, s.seg_len) / s.seg_len;
-  if (s.cu) {
-    s.segs = reinterpret_cast<Segment*>(ws);
-    s.nsegs = reinterpret_cast<int*>(ws + L.table) + s.N + 1;  // behind the N + 1 first segments
-  }
+  s.first = s.cu ? reinterpret_cast<const int*>(ws) : nullptr;
+  s.starts = reinterpret_cast<const int4*>(ws + L.first);
+  s.piece_state = reinterpret_cast<float*>(ws + L.first + L.starts);
 }
 
-int seg_tokens(int64_t T, int N, int chunk, int64_t per_seg, int slots, double extra) {
-  const int64_t chunks = round_up(T, chunk) / chunk;
-  const double even = (double)per_seg * (double)(chunks + N) / slots;  // chunks per slot if all were equal
-  double best = (double)(chunks > even ? chunks : even) + 2;
-  int seg = 0;
-  for (int64_t c = 2; c < chunks; c += c < 16 ? 1 : c / 8) {
-    const int64_t ctas = per_seg * (round_up(chunks, c) / c + N - 1);
-    const double cost = (double)((ctas + slots - 1) / slots) * ((double)c + 2) * (1 + extra) + 4;
-    if (cost < best) {
-      best = cost;
-      seg = (int)(c * chunk);
+Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, int slots, double extra, double chunk_ns) {
+  const int64_t chunks = round_up(T, chunk) / chunk, units = H * (chunks + N);
+  if (T == 0 || units >= INT32_MAX / 2) return {0, 1};  // a chunk's index is an int
+  const double even = (double)groups * (double)units / slots;  // chunks per slot if all were equal
+  // Neighbouring heads lie side by side in memory: the largest gang, unless a
+  // smaller one divides the work better (8192 tokens of 5 sequences, 32 heads
+  // of 128, backward: 325 us in gangs of 8, 334 in gangs of 1).
+  Cut cut{0, 1};
+  double best = 1e300;
+  for (int gang = 8; gang >= 1; --gang) {
+    if (H % gang || gang > slots / groups) continue;
+    const int64_t gangs = H / gang;
+    for (int least = 1; least <= 4; ++least) {  // chunks of a range
+      int64_t parts = slots / groups / gang;
+      if (parts > gangs * chunks / least) parts = gangs * chunks / least;
+      if (parts == 0) break;
+      const double pieces = (double)(parts + gangs * N);  // of a gang's head
+      const double bytes = pieces * gang * Da * Dc * 16;  // written, read, replaced and read
+      const double join = bytes / 6500 + 250. * (double)parts / (double)gangs + 12000;
+      const double cost = ((double)(gangs * chunks) + pieces) / (double)parts * (1 + extra) + join / chunk_ns;
+      if (cost < 0.95 * best) {
+        best = cost;
+        cut = {(int)parts, gang};
+      }
     }
   }
-  return seg;
+  const double whole = (double)(chunks > even ? chunks : even) + 2;  // every sequence in one piece
+  if (best >= whole) cut.parts = 0;
+  return cut;
 }
 
-cudaError_t launch_seg_plan(const ScanArgs& s, cudaStream_t stream) {
-  if (!s.segs) return cudaSuccess;
-  int* first_of = const_cast<int*>(s.nsegs) - s.N - 1;
-  return launch_kernel(la_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, s.cu, s.N, s.T, s.seg_len, s.reverse,
-                       const_cast<Segment*>(s.segs), first_of, first_of + s.N + 1);
+cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream) {
+  if (!s.first) return cudaSuccess;
+  return launch_kernel(la_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, s);
 }
 
-cudaError_t launch_seg_combine(const ScanArgs& s, cudaStream_t stream) {
+cudaError_t launch_piece_combine(const ScanArgs& s, cudaStream_t stream) {
   const int per_head = s.Da * s.Dc;
-  const int* first_of = s.segs ? s.nsegs - s.N - 1 : nullptr;
   const int64_t all = (int64_t)s.H * per_head;
   if (per_head % 4 == 0)
-    return launch_kernel(la_combine_kernel<4>, dim3((unsigned)((all / 4 + 255) / 256), s.N), dim3(256), 0, stream, s, first_of, per_head);
-  return launch_kernel(la_combine_kernel<1>, dim3((unsigned)((all + 255) / 256), s.N), dim3(256), 0, stream, s, first_of, per_head);
+    return launch_kernel(la_combine_kernel<4>, dim3((unsigned)((all / 4 + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
+  return launch_kernel(la_combine_kernel<1>, dim3((unsigned)((all + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
 }
 
 int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int dtype, int N) {
   if (scan_tc_dims(Dk, Dv, dtype)) return scan_tc_workspace(T, H, Dk, Dv, N);
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return seg_layout(T, H, Dk, Dv, N, scan_any_segment(T, H, Dk, Dv, N, di)).total;
+  return piece_layout(H, Dk, Dv, N, scan_any_cut(T, H, Dk, Dv, N, di)).total;
 }
 
 namespace {
@@ -647,12 +666,12 @@ cudaError_t launch_scan(const LinAttnArgs& a, const ScanArgs& s, bool tc, bool s
                                  : launch_scan_type<float>(s, a.workspace, a.workspace_bytes, states_ready, a.stream);
 }
 
-// whether long sequences are cut into segments on the CUDA cores
-bool scan_any_segmented(const LinAttnArgs& a) {
+// whether the scan runs in pieces on the CUDA cores
+bool scan_any_in_pieces(const LinAttnArgs& a) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return false;
-  const int seg = scan_any_segment(a.T, a.H, a.Dk, a.Dv, a.N, di);
-  return seg > 0 && seg_layout(a.T, a.H, a.Dk, a.Dv, a.N, seg).total <= a.workspace_bytes;
+  const Cut cut = scan_any_cut(a.T, a.H, a.Dk, a.Dv, a.N, di);
+  return cut.parts > 0 && piece_layout(a.H, a.Dk, a.Dv, a.N, cut).total <= a.workspace_bytes;
 }
 
 }  // namespace
@@ -684,10 +703,10 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   v.p_scale = v.up_scale = a.scale;
   const bool tc = scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(q) && scan_tc_ok(k) && scan_tc_ok(v);
   // dk and dv carry the same reversed state ([Dk, Dv] in memory for both): in
-  // segments it is formed once.  grad_initial_state may lie over
+  // pieces it is formed once.  grad_initial_state may lie over
   // grad_final_state, so it is written after the last read of that: where
-  // the segments' states are joined, or by dv's scan.
-  const bool cut = tc ? scan_tc_segmented(a.T, a.H, a.N) : scan_any_segmented(a);
+  // the pieces' states are joined, or by dv's scan.
+  const bool cut = tc ? scan_tc_in_pieces(a.T, a.H, a.Dk, a.Dv, a.N) : scan_any_in_pieces(a);
   (cut ? k : v).s_out = a.ds0;
   cudaError_t e = launch_scan(a, q, tc, false);
   if (e == cudaSuccess) e = launch_scan(a, k, tc, false);

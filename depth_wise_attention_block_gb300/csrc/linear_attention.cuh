@@ -24,21 +24,12 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int n, long lon
 // l^n = exp(n log_decay), and l^0 = 1 for a decay that leaves nothing (-inf) too
 __device__ __forceinline__ float decay_pow(float log_decay, int n) { return n == 0 ? 1.f : expf(log_decay * (float)n); }
 
-struct Segment {
-  int seq, first, len, last;  // sequence, first token, tokens, whether the sequence ends with it
+// What a CTA scans in one go: tokens of one sequence and head.
+struct Piece {
+  int seq, head, first, len;  // first: the lowest row
+  int id;                     // of its state
+  int last;                   // whether the sequence ends with it, in the direction of the scan
 };
-
-// segment `i` of a sequence, in the direction of the scan
-__device__ __forceinline__ Segment cut(int n, const SeqRange& r, int i, int seg_len, bool reverse) {
-  Segment g;
-  g.seq = n;
-  const long long i0 = (long long)i * seg_len;
-  const long long len = seg_len > 0 && r.len - i0 > seg_len ? seg_len : r.len - i0;
-  g.len = (int)len;
-  g.first = (int)(reverse ? r.start + r.len - i0 - len : r.start + i0);
-  g.last = i0 + len >= r.len;
-  return g;
-}
 
 struct ScanArgs {
   const void *a, *b, *c;   // [T, H, Da], [T, H, Da], [T, H, Dc]; token strides
@@ -57,46 +48,112 @@ struct ScanArgs {
   bool vec_a, vec_b, vec_c;  // rows in vectors of 4 elements (set by the launch)
   float p_scale, in_scale, up_scale;  // factors of the triangle, of the carried state's part, of what enters the state
 
-  // segments: null, and a segment is a sequence, or arithmetic over the one
-  // there is
-  const Segment* segs;
-  const int* nsegs;
-  int seg_len;             // tokens per segment (0: a sequence is one segment)
-  float* seg_state;        // [segment][H][..]: each segment's own state, then the state before it
+  // parts > 0: the heads in gangs of neighbours, the gangs' chunks (gang by
+  // gang, the sequences in order) in `parts` even ranges, a CTA to each range
+  // and head of its gang; a piece is what a range holds of a sequence.  0: a
+  // CTA per sequence and head
+  int chunk, parts, gang;  // tokens per chunk; heads per gang, which divides H
+  const int* first;        // of a ragged batch: [N + 1] a head's chunks before each sequence,
+  const int4* starts;      // [parts + 1] each range's first chunk, its gang and sequence, and a head's chunks
+  float* piece_state;      // [piece][..]: each piece's own state, then the state before it
 
   __host__ __device__ int state_at(int da, int dc) const { return transposed ? dc * Da + da : da * Dc + dc; }
 };
 
-__device__ __forceinline__ Segment segment_of(const ScanArgs& s, int i) {
-  if (s.segs) return s.segs[i];
-  if (s.cu) return cut(i, seq_range(s.cu, i, s.T), 0, 0, s.reverse);
-  return cut(0, {0, s.T}, i, s.seg_len, s.reverse);
-}
-
-// Workspace of a scan in segments: at most `segs` of them; bytes of the table,
-// of the sequences' first segments and of the states.
-struct SegLayout {
-  int64_t segs, table, first, states, total;
+// The ranges: range i's first chunk, and the range that has chunk u.
+struct Ranges {
+  int per_head, q, rem;
+  __device__ explicit Ranges(const ScanArgs& s) {
+    per_head = s.first ? s.first[s.N] : (int)((s.T + s.chunk - 1) / s.chunk);
+    const int units = per_head * (s.H / s.gang);
+    q = units / s.parts;
+    rem = units - q * s.parts;
+  }
+  __device__ int begin(int i) const { return q * i + (i < rem ? i : rem); }
+  __device__ int owner(int u) const { return u < rem * (q + 1) ? u / (q + 1) : rem + (u - rem * (q + 1)) / q; }
 };
-SegLayout seg_layout(int64_t T, int H, int Da, int Dc, int N, int seg_len);
-// Points s at the workspace; *segs: the CTAs' segments.
-void seg_place(ScanArgs& s, const SegLayout& L, void* workspace, int64_t* segs);
-// Tokens per segment (0: every sequence in one piece): a wave of `slots` CTAs
-// (per_seg of them to a segment) takes a segment's chunks and about two more
-// to start and end; the segments' own states cost `extra` of a scan, and the
-// launches about 4 chunks.  The lengths are on the device, so the longest
-// sequence is taken to be all T tokens.
-int seg_tokens(int64_t T, int N, int chunk, int64_t per_seg, int slots, double extra);
-cudaError_t launch_seg_plan(const ScanArgs& s, cudaStream_t stream);      // the table of a ragged batch
-cudaError_t launch_seg_combine(const ScanArgs& s, cudaStream_t stream);   // own states -> the states before, and the final ones
+// Chunks c0 .. c0 + n - 1 of a sequence as a piece.
+__device__ __forceinline__ Piece cut_piece(const ScanArgs& s, int seq, int head, int c0, int n) {
+  const SeqRange r = seq_range(s.cu, seq, s.T);
+  const long long i0 = (long long)c0 * s.chunk, all = (long long)n * s.chunk, len = r.len - i0 < all ? r.len - i0 : all;
+  return {seq, head, (int)(s.reverse ? r.start + r.len - i0 - len : r.start + i0), (int)len, 0, i0 + len >= r.len};
+}
+__device__ __forceinline__ Piece whole_sequence(const ScanArgs& s, int seq, int head) {
+  const SeqRange r = seq_range(s.cu, seq, s.T);
+  return {seq, head, (int)r.start, (int)r.len, 0, 1};
+}
+// The sequence with a head's chunk c: the last one that starts at c or before.
+__device__ __forceinline__ int sequence_of(const int* first, int N, int c) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (first[mid] <= c)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+// The pieces of CTA `cta`, one after the other.
+struct PieceWalk {
+  int u = 0, end = 0, gang = 0, seq = 0, per_head = 0;
+  __device__ PieceWalk() {}
+  __device__ PieceWalk(const ScanArgs& s, int cta) {
+    const int part = cta / s.gang;
+    if (s.first) {
+      const int4 a = s.starts[part];
+      u = a.x, gang = a.y, seq = a.z, per_head = a.w;
+      end = s.starts[part + 1].x;
+    } else {
+      const Ranges r(s);
+      u = r.begin(part), end = r.begin(part + 1), per_head = r.per_head;
+      gang = u / per_head;
+    }
+  }
+  __device__ bool next(const ScanArgs& s, int cta, Piece* p) {
+    if (u >= end) return false;
+    if (u == (gang + 1) * per_head) ++gang, seq = 0;
+    const int c = u - gang * per_head;
+    int f0 = 0, f1 = per_head;
+    if (s.first) {
+      f0 = s.first[seq], f1 = s.first[seq + 1];
+      while (f1 <= c) f0 = f1, f1 = s.first[++seq + 1];
+    }
+    const int n = f1 - c < end - u ? f1 - c : end - u, part = cta / s.gang, member = cta - part * s.gang;
+    *p = cut_piece(s, seq, gang * s.gang + member, c - f0, n);
+    p->id = (part + gang * s.N + seq) * s.gang + member;  // part + gang N + seq grows from piece to piece
+    u += n;
+    return true;
+  }
+};
+
+// Workspace of a scan in pieces: bytes of the tables and of the states.
+struct PieceLayout {
+  int64_t first, starts, states, total;
+};
+struct Cut {
+  int parts, gang;
+};
+PieceLayout piece_layout(int H, int Da, int Dc, int N, Cut cut);
+void piece_place(ScanArgs& s, const PieceLayout& L, void* workspace);  // points s at the workspace
+// Ranges to cut the chunks into (0: every sequence in one piece).  A range
+// takes its chunks and about one more per piece; the pieces' own states cost
+// `extra` of a scan, then there are their bytes, 250 ns for each of a
+// sequence's pieces that are joined, and three launches.  `slots`
+// CTAs run at once, `groups` of them to a range and head, a chunk takes
+// chunk_ns.  The lengths are on the device, so the longest sequence is taken
+// to be all T tokens.
+Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, int slots, double extra, double chunk_ns);
+cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream);     // the tables of a ragged batch
+cudaError_t launch_piece_combine(const ScanArgs& s, cudaStream_t stream);  // own states -> the states before, and the final ones
 
 // The scan on the tensor cores (linear_attention_tc.cu).
 constexpr int kScanChunk = 128;  // tokens per chunk
 bool scan_tc_dims(int Dk, int Dv, int dtype);
 bool scan_tc_ok(const ScanArgs& s);  // alignment, sizes
-bool scan_tc_segmented(int64_t T, int H, int N);  // whether long sequences are cut into segments
+bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N);  // whether the scan runs in pieces
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N);
-// states_ready: the workspace holds the states before the segments already,
+// states_ready: the workspace holds the states before the pieces already,
 // left there by a scan of the same direction, states and sums b c^T (which
 // wrote the final state, if any)
 cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream);

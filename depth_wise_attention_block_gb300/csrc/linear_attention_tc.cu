@@ -19,10 +19,13 @@
 // A reversed scan (gradients of k and v) takes the chunks from the end and
 // mirrors the mask and the powers; nothing is reordered in memory.
 //
-// Few heads and sequences do not fill the GPU.  A long sequence is then cut
-// into segments: state_tc_kernel forms every segment's own state (it
-// reads b and c only), la_combine_kernel runs through the segments and
-// leaves the state before each, and the scan runs over all segments at once.
+// Few heads and sequences do not fill the GPU, and many of unequal lengths
+// fill it badly.  The chunks of all heads are then cut into even ranges, one
+// to an SM: state_tc_kernel forms the state of every piece of a sequence in a
+// range (it reads b and c only), la_combine_kernel runs through a sequence's
+// pieces and leaves the state before each, and the scan runs over the ranges.
+// The loads run ahead from piece to piece; a table in shared memory tells the
+// other warps of each.
 //
 // Bound: HBM.  A chunk of 128 x 128 heads takes 6 x 512 cycles of the tensor
 // cores against about 5500 cycles of HBM time per SM.
@@ -43,6 +46,7 @@ constexpr int kC = kScanChunk;         // tokens per chunk
 constexpr int kTileThreads = 576;      // the states' kernel: 16 warps of arithmetic, TMA, MMA
 constexpr int kScanThreads = 608;      // the scan: 8 warps scores and outputs, 8 state, TMA, two MMA
 constexpr int kMaxSlots = 8;
+constexpr int kPieces = 8;  // of the table of pieces; the loads are at most four pieces ahead
 // Dynamic shared memory of sm_103a's 227 KB per CTA beside 2 KB of barriers
 // and tables.  The rings' lengths are constants: a division by a length read
 // from a parameter costs the issuing threads more than a product.
@@ -82,11 +86,11 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// D[tmem] (+)= A[tmem] x B[smem]^T
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] x B[smem]^T, by a whole warp
+__device__ __forceinline__ void tc_mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -136,14 +140,19 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, b_ready, u_full, u_free;
+  __shared__ __align__(8) uint64_t t_ready;
   __shared__ uint32_t tmem_base;
-  __shared__ float tab[2 * kC], pw[kC + 2];  // p_scale l^(i - kC), 0 below; l^i
+  // l^i, and p_scale l^i behind it: distances below 0, which the mask covers
+  // and which reach -46, read into the first
+  __shared__ float pw[2 * kC + 4];
+  float* const tab = pw + kC + 4;
+  __shared__ Piece pieces[kPieces];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_buf = base + kSlots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
+  const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
+    mbar_init(smem_addr(&t_ready), 16);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 2);  // two arrivals free a slot: each MMA warp's (c), or one warp's two (a, b)
@@ -162,27 +171,27 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = warp_value(tmem_base);
   pdl_wait();
   pdl_trigger();
-  const float g = __ldg(p.s.log_decay + h);
-  if (tid < kC + 2) {
-    const float l = decay_pow(g, tid);
-    pw[tid] = l;
-    if (tid < kC) {
-      tab[tid] = 0.f;
-      tab[kC + tid] = p.s.p_scale * l;
+  const bool cut = p.s.parts > 0, rev = p.s.reverse;
+  // the table of pieces: its first one, then what the loads publish
+  PieceWalk walk;
+  if (warp == 16 && lane == 0) {
+    Piece pc{0, 0, 0, 0, 0, 0};
+    if (cut) {
+      walk = PieceWalk(p.s, blockIdx.x);
+      walk.next(p.s, blockIdx.x, &pc);
+    } else {
+      pc = whole_sequence(p.s, blockIdx.x / p.s.H, blockIdx.x % p.s.H);
     }
+    pieces[0] = pc;
   }
   __syncthreads();
-  const bool live = !p.s.nsegs || seg_i < *p.s.nsegs;
-  Segment sg{0, 0, 0, 0};
-  if (live) sg = segment_of(p.s, seg_i);
-  const int nchunk = live ? (sg.len + kC - 1) / kC : 0;
-  const bool rev = p.s.reverse;
-  // chunk n's first token and length (a reversed scan's short chunk is its last)
-  auto chunk_len = [&](int n) { return sg.len - n * kC < kC ? sg.len - n * kC : kC; };
-  auto chunk_at = [&](int n) { return rev ? sg.first + sg.len - n * kC - chunk_len(n) : sg.first + n * kC; };
+  const bool live = !cut || pieces[0].len > 0;
+  // first token of the chunk that begins `left` tokens before a piece's end
+  // (a reversed scan's short chunk is its last)
+  auto chunk_at = [&](const Piece& q, int left) { return rev ? q.first + (left > kC ? left - kC : 0) : q.first + q.len - left; };
   // once a wait runs out, the others of this thread return at once
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -199,17 +208,31 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   if (warp == 16) {
     if (lane == 0) {
       int it = 0;
-      for (int n = 0; n < nchunk && ok; ++n) {
-        const int t = chunk_at(n);
-        for (int k = 0; k < kTiles; ++k, ++it) {
-          const int st = it % kSlots;
-          wait(&empty[st], (uint32_t)(it / kSlots) + 1u);
-          if (!ok) break;
-          const int D = k == 2 ? DC : DA;
-          const CUtensorMap* m = k == 0 ? &p.ma : k == 1 ? &p.mb : &p.mc;
-          const uint32_t fb = smem_addr(&full[st]);
-          mbar_arrive_expect_tx(fb, D * kC * 2);
-          for (int x = 0; x < D; x += 64) tma_load_2d(base + st * kTile + x / 64 * kPanel, m, h * D + x, t, fb);
+      Piece pc = pieces[0];
+      for (int k = 1; ok; ++k) {
+        for (int left = pc.len; left > 0 && ok; left -= kC) {
+          const int t = chunk_at(pc, left);
+          for (int x = 0; x < kTiles; ++x, ++it) {
+            const int st = it % kSlots;
+            wait(&empty[st], (uint32_t)(it / kSlots) + 1u);
+            if (!ok) break;
+            const int D = x == 2 ? DC : DA;
+            const CUtensorMap* m = x == 0 ? &p.ma : x == 1 ? &p.mb : &p.mc;
+            const uint32_t fb = smem_addr(&full[st]);
+            mbar_arrive_expect_tx(fb, D * kC * 2);
+            for (int y = 0; y < D; y += 64) tma_load_2d(base + st * kTile + y / 64 * kPanel, m, pc.head * D + y, t, fb);
+          }
+        }
+        if (!cut || !live || !ok) break;
+        // the next piece, which its first tile's barrier publishes; behind the
+        // last a barrier of no bytes
+        const bool more = walk.next(p.s, blockIdx.x, &pc);
+        if (!more) pc.len = 0;
+        pieces[k % kPieces] = pc;
+        if (!more) {
+          wait(&empty[it % kSlots], (uint32_t)(it / kSlots) + 1u);
+          if (ok) mbar_arrive(smem_addr(&full[it++ % kSlots]));
+          break;
         }
       }
       // the CTA never exits under a copy
@@ -218,65 +241,82 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     }
     __syncwarp();
   } else if (warp == 17) {
-    if (lane == 0) {
-      constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC);
-      auto slot = [&](int i) { return base + i % kSlots * kTile; };
-      auto wait_tile = [&](int i) { wait(&full[i % kSlots], (uint32_t)(i / kSlots)); };
-      // scores of chunk n, over those of n - 1 (whose P c is done)
-      auto scores = [&](int n) {
-        const int it = n * kTiles;
-        if (n > 0) wait(&o_full, (uint32_t)n - 1u);
-        wait_tile(it);
-        wait_tile(it + 1);
-        tc_fence_after();
-        const uint64_t da = smem_desc_k128(slot(it)), db = smem_desc_k128(slot(it + 1));
+    constexpr uint32_t kI1 = tc_idesc_bf16(128, 128), kI2 = tc_idesc_bf16(128, DC, false, true), kI3 = tc_idesc_bf16(128, DC);
+    auto slot = [&](int i) { return base + i % kSlots * kTile; };
+    auto wait_tile = [&](int i) { warp_wait(&full[i % kSlots], (uint32_t)(i / kSlots)); };
+    // scores of chunk m, over those of m - 1 (whose P c is done)
+    auto before = [&](int m) {
+      if (m > 0) warp_wait(&o_full, (uint32_t)m - 1u);
+      wait_tile(m * kTiles);
+    };
+    auto scores = [&](int m) {
+      const int it = m * kTiles;
+      wait_tile(it + 1);
+      tc_fence_after();
+      const uint64_t da = smem_desc_k128(slot(it)), db = smem_desc_k128(slot(it + 1));
 #pragma unroll
-        for (int kk = 0; kk < DA / 16; ++kk) {
-          const uint32_t off = (kk / 4 * kPanel + kk % 4 * 32) / 16;
-          tc_mma_bf16(tmem + kColP, da + off, db + off, kI1, kk > 0);
-        }
-        tc_commit(smem_addr(&p_full));
-      };
-      if (nchunk > 0) scores(0);
-      for (int n = 0; n < nchunk && ok; ++n) {
-        const int it = n * kTiles, ic = it + 2;
-        const uint32_t ph = (uint32_t)n;
+      for (int kk = 0; kk < DA / 16; ++kk) {
+        const uint32_t off = (kk / 4 * kPanel + kk % 4 * 32) / 16;
+        tc_mma_bf16_warp(tmem + kColP, da + off, db + off, kI1, kk > 0);
+      }
+      tc_commit_warp(smem_addr(&p_full));
+    };
+    int m = 0, left = warp_value(pieces[0].len);  // chunk of all pieces; tokens to go in this one
+    if (left > 0) {
+      before(0);
+      scores(0);
+    }
+    for (int k = 1; left > 0 && ok; ++k) {
+      for (; left > 0 && ok; left -= kC, ++m) {
+        const int it = m * kTiles, ic = it + 2;
+        const uint32_t ph = (uint32_t)m;
         const uint64_t dc = smem_desc_mn128(slot(ic), kPanel);
-        wait(&s_ready, ph);
-        wait(&o_free, ph + 1);
+        warp_wait(&s_ready, ph);
+        warp_wait(&o_free, ph + 1);
         tc_fence_after();
         const uint64_t da = smem_desc_k128(slot(it)), ds = smem_desc_k128(s_buf);
 #pragma unroll
         for (int kk = 0; kk < DA / 16; ++kk)
-          tc_mma_bf16(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
-        tc_commit(smem_addr(&empty[it % kSlots]));
-        tc_commit(smem_addr(&empty[it % kSlots]));
+          tc_mma_bf16_warp(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
+        tc_commit_warp(smem_addr(&empty[it % kSlots]));
+        tc_commit_warp(smem_addr(&empty[it % kSlots]));
         wait_tile(ic);
         // rows behind a short chunk's end are cleared with the weighted rows
-        if (chunk_len(n) < kC) wait(&b_ready, ph);
-        wait(&p_ready, ph);
+        if (left < kC) warp_wait(&b_ready, ph);
+        warp_wait(&p_ready, ph);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk)
-          tc_mma_bf16_ts(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
-        tc_commit(smem_addr(&o_full));
-        tc_commit(smem_addr(&empty[ic % kSlots]));
-        if (n + 1 < nchunk) scores(n + 1);
+          tc_mma_bf16_ts_warp(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
+        tc_commit_warp(smem_addr(&o_full));
+        tc_commit_warp(smem_addr(&empty[ic % kSlots]));
+        if (left > kC) {
+          before(m + 1);
+          scores(m + 1);
+        }
       }
+      if (!cut || !ok) break;
+      before(m);
+      left = ok ? warp_value(pieces[k % kPieces].len) : 0;
+      if (left > 0)
+        scores(m);
+      else if (ok && lane == 0)
+        mbar_arrive(smem_addr(&p_full));  // the others read of the end behind it
     }
     __syncwarp();
   } else if (warp == 18) {
-    if (lane == 0) {
-      // a warp of its own: an instruction of 128 columns takes about as long
-      // to issue as to execute, and these products wait for other things
-      constexpr uint32_t kI4 = tc_idesc_bf16(128, DA, true, true);
-      for (int n = 0; n < nchunk && ok; ++n) {
-        const int ib = n * kTiles + 1, ic = ib + 1;
-        const uint32_t ph = (uint32_t)n, b0 = base + ib % kSlots * kTile;
+    // a warp of its own: an instruction of 128 columns takes about as long
+    // to issue as to execute, and these products wait for other things
+    constexpr uint32_t kI4 = tc_idesc_bf16(128, DA, true, true);
+    int m = 0, left = warp_value(pieces[0].len);
+    for (int k = 1; left > 0 && ok; ++k) {
+      for (; left > 0 && ok; left -= kC, ++m) {
+        const int ib = m * kTiles + 1, ic = ib + 1;
+        const uint32_t ph = (uint32_t)m, b0 = base + ib % kSlots * kTile;
         const uint64_t dc = smem_desc_mn128(base + ic % kSlots * kTile, kPanel);
-        wait(&full[ic % kSlots], (uint32_t)(ic / kSlots));
-        wait(&b_ready, ph);
-        wait(&u_free, ph + 1);
+        warp_wait(&b_ready, ph);
+        warp_wait(&full[ic % kSlots], (uint32_t)(ic / kSlots));
+        warp_wait(&u_free, ph + 1);
         tc_fence_after();
         // c's channels as the 128 rows (64 channels: the other 64 rows are
         // whatever lies behind, and are not read)
@@ -284,13 +324,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int term = 0; term < TERMS; ++term) {
           const uint64_t dt = smem_desc_mn128(term == 0 ? b0 : rest + (term - 1) * (kC * DA * 2), kPanel);
 #pragma unroll
-          for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
+          for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16_warp(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
-        tc_commit(smem_addr(&u_full));
-        tc_commit(smem_addr(&empty[ib % kSlots]));
-        tc_commit(smem_addr(&empty[ib % kSlots]));
-        tc_commit(smem_addr(&empty[ic % kSlots]));
+        tc_commit_warp(smem_addr(&u_full));
+        tc_commit_warp(smem_addr(&empty[ib % kSlots]));
+        tc_commit_warp(smem_addr(&empty[ib % kSlots]));
+        tc_commit_warp(smem_addr(&empty[ic % kSlots]));
       }
+      if (!cut || !ok) break;
+      warp_wait(&b_ready, (uint32_t)m);  // of the next piece's first chunk, or of the end
+      left = ok ? warp_value(pieces[k % kPieces].len) : 0;
     }
     __syncwarp();
   } else {
@@ -298,26 +341,59 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     // a quarter, each with half of the columns
     const int quarter = warp & 3, half = warp >> 2 & 1, row = 32 * quarter + lane;
     const uint32_t lanes_at = tmem + ((uint32_t)(32 * quarter) << 16);
+    // the powers of piece k's head, where it is not the last piece's (all
+    // sixteen warps: once they are done with the old ones, each its part)
+    int meets = 0;
+    auto meet = [&] {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&t_ready));
+      warp_wait(&t_ready, meets++);
+    };
+    auto powers = [&](int k) {
+      const int head = pieces[k % kPieces].head;
+      if (k > 0) {
+        if (pieces[(k - 1) % kPieces].head == head) return;
+        meet();
+      }
+      const float g = __ldg(p.s.log_decay + head);
+      if (tid < kC + 4) {
+        const float l = decay_pow(g, tid);
+        pw[tid] = l;
+        if (tid < kC) tab[tid] = p.s.p_scale * l;
+      }
+      meet();
+    };
+    // whether there is a piece k, which chunk m begins
+    auto more = [&](int k, int m) {
+      if (!cut || !ok) return false;
+      warp_wait(&p_full, m);
+      if (!ok) return false;
+      if (pieces[k % kPieces].len > 0) return true;
+      if (lane == 0) mbar_arrive(smem_addr(&b_ready));  // the token sums' warp reads of the end behind it
+      return false;
+    };
     // b's rows times their decay, as three bf16 terms (hi over b itself)
-    auto split = [&](int n, int t0) {
-      const int len = chunk_len(n);
-      const uint32_t B = base + (n * kTiles + 1) % kSlots * kTile, Ct = base + (n * kTiles + 2) % kSlots * kTile;
+    auto split = [&](int len, int m, int t0) {
+      const uint32_t B = base + (m * kTiles + 1) % kSlots * kTile, Ct = base + (m * kTiles + 2) % kSlots * kTile;
       // thread t0's vectors of 8 channels lie in rows t0 / 8 + kStep i of each
       // panel, i < kBatch; a panel's are loaded before the first is stored
-      const float* fac = pw + p.s.shift + (rev ? 0 : len - 1);
       constexpr int kStep = 512 / 8, kBatch = kC / kStep;
       static_assert(kBatch >= 1 && kBatch * kStep == kC, "the batches cover a panel's rows once");
+      float f[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = t0 / 8 + i * kStep;
+        f[i] = p.s.up_scale * pw[p.s.shift + (rev ? j : j < len ? len - 1 - j : 0)];
+      }
 #pragma unroll 1
       for (int x = 0; x < DA / 64; ++x) {
         const int j0 = t0 / 8;
         const uint32_t at = x * kPanel + j0 * 128 + t0 % 8 * 16;
         uint4 w[kBatch];
-        float f[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
           const int j = j0 + i * kStep;
           w[i] = ld_shared_v4(B + at + i * kStep * 128);
-          f[i] = p.s.up_scale * (rev ? fac[j] : fac[j < len ? -j : 0]);
           if (j >= len) w[i] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
         }
 #pragma unroll
@@ -349,188 +425,198 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     };
 
     if (warp < 8) {
-      for (int n = 0; n < nchunk; ++n) {
-        const int len = chunk_len(n);
-        warp_wait(&p_full, n);
-        tc_fence_after();
-        // 16 columns at a time (a short loop: the warps of the roles share
-        // the instruction cache); each half's P lies over the first half of
-        // its own scores
+      int m = 0, k = 0;  // chunk of all pieces, piece
+      if (live) do {
+        powers(k);
+        const Piece& q = pieces[k % kPieces];
+        for (int left = q.len; left > 0; left -= kC, ++m) {
+          const int len = left < kC ? left : kC;
+          warp_wait(&p_full, m);
+          tc_fence_after();
+          // 16 columns at a time (a short loop: the warps of the roles share
+          // the instruction cache); each half's P lies over the first half of
+          // its own scores
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          const int j0 = half * 64 + b * 16, lo_row = 32 * quarter;
-          uint32_t w[8];
-          if (rev ? j0 + 15 < lo_row || j0 >= len : j0 > lo_row + 31) {  // empty for all of the warp's rows
+          for (int b = 0; b < 4; ++b) {
+            const int j0 = half * 64 + b * 16, lo_row = 32 * quarter;
+            uint32_t w[8];
+            if (rev ? j0 + 15 < lo_row || j0 >= len : j0 > lo_row + 31) {  // empty for all of the warp's rows
 #pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = 0;
-          } else {
-            uint32_t v[16];
-            tmem_ld16(lanes_at + kColP + j0, v);
-            // 0 where the mask is; a reversed scan's distances grow with the column
-            const float* t = tab + kC + (rev ? j0 - row : row - j0 - 15);
-            float f[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = t[k];
-            tmem_ld_wait();
-            if (rev) {
-#pragma unroll
-              for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
+              for (int k = 0; k < 8; ++k) w[k] = 0;
             } else {
+              uint32_t v[16];
+              tmem_ld16(lanes_at + kColP + j0, v);
+              // 0 where the mask is; a reversed scan's distances grow with the column
+              const float* t = tab + (rev ? j0 - row : row - j0 - 15);
+              float f[16];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float x = f[15 - k] * __uint_as_float(v[k]), y = f[k] * __uint_as_float(v[15 - k]);
-                f[k] = x;
-                f[15 - k] = y;
+              for (int k = 0; k < 16; ++k) f[k] = t[k];
+              tmem_ld_wait();
+              if (rev) {
+#pragma unroll
+                for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float x = f[15 - k] * __uint_as_float(v[k]), y = f[k] * __uint_as_float(v[15 - k]);
+                  f[k] = x;
+                  f[15 - k] = y;
+                }
+              }
+              if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
+                const int last = rev ? len : row + 1, first = rev ? row : 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
+              }
+#pragma unroll
+              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+            }
+            tmem_st8(lanes_at + kColP + half * 64 + b * 8, w);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&p_ready));
+
+          // b's weighted rows: a b^T has read b, and the last chunk's sums
+          // have read its terms
+          if (m > 0) warp_wait(&u_full, m - 1);
+          const int ib = m * kTiles + 1;
+          warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
+          if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
+          split(len, m, tid);
+
+          warp_wait(&o_full, m);
+          tc_fence_after();
+          const bool in = row < len;
+          const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
+          const float coef = in ? p.s.in_scale * pw[e] : 0.f;
+          bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(q, left) + row) * p.s.os + (long long)q.head * DC;
+          uint64_t sum = 0;  // 0, or NaN where a value is not finite
+#pragma unroll 1
+          for (int c0 = half * (DC / 2); c0 < (half + 1) * (DC / 2); c0 += 32) {
+            uint32_t x[32], y[32];
+            tmem_ld16(lanes_at + kColO1 + c0, x);
+            tmem_ld16(lanes_at + kColO2 + c0, y);
+            tmem_ld16(lanes_at + kColO1 + c0 + 16, x + 16);
+            tmem_ld16(lanes_at + kColO2 + c0 + 16, y + 16);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 16; ++k) sum = f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), 0ull, sum);
+            uint32_t w[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+              w[k] = ok ? pack_bf16x2(fmaf(coef, __uint_as_float(y[2 * k]), __uint_as_float(x[2 * k])),
+                                      fmaf(coef, __uint_as_float(y[2 * k + 1]), __uint_as_float(x[2 * k + 1])))
+                        : 0x7fc07fc0u;
+            if (in) {
+              if (p.s.wide_out) {
+                st_global_v8(out + c0, w);
+                st_global_v8(out + c0 + 16, w + 8);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  reinterpret_cast<uint4*>(out + c0)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
               }
             }
-            if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
-              const int last = rev ? len : row + 1, first = rev ? row : 0;
-#pragma unroll
-              for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
           }
-          tmem_st8(lanes_at + kColP + half * 64 + b * 8, w);
+          const bool bad = in && ok && f2_hsum(sum) != 0.f;
+          if (__any_sync(0xffffffffu, bad))
+            masked_row<DA>(p.s, tab, lanes_at + kColO2, chunk_at(q, left), q.head, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&o_free));
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&p_ready));
-
-        // b's weighted rows: a b^T has read b, and the last chunk's sums
-        // have read its terms
-        if (n > 0) warp_wait(&u_full, n - 1);
-        const int ib = n * kTiles + 1;
-        warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
-        if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
-        split(n, tid);
-
-        warp_wait(&o_full, n);
-        tc_fence_after();
-        const bool in = row < len;
-        const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
-        const float coef = in ? p.s.in_scale * pw[e] : 0.f;
-        bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(n) + row) * p.s.os + (long long)h * DC;
-        uint64_t sum = 0;  // 0, or NaN where a value is not finite
-#pragma unroll 1
-        for (int c0 = half * (DC / 2); c0 < (half + 1) * (DC / 2); c0 += 32) {
-          uint32_t x[32], y[32];
-          tmem_ld16(lanes_at + kColO1 + c0, x);
-          tmem_ld16(lanes_at + kColO2 + c0, y);
-          tmem_ld16(lanes_at + kColO1 + c0 + 16, x + 16);
-          tmem_ld16(lanes_at + kColO2 + c0 + 16, y + 16);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) sum = f2_fma(f2_pack(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), 0ull, sum);
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            w[k] = ok ? pack_bf16x2(fmaf(coef, __uint_as_float(y[2 * k]), __uint_as_float(x[2 * k])),
-                                    fmaf(coef, __uint_as_float(y[2 * k + 1]), __uint_as_float(x[2 * k + 1])))
-                      : 0x7fc07fc0u;
-          if (in) {
-            if (p.s.wide_out) {
-              st_global_v8(out + c0, w);
-              st_global_v8(out + c0 + 16, w + 8);
-            } else {
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                reinterpret_cast<uint4*>(out + c0)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-            }
-          }
-        }
-        const bool bad = in && ok && f2_hsum(sum) != 0.f;
-        if (__any_sync(0xffffffffu, bad))
-          masked_row<DA>(p.s, tab + kC, lanes_at + kColO2, chunk_at(n), h, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&o_free));
-      }
+      } while (more(++k, m));
     } else {
       // the state: a thread holds S[d0 .. d0 + DH)[row]
       constexpr int DH = DA / 2;
       const int d0 = half * DH;
       float S[DH];
-      const long long st = ((long long)(p.s.seg_state ? seg_i : sg.seq) * p.s.H + h) * DA * DC;
-      const float* from = p.s.seg_state ? p.s.seg_state : p.s.s_in;
-      const bool mine = row < DC && live;
-      if (from && mine) {
-        if (p.s.transposed) {
+      const float* from = cut ? p.s.piece_state : p.s.s_in;
+      int m = 0, k = 0;
+      if (live) do {
+        powers(k);
+        const Piece& q = pieces[k % kPieces];
+        const long long st = (cut ? q.id : (long long)q.seq * p.s.H + q.head) * DA * DC;
+        if (from && row < DC) {
+          if (p.s.transposed) {
 #pragma unroll
-          for (int d = 0; d < DH; d += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(from + st + (long long)row * DA + d0 + d);
-            S[d] = v.x, S[d + 1] = v.y, S[d + 2] = v.z, S[d + 3] = v.w;
+            for (int d = 0; d < DH; d += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(from + st + (long long)row * DA + d0 + d);
+              S[d] = v.x, S[d + 1] = v.y, S[d + 2] = v.z, S[d + 3] = v.w;
+            }
+          } else {
+#pragma unroll
+            for (int d = 0; d < DH; ++d) S[d] = from[st + (d0 + d) * DC + row];
           }
         } else {
 #pragma unroll
-          for (int d = 0; d < DH; ++d) S[d] = from[st + (d0 + d) * DC + row];
+          for (int d = 0; d < DH; ++d) S[d] = 0.f;
         }
-      } else {
+        // S rounded to bf16 for a S: 8 values of this thread's row, [DC rows][DA]
+        // in the 128-byte swizzle
+        auto put = [&](int d) {
+          const int at = d0 + d;
+          if (row < DC)
+            st_shared_v4(s_buf + at / 64 * (DC * 128) + row * 128 + (((at / 8) ^ row) & 7) * 16, pack_bf16x2(S[d], S[d + 1]),
+                         pack_bf16x2(S[d + 2], S[d + 3]), pack_bf16x2(S[d + 4], S[d + 5]), pack_bf16x2(S[d + 6], S[d + 7]));
+        };
+        // ready for chunk m, whose scores this warp sees first: the next ones
+        // follow on this, so that it cannot miss a phase of p_full
+        auto put_done = [&](int m) {
+          fence_proxy_async_smem();
+          warp_wait(&p_full, m);
+          if (lane == 0) mbar_arrive(smem_addr(&s_ready));
+        };
+        if (q.len > 0) {
 #pragma unroll
-        for (int d = 0; d < DH; ++d) S[d] = 0.f;
-      }
-      // S rounded to bf16 for a S: 8 values of this thread's row, [DC rows][DA]
-      // in the 128-byte swizzle
-      auto put = [&](int d) {
-        const int at = d0 + d;
-        if (row < DC)
-          st_shared_v4(s_buf + at / 64 * (DC * 128) + row * 128 + (((at / 8) ^ row) & 7) * 16, pack_bf16x2(S[d], S[d + 1]),
-                       pack_bf16x2(S[d + 2], S[d + 3]), pack_bf16x2(S[d + 4], S[d + 5]), pack_bf16x2(S[d + 6], S[d + 7]));
-      };
-      auto put_done = [&] {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&s_ready));
-      };
-      if (nchunk > 0) {
+          for (int d = 0; d < DH; d += 8) put(d);
+          put_done(m);
+        }
+        for (int left = q.len; left > 0; left -= kC, ++m) {
+          // this group's half of b's weighted rows
+          const int ib = m * kTiles + 1, len = left < kC ? left : kC;
+          warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
+          if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
+          split(len, m, tid);
+          const float decay = pw[len];
+          warp_wait(&u_full, m);
+          warp_wait(&o_full, m);  // a S has read the state before
+          tc_fence_after();
+          const bool next = left > kC;
 #pragma unroll
-        for (int d = 0; d < DH; d += 8) put(d);
-        put_done();
-      }
-      for (int n = 0; n < nchunk; ++n) {
-        // this group's half of b's weighted rows
-        const int ib = n * kTiles + 1, len = chunk_len(n);
-        warp_wait(&p_full, n);
-        warp_wait(&full[ib % kSlots], (uint32_t)(ib / kSlots));
-        if (len < kC) warp_wait(&full[(ib + 1) % kSlots], (uint32_t)((ib + 1) / kSlots));
-        split(n, tid);
-        const float decay = expf(g * (float)len);
-        warp_wait(&u_full, n);
-        warp_wait(&o_full, n);  // a S has read the state before
-        tc_fence_after();
-        const bool next = n + 1 < nchunk;
+          for (int d = 0; d < DH; d += 16) {
+            uint32_t v[16];
+            tmem_ld16(lanes_at + kColU + d0 + d, v);
+            tmem_ld_wait();
 #pragma unroll
-        for (int d = 0; d < DH; d += 16) {
-          uint32_t v[16];
-          tmem_ld16(lanes_at + kColU + d0 + d, v);
-          tmem_ld_wait();
+            for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]));
+            if (next) {
+              put(d);
+              put(d + 8);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&u_free));
+          if (next) put_done(m + 1);
+        }
+        // the state behind a sequence in one piece (others: joined before)
+        if (row < DC && p.s.s_out && !cut) {
+          float* to = p.s.s_out + st;
+          const float nan = __int_as_float(0x7fc00000);
+          if (p.s.transposed) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]));
-          if (next) {
-            put(d);
-            put(d + 8);
+            for (int d = 0; d < DH; d += 4)
+              *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
+                  ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
+          } else {
+#pragma unroll
+            for (int d = 0; d < DH; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&u_free));
-        if (next) put_done();
-      }
-      // the state behind a sequence in one piece (segments: joined before)
-      if (mine && p.s.s_out && !p.s.seg_state) {
-        float* to = p.s.s_out + st;
-        const float nan = __int_as_float(0x7fc00000);
-        if (p.s.transposed) {
-#pragma unroll
-          for (int d = 0; d < DH; d += 4)
-            *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
-                ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
-        } else {
-#pragma unroll
-          for (int d = 0; d < DH; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
-        }
-      }
+      } while (more(++k, m));
     }
   }
   tc_fence_before();
@@ -541,19 +627,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   }
 }
 
-// Every segment's own state, sum_j l^{len-1-j} b_j c_j^T over its tokens, in
+// Every piece's own state, sum_j l^{len-1-j} b_j c_j^T over its tokens, in
 // half chunks of 64 tokens: while the tensor cores take one half, eight warps
 // weigh the rows of the next and eight others those of the one behind it
 // (each group has its buffer of terms, and its latencies fall into the
 // other's arithmetic), and all sixteen add the last whole chunk's sums, from
 // one of two accumulators in TMEM, to the state (a quarter of a row of DA per
-// thread).  The first two terms lie one
-// behind the other and form one operand of 2 DA columns with sums of their
-// own, to which the third term's are added: two instructions per 16 tokens
-// instead of three, which matters because issuing one takes as long as 128
-// columns take to execute.  One barrier per stage says that a half's products
-// are done: to the loads, to the terms' next writers and to the sums' readers.
-// The bound is HBM.
+// thread).  The first two terms lie one behind the other and form one operand
+// of 2 DA columns with sums of their own, to which the third term's are
+// added: two instructions per 16 tokens instead of three, which matters
+// because issuing one takes as long as 128 columns take to execute.  One
+// barrier per stage says that a half's products are done: to the loads, to
+// the terms' next writers and to the sums' readers.  The bound is HBM.
 constexpr int kHalfPanel = kHalf * 128;  // bytes of 64 channels of a half chunk
 
 template <int DA, int DC>
@@ -563,12 +648,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxSlots], done[kMaxSlots], b_ready[2], u_free[2];
   __shared__ uint32_t tmem_base;
-  __shared__ float pw[kC + 2];  // l^i
+  __shared__ Piece pieces[kPieces];
   // stages (b, c), then two buffers of three terms (which an operand of 64
   // channels reads into behind the last stage: rows of its product not used)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + kSlots * kStage;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int h = blockIdx.x % p.s.H, seg_i = blockIdx.x / p.s.H;
+  const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -585,21 +669,24 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = warp_value(tmem_base);
   pdl_wait();
   pdl_trigger();
-  const float g = __ldg(p.s.log_decay + h);
-  if (tid < kC + 2) pw[tid] = decay_pow(g, tid);
-  __syncthreads();
-  Segment sg{0, 0, 0, 1};
-  if (!p.s.nsegs || seg_i < *p.s.nsegs) sg = segment_of(p.s, seg_i);
-  const bool work = sg.len > 0 && !(sg.last && !p.s.s_out);  // a last segment's own state is part of the final one only
-  const int nchunk = work ? (sg.len + kC - 1) / kC : 0;
   const bool rev = p.s.reverse;
-  auto chunk_len = [&](int n) { return sg.len - n * kC < kC ? sg.len - n * kC : kC; };
-  auto chunk_at = [&](int n) { return rev ? sg.first + sg.len - n * kC - chunk_len(n) : sg.first + n * kC; };
-  // halves: two per chunk, one where the last chunk has at most 64 tokens
-  const int nhalf = nchunk > 0 ? 2 * nchunk - (chunk_len(nchunk - 1) <= kHalf ? 1 : 0) : 0;
+  PieceWalk walk(p.s, blockIdx.x);
+  Piece pc;
+  // the next piece that has a state of its own: a last one's is part of the
+  // final state only
+  auto step = [&] {
+    do {
+      if (!walk.next(p.s, blockIdx.x, &pc)) return false;
+    } while (pc.last && !p.s.s_out);
+    return true;
+  };
+  bool live = step();
+  int nchunk = live ? (pc.len + kC - 1) / kC : 0;
+  auto chunk_len = [&](int n) { return pc.len - n * kC < kC ? pc.len - n * kC : kC; };
+  auto chunk_at = [&](int n) { return rev ? pc.first + pc.len - n * kC - chunk_len(n) : pc.first + n * kC; };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (ok && !mbar_wait_bounded(smem_addr(bar), parity & 1u, p.wait_ns)) {
@@ -614,17 +701,34 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
 
   if (warp == 16) {
     if (lane == 0) {
-      int i = 0;
-      for (; i < nhalf; ++i) {
-        const int st = i % kSlots, t = chunk_at(i / 2) + i % 2 * kHalf;
-        wait(&done[st], (uint32_t)(i / kSlots) + 1u);
-        if (!ok) break;
-        const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
-        mbar_arrive_expect_tx(fb, kStage);
+      int i = 0;  // half of all pieces
+      for (int k = 1; ok; ++k) {
+        for (int n = 0; n < 2 * nchunk; ++n, ++i) {
+          const int st = i % kSlots, t = chunk_at(n / 2) + n % 2 * kHalf;
+          wait(&done[st], (uint32_t)(i / kSlots) + 1u);
+          if (!ok) break;
+          const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
+          mbar_arrive_expect_tx(fb, kStage);
 #pragma unroll
-        for (int x = 0; x < DA; x += 64) tma_load_2d(to + x / 64 * kHalfPanel, &p.mb, h * DA + x, t, fb);
+          for (int x = 0; x < DA; x += 64) tma_load_2d(to + x / 64 * kHalfPanel, &p.mb, pc.head * DA + x, t, fb);
 #pragma unroll
-        for (int x = 0; x < DC; x += 64) tma_load_2d(to + kTileB + x / 64 * kHalfPanel, &p.mc, h * DC + x, t, fb);
+          for (int x = 0; x < DC; x += 64) tma_load_2d(to + kTileB + x / 64 * kHalfPanel, &p.mc, pc.head * DC + x, t, fb);
+        }
+        if (!live || !ok) break;
+        // the next piece, which its first halves' barriers publish; behind
+        // the last two barriers of no bytes
+        live = step();
+        if (!live) pc.len = 0;
+        nchunk = (pc.len + kC - 1) / kC;
+        pieces[k % kPieces] = pc;
+        if (!live) {
+          for (int e = 0; e < 2; ++e, ++i) {
+            wait(&done[i % kSlots], (uint32_t)(i / kSlots) + 1u);
+            if (!ok) break;
+            mbar_arrive(smem_addr(&full[i % kSlots]));
+          }
+          break;
+        }
       }
       // the CTA never exits under a copy
       const int armed = i < kSlots ? i : kSlots;
@@ -632,23 +736,28 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     }
     __syncwarp();
   } else if (warp == 17) {
-    if (lane == 0) {
-      constexpr uint32_t kI2 = tc_idesc_bf16(128, 2 * DA, true, true), kI1 = tc_idesc_bf16(128, DA, true, true);
-      for (int i = 0; i < nhalf && ok; ++i) {
+    constexpr uint32_t kI2 = tc_idesc_bf16(128, 2 * DA, true, true), kI1 = tc_idesc_bf16(128, DA, true, true);
+    nchunk = warp_value(nchunk);
+    int i = 0;
+    for (int k = 1; nchunk > 0 && ok; ++k) {
+      for (int end = i + 2 * nchunk; i < end && ok; ++i) {
         const int st = i % kSlots, n = i / 2;
         const uint32_t d = tmem + (n & 1) * kColU, more = i % 2;
         const uint64_t dc = smem_desc_mn128(base + st * kStage + kTileB, kHalfPanel);
         const uint64_t dt = smem_desc_mn128(rest + (i & 1) * 3 * kTileB, kHalfPanel);
-        wait(&b_ready[i & 1], (uint32_t)(i / 2));
-        if (i % 2 == 0) wait(&u_free[n & 1], (uint32_t)(n / 2) + 1u);
+        warp_wait(&b_ready[i & 1], (uint32_t)(i / 2));
+        if (i % 2 == 0) warp_wait(&u_free[n & 1], (uint32_t)(n / 2) + 1u);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < kHalf / 16; ++kk) {
-          tc_mma_bf16(d, dc + kk * 128, dt + kk * 128, kI2, kk > 0 ? 1u : more);
-          tc_mma_bf16(d + DA, dc + kk * 128, dt + 2 * kTileB / 16 + kk * 128, kI1, 1u);
+          tc_mma_bf16_warp(d, dc + kk * 128, dt + kk * 128, kI2, kk > 0 ? 1u : more);
+          tc_mma_bf16_warp(d + DA, dc + kk * 128, dt + 2 * kTileB / 16 + kk * 128, kI1, 1u);
         }
-        tc_commit(smem_addr(&done[st]));
+        tc_commit_warp(smem_addr(&done[st]));
       }
+      warp_wait(&b_ready[0], (uint32_t)(i / 2));  // of the next piece's first half, or of the end
+      pc.len = warp_value(pieces[k % kPieces].len);
+      nchunk = ok ? (pc.len + kC - 1) / kC : 0;
     }
     __syncwarp();
   } else {
@@ -659,86 +768,98 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     float S[DQ];
 #pragma unroll
     for (int d = 0; d < DQ; ++d) S[d] = 0.f;
-    auto add = [&](int n) {
-      const float decay = expf(g * (float)chunk_len(n));
-      const int i = 2 * n + 1 < nhalf ? 2 * n + 1 : nhalf - 1;  // the chunk's last half
+    float g = 0.f;
+    // chunk n of the piece, m of all
+    auto add = [&](int n, int m) {
+      const float decay = decay_pow(g, chunk_len(n));
+      const int i = 2 * m + 1;  // its last half
       warp_wait(&done[i % kSlots], (uint32_t)(i / kSlots));
       tc_fence_after();
 #pragma unroll
       for (int d = 0; d < DQ; d += 16) {
         uint32_t v[16], w[16];
-        tmem_ld16(from + (n & 1) * kColU + d, v);
-        tmem_ld16(from + (n & 1) * kColU + DA + d, w);
+        tmem_ld16(from + (m & 1) * kColU + d, v);
+        tmem_ld16(from + (m & 1) * kColU + DA + d, w);
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 16; ++k) S[d + k] = fmaf(S[d + k], decay, __uint_as_float(v[k]) + __uint_as_float(w[k]));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&u_free[n & 1]));
+      if (lane == 0) mbar_arrive(smem_addr(&u_free[m & 1]));
     };
     const int group = warp >> 3, tg = tid & 255;
-    for (int i = group; i < nhalf; i += 2) {
-      const int st = i % kSlots, len = chunk_len(i / 2), j0 = group * kHalf;  // rows j0 .. of the chunk
-      const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + group * 3 * kTileB;
-      warp_wait(&full[st], (uint32_t)(i / kSlots));
-      if (i >= 2) warp_wait(&done[(i - 2) % kSlots], (uint32_t)((i - 2) / kSlots));  // the terms' last readers
-      // vectors of 8 channels: rows tg / 8 and 32 further of every panel of 64
-      constexpr int kVecs = 2 * DA / 64;
-      float f[2];
-      uint4 w[kVecs];
+    int m = 0;  // chunk of all pieces
+    for (int k = 1; nchunk > 0 && ok; ++k) {
+      g = __ldg(p.s.log_decay + pc.head);
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int j = j0 + tg / 8 + 32 * r;
-        f[r] = j < len ? p.s.up_scale * pw[p.s.shift + (rev ? j : len - 1 - j)] : 0.f;
+      for (int d = 0; d < DQ; ++d) S[d] = 0.f;
+      for (int n = 0; n < nchunk; ++n, ++m) {
+        const int i = 2 * m + group, st = i % kSlots, len = chunk_len(n), j0 = group * kHalf;  // rows j0 .. of the chunk
+        const uint32_t B = base + st * kStage, Ct = B + kTileB, T = rest + group * 3 * kTileB;
+        warp_wait(&full[st], (uint32_t)(i / kSlots));
+        if (i >= 2) warp_wait(&done[(i - 2) % kSlots], (uint32_t)((i - 2) / kSlots));  // the terms' last readers
+        // vectors of 8 channels: rows tg / 8 and 32 further of every panel of 64
+        constexpr int kVecs = 2 * DA / 64;
+        float f[2];
+        uint4 w[kVecs];
 #pragma unroll
-        for (int x = 0; x < DA / 64; ++x) {
-          const int v = r * (DA / 64) + x;
-          w[v] = ld_shared_v4(B + x * kHalfPanel + r * 4096 + tg * 16);
-          if (j >= len) w[v] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+        for (int r = 0; r < 2; ++r) {
+          const int j = j0 + tg / 8 + 32 * r;
+          f[r] = j < len ? p.s.up_scale * decay_pow(g, p.s.shift + (rev ? j : len - 1 - j)) : 0.f;
+#pragma unroll
+          for (int x = 0; x < DA / 64; ++x) {
+            const int v = r * (DA / 64) + x;
+            w[v] = ld_shared_v4(B + x * kHalfPanel + r * 4096 + tg * 16);
+            if (j >= len) w[v] = make_uint4(0, 0, 0, 0);  // behind the chunk's end: another chunk's or sequence's row
+          }
+          if (j >= len) {
+#pragma unroll
+            for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kHalfPanel + r * 4096 + tg * 16, 0, 0, 0, 0);
+          }
         }
-        if (j >= len) {
 #pragma unroll
-          for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kHalfPanel + r * 4096 + tg * 16, 0, 0, 0, 0);
+        for (int v = 0; v < kVecs; ++v) {
+          const uint32_t at = v % (DA / 64) * kHalfPanel + v / (DA / 64) * 4096 + tg * 16, in[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
+          const float fv = f[v / (DA / 64)];
+          uint32_t th[4], tm[4], tl[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float a = bf16lo(in[k]) * fv, b = bf16hi(in[k]) * fv;
+            th[k] = pack_bf16x2(a, b);
+            const float a1 = a - bf16lo(th[k]), b1 = b - bf16hi(th[k]);
+            tm[k] = pack_bf16x2(a1, b1);
+            tl[k] = pack_bf16x2(a1 - bf16lo(tm[k]), b1 - bf16hi(tm[k]));
+          }
+          st_shared_v4(T + at, th[0], th[1], th[2], th[3]);
+          st_shared_v4(T + kTileB + at, tm[0], tm[1], tm[2], tm[3]);
+          st_shared_v4(T + 2 * kTileB + at, tl[0], tl[1], tl[2], tl[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&b_ready[group]));
+        if (n > 0) add(n - 1, m - 1);
+      }
+      add(nchunk - 1, m - 1);
+      if (row < DC) {
+        float* to = p.s.piece_state + (long long)pc.id * DA * DC;
+        const float nan = __int_as_float(0x7fc00000);
+        if (p.s.transposed) {
+#pragma unroll
+          for (int d = 0; d < DQ; d += 4)
+            *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
+                ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
+        } else {
+#pragma unroll
+          for (int d = 0; d < DQ; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
         }
       }
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v) {
-        const uint32_t at = v % (DA / 64) * kHalfPanel + v / (DA / 64) * 4096 + tg * 16, in[4] = {w[v].x, w[v].y, w[v].z, w[v].w};
-        const float fv = f[v / (DA / 64)];
-        uint32_t th[4], tm[4], tl[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float a = bf16lo(in[k]) * fv, b = bf16hi(in[k]) * fv;
-          th[k] = pack_bf16x2(a, b);
-          const float a1 = a - bf16lo(th[k]), b1 = b - bf16hi(th[k]);
-          tm[k] = pack_bf16x2(a1, b1);
-          tl[k] = pack_bf16x2(a1 - bf16lo(tm[k]), b1 - bf16hi(tm[k]));
-        }
-        st_shared_v4(T + at, th[0], th[1], th[2], th[3]);
-        st_shared_v4(T + kTileB + at, tm[0], tm[1], tm[2], tm[3]);
-        st_shared_v4(T + 2 * kTileB + at, tl[0], tl[1], tl[2], tl[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&b_ready[group]));
-      if (i > 1) add(i / 2 - 1);
-    }
-    // a last chunk of one half left the second group one chunk behind
-    if (group == 1 && nhalf % 2 == 1 && nchunk > 1) add(nchunk - 2);
-    if (nchunk > 0) add(nchunk - 1);
-    if (work && row < DC) {
-      float* to = p.s.seg_state + ((long long)seg_i * p.s.H + h) * DA * DC;
-      const float nan = __int_as_float(0x7fc00000);
-      if (p.s.transposed) {
-#pragma unroll
-        for (int d = 0; d < DQ; d += 4)
-          *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
-              ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
-      } else {
-#pragma unroll
-        for (int d = 0; d < DQ; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
-      }
+      // the next piece, in its first chunk's half of this group
+      const int i = 2 * m + group;
+      warp_wait(&full[i % kSlots], (uint32_t)(i / kSlots));
+      pc = pieces[k % kPieces];
+      nchunk = ok ? (pc.len + kC - 1) / kC : 0;
+      if (ok && nchunk == 0 && lane == 0) mbar_arrive(smem_addr(&b_ready[group]));  // the products' warp reads of the end behind it
     }
   }
   tc_fence_before();
@@ -750,37 +871,37 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
 }
 
 template <int DA, int DC, int TERMS>
-cudaError_t launch_scan_tile(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+cudaError_t launch_scan_tile(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
   constexpr int kBytes = ScanSmem<DA, DC, TERMS>::kBytes;
   if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
   const auto kern = scan_tc_kernel<DA, DC, TERMS>;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kScanThreads), (size_t)kBytes, stream, p);
+  return launch_kernel(kern, dim3((unsigned)(p.s.parts > 0 ? p.s.parts * p.s.gang : p.s.N * p.s.H)), dim3(kScanThreads), (size_t)kBytes, stream, p);
 }
 
 template <int TERMS>
-cudaError_t launch_scan_dims(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+cudaError_t launch_scan_dims(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
   if (p.s.Da == 128)
-    return p.s.Dc == 128 ? launch_scan_tile<128, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<128, 64, TERMS>(p, segs, di, stream);
-  return p.s.Dc == 128 ? launch_scan_tile<64, 128, TERMS>(p, segs, di, stream) : launch_scan_tile<64, 64, TERMS>(p, segs, di, stream);
+    return p.s.Dc == 128 ? launch_scan_tile<128, 128, TERMS>(p, di, stream) : launch_scan_tile<128, 64, TERMS>(p, di, stream);
+  return p.s.Dc == 128 ? launch_scan_tile<64, 128, TERMS>(p, di, stream) : launch_scan_tile<64, 64, TERMS>(p, di, stream);
 }
 
 template <int DA, int DC>
-cudaError_t launch_state_tile(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
+cudaError_t launch_state_tile(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
   constexpr int kBytes = StateSmem<DA, DC>::kBytes;
   if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
   const auto kern = state_tc_kernel<DA, DC>;
   const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(segs * p.s.H)), dim3(kTileThreads), (size_t)kBytes, stream, p);
+  return launch_kernel(kern, dim3((unsigned)(p.s.parts * p.s.gang)), dim3(kTileThreads), (size_t)kBytes, stream, p);
 }
 
-cudaError_t launch_state_dims(const ScanTcParams& p, int64_t segs, const DeviceInfo& di, cudaStream_t stream) {
-  if (p.s.Da == 128) return p.s.Dc == 128 ? launch_state_tile<128, 128>(p, segs, di, stream) : launch_state_tile<128, 64>(p, segs, di, stream);
-  return p.s.Dc == 128 ? launch_state_tile<64, 128>(p, segs, di, stream) : launch_state_tile<64, 64>(p, segs, di, stream);
+cudaError_t launch_state_dims(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
+  if (p.s.Da == 128) return p.s.Dc == 128 ? launch_state_tile<128, 128>(p, di, stream) : launch_state_tile<128, 64>(p, di, stream);
+  return p.s.Dc == 128 ? launch_state_tile<64, 128>(p, di, stream) : launch_state_tile<64, 64>(p, di, stream);
 }
 
 bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_t stride, int tokens = kC) {
@@ -794,24 +915,27 @@ bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_
 
 bool scan_tc_dims(int Dk, int Dv, int dtype) { return dtype == ATTNRES_BF16 && (Dk == 64 || Dk == 128) && (Dv == 64 || Dv == 128); }
 
-static int scan_tc_segment(int64_t T, int H, int N, int sm_count) { return seg_tokens(T, N, kC, H, sm_count, 0.5); }
+// (a chunk's HBM time on one of 152 SMs is 23 ns per channel)
+static Cut scan_tc_cut(int64_t T, int H, int Dk, int Dv, int N, int sm_count) {
+  return choose_cut(T, H, Dk, Dv, N, kC, 1, sm_count, 0.55, 23. * (Dk > Dv ? Dk : Dv));
+}
 
-bool scan_tc_segmented(int64_t T, int H, int N) {
+bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N) {
   DeviceInfo di;
-  return device_info(&di) == cudaSuccess && scan_tc_segment(T, H, N, di.sm_count) > 0;
+  return device_info(&di) == cudaSuccess && scan_tc_cut(T, H, Dk, Dv, N, di.sm_count).parts > 0;
 }
 
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return seg_layout(T, H, Dk, Dv, N, scan_tc_segment(T, H, N, di.sm_count)).total;
+  return piece_layout(H, Dk, Dv, N, scan_tc_cut(T, H, Dk, Dv, N, di.sm_count)).total;
 }
 
 bool scan_tc_ok(const ScanArgs& s) {
   auto rows = [](const void* p, long long stride) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && stride % 8 == 0; };
   auto state = [](const float* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
   return rows(s.a, s.as) && rows(s.b, s.bs) && rows(s.c, s.cs) && rows(s.out, s.os) && state(s.s_in) && state(s.s_out) && s.T > 0 &&
-         s.T * 2 < INT32_MAX && ((s.T + kC - 1) / kC + s.N) * s.H < INT32_MAX;
+         s.T * 2 < INT32_MAX && (int64_t)s.N * s.H < INT32_MAX;
 }
 
 cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream) {
@@ -826,20 +950,22 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready
     return cudaErrorInvalidValue;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
-  p.s.seg_len = scan_tc_segment(s.T, s.H, s.N, di.sm_count);
-  int64_t segs;
-  seg_place(p.s, seg_layout(s.T, s.H, s.Da, s.Dc, s.N, p.s.seg_len), workspace, &segs);
-  if (p.s.seg_len > 0 && !states_ready) {
-    e = launch_seg_plan(p.s, stream);
+  p.s.chunk = kC;
+  const Cut cut = scan_tc_cut(s.T, s.H, s.Da, s.Dc, s.N, di.sm_count);
+  p.s.parts = cut.parts;
+  p.s.gang = cut.gang;
+  if (p.s.parts > 0) piece_place(p.s, piece_layout(s.H, s.Da, s.Dc, s.N, cut), workspace);
+  if (p.s.parts > 0 && !states_ready) {
+    e = launch_piece_plan(p.s, stream);
     if (e != cudaSuccess) return e;
     ScanTcParams ps = p;
     if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))
       return cudaErrorInvalidValue;
-    e = launch_state_dims(ps, segs, di, stream);
-    if (e == cudaSuccess) e = launch_seg_combine(p.s, stream);
+    e = launch_state_dims(ps, di, stream);
+    if (e == cudaSuccess) e = launch_piece_combine(p.s, stream);
     if (e != cudaSuccess) return e;
   }
-  return s.s_out && p.s.seg_len == 0 ? launch_scan_dims<3>(p, segs, di, stream) : launch_scan_dims<2>(p, segs, di, stream);
+  return s.s_out && p.s.parts == 0 ? launch_scan_dims<3>(p, di, stream) : launch_scan_dims<2>(p, di, stream);
 }
 
 }  // namespace attnres
