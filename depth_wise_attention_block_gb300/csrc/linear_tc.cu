@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], split[FUSED ? kMaxStages : 1], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
   const int rank = SWAP && p.ksplit > 1 ? (int)cluster_ctarank() : 0;
   const int ntiles = p.tiles_l * p.tiles_c;
   const int tile0 = SWAP ? blockIdx.x / p.ksplit : blockIdx.x, tstep = SWAP ? ntiles : gridDim.x;
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = warp_value(tmem_base);
   pdl_wait();
   pdl_trigger();
 
@@ -373,65 +373,63 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // descriptors of the first stage; a stage, a plane and 16 steps further
-      // are additions to the address field (units of 16 bytes)
-      const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + NP * p.plane_a, p.b_mn, 0);
-      const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2, pa = p.plane_a / 16, pb = p.plane_b / 16;
-      RingPos r;
-      int g = 0;
-      bool ok = true;
-      for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
-        for (int kb = kb0; kb < kb1 && ok; ++g) {
-          const int end = kb + group < kb1 ? kb + group : kb1;
-          const int buf = g & 1;
-          if (!mbar_wait_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns)) {
+    // descriptors of the first stage; a stage, a plane and 16 steps further
+    // are additions to the address field (units of 16 bytes)
+    const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + NP * p.plane_a, p.b_mn, 0);
+    const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2, pa = p.plane_a / 16, pb = p.plane_b / 16;
+    RingPos r;
+    int g = 0;
+    bool ok = true;
+    for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
+      for (int kb = kb0; kb < kb1 && ok; ++g) {
+        const int end = kb + group < kb1 ? kb + group : kb1;
+        const int buf = g & 1;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns))) {
+          report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + buf * p.acc_cols, d1 = d + p.acc_cols / 2;
+        uint32_t acc = 0;
+        for (; kb < end; ++kb) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns) &&
+                                           (!FUSED || mbar_wait_bounded(smem_addr(&split[r.st]), r.lap, p.wait_ns)))) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + buf * p.acc_cols, d1 = d + p.acc_cols / 2;
-          uint32_t acc = 0;
-          for (; kb < end; ++kb) {
-            if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns) ||
-                (FUSED && !mbar_wait_bounded(smem_addr(&split[r.st]), r.lap, p.wait_ns))) {
-              report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t at = r.st * (p.stage_bytes / 16);
-            const uint64_t da = da0 + at, db = db0 + at;
-            if (NP == 3 && p.stacked) {
+          const uint32_t at = r.st * (p.stage_bytes / 16);
+          const uint64_t da = da0 + at, db = db0 + at;
+          if (NP == 3 && p.stacked) {
 #pragma unroll
-              for (int kk = 0; kk < kKB / 16; ++kk) {
-                const uint64_t a = da + kk * sa, b = db + kk * sb;
-                tc_mma_bf16(d, a, b, p.idesc3, acc);                    // hi (hi, mid, lo)
-                tc_mma_bf16(d + p.bn, a + pa, b, p.idesc2, 1u);         // mid (hi, mid)
-                tc_mma_bf16(d + 2 * p.bn, a + 2 * pa, b, p.idesc, 1u);  // lo hi
-                acc = 1;
-              }
-            } else {
-#pragma unroll
-              for (int kk = 0; kk < kKB / 16; ++kk) {
-                const uint64_t a = da + kk * sa, b = db + kk * sb;
-                tc_mma_bf16(d, a, b, p.idesc, acc);
-                if constexpr (NP == 3) {
-                  tc_mma_bf16(d1, a, b + 2 * pb, p.idesc, acc);
-                  tc_mma_bf16(d1, a + 2 * pa, b, p.idesc, 1u);
-                  tc_mma_bf16(d1, a + pa, b + pb, p.idesc, 1u);
-                  tc_mma_bf16(d1, a, b + pb, p.idesc, 1u);
-                  tc_mma_bf16(d1, a + pa, b, p.idesc, 1u);
-                }
-                acc = 1;
-              }
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              const uint64_t a = da + kk * sa, b = db + kk * sb;
+              tc_mma_bf16_warp(d, a, b, p.idesc3, acc);                    // hi (hi, mid, lo)
+              tc_mma_bf16_warp(d + p.bn, a + pa, b, p.idesc2, 1u);         // mid (hi, mid)
+              tc_mma_bf16_warp(d + 2 * p.bn, a + 2 * pa, b, p.idesc, 1u);  // lo hi
+              acc = 1;
             }
-            tc_commit(smem_addr(&empty[r.st]));
-            r.next(p.stages);
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              const uint64_t a = da + kk * sa, b = db + kk * sb;
+              tc_mma_bf16_warp(d, a, b, p.idesc, acc);
+              if constexpr (NP == 3) {
+                tc_mma_bf16_warp(d1, a, b + 2 * pb, p.idesc, acc);
+                tc_mma_bf16_warp(d1, a + 2 * pa, b, p.idesc, 1u);
+                tc_mma_bf16_warp(d1, a + pa, b + pb, p.idesc, 1u);
+                tc_mma_bf16_warp(d1, a, b + pb, p.idesc, 1u);
+                tc_mma_bf16_warp(d1, a + pa, b, p.idesc, 1u);
+              }
+              acc = 1;
+            }
           }
-          tc_commit(smem_addr(&acc_full[buf]));
+          tc_commit_warp(smem_addr(&empty[r.st]));
+          r.next(p.stages);
         }
+        tc_commit_warp(smem_addr(&acc_full[buf]));
       }
     }
     __syncwarp();
