@@ -620,18 +620,21 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// (by a whole warp)
 __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "{\n\t.reg .pred p, q;\n\telect.sync _|q, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // one arrival at `bar` of both CTAs once the MMAs issued so far are done
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-               "h"((uint16_t)3)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
@@ -659,8 +662,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
   __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   __shared__ uint32_t tmem_base;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_ctarank();
+  const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
+  const int rank = warp_value((int)cluster_ctarank());
   const int ntiles = p.tiles_l * p.tiles_c, tile0 = blockIdx.x / 2, tstep = gridDim.x / 2;
 
   if (tid == 0) {
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
   __syncthreads();
   cluster_sync_all();  // both CTAs' barriers are there
   tc_fence_after();
-  const uint32_t tmem = tmem_base;
+  const uint32_t tmem = warp_value(tmem_base);
   pdl_wait();
   pdl_trigger();
 
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       const uint64_t da0 = plane_desc(base, p.a_mn, 0), db0 = plane_desc(base + kPairBlock / 2, p.b_mn, 0);
       const uint32_t sa = p.a_mn ? 128 : 2, sb = p.b_mn ? 128 : 2;  // 16 contraction steps, in units of 16 bytes
       RingPos r;
@@ -732,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
       bool ok = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep, ++g) {
         const int buf = g & 1;
-        if (!mbar_wait_cluster_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns))) {
           report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
           break;
         }
@@ -740,7 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
         const uint32_t d = tmem + buf * kPairN;
         uint32_t acc = 0;
         for (int kb = 0; kb < p.kblocks; kb += 2) {
-          if (!mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_bounded(smem_addr(&full[r.st]), r.lap, p.wait_ns))) {
             report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
             ok = false;
             break;
