@@ -929,14 +929,22 @@ TcPlan tc_plan(int64_t M, int N, int64_t K, int np, int sm_count) {
   const int64_t kblocks = up(K, kKB) / kKB;
   const int bn_max = np == 3 ? 128 : 256;
   double cost = 1e300;
-  // All in nanoseconds.  Whole waves of tiles: an instruction of a single
-  // tile of 256 columns takes about 130 (L2), of 128 or fewer about 68, of a
-  // pair's tile 70; then the start and end of a tile's pipeline.
+  // All in nanoseconds.  Whole waves of tiles, of as many columns as make the
+  // waves even: an instruction of a single tile of 256 columns takes about 130
+  // (L2), of 128 or fewer about 68, of a pair's tile 70; then the start and
+  // end of a tile's pipeline.  With few rows the loads are the bound: an SM
+  // gets 80 bytes per ns with the 192 KB it keeps in flight, all of them 6500
+  // (64 x 21504 x 7168: 57 us in 84 tiles of 256 columns, 51 in 150 of 144).
   constexpr double kTileNs = 800, kLaunchNs = 800;
-  for (int bn = 64; bn <= bn_max; bn *= 2) {
-    const int64_t tiles = up(M, kLanes) / kLanes * (up(N, bn) / bn);
-    const double tile = (double)kblocks * (np == 3 ? (bn <= 64 ? 16 : 24) * 68 : 4 * (bn == 256 ? 130 : 68)) + kTileNs;
-    const double c = (double)((tiles + sm_count - 1) / sm_count) * tile + kLaunchNs + prep;
+  for (int bn = 64; bn <= bn_max; bn += 16) {
+    const int64_t rows = up(M, kLanes) / kLanes, tiles = rows * (up(N, bn) / bn);
+    const double instr = bn <= 128 ? 68 : 68 + 62. * (bn - 128) / 128;
+    const double mma = (double)kblocks * (np == 3 ? (bn <= 64 ? 16 : 24) * 68 : 4 * instr);
+    const double load = (double)kblocks * np * 128 * ((rows > 1 ? kLanes : M) + bn) / 80;
+    const double waves = (double)((tiles + sm_count - 1) / sm_count), hbm = (double)(M + N) * (double)kblocks * np * 128 / 6500;
+    double c = waves * (mma > load ? mma : load);
+    if (c < hbm) c = hbm;
+    c += waves * kTileNs + kLaunchNs + prep;
     if (c < cost) {
       cost = c;
       best = {TcPlan::kWide, bn, 1, 0, false};

@@ -59,7 +59,8 @@ def _err():
 
 LINEAR = [(1, 1, 1), (1, 16, 8), (3, 5, 7), (16, 128, 64), (17, 130, 72), (64, 512, 1024), (65, 127, 129), (128, 256, 64),
           (129, 257, 200), (300, 264, 520), (257, 1000, 96), (513, 384, 1600),
-          (1, 700, 1100), (40, 1030, 333), (128, 260, 901)]
+          (1, 700, 1100), (40, 1030, 333), (128, 260, 901),
+          (64, 12100, 72), (200, 9000, 136), (70, 72, 9000)]  # tiles as wide as make the waves even
 
 
 def _linear_inputs(m, n, k, dt, seed, strided=False):
