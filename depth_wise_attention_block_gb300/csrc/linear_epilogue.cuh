@@ -60,7 +60,7 @@ __device__ __forceinline__ float act_value(float z) {
   } else if constexpr (ACT == ATTNRES_ACT_GELU_TANH) {
     return 0.5f * z * (1.f + tanh_exp(kSqrt2OverPi * fmaf(kGeluCubic * z * z, z, z)));
   } else if constexpr (ACT == ATTNRES_ACT_SILU) {
-    return z / (1.f + __expf(-z));
+    return z * __fdividef(1.f, 1.f + __expf(-z));  // (0 from z = -87 down)
   } else {
     return z;
   }

@@ -779,17 +779,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
       const long long m = l0 + 32 * quarter + lane;
       const int buf = g & 1;
       Raw16<bf16_t> res[2];
-      epi.ahead(res[0], m, c0 + half * 16);
+      epi.ahead(res[0], m, c0 + half * (kPairN / 2));
       if (ok && !__all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&acc_full[buf]), (uint32_t)(g >> 1) & 1u, p.wait_ns))) {
         if (lane == 0) report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
         ok = false;
       }
       tc_fence_after();
 #pragma unroll 2
-      for (int ch = half; ch < kPairN / 16; ch += 2) {
+      for (int ch = half * (kPairN / 32); ch < (half + 1) * (kPairN / 32); ++ch) {
         uint32_t v[16];
         tmem_ld16(lanes_at + buf * kPairN + ch * 16, v);
-        epi.ahead(res[1], m, c0 + (ch + 2) * 16);
+        if (ch + 1 < (half + 1) * (kPairN / 32)) epi.ahead(res[1], m, c0 + (ch + 1) * 16);
         tmem_ld_wait();
         float f[16];
 #pragma unroll
