@@ -5,7 +5,7 @@
 // Operands come in by TMA, 64 steps of the contraction at a time, in the
 // 128-byte swizzle, either K-major (rows of the contraction: x, w, dz in
 // dz w) or MN-major (columns of it: w in dz w, both operands of dz^T x), so
-// that no operand is ever transposed in memory.  One thread issues
+// that no operand is ever transposed in memory.  One warp issues
 // tcgen05.mma (M = 128 rows, fp32 accumulators in TMEM); eight warps run the
 // epilogue while the next tile's products are formed in the other half of
 // TMEM.
@@ -15,9 +15,12 @@
 //    (tcgen05.mma.cta_group::2): each loads 128 rows of A and 128 rows of B,
 //    half the L2 traffic per product of a 128 x 256 tile, whose 94 bytes per
 //    cycle and SM are more than L2 delivers (2048 x 7168 x 7168: 175 us with
-//    single tiles).  Persistent, the bound is the tensor cores.
+//    single tiles, 117 with pairs: 1.80 PFLOP/s).  Persistent, the bound is
+//    the tensor cores.
 //  - wide: persistent single CTAs over tiles of 128 x bn, where there are too
-//    few 256 x 256 tiles, and for fp32 operands.
+//    few 256 x 256 tiles, for fp32 operands, and for few rows of x where so
+//    many columns to a tile as make one wave read the weights at HBM's rate
+//    (64 x 21504 x 7168: 51 us, 6.1 TB/s).
 //  - narrow (SWAP): few rows of one operand (decode).  The wide operand's
 //    rows become the 128 lanes and the few rows the columns, so the weights
 //    are read once; the contraction is split over a cluster of `ksplit` CTAs

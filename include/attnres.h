@@ -646,8 +646,8 @@ int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, 
  * 128, 16-byte aligned rows, run in chunks of 128 tokens on the tensor cores
  * (tcgen05): scores and states enter those products rounded to bf16, the
  * state's own sums keep fp32 precision.  Others run on the CUDA cores in
- * fp32.  Long sequences are cut into segments where the batch does not fill
- * the GPU (their states lie in the workspace).  Infinities and NaN reach the
+ * fp32.  Where the sequences do not fill the GPU evenly they are cut into
+ * pieces (whose states lie in the workspace).  Infinities and NaN reach the
  * tokens behind them and no others; an infinity becomes NaN in the state.
  * ---------------------------------------------------------------------- */
 int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

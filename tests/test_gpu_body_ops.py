@@ -292,7 +292,7 @@ ATT = [  # T, sequences, H, Dk, Dv
     (1, 1, 1, 8, 8), (5, 1, 2, 64, 64), (128, 1, 2, 128, 128), (129, 1, 3, 128, 128), (300, 4, 2, 128, 64), (257, 3, 2, 64, 128),
     (700, 9, 1, 64, 64), (1000, 1, 1, 128, 128), (200, 30, 2, 128, 128), (77, 3, 2, 96, 160), (70, 2, 1, 37, 5), (50, 2, 2, 1, 256),
     (90, 1, 1, 256, 33),
-    (2000, 1, 2, 128, 128), (4100, 5, 1, 64, 128), (3001, 3, 2, 40, 24),  # long enough to be cut into segments
+    (2000, 1, 2, 128, 128), (4100, 5, 1, 64, 128), (3001, 3, 2, 40, 24),  # long enough to be cut into pieces
 ]
 
 
@@ -519,7 +519,7 @@ def test_bad_offsets_are_clamped(A):
                                         (torch.float32, 300, 4, 3, 40), (torch.float32, 6000, 3, 1, 24)])
 def test_a_decay_that_leaves_nothing(A, dt, T, n, H, D):
     """log_decay = -inf is a decay of 0, which -200 rounds to in fp32: the
-    same bits, in one piece and in segments, with an empty sequence."""
+    same bits, in one piece and in several, with an empty sequence."""
     q, k, v, _, cu, s0 = _att_inputs(T, n, H, D, D, dt, 13)
     cu[1] = cu[2]
     do = _randn(_gen(14), T, H, D, dtype=dt)
