@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(256 * W, 2 / W) scan_any_kernel(const __grid_c
   for (bool first = true;; first = false) {
     if (p.parts > 0) {
       if (!walk.next(p, blockIdx.y, &pc)) return;
-      if (STATE && pc.last && !p.s_out) continue;  // a last piece's own state is part of the final one only
+      if (STATE && pc.last) continue;  // its own state is part of the final one only, which the scan writes
     } else {
       if (!first) return;
       pc = whole_sequence(p, blockIdx.z, blockIdx.y);
@@ -143,11 +143,12 @@ __global__ void __launch_bounds__(256 * W, 2 / W) scan_any_kernel(const __grid_c
     __syncthreads();  // the piece before is done with
     if (tid <= kSC) pw[tid] = decay_pow(g, tid);
     const SeqRange sr{pc.first, pc.len};
-    const long long st = (p.parts > 0 ? pc.id : (long long)pc.seq * p.H + h) * Da * Dc;
-    const float* before = STATE ? nullptr : p.parts > 0 ? p.piece_state : p.s_in;
+    const long long of_seq = ((long long)pc.seq * p.H + h) * Da * Dc, of_piece = (long long)pc.id * Da * Dc;
+    const float* before = STATE ? nullptr : pc.whole ? p.s_in : p.piece_state;
+    if (before) before += pc.whole ? of_seq : of_piece;
     for (int i = tid; i < Dr * NC; i += kThreads) {
       const int da = i / NC, dc = c0 + i % NC;
-      S[i] = before && da < Da && dc < Dc ? before[st + p.state_at(da, dc)] : 0.f;
+      S[i] = before && da < Da && dc < Dc ? before[p.state_at(da, dc)] : 0.f;
     }
     for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
       const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
@@ -257,11 +258,11 @@ __global__ void __launch_bounds__(256 * W, 2 / W) scan_any_kernel(const __grid_c
       }
     }
     __syncthreads();
-    float* to = STATE ? p.piece_state : p.parts > 0 ? nullptr : p.s_out;  // pieces: the final state is joined with the others
+    float* to = STATE ? p.piece_state + of_piece : p.s_out && pc.last && !p.keep_final ? p.s_out + of_seq : nullptr;
     if (to)
       for (int i = tid; i < Da * NC; i += kThreads) {
         const int da = i / NC, dc = c0 + i % NC;
-        if (dc < Dc) to[st + p.state_at(da, dc)] = S[i];
+        if (dc < Dc) to[p.state_at(da, dc)] = S[i];
       }
   }
 }
@@ -318,6 +319,7 @@ cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t worksp
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
   s.chunk = kSC;
+  s.final_in_scan = true;
   // one cut for both orders of the two head sizes: the gradients' scans share states
   const Cut cut = scan_any_cut(s.T, s.H, s.transposed ? s.Dc : s.Da, s.transposed ? s.Da : s.Dc, s.N, di);
   const PieceLayout L = piece_layout(s.H, s.Da, s.Dc, s.N, cut);
@@ -402,6 +404,7 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
   const int u0 = at_gang + (p.first ? p.first[n] : 0), u1 = at_gang + (p.first ? p.first[n + 1] : r.per_head);
   const int i0 = u0 < u1 ? r.owner(u0) : 0, i1 = u0 < u1 ? r.owner(u1 - 1) + 1 : 0;
   const long long step = (long long)p.gang * per_head;  // from a piece's state to the next one's
+  if (p.final_in_scan && i1 - i0 == 1) return;  // a whole sequence
   float* const at0 = p.piece_state + ((long long)gang * p.N + n) * step + (h - gang * p.gang) * (long long)per_head + (e - (long long)h * per_head);
   float w[VEC];
 #pragma unroll
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
         const Piece pc = cut_piece(p, n, h, b - u0, f - b);
         d[j] = decay_pow(g, pc.len);
         const float* at = at0 + (i + j) * step;
-        if (!pc.last || p.s_out) {
+        if (!pc.last || (p.s_out && !p.final_in_scan)) {
           if constexpr (VEC == 4) {
             const float4 x = *reinterpret_cast<const float4*>(at);
             u[j][0] = x.x, u[j][1] = x.y, u[j][2] = x.z, u[j][3] = x.w;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
       for (int k = 0; k < VEC; ++k) w[k] = fmaf(w[k], d[j], u[j][k]);
     }
   }
-  if (p.s_out) {
+  if (p.s_out && (!p.final_in_scan || i0 == i1)) {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) p.s_out[n * all + e + k] = w[k];
   }
@@ -707,9 +710,12 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   // dk and dv carry the same reversed state ([Dk, Dv] in memory for both): in
   // pieces it is formed once.  grad_initial_state may lie over
   // grad_final_state, so it is written after the last read of that: where
-  // the pieces' states are joined, or by dv's scan.
+  // the pieces' states are joined, or by dv's scan (on the CUDA cores: by
+  // both, the former for empty sequences).
   const bool cut = tc ? scan_tc_in_pieces(a.T, a.H, a.Dk, a.Dv, a.N) : scan_any_in_pieces(a);
-  (cut ? k : v).s_out = a.ds0;
+  if (cut) k.s_out = a.ds0;
+  if (!cut || !tc) v.s_out = a.ds0;
+  k.keep_final = true;
   cudaError_t e = launch_scan(a, q, tc, false);
   if (e == cudaSuccess) e = launch_scan(a, k, tc, false);
   if (e == cudaSuccess) e = launch_scan(a, v, tc, cut);

@@ -28,7 +28,7 @@ __device__ __forceinline__ float decay_pow(float log_decay, int n) { return n ==
 struct Piece {
   int seq, head, first, len;  // first: the lowest row
   int id;                     // of its state
-  int last;                   // whether the sequence ends with it, in the direction of the scan
+  int last, whole;            // whether the sequence ends with it, in the direction of the scan; and begins, too
 };
 
 struct ScanArgs {
@@ -56,6 +56,11 @@ struct ScanArgs {
   const int* first;        // of a ragged batch: [N + 1] a head's chunks before each sequence,
   const int4* starts;      // [parts + 1] each range's first chunk, its gang and sequence, and a head's chunks
   float* piece_state;      // [piece][..]: each piece's own state, then the state before it
+  // where the scan itself is exact enough: the last pieces' own states are not
+  // formed, it writes the final states (but for empty sequences), and whole
+  // sequences are not joined
+  bool final_in_scan;
+  bool keep_final;         // the final states are another scan's to write, after this one
 
   __host__ __device__ int state_at(int da, int dc) const { return transposed ? dc * Da + da : da * Dc + dc; }
 };
@@ -76,11 +81,11 @@ struct Ranges {
 __device__ __forceinline__ Piece cut_piece(const ScanArgs& s, int seq, int head, int c0, int n) {
   const SeqRange r = seq_range(s.cu, seq, s.T);
   const long long i0 = (long long)c0 * s.chunk, all = (long long)n * s.chunk, len = r.len - i0 < all ? r.len - i0 : all;
-  return {seq, head, (int)(s.reverse ? r.start + r.len - i0 - len : r.start + i0), (int)len, 0, i0 + len >= r.len};
+  return {seq, head, (int)(s.reverse ? r.start + r.len - i0 - len : r.start + i0), (int)len, 0, i0 + len >= r.len, i0 == 0 && len >= r.len};
 }
 __device__ __forceinline__ Piece whole_sequence(const ScanArgs& s, int seq, int head) {
   const SeqRange r = seq_range(s.cu, seq, s.T);
-  return {seq, head, (int)r.start, (int)r.len, 0, 1};
+  return {seq, head, (int)r.start, (int)r.len, 0, 1, 1};
 }
 // The sequence with a head's chunk c: the last one that starts at c or before.
 __device__ __forceinline__ int sequence_of(const int* first, int N, int c) {
