@@ -46,32 +46,43 @@ __host__ constexpr int scan_smem(int Da, int nc) {  // nc columns of c
   return (2 * kSC * scan_rows(Da) + kSC * nc + kSC * kSPitchP + d * nc + kSC + 8) * 4;
 }
 
-// rows 0 .. kSC - 1 (zero from len on) of `width` channels to dst, columns up to `cols` zero-filled
+// rows 0 .. kSC - 1 (zero from len on) of `width` channels to dst, columns up
+// to `cols` zero-filled; four vectors per thread are on their way at a time
 template <typename T, int THREADS>
 __device__ __forceinline__ void scan_load(float* dst, int pitch, const void* src, long long stride, int off, int width, int cols, int len,
                                           const SeqRange& sr, long long i0, bool reverse, bool vec) {
-  const T* p = static_cast<const T*>(src) + off;
-  const int q = cols / 4;
-  for (int i = threadIdx.x; i < kSC * q; i += THREADS) {
-    const int r = i / q, c = i % q * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r < len) {
-      const T* at = p + sr.row(i0 + r, reverse) * stride + c;
-      if (vec && c + 4 <= width) {
-        if constexpr (sizeof(T) == 4) {
-          v = __ldg(reinterpret_cast<const float4*>(at));
+  constexpr int kBatch = 4;
+  const T* p = static_cast<const T*>(src) + off + sr.row(i0, reverse) * stride;
+  const long long step = reverse ? -stride : stride;
+  const int q = cols / 4, total = kSC * q;
+  for (int i = threadIdx.x; i < total; i += kBatch * THREADS) {
+    float4 v[kBatch];
+    int to[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int at_i = i + u * THREADS, r = at_i / q, c = (at_i - r * q) * 4;
+      to[u] = at_i < total ? r * pitch + c : -1;
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < len) {  // (rows past the tile are past len)
+        const T* at = p + r * step + c;
+        if (vec && c + 4 <= width) {
+          if constexpr (sizeof(T) == 4) {
+            v[u] = __ldg(reinterpret_cast<const float4*>(at));
+          } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
+            v[u] = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+          }
         } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(at));
-          v = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+          if (c < width) v[u].x = load_elem(at);
+          if (c + 1 < width) v[u].y = load_elem(at + 1);
+          if (c + 2 < width) v[u].z = load_elem(at + 2);
+          if (c + 3 < width) v[u].w = load_elem(at + 3);
         }
-      } else {
-        if (c < width) v.x = load_elem(at);
-        if (c + 1 < width) v.y = load_elem(at + 1);
-        if (c + 2 < width) v.z = load_elem(at + 2);
-        if (c + 3 < width) v.w = load_elem(at + 3);
       }
     }
-    *reinterpret_cast<float4*>(dst + r * pitch + c) = v;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (to[u] >= 0) *reinterpret_cast<float4*>(dst + to[u]) = v[u];
   }
 }
 
@@ -146,9 +157,16 @@ __global__ void __launch_bounds__(256 * W, 2 / W) scan_any_kernel(const __grid_c
     const long long of_seq = ((long long)pc.seq * p.H + h) * Da * Dc, of_piece = (long long)pc.id * Da * Dc;
     const float* before = STATE ? nullptr : pc.whole ? p.s_in : p.piece_state;
     if (before) before += pc.whole ? of_seq : of_piece;
-    for (int i = tid; i < Dr * NC; i += kThreads) {
-      const int da = i / NC, dc = c0 + i % NC;
-      S[i] = before && da < Da && dc < Dc ? before[p.state_at(da, dc)] : 0.f;
+    for (int i0 = tid; i0 < Dr * NC; i0 += 8 * kThreads) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * kThreads, da = i / NC, dc = c0 + i % NC;
+        v[u] = before && da < Da && dc < Dc ? before[p.state_at(da, dc)] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u * kThreads < Dr * NC) S[i0 + u * kThreads] = v[u];
     }
     for (long long i0 = 0; i0 < sr.len; i0 += kSC) {
       const int len = (int)(sr.len - i0 < kSC ? sr.len - i0 : kSC);
