@@ -325,7 +325,7 @@ Cut scan_any_cut(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) 
 }
 
 template <typename T>
-cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t workspace_bytes, bool states_ready, cudaStream_t stream) {
+cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t workspace_bytes, ScanReady ready, cudaStream_t stream) {
   ScanArgs s = in;
   auto vec = [](const void* p, long long stride, int D) {
     return (reinterpret_cast<uintptr_t>(p) & (4 * sizeof(T) - 1)) == 0 && stride % 4 == 0 && D % 4 == 0;
@@ -345,8 +345,8 @@ cudaError_t launch_scan_type(const ScanArgs& in, void* workspace, int64_t worksp
   s.parts = L.total > workspace_bytes ? 0 : cut.parts;  // tensors that the tensor cores would have taken but for their alignment
   const int nc = scan_columns(s.Da, s.Dc, di.max_smem_optin);
   if (s.parts > 0) piece_place(s, L, workspace);
-  if (s.parts > 0 && !states_ready) {
-    e = launch_piece_plan(s, stream);
+  if (s.parts > 0 && ready < kStates) {
+    if (ready < kTables) e = launch_piece_plan(s, stream);
     if (e == cudaSuccess) e = launch_scan_groups<T, true>(s, nc, stream);
     if (e == cudaSuccess) e = launch_piece_combine(s, stream);
     if (e != cudaSuccess) return e;
@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const __grid_cons
   int* first = const_cast<int*>(p.first);
   // 64 bits: offsets that decrease can ask for any number of chunks
   __shared__ long long sums[32], carry;
+  __shared__ int near[kPlanThreads + 1];  // first, of up to 1024 sequences
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long cap = (T + chunk - 1) / chunk + N;  // what offsets that do not decrease stay below
   pdl_wait();
@@ -388,18 +389,19 @@ __global__ void __launch_bounds__(kPlanThreads) la_plan_kernel(const __grid_cons
     }
     __syncthreads();
     const long long at = carry + (warp ? sums[warp - 1] : 0) + x - cnt;
-    if (n < N) first[n] = (int)(at < cap ? at : cap);
+    if (n < N) first[n] = near[tid] = (int)(at < cap ? at : cap);
     const long long total = sums[31];
     __syncthreads();
     if (tid == 0) carry += total;
     __syncthreads();
   }
-  if (tid == 0) first[N] = (int)(carry < cap ? carry : cap);
+  if (tid == 0) first[N] = near[N < kPlanThreads ? N : kPlanThreads] = (int)(carry < cap ? carry : cap);
   __syncthreads();
   const Ranges r(p);
+  const int* const from = N <= kPlanThreads ? near : first;
   for (int i = tid; i <= p.parts; i += kPlanThreads) {
     const int u = r.begin(i), gang = r.per_head > 0 ? u / r.per_head : 0;
-    const_cast<int4*>(p.starts)[i] = make_int4(u, gang, sequence_of(first, N, u - gang * r.per_head), r.per_head);
+    const_cast<int4*>(p.starts)[i] = make_int4(u, gang, sequence_of(from, N, u - gang * r.per_head), r.per_head);
   }
 }
 
@@ -683,10 +685,10 @@ int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int d
 
 namespace {
 
-cudaError_t launch_scan(const LinAttnArgs& a, const ScanArgs& s, bool tc, bool states_ready) {
-  if (tc) return launch_scan_tc(s, a.workspace, states_ready, a.dev_err, a.stream);
-  return a.dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, a.workspace, a.workspace_bytes, states_ready, a.stream)
-                                 : launch_scan_type<float>(s, a.workspace, a.workspace_bytes, states_ready, a.stream);
+cudaError_t launch_scan(const LinAttnArgs& a, const ScanArgs& s, bool tc, ScanReady ready) {
+  if (tc) return launch_scan_tc(s, a.workspace, ready, a.dev_err, a.stream);
+  return a.dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, a.workspace, a.workspace_bytes, ready, a.stream)
+                                 : launch_scan_type<float>(s, a.workspace, a.workspace_bytes, ready, a.stream);
 }
 
 // whether the scan runs in pieces on the CUDA cores
@@ -704,7 +706,7 @@ cudaError_t launch_linear_attention(const LinAttnArgs& a) {
   s.s_in = a.s0;
   s.s_out = a.s1;
   s.p_scale = s.in_scale = a.scale;
-  return launch_scan(a, s, scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(s), false);
+  return launch_scan(a, s, scan_tc_dims(a.Dk, a.Dv, a.dtype) && scan_tc_ok(s), kNothing);
 }
 
 cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
@@ -734,9 +736,9 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   if (cut) k.s_out = a.ds0;
   if (!cut || !tc) v.s_out = a.ds0;
   k.keep_final = true;
-  cudaError_t e = launch_scan(a, q, tc, false);
-  if (e == cudaSuccess) e = launch_scan(a, k, tc, false);
-  if (e == cudaSuccess) e = launch_scan(a, v, tc, cut);
+  cudaError_t e = launch_scan(a, q, tc, kNothing);
+  if (e == cudaSuccess) e = launch_scan(a, k, tc, kTables);
+  if (e == cudaSuccess) e = launch_scan(a, v, tc, kStates);
   return e;
 }
 

@@ -158,9 +158,10 @@ bool scan_tc_dims(int Dk, int Dv, int dtype);
 bool scan_tc_ok(const ScanArgs& s);  // alignment, sizes
 bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N);  // whether the scan runs in pieces
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N);
-// states_ready: the workspace holds the states before the pieces already,
-// left there by a scan of the same direction, states and sums b c^T (which
-// wrote the final state, if any)
-cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream);
+// What the workspace holds already: the tables of pieces, left by a scan of the
+// same sequences; and the states before the pieces, left by one of the same
+// direction, states and sums b c^T (which wrote the final state, if any).
+enum ScanReady { kNothing = 0, kTables = 1, kStates = 2 };
+cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, int* dev_err, cudaStream_t stream);
 
 }  // namespace attnres

@@ -940,7 +940,7 @@ bool scan_tc_ok(const ScanArgs& s) {
          s.T * 2 < INT32_MAX && (int64_t)s.N * s.H < INT32_MAX;
 }
 
-cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready, int* dev_err, cudaStream_t stream) {
+cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, int* dev_err, cudaStream_t stream) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
@@ -957,8 +957,8 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, bool states_ready
   p.s.parts = cut.parts;
   p.s.gang = cut.gang;
   if (p.s.parts > 0) piece_place(p.s, piece_layout(s.H, s.Da, s.Dc, s.N, cut), workspace);
-  if (p.s.parts > 0 && !states_ready) {
-    e = launch_piece_plan(p.s, stream);
+  if (p.s.parts > 0 && ready < kStates) {
+    if (ready < kTables) e = launch_piece_plan(p.s, stream);
     if (e != cudaSuccess) return e;
     ScanTcParams ps = p;
     if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))

@@ -515,6 +515,27 @@ def test_bad_offsets_are_clamped(A):
     assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt,D", [(torch.bfloat16, 64), (torch.float32, 24)])
+def test_offsets_that_decrease_stay_inside(A, dt, D):
+    """What they select is not defined, but nothing outside the rows is
+    written, and the call returns (long enough to run in pieces)."""
+    T, H = 4100, 2
+    cu = torch.tensor([0, 4000, 100, 4100, 50, 4100, 0], dtype=torch.int32, device="cuda")
+    assert A.attnres_linear_attention_workspace_size(T, H, D, D, dt, 6) > 0
+    rows = _randn(_gen(18), T, 3 * H * D, dtype=dt)
+    q, k, v = (rows[:, i * H * D:(i + 1) * H * D].unflatten(1, (H, D)) for i in range(3))
+    decay, fin = torch.full((H,), -0.01, device="cuda"), torch.zeros(8, H, D, D, device="cuda")
+    outs = [torch.full((T + 256, H, D), 7.0, dtype=dt, device="cuda") for _ in range(4)]
+    views = [o[128:T + 128] for o in outs]
+    err = _err()
+    A.attnres_linear_attention(q, k, v, decay, views[0], cu_seqlens=cu, final_state=fin[1:7], dev_err=err)
+    A.attnres_linear_attention_backward(q, k, v, decay, v, *views[1:], cu_seqlens=cu, grad_initial_state=fin[1:7], dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and not fin[0].any() and not fin[7].any()
+    for o in outs:
+        assert (o[:128] == 7).all() and (o[T + 128:] == 7).all()
+
+
 @pytest.mark.parametrize("dt,T,n,H,D", [(torch.bfloat16, 300, 4, 3, 128), (torch.bfloat16, 9000, 3, 1, 64),
                                         (torch.float32, 300, 4, 3, 40), (torch.float32, 6000, 3, 1, 24)])
 def test_a_decay_that_leaves_nothing(A, dt, T, n, H, D):
