@@ -466,25 +466,28 @@ __global__ void __launch_bounds__(kQkThreads) qk_any_kernel(const __grid_constan
   }
 }
 
-// gain gradients: the CTAs' partial rows, summed in order (32 channels x 8
-// interleaved runs of rows per CTA; blockIdx.y: q or k)
-__global__ void __launch_bounds__(256) qk_dgain_kernel(const float* part, int blocks0, int blocks, int D, float* dq,
-                                                       float* dk) {
-  __shared__ float sums[8][32];
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), r = threadIdx.x >> 5;
+// gain gradients: the CTAs' partial rows, summed in order (32 channels x 32
+// interleaved runs of rows per CTA, whose loads do not wait for one another;
+// blockIdx.y: q or k)
+constexpr int kGainRuns = 32;
+__global__ void __launch_bounds__(32 * kGainRuns) qk_dgain_kernel(const float* part, int blocks0, int blocks, int D, float* dq, float* dk) {
+  __shared__ float sums[kGainRuns][33];
+  const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
   const int b0 = blockIdx.y ? blocks0 : 0, b1 = blockIdx.y ? blocks : blocks0;
   float* out = blockIdx.y ? dk : dq;
   pdl_wait();
   pdl_trigger();
+  if (!out) return;
   float s = 0.f;
-  if (c < D && out)
-    for (int b = b0 + r; b < b1; b += 8) s += part[(long long)b * D + c];
-  sums[r][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (r == 0 && c < D && out) {
-    for (int k = 1; k < 8; ++k) s += sums[k][threadIdx.x & 31];
-    out[c] = s;
+  if (c < D) {
+#pragma unroll 8
+    for (int b = b0 + r; b < b1; b += kGainRuns) s += part[(long long)b * D + c];
   }
+  sums[r][lane] = s;
+  __syncthreads();
+  // warp r: channel r of the CTA's
+  s = warp_sum(sums[lane][r]);
+  if (lane == 0 && blockIdx.x * 32 + r < D) out[blockIdx.x * 32 + r] = s;
 }
 
 template <typename T, int L, bool BWD>
@@ -606,7 +609,7 @@ cudaError_t launch_qk_norm_rope(const QkArgs& a) {
                      : launch_kernel(qk_any_kernel<float, false>, dim3(grid), dim3(kQkThreads), smem, a.stream, p, a.interleaved);
   }
   if (e != cudaSuccess || !dgain) return e;
-  return launch_kernel(qk_dgain_kernel, dim3((a.D + 31) / 32, 2), dim3(256), 0, a.stream, (const float*)p.part, p.blocks0, grid, a.D,
+  return launch_kernel(qk_dgain_kernel, dim3((a.D + 31) / 32, 2), dim3(32 * kGainRuns), 0, a.stream, (const float*)p.part, p.blocks0, grid, a.D,
                        a.h[0].dgain, a.h[1].dgain);
 }
 
