@@ -80,6 +80,7 @@ struct ScanTcParams {
   ScanArgs s;
   int* dev_err;
   unsigned long long wait_ns;
+  int withhold1;  // bounded-wait test: 1 + the tile that each CTA arms without its copies
 };
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* v) {
@@ -134,6 +135,26 @@ __device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint3
   }
 }
 
+// After a wait that ran out, by a warp: NaN to the outputs of a CTA's whole
+// range (STATES: to its pieces' own states).
+template <bool STATES>
+__device__ __noinline__ void poison_range(const ScanArgs& s, int cta, int lane) {
+  PieceWalk walk(s, cta);
+  Piece q;
+  const float nan = __int_as_float(0x7fc00000);
+  while (walk.next(s, cta, &q)) {
+    if constexpr (STATES) {
+      if (q.last && !s.s_out) continue;
+      const long long n = (long long)s.Da * s.Dc;
+      for (long long i = lane; i < n; i += 32) s.piece_state[q.id * n + i] = nan;
+    } else {
+      for (int r = 0; r < q.len; ++r)
+        for (int c = lane; c < s.Dc; c += 32)
+          store_elem(static_cast<bf16_t*>(s.out) + (long long)(q.first + r) * s.os + (long long)q.head * s.Dc + c, nan);
+    }
+  }
+}
+
 // TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
 // where only bf16 outputs follow from it.
 template <int DA, int DC, int TERMS>
@@ -143,7 +164,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, b_ready, u_full, u_free;
-  __shared__ __align__(8) uint64_t t_ready;
+  __shared__ __align__(8) uint64_t t_ready, drained[2];
   __shared__ uint32_t tmem_base;
   // l^i, and p_scale l^i behind it: distances below 0, which the mask covers
   // and which reach -46, read into the first
@@ -156,6 +177,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 
   if (tid == 0) {
     mbar_init(smem_addr(&t_ready), 16);
+    mbar_init(smem_addr(&drained[0]), 1);
+    mbar_init(smem_addr(&drained[1]), 1);
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 2);  // two arrivals free a slot: each MMA warp's (c), or one warp's two (a, b)
@@ -207,6 +230,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
   };
+  // Nothing is passed on once a wait has run out: the other roles' waits run
+  // out, too, and the results are NaN.
+  auto commit = [&](uint64_t* bar) {
+    if (ok) tc_commit_warp(smem_addr(bar));
+  };
+  // no product of this warp is under way when shared memory and TMEM are given back
+  auto drain = [&](uint64_t* bar) {
+    if (!ok) {
+      tc_commit_warp(smem_addr(bar));
+      mbar_wait_bounded(smem_addr(bar), 0);
+    }
+  };
 
   if (warp == 16) {
     if (lane == 0) {
@@ -223,7 +258,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             const CUtensorMap* m = x == 0 ? &p.ma : x == 1 ? &p.mb : &p.mc;
             const uint32_t fb = smem_addr(&full[st]);
             mbar_arrive_expect_tx(fb, D * kC * 2);
-            for (int y = 0; y < D; y += 64) tma_load_2d(base + st * kTile + y / 64 * kPanel, m, pc.head * D + y, t, fb);
+            for (int y = 0; y < D && it + 1 != p.withhold1; y += 64) tma_load_2d(base + st * kTile + y / 64 * kPanel, m, pc.head * D + y, t, fb);
           }
         }
         if (!cut || !live || !ok) break;
@@ -239,8 +274,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         }
       }
       // the CTA never exits under a copy
-      const int armed = it < kSlots ? it : kSlots;
-      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / kSlots) & 1u);
+      // (a tile armed without copies is its slot's last and never completes)
+      const int armed = it < kSlots ? it : kSlots, skip = p.withhold1 > 0 && it >= p.withhold1 ? (p.withhold1 - 1) % kSlots : -1;
+      for (int st = 0; st < armed; ++st)
+        if (st != skip) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((it - 1 - st) / kSlots) & 1u);
     }
     __syncwarp();
   } else if (warp == 17) {
@@ -262,7 +299,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         const uint32_t off = (kk / 4 * kPanel + kk % 4 * 32) / 16;
         tc_mma_bf16_warp(tmem + kColP, da + off, db + off, kI1, kk > 0);
       }
-      tc_commit_warp(smem_addr(&p_full));
+      commit(&p_full);
     };
     int m = 0, left = warp_value(pieces[0].len);  // chunk of all pieces; tokens to go in this one
     if (left > 0) {
@@ -281,8 +318,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < DA / 16; ++kk)
           tc_mma_bf16_warp(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
-        tc_commit_warp(smem_addr(&empty[it % kSlots]));
-        tc_commit_warp(smem_addr(&empty[it % kSlots]));
+        commit(&empty[it % kSlots]);
+        commit(&empty[it % kSlots]);
         wait_tile(ic);
         // rows behind a short chunk's end are cleared with the weighted rows
         if (left < kC) warp_wait(&b_ready, ph);
@@ -291,8 +328,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
         for (int kk = 0; kk < kC / 16; ++kk)
           tc_mma_bf16_ts_warp(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
-        tc_commit_warp(smem_addr(&o_full));
-        tc_commit_warp(smem_addr(&empty[ic % kSlots]));
+        commit(&o_full);
+        commit(&empty[ic % kSlots]);
         if (left > kC) {
           before(m + 1);
           scores(m + 1);
@@ -306,6 +343,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       else if (ok && lane == 0)
         mbar_arrive(smem_addr(&p_full));  // the others read of the end behind it
     }
+    drain(&drained[0]);
     __syncwarp();
   } else if (warp == 18) {
     // a warp of its own, since these products wait for other things
@@ -328,15 +366,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
           for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16_warp(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
-        tc_commit_warp(smem_addr(&u_full));
-        tc_commit_warp(smem_addr(&empty[ib % kSlots]));
-        tc_commit_warp(smem_addr(&empty[ib % kSlots]));
-        tc_commit_warp(smem_addr(&empty[ic % kSlots]));
+        commit(&u_full);
+        commit(&empty[ib % kSlots]);
+        commit(&empty[ib % kSlots]);
+        commit(&empty[ic % kSlots]);
       }
       if (!cut || !ok) break;
       warp_wait(&b_ready, (uint32_t)m);  // of the next piece's first chunk, or of the end
       left = ok ? warp_value(pieces[k % kPieces].len) : 0;
     }
+    drain(&drained[1]);
     __syncwarp();
   } else {
     // warp w reads TMEM lanes 32 (w mod 4) .. + 31; two warps of a group share
@@ -348,7 +387,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     int meets = 0;
     auto meet = [&] {
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&t_ready));
+      if (ok && lane == 0) mbar_arrive(smem_addr(&t_ready));
       warp_wait(&t_ready, meets++);
     };
     auto powers = [&](int k) {
@@ -371,7 +410,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       warp_wait(&p_full, m);
       if (!ok) return false;
       if (pieces[k % kPieces].len > 0) return true;
-      if (lane == 0) mbar_arrive(smem_addr(&b_ready));  // the token sums' warp reads of the end behind it
+      if (ok && lane == 0) mbar_arrive(smem_addr(&b_ready));  // the token sums' warp reads of the end behind it
       return false;
     };
     // b's rows times their decay, as three bf16 terms (hi over b itself)
@@ -423,7 +462,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         for (int x = 0; x < DC / 64; ++x) st_shared_v4(Ct + x * kPanel + v * 16, 0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&b_ready));
+      if (ok && lane == 0) mbar_arrive(smem_addr(&b_ready));
     };
 
     if (warp < 8) {
@@ -478,7 +517,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&p_ready));
+          if (ok && lane == 0) mbar_arrive(smem_addr(&p_ready));
 
           // b's weighted rows: a b^T has read b, and the last chunk's sums
           // have read its terms
@@ -527,9 +566,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             masked_row<DA>(p.s, tab, lanes_at + kColO2, chunk_at(q, left), q.head, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&o_free));
+          if (ok && lane == 0) mbar_arrive(smem_addr(&o_free));
         }
       } while (more(++k, m));
+      if (cut && !ok) poison_range<false>(p.s, blockIdx.x, lane);
     } else {
       // the state: a thread holds S[d0 .. d0 + DH)[row]
       constexpr int DH = DA / 2;
@@ -569,7 +609,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         auto put_done = [&](int m) {
           fence_proxy_async_smem();
           warp_wait(&p_full, m);
-          if (lane == 0) mbar_arrive(smem_addr(&s_ready));
+          if (ok && lane == 0) mbar_arrive(smem_addr(&s_ready));
         };
         if (q.len > 0) {
 #pragma unroll
@@ -601,7 +641,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_addr(&u_free));
+          if (ok && lane == 0) mbar_arrive(smem_addr(&u_free));
           if (next) put_done(m + 1);
         }
         // the state behind a sequence in one piece (others: joined before)
@@ -648,7 +688,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   constexpr int kTileB = kHalf * DA * 2, kStage = StateSmem<DA, DC>::kStage, kSlots = StateSmem<DA, DC>::kSlots;
   constexpr uint32_t kColU = 2 * DA;  // columns between the accumulators: first terms' sums, then the others'
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxSlots], done[kMaxSlots], b_ready[2], u_free[2];
+  __shared__ __align__(8) uint64_t full[kMaxSlots], done[kMaxSlots], b_ready[2], u_free[2], drained;
   __shared__ uint32_t tmem_base;
   __shared__ Piece pieces[kPieces];
   // stages (b, c), then two buffers of three terms (which an operand of 64
@@ -661,6 +701,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&done[s]), 1);
     }
+    mbar_init(smem_addr(&drained), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&b_ready[b]), 8);
       mbar_init(smem_addr(&u_free[b]), 16);
@@ -700,6 +741,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
     wait(bar, parity);
     ok = __all_sync(0xffffffffu, ok);
   };
+  // Nothing is passed on once a wait has run out: the other roles' waits run
+  // out, too, and the results are NaN.
+  auto commit = [&](uint64_t* bar) {
+    if (ok) tc_commit_warp(smem_addr(bar));
+  };
+  // no product of this warp is under way when shared memory and TMEM are given back
+  auto drain = [&](uint64_t* bar) {
+    if (!ok) {
+      tc_commit_warp(smem_addr(bar));
+      mbar_wait_bounded(smem_addr(bar), 0);
+    }
+  };
 
   if (warp == 16) {
     if (lane == 0) {
@@ -711,6 +764,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
           if (!ok) break;
           const uint32_t fb = smem_addr(&full[st]), to = base + st * kStage;
           mbar_arrive_expect_tx(fb, kStage);
+          if (i + 1 == p.withhold1) continue;
 #pragma unroll
           for (int x = 0; x < DA; x += 64) tma_load_2d(to + x / 64 * kHalfPanel, &p.mb, pc.head * DA + x, t, fb);
 #pragma unroll
@@ -733,8 +787,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
         }
       }
       // the CTA never exits under a copy
-      const int armed = i < kSlots ? i : kSlots;
-      for (int st = 0; st < armed; ++st) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((i - 1 - st) / kSlots) & 1u);
+      const int armed = i < kSlots ? i : kSlots, skip = p.withhold1 > 0 && i >= p.withhold1 ? (p.withhold1 - 1) % kSlots : -1;
+      for (int st = 0; st < armed; ++st)
+        if (st != skip) mbar_wait_bounded(smem_addr(&full[st]), (uint32_t)((i - 1 - st) / kSlots) & 1u);
     }
     __syncwarp();
   } else if (warp == 17) {
@@ -755,12 +810,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
           tc_mma_bf16_warp(d, dc + kk * 128, dt + kk * 128, kI2, kk > 0 ? 1u : more);
           tc_mma_bf16_warp(d + DA, dc + kk * 128, dt + 2 * kTileB / 16 + kk * 128, kI1, 1u);
         }
-        tc_commit_warp(smem_addr(&done[st]));
+        commit(&done[st]);
       }
       warp_wait(&b_ready[0], (uint32_t)(i / 2));  // of the next piece's first half, or of the end
       pc.len = warp_value(pieces[k % kPieces].len);
       nchunk = ok ? (pc.len + kC - 1) / kC : 0;
     }
+    drain(&drained);
     __syncwarp();
   } else {
     // thread: row `row` of the state, DA / 4 of its values from d0
@@ -788,7 +844,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&u_free[m & 1]));
+      if (ok && lane == 0) mbar_arrive(smem_addr(&u_free[m & 1]));
     };
     const int group = warp >> 3, tg = tid & 255;
     int m = 0;  // chunk of all pieces
@@ -839,7 +895,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&b_ready[group]));
+        if (ok && lane == 0) mbar_arrive(smem_addr(&b_ready[group]));
         if (n > 0) add(n - 1, m - 1);
       }
       add(nchunk - 1, m - 1);
@@ -863,6 +919,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
       nchunk = ok ? (pc.len + kC - 1) / kC : 0;
       if (ok && nchunk == 0 && lane == 0) mbar_arrive(smem_addr(&b_ready[group]));  // the products' warp reads of the end behind it
     }
+    if (!ok) poison_range<true>(p.s, blockIdx.x, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -952,6 +1009,7 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, 
     return cudaErrorInvalidValue;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
+  p.withhold1 = debug_withhold_row1();
   p.s.chunk = kC;
   const Cut cut = scan_tc_cut(s.T, s.H, s.Da, s.Dc, s.N, di.sm_count);
   p.s.parts = cut.parts;

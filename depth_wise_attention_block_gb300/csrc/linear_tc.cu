@@ -83,6 +83,7 @@ struct TcParams {
   LinearEpilogue epi;
   int* dev_err;
   unsigned long long wait_ns;
+  int withhold1;         // bounded-wait test: 1 + the block that each CTA arms without its copies
 };
 
 // A place in the ring of stages and the parity of its lap, without the
@@ -99,10 +100,12 @@ struct RingPos {
 };
 // waits for the last phase of every stage that a producer armed: the CTA
 // never exits under a copy (`r` is the place after the last armed one, `lap0`
-// whether it is still in the first lap)
-__device__ __forceinline__ void drain_stages(const uint64_t* full, const RingPos& r, bool lap0, int stages) {
+// whether it is still in the first lap; a block armed without copies is its
+// stage's last and never completes)
+__device__ __forceinline__ void drain_stages(const uint64_t* full, const RingPos& r, bool lap0, int stages, int issued, int withhold1) {
+  const int skip = withhold1 > 0 && issued >= withhold1 ? (withhold1 - 1) % stages : -1;
   for (int st = 0; st < (lap0 ? r.st : stages); ++st)
-    mbar_wait_bounded(smem_addr(&full[st]), st < r.st ? r.lap : r.lap ^ 1u);
+    if (st != skip) mbar_wait_bounded(smem_addr(&full[st]), st < r.st ? r.lap : r.lap ^ 1u);
 }
 
 // One plane of an operand's tile, block kb of the contraction, rows from r0.
@@ -317,7 +320,7 @@ template <int NP, int MODE, bool SWAP, int FUSED>
 __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant__ TcParams p) {
   using T = typename std::conditional<NP == 3, float, bf16_t>::type;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], split[FUSED ? kMaxStages : 1], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], split[FUSED ? kMaxStages : 1], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
       mbar_init(smem_addr(&empty[s]), 1);
       if (FUSED) mbar_init(smem_addr(&split[s]), kEpiWarps);
     }
+    mbar_init(smem_addr(&drained), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&acc_full[b]), 1);
       mbar_init(smem_addr(&acc_empty[b]), kEpiWarps);
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
     if (lane == 0) {
       const int brows = p.b_mn ? (p.bn + 63) / 64 * 64 : p.bn;
       RingPos r;
+      int issued = 0;
       bool ok = true, lap0 = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int l0 = tile % p.tiles_l * kLanes, c0 = tile / p.tiles_l * p.bn;
@@ -363,8 +368,10 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
           }
           const uint32_t fb = smem_addr(&full[st]), a = base + st * p.stage_bytes, b = a + NP * p.plane_a;
           mbar_arrive_expect_tx(fb, NP * ((FUSED ? 0 : kLanes * 128) + brows * 128));
+          ++issued;
 #pragma unroll
           for (int pl = 0; pl < NP; ++pl) {
+            if (issued == p.withhold1) break;
             if (!FUSED) load_plane(a + pl * p.plane_a, &p.ma, p.a_mn, l0, kLanes, kb, pl, fb);
             load_plane(b + pl * p.plane_b, &p.mb, p.b_mn, c0, brows, kb, pl, fb);
           }
@@ -372,7 +379,7 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
           lap0 = lap0 && r.st > 0;
         }
       }
-      drain_stages(full, r, lap0, p.stages);
+      drain_stages(full, r, lap0, p.stages, issued, p.withhold1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -432,8 +439,12 @@ __global__ void __launch_bounds__(kThreads) tc_gemm_kernel(const __grid_constant
           tc_commit_warp(smem_addr(&empty[r.st]));
           r.next(p.stages);
         }
-        tc_commit_warp(smem_addr(&acc_full[buf]));
+        if (ok) tc_commit_warp(smem_addr(&acc_full[buf]));  // (else the epilogue's wait runs out, too, and it writes NaN)
       }
+    }
+    if (!ok) {  // no product is under way when shared memory and TMEM are given back
+      tc_commit_warp(smem_addr(&drained));
+      mbar_wait_bounded(smem_addr(&drained), 0);
     }
     __syncwarp();
   } else {
@@ -662,7 +673,7 @@ constexpr int kPairTmem = 512;                           // two accumulators of 
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_constant__ TcParams p) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2], drained;
   __shared__ uint32_t tmem_base;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
@@ -674,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&empty[s]), 1);
     }
+    mbar_init(smem_addr(&drained), 1);
     for (int b = 0; b < 2; ++b) {
       mbar_init(smem_addr(&acc_full[b]), 1);
       mbar_init(smem_addr(&acc_empty[b]), 2 * kEpiWarps);
@@ -692,6 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
   if (warp == 0) {
     if (lane == 0) {
       RingPos r;
+      int issued = 0;
       bool ok = true, lap0 = true;
       for (int tile = tile0; tile < ntiles && ok; tile += tstep) {
         const int l0 = tile % p.tiles_l * (2 * kLanes) + rank * kLanes, c0 = tile / p.tiles_l * kPairN + rank * kLanes;
@@ -705,7 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
           const uint32_t fb = smem_addr(&full[r.st]);
           if (rank == 0) mbar_arrive_expect_tx(fb, 2 * kPairBlock * blocks);
           const uint32_t bar = map_shared_rank(fb, 0);
-          for (int i = 0; i < blocks; ++i) {
+          ++issued;
+          for (int i = 0; i < blocks && issued != p.withhold1; ++i) {
             const uint32_t a = base + r.st * kPairStage + i * kPairBlock, b = a + kPairBlock / 2;
             const int k = (kb + i) * kKB;
             if (p.a_mn) {
@@ -726,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
         }
       }
       // no CTA exits under a copy: rank 0 sees the bytes of both
-      if (rank == 0) drain_stages(full, r, lap0, p.stages);
+      if (rank == 0) drain_stages(full, r, lap0, p.stages, issued, p.withhold1);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -740,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
         const int buf = g & 1;
         if (!__all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&acc_empty[buf]), ((uint32_t)(g >> 1) & 1u) ^ 1u, p.wait_ns))) {
           report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+          ok = false;
           break;
         }
         tc_fence_after();
@@ -766,7 +781,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_pair_kernel(const __grid_const
           tc_commit_pair(smem_addr(&empty[r.st]));
           r.next(p.stages);
         }
-        tc_commit_pair(smem_addr(&acc_full[buf]));
+        if (ok) tc_commit_pair(smem_addr(&acc_full[buf]));
+      }
+      if (!ok) {
+        tc_commit_pair(smem_addr(&drained));
+        mbar_wait_bounded(smem_addr(&drained), 0);
       }
     }
     __syncwarp();
@@ -1065,6 +1084,7 @@ cudaError_t launch_tc_gemm(const TcPlan& plan, const TcOperand& A, const TcOpera
   p.epi = epi;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
+  p.withhold1 = debug_withhold_row1();
   // shared memory: the stages; narrow tiles also park their partial sums there
   const int smem_max = di.max_smem_optin - 1024;  // the kernels' static shared memory fits in the rest
   const int budget = (swap && np == 1 ? kNarrowSmem : smem_max) - 1024;
