@@ -1,5 +1,7 @@
 // The scan of linear attention (linear_attention.cu) on the tensor cores:
-// bf16 tensors with head sizes of 64 or 128, in chunks of 128 tokens.
+// bf16 tensors with head sizes of up to 128, multiples of 16, in chunks of 128
+// tokens.  DA and DC are the sizes rounded up to 64 or 128: the loads fill the
+// channels behind a head's last with zeros.
 //
 //   P    = a b^T, masked and decayed       scores of the chunk   [128 x 128]
 //   out  = P c + l^{i+1} (a S)             S: the state before it
@@ -108,23 +110,22 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // masked row counts as 0 times its values, met an infinity or a NaN.  o2: the
 // row's a S in TMEM, which a whole warp reads; `bad`: this lane's row is
 // redone; l: p_scale l^distance.
-template <int DA>
 __device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint32_t o2, long long t0, int h, int row, int len, int c0, int c1,
                                         float coef, bool bad) {
   for (; c0 < c1; c0 += 16) {
     uint32_t y[16];
     tmem_ld16(o2 + c0, y);
     tmem_ld_wait();
-    if (!bad) continue;
-    const bf16_t* a = static_cast<const bf16_t*>(s.a) + (t0 + row) * s.as + (long long)h * DA;
+    if (!bad || c0 >= s.Dc) continue;
+    const bf16_t* a = static_cast<const bf16_t*>(s.a) + (t0 + row) * s.as + (long long)h * s.Da;
     float x[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) x[k] = coef * __uint_as_float(y[k]);
     for (int j = s.reverse ? row : 0; j < (s.reverse ? len : row + 1); ++j) {
-      const bf16_t* b = static_cast<const bf16_t*>(s.b) + (t0 + j) * s.bs + (long long)h * DA;
+      const bf16_t* b = static_cast<const bf16_t*>(s.b) + (t0 + j) * s.bs + (long long)h * s.Da;
       const bf16_t* c = static_cast<const bf16_t*>(s.c) + (t0 + j) * s.cs + (long long)h * s.Dc + c0;
       float dot = 0.f;
-      for (int d = 0; d < DA; ++d) dot = fmaf(load_elem(a + d), load_elem(b + d), dot);
+      for (int d = 0; d < s.Da; ++d) dot = fmaf(load_elem(a + d), load_elem(b + d), dot);
       const float f = bf16lo(pack_bf16x2(dot * l[s.reverse ? j - row : row - j], 0.f));
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = fmaf(f, load_elem(c + k), x[k]);
@@ -155,9 +156,9 @@ __device__ __noinline__ void poison_range(const ScanArgs& s, int cta, int lane) 
   }
 }
 
-// TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
+// FULL: the head sizes are DA and DC.  TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
 // where only bf16 outputs follow from it.
-template <int DA, int DC, int TERMS>
+template <int DA, int DC, int TERMS, bool FULL>
 __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_constant__ ScanTcParams p) {
   constexpr int kTile = ScanSmem<DA, DC, TERMS>::kTile, kSlots = ScanSmem<DA, DC, TERMS>::kSlots;
   constexpr int kTiles = 3;                            // tiles per chunk: a, b, c
@@ -174,6 +175,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_buf = base + kSlots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
   const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
+  const int Da = FULL ? DA : p.s.Da, Dc = FULL ? DC : p.s.Dc;
 
   if (tid == 0) {
     mbar_init(smem_addr(&t_ready), 16);
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             const CUtensorMap* m = x == 0 ? &p.ma : x == 1 ? &p.mb : &p.mc;
             const uint32_t fb = smem_addr(&full[st]);
             mbar_arrive_expect_tx(fb, D * kC * 2);
-            for (int y = 0; y < D && it + 1 != p.withhold1; y += 64) tma_load_2d(base + st * kTile + y / 64 * kPanel, m, pc.head * D + y, t, fb);
+            for (int y = 0; y < D && it + 1 != p.withhold1; y += 64) tma_load_3d(base + st * kTile + y / 64 * kPanel, m, y, pc.head, t, fb);
           }
         }
         if (!cut || !live || !ok) break;
@@ -532,7 +534,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           const bool in = row < len;
           const int e = rev ? len - row - p.s.shift : row + 1 - p.s.shift;
           const float coef = in ? p.s.in_scale * pw[e] : 0.f;
-          bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(q, left) + row) * p.s.os + (long long)q.head * DC;
+          bf16_t* out = static_cast<bf16_t*>(p.s.out) + (long long)(chunk_at(q, left) + row) * p.s.os + (long long)q.head * Dc;
           uint64_t sum = 0;  // 0, or NaN where a value is not finite
 #pragma unroll 1
           for (int c0 = half * (DC / 2); c0 < (half + 1) * (DC / 2); c0 += 32) {
@@ -552,18 +554,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                         : 0x7fc07fc0u;
             if (in) {
               if (p.s.wide_out) {
-                st_global_v8(out + c0, w);
-                st_global_v8(out + c0 + 16, w + 8);
+                if (FULL || c0 < Dc) st_global_v8(out + c0, w);
+                if (FULL || c0 + 16 < Dc) st_global_v8(out + c0 + 16, w + 8);
               } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                  reinterpret_cast<uint4*>(out + c0)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                  if (FULL || c0 + 8 * k < Dc) reinterpret_cast<uint4*>(out + c0)[k] = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
               }
             }
           }
           const bool bad = in && ok && f2_hsum(sum) != 0.f;
           if (__any_sync(0xffffffffu, bad))
-            masked_row<DA>(p.s, tab, lanes_at + kColO2, chunk_at(q, left), q.head, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
+            masked_row(p.s, tab, lanes_at + kColO2, chunk_at(q, left), q.head, row, len, half * (DC / 2), (half + 1) * (DC / 2), coef, bad);
           tc_fence_before();
           __syncwarp();
           if (ok && lane == 0) mbar_arrive(smem_addr(&o_free));
@@ -580,17 +582,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       if (live) do {
         powers(k);
         const Piece& q = pieces[k % kPieces];
-        const long long st = (cut ? q.id : (long long)q.seq * p.s.H + q.head) * DA * DC;
-        if (from && row < DC) {
+        const long long st = (cut ? q.id : (long long)q.seq * p.s.H + q.head) * Da * Dc;
+        if (from && row < Dc) {
           if (p.s.transposed) {
 #pragma unroll
             for (int d = 0; d < DH; d += 4) {
-              const float4 v = *reinterpret_cast<const float4*>(from + st + (long long)row * DA + d0 + d);
+              float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (FULL || d0 + d < Da) v = *reinterpret_cast<const float4*>(from + st + (long long)row * Da + d0 + d);
               S[d] = v.x, S[d + 1] = v.y, S[d + 2] = v.z, S[d + 3] = v.w;
             }
           } else {
 #pragma unroll
-            for (int d = 0; d < DH; ++d) S[d] = from[st + (d0 + d) * DC + row];
+            for (int d = 0; d < DH; ++d) S[d] = FULL || d0 + d < Da ? from[st + (d0 + d) * Dc + row] : 0.f;
           }
         } else {
 #pragma unroll
@@ -645,17 +648,18 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           if (next) put_done(m + 1);
         }
         // the state behind a sequence in one piece (others: joined before)
-        if (row < DC && p.s.s_out && !cut) {
+        if (row < Dc && p.s.s_out && !cut) {
           float* to = p.s.s_out + st;
           const float nan = __int_as_float(0x7fc00000);
           if (p.s.transposed) {
 #pragma unroll
             for (int d = 0; d < DH; d += 4)
-              *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
+              if (FULL || d0 + d < Da) *reinterpret_cast<float4*>(to + (long long)row * Da + d0 + d) =
                   ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
           } else {
 #pragma unroll
-            for (int d = 0; d < DH; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
+            for (int d = 0; d < DH; ++d)
+              if (FULL || d0 + d < Da) to[(d0 + d) * Dc + row] = ok ? S[d] : nan;
           }
         }
       } while (more(++k, m));
@@ -683,7 +687,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 // the terms' next writers and to the sums' readers.  The bound is HBM.
 constexpr int kHalfPanel = kHalf * 128;  // bytes of 64 channels of a half chunk
 
-template <int DA, int DC>
+template <int DA, int DC, bool FULL>
 __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_constant__ ScanTcParams p) {
   constexpr int kTileB = kHalf * DA * 2, kStage = StateSmem<DA, DC>::kStage, kSlots = StateSmem<DA, DC>::kSlots;
   constexpr uint32_t kColU = 2 * DA;  // columns between the accumulators: first terms' sums, then the others'
@@ -695,6 +699,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   // channels reads into behind the last stage: rows of its product not used)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u, rest = base + kSlots * kStage;
   const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
+  const int Da = FULL ? DA : p.s.Da, Dc = FULL ? DC : p.s.Dc;
 
   if (tid == 0) {
     for (int s = 0; s < kSlots; ++s) {
@@ -766,9 +771,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
           mbar_arrive_expect_tx(fb, kStage);
           if (i + 1 == p.withhold1) continue;
 #pragma unroll
-          for (int x = 0; x < DA; x += 64) tma_load_2d(to + x / 64 * kHalfPanel, &p.mb, pc.head * DA + x, t, fb);
+          for (int x = 0; x < DA; x += 64) tma_load_3d(to + x / 64 * kHalfPanel, &p.mb, x, pc.head, t, fb);
 #pragma unroll
-          for (int x = 0; x < DC; x += 64) tma_load_2d(to + kTileB + x / 64 * kHalfPanel, &p.mc, pc.head * DC + x, t, fb);
+          for (int x = 0; x < DC; x += 64) tma_load_3d(to + kTileB + x / 64 * kHalfPanel, &p.mc, x, pc.head, t, fb);
         }
         if (!live || !ok) break;
         // the next piece, which its first halves' barriers publish; behind
@@ -899,17 +904,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
         if (n > 0) add(n - 1, m - 1);
       }
       add(nchunk - 1, m - 1);
-      if (row < DC) {
-        float* to = p.s.piece_state + (long long)pc.id * DA * DC;
+      if (row < Dc) {
+        float* to = p.s.piece_state + (long long)pc.id * Da * Dc;
         const float nan = __int_as_float(0x7fc00000);
         if (p.s.transposed) {
 #pragma unroll
           for (int d = 0; d < DQ; d += 4)
-            *reinterpret_cast<float4*>(to + (long long)row * DA + d0 + d) =
+            if (FULL || d0 + d < Da) *reinterpret_cast<float4*>(to + (long long)row * Da + d0 + d) =
                 ok ? make_float4(S[d], S[d + 1], S[d + 2], S[d + 3]) : make_float4(nan, nan, nan, nan);
         } else {
 #pragma unroll
-          for (int d = 0; d < DQ; ++d) to[(d0 + d) * DC + row] = ok ? S[d] : nan;
+          for (int d = 0; d < DQ; ++d)
+            if (FULL || d0 + d < Da) to[(d0 + d) * Dc + row] = ok ? S[d] : nan;
         }
       }
       // the next piece, in its first chunk's half of this group
@@ -929,54 +935,60 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   }
 }
 
-template <int DA, int DC, int TERMS>
+template <typename K>
+cudaError_t launch_tile(K kern, SmemOptIn& optin, int bytes, int threads, int64_t ctas, const ScanTcParams& p, const DeviceInfo& di,
+                        cudaStream_t stream) {
+  if (bytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
+  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), bytes);
+  return e != cudaSuccess ? e : launch_kernel(kern, dim3((unsigned)ctas), dim3(threads), (size_t)bytes, stream, p);
+}
+
+template <int DA, int DC, int TERMS, bool FULL>
 cudaError_t launch_scan_tile(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
-  constexpr int kBytes = ScanSmem<DA, DC, TERMS>::kBytes;
-  if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
-  const auto kern = scan_tc_kernel<DA, DC, TERMS>;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(p.s.parts > 0 ? p.s.parts * p.s.gang : p.s.N * p.s.H)), dim3(kScanThreads), (size_t)kBytes, stream, p);
+  return launch_tile(scan_tc_kernel<DA, DC, TERMS, FULL>, optin, ScanSmem<DA, DC, TERMS>::kBytes, kScanThreads,
+                     p.s.parts > 0 ? p.s.parts * p.s.gang : (int64_t)p.s.N * p.s.H, p, di, stream);
 }
-
-template <int TERMS>
-cudaError_t launch_scan_dims(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
-  if (p.s.Da == 128)
-    return p.s.Dc == 128 ? launch_scan_tile<128, 128, TERMS>(p, di, stream) : launch_scan_tile<128, 64, TERMS>(p, di, stream);
-  return p.s.Dc == 128 ? launch_scan_tile<64, 128, TERMS>(p, di, stream) : launch_scan_tile<64, 64, TERMS>(p, di, stream);
-}
-
 template <int DA, int DC>
+cudaError_t launch_scan_size(const ScanTcParams& p, bool three, const DeviceInfo& di, cudaStream_t stream) {
+  const bool full = p.s.Da == DA && p.s.Dc == DC;
+  if (three) return full ? launch_scan_tile<DA, DC, 3, true>(p, di, stream) : launch_scan_tile<DA, DC, 3, false>(p, di, stream);
+  return full ? launch_scan_tile<DA, DC, 2, true>(p, di, stream) : launch_scan_tile<DA, DC, 2, false>(p, di, stream);
+}
+cudaError_t launch_scan_dims(const ScanTcParams& p, bool three, const DeviceInfo& di, cudaStream_t stream) {
+  if (p.s.Da > 64) return p.s.Dc > 64 ? launch_scan_size<128, 128>(p, three, di, stream) : launch_scan_size<128, 64>(p, three, di, stream);
+  return p.s.Dc > 64 ? launch_scan_size<64, 128>(p, three, di, stream) : launch_scan_size<64, 64>(p, three, di, stream);
+}
+
+template <int DA, int DC, bool FULL>
 cudaError_t launch_state_tile(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
-  constexpr int kBytes = StateSmem<DA, DC>::kBytes;
-  if (kBytes + 2048 > di.max_smem_optin) return cudaErrorInvalidValue;
   static SmemOptIn optin;
-  const auto kern = state_tc_kernel<DA, DC>;
-  const cudaError_t e = optin.ensure(reinterpret_cast<const void*>(kern), kBytes);
-  if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3((unsigned)(p.s.parts * p.s.gang)), dim3(kTileThreads), (size_t)kBytes, stream, p);
+  return launch_tile(state_tc_kernel<DA, DC, FULL>, optin, StateSmem<DA, DC>::kBytes, kTileThreads, (int64_t)p.s.parts * p.s.gang, p, di, stream);
 }
-
+template <int DA, int DC>
+cudaError_t launch_state_size(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
+  return p.s.Da == DA && p.s.Dc == DC ? launch_state_tile<DA, DC, true>(p, di, stream) : launch_state_tile<DA, DC, false>(p, di, stream);
+}
 cudaError_t launch_state_dims(const ScanTcParams& p, const DeviceInfo& di, cudaStream_t stream) {
-  if (p.s.Da == 128) return p.s.Dc == 128 ? launch_state_tile<128, 128>(p, di, stream) : launch_state_tile<128, 64>(p, di, stream);
-  return p.s.Dc == 128 ? launch_state_tile<64, 128>(p, di, stream) : launch_state_tile<64, 64>(p, di, stream);
+  if (p.s.Da > 64) return p.s.Dc > 64 ? launch_state_size<128, 128>(p, di, stream) : launch_state_size<128, 64>(p, di, stream);
+  return p.s.Dc > 64 ? launch_state_size<64, 128>(p, di, stream) : launch_state_size<64, 64>(p, di, stream);
 }
 
-bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int64_t width, int64_t stride, int tokens = kC) {
-  const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)T};
-  const cuuint64_t strides[1] = {(cuuint64_t)stride * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)tokens};
-  return make_tensor_map(m, ptr, 2, dims, strides, box);
+// [T, H, D] with tokens `stride` elements apart, boxes of 64 channels of a head
+bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int H, int D, int64_t stride, int tokens = kC) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)tokens};
+  return make_tensor_map(m, ptr, 3, dims, strides, box);
 }
 
 }  // namespace
 
-bool scan_tc_dims(int Dk, int Dv, int dtype) { return dtype == ATTNRES_BF16 && (Dk == 64 || Dk == 128) && (Dv == 64 || Dv == 128); }
+bool scan_tc_dims(int Dk, int Dv, int dtype) { return dtype == ATTNRES_BF16 && Dk <= 128 && Dv <= 128 && Dk % 16 == 0 && Dv % 16 == 0; }
 
 // (a chunk's HBM time on one of 152 SMs is 23 ns per channel)
 static Cut scan_tc_cut(int64_t T, int H, int Dk, int Dv, int N, int sm_count) {
-  return choose_cut(T, H, Dk, Dv, N, kC, 1, sm_count, 0.55, 23. * (Dk > Dv ? Dk : Dv));
+  return choose_cut(T, H, Dk, Dv, N, kC, 1, sm_count, 0.55, 23. * (Dk > 64 || Dv > 64 ? 128 : 64));
 }
 
 bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N) {
@@ -1004,8 +1016,8 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, 
   ScanTcParams p{};
   p.s = s;
   p.s.wide_out = (reinterpret_cast<uintptr_t>(s.out) & 31) == 0 && s.os % 16 == 0;
-  if (!token_map(&p.ma, s.a, s.T, (int64_t)s.H * s.Da, s.as) || !token_map(&p.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs) ||
-      !token_map(&p.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs))
+  if (!token_map(&p.ma, s.a, s.T, s.H, s.Da, s.as) || !token_map(&p.mb, s.b, s.T, s.H, s.Da, s.bs) ||
+      !token_map(&p.mc, s.c, s.T, s.H, s.Dc, s.cs))
     return cudaErrorInvalidValue;
   p.dev_err = dev_err;
   p.wait_ns = wait_limit_ns();
@@ -1019,13 +1031,13 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, 
     if (ready < kTables) e = launch_piece_plan(p.s, stream);
     if (e != cudaSuccess) return e;
     ScanTcParams ps = p;
-    if (!token_map(&ps.mb, s.b, s.T, (int64_t)s.H * s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, (int64_t)s.H * s.Dc, s.cs, kHalf))
+    if (!token_map(&ps.mb, s.b, s.T, s.H, s.Da, s.bs, kHalf) || !token_map(&ps.mc, s.c, s.T, s.H, s.Dc, s.cs, kHalf))
       return cudaErrorInvalidValue;
     e = launch_state_dims(ps, di, stream);
     if (e == cudaSuccess) e = launch_piece_combine(p.s, stream);
     if (e != cudaSuccess) return e;
   }
-  return s.s_out && p.s.parts == 0 ? launch_scan_dims<3>(p, di, stream) : launch_scan_dims<2>(p, di, stream);
+  return launch_scan_dims(p, s.s_out && p.s.parts == 0, di, stream);
 }
 
 }  // namespace attnres

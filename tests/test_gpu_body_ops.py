@@ -293,6 +293,7 @@ ATT = [  # T, sequences, H, Dk, Dv
     (700, 9, 1, 64, 64), (1000, 1, 1, 128, 128), (200, 30, 2, 128, 128), (77, 3, 2, 96, 160), (70, 2, 1, 37, 5), (50, 2, 2, 1, 256),
     (90, 1, 1, 256, 33),
     (2000, 1, 2, 128, 128), (4100, 5, 1, 64, 128), (3001, 3, 2, 40, 24),  # long enough to be cut into pieces
+    (300, 4, 2, 96, 96), (2000, 2, 2, 96, 80), (500, 3, 2, 32, 112), (140, 2, 1, 16, 16), (3001, 3, 2, 80, 48),
 ]
 
 
@@ -415,7 +416,7 @@ def test_one_sequence_does_not_reach_another(A):
     assert torch.isnan(out2[100:200]).all() and torch.isnan(fin2[1]).all()
 
 
-@pytest.mark.parametrize("dt,D,T", [(torch.bfloat16, 128, 300), (torch.bfloat16, 64, 6000), (torch.float32, 40, 150),
+@pytest.mark.parametrize("dt,D,T", [(torch.bfloat16, 128, 300), (torch.bfloat16, 64, 6000), (torch.bfloat16, 96, 300), (torch.float32, 40, 150),
                                     (torch.bfloat16, 24, 6000)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_no_token_reaches_an_earlier_one(A, dt, D, T, bad):
