@@ -16,6 +16,8 @@ gradient for bf16 sources is rounded to bf16 first.
 names the same way: nothing but the inputs is kept, the backward recomputes
 what it needs, incoming gradients are taken in the tensors' dtype, and
 gradients nobody asks for are not formed.  They can be differentiated once.
+Before a backward is captured in a CUDA graph, let go of eager graphs of the
+same leaves (torch runs their accumulation on the stream they were made on).
 """
 from __future__ import annotations
 

@@ -39,7 +39,8 @@ constexpr int kSPitchP = kSC + 4;
 // Rows lie 16 bytes further apart than their length (no bank conflicts
 // between a tile's rows).  The bound is the FMA rate, of which shared-memory
 // loads leave about half (8192 tokens of 3 sequences, 24 heads of 128 in fp32:
-// 999 us in even ranges, 1157 with the sequences cut into lengths of one size).
+// 875 us; 999 with one vector per thread on its way, 1157 with the sequences
+// cut into lengths of one size).
 __host__ __device__ constexpr int scan_rows(int Da) { return (Da + 3) / 4 * 4 + 4; }  // pitch of a and b
 __host__ constexpr int scan_smem(int Da, int nc) {  // nc columns of c
   const int d = (Da + 63) / 64 * 64;  // the state's rows, whole tiles

@@ -32,7 +32,7 @@
 // Bound: HBM, with the arithmetic warps close behind.  A chunk of 128 x 128
 // heads takes about 5500 cycles of HBM time per SM, its five products 2600 of
 // the tensor cores, and the warps that turn scores into P and write outputs
-// about 6000.  16384 tokens x 56 heads of 128: the scan 168 us (5.6 TB/s), the
+// about 6000.  16384 tokens x 56 heads of 128: the scan 170 us (5.5 TB/s), the
 // pieces' states 92 us (5.1 TB/s), joining them 10 us.
 #include <math.h>
 
