@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
 #pragma unroll
   for (int k = 0; k < VEC; ++k) w[k] = p.s_in ? p.s_in[n * all + e + k] : 0.f;
   // four pieces' states are loaded before the first of them is replaced
-  constexpr int kAhead = VEC == 8 ? 2 : 4;
+  constexpr int kAhead = 4;
   for (int i = i0; i < i1; i += kAhead) {
     float u[kAhead][VEC], d[kAhead];
 #pragma unroll
@@ -445,12 +445,9 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
         d[j] = decay_pow(g, pc.len);
         const float* at = at0 + (i + j) * step;
         if (!pc.last || (p.s_out && !p.final_in_scan)) {
-          if constexpr (VEC > 1) {
-#pragma unroll
-            for (int k = 0; k < VEC; k += 4) {
-              const float4 x = reinterpret_cast<const float4*>(at)[k / 4];
-              u[j][k] = x.x, u[j][k + 1] = x.y, u[j][k + 2] = x.z, u[j][k + 3] = x.w;
-            }
+          if constexpr (VEC == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at);
+            u[j][0] = x.x, u[j][1] = x.y, u[j][2] = x.z, u[j][3] = x.w;
           } else {
             u[j][0] = *at;
           }
@@ -461,10 +458,9 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
     for (int j = 0; j < kAhead; ++j) {
       if (i + j < i1) {
         float* at = at0 + (i + j) * step;
-        if constexpr (VEC > 1) {
-#pragma unroll
-          for (int k = 0; k < VEC; k += 4) reinterpret_cast<float4*>(at)[k / 4] = make_float4(w[k], w[k + 1], w[k + 2], w[k + 3]);
-        } else
+        if constexpr (VEC == 4)
+          *reinterpret_cast<float4*>(at) = make_float4(w[0], w[1], w[2], w[3]);
+        else
           *at = w[0];
       }
 #pragma unroll
@@ -676,8 +672,8 @@ cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream) {
 cudaError_t launch_piece_combine(const ScanArgs& s, cudaStream_t stream) {
   const int per_head = s.Da * s.Dc;
   const int64_t all = (int64_t)s.H * per_head;
-  if (per_head % 8 == 0)
-    return launch_kernel(la_combine_kernel<8>, dim3((unsigned)((all / 8 + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
+  if (per_head % 4 == 0)
+    return launch_kernel(la_combine_kernel<4>, dim3((unsigned)((all / 4 + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
   return launch_kernel(la_combine_kernel<1>, dim3((unsigned)((all + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
 }
 
