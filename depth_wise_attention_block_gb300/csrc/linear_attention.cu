@@ -430,8 +430,8 @@ __global__ void __launch_bounds__(256) la_combine_kernel(const __grid_constant__
   float w[VEC];
 #pragma unroll
   for (int k = 0; k < VEC; ++k) w[k] = p.s_in ? p.s_in[n * all + e + k] : 0.f;
-  // four pieces' states are loaded before the first of them is replaced
-  constexpr int kAhead = 4;
+  // several pieces' states are loaded before the first of them is replaced
+  constexpr int kAhead = VEC == 4 ? 4 : 16;
   for (int i = i0; i < i1; i += kAhead) {
     float u[kAhead][VEC], d[kAhead];
 #pragma unroll
@@ -672,7 +672,13 @@ cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream) {
 cudaError_t launch_piece_combine(const ScanArgs& s, cudaStream_t stream) {
   const int per_head = s.Da * s.Dc;
   const int64_t all = (int64_t)s.H * per_head;
-  if (per_head % 4 == 0)
+  // four values per thread where that gives every SM a CTA; else one, with
+  // more of a sequence's pieces at a time (8192 tokens of 4 heads of 128 in
+  // fp32: the whole call 190 us with four, 182 with one)
+  DeviceInfo di;
+  const cudaError_t e = device_info(&di);
+  if (e != cudaSuccess) return e;
+  if (per_head % 4 == 0 && all * s.N >= 4 * 256 * (int64_t)di.sm_count)
     return launch_kernel(la_combine_kernel<4>, dim3((unsigned)((all / 4 + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
   return launch_kernel(la_combine_kernel<1>, dim3((unsigned)((all + 255) / 256), s.N), dim3(256), 0, stream, s, per_head);
 }
