@@ -472,6 +472,11 @@ def _device_of(t, name: str) -> int:
     return dev
 
 
+def _stream_on(stream, cur: int) -> int:
+    """_stream_ptr where the current device is known."""
+    return _RAW_STREAM(cur) if stream is None and _RAW_STREAM is not None else _stream_ptr(stream)
+
+
 def _where(t, name: str, dtype: torch.dtype, cur: int) -> None:
     """Say what is wrong with a tensor that is not of `dtype` on device `cur`."""
     _dev_ptr(t, name, dtype, contiguous=False)
@@ -564,7 +569,7 @@ def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: to
     need = 0 if workspace is not None else attnres_linear_workspace_size(M, N, K, dt)
     _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
     rc = _N.lib.attnres_linear(xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), rp, ldr, op, ldo, M, N, K, code, act,
-                               ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+                               ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_linear")
 
 
@@ -596,7 +601,7 @@ def attnres_linear_backward(x: torch.Tensor, w: torch.Tensor, grad_out: torch.Te
     rc = _N.lib.attnres_linear_backward(
         xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), gp, ldg, _vec(grad_x, "grad_x", (M, K), dt, cur),
         _vec(grad_w, "grad_w", (N, K), dt, cur), _vec(grad_bias, "grad_bias", (N,), torch.float32, cur), M, N, K, code, act, ws,
-        nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+        nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_linear_backward")
 
 
@@ -641,7 +646,7 @@ def attnres_qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, q_out: 
     ko, kos = _rows(k_out if k is not None else None, "k_out", (T, Hk, D), dt, cur)
     rc = _N.lib.attnres_qk_norm_rope(qp, qs, Hq, kp, ks, Hk, T, D, code, _vec(q_gain, "q_gain", (D,), torch.float32, cur),
                                      _vec(k_gain, "k_gain", (D,), torch.float32, cur), float(eps), pos, freq, rot, inter,
-                                     qo, qos, ko, kos, _stream_ptr(stream))
+                                     qo, qos, ko, kos, _stream_on(stream, cur))
     _N.check(rc, "attnres_qk_norm_rope")
 
 
@@ -681,7 +686,7 @@ def attnres_qk_norm_rope_backward(q: torch.Tensor | None, k: torch.Tensor | None
     rc = _N.lib.attnres_qk_norm_rope_backward(
         qp, qs, Hq, kp, ks, Hk, T, D, code, _vec(q_gain, "q_gain", (D,), torch.float32, cur),
         _vec(k_gain, "k_gain", (D,), torch.float32, cur), float(eps), pos, freq, rot, inter, gqo, gqos, gko, gkos, gq, gqs,
-        gk, gks, dgq, dgk, ws, nbytes, _stream_ptr(stream))
+        gk, gks, dgq, dgk, ws, nbytes, _stream_on(stream, cur))
     _N.check(rc, "attnres_qk_norm_rope_backward")
 
 
@@ -733,7 +738,7 @@ def attnres_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     need = 0 if workspace is not None else attnres_linear_attention_workspace_size(T, H, Dk, Dv, dt, N)
     _keep, ws, nbytes = _workspace(workspace, need, q.device, stream)
     rc = _N.lib.attnres_linear_attention(*head, cu, N, s0, s1, float(Dk ** -0.5 if scale is None else scale), op, os_,
-                                         ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+                                         ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_linear_attention")
 
 
@@ -766,7 +771,7 @@ def attnres_linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch
     rc = _N.lib.attnres_linear_attention_backward(
         *head, cu, N, s0, float(Dk ** -0.5 if scale is None else scale), gp, gs, ds1, _vec(grad_q, "grad_q", (T, H, Dk), dt, cur),
         _vec(grad_k, "grad_k", (T, H, Dk), dt, cur), _vec(grad_v, "grad_v", (T, H, Dv), dt, cur), ds0, ws, nbytes,
-        _dev_ptr(dev_err, "dev_err", torch.int32), _stream_ptr(stream))
+        _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_linear_attention_backward")
 
 
@@ -786,5 +791,5 @@ def attnres_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
     sp = _vec(state, "state", (num_slots, H, Dk, Dv), torch.float32, cur)
     rc = _N.lib.attnres_linear_attention_step(*head, sp, num_slots, _vec(slots, "slots", (B,), torch.int32, cur),
                                               float(Dk ** -0.5 if scale is None else scale), op, os_,
-                                              _stream_ptr(stream))
+                                              _stream_on(stream, cur))
     _N.check(rc, "attnres_linear_attention_step")
