@@ -156,6 +156,24 @@ __device__ __noinline__ void poison_range(const ScanArgs& s, int cta, int lane) 
   }
 }
 
+// mbar_wait_bounded with one try in the code: the roles' waits are many, and
+// they share the instruction cache.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  uint64_t t0 = 0;
+#pragma unroll 1
+  for (uint32_t it = 0; it < kWaitMaxPolls; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 31u) == 0) {
+      const uint64_t t = global_timer_ns();
+      if (it == 0)
+        t0 = t;
+      else if (t - t0 > limit_ns)
+        return false;
+    }
+  }
+  return false;
+}
+
 // FULL: the head sizes are DA and DC.  TERMS: bf16 terms of b's weighted rows, 3 where the state is a result, 2
 // where only bf16 outputs follow from it.
 template <int DA, int DC, int TERMS, bool FULL>
@@ -223,7 +241,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   // once a wait runs out, the others of this thread return at once
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_wait_bounded(smem_addr(bar), parity & 1u, p.wait_ns)) {
+    if (ok && !poll(smem_addr(bar), parity & 1u, p.wait_ns)) {
       report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
       ok = false;
     }
@@ -737,7 +755,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) state_tc_kernel(const __grid_
   auto chunk_at = [&](int n) { return rev ? pc.first + pc.len - n * kC - chunk_len(n) : pc.first + n * kC; };
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (ok && !mbar_wait_bounded(smem_addr(bar), parity & 1u, p.wait_ns)) {
+    if (ok && !poll(smem_addr(bar), parity & 1u, p.wait_ns)) {
       report_error(p.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
       ok = false;
     }
