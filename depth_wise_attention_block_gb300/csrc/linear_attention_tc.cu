@@ -109,7 +109,7 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
 // mask leaves alone, channels c0 .. c1 - 1: where the products, in which a
 // masked row counts as 0 times its values, met an infinity or a NaN.  o2: the
 // row's a S in TMEM, which a whole warp reads; `bad`: this lane's row is
-// redone; l: p_scale l^distance.
+// redone; l: the table of p_scale l^distance.
 __device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint32_t o2, long long t0, int h, int row, int len, int c0, int c1,
                                         float coef, bool bad) {
   for (; c0 < c1; c0 += 16) {
@@ -126,7 +126,7 @@ __device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint3
       const bf16_t* c = static_cast<const bf16_t*>(s.c) + (t0 + j) * s.cs + (long long)h * s.Dc + c0;
       float dot = 0.f;
       for (int d = 0; d < s.Da; ++d) dot = fmaf(load_elem(a + d), load_elem(b + d), dot);
-      const float f = bf16lo(pack_bf16x2(dot * l[s.reverse ? j - row : row - j], 0.f));
+      const float f = bf16lo(pack_bf16x2(dot * l[s.reverse ? j - row : kC - 1 - row + j], 0.f));
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = fmaf(f, load_elem(c + k), x[k]);
     }
@@ -185,9 +185,10 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, b_ready, u_full, u_free;
   __shared__ __align__(8) uint64_t t_ready, drained[2];
   __shared__ uint32_t tmem_base;
-  // l^i, and p_scale l^i behind it: distances below 0, which the mask covers
-  // and which reach -46, read into the first
-  __shared__ float pw[2 * kC + 4];
+  // l^i; and p_scale l^distance in the order of a row's columns: distances
+  // below 0, which the mask covers, read up to 46 places before it (reversed)
+  // or behind it
+  __shared__ float pw[2 * kC + 4 + 48];
   float* const tab = pw + kC + 4;
   __shared__ Piece pieces[kPieces];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -420,7 +421,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       if (tid < kC + 4) {
         const float l = decay_pow(g, tid);
         pw[tid] = l;
-        if (tid < kC) tab[tid] = p.s.p_scale * l;
+        if (tid < kC) tab[rev ? tid : kC - 1 - tid] = p.s.p_scale * l;
       }
       meet();
     };
@@ -507,24 +508,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
             } else {
               uint32_t v[16];
               tmem_ld16(lanes_at + kColP + j0, v);
-              // 0 where the mask is; a reversed scan's distances grow with the column
-              const float* t = tab + (rev ? j0 - row : row - j0 - 15);
-              float f[16];
+              // the powers of 16 columns' distances (masked ones: whatever lies there)
+            const float* t = tab + (rev ? j0 - row : kC - 1 - row + j0);
+            float f[16];
 #pragma unroll
-              for (int k = 0; k < 16; ++k) f[k] = t[k];
-              tmem_ld_wait();
-              if (rev) {
+            for (int k = 0; k < 16; ++k) f[k] = t[k];
+            tmem_ld_wait();
 #pragma unroll
-                for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
-              } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const float x = f[15 - k] * __uint_as_float(v[k]), y = f[k] * __uint_as_float(v[15 - k]);
-                  f[k] = x;
-                  f[15 - k] = y;
-                }
-              }
-              if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
+            for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
+            if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
                 const int last = rev ? len : row + 1, first = rev ? row : 0;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
