@@ -27,12 +27,14 @@
 // range (it reads b and c only), la_combine_kernel runs through a sequence's
 // pieces and leaves the state before each, and the scan runs over the ranges.
 // The loads run ahead from piece to piece; a table in shared memory tells the
-// other warps of each.
+// other warps of each.  Code and registers are kept small: the roles share the
+// instruction cache (unrolling the scores' loop twice cost 4 %), and pieces
+// held in registers 8 %.
 //
 // Bound: HBM, with the arithmetic warps close behind.  A chunk of 128 x 128
 // heads takes about 5500 cycles of HBM time per SM, its five products 2600 of
 // the tensor cores, and the warps that turn scores into P and write outputs
-// about 6000.  16384 tokens x 56 heads of 128: the scan 170 us (5.5 TB/s), the
+// about 6000.  16384 tokens x 56 heads of 128: the scan 166 us (5.7 TB/s), the
 // pieces' states 92 us (5.1 TB/s), joining them 10 us.
 #include <math.h>
 
@@ -315,7 +317,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
       wait_tile(it + 1);
       tc_fence_after();
       const uint64_t da = smem_desc_k128(slot(it)), db = smem_desc_k128(slot(it + 1));
-#pragma unroll
+#pragma unroll 4
       for (int kk = 0; kk < DA / 16; ++kk) {
         const uint32_t off = (kk / 4 * kPanel + kk % 4 * 32) / 16;
         tc_mma_bf16_warp(tmem + kColP, da + off, db + off, kI1, kk > 0);
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         warp_wait(&o_free, ph + 1);
         tc_fence_after();
         const uint64_t da = smem_desc_k128(slot(it)), ds = smem_desc_k128(s_buf);
-#pragma unroll
+#pragma unroll 4
         for (int kk = 0; kk < DA / 16; ++kk)
           tc_mma_bf16_warp(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
         commit(&empty[it % kSlots]);
@@ -346,7 +348,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         if (left < kC) warp_wait(&b_ready, ph);
         warp_wait(&p_ready, ph);
         tc_fence_after();
-#pragma unroll
+#pragma unroll 4
         for (int kk = 0; kk < kC / 16; ++kk)
           tc_mma_bf16_ts_warp(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
         commit(&o_full);
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint64_t dt = smem_desc_mn128(term == 0 ? b0 : rest + (term - 1) * (kC * DA * 2), kPanel);
-#pragma unroll
+#pragma unroll 4
           for (int kk = 0; kk < kC / 16; ++kk) tc_mma_bf16_warp(tmem + kColU, dc + kk * 128, dt + kk * 128, kI4, term > 0 || kk > 0);
         }
         commit(&u_full);
