@@ -359,8 +359,12 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
 
 int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype) {
   if (small_fp32(M, N, K, dtype) || (dtype == ATTNRES_BF16 && K % 8 == 0)) return 0;
+  if (M == 0) return 0;
   const int np = dtype == ATTNRES_BF16 ? 1 : 3;
-  return tc_prep_bytes(M, K, np) + tc_prep_bytes(N, K, np);
+  DeviceInfo di;
+  // (without a device: enough for any plan)
+  const bool fused = np == 3 && device_info(&di) == cudaSuccess && tc_plan(M, N, K, np, di.sm_count).fused;
+  return tc_prep_bytes(M, K, np) + (fused ? 0 : tc_prep_bytes(N, K, np));
 }
 
 int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act) {
