@@ -10,7 +10,7 @@
 // Every product is a tcgen05.mma with its accumulator in TMEM.  a, b and c
 // arrive by TMA in the 128-byte swizzle and serve K-major (a b^T, a S) or
 // MN-major (P c, the token sums) from the same tile.  Eight warps turn the
-// scores into P (bf16, back into TMEM as the next product's operand) and
+// scores into P (two bf16 terms, back into TMEM as the next product's operand) and
 // write the outputs; eight warps hold the state in fp32 registers (half a
 // row of Da per thread) and give it to the products rounded to bf16; all of
 // them weigh b with the decays.  The weighted rows enter as three bf16 terms
@@ -34,7 +34,7 @@
 // Bound: HBM, with the arithmetic warps close behind.  A chunk of 128 x 128
 // heads takes about 5500 cycles of HBM time per SM, its five products 2600 of
 // the tensor cores, and the warps that turn scores into P and write outputs
-// about 6000.  16384 tokens x 56 heads of 128: the scan 166 us (5.7 TB/s), the
+// about 6000.  16384 tokens x 56 heads of 128: the scan 181 us (5.2 TB/s), the
 // pieces' states 92 us (5.1 TB/s), joining them 10 us.
 #include <math.h>
 
@@ -128,7 +128,7 @@ __device__ __noinline__ void masked_row(const ScanArgs& s, const float* l, uint3
       const bf16_t* c = static_cast<const bf16_t*>(s.c) + (t0 + j) * s.cs + (long long)h * s.Dc + c0;
       float dot = 0.f;
       for (int d = 0; d < s.Da; ++d) dot = fmaf(load_elem(a + d), load_elem(b + d), dot);
-      const float f = bf16lo(pack_bf16x2(dot * l[s.reverse ? j - row : kC - 1 - row + j], 0.f));
+      const float f = dot * l[s.reverse ? j - row : kC - 1 - row + j];
 #pragma unroll
       for (int k = 0; k < 16; ++k) x[k] = fmaf(f, load_elem(c + k), x[k]);
     }
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         tc_fence_after();
 #pragma unroll 4
         for (int kk = 0; kk < kC / 16; ++kk)
-          tc_mma_bf16_ts_warp(tmem + kColO1, tmem + kColP + kk / 4 * 64 + kk % 4 * 8, dc + kk * 128, kI2, kk > 0);
+          for (int lo = 0; lo < 2; ++lo) tc_mma_bf16_ts_warp(tmem + kColO1, tmem + kColP + kk * 16 + lo * 8, dc + kk * 128, kI2, lo > 0 || kk > 0);
         commit(&o_full);
         commit(&empty[ic % kSlots]);
         if (left > kC) {
@@ -498,15 +498,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
           warp_wait(&p_full, m);
           tc_fence_after();
           // 16 columns at a time (a short loop: the warps of the roles share
-          // the instruction cache); each half's P lies over the first half of
-          // its own scores
+          // the instruction cache); P's two bf16 terms lie over their scores
+          // (one term, rounded once more than the output, gives 1.4 times the
+          // error of the output's rounding alone)
 #pragma unroll 1
           for (int b = 0; b < 4; ++b) {
             const int j0 = half * 64 + b * 16, lo_row = 32 * quarter;
-            uint32_t w[8];
+            uint32_t w[16];
             if (rev ? j0 + 15 < lo_row || j0 >= len : j0 > lo_row + 31) {  // empty for all of the warp's rows
 #pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = 0;
+              for (int k = 0; k < 16; ++k) w[k] = 0;
             } else {
               uint32_t v[16];
               tmem_ld16(lanes_at + kColP + j0, v);
@@ -524,9 +525,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
                 for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
               }
 #pragma unroll
-              for (int k = 0; k < 8; ++k) w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+              for (int k = 0; k < 8; ++k) {
+                w[k] = pack_bf16x2(f[2 * k], f[2 * k + 1]);
+                w[8 + k] = pack_bf16x2(f[2 * k] - bf16lo(w[k]), f[2 * k + 1] - bf16hi(w[k]));
+              }
             }
-            tmem_st8(lanes_at + kColP + half * 64 + b * 8, w);
+            tmem_st8(lanes_at + kColP + j0, w);
+            tmem_st8(lanes_at + kColP + j0 + 8, w + 8);
           }
           tmem_st_wait();
           tc_fence_before();
