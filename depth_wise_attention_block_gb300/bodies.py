@@ -9,6 +9,7 @@ be captured in a CUDA graph with the stack around them.
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
 from dataclasses import dataclass
 from typing import Sequence
 
@@ -39,6 +40,13 @@ class LinearAttentionWeights:
     k_gain: torch.Tensor | None = None
 
 
+def _on(stream):
+    """Makes torch's calls run on `stream` (None: the current one)."""
+    if stream is None:
+        return nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream)))
+
+
 class LinearAttentionBody:
     """The body of every layer of one stack over T rows.
 
@@ -52,7 +60,8 @@ class LinearAttentionBody:
     Prompts: cu_seqlens [n + 1] int32 on the device cuts the T rows into
     sequences (None: one).  Decoding (decode=True): row b is the next token of
     the sequence in slot slots[b] ([T] int32; None: slot b).  Rows outside
-    every sequence or slot give v = b_out.
+    every sequence or slot give v = b_out.  A caller may overwrite both between
+    forwards, captured or not (not between the layers of one).
 
     The body's buffers and workspace belong to one forward at a time: two
     stacks, or two captured graphs of one, that run at once need a body each.
@@ -80,8 +89,10 @@ class LinearAttentionBody:
         self.q = self.qkv[:, :heads * Dk].unflatten(1, (heads, Dk))
         self.k = self.qkv[:, heads * Dk:2 * heads * Dk].unflatten(1, (heads, Dk))
         self.v = self.qkv[:, 2 * heads * Dk:].unflatten(1, (heads, Dv))
-        # rows outside every sequence or slot are never written: zero
+        # the attention leaves rows outside every sequence or slot as they are:
+        # zero, by each forward's first layer (issue)
         self.o = torch.zeros((T, heads, Dv), dtype=dt, device=dev)
+        self._goes_on = None  # the layer that goes on from the last one issued
         n = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
         need = [attnres_linear_workspace_size(T, width, d, dt), attnres_linear_workspace_size(T, d, heads * Dv, dt)]
         if not decode:
@@ -91,6 +102,12 @@ class LinearAttentionBody:
 
     def issue(self, layer: int, r: torch.Tensor, F: torch.Tensor, stream=None) -> None:
         w, state = self.layers[layer - 1], self.states[layer - 1]
+        if layer != self._goes_on and (self.slots is not None or self.cu_seqlens is not None):
+            # a forward (or a stage's part of one) begins: a row may have been
+            # live in the last one and be padding now
+            with _on(stream):
+                self.o.zero_()
+        self._goes_on = layer + 1
         attnres_linear(r, w.w_qkv, self.qkv, bias=w.b_qkv, workspace=self.workspace, dev_err=self.dev_err, stream=stream)
         attnres_qk_norm_rope(self.q, self.k, self.q, self.k, q_gain=w.q_gain, k_gain=w.k_gain, eps=self.eps,
                              stream=stream, **self.rope)
