@@ -9,7 +9,7 @@ be captured in a CUDA graph with the stack around them.
 """
 from __future__ import annotations
 
-from contextlib import nullcontext
+from contextlib import contextmanager, nullcontext
 from dataclasses import dataclass
 from typing import Sequence
 
@@ -120,3 +120,18 @@ class LinearAttentionBody:
                                      workspace=self.workspace, dev_err=self.dev_err, stream=stream)
         attnres_linear(self.o.flatten(1), w.w_out, F, bias=w.b_out, workspace=self.workspace, dev_err=self.dev_err,
                        stream=stream)
+
+    @contextmanager
+    def idle(self):
+        """Within it no row is of any sequence or slot: forwards issue the same
+        kernels and change no state (StackForward.capture's eager run)."""
+        kept = self.slots, self.cu_seqlens
+        if self.decode:
+            self.slots = torch.full((self.o.shape[0],), -1, dtype=torch.int32, device=self.o.device)
+        else:
+            n = 1 if self.cu_seqlens is None else self.cu_seqlens.numel() - 1
+            self.cu_seqlens = torch.zeros(n + 1, dtype=torch.int32, device=self.o.device)
+        try:
+            yield
+        finally:
+            self.slots, self.cu_seqlens = kept

@@ -25,6 +25,8 @@ on a GB300 the 93-layer T = 2048 prefill then takes 4.35 ms against
 """
 from __future__ import annotations
 
+from contextlib import nullcontext
+
 import torch
 
 from . import (
@@ -87,7 +89,9 @@ class StackForward:
     Sc may then be None): an object whose `issue(layer, r, F, stream)` issues
     launches that write v_layer to F from r and write nothing of the state's
     rows (LinearAttentionBody is one).  With early_loads its last launch has
-    to meet that flag's conditions, as every call of the library does.
+    to meet that flag's conditions, as every call of the library does.  A body
+    that keeps a state from forward to forward has an `idle()`: a context in
+    which its launches leave that state as it is.
     """
 
     def __init__(self, h0, W, G, Sc, num_layers: int, block_size: int, eps: float = 1e-5,
@@ -270,8 +274,10 @@ class StackForward:
         return self.r
 
     def capture(self) -> None:
-        """Record the whole forward into a CUDA graph (after one eager run)."""
-        self._issue()
+        """Record the whole forward into a CUDA graph (after one eager run,
+        in which a body with a state is idle: recording advances no sequence)."""
+        with getattr(self.body, "idle", nullcontext)():
+            self._issue()
         torch.cuda.synchronize()
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):

@@ -90,3 +90,35 @@ def test_rows_that_become_padding_in_a_chunk_of_layers(A):
     for layer in (2, 3):
         body.issue(layer, r, F)
         assert (F[1] == body.layers[layer - 1].b_out.bfloat16()).all()
+
+
+@pytest.mark.parametrize("schedule", ["single", "hybrid"])
+@pytest.mark.parametrize("decode,T,n,index,dt,D", [
+    (True, 5, 5, None, torch.bfloat16, 64), (True, 5, 8, (7, 1, -1, 3, 1), torch.bfloat16, 128), (True, 3, 3, None, torch.float32, 24),
+    (False, 70, 1, None, torch.bfloat16, 64), (False, 300, 3, (0, 0, 120, 300), torch.bfloat16, 128),
+    (False, 6000, 1, None, torch.bfloat16, 128), (False, 6000, 2, (0, 90, 6000), torch.bfloat16, 64),
+    (False, 6000, 2, (0, 90, 6000), torch.float32, 24), (False, 200, 1, None, torch.float32, 24),
+])
+def test_capture_leaves_the_states(A, decode, T, n, index, dt, D, schedule):
+    """Recording a forward is not running one: the states after capture() are
+    the bits before it (an infinity and a NaN among them), and the first
+    replay is the first forward."""
+    index = None if index is None else _index(*index)
+    body, fwd, states = _make(T, n, decode, dt, D=D, index=index)
+    fwd_kw = dict(schedule=schedule, two_phase_from=2, keep_weights=False)
+    from depth_wise_attention_block_gb300.stack import StackForward
+    fwd = StackForward(fwd.state.h0, fwd.W, None, None, 3, 2, body=body, **fwd_kw)
+    start = states.clone()
+    odd = start.clone()
+    odd.view(-1)[3], odd.view(-1)[7] = float("inf"), float("nan")
+    states.copy_(odd)
+    fwd.capture()
+    torch.cuda.synchronize()
+    assert torch.equal(states.view(torch.int32), odd.view(torch.int32))
+    assert (body.slots if decode else body.cu_seqlens) is index
+    states.copy_(start)
+    got = [(fwd.run().clone(), states.clone()) for _ in range(2)]
+    states.copy_(start)
+    eager = StackForward(fwd.state.h0, fwd.W, None, None, 3, 2, body=body, **fwd_kw)
+    for r, s in got:
+        assert torch.equal(eager.run(), r) and torch.equal(states, s)
