@@ -117,21 +117,22 @@ class _QkNormRope(torch.autograd.Function):
     def forward(ctx, q, k, q_gain, k_gain, positions, inv_freq, interleaved, eps):
         q, k = _rows_contiguous(q), _rows_contiguous(k)
         outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
-        ctx.rope = dict(positions=positions, inv_freq=inv_freq, interleaved=interleaved, eps=eps)
-        attnres_qk_norm_rope(q, k, *outs, q_gain=q_gain, k_gain=k_gain, **ctx.rope)
-        ctx.save_for_backward(q, k, q_gain, k_gain)
+        ctx.rope = dict(interleaved=interleaved, eps=eps)
+        attnres_qk_norm_rope(q, k, *outs, q_gain=q_gain, k_gain=k_gain, positions=positions, inv_freq=inv_freq, **ctx.rope)
+        # (saved, so that torch refuses a backward whose angles were written over)
+        ctx.save_for_backward(q, k, q_gain, k_gain, positions, inv_freq)
         return tuple(outs)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, gq, gk):
-        q, k, q_gain, k_gain = ctx.saved_tensors
+        q, k, q_gain, k_gain, positions, inv_freq = ctx.saved_tensors
         grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
         gains = [torch.empty_like(g) if g is not None and need else None
                  for g, need in zip((q_gain, k_gain), ctx.needs_input_grad[2:4])]
         attnres_qk_norm_rope_backward(q, k, _rows_contiguous(gq.to(q.dtype)), _rows_contiguous(gk.to(k.dtype)), *grads,
                                       q_gain=q_gain, k_gain=k_gain, grad_q_gain=gains[0], grad_k_gain=gains[1],
-                                      **ctx.rope)
+                                      positions=positions, inv_freq=inv_freq, **ctx.rope)
         return (*grads, *gains, None, None, None, None)
 
 
