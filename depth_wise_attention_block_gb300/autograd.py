@@ -117,6 +117,8 @@ class _QkNormRope(torch.autograd.Function):
     def forward(ctx, q, k, q_gain, k_gain, positions, inv_freq, interleaved, eps):
         q, k = _rows_contiguous(q), _rows_contiguous(k)
         outs = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
+        if ctx.needs_input_grad[5]:
+            raise ValueError("inv_freq is a constant: it gets no gradient")
         ctx.rope = dict(interleaved=interleaved, eps=eps)
         attnres_qk_norm_rope(q, k, *outs, q_gain=q_gain, k_gain=k_gain, positions=positions, inv_freq=inv_freq, **ctx.rope)
         # (saved, so that torch refuses a backward whose angles were written over)

@@ -45,3 +45,10 @@ def test_angles_kept_give_the_gradients(F):
     with torch.no_grad():
         A.attnres_qk_norm_rope_backward(q, k, ga, gb, *want, positions=pos, inv_freq=freq)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_frequencies_get_no_gradient(F):
+    """Refused, not left out."""
+    q, k, pos, freq = _rope(F)
+    with pytest.raises(ValueError, match="constant"):
+        F.qk_norm_rope(q, k, positions=pos, inv_freq=freq.requires_grad_())
