@@ -750,15 +750,16 @@ def attnres_linear_attention_backward_workspace_size(T: int, H: int, Dk: int, Dv
 
 
 def attnres_linear_attention_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
-                                      grad_out: torch.Tensor, grad_q: torch.Tensor, grad_k: torch.Tensor,
-                                      grad_v: torch.Tensor, cu_seqlens: torch.Tensor | None = None,
+                                      grad_out: torch.Tensor, grad_q: torch.Tensor | None, grad_k: torch.Tensor | None,
+                                      grad_v: torch.Tensor | None, cu_seqlens: torch.Tensor | None = None,
                                       initial_state: torch.Tensor | None = None,
                                       grad_final_state: torch.Tensor | None = None,
                                       grad_initial_state: torch.Tensor | None = None, scale: float | None = None,
                                       workspace: torch.Tensor | None = None, dev_err: torch.Tensor | None = None,
                                       stream=None) -> None:
     """Gradients of attnres_linear_attention from the forward's inputs
-    (grad_q, grad_k, grad_v contiguous, of q's dtype; the states' float32)."""
+    (grad_q, grad_k, grad_v contiguous, of q's dtype; the states' float32).
+    Those that are None are not formed; grad_initial_state comes with grad_v."""
     cur = _device_of(q, "q")
     T, H, Dk, Dv, dt, head, cu, N = _attention_args(q, k, v, log_decay, cu_seqlens, cur)
     gp, gs = _rows(grad_out, "grad_out", (T, H, Dv), dt, cur)

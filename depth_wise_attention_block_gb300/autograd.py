@@ -129,10 +129,13 @@ class _QkNormRope(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, gq, gk):
         q, k, q_gain, k_gain, positions, inv_freq = ctx.saved_tensors
-        grads = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
-        gains = [torch.empty_like(g) if g is not None and need else None
-                 for g, need in zip((q_gain, k_gain), ctx.needs_input_grad[2:4])]
-        attnres_qk_norm_rope_backward(q, k, _rows_contiguous(gq.to(q.dtype)), _rows_contiguous(gk.to(k.dtype)), *grads,
+        need_q, need_k, need_qg, need_kg = ctx.needs_input_grad[:4]
+        # (a gain's gradient comes with its tensor's)
+        q, k = q if need_q or need_qg else None, k if need_k or need_kg else None
+        grads = [None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k)]
+        gains = [torch.empty_like(g) if need else None for g, need in ((q_gain, need_qg), (k_gain, need_kg))]
+        gq, gk = (None if t is None else _rows_contiguous(g.to(t.dtype)) for g, t in ((gq, q), (gk, k)))
+        attnres_qk_norm_rope_backward(q, k, gq, gk, *grads,
                                       q_gain=q_gain, k_gain=k_gain, grad_q_gain=gains[0], grad_k_gain=gains[1],
                                       positions=positions, inv_freq=inv_freq, **ctx.rope)
         return (*grads, *gains, None, None, None, None)
@@ -170,8 +173,11 @@ class _LinearAttention(torch.autograd.Function):
         if grad_out is None:
             grad_out = torch.zeros(v.shape, dtype=v.dtype, device=v.device)
         make = torch.empty if cu_seqlens is None else torch.zeros
-        grads = [make(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v)]
-        g0 = torch.empty_like(initial_state) if initial_state is not None and ctx.needs_input_grad[5] else None
+        need_q, need_k, need_v, _, _, need_0, _ = ctx.needs_input_grad
+        # (the initial state's gradient comes with v's)
+        grads = [make(t.shape, dtype=t.dtype, device=t.device) if need else None
+                 for t, need in ((q, need_q), (k, need_k), (v, need_v or need_0))]
+        g0 = torch.empty_like(initial_state) if need_0 else None
         attnres_linear_attention_backward(q, k, v, log_decay, _rows_contiguous(grad_out.to(v.dtype)), *grads,
                                           cu_seqlens=cu_seqlens, initial_state=initial_state,
                                           grad_final_state=None if grad_final is None else grad_final.contiguous(),

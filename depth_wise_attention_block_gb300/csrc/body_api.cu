@@ -436,7 +436,9 @@ int attnres_linear_attention_backward(const void* q, int64_t q_stride, const voi
                                       int64_t workspace_bytes, int* dev_err, void* stream) {
   int rc = check_la(q, q_stride, k, k_stride, v, v_stride, T, H, Dk, Dv, dtype, log_decay, cu_seqlens, num_seqs, scale);
   if (rc != ATTNRES_OK) return rc;
-  if (T > 0 && (!grad_out || !grad_q || !grad_k || !grad_v)) return fail(ATTNRES_EINVAL, "a gradient is NULL");
+  if (!grad_q && !grad_k && !grad_v && !grad_initial_state) return ok();
+  if (T > 0 && !grad_out) return fail(ATTNRES_EINVAL, "grad_out is NULL");
+  if (T > 0 && grad_initial_state && !grad_v) return fail(ATTNRES_EINVAL, "grad_initial_state comes with grad_v");
   if (!stride_ok(grad_out_stride, (int64_t)H * Dv))
     return fail(ATTNRES_EINVAL, "grad_out_stride is shorter than its row");
   if (!span_ok(T, grad_out_stride)) return fail(ATTNRES_ERANGE, "T*stride too large");

@@ -738,14 +738,16 @@ cudaError_t launch_linear_attention_backward(const LinAttnArgs& a) {
   // pieces it is formed once.  grad_initial_state may lie over
   // grad_final_state, so it is written after the last read of that: where
   // the pieces' states are joined, or by dv's scan (on the CUDA cores: by
-  // both, the former for empty sequences).
+  // both, the former for empty sequences).  It comes with dv, whose scan runs
+  // for it alone where there are no rows.
   const bool cut = tc ? scan_tc_in_pieces(a.T, a.H, a.Dk, a.Dv, a.N) : scan_any_in_pieces(a);
-  if (cut) k.s_out = a.ds0;
-  if (!cut || !tc) v.s_out = a.ds0;
+  if (cut && a.dk) k.s_out = a.ds0;
+  if (!cut || !tc || !a.dk) v.s_out = a.ds0;
   k.keep_final = true;
-  cudaError_t e = launch_scan(a, q, tc, kNothing);
-  if (e == cudaSuccess) e = launch_scan(a, k, tc, kTables);
-  if (e == cudaSuccess) e = launch_scan(a, v, tc, kStates);
+  cudaError_t e = cudaSuccess;
+  if (a.dq) e = launch_scan(a, q, tc, kNothing);
+  if (a.dk && e == cudaSuccess) e = launch_scan(a, k, tc, a.dq ? kTables : kNothing);
+  if ((a.dv || a.ds0) && e == cudaSuccess) e = launch_scan(a, v, tc, a.dk ? kStates : a.dq ? kTables : kNothing);
   return e;
 }
 

@@ -668,10 +668,12 @@ int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv
  *   grad_initial_state = exp(log_decay) R_{first}
  *   (grad_final_state itself for an empty sequence).
  * grad_out    device [T, H, Dv] of dtype, token stride given
- * grad_q, grad_k, grad_v  device, contiguous [T, H, D] of dtype; rows outside
- *             every sequence are left as they are
+ * grad_q, grad_k, grad_v  device, contiguous [T, H, D] of dtype, or NULL to
+ *             skip (its scan does not run); rows outside every sequence are
+ *             left as they are
  * grad_final_state    device [num_seqs, H, Dk, Dv] fp32 or NULL (zero)
- * grad_initial_state  the same shape or NULL; it may be grad_final_state
+ * grad_initial_state  the same shape or NULL; it may be grad_final_state.  It
+ *             comes with grad_v (ATTNRES_EINVAL without, but for T = 0)
  * Other arguments as in attnres_linear_attention; workspace of at least
  * attnres_linear_attention_backward_workspace_size(...) bytes.  Infinities
  * and NaN reach grad_q of the tokens behind them, grad_k and grad_v of those
