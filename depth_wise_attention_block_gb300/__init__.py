@@ -540,9 +540,18 @@ def _matrix(t: torch.Tensor, name: str) -> tuple[int, int]:
     return t.shape[0], t.shape[1]
 
 
-def attnres_linear_workspace_size(M: int, N: int, K: int, dtype: torch.dtype) -> int:
-    """Bytes of device workspace with which attnres_linear takes its fastest path for these sizes."""
-    return _N.check(_N.lib.attnres_linear_workspace_size(M, N, K, dtype_code(dtype)), "attnres_linear_workspace_size")
+def _place(t: torch.Tensor | None, cols: int) -> tuple[int | None, int]:
+    """Address and row stride of an operand ([rows, cols]; None: aligned rows)."""
+    return (None, cols) if t is None else (t.data_ptr(), t.stride(0) if t.shape[0] > 1 else cols)
+
+
+def attnres_linear_workspace_size(M: int, N: int, K: int, dtype: torch.dtype, x: torch.Tensor | None = None,
+                                  w: torch.Tensor | None = None) -> int:
+    """Bytes of device workspace with which attnres_linear takes its fastest
+    path for contiguous operands of these sizes; given x or w, for these ones
+    (bf16 rows off the 16-byte boundaries are copied)."""
+    return _N.check(_N.lib.attnres_linear_operands_workspace_size(*_place(x, K), _place(w, K)[0], M, N, K, dtype_code(dtype)),
+                    "attnres_linear_workspace_size")
 
 
 def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: torch.Tensor | None = None,
@@ -554,7 +563,7 @@ def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: to
     (rows contiguous, w wholly); bias: [N] float32; residual may be out
     itself.  activation: "none", "gelu", "gelu_tanh" or "silu".  workspace:
     a device buffer of attnres_linear_workspace_size bytes (allocated here
-    through torch when None).
+    through torch when None, with room for the operands as they lie).
     """
     M, K = _matrix(x, "x")
     N = _matrix(w, "w")[0]
@@ -566,17 +575,23 @@ def attnres_linear(x: torch.Tensor, w: torch.Tensor, out: torch.Tensor, bias: to
     wp = _vec(w, "w", (N, K), dt, cur)
     op, ldo = _rows(out, "out", (M, N), dt, cur)
     rp, ldr = _rows(residual, "residual", (M, N), dt, cur)
-    need = 0 if workspace is not None else attnres_linear_workspace_size(M, N, K, dt)
+    need = 0
+    if workspace is None:
+        need = _N.check(_N.lib.attnres_linear_operands_workspace_size(xp, ldx, wp, M, N, K, code), "attnres_linear_workspace_size")
     _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
     rc = _N.lib.attnres_linear(xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), rp, ldr, op, ldo, M, N, K, code, act,
                                ws, nbytes, _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_linear")
 
 
-def attnres_linear_backward_workspace_size(M: int, N: int, K: int, dtype: torch.dtype, activation: str = "none") -> int:
-    """Bytes of device workspace attnres_linear_backward needs."""
-    return _N.check(_N.lib.attnres_linear_backward_workspace_size(M, N, K, dtype_code(dtype), activation_code(activation)),
-                    "attnres_linear_backward_workspace_size")
+def attnres_linear_backward_workspace_size(M: int, N: int, K: int, dtype: torch.dtype, activation: str = "none",
+                                           x: torch.Tensor | None = None, w: torch.Tensor | None = None,
+                                           grad_out: torch.Tensor | None = None) -> int:
+    """Bytes of device workspace attnres_linear_backward needs; given operands,
+    with room for the copies of those off the 16-byte boundaries."""
+    return _N.check(_N.lib.attnres_linear_backward_operands_workspace_size(
+        *_place(x, K), _place(w, K)[0], *_place(grad_out, N), M, N, K, dtype_code(dtype), activation_code(activation)),
+        "attnres_linear_backward_workspace_size")
 
 
 def attnres_linear_backward(x: torch.Tensor, w: torch.Tensor, grad_out: torch.Tensor,
@@ -596,7 +611,10 @@ def attnres_linear_backward(x: torch.Tensor, w: torch.Tensor, grad_out: torch.Te
     xp, ldx = _rows(x, "x", (M, K), dt, cur)
     wp = _vec(w, "w", (N, K), dt, cur)
     gp, ldg = _rows(grad_out, "grad_out", (M, N), dt, cur)
-    need = 0 if workspace is not None else attnres_linear_backward_workspace_size(M, N, K, dt, activation)
+    need = 0
+    if workspace is None:
+        need = _N.check(_N.lib.attnres_linear_backward_operands_workspace_size(xp, ldx, wp, gp, ldg, M, N, K, code, act),
+                        "attnres_linear_backward_workspace_size")
     _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
     rc = _N.lib.attnres_linear_backward(
         xp, ldx, wp, _vec(bias, "bias", (N,), torch.float32, cur), gp, ldg, _vec(grad_x, "grad_x", (M, K), dt, cur),

@@ -57,8 +57,10 @@ EXPORTED = (
     "attnres_fold",
     "attnres_linear",
     "attnres_linear_workspace_size",
+    "attnres_linear_operands_workspace_size",
     "attnres_linear_backward",
     "attnres_linear_backward_workspace_size",
+    "attnres_linear_backward_operands_workspace_size",
     "attnres_qk_norm_rope",
     "attnres_qk_norm_rope_backward",
     "attnres_qk_norm_rope_backward_workspace_size",
@@ -127,9 +129,11 @@ def _load() -> ctypes.CDLL:
         "attnres_fold": (i32, [vp, vp, vp, i64, i32, i32, vp]),
         "attnres_linear": (i32, [vp, i64, vp, vp, vp, i64, vp, i64, i64, i32, i32, i32, i32, vp, i64, vp, vp]),
         "attnres_linear_workspace_size": (i64, [i64, i32, i32, i32]),
+        "attnres_linear_operands_workspace_size": (i64, [vp, i64, vp, i64, i32, i32, i32]),
         "attnres_linear_backward": (i32, [vp, i64, vp, vp, vp, i64, vp, vp, vp, i64, i32, i32, i32, i32, vp, i64, vp,
                                           vp]),
         "attnres_linear_backward_workspace_size": (i64, [i64, i32, i32, i32, i32]),
+        "attnres_linear_backward_operands_workspace_size": (i64, [vp, i64, vp, vp, i64, i64, i32, i32, i32, i32]),
         "attnres_qk_norm_rope": (i32, [vp, i64, i32, vp, i64, i32, i64, i32, i32, vp, vp, f32, vp, vp, i32, i32, vp,
                                        i64, vp, i64, vp]),
         "attnres_qk_norm_rope_backward": (i32, [vp, i64, i32, vp, i64, i32, i64, i32, i32, vp, vp, f32, vp, vp, i32,

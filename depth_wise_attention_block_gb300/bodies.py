@@ -94,7 +94,8 @@ class LinearAttentionBody:
         self.o = torch.zeros((T, heads, Dv), dtype=dt, device=dev)
         self._goes_on = None  # the layer that goes on from the last one issued
         n = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
-        need = [attnres_linear_workspace_size(T, width, d, dt), attnres_linear_workspace_size(T, d, heads * Dv, dt)]
+        need = [n for l in self.layers for n in (attnres_linear_workspace_size(T, width, d, dt, w=l.w_qkv),
+                                                 attnres_linear_workspace_size(T, d, heads * Dv, dt, w=l.w_out))]
         if not decode:
             need.append(attnres_linear_attention_workspace_size(T, heads, Dk, Dv, dt, n))
         # the four calls of a layer follow one another on one stream

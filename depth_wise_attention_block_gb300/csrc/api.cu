@@ -178,7 +178,7 @@ struct HostPipe {
 
 extern "C" {
 
-int attnres_version(void) { return (2 << 16) | 1; }
+int attnres_version(void) { return (2 << 16) | 2; }
 
 const char* attnres_status_string(int status) {
   switch (status) {

@@ -29,7 +29,16 @@ struct LinearArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_linear(const LinearArgs& a);
-int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype);
+// bf16 operands that TMA does not take as they are (rows off the 16-byte
+// boundaries), whose copies the workspace has room for.
+struct LinearUneven {
+  bool x, w, g;
+};
+// of contiguous aligned operands: by the length of a row
+inline LinearUneven linear_uneven_sizes(int N, int K) { return {K % 8 != 0, K % 8 != 0, N % 8 != 0}; }
+// of these ones (and no fewer than by the sizes)
+LinearUneven linear_uneven(const void* x, int64_t ldx, const void* w, const void* g, int64_t ldg, int N, int K);
+int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype, LinearUneven u);
 
 struct LinearBwdArgs {
   const void* x;
@@ -51,7 +60,7 @@ struct LinearBwdArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_linear_backward(const LinearBwdArgs& a);
-int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act);
+int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act, LinearUneven u);
 
 // ----------------------------------------------------- qk norm + rope ----
 

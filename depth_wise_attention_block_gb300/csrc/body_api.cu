@@ -121,7 +121,15 @@ int64_t attnres_linear_workspace_size(int64_t M, int N, int K, int dtype) {
   const int rc = check_linear_sizes(M, N, K, dtype, ATTNRES_ACT_NONE);
   if (rc != ATTNRES_OK) return rc;
   ok();
-  return linear_workspace_bytes(M, N, K, dtype);
+  return linear_workspace_bytes(M, N, K, dtype, linear_uneven_sizes(N, K));
+}
+
+int64_t attnres_linear_operands_workspace_size(const void* x, int64_t ldx, const void* w, int64_t M, int N, int K, int dtype) {
+  const int rc = check_linear_sizes(M, N, K, dtype, ATTNRES_ACT_NONE);
+  if (rc != ATTNRES_OK) return rc;
+  if (!stride_ok(ldx, K)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  ok();
+  return linear_workspace_bytes(M, N, K, dtype, linear_uneven(x, ldx, w, nullptr, 0, N, K));
 }
 
 int attnres_linear(const void* x, int64_t ldx, const void* w, const float* bias, const void* residual, int64_t ldr,
@@ -176,7 +184,16 @@ int64_t attnres_linear_backward_workspace_size(int64_t M, int N, int K, int dtyp
   const int rc = check_linear_sizes(M, N, K, dtype, act);
   if (rc != ATTNRES_OK) return rc;
   ok();
-  return linear_backward_workspace_bytes(M, N, K, dtype, act);
+  return linear_backward_workspace_bytes(M, N, K, dtype, act, linear_uneven_sizes(N, K));
+}
+
+int64_t attnres_linear_backward_operands_workspace_size(const void* x, int64_t ldx, const void* w, const void* grad_out, int64_t ldg,
+                                                        int64_t M, int N, int K, int dtype, int act) {
+  const int rc = check_linear_sizes(M, N, K, dtype, act);
+  if (rc != ATTNRES_OK) return rc;
+  if (!stride_ok(ldx, K) || !stride_ok(ldg, N)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  ok();
+  return linear_backward_workspace_bytes(M, N, K, dtype, act, linear_uneven(x, ldx, w, grad_out, ldg, N, K));
 }
 
 int attnres_linear_backward(const void* x, int64_t ldx, const void* w, const float* bias, const void* grad_out,
@@ -193,7 +210,8 @@ int attnres_linear_backward(const void* x, int64_t ldx, const void* w, const flo
     if ((x && !stride_ok(ldx, K)) || !stride_ok(ldg, N))
       return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
     if ((x && !span_ok(M, ldx)) || !span_ok(M, ldg)) return fail(ATTNRES_ERANGE, "M*stride too large");
-    rc = check_workspace(workspace, workspace_bytes, linear_backward_workspace_bytes(M, N, K, dtype, act));
+    rc = check_workspace(workspace, workspace_bytes,
+                         linear_backward_workspace_bytes(M, N, K, dtype, act, linear_uneven_sizes(N, K)));
     if (rc != ATTNRES_OK) return rc;
   }
   {

@@ -169,7 +169,7 @@ int64_t dz_pitch(int N) { return ((int64_t)N + 7) / 8 * 8; }
 struct BwdLayout {
   int64_t dz, part, x, w, g, total;
 };
-BwdLayout bwd_layout(int64_t M, int N, int K, int dtype, int act) {
+BwdLayout bwd_layout(int64_t M, int N, int K, int dtype, int act, LinearUneven u) {
   const bool bf16 = dtype == ATTNRES_BF16;
   const int np = bf16 ? 1 : 3;
   BwdLayout L;
@@ -178,9 +178,9 @@ BwdLayout bwd_layout(int64_t M, int N, int K, int dtype, int act) {
   // pairs), or the clusters' of up to 1024 tokens (16 per tile of 128)
   const int64_t rows = M <= 1024 ? (M + 127) / 128 * 16 : (M + 255) / 256 * 8;
   L.part = align_up(rows * N * 4);
-  L.x = !bf16 || K % 8 ? tc_prep_bytes(M, K, np) : 0;
-  L.w = !bf16 || K % 8 ? tc_prep_bytes(N, K, np) : 0;
-  L.g = !bf16 || (act == ATTNRES_ACT_NONE && N % 8) ? tc_prep_bytes(M, N, np) : 0;
+  L.x = !bf16 || u.x ? tc_prep_bytes(M, K, np) : 0;
+  L.w = !bf16 || u.w ? tc_prep_bytes(N, K, np) : 0;
+  L.g = !bf16 || (act == ATTNRES_ACT_NONE && u.g) ? tc_prep_bytes(M, N, np) : 0;
   L.total = L.dz + L.part + L.x + L.w + L.g;
   return L;
 }
@@ -199,7 +199,7 @@ cudaError_t launch_rowsum(const float* part, int rows, const LinearBwdArgs& a) {
 template <typename T>
 cudaError_t linear_backward_any(const LinearBwdArgs& a) {
   const T *x = static_cast<const T*>(a.x), *w = static_cast<const T*>(a.w), *g = static_cast<const T*>(a.grad_out);
-  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act);
+  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act, {});
   char* ws = static_cast<char*>(a.workspace);
   float* part = reinterpret_cast<float*>(ws + L.dz);
   const T* dz = g;
@@ -291,7 +291,7 @@ cudaError_t linear_tc(const LinearArgs& a, bool* done) {
 cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
   const bool bf16 = a.dtype == ATTNRES_BF16, act = a.act != ATTNRES_ACT_NONE;
   const int np = bf16 ? 1 : 3;
-  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act);
+  const BwdLayout L = bwd_layout(a.M, a.N, a.K, a.dtype, a.act, {});
   Arena ws{static_cast<char*>(a.workspace), a.workspace_bytes};
   void* dz_buf = L.dz ? ws.take(L.dz) : nullptr;
   float* part = static_cast<float*>(ws.take(L.part));
@@ -357,18 +357,25 @@ cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
 
 }  // namespace
 
-int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype) {
-  if (small_fp32(M, N, K, dtype) || (dtype == ATTNRES_BF16 && K % 8 == 0)) return 0;
-  if (M == 0) return 0;
-  const int np = dtype == ATTNRES_BF16 ? 1 : 3;
-  DeviceInfo di;
-  // (without a device: enough for any plan)
-  const bool fused = np == 3 && device_info(&di) == cudaSuccess && tc_plan(M, N, K, np, di.sm_count).fused;
-  return tc_prep_bytes(M, K, np) + (fused ? 0 : tc_prep_bytes(N, K, np));
+LinearUneven linear_uneven(const void* x, int64_t ldx, const void* w, const void* g, int64_t ldg, int N, int K) {
+  LinearUneven u = linear_uneven_sizes(N, K);
+  u.x |= !tc_rows_ok(x, ldx);
+  u.w |= !tc_rows_ok(w, K);
+  u.g |= !tc_rows_ok(g, ldg);
+  return u;
 }
 
-int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act) {
-  return bwd_layout(M, N, K, dtype, act).total;
+int64_t linear_workspace_bytes(int64_t M, int N, int K, int dtype, LinearUneven u) {
+  if (small_fp32(M, N, K, dtype) || M == 0) return 0;
+  if (dtype == ATTNRES_BF16) return (u.x ? tc_prep_bytes(M, K, 1) : 0) + (u.w ? tc_prep_bytes(N, K, 1) : 0);
+  DeviceInfo di;
+  // (without a device: enough for any plan)
+  const bool fused = device_info(&di) == cudaSuccess && tc_plan(M, N, K, 3, di.sm_count).fused;
+  return tc_prep_bytes(M, K, 3) + (fused ? 0 : tc_prep_bytes(N, K, 3));
+}
+
+int64_t linear_backward_workspace_bytes(int64_t M, int N, int K, int dtype, int act, LinearUneven u) {
+  return bwd_layout(M, N, K, dtype, act, u).total;
 }
 
 cudaError_t launch_linear(const LinearArgs& a) {

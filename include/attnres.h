@@ -537,6 +537,12 @@ int attnres_linear(const void* x, int64_t ldx, const void* w, const float* bias,
  * attnres_status on bad arguments. */
 int64_t attnres_linear_workspace_size(int64_t M, int N, int K, int dtype);
 
+/* The same for these operands, wherever they lie (x, w: pointers or NULL for
+ * aligned ones, not dereferenced): bf16 rows off the 16-byte boundaries have
+ * room for their copies, without which the CUDA cores take the call. */
+int64_t attnres_linear_operands_workspace_size(const void* x, int64_t ldx, const void* w, int64_t M, int N, int K,
+                                               int dtype);
+
 /* ------------------------------------------------------------------------
  * attnres_linear_backward -- gradients of attnres_linear, nothing kept from
  * the forward (z is recomputed where the activation needs it):
@@ -566,6 +572,11 @@ int attnres_linear_backward(const void* x, int64_t ldx, const void* w, const flo
 /* Bytes of workspace attnres_linear_backward needs.  Negative
  * attnres_status on bad arguments. */
 int64_t attnres_linear_backward_workspace_size(int64_t M, int N, int K, int dtype, int act);
+
+/* The same with room for the copies of these operands (as
+ * attnres_linear_operands_workspace_size); never less than by sizes alone. */
+int64_t attnres_linear_backward_operands_workspace_size(const void* x, int64_t ldx, const void* w, const void* grad_out,
+                                                        int64_t ldg, int64_t M, int N, int K, int dtype, int act);
 
 /* ------------------------------------------------------------------------
  * attnres_qk_norm_rope -- RMSNorm of every head of q and k and rotation by
