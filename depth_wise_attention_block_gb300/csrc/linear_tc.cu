@@ -234,7 +234,7 @@ struct RowEpilogue {
 #pragma unroll
         for (int i = 0; i < 16; ++i) r[i] = 0.f;
       }
-      act_apply<MODE, 16>(e.act, v, r);
+      act_apply<T, MODE, 16>(e.act, v, r);
       if (row) {
         T* dst = static_cast<T*>(e.out) + m * e.ldo + n0;
         if (vec_out) {

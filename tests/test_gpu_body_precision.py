@@ -205,3 +205,74 @@ def test_bf16_attention_rounds_once_inside_a_chunk(A, T, cu, Dk, Dv):
         bound = UB * np.abs(ref) + (2.0 ** -16 + fp32) * inside + (UB + 2.0 ** -16 + fp32) * (1 + UB) * before + 2.0 ** -129
         err = np.abs(to64(got) - ref)
         assert (err <= bound).all(), (name, float((err / bound).max()))
+
+
+# --------------------------------------------- activations far from zero -------
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu"])
+@pytest.mark.parametrize("shape", ["few rows", "many rows", "small"])
+def test_fp32_activations_keep_their_digits_far_out(A, act, shape):
+    """z itself exact (one product with 1), from -9 to 9: relative to the value.
+    An activation's value and slope at z are those of z (1 + a few 2^-24), which
+    the exponent z^2 / 2 (gelu), 0.8 (z + 0.045 z^3) (tanh gelu, both doubled) or
+    z (silu) multiplies; 16 operations more."""
+    z = torch.linspace(-9, 9, 1537, device="cuda")
+    z = z[(z.abs() > 1e-3)]
+    m = {"few rows": 64, "many rows": 2048, "small": 4}[shape]
+    n = {"few rows": 4096, "many rows": 2048, "small": 4}[shape]
+    k = 4 if shape == "small" else 128
+    x, w = torch.zeros(m, k, device="cuda"), torch.zeros(n, k, device="cuda")
+    x[:, 0] = z[torch.arange(m, device="cuda") * 37 % z.numel()] if shape != "small" else torch.tensor([-8.5, -5.0, -3.0, 4.0], device="cuda")
+    w[:, 0] = 1
+    out = torch.empty(m, n, device="cuda")
+    A.attnres_linear(x, w, out, activation=act)
+    z64 = to64(x[:, 0])
+    erfc = np.vectorize(math.erfc)
+    c = math.sqrt(2 / math.pi)
+    u2 = 2 * c * (z64 + 0.044715 * z64 ** 3)
+    sig = lambda t: 1 / (1 + np.exp(-t))
+    value, slope, grow = {
+        "gelu": (z64 * 0.5 * erfc(-z64 / math.sqrt(2)),
+                 0.5 * erfc(-z64 / math.sqrt(2)) + z64 * np.exp(-z64 ** 2 / 2) / math.sqrt(2 * math.pi), z64 ** 2),
+        "gelu_tanh": (z64 * sig(u2), sig(u2) + z64 * sig(u2) * sig(-u2) * 2 * c * (1 + 3 * 0.044715 * z64 ** 2), np.abs(u2) * 3),
+        "silu": (z64 * sig(z64), sig(z64) * (1 + z64 * sig(-z64)), np.abs(z64)),
+    }[act]
+    bar = 2 * (16 + 2 * grow) * E
+    got = to64(out)
+    assert (got == got[:, :1]).all()
+    assert (np.abs(got[:, 0] / value - 1) <= bar).all(), float((np.abs(got[:, 0] / value - 1) / bar).max())
+    # the slope, as dz = slope * 1: a sum of two addends that cancel near its zero
+    dx = torch.empty_like(x)
+    gy = torch.zeros(m, n, device="cuda")
+    gy[:, 0] = 1
+    A.attnres_linear_backward(x, w, gy, dx, activation=act)
+    addends = np.abs(value / z64) + np.abs(slope - value / z64)
+    err = np.abs(to64(dx[:, 0]) - slope)
+    assert (err <= bar * addends).all(), float((err / (bar * addends)).max())
+
+
+@gpu
+@pytest.mark.parametrize("act", ["gelu_tanh", "silu"])
+def test_bf16_activations_round_once(A, act):
+    """Values and slopes far below zero: off by their own rounding, and the
+    exponent's relative error (a few 2^-24 of it) times 4, in fp32."""
+    z = torch.linspace(-9, 9, 1024, device="cuda").bfloat16()
+    x, w = torch.zeros(1024, 64, device="cuda", dtype=torch.bfloat16), torch.zeros(64, 64, device="cuda", dtype=torch.bfloat16)
+    x[:, 0], w[:, 0] = z, 1
+    out, dx = torch.empty(1024, 64, device="cuda", dtype=torch.bfloat16), torch.empty_like(x)
+    gy = torch.zeros_like(out)
+    gy[:, 0] = 1
+    A.attnres_linear(x, w, out, activation=act)
+    A.attnres_linear_backward(x, w, gy, dx, activation=act)
+    z64 = to64(z)
+    c = math.sqrt(2 / math.pi)
+    v = 2 * c * (z64 + 0.044715 * z64 ** 3) if act == "gelu_tanh" else z64
+    dv = 2 * c * (1 + 3 * 0.044715 * z64 ** 2) if act == "gelu_tanh" else np.ones_like(z64)
+    s, rest = 1 / (1 + np.exp(-v)), 1 / (1 + np.exp(v))
+    fp32 = (16 + 4 * np.abs(v)) * 2 * E
+    value, slope = z64 * s, s + z64 * s * rest * dv
+    assert (np.abs(to64(out[:, 0]) - value) <= (UB + fp32) * np.abs(value) + 2.0 ** -129).all()
+    # (1 - s is off by 2^-22 where it is small, times z dv, at most 80)
+    bound = UB * np.abs(slope) + fp32 * (s + np.abs(z64 * s * rest * dv)) + s * np.abs(z64 * dv) * 2.0 ** -21
+    assert (np.abs(to64(dx[:, 0]) - slope) <= bound + 2.0 ** -129).all()
