@@ -13,6 +13,7 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 42;  // element offsets stay far inside int64
 constexpr int kMaxWidth = 1 << 30;               // of a projection: tiles past its end stay inside int
+constexpr int64_t kMaxRows = INT32_MAX - 64;     // of a projection (grad_w's contraction): a step past its end, too
 
 // `rows` rows of `width` bytes, `pitch` bytes apart
 struct Rows {
@@ -50,7 +51,7 @@ int check_apart(const Rows* in, int nin, const Rows* out, int nout, const int* i
 int check_linear_sizes(int64_t M, int N, int K, int dtype, int act) {
   if (!valid_dtype(dtype)) return fail(ATTNRES_EDTYPE, "dtype %d", dtype);
   if (M < 0 || N < 1 || K < 1) return fail(ATTNRES_EINVAL, "M=%lld N=%d K=%d", (long long)M, N, K);
-  if (M > INT32_MAX) return fail(ATTNRES_ERANGE, "M=%lld", (long long)M);
+  if (M > kMaxRows) return fail(ATTNRES_ERANGE, "M=%lld", (long long)M);
   if (N > kMaxWidth || K > kMaxWidth) return fail(ATTNRES_ERANGE, "N=%d K=%d", N, K);
   if (M > kMaxElems / N || M > kMaxElems / K || N > kMaxElems / K) return fail(ATTNRES_ERANGE, "M*N, M*K or N*K too large");
   if (act < ATTNRES_ACT_NONE || act > ATTNRES_ACT_SILU) return fail(ATTNRES_EINVAL, "activation %d", act);

@@ -514,7 +514,7 @@ typedef enum {
  * residual  device [M, N] of dtype, row stride ldr, or NULL; it may be out
  *           itself (with ldr = ldo)
  * out       device [M, N] of dtype, row stride ldo
- * M >= 0 (0 launches nothing and accepts NULL buffers), N, K 1..2^30
+ * M 0..2^31 - 65 (0 launches nothing and accepts NULL buffers), N, K 1..2^30
  *           (ATTNRES_ERANGE above)
  * act       one of attnres_activation
  * workspace NULL, or device scratch of workspace_bytes, 256-byte aligned,

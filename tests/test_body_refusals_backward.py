@@ -20,3 +20,14 @@ def test_refused(N, kw):  # noqa: F811
 
 def test_nothing_asked_for(N):  # noqa: F811
     assert _call(N, dq=None, dk=None, dv=None, go=None) == 0
+
+
+@pytest.mark.parametrize("M", [(1 << 31) - 1, (1 << 31) - 64])
+def test_rows_whose_last_step_leaves_an_int(N, M):  # noqa: F811
+    """grad_w contracts over the rows 16 at a time, in 32 bits."""
+    ws = 1 << 50
+    assert N.lib.attnres_linear_backward(X, 8, W, None, 1 << 45, 8, None, OUT, None, M, 8, 8, 1, 0, 1 << 46, ws, None,
+                                         None) == N.ATTNRES_ERANGE
+    assert N.lib.attnres_linear_backward_workspace_size(M, 8, 8, 1, 0) == N.ATTNRES_ERANGE
+    assert N.lib.attnres_linear_workspace_size(M, 8, 8, 1) == N.ATTNRES_ERANGE
+    assert N.lib.attnres_linear_workspace_size((1 << 31) - 65, 8, 8, 1) == 0
