@@ -729,7 +729,8 @@ def _attention_args(q, k, v, log_decay, cu_seqlens, cur: int):
 
 
 def attnres_linear_attention_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: torch.dtype, num_seqs: int = 1) -> int:
-    """Bytes of device workspace attnres_linear_attention needs (0: none)."""
+    """Bytes of device workspace that attnres_linear_attention needs for up to T
+    tokens in up to num_seqs sequences (0: none)."""
     return _N.check(_N.lib.attnres_linear_attention_workspace_size(T, H, Dk, Dv, dtype_code(dtype), num_seqs),
                     "attnres_linear_attention_workspace_size")
 
@@ -762,7 +763,8 @@ def attnres_linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
 
 def attnres_linear_attention_backward_workspace_size(T: int, H: int, Dk: int, Dv: int, dtype: torch.dtype,
                                                      num_seqs: int = 1) -> int:
-    """Bytes of device workspace attnres_linear_attention_backward needs (0: none)."""
+    """Bytes of device workspace that attnres_linear_attention_backward needs for
+    up to T tokens in up to num_seqs sequences (0: none)."""
     return _N.check(_N.lib.attnres_linear_attention_backward_workspace_size(T, H, Dk, Dv, dtype_code(dtype), num_seqs),
                     "attnres_linear_attention_backward_workspace_size")
 

@@ -318,11 +318,14 @@ cudaError_t launch_scan_groups(const ScanArgs& s, int nc, cudaStream_t stream) {
 
 // Ranges on the CUDA cores: a chunk's products at the 110 FMA per ns that an
 // SM gives them, shared by the CTAs of an SM.
-Cut scan_any_cut(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
+CutRule scan_any_rule(int Da, int Dc, const DeviceInfo& di) {
   const int nc = scan_columns(Da, Dc, di.max_smem_optin);
   const int per_sm = 2 * scan_smem(Da, nc) + 2048 <= di.max_smem_optin ? 2 : 1;
   const double chunk_ns = per_sm * (double)kSC * (kSC * (Da + nc) + 2 * Da * nc) / 110;
-  return choose_cut(T, H, Da, Dc, N, kSC, (Dc + nc - 1) / nc, per_sm * di.sm_count, 0.4, chunk_ns);
+  return {kSC, (Dc + nc - 1) / nc, per_sm * di.sm_count, 0.4, chunk_ns};
+}
+Cut scan_any_cut(int64_t T, int H, int Da, int Dc, int N, const DeviceInfo& di) {
+  return choose_cut(T, H, Da, Dc, N, scan_any_rule(Da, Dc, di));
 }
 
 template <typename T>
@@ -633,8 +636,9 @@ void piece_place(ScanArgs& s, const PieceLayout& L, void* workspace) {
   s.piece_state = reinterpret_cast<float*>(ws + L.first + L.starts);
 }
 
-Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, int slots, double extra, double chunk_ns) {
-  const int64_t chunks = round_up(T, chunk) / chunk, units = H * (chunks + N);
+Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, const CutRule& r) {
+  const int64_t chunks = round_up(T, r.chunk) / r.chunk, units = H * (chunks + N);
+  const int groups = r.groups, slots = r.slots;
   if (T == 0 || units >= INT32_MAX / 2) return {0, 1};  // a chunk's index is an int
   const double even = (double)groups * (double)units / slots;  // chunks per slot if all were equal
   // Neighbouring heads lie side by side in memory: the largest gang, unless a
@@ -652,7 +656,7 @@ Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, i
       const double pieces = (double)(parts + gangs * N);  // of a gang's head
       const double bytes = pieces * gang * Da * Dc * 16;  // written, read, replaced and read
       const double join = bytes / 6500 + 250. * (double)parts / (double)gangs + 12000;
-      const double cost = ((double)(gangs * chunks) + pieces) / (double)parts * (1 + extra) + join / chunk_ns;
+      const double cost = ((double)(gangs * chunks) + pieces) / (double)parts * (1 + r.extra) + join / r.chunk_ns;
       if (cost < 0.95 * best) {
         best = cost;
         cut = {(int)parts, gang};
@@ -662,6 +666,24 @@ Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, i
   const double whole = (double)(chunks > even ? chunks : even) + 2;  // every sequence in one piece
   if (best >= whole) cut.parts = 0;
   return cut;
+}
+
+// A cut's cost is at least even (1 + extra) + (1 + extra) + join (no more
+// ranges than CTAs at once) and at least (2 + N / chunks) (1 + extra) + join
+// (no more than chunks), with join no less than the sequences' own states and
+// the launches; it has to be below chunks + 2 (where `even` is the larger part
+// of `whole`, the first bound alone exceeds it).  Both leave a largest N, which
+// grows with T; more sequences than that are never cut.
+int64_t piece_bytes(int64_t T, int H, int Da, int Dc, int N, const CutRule& r) {
+  const int64_t chunks = round_up(T, r.chunk) / r.chunk;
+  if (chunks == 0) return 0;
+  const double m = (double)chunks, x = r.extra, fixed = 12000 / r.chunk_ns, state = (double)H * Da * Dc * 16 / 6500 / r.chunk_ns;
+  const double share = (double)r.groups * H / r.slots * (1 + x);  // of `even` (1 + extra), per chunk
+  const double n1 = (m * (1 - share) + 1 - x - fixed) / (share + state), n2 = (m - 2 * x - fixed) / ((1 + x) / m + state);
+  const double most = n1 < n2 ? n1 : n2;
+  if (most <= 1) return 0;
+  const Cut widest{r.slots / r.groups, 1};
+  return piece_layout(H, Da, Dc, most < N ? (int)most : N, widest).total;
 }
 
 cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream) {
@@ -687,13 +709,13 @@ int64_t linear_attention_workspace_bytes(int64_t T, int H, int Dk, int Dv, int d
   if (scan_tc_dims(Dk, Dv, dtype)) return scan_tc_workspace(T, H, Dk, Dv, N);
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return piece_layout(H, Dk, Dv, N, scan_any_cut(T, H, Dk, Dv, N, di)).total;
+  return piece_bytes(T, H, Dk, Dv, N, scan_any_rule(Dk, Dv, di));
 }
 
 namespace {
 
 cudaError_t launch_scan(const LinAttnArgs& a, const ScanArgs& s, bool tc, ScanReady ready) {
-  if (tc) return launch_scan_tc(s, a.workspace, ready, a.dev_err, a.stream);
+  if (tc) return launch_scan_tc(s, a.workspace, a.workspace_bytes, ready, a.dev_err, a.stream);
   return a.dtype == ATTNRES_BF16 ? launch_scan_type<bf16_t>(s, a.workspace, a.workspace_bytes, ready, a.stream)
                                  : launch_scan_type<float>(s, a.workspace, a.workspace_bytes, ready, a.stream);
 }

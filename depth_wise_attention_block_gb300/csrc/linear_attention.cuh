@@ -148,7 +148,15 @@ void piece_place(ScanArgs& s, const PieceLayout& L, void* workspace);  // points
 // CTAs run at once, `groups` of them to a range and head, a chunk takes
 // chunk_ns.  The lengths are on the device, so the longest sequence is taken
 // to be all T tokens.
-Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, int chunk, int groups, int slots, double extra, double chunk_ns);
+struct CutRule {
+  int chunk, groups, slots;  // tokens per chunk
+  double extra, chunk_ns;
+};
+Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, const CutRule& r);
+// Bytes that suffice for every cut of up to T tokens in up to N sequences: a
+// buffer kept for the largest batch serves the smaller ones, which may be cut
+// where that is not.
+int64_t piece_bytes(int64_t T, int H, int Da, int Dc, int N, const CutRule& r);
 cudaError_t launch_piece_plan(const ScanArgs& s, cudaStream_t stream);     // the tables of a ragged batch
 cudaError_t launch_piece_combine(const ScanArgs& s, cudaStream_t stream);  // own states -> the states before, and the final ones
 
@@ -162,6 +170,7 @@ int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N);
 // same sequences; and the states before the pieces, left by one of the same
 // direction, states and sums b c^T (which wrote the final state, if any).
 enum ScanReady { kNothing = 0, kTables = 1, kStates = 2 };
-cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, int* dev_err, cudaStream_t stream);
+cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, int64_t workspace_bytes, ScanReady ready, int* dev_err,
+                           cudaStream_t stream);
 
 }  // namespace attnres

@@ -1004,8 +1004,11 @@ bool token_map(CUtensorMap* m, const void* ptr, int64_t T, int H, int D, int64_t
 bool scan_tc_dims(int Dk, int Dv, int dtype) { return dtype == ATTNRES_BF16 && Dk <= 128 && Dv <= 128 && Dk % 16 == 0 && Dv % 16 == 0; }
 
 // (a chunk's HBM time on one of 152 SMs is 23 ns per channel)
+static CutRule scan_tc_rule(int Dk, int Dv, int sm_count) {
+  return {kC, 1, sm_count, 0.55, 23. * (Dk > 64 || Dv > 64 ? 128 : 64)};
+}
 static Cut scan_tc_cut(int64_t T, int H, int Dk, int Dv, int N, int sm_count) {
-  return choose_cut(T, H, Dk, Dv, N, kC, 1, sm_count, 0.55, 23. * (Dk > 64 || Dv > 64 ? 128 : 64));
+  return choose_cut(T, H, Dk, Dv, N, scan_tc_rule(Dk, Dv, sm_count));
 }
 
 bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N) {
@@ -1016,7 +1019,7 @@ bool scan_tc_in_pieces(int64_t T, int H, int Dk, int Dv, int N) {
 int64_t scan_tc_workspace(int64_t T, int H, int Dk, int Dv, int N) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  return piece_layout(H, Dk, Dv, N, scan_tc_cut(T, H, Dk, Dv, N, di.sm_count)).total;
+  return piece_bytes(T, H, Dk, Dv, N, scan_tc_rule(Dk, Dv, di.sm_count));
 }
 
 bool scan_tc_ok(const ScanArgs& s) {
@@ -1026,7 +1029,7 @@ bool scan_tc_ok(const ScanArgs& s) {
          s.T * 2 < INT32_MAX && (int64_t)s.N * s.H < INT32_MAX;
 }
 
-cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, int* dev_err, cudaStream_t stream) {
+cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, int64_t workspace_bytes, ScanReady ready, int* dev_err, cudaStream_t stream) {
   DeviceInfo di;
   cudaError_t e = device_info(&di);
   if (e != cudaSuccess) return e;
@@ -1043,7 +1046,11 @@ cudaError_t launch_scan_tc(const ScanArgs& s, void* workspace, ScanReady ready, 
   const Cut cut = scan_tc_cut(s.T, s.H, s.Da, s.Dc, s.N, di.sm_count);
   p.s.parts = cut.parts;
   p.s.gang = cut.gang;
-  if (p.s.parts > 0) piece_place(p.s, piece_layout(s.H, s.Da, s.Dc, s.N, cut), workspace);
+  if (p.s.parts > 0) {
+    const PieceLayout L = piece_layout(s.H, s.Da, s.Dc, s.N, cut);
+    if (L.total > workspace_bytes) return cudaErrorInvalidValue;
+    piece_place(p.s, L, workspace);
+  }
   if (p.s.parts > 0 && ready < kStates) {
     if (ready < kTables) e = launch_piece_plan(p.s, stream);
     if (e != cudaSuccess) return e;

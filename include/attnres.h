@@ -667,7 +667,8 @@ int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int
                              float scale, void* out, int64_t out_stride, void* workspace, int64_t workspace_bytes,
                              int* dev_err, void* stream);
 
-/* Bytes of workspace attnres_linear_attention needs (0: none). */
+/* Bytes of workspace that every call of up to T tokens in up to num_seqs
+ * sequences needs (0: none; other arguments as in the calls). */
 int64_t attnres_linear_attention_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs);
 
 /* ------------------------------------------------------------------------
@@ -698,6 +699,7 @@ int attnres_linear_attention_backward(const void* q, int64_t q_stride, const voi
                                       void* grad_k, void* grad_v, float* grad_initial_state, void* workspace,
                                       int64_t workspace_bytes, int* dev_err, void* stream);
 
+/* The same for attnres_linear_attention_backward. */
 int64_t attnres_linear_attention_backward_workspace_size(int64_t T, int H, int Dk, int Dv, int dtype, int num_seqs);
 
 /* ------------------------------------------------------------------------
