@@ -512,14 +512,14 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
               uint32_t v[16];
               tmem_ld16(lanes_at + kColP + j0, v);
               // the powers of 16 columns' distances (masked ones: whatever lies there)
-            const float* t = tab + (rev ? j0 - row : kC - 1 - row + j0);
-            float f[16];
+              const float* t = tab + (rev ? j0 - row : kC - 1 - row + j0);
+              float f[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] = t[k];
-            tmem_ld_wait();
+              for (int k = 0; k < 16; ++k) f[k] = t[k];
+              tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
-            if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
+              for (int k = 0; k < 16; ++k) f[k] *= __uint_as_float(v[k]);
+              if (rev ? j0 < lo_row + 31 || j0 + 16 > len : j0 + 15 > lo_row) {  // a masked score may be infinite or NaN
                 const int last = rev ? len : row + 1, first = rev ? row : 0;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) f[k] = j0 + k >= first && j0 + k < last ? f[k] : 0.f;
