@@ -34,8 +34,9 @@
 // Bound: HBM, with the arithmetic warps close behind.  A chunk of 128 x 128
 // heads takes about 5500 cycles of HBM time per SM, its five products 2600 of
 // the tensor cores, and the warps that turn scores into P and write outputs
-// about 6000.  16384 tokens x 56 heads of 128: the scan 181 us (5.2 TB/s), the
-// pieces' states 92 us (5.1 TB/s), joining them 10 us.
+// about 6000.  16384 tokens x 56 heads of 128: the scan 189 us (4.9 TB/s), the
+// pieces' states 92 us (5.2 TB/s), joining them 10.6 us (each by itself, cold;
+// the whole call in a graph 289).
 #include <math.h>
 
 #include "attnres.h"

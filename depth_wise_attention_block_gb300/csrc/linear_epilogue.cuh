@@ -41,8 +41,9 @@ constexpr float kGeluCubic = 0.044715f;
 // the rational-exponential form 7.1.26 of Abramowitz and Stegun (absolute
 // error 1.5e-7, relative below half a bf16 step down to z = -5), which shares
 // its exponential with the density that the slope of z Phi(z) needs; library
-// erfcf, which keeps its digits however far out, costs the epilogue about
-// twice as much.
+// erfcf and expf, which keep their digits however far out, cost 2048 x 7168 x
+// 7168 in bf16 127 us instead of 120, the backward of 2048 x 7168 x 2048 172
+// instead of 143.
 template <bool FAST>
 __device__ __forceinline__ float normal_cdf(float z, float* gauss) {
   if constexpr (FAST) {

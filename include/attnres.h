@@ -486,8 +486,9 @@ int attnres_fold(const void* prev, const void* F, void* dst, int64_t T, int d, i
  * its output v_l; the calls below are what such a body is made of: the
  * projections around it (attnres_linear), the norm and rotation of its heads
  * (attnres_qk_norm_rope) and a token mixer with a state of fixed size
- * (attnres_linear_attention).  The pages leave the body open; the formulas
- * here define the operations.
+ * (attnres_linear_attention).  It is a simpler mixer than the pages' own (a
+ * delta rule with forgetting per channel, gated latent attention, experts),
+ * which are not here; the formulas here define the operations.
  *
  * Row strides (ld*, *_stride) are in elements between consecutive rows
  * (tokens) of a tensor whose rows are otherwise contiguous: slices of one
