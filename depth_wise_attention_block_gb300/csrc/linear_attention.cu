@@ -643,7 +643,8 @@ Cut choose_cut(int64_t T, int H, int Da, int Dc, int N, const CutRule& r) {
   const double even = (double)groups * (double)units / slots;  // chunks per slot if all were equal
   // Neighbouring heads lie side by side in memory: the largest gang, unless a
   // smaller one divides the work better (8192 tokens of 5 sequences, 32 heads
-  // of 128, backward: 334 us in gangs of 8, 344 in gangs of 1).
+  // of 128, backward: 334 us in gangs of 8, 344 in gangs of 1, before the state entered
+  // its products as two terms).
   Cut cut{0, 1};
   double best = 1e300;
   for (int gang = 8; gang >= 1; --gang) {

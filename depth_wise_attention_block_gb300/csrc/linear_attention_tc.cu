@@ -12,8 +12,9 @@
 // MN-major (P c, the token sums) from the same tile.  Eight warps turn the
 // scores into P (two bf16 terms, back into TMEM as the next product's operand) and
 // write the outputs; eight warps hold the state in fp32 registers (half a
-// row of Da per thread) and give it to the products rounded to bf16; all of
-// them weigh b with the decays.  The weighted rows enter as three bf16 terms
+// row of Da per thread) and give it to the products as two bf16 terms (one
+// term, whose error is the output's own rounding once more, is 5 % faster: 288
+// us instead of 302 for the prompt below); all of them weigh b with the decays.  The weighted rows enter as three bf16 terms
 // (24 bits) where the state is a result, so that it keeps fp32 precision over
 // any number of chunks; each chunk's U starts from zero in TMEM and is added
 // in fp32 round-to-nearest.
@@ -32,11 +33,11 @@
 // held in registers 8 %.
 //
 // Bound: HBM, with the arithmetic warps close behind.  A chunk of 128 x 128
-// heads takes about 5500 cycles of HBM time per SM, its five products 2600 of
+// heads takes about 5500 cycles of HBM time per SM, its products 3800 of
 // the tensor cores, and the warps that turn scores into P and write outputs
-// about 6000.  16384 tokens x 56 heads of 128: the scan 189 us (4.9 TB/s), the
+// about 6000.  16384 tokens x 56 heads of 128: the scan 199 us (4.7 TB/s), the
 // pieces' states 92 us (5.2 TB/s), joining them 10.6 us (each by itself, cold;
-// the whole call in a graph 289).
+// the whole call in a graph 302).
 #include <math.h>
 
 #include "attnres.h"
@@ -64,7 +65,10 @@ constexpr int kDynSmem = 232448 - 2048;
 template <int DA, int DC, int TERMS>
 struct ScanSmem {
   static constexpr int kTile = kC * (DA > DC ? DA : DC) * 2;
-  static constexpr int kFixed = DC * DA * 2 + (TERMS - 1) * kC * DA * 2 + 1024;
+  static constexpr int kState = DC * DA * 2, kTerms = (TERMS - 1) * kC * DA * 2;
+  // the state's second term: a place of its own where that leaves enough slots
+  static constexpr bool kOwnLow = kDynSmem - 2 * kState - kTerms - 1024 >= 4 * kTile;
+  static constexpr int kFixed = (kOwnLow ? 2 : 1) * kState + kTerms + 1024;
   static constexpr int kFit = (kDynSmem - kFixed) / kTile, kSlots = kFit < kMaxSlots ? kFit : kMaxSlots;
   static constexpr int kBytes = kFixed + kSlots * kTile;
   static_assert(kSlots >= 4, "a chunk's tiles and the next chunk's first");
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   constexpr int kTiles = 3;                            // tiles per chunk: a, b, c
   constexpr uint32_t kColP = 0, kColO1 = 128, kColO2 = 256, kColU = 384;  // TMEM columns
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, b_ready, u_full, u_free;
+  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots], p_full, p_ready, o_full, o_free, s_ready, s_read, b_ready, u_full, u_free;
   __shared__ __align__(8) uint64_t t_ready, drained[2];
   __shared__ uint32_t tmem_base;
   // l^i; and p_scale l^distance in the order of a row's columns: distances
@@ -196,6 +200,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
   __shared__ Piece pieces[kPieces];
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_buf = base + kSlots * kTile, rest = s_buf + DC * DA * 2;  // the terms behind the first
+  // the state's second term lies behind them, or (not kOwnLow) where the last
+  // of them does: it is written once the chunk before has summed that up, and
+  // read by a S before split writes the chunk's own
+  constexpr bool kOwnLow = ScanSmem<DA, DC, TERMS>::kOwnLow;
+  const uint32_t s_low = rest + (TERMS - (kOwnLow ? 1 : 2)) * (kC * DA * 2);
   const int tid = threadIdx.x, warp = warp_value(tid >> 5), lane = tid & 31;
   const int Da = FULL ? DA : p.s.Da, Dc = FULL ? DC : p.s.Dc;
 
@@ -212,6 +221,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     mbar_init(smem_addr(&o_full), 1);
     mbar_init(smem_addr(&o_free), 8);
     mbar_init(smem_addr(&s_ready), 8);
+    mbar_init(smem_addr(&s_read), 1);
     mbar_init(smem_addr(&b_ready), 16);
     mbar_init(smem_addr(&u_full), 1);
     mbar_init(smem_addr(&u_free), 8);
@@ -338,10 +348,15 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
         warp_wait(&s_ready, ph);
         warp_wait(&o_free, ph + 1);
         tc_fence_after();
-        const uint64_t da = smem_desc_k128(slot(it)), ds = smem_desc_k128(s_buf);
+        const uint64_t da = smem_desc_k128(slot(it)), ds = smem_desc_k128(s_buf), dl = smem_desc_k128(s_low);
 #pragma unroll 4
-        for (int kk = 0; kk < DA / 16; ++kk)
-          tc_mma_bf16_warp(tmem + kColO2, da + (kk / 4 * kPanel + kk % 4 * 32) / 16, ds + (kk / 4 * (DC * 128) + kk % 4 * 32) / 16, kI3, kk > 0);
+        for (int kk = 0; kk < DA / 16; ++kk) {
+          const uint32_t at = (kk / 4 * (DC * 128) + kk % 4 * 32) / 16;
+          const uint64_t a = da + (kk / 4 * kPanel + kk % 4 * 32) / 16;
+          tc_mma_bf16_warp(tmem + kColO2, a, ds + at, kI3, kk > 0);
+          tc_mma_bf16_warp(tmem + kColO2, a, dl + at, kI3, 1u);
+        }
+        if constexpr (!kOwnLow) commit(&s_read);
         commit(&empty[it % kSlots]);
         commit(&empty[it % kSlots]);
         wait_tile(ic);
@@ -440,6 +455,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
     // b's rows times their decay, as three bf16 terms (hi over b itself)
     auto split = [&](int len, int m, int t0) {
       const uint32_t B = base + (m * kTiles + 1) % kSlots * kTile, Ct = base + (m * kTiles + 2) % kSlots * kTile;
+      if constexpr (!kOwnLow) warp_wait(&s_read, m);
       // thread t0's vectors of 8 channels lie in rows t0 / 8 + kStep i of each
       // panel, i < kBatch; a panel's are loaded before the first is stored
       constexpr int kStep = 512 / 8, kBatch = kC / kStep;
@@ -617,13 +633,23 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
 #pragma unroll
           for (int d = 0; d < DH; ++d) S[d] = 0.f;
         }
-        // S rounded to bf16 for a S: 8 values of this thread's row, [DC rows][DA]
-        // in the 128-byte swizzle
+        // S as two bf16 terms for a S: 8 values of this thread's row, [DC
+        // rows][DA] in the 128-byte swizzle
         auto put = [&](int d) {
           const int at = d0 + d;
-          if (row < DC)
-            st_shared_v4(s_buf + at / 64 * (DC * 128) + row * 128 + (((at / 8) ^ row) & 7) * 16, pack_bf16x2(S[d], S[d + 1]),
-                         pack_bf16x2(S[d + 2], S[d + 3]), pack_bf16x2(S[d + 4], S[d + 5]), pack_bf16x2(S[d + 6], S[d + 7]));
+          const uint32_t to = at / 64 * (DC * 128) + row * 128 + (((at / 8) ^ row) & 7) * 16;
+          if (row < DC) {
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              h[k] = pack_bf16x2(S[d + 2 * k], S[d + 2 * k + 1]);
+              float x, y;
+              f2_unpack(f2_fma(f2_pack(bf16lo(h[k]), bf16hi(h[k])), f2_pack(-1.f, -1.f), f2_pack(S[d + 2 * k], S[d + 2 * k + 1])), x, y);
+              l[k] = pack_bf16x2(x, y);
+            }
+            st_shared_v4(s_buf + to, h[0], h[1], h[2], h[3]);
+            st_shared_v4(s_low + to, l[0], l[1], l[2], l[3]);
+          }
         };
         // ready for chunk m, whose scores this warp sees first: the next ones
         // follow on this, so that it cannot miss a phase of p_full

@@ -656,11 +656,12 @@ int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, 
  * T >= 0, H 1..65535, Dk, Dv 1..256, num_seqs 1..65535 (ATTNRES_ERANGE
  * above).  The state is held in fp32.  bf16 tensors with Dk and Dv up to 128
  * and multiples of 16, 16-byte aligned rows, run in chunks of 128 tokens on
- * the tensor cores (tcgen05): the state enters an output's product rounded to
- * bf16 (the chunk's scores with 16 bits), its own sums keep fp32 precision.
- * Others run on the CUDA cores in fp32.  Where the sequences do not fill the GPU evenly they are cut into
- * pieces (whose states lie in the workspace).  Infinities and NaN reach the
- * tokens behind them and no others; an infinity becomes NaN in the state.
+ * the tensor cores (tcgen05): the state and the chunk's scores enter an
+ * output's products with 16 bits, the state's own sums keep fp32 precision.
+ * Others run on the CUDA cores in fp32.  Where the sequences do not fill the
+ * GPU evenly they are cut into pieces (whose states lie in the workspace).
+ * Infinities and NaN reach the tokens behind them and no others; an infinity
+ * becomes NaN in the state.
  * ---------------------------------------------------------------------- */
 int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype, const float* log_decay,

@@ -142,7 +142,7 @@ def test_states_keep_24_bits(A, dt, T, Dk, Dv):
     assert (rel.abs() <= bar).all(), float(rel.abs().max() / bar)
 
 
-# ------------------------------------- bf16 attention: scores in two terms -----
+# --------------------------- bf16 attention: scores and state in two terms -----
 
 def _att(T, n, H, Dk, Dv, seed, initial):
     q, k, v, do = (_randn(seed + i, T, H, D, dtype=torch.bfloat16) for i, D in enumerate((Dk, Dk, Dv, Dv)))
@@ -182,11 +182,11 @@ def _conds(a, b, c, g, cu, scale, reverse, mask):
 @pytest.mark.parametrize("T,cu,Dk,Dv", [
     (128, (0, 128), 128, 128), (97, (0, 40, 97), 64, 64), (128, (0, 1, 128), 96, 48), (500, (0, 130, 500), 128, 64),
     (3000, (0, 1100, 3000), 64, 128), (3000, (0, 3000), 128, 128)])
-def test_bf16_attention_rounds_once_inside_a_chunk(A, T, cu, Dk, Dv):
-    """Inside a chunk: the scores as two bf16 terms (2^-16 of them) and the
-    output's own rounding.  From the chunks before: the state rounded to bf16 as
-    well, its own sums with at least 16 bits.  Scores of one term would miss
-    by up to 2^-8 of the chunk's sums, 250 times their share of this bar."""
+def test_bf16_attention_rounds_once(A, T, cu, Dk, Dv):
+    """The scores of the chunk and the state from those before as two bf16 terms
+    each (2^-16 of them), the state's own sums with at least 16 bits, and the
+    output's own rounding.  One term of either would miss by up to 2^-8 of its
+    sums, 100 times their share of this bar."""
     H = 2
     q, k, v, do, _ = _att(T, len(cu) - 1, H, Dk, Dv, 10, False)
     g = -torch.tensor([0.003, 0.05], device="cuda")
@@ -202,7 +202,7 @@ def test_bf16_attention_rounds_once_inside_a_chunk(A, T, cu, Dk, Dv):
     fp32 = (Dk + Dv + T + 64) * E
     for name, got, ref, (a, b, c, rev) in zip(("out", "dq", "dk", "dv"), [out, *grads], want, scans):
         inside, before = _conds(a, b, c, g64, np.array(cu), scale, rev, _score_part(a, b, g64, cu, rev))
-        bound = UB * np.abs(ref) + (2.0 ** -16 + fp32) * inside + (UB + 2.0 ** -16 + fp32) * (1 + UB) * before + 2.0 ** -129
+        bound = UB * np.abs(ref) + (2.0 ** -16 + fp32) * (inside + 2 * before) + 2.0 ** -129
         err = np.abs(to64(got) - ref)
         assert (err <= bound).all(), (name, float((err / bound).max()))
 
