@@ -288,6 +288,10 @@ cudaError_t linear_tc(const LinearArgs& a, bool* done) {
   return launch_tc_gemm(plan, op[0], op[1], a.M, a.N, a.K, np, kEpiForward, forward_epilogue(a), a.dev_err, a.stream);
 }
 
+// bf16: dz enters grad_x's and grad_w's products rounded once (their error in
+// the 2-norm is then 0.0023, 0.0017 with an exact dz).  A second term would
+// double both products, 85 of the 141 us of 2048 x 7168 x 2048, for less than
+// one more rounding of the result.
 cudaError_t linear_backward_tc(const LinearBwdArgs& a, bool* done) {
   const bool bf16 = a.dtype == ATTNRES_BF16, act = a.act != ATTNRES_ACT_NONE;
   const int np = bf16 ? 1 : 3;
