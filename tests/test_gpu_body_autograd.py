@@ -143,3 +143,26 @@ def test_rope_gradients_of_some_inputs(F, monkeypatch, D, need):
             hat = x[i - 2] * torch.rsqrt(x[i - 2].square().mean(-1, keepdim=True) + 1e-5)
             cond = (_randn(3 + i, 12, x[i - 2].shape[1], D) * hat).abs().sum((0, 1))
             assert ((t - full[i]).abs() <= 128 * E * cond).all()
+
+
+@pytest.mark.parametrize("dt,T,D", [(torch.float32, 150, 24), (torch.bfloat16, 200, 64), (torch.bfloat16, 6000, 64), (torch.float32, 6000, 24),
+                                    (torch.bfloat16, 6000, 128), (torch.float32, 0, 24), (torch.bfloat16, 0, 64)])
+def test_state_gradient_in_place_without_the_others(dt, T, D):
+    """grad_initial_state over grad_final_state, with grad_v only: the same bits
+    as apart (no rows: with no other output at all), empty sequences among
+    them."""
+    import depth_wise_attention_block_gb300 as A
+    H, n = 2, 4
+    q, k, v, do = (_randn(i, T, H, D, dtype=dt) for i in range(4))
+    cu = torch.tensor([0, T // 3, T // 3, T, T], dtype=torch.int32, device="cuda")
+    g, ds = -torch.tensor([0.02, 0.4], device="cuda"), _randn(5, n, H, D, D)
+    apart, over = torch.empty_like(ds), ds.clone()
+    gv = [torch.empty_like(v) if T else None for _ in range(2)]
+    A.attnres_linear_attention_backward(q, k, v, g, do, None, None, gv[0], cu_seqlens=cu, grad_final_state=ds, grad_initial_state=apart)
+    A.attnres_linear_attention_backward(q, k, v, g, do, None, None, gv[1], cu_seqlens=cu, grad_final_state=over, grad_initial_state=over)
+    assert torch.equal(apart, over) and torch.isfinite(over).all()
+    assert torch.equal(over[[1, 3]], ds[[1, 3]])
+    if T:
+        assert torch.equal(gv[0], gv[1])
+    else:
+        assert torch.equal(over, ds)
