@@ -10,14 +10,14 @@
 // Every product is a tcgen05.mma with its accumulator in TMEM.  a, b and c
 // arrive by TMA in the 128-byte swizzle and serve K-major (a b^T, a S) or
 // MN-major (P c, the token sums) from the same tile.  Eight warps turn the
-// scores into P (two bf16 terms, back into TMEM as the next product's operand) and
-// write the outputs; eight warps hold the state in fp32 registers (half a
+// scores into P (two bf16 terms, back into TMEM as the next product's operand)
+// and write the outputs; eight warps hold the state in fp32 registers (half a
 // row of Da per thread) and give it to the products as two bf16 terms (one
 // term, whose error is the output's own rounding once more, is 5 % faster: 288
-// us instead of 302 for the prompt below); all of them weigh b with the decays.  The weighted rows enter as three bf16 terms
-// (24 bits) where the state is a result, so that it keeps fp32 precision over
-// any number of chunks; each chunk's U starts from zero in TMEM and is added
-// in fp32 round-to-nearest.
+// us instead of 304 for the prompt below); all of them weigh b with the decays.
+// The weighted rows enter as three bf16 terms (24 bits) where the state is a
+// result, so that it keeps fp32 precision over any number of chunks; each
+// chunk's U starts from zero in TMEM and is added in fp32 round-to-nearest.
 //
 // A reversed scan (gradients of k and v) takes the chunks from the end and
 // mirrors the mask and the powers; nothing is reordered in memory.
@@ -37,7 +37,7 @@
 // the tensor cores, and the warps that turn scores into P and write outputs
 // about 6000.  16384 tokens x 56 heads of 128: the scan 199 us (4.7 TB/s), the
 // pieces' states 92 us (5.2 TB/s), joining them 10.6 us (each by itself, cold;
-// the whole call in a graph 302).
+// the whole call in a graph 304).
 #include <math.h>
 
 #include "attnres.h"
@@ -110,6 +110,13 @@ __device__ __forceinline__ void tc_mma_bf16_ts_warp(uint32_t d_tmem, uint32_t a_
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// two bf16 values, 1e30 in the place of a NaN (and of what is larger)
+__device__ __forceinline__ uint32_t finite_or_large(uint32_t v) {
+  uint32_t r;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x714A714Au));
+  return r;
 }
 
 // The outputs of one row from the tensors in memory, over the rows that the
@@ -645,7 +652,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) scan_tc_kernel(const __grid_c
               h[k] = pack_bf16x2(S[d + 2 * k], S[d + 2 * k + 1]);
               float x, y;
               f2_unpack(f2_fma(f2_pack(bf16lo(h[k]), bf16hi(h[k])), f2_pack(-1.f, -1.f), f2_pack(S[d + 2 * k], S[d + 2 * k + 1])), x, y);
-              l[k] = pack_bf16x2(x, y);
+              l[k] = finite_or_large(pack_bf16x2(x, y));  // (NaN behind an infinity, which keeps its sign so)
             }
             st_shared_v4(s_buf + to, h[0], h[1], h[2], h[3]);
             st_shared_v4(s_low + to, l[0], l[1], l[2], l[3]);

@@ -660,8 +660,9 @@ int64_t attnres_qk_norm_rope_backward_workspace_size(int64_t T, int Hq, int Hk, 
  * output's products with 16 bits, the state's own sums keep fp32 precision.
  * Others run on the CUDA cores in fp32.  Where the sequences do not fill the
  * GPU evenly they are cut into pieces (whose states lie in the workspace).
- * Infinities and NaN reach the tokens behind them and no others; an infinity
- * becomes NaN in the state.
+ * Infinities and NaN reach the tokens behind them and no others; a token's
+ * infinity becomes NaN in the state (one of the initial state stays what it
+ * is).
  * ---------------------------------------------------------------------- */
 int attnres_linear_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                              int64_t v_stride, int64_t T, int H, int Dk, int Dv, int dtype, const float* log_decay,

@@ -276,3 +276,27 @@ def test_bf16_activations_round_once(A, act):
     # (1 - s is off by 2^-22 where it is small, times z dv, at most 80)
     bound = UB * np.abs(slope) + fp32 * (s + np.abs(z64 * s * rest * dv)) + s * np.abs(z64 * dv) * 2.0 ** -21
     assert (np.abs(to64(dx[:, 0]) - slope) <= bound + 2.0 ** -129).all()
+
+
+@gpu
+@pytest.mark.parametrize("dt,T,D", [(torch.bfloat16, 100, 128), (torch.bfloat16, 400, 64), (torch.bfloat16, 6000, 128), (torch.bfloat16, 300, 96),
+                                    (torch.float32, 100, 40), (torch.float32, 6000, 24)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_an_infinite_initial_state_stays_infinite(A, dt, T, D, sign):
+    """One infinite entry (d, c): outputs of channel c are infinities of q_d's
+    sign, all others as without it; the final state keeps it."""
+    H, d, c = 2, 5, 9
+    q, k, v = (_randn(20 + i, T, H, D, dtype=dt) for i in range(3))
+    decay, s0 = -torch.tensor([0.01, 0.0], device="cuda"), _randn(24, 1, H, D, D)
+    runs = []
+    for bad in (False, True):
+        if bad:
+            s0[0, :, d, c] = sign * float("inf")
+        out, fin = torch.empty_like(v), torch.empty_like(s0)
+        A.attnres_linear_attention(q, k, v, decay, out, initial_state=s0, final_state=fin)
+        runs.append((out, fin))
+    (a, fa), (b, fb) = runs
+    keep = [i for i in range(D) if i != c]
+    assert torch.equal(a[..., keep], b[..., keep]) and torch.equal(fa[..., keep], fb[..., keep])
+    assert (b[..., c] == q[..., d].sign() * sign * float("inf")).all()
+    assert (fb[0, :, d, c] == sign * float("inf")).all()
