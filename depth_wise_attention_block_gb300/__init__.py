@@ -30,6 +30,7 @@ from ._native import (  # noqa: F401
     ATTNRES_F32,
     ATTNRES_MAX_BLOCKS,
     ATTNRES_MAX_SOURCES,
+    ATTNRES_RECURRENCE_CHUNK,
     ATTNRES_STATE_EARLY_LOADS,
     AttnresError,
     LIB_PATH,
@@ -45,6 +46,9 @@ __all__ = [
     "attnres_qk_norm_rope_backward_workspace_size", "attnres_linear_attention",
     "attnres_linear_attention_workspace_size", "attnres_linear_attention_backward",
     "attnres_linear_attention_backward_workspace_size", "attnres_linear_attention_step",
+    "attnres_layer_norm", "attnres_layer_norm_backward", "attnres_layer_norm_backward_workspace_size",
+    "attnres_gated_recurrence", "attnres_gated_recurrence_backward", "attnres_gated_recurrence_step",
+    "attnres_grad_clip", "attnres_grad_clip_workspace_size",
     "attnres_version", "AttnResState",
     "attnres_aggregate_host", "attnres_aggregate_host_workspace_size", "dtype_code", "AttnresError",
 ]
@@ -814,3 +818,191 @@ def attnres_linear_attention_step(q: torch.Tensor, k: torch.Tensor, v: torch.Ten
                                               float(Dk ** -0.5 if scale is None else scale), op, os_,
                                               _stream_on(stream, cur))
     _N.check(rc, "attnres_linear_attention_step")
+
+
+def attnres_layer_norm(x: torch.Tensor, out: torch.Tensor, gain: torch.Tensor | None = None,
+                       bias: torch.Tensor | None = None, eps: float = ATTNRES_DEFAULT_EPS, stream=None) -> None:
+    """out = gain (x - mean) / sqrt(var + eps) + bias over the rows of x [T, d].
+
+    x, out: float32 or bfloat16, rows contiguous at any stride; out may be x
+    itself; gain, bias: [d] float32 or None (1 and 0).
+    """
+    T, d = _matrix(x, "x")
+    dt = x.dtype
+    code = dtype_code(dt)
+    cur = _device_of(x, "x")
+    xp, xs = _rows(x, "x", (T, d), dt, cur)
+    op, os_ = _rows(out, "out", (T, d), dt, cur)
+    rc = _N.lib.attnres_layer_norm(xp, xs, T, d, code, _vec(gain, "gain", (d,), torch.float32, cur),
+                                   _vec(bias, "bias", (d,), torch.float32, cur), float(eps), op, os_,
+                                   _stream_on(stream, cur))
+    _N.check(rc, "attnres_layer_norm")
+
+
+def attnres_layer_norm_backward_workspace_size(T: int, d: int) -> int:
+    """Bytes of device workspace the gain and bias gradients of up to T rows need."""
+    return _N.check(_N.lib.attnres_layer_norm_backward_workspace_size(T, d), "attnres_layer_norm_backward_workspace_size")
+
+
+def attnres_layer_norm_backward(x: torch.Tensor, grad_out: torch.Tensor, grad_x: torch.Tensor | None,
+                                gain: torch.Tensor | None = None, grad_gain: torch.Tensor | None = None,
+                                grad_bias: torch.Tensor | None = None, eps: float = ATTNRES_DEFAULT_EPS,
+                                workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of attnres_layer_norm from the forward's input.  grad_x
+    [T, d] of x's dtype may be grad_out itself; grad_gain and grad_bias are
+    [d] float32.  They are overwritten; those that are None are skipped."""
+    T, d = _matrix(x, "x")
+    dt = x.dtype
+    code = dtype_code(dt)
+    cur = _device_of(x, "x")
+    xp, xs = _rows(x, "x", (T, d), dt, cur)
+    gp, gs = _rows(grad_out, "grad_out", (T, d), dt, cur)
+    op, os_ = _rows(grad_x, "grad_x", (T, d), dt, cur)
+    dg = _vec(grad_gain, "grad_gain", (d,), torch.float32, cur)
+    db = _vec(grad_bias, "grad_bias", (d,), torch.float32, cur)
+    need = 0
+    if workspace is None and (dg is not None or db is not None):
+        need = attnres_layer_norm_backward_workspace_size(T, d)
+    _keep, ws, nbytes = _workspace(workspace, need, x.device, stream)
+    rc = _N.lib.attnres_layer_norm_backward(xp, xs, T, d, code, _vec(gain, "gain", (d,), torch.float32, cur), float(eps), gp,
+                                            gs, op, os_, dg, db, ws, nbytes, _stream_on(stream, cur))
+    _N.check(rc, "attnres_layer_norm_backward")
+
+
+def _recurrence_args(x, forget, gate, cu_seqlens, cur: int):
+    T, C = _matrix(x, "x")
+    dt = x.dtype
+    code = dtype_code(dt)
+    xp, xs = _rows(x, "x", (T, C), dt, cur)
+    if forget is None:
+        raise ValueError("forget must be a tensor")
+    fp, fs = _rows(forget, "forget", (T, C), dt, cur)
+    gp, gs = _rows(gate, "gate", (T, C), dt, cur)
+    N = 1
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        if N < 1:
+            raise ValueError("cu_seqlens must hold at least two offsets")
+    cu = _vec(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, cur)
+    return T, C, dt, (xp, xs, fp, fs, gp, gs, T, C, code), cu, N
+
+
+def attnres_gated_recurrence(x: torch.Tensor, forget: torch.Tensor, out: torch.Tensor, gate: torch.Tensor | None = None,
+                             cu_seqlens: torch.Tensor | None = None, initial_state: torch.Tensor | None = None,
+                             final_state: torch.Tensor | None = None, chunk_states: torch.Tensor | None = None,
+                             stream=None) -> None:
+    """Gated linear recurrence over prompts, h_t = a_t h_{t-1} + (1 - a_t) x_t
+    with a = sigmoid(forget), out = h silu(gate) (h where gate is None).
+
+    x, forget, gate, out: [T, C] float32 or bfloat16, rows contiguous at any
+    stride; cu_seqlens: [num_seqs + 1] int32 on the device (None: one
+    sequence); initial_state, final_state: [num_seqs, C] float32 or None,
+    possibly the same tensor; chunk_states: [ceil(T / ATTNRES_RECURRENCE_CHUNK),
+    C] float32 for the backward, or None.
+    """
+    cur = _device_of(x, "x")
+    T, C, dt, head, cu, N = _recurrence_args(x, forget, gate, cu_seqlens, cur)
+    op, os_ = _rows(out, "out", (T, C), dt, cur)
+    rc = _N.lib.attnres_gated_recurrence(
+        *head, cu, N, _vec(initial_state, "initial_state", (N, C), torch.float32, cur),
+        _vec(final_state, "final_state", (N, C), torch.float32, cur), op, os_,
+        _vec(chunk_states, "chunk_states", (-(-T // ATTNRES_RECURRENCE_CHUNK), C), torch.float32, cur),
+        _stream_on(stream, cur))
+    _N.check(rc, "attnres_gated_recurrence")
+
+
+def attnres_gated_recurrence_backward(x: torch.Tensor, forget: torch.Tensor, chunk_states: torch.Tensor,
+                                      grad_out: torch.Tensor, grad_x: torch.Tensor | None,
+                                      grad_forget: torch.Tensor | None, grad_gate: torch.Tensor | None = None,
+                                      gate: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
+                                      initial_state: torch.Tensor | None = None,
+                                      grad_final_state: torch.Tensor | None = None,
+                                      grad_initial_state: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of attnres_gated_recurrence from the forward's inputs and the
+    chunk_states it wrote (grad_x, grad_forget, grad_gate [T, C] of x's dtype,
+    rows contiguous at any stride; the states' float32).  Those that are None
+    are not formed; grad_initial_state may be grad_final_state itself."""
+    cur = _device_of(x, "x")
+    T, C, dt, head, cu, N = _recurrence_args(x, forget, gate, cu_seqlens, cur)
+    dp, ds = _rows(grad_out, "grad_out", (T, C), dt, cur)
+    gx, gxs = _rows(grad_x, "grad_x", (T, C), dt, cur)
+    gf, gfs = _rows(grad_forget, "grad_forget", (T, C), dt, cur)
+    gg, ggs = _rows(grad_gate, "grad_gate", (T, C), dt, cur)
+    rc = _N.lib.attnres_gated_recurrence_backward(
+        *head, cu, N, _vec(initial_state, "initial_state", (N, C), torch.float32, cur),
+        _vec(chunk_states, "chunk_states", (-(-T // ATTNRES_RECURRENCE_CHUNK), C), torch.float32, cur), dp, ds,
+        _vec(grad_final_state, "grad_final_state", (N, C), torch.float32, cur), gx, gxs, gf, gfs, gg, ggs,
+        _vec(grad_initial_state, "grad_initial_state", (N, C), torch.float32, cur), _stream_on(stream, cur))
+    _N.check(rc, "attnres_gated_recurrence_backward")
+
+
+def attnres_gated_recurrence_step(x: torch.Tensor, forget: torch.Tensor, state: torch.Tensor, out: torch.Tensor,
+                                  gate: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                                  stream=None) -> None:
+    """One token per row: state [num_slots, C] float32 of slot slots[b]
+    (int32; None: b) updated in place, out [B, C] written.  A slot outside the
+    pool marks a padding row (its out row stays); rows of one slot are
+    consecutive tokens in row order."""
+    cur = _device_of(x, "x")
+    B, C, dt, head, _, _ = _recurrence_args(x, forget, gate, None, cur)
+    op, os_ = _rows(out, "out", (B, C), dt, cur)
+    num_slots = _matrix(state, "state")[0]
+    rc = _N.lib.attnres_gated_recurrence_step(*head, _vec(state, "state", (num_slots, C), torch.float32, cur), num_slots,
+                                              _vec(slots, "slots", (B,), torch.int32, cur), op, os_,
+                                              _stream_on(stream, cur))
+    _N.check(rc, "attnres_gated_recurrence_step")
+
+
+# ------------------------------------------------------ gradient clipping --
+
+def attnres_grad_clip_workspace_size() -> int:
+    """Bytes of device workspace attnres_grad_clip needs on the current device."""
+    return _N.check(_N.lib.attnres_grad_clip_workspace_size(), "attnres_grad_clip_workspace_size")
+
+
+def _flat_ptrs(tensors, name: str, like, cur: int):
+    """Pointers of contiguous tensors on device `cur`, of the dtypes and sizes of `like`."""
+    for i, (t, g) in enumerate(zip(tensors, like)):
+        if not isinstance(t, torch.Tensor) or t.get_device() != cur or t.dtype is not g.dtype:
+            _where(t, f"{name}[{i}]", g.dtype if isinstance(g, torch.Tensor) else None, cur)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if t is not g and t.numel() != g.numel():
+            raise ValueError(f"{name}[{i}] must hold {g.numel()} elements")
+    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+
+
+def attnres_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor,
+                      outs: Sequence[torch.Tensor] | None = None, workspace: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """norm [1] float32 = the 2-norm of all `grads` taken as one vector; where
+    it is above max_norm they are multiplied by max_norm / norm.
+
+    grads: contiguous float32 or bfloat16 tensors on one device; outs: where
+    the results go, tensor by tensor (None: in place, and nothing is written
+    where nothing is clipped; max_norm infinity: only the norm).  A norm that
+    is not finite scales nothing.  workspace: a device buffer of
+    attnres_grad_clip_workspace_size() bytes (allocated here through torch
+    when None).
+    """
+    grads = list(grads)
+    n = len(grads)
+    cur = _device_of(norm, "norm")
+    max_norm = float(max_norm)
+    gp = _flat_ptrs(grads, "grads", grads, cur)
+    if outs is None:
+        op = None if max_norm == float("inf") else gp
+    else:
+        outs = list(outs)
+        if len(outs) != n:
+            raise ValueError(f"{n} gradients, {len(outs)} outs")
+        op = _flat_ptrs(outs, "outs", grads, cur)
+    numels = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
+    dtypes = (ctypes.c_int * n)(*[dtype_code(t.dtype) for t in grads])
+    if not max_norm >= 0.0:
+        raise ValueError("max_norm must be >= 0")
+    need = attnres_grad_clip_workspace_size() if workspace is None else 0
+    _keep, ws, nbytes = _workspace(workspace, need, norm.device, stream)
+    rc = _N.lib.attnres_grad_clip(gp, op, numels, dtypes, n, max_norm, _vec(norm, "norm", (1,), torch.float32, cur), ws, nbytes,
+                                  _stream_on(stream, cur))
+    _N.check(rc, "attnres_grad_clip")

@@ -33,6 +33,8 @@ ATTNRES_ACT_GELU = 1
 ATTNRES_ACT_GELU_TANH = 2
 ATTNRES_ACT_SILU = 3
 
+ATTNRES_RECURRENCE_CHUNK = 64
+
 # every function declared in include/attnres.h
 EXPORTED = (
     "attnres_aggregate",
@@ -69,6 +71,14 @@ EXPORTED = (
     "attnres_linear_attention_backward",
     "attnres_linear_attention_backward_workspace_size",
     "attnres_linear_attention_step",
+    "attnres_layer_norm",
+    "attnres_layer_norm_backward",
+    "attnres_layer_norm_backward_workspace_size",
+    "attnres_gated_recurrence",
+    "attnres_gated_recurrence_backward",
+    "attnres_gated_recurrence_step",
+    "attnres_grad_clip",
+    "attnres_grad_clip_workspace_size",
     "attnres_debug_wait_test",
     "attnres_status_string",
     "attnres_last_error",
@@ -147,6 +157,16 @@ def _load() -> ctypes.CDLL:
         "attnres_linear_attention_backward_workspace_size": (i64, [i64, i32, i32, i32, i32, i32]),
         "attnres_linear_attention_step": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, i32, i32, vp, vp, i32, vp,
                                                 f32, vp, i64, vp]),
+        "attnres_layer_norm": (i32, [vp, i64, i64, i32, i32, vp, vp, f32, vp, i64, vp]),
+        "attnres_layer_norm_backward": (i32, [vp, i64, i64, i32, i32, vp, f32, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
+        "attnres_layer_norm_backward_workspace_size": (i64, [i64, i32]),
+        "attnres_gated_recurrence": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]),
+        "attnres_gated_recurrence_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp,
+                                                    vp, i64, vp, i64, vp, i64, vp, vp]),
+        "attnres_gated_recurrence_step": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i32, vp, vp, i64, vp]),
+        "attnres_grad_clip": (i32, [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i32), i32,
+                                    f32, vp, vp, i64, vp]),
+        "attnres_grad_clip_workspace_size": (i64, []),
         "attnres_debug_wait_test": (i32, [ctypes.c_uint64, i32]),
         "attnres_status_string": (ctypes.c_char_p, [i32]),
         "attnres_last_error": (ctypes.c_char_p, []),

@@ -12,12 +12,15 @@ tokens in a fixed order, so bit-reproducible).  The incoming gradient of r
 is taken in the sources' dtype (the backward kernel reads it so): an fp32
 gradient for bf16 sources is rounded to bf16 first.
 
-`linear`, `qk_norm_rope` and `linear_attention` wrap the calls of the same
-names the same way: nothing but the inputs is kept, the backward recomputes
-what it needs, incoming gradients are taken in the tensors' dtype, and
-gradients nobody asks for are not formed.  They can be differentiated once.
+`linear`, `qk_norm_rope`, `linear_attention`, `layer_norm` and
+`gated_recurrence` wrap the calls of the same names the same way: nothing but
+the inputs is kept (of the recurrence also its states ahead of every 64th
+row), the backward recomputes what it needs, incoming gradients are taken in
+the tensors' dtype, and gradients nobody asks for are not formed.  They can be differentiated once.
 Before a backward is captured in a CUDA graph, let go of eager graphs of the
 same leaves (torch runs their accumulation on the stream they were made on).
+
+`clip_grad_norm` ends a training step: it clips the gradients that leaves hold.
 """
 from __future__ import annotations
 
@@ -26,8 +29,14 @@ from torch.autograd.function import once_differentiable
 
 from . import (
     ATTNRES_DEFAULT_EPS,
+    ATTNRES_RECURRENCE_CHUNK,
     attnres_aggregate,
     attnres_aggregate_backward,
+    attnres_gated_recurrence,
+    attnres_gated_recurrence_backward,
+    attnres_grad_clip,
+    attnres_layer_norm,
+    attnres_layer_norm_backward,
     attnres_linear,
     attnres_linear_attention,
     attnres_linear_attention_backward,
@@ -36,7 +45,8 @@ from . import (
     attnres_qk_norm_rope_backward,
 )
 
-__all__ = ["AttnResAggregate", "aggregate", "linear", "qk_norm_rope", "linear_attention"]
+__all__ = ["AttnResAggregate", "aggregate", "linear", "qk_norm_rope", "linear_attention", "layer_norm",
+           "gated_recurrence", "clip_grad_norm"]
 
 
 class AttnResAggregate(torch.autograd.Function):
@@ -192,3 +202,98 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_deca
     attnres_linear_attention, differentiable in q, k, v and the initial
     states; rows outside every sequence are zero and get zero gradients."""
     return _LinearAttention.apply(q, k, v, log_decay, cu_seqlens, initial_state, scale)
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gain, bias, eps):
+        x = _rows_contiguous(x)
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        attnres_layer_norm(x, out, gain=gain, bias=bias, eps=eps)
+        ctx.save_for_backward(x, gain)
+        ctx.eps = eps
+        return out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad):
+        x, gain = ctx.saved_tensors
+        need_x, need_g, need_b, _ = ctx.needs_input_grad
+        gx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_x else None
+        gg, gb = (torch.empty(x.shape[1], dtype=torch.float32, device=x.device) if need else None for need in (need_g, need_b))
+        attnres_layer_norm_backward(x, _rows_contiguous(grad.to(x.dtype)), gx, gain=gain, grad_gain=gg, grad_bias=gb,
+                                    eps=ctx.eps)
+        return gx, gg, gb, None
+
+
+def layer_norm(x: torch.Tensor, gain: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+               eps: float = ATTNRES_DEFAULT_EPS) -> torch.Tensor:
+    """gain (x - mean) / sqrt(var + eps) + bias over x's last dimension; gain and bias [d] float32 or None."""
+    return _LayerNorm.apply(x.reshape(-1, x.shape[-1]), gain, bias, eps).reshape(x.shape)
+
+
+class _GatedRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, forget, gate, cu_seqlens, initial_state):
+        x, forget = _rows_contiguous(x), _rows_contiguous(forget)
+        gate = None if gate is None else _rows_contiguous(gate)
+        n = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+        T, C = x.shape
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if cu_seqlens is not None:
+            out.zero_()  # rows outside every sequence
+        final = torch.empty((n, C), dtype=torch.float32, device=x.device)
+        chunk = None
+        if any(ctx.needs_input_grad):
+            chunk = torch.empty((-(-T // ATTNRES_RECURRENCE_CHUNK), C), dtype=torch.float32, device=x.device)
+        initial_state = None if initial_state is None else initial_state.contiguous()
+        attnres_gated_recurrence(x, forget, out, gate=gate, cu_seqlens=cu_seqlens, initial_state=initial_state,
+                                 final_state=final, chunk_states=chunk)
+        ctx.save_for_backward(x, forget, gate, cu_seqlens, initial_state, chunk)
+        ctx.set_materialize_grads(False)
+        return out, final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_final):
+        x, forget, gate, cu_seqlens, initial_state, chunk = ctx.saved_tensors
+        if grad_out is None:
+            grad_out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        make = torch.empty if cu_seqlens is None else torch.zeros
+        need_x, need_f, need_g, _, need_0 = ctx.needs_input_grad
+        grads = [make(x.shape, dtype=x.dtype, device=x.device) if need else None for need in (need_x, need_f, need_g)]
+        g0 = torch.empty_like(initial_state) if need_0 else None
+        attnres_gated_recurrence_backward(x, forget, chunk, _rows_contiguous(grad_out.to(x.dtype)), *grads, gate=gate,
+                                          cu_seqlens=cu_seqlens, initial_state=initial_state,
+                                          grad_final_state=None if grad_final is None else grad_final.contiguous(),
+                                          grad_initial_state=g0)
+        return (*grads, None, g0)
+
+
+def gated_recurrence(x: torch.Tensor, forget: torch.Tensor, gate: torch.Tensor | None = None,
+                     cu_seqlens: torch.Tensor | None = None,
+                     initial_state: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(out [T, C], final states [num_seqs, C] float32) of
+    attnres_gated_recurrence, differentiable in x, forget, gate and the
+    initial states; rows outside every sequence are zero and get zero
+    gradients."""
+    return _GatedRecurrence.apply(x, forget, gate, cu_seqlens, initial_state)
+
+
+def clip_grad_norm(leaves, max_norm: float) -> torch.Tensor:
+    """The 2-norm [1] float32 of all the gradients that `leaves` hold, which are
+    then clipped in place to max_norm (attnres_grad_clip).  Nothing is copied to
+    the host.  A gradient that is not contiguous is replaced by a contiguous
+    copy first."""
+    leaves = [leaves] if isinstance(leaves, torch.Tensor) else list(leaves)
+    grads = []
+    for p in {id(p): p for p in leaves}.values():  # a leaf named twice counts once
+        if p.grad is not None:
+            if not p.grad.is_contiguous():
+                p.grad = p.grad.contiguous()
+            grads.append(p.grad)
+    if not grads:
+        raise ValueError("none of the leaves holds a gradient")
+    norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+    attnres_grad_clip(grads, max_norm, norm)
+    return norm

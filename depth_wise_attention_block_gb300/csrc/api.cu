@@ -178,7 +178,7 @@ struct HostPipe {
 
 extern "C" {
 
-int attnres_version(void) { return (2 << 16) | 2; }
+int attnres_version(void) { return (2 << 16) | 3; }
 
 const char* attnres_status_string(int status) {
   switch (status) {

@@ -1,6 +1,7 @@
 // Host-side launch interface between the C ABI (body_api.cu) and the kernels
 // of a layer body: matrix products with a fused epilogue, head norms with
-// rotation, and linear attention with a decay per head.
+// rotation, linear attention with a decay per head, layer norms, the gated
+// linear recurrence; and the norm and clipping of a training step's gradients.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -139,5 +140,84 @@ struct LinAttnStepArgs {
   cudaStream_t stream;
 };
 cudaError_t launch_linear_attention_step(const LinAttnStepArgs& a);
+
+// -------------------------------------------------------- layer norm -----
+
+struct LayerNormArgs {
+  const void* x;
+  int64_t xs;  // row strides, elements
+  const void* dy;
+  int64_t dys;  // backward: the incoming gradient
+  void* out;
+  int64_t os;  // forward: the result; backward: x's gradient
+  const float *gain, *bias;
+  float *dgain, *dbias;
+  int64_t T;
+  int d;
+  int dtype;
+  float eps;
+  bool backward;
+  float* workspace;  // gain and bias gradients' partial rows
+  cudaStream_t stream;
+};
+cudaError_t launch_layer_norm(const LayerNormArgs& a);
+int64_t layer_norm_backward_workspace_bytes(int64_t T, int d);
+
+// --------------------------------------------------- gated recurrence ----
+
+struct RecurrenceArgs {
+  const void *x, *f, *g;  // value, forget gate, output gate (or null)
+  int64_t xs, fs, gs;     // row strides, elements
+  int64_t T;
+  int C;
+  int dtype;
+  const int32_t* cu;  // null: one sequence of T rows
+  int N;
+  const float* s0;
+  float* s1;
+  void* out;
+  int64_t os;
+  float* chunk;  // [ceil(T / 64), C] states before every 64th row: the forward writes them (or null), the backward reads them
+  // backward
+  const void* dout;
+  int64_t dos;
+  const float* ds1;
+  void *dx, *df, *dg;  // each may be null
+  int64_t dxs, dfs, dgs;
+  float* ds0;
+  cudaStream_t stream;
+};
+cudaError_t launch_gated_recurrence(const RecurrenceArgs& a);
+cudaError_t launch_gated_recurrence_backward(const RecurrenceArgs& a);
+
+struct RecurrenceStepArgs {
+  const void *x, *f, *g;
+  int64_t xs, fs, gs;
+  int B, C;
+  int dtype;
+  float* state;
+  int num_slots;
+  const int32_t* slots;
+  void* out;
+  int64_t os;
+  cudaStream_t stream;
+};
+cudaError_t launch_gated_recurrence_step(const RecurrenceStepArgs& a);
+
+// ------------------------------------------------- gradient clipping -----
+
+struct GradClipArgs {
+  const void* const* grads;
+  void* const* outs;  // null: only the norm
+  const int64_t* numels;
+  const int* dtypes;
+  int n;
+  float max_norm;
+  float* norm;
+  double* workspace;  // sums of squares, one per CTA
+  cudaStream_t stream;
+};
+cudaError_t launch_grad_clip(const GradClipArgs& a);
+int64_t grad_clip_workspace_bytes();
 
 }  // namespace attnres

@@ -1,7 +1,11 @@
-// The C ABI of a layer body's operators (declared in include/attnres.h):
-// argument checks and dispatch to the kernels (linear.cu, qk_norm_rope.cu,
-// linear_attention.cu).
+// The C ABI of a layer body's operators and of gradient clipping (declared in
+// include/attnres.h): argument checks and dispatch to the kernels (linear.cu,
+// qk_norm_rope.cu, linear_attention.cu, layer_norm.cu, gated_recurrence.cu,
+// grad_clip.cu).
+#include <algorithm>
 #include <cmath>
+#include <memory>
+#include <new>
 
 #include "api_common.h"
 #include "body.h"
@@ -112,6 +116,62 @@ int check_la(const void* q, int64_t qs, const void* k, int64_t ks, const void* v
   if (!log_decay) return fail(ATTNRES_EINVAL, "log_decay is NULL");
   if (T > 0 && (!q || !k || !v)) return fail(ATTNRES_EINVAL, "q/k/v is NULL");
   return ATTNRES_OK;
+}
+
+constexpr int kMaxNormWidth = 1 << 24;   // of a layer norm's row
+constexpr int kMaxChannels = 1 << 24;    // of a recurrence
+constexpr int kMaxTensors = 65535;       // of a list of gradients
+
+int check_ln(const void* x, int64_t xs, int64_t T, int d, int dtype, float eps) {
+  if (!valid_dtype(dtype)) return fail(ATTNRES_EDTYPE, "dtype %d", dtype);
+  if (T < 0 || d < 1) return fail(ATTNRES_EINVAL, "T=%lld d=%d", (long long)T, d);
+  if (d > kMaxNormWidth) return fail(ATTNRES_ERANGE, "d=%d", d);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(ATTNRES_EINVAL, "eps must be finite and >= 0");
+  if (!stride_ok(xs, d)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  if (!span_ok(T, xs)) return fail(ATTNRES_ERANGE, "T*stride too large");
+  if (T > 0 && !x) return fail(ATTNRES_EINVAL, "x is NULL");
+  return ATTNRES_OK;
+}
+
+// a row tensor [T, C] that a recurrence reads or writes (null: absent)
+int check_gr_rows(const void* p, int64_t stride, int64_t T, int C) {
+  if (!p) return ATTNRES_OK;
+  if (!stride_ok(stride, C)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  if (!span_ok(T, stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
+  return ATTNRES_OK;
+}
+
+int check_gr(const void* x, int64_t xs, const void* f, int64_t fs, const void* g, int64_t gs, int64_t T, int C, int dtype,
+             const int32_t* cu, int N) {
+  if (!valid_dtype(dtype)) return fail(ATTNRES_EDTYPE, "dtype %d", dtype);
+  if (T < 0 || C < 1 || N < 1) return fail(ATTNRES_EINVAL, "T=%lld C=%d num_seqs=%d", (long long)T, C, N);
+  if (T > INT32_MAX - 65536 || C > kMaxChannels || N > 65535)
+    return fail(ATTNRES_ERANGE, "T=%lld C=%d num_seqs=%d", (long long)T, C, N);
+  if (!cu && N != 1) return fail(ATTNRES_EINVAL, "num_seqs=%d without cu_seqlens", N);
+  if (T > 0 && (!x || !f)) return fail(ATTNRES_EINVAL, "x/forget is NULL");
+  int rc = check_gr_rows(x, xs, T, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(f, fs, T, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(g, gs, T, C);
+  return rc;
+}
+
+// [begin, end) of a tensor of a list, and whether it is written
+struct Interval {
+  uintptr_t begin, end;
+  bool out;
+};
+
+// Every output apart from every other output and from every input but its
+// own (which is left out of the list where they are the same).
+bool intervals_apart(Interval* v, int n) {
+  std::sort(v, v + n, [](const Interval& a, const Interval& b) { return a.begin < b.begin; });
+  uintptr_t read_to = 0, written_to = 0;
+  for (int i = 0; i < n; ++i) {
+    if (v[i].begin < written_to || (v[i].out && v[i].begin < read_to)) return false;
+    uintptr_t& to = v[i].out ? written_to : read_to;
+    if (v[i].end > to) to = v[i].end;
+  }
+  return true;
 }
 
 }  // namespace
@@ -565,6 +625,296 @@ int attnres_linear_attention_step(const void* q, int64_t q_stride, const void* k
   a.os = out_stride;
   const cudaError_t e = (a.stream = static_cast<cudaStream_t>(stream), launch_linear_attention_step(a));
   if (e != cudaSuccess) return cuda_fail(e, "attnres_linear_attention_step launch");
+  return ok();
+}
+
+int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, const float* bias,
+                       float eps, void* out, int64_t out_stride, void* stream) {
+  const int rc = check_ln(x, x_stride, T, d, dtype, eps);
+  if (rc != ATTNRES_OK) return rc;
+  if (!stride_ok(out_stride, d)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  if (!span_ok(T, out_stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
+  if (T == 0) return ok();
+  if (!out) return fail(ATTNRES_EINVAL, "out is NULL");
+  const int64_t es = dtype_bytes(dtype), w = d * es;
+  {
+    const Rows in[3] = {{x, T, w, x_stride * es}, {gain, 1, d * 4LL, d * 4LL}, {bias, 1, d * 4LL, d * 4LL}};
+    const Rows outs[1] = {{out, T, w, out_stride * es}};
+    const int in_place[1] = {0};
+    const int ra = check_apart(in, 3, outs, 1, in_place);
+    if (ra != ATTNRES_OK) return ra;
+  }
+  LayerNormArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.out = out;
+  a.os = out_stride;
+  a.gain = gain;
+  a.bias = bias;
+  a.T = T;
+  a.d = d;
+  a.dtype = dtype;
+  a.eps = eps;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_layer_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_layer_norm launch");
+  return ok();
+}
+
+int64_t attnres_layer_norm_backward_workspace_size(int64_t T, int d) {
+  if (T < 0 || d < 1) return fail(ATTNRES_EINVAL, "T=%lld d=%d", (long long)T, d);
+  if (d > kMaxNormWidth) return fail(ATTNRES_ERANGE, "d=%d", d);
+  const int64_t n = layer_norm_backward_workspace_bytes(T, d);
+  if (n < 0) return fail(ATTNRES_ECUDA, "device query");
+  ok();
+  return n;
+}
+
+int attnres_layer_norm_backward(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, float eps,
+                                const void* grad_out, int64_t grad_out_stride, void* grad_x, int64_t grad_x_stride,
+                                float* grad_gain, float* grad_bias, void* workspace, int64_t workspace_bytes, void* stream) {
+  int rc = check_ln(x, x_stride, T, d, dtype, eps);
+  if (rc != ATTNRES_OK) return rc;
+  const int64_t es = dtype_bytes(dtype), w = d * es, vec = d * 4LL;
+  if (!stride_ok(grad_out_stride, d) || !stride_ok(grad_x_stride, d))
+    return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
+  if (!span_ok(T, grad_out_stride) || !span_ok(T, grad_x_stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
+  if (!grad_x && !grad_gain && !grad_bias) return ok();
+  if (T > 0 && !grad_out) return fail(ATTNRES_EINVAL, "grad_out is NULL");
+  {
+    const int64_t wsb = workspace && workspace_bytes > 0 ? workspace_bytes : 0;
+    const Rows in[3] = {{grad_out, T, w, grad_out_stride * es}, {x, T, w, x_stride * es}, {gain, 1, vec, vec}};
+    const Rows out[4] = {{grad_x, T, w, grad_x_stride * es}, {grad_gain, 1, vec, vec}, {grad_bias, 1, vec, vec}, {workspace, 1, wsb, wsb}};
+    const int in_place[4] = {0, -1, -1, -1};
+    rc = check_apart(in, 3, out, 4, in_place);
+    if (rc != ATTNRES_OK) return rc;
+  }
+  if (T > 0 && (grad_gain || grad_bias)) {
+    if (!workspace) return fail(ATTNRES_EINVAL, "the gain and bias gradients need a workspace");
+    const int64_t need = layer_norm_backward_workspace_bytes(T, d);
+    if (need < 0) return fail(ATTNRES_ECUDA, "device query");
+    rc = check_workspace(workspace, workspace_bytes, need);
+    if (rc != ATTNRES_OK) return rc;
+  }
+  LayerNormArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.dy = grad_out;
+  a.dys = grad_out_stride;
+  a.out = grad_x;
+  a.os = grad_x_stride;
+  a.gain = gain;
+  a.dgain = grad_gain;
+  a.dbias = grad_bias;
+  a.T = T;
+  a.d = d;
+  a.dtype = dtype;
+  a.eps = eps;
+  a.backward = true;
+  a.workspace = static_cast<float*>(workspace);
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_layer_norm(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_layer_norm_backward launch");
+  return ok();
+}
+
+int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
+                             int64_t gate_stride, int64_t T, int C, int dtype, const int32_t* cu_seqlens, int num_seqs,
+                             const float* initial_state, float* final_state, void* out, int64_t out_stride,
+                             float* chunk_states, void* stream) {
+  int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, T, C, dtype, cu_seqlens, num_seqs);
+  if (rc != ATTNRES_OK) return rc;
+  if (T > 0 && !out) return fail(ATTNRES_EINVAL, "out is NULL");
+  rc = check_gr_rows(out, out_stride, T, C);
+  if (rc != ATTNRES_OK) return rc;
+  if (T == 0 && !final_state) return ok();
+  {
+    const int64_t es = dtype_bytes(dtype), w = C * es, st = (int64_t)num_seqs * C * 4, cub = (num_seqs + 1) * 4LL;
+    const int64_t ch = (T + ATTNRES_RECURRENCE_CHUNK - 1) / ATTNRES_RECURRENCE_CHUNK * C * 4;
+    const Rows in[5] = {{x, T, w, x_stride * es}, {forget, T, w, forget_stride * es}, {gate, T, w, gate_stride * es},
+                        {cu_seqlens, 1, cub, cub}, {initial_state, 1, st, st}};
+    const Rows outs[3] = {{out, T, w, out_stride * es}, {final_state, 1, st, st}, {chunk_states, 1, ch, ch}};
+    const int in_place[3] = {-1, 4, -1};
+    rc = check_apart(in, 5, outs, 3, in_place);
+    if (rc != ATTNRES_OK) return rc;
+  }
+  RecurrenceArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.f = forget;
+  a.fs = forget_stride;
+  a.g = gate;
+  a.gs = gate_stride;
+  a.T = T;
+  a.C = C;
+  a.dtype = dtype;
+  a.cu = cu_seqlens;
+  a.N = num_seqs;
+  a.s0 = initial_state;
+  a.s1 = final_state;
+  a.out = out;
+  a.os = out_stride;
+  a.chunk = T > 0 ? chunk_states : nullptr;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_gated_recurrence(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_gated_recurrence launch");
+  return ok();
+}
+
+int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride,
+                                      const void* gate, int64_t gate_stride, int64_t T, int C, int dtype,
+                                      const int32_t* cu_seqlens, int num_seqs, const float* initial_state,
+                                      const float* chunk_states, const void* grad_out, int64_t grad_out_stride,
+                                      const float* grad_final_state, void* grad_x, int64_t grad_x_stride, void* grad_forget,
+                                      int64_t grad_forget_stride, void* grad_gate, int64_t grad_gate_stride,
+                                      float* grad_initial_state, void* stream) {
+  int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, T, C, dtype, cu_seqlens, num_seqs);
+  if (rc != ATTNRES_OK) return rc;
+  if (grad_gate && !gate) return fail(ATTNRES_EINVAL, "grad_gate without gate");
+  if (!grad_x && !grad_forget && !grad_gate && !grad_initial_state) return ok();
+  if (T == 0 && !grad_initial_state) return ok();
+  if (T > 0 && (!grad_out || !chunk_states)) return fail(ATTNRES_EINVAL, "grad_out/chunk_states is NULL");
+  rc = check_gr_rows(grad_out, grad_out_stride, T, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_x, grad_x_stride, T, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_forget, grad_forget_stride, T, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_gate, grad_gate_stride, T, C);
+  if (rc != ATTNRES_OK) return rc;
+  {
+    const int64_t es = dtype_bytes(dtype), w = C * es, st = (int64_t)num_seqs * C * 4, cub = (num_seqs + 1) * 4LL;
+    const int64_t ch = (T + ATTNRES_RECURRENCE_CHUNK - 1) / ATTNRES_RECURRENCE_CHUNK * C * 4;
+    const Rows in[8] = {{x, T, w, x_stride * es}, {forget, T, w, forget_stride * es}, {gate, T, w, gate_stride * es},
+                        {cu_seqlens, 1, cub, cub}, {initial_state, 1, st, st}, {chunk_states, 1, ch, ch},
+                        {grad_out, T, w, grad_out_stride * es}, {grad_final_state, 1, st, st}};
+    const Rows outs[4] = {{grad_x, T, w, grad_x_stride * es}, {grad_forget, T, w, grad_forget_stride * es},
+                          {grad_gate, T, w, grad_gate_stride * es}, {grad_initial_state, 1, st, st}};
+    const int in_place[4] = {-1, -1, -1, 7};
+    rc = check_apart(in, 8, outs, 4, in_place);
+    if (rc != ATTNRES_OK) return rc;
+  }
+  RecurrenceArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.f = forget;
+  a.fs = forget_stride;
+  a.g = gate;
+  a.gs = gate_stride;
+  a.T = T;
+  a.C = C;
+  a.dtype = dtype;
+  a.cu = cu_seqlens;
+  a.N = num_seqs;
+  a.s0 = initial_state;
+  a.chunk = const_cast<float*>(chunk_states);
+  a.dout = grad_out;
+  a.dos = grad_out_stride;
+  a.ds1 = grad_final_state;
+  a.dx = grad_x;
+  a.dxs = grad_x_stride;
+  a.df = grad_forget;
+  a.dfs = grad_forget_stride;
+  a.dg = grad_gate;
+  a.dgs = grad_gate_stride;
+  a.ds0 = grad_initial_state;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_gated_recurrence_backward(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_gated_recurrence_backward launch");
+  return ok();
+}
+
+int attnres_gated_recurrence_step(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
+                                  int64_t gate_stride, int B, int C, int dtype, float* state, int num_slots,
+                                  const int32_t* slots, void* out, int64_t out_stride, void* stream) {
+  if (B < 0 || num_slots < 0) return fail(ATTNRES_EINVAL, "B=%d num_slots=%d", B, num_slots);
+  if (B > 65535) return fail(ATTNRES_ERANGE, "B=%d", B);
+  int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, B, C, dtype, nullptr, 1);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(out, out_stride, B, C);
+  if (rc != ATTNRES_OK) return rc;
+  if (!slots && B > num_slots) return fail(ATTNRES_EINVAL, "B=%d rows for %d slots", B, num_slots);
+  if (B == 0 || num_slots == 0) return ok();
+  if (!state || !out) return fail(ATTNRES_EINVAL, "state/out is NULL");
+  {
+    const int64_t es = dtype_bytes(dtype), w = C * es, st = (int64_t)num_slots * C * 4;
+    const Rows in[4] = {{x, B, w, x_stride * es}, {forget, B, w, forget_stride * es}, {gate, B, w, gate_stride * es},
+                        {slots, 1, B * 4LL, B * 4LL}};
+    const Rows outs[2] = {{out, B, w, out_stride * es}, {state, 1, st, st}};
+    rc = check_apart(in, 4, outs, 2, nullptr);
+    if (rc != ATTNRES_OK) return rc;
+  }
+  RecurrenceStepArgs a{};
+  a.x = x;
+  a.xs = x_stride;
+  a.f = forget;
+  a.fs = forget_stride;
+  a.g = gate;
+  a.gs = gate_stride;
+  a.B = B;
+  a.C = C;
+  a.dtype = dtype;
+  a.state = state;
+  a.num_slots = num_slots;
+  a.slots = slots;
+  a.out = out;
+  a.os = out_stride;
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_gated_recurrence_step(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_gated_recurrence_step launch");
+  return ok();
+}
+
+int64_t attnres_grad_clip_workspace_size(void) {
+  const int64_t n = grad_clip_workspace_bytes();
+  if (n < 0) return fail(ATTNRES_ECUDA, "device query");
+  ok();
+  return n;
+}
+
+int attnres_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes, int n,
+                      float max_norm, float* out_norm, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (n < 0) return fail(ATTNRES_EINVAL, "n=%d", n);
+  if (n > kMaxTensors) return fail(ATTNRES_ERANGE, "n=%d", n);
+  if (n > 0 && (!grads || !numels || !dtypes)) return fail(ATTNRES_EINVAL, "grads/numels/dtypes is NULL");
+  if (outs && !(max_norm >= 0.f)) return fail(ATTNRES_EINVAL, "max_norm must be >= 0");
+  if (!out_norm) return fail(ATTNRES_EINVAL, "out_norm is NULL");
+  if (!aligned(out_norm, 4)) return fail(ATTNRES_EINVAL, "out_norm is not 4-byte aligned");
+  std::unique_ptr<Interval[]> v(new (std::nothrow) Interval[2 * (size_t)n + 2]);
+  if (!v) return fail(ATTNRES_ERANGE, "no host memory for a list of %d tensors", n);
+  int m = 0;
+  auto add = [&](const void* p, int64_t bytes, bool out) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes > 0) v[m++] = {b, b + (uintptr_t)bytes, out};
+  };
+  for (int i = 0; i < n; ++i) {
+    if (!valid_dtype(dtypes[i])) return fail(ATTNRES_EDTYPE, "tensor %d: dtype %d", i, dtypes[i]);
+    if (numels[i] < 0) return fail(ATTNRES_EINVAL, "tensor %d: %lld elements", i, (long long)numels[i]);
+    if (numels[i] > kMaxElems) return fail(ATTNRES_ERANGE, "tensor %d: %lld elements", i, (long long)numels[i]);
+    if (numels[i] == 0) continue;
+    const int es = (int)dtype_bytes(dtypes[i]);
+    if (!grads[i] || (outs && !outs[i])) return fail(ATTNRES_EINVAL, "tensor %d is NULL", i);
+    if (!aligned(grads[i], es) || (outs && !aligned(outs[i], es)))
+      return fail(ATTNRES_EINVAL, "tensor %d is not aligned to its elements", i);
+    const bool same = outs && outs[i] == grads[i];
+    if (!same) add(grads[i], numels[i] * es, false);
+    if (outs) add(outs[i], numels[i] * es, true);
+  }
+  add(out_norm, 4, true);
+  if (workspace && workspace_bytes > 0) add(workspace, workspace_bytes, true);
+  if (!intervals_apart(v.get(), m)) return fail(ATTNRES_EINVAL, "an output overlaps another tensor of the call");
+  const int64_t need = grad_clip_workspace_bytes();
+  if (need < 0) return fail(ATTNRES_ECUDA, "device query");
+  const int rc = check_workspace(workspace, workspace_bytes, need);
+  if (rc != ATTNRES_OK) return rc;
+  GradClipArgs a{};
+  a.grads = grads;
+  a.outs = outs;
+  a.numels = numels;
+  a.dtypes = dtypes;
+  a.n = n;
+  a.max_norm = max_norm;
+  a.norm = out_norm;
+  a.workspace = static_cast<double*>(workspace);
+  a.stream = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_grad_clip(a);
+  if (e != cudaSuccess) return cuda_fail(e, "attnres_grad_clip launch");
   return ok();
 }
 

@@ -36,6 +36,8 @@ from . import (
     attnres_aggregate_backward_workspace_size,
     attnres_aggregate_fold,
     attnres_block_step,
+    attnres_grad_clip,
+    attnres_grad_clip_workspace_size,
     attnres_interblock,
     attnres_interblock_workspace_size,
     attnres_intrablock_step,
@@ -335,6 +337,8 @@ class StackBackward:
         self.dW = torch.empty((fwd.L + 1, d), dtype=torch.float32, device=dev)
         nbytes = attnres_aggregate_backward_workspace_size(T, d)
         self.ws = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=dev)
+        self.norm = torch.empty(1, dtype=torch.float32, device=dev)
+        self.clip_ws = torch.empty(attnres_grad_clip_workspace_size(), dtype=torch.uint8, device=dev)
         self.graph = None
 
     def _issue(self, dr_out, stream=None, on_call=None) -> None:
@@ -396,6 +400,14 @@ class StackBackward:
         else:
             self._issue(dr_out, stream, on_call)
         return self.dh0, self.dW
+
+    def clip(self, max_norm: float, others=(), stream=None) -> torch.Tensor:
+        """The 2-norm [1] float32 of dW and the tensors of `others` (gradients of
+        the same step, contiguous) taken as one vector, all of which are then
+        clipped in place to max_norm (attnres_grad_clip).  dh0, the gradient
+        at the stack's input, flows on as it is unless it is among them."""
+        attnres_grad_clip([self.dW, *others], max_norm, self.norm, workspace=self.clip_ws, stream=stream)
+        return self.norm
 
     def capture(self, dr_out) -> None:
         """Record the whole backward for dr_out into a CUDA graph (after one

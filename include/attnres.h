@@ -723,6 +723,148 @@ int attnres_linear_attention_step(const void* q, int64_t q_stride, const void* k
                                   int64_t out_stride, void* stream);
 
 /* ------------------------------------------------------------------------
+ * attnres_layer_norm -- layer norm of whole rows:
+ *   h = (x - mean_c x) / sqrt(mean_c (x - mean)^2 + eps),  out = gain h + bias
+ * x, out      device [T, d] of dtype, row strides given; out may be x itself
+ *             (same stride) and may share no other memory with an input
+ * gain, bias  device [d] fp32 or NULL (1 and 0)
+ * eps         finite, >= 0
+ * T >= 0 (0 launches nothing and accepts NULL buffers), d 1..2^24
+ * (ATTNRES_ERANGE above).  Sums are fp32; the mean is held as two numbers, so
+ * rows whose mean is far from zero keep their digits.
+ * ---------------------------------------------------------------------- */
+int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, const float* bias,
+                       float eps, void* out, int64_t out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attnres_layer_norm_backward -- its gradients, from the forward's input
+ * (nothing is kept).  With n = gain * grad_out and sigma the row's divisor:
+ *   grad_x = (n - mean_c n - h mean_c(n h)) / sigma
+ *   grad_gain[c] = sum_t grad_out h,   grad_bias[c] = sum_t grad_out
+ * grad_out    device [T, d] of dtype, row stride given
+ * grad_x      the same, or NULL to skip; it may be grad_out itself (same stride)
+ * grad_gain, grad_bias  device [d] fp32, overwritten, or NULL to skip; summed
+ *             in fp32 in a fixed order (bit-reproducible)
+ * workspace   device scratch, 256-byte aligned, of at least
+ *             attnres_layer_norm_backward_workspace_size(T, d) bytes; may be
+ *             NULL when neither grad_gain nor grad_bias is wanted.  Calls that
+ *             overlap in time need one each.
+ * T = 0 only zeroes grad_gain and grad_bias.
+ * ---------------------------------------------------------------------- */
+int attnres_layer_norm_backward(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, float eps,
+                                const void* grad_out, int64_t grad_out_stride, void* grad_x, int64_t grad_x_stride,
+                                float* grad_gain, float* grad_bias, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the gain and bias gradients of up to T rows need on the
+ * current device. */
+int64_t attnres_layer_norm_backward_workspace_size(int64_t T, int d);
+
+/* ------------------------------------------------------------------------
+ * attnres_gated_recurrence -- gated linear recurrence over prompts: a state
+ * of C channels per sequence, forgetting by a gate per token and channel:
+ *   a_t = 1 / (1 + exp(-forget_t)),   h_t = a_t h_{t-1} + (1 - a_t) x_t
+ *   out_t = h_t gate_t / (1 + exp(-gate_t))   (h_t where gate is NULL)
+ * x, forget   device [T, C] of dtype, row strides given (slices of one
+ *             projection's rows, say)
+ * gate        the same or NULL
+ * cu_seqlens  device [num_seqs + 1] int32, non-decreasing, 0 <= .. <= T:
+ *             sequence n is rows cu_seqlens[n] .. cu_seqlens[n+1] - 1 (it may
+ *             be empty).  Rows outside every sequence are left as they are.
+ *             Values outside 0..T are clamped; offsets that decrease give
+ *             unspecified results.  NULL: one sequence of T rows (num_seqs =
+ *             1).
+ * initial_state device [num_seqs, C] fp32 or NULL (zero)
+ * final_state device [num_seqs, C] fp32 or NULL; it may be initial_state
+ *             itself
+ * out         device [T, C] of dtype, row stride given; it shares no memory
+ *             with an input
+ * chunk_states device [ceil(T / ATTNRES_RECURRENCE_CHUNK), C] fp32 or NULL:
+ *             the states ahead of every 64th row, which the backward goes on
+ *             from (rows of it that lie in no sequence are unspecified)
+ * T 0..2^31 - 65537, C 1..2^24, num_seqs 1..65535 (ATTNRES_ERANGE above).
+ * The state is held in fp32.  A forget gate below -83 counts as -83 (a_t of
+ * 1e-36).  Infinities and NaN reach the tokens of their channel and sequence
+ * behind them and no others (an infinite state may become NaN).
+ * ---------------------------------------------------------------------- */
+#define ATTNRES_RECURRENCE_CHUNK 64
+int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
+                             int64_t gate_stride, int64_t T, int C, int dtype, const int32_t* cu_seqlens, int num_seqs,
+                             const float* initial_state, float* final_state, void* out, int64_t out_stride,
+                             float* chunk_states, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attnres_gated_recurrence_backward -- its gradients, from the forward's
+ * inputs and its chunk_states.  With s = gate / (1 + exp(-gate)) (1 without a
+ * gate) and dh_t the gradient at h_t:
+ *   dh_t = grad_out_t s_t + a_{t+1} dh_{t+1}
+ *   (of a sequence's last token: grad_out s + grad_final_state)
+ *   grad_x = (1 - a) dh,   grad_forget = dh (h_{t-1} - x) a (1 - a),
+ *   grad_gate = grad_out h ds/dgate,
+ *   grad_initial_state = a dh of the first token (grad_final_state itself for
+ *   an empty sequence).
+ * chunk_states  as the forward wrote them for the same arguments
+ * grad_out      device [T, C] of dtype, row stride given
+ * grad_x, grad_forget, grad_gate  device [T, C] of dtype, row strides given,
+ *             or NULL to skip; rows outside every sequence are left as they
+ *             are.  grad_gate needs gate.
+ * grad_final_state    device [num_seqs, C] fp32 or NULL (zero)
+ * grad_initial_state  the same shape or NULL; it may be grad_final_state
+ * Other arguments as in attnres_gated_recurrence.
+ * ---------------------------------------------------------------------- */
+int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride,
+                                      const void* gate, int64_t gate_stride, int64_t T, int C, int dtype,
+                                      const int32_t* cu_seqlens, int num_seqs, const float* initial_state,
+                                      const float* chunk_states, const void* grad_out, int64_t grad_out_stride,
+                                      const float* grad_final_state, void* grad_x, int64_t grad_x_stride, void* grad_forget,
+                                      int64_t grad_forget_stride, void* grad_gate, int64_t grad_gate_stride,
+                                      float* grad_initial_state, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attnres_gated_recurrence_step -- the form for decoding: row b of the batch
+ * is one token of the sequence whose state lies in slot slots[b].
+ * x, forget, gate, out  device [B, C] of dtype, row strides given (gate: or
+ *             NULL)
+ * state       device [num_slots, C] fp32, updated in place
+ * slots       device [B] int32, or NULL (row b in slot b, B <= num_slots).
+ *             A row whose slot is outside 0..num_slots-1 is padding: its out
+ *             row is left as it is.  Rows that name the same slot are
+ *             consecutive tokens of that sequence, in the order of the rows.
+ * B 0..65535 (0 launches nothing); C as above.
+ * ---------------------------------------------------------------------- */
+int attnres_gated_recurrence_step(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
+                                  int64_t gate_stride, int B, int C, int dtype, float* state, int num_slots,
+                                  const int32_t* slots, void* out, int64_t out_stride, void* stream);
+
+/* ------------------------------------------------------------------------
+ * attnres_grad_clip -- the norm of a list of gradients taken as one vector,
+ * and their clipping:
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   out = g * (max_norm / norm) where norm > max_norm, else g
+ * A norm that is not finite scales nothing: out = g, and out_norm says so.
+ * grads       host array of n device pointers, contiguous tensors
+ * outs        host array of n device pointers, or NULL (only the norm).
+ *             outs[i] may be grads[i] itself (in place: nothing is written
+ *             where nothing is clipped); it shares no other memory with a
+ *             tensor of the call
+ * numels      host array of n element counts (0: the pointers may be NULL)
+ * dtypes      host array of n attnres_dtype (outs[i] has that of grads[i])
+ * n 0..65535 (ATTNRES_ERANGE above)
+ * max_norm    >= 0 (infinity: nothing is clipped); not read without outs
+ * out_norm    device fp32 [1]
+ * workspace   device scratch, 256-byte aligned, of at least
+ *             attnres_grad_clip_workspace_size() bytes.  Calls that overlap in
+ *             time need one each.
+ * The host arrays are read during the call only.  The squares are summed in
+ * fp32 over chunks, those in fp64 (in fp64 throughout where fp32 does not
+ * hold the squares), in a fixed order (bit-reproducible).
+ * ---------------------------------------------------------------------- */
+int attnres_grad_clip(const void* const* grads, void* const* outs, const int64_t* numels, const int* dtypes, int n,
+                      float max_norm, float* out_norm, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace attnres_grad_clip needs on the current device. */
+int64_t attnres_grad_clip_workspace_size(void);
+
+/* ------------------------------------------------------------------------
  * attnres_debug_wait_test -- a diagnostic with no counterpart in the pages:
  * makes the bounded waits of the ring kernels launched afterwards from this
  * process run out on a healthy GPU, so that their timeout path can be tested

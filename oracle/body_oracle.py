@@ -127,3 +127,88 @@ def linear_attention_step(q, k, v, log_decay, state, slots, scale):
             state[s] = lam * state[s] + k[b][:, :, None] * v[b][:, None, :]
             out[b] = scale * (q[b][:, None, :] @ state[s])[:, 0]
     return out, state
+
+
+# -------------------------------------------------------------- layer norm --
+
+def layer_norm(x, gain, bias, eps):
+    """x [T, d]; gain, bias [d] or None."""
+    z = x - x.mean(-1, keepdims=True)
+    h = z / np.sqrt((z * z).mean(-1, keepdims=True) + eps)
+    return h * (1.0 if gain is None else gain) + (0.0 if bias is None else bias)
+
+
+def layer_norm_backward(x, gain, eps, dy):
+    """(dx, dgain, dbias)."""
+    z = x - x.mean(-1, keepdims=True)
+    sigma = np.sqrt((z * z).mean(-1, keepdims=True) + eps)
+    h = z / sigma
+    n = dy if gain is None else dy * gain
+    dx = (n - n.mean(-1, keepdims=True) - h * (n * h).mean(-1, keepdims=True)) / sigma
+    return dx, (dy * h).sum(0), dy.sum(0)
+
+
+# -------------------------------------------------------- gated recurrence --
+
+def sigmoid(z):
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
+
+
+def silu(g):
+    return 1.0 if g is None else g * sigmoid(g)
+
+
+def silu_slope(g):
+    return sigmoid(g) * (1.0 + g * sigmoid(-g))
+
+
+def gated_recurrence(x, f, g, cu, s0):
+    """(out, final states, states before every token); rows outside every sequence NaN."""
+    a, b = sigmoid(f), sigmoid(-f) * x
+    n, (T, C) = len(cu) - 1, x.shape
+    h, before = np.full((T, C), np.nan), np.full((T, C), np.nan)
+    fin = np.zeros((n, C)) if s0 is None else s0.copy()
+    for i in range(n):
+        for t in range(cu[i], cu[i + 1]):
+            before[t] = fin[i]
+            fin[i] = a[t] * fin[i] + b[t]
+            h[t] = fin[i]
+    return h * silu(g), fin, before
+
+
+def gated_recurrence_backward(x, f, g, cu, s0, dy, ds1):
+    """(dx, df, dg, d initial state); dg None without a gate."""
+    a, rest = sigmoid(f), sigmoid(-f)
+    n, C = len(cu) - 1, x.shape[1]
+    _, _, before = gated_recurrence(x, f, None, cu, s0)
+    dx, df = np.full(x.shape, np.nan), np.full(x.shape, np.nan)
+    ds0 = np.zeros((n, C)) if ds1 is None else ds1.copy()
+    do = dy * silu(g)
+    for i in range(n):
+        for t in range(cu[i + 1] - 1, cu[i] - 1, -1):
+            dh = do[t] + ds0[i]
+            dx[t] = rest[t] * dh
+            df[t] = dh * (before[t] - x[t]) * a[t] * rest[t]
+            ds0[i] = a[t] * dh
+    dg = None if g is None else dy * (a * before + rest * x) * silu_slope(g)
+    return dx, df, dg, ds0
+
+
+def gated_recurrence_step(x, f, g, state, slots):
+    """(out, states): rows in order; a row without a slot gives NaN."""
+    state, out = state.copy(), np.full(x.shape, np.nan)
+    for b, s in enumerate(slots):
+        if 0 <= s < len(state):
+            state[s] = sigmoid(f[b]) * state[s] + sigmoid(-f[b]) * x[b]
+            out[b] = state[s] * (1.0 if g is None else silu(g[b]))
+    return out, state
+
+
+# ------------------------------------------------------- gradient clipping --
+
+def grad_clip(grads, max_norm):
+    """(norm, clipped gradients)."""
+    norm = math.sqrt(sum(float((g * g).sum()) for g in grads))
+    factor = max_norm / norm if math.isfinite(norm) and norm > max_norm else 1.0
+    return norm, [g * factor for g in grads]
