@@ -890,7 +890,7 @@ def _recurrence_args(x, forget, gate, cu_seqlens, cur: int):
 def attnres_gated_recurrence(x: torch.Tensor, forget: torch.Tensor, out: torch.Tensor, gate: torch.Tensor | None = None,
                              cu_seqlens: torch.Tensor | None = None, initial_state: torch.Tensor | None = None,
                              final_state: torch.Tensor | None = None, chunk_states: torch.Tensor | None = None,
-                             stream=None) -> None:
+                             dev_err: torch.Tensor | None = None, stream=None) -> None:
     """Gated linear recurrence over prompts, h_t = a_t h_{t-1} + (1 - a_t) x_t
     with a = sigmoid(forget), out = h silu(gate) (h where gate is None).
 
@@ -907,7 +907,7 @@ def attnres_gated_recurrence(x: torch.Tensor, forget: torch.Tensor, out: torch.T
         *head, cu, N, _vec(initial_state, "initial_state", (N, C), torch.float32, cur),
         _vec(final_state, "final_state", (N, C), torch.float32, cur), op, os_,
         _vec(chunk_states, "chunk_states", (-(-T // ATTNRES_RECURRENCE_CHUNK), C), torch.float32, cur),
-        _stream_on(stream, cur))
+        _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_gated_recurrence")
 
 
@@ -917,7 +917,8 @@ def attnres_gated_recurrence_backward(x: torch.Tensor, forget: torch.Tensor, chu
                                       gate: torch.Tensor | None = None, cu_seqlens: torch.Tensor | None = None,
                                       initial_state: torch.Tensor | None = None,
                                       grad_final_state: torch.Tensor | None = None,
-                                      grad_initial_state: torch.Tensor | None = None, stream=None) -> None:
+                                      grad_initial_state: torch.Tensor | None = None,
+                                      dev_err: torch.Tensor | None = None, stream=None) -> None:
     """Gradients of attnres_gated_recurrence from the forward's inputs and the
     chunk_states it wrote (grad_x, grad_forget, grad_gate [T, C] of x's dtype,
     rows contiguous at any stride; the states' float32).  Those that are None
@@ -932,7 +933,8 @@ def attnres_gated_recurrence_backward(x: torch.Tensor, forget: torch.Tensor, chu
         *head, cu, N, _vec(initial_state, "initial_state", (N, C), torch.float32, cur),
         _vec(chunk_states, "chunk_states", (-(-T // ATTNRES_RECURRENCE_CHUNK), C), torch.float32, cur), dp, ds,
         _vec(grad_final_state, "grad_final_state", (N, C), torch.float32, cur), gx, gxs, gf, gfs, gg, ggs,
-        _vec(grad_initial_state, "grad_initial_state", (N, C), torch.float32, cur), _stream_on(stream, cur))
+        _vec(grad_initial_state, "grad_initial_state", (N, C), torch.float32, cur),
+        _dev_ptr(dev_err, "dev_err", torch.int32), _stream_on(stream, cur))
     _N.check(rc, "attnres_gated_recurrence_backward")
 
 

@@ -160,9 +160,9 @@ def _load() -> ctypes.CDLL:
         "attnres_layer_norm": (i32, [vp, i64, i64, i32, i32, vp, vp, f32, vp, i64, vp]),
         "attnres_layer_norm_backward": (i32, [vp, i64, i64, i32, i32, vp, f32, vp, i64, vp, i64, vp, vp, vp, i64, vp]),
         "attnres_layer_norm_backward_workspace_size": (i64, [i64, i32]),
-        "attnres_gated_recurrence": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp]),
+        "attnres_gated_recurrence": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp, vp, vp]),
         "attnres_gated_recurrence_backward": (i32, [vp, i64, vp, i64, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i64, vp,
-                                                    vp, i64, vp, i64, vp, i64, vp, vp]),
+                                                    vp, i64, vp, i64, vp, i64, vp, vp, vp]),
         "attnres_gated_recurrence_step": (i32, [vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i32, vp, vp, i64, vp]),
         "attnres_grad_clip": (i32, [ctypes.POINTER(vp), ctypes.POINTER(vp), ctypes.POINTER(i64), ctypes.POINTER(i32), i32,
                                     f32, vp, vp, i64, vp]),

@@ -210,5 +210,5 @@ class GatedRecurrenceBody(_Body):
                                           stream=stream)
         else:
             attnres_gated_recurrence(self.x, self.forget, self.o, gate=self.gate, cu_seqlens=self.cu_seqlens,
-                                     initial_state=state, final_state=state, stream=stream)
+                                     initial_state=state, final_state=state, dev_err=self.dev_err, stream=stream)
         attnres_linear(self.o, w.w_out, F, bias=w.b_out, workspace=self.workspace, dev_err=self.dev_err, stream=stream)

@@ -185,6 +185,7 @@ struct RecurrenceArgs {
   void *dx, *df, *dg;  // each may be null
   int64_t dxs, dfs, dgs;
   float* ds0;
+  int* dev_err;
   cudaStream_t stream;
 };
 cudaError_t launch_gated_recurrence(const RecurrenceArgs& a);

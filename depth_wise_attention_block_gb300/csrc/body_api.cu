@@ -130,12 +130,14 @@ int check_ln(const void* x, int64_t xs, int64_t T, int d, int dtype, float eps) 
   if (!stride_ok(xs, d)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
   if (!span_ok(T, xs)) return fail(ATTNRES_ERANGE, "T*stride too large");
   if (T > 0 && !x) return fail(ATTNRES_EINVAL, "x is NULL");
+  if (!aligned(x, (int)dtype_bytes(dtype))) return fail(ATTNRES_EINVAL, "a tensor is not aligned to its elements");
   return ATTNRES_OK;
 }
 
-// a row tensor [T, C] that a recurrence reads or writes (null: absent)
-int check_gr_rows(const void* p, int64_t stride, int64_t T, int C) {
+// a row tensor [T, C] that an operator reads or writes (null: absent)
+int check_gr_rows(const void* p, int64_t stride, int64_t T, int C, int dtype) {
   if (!p) return ATTNRES_OK;
+  if (!aligned(p, (int)dtype_bytes(dtype))) return fail(ATTNRES_EINVAL, "a tensor is not aligned to its elements");
   if (!stride_ok(stride, C)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
   if (!span_ok(T, stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
   return ATTNRES_OK;
@@ -149,9 +151,9 @@ int check_gr(const void* x, int64_t xs, const void* f, int64_t fs, const void* g
     return fail(ATTNRES_ERANGE, "T=%lld C=%d num_seqs=%d", (long long)T, C, N);
   if (!cu && N != 1) return fail(ATTNRES_EINVAL, "num_seqs=%d without cu_seqlens", N);
   if (T > 0 && (!x || !f)) return fail(ATTNRES_EINVAL, "x/forget is NULL");
-  int rc = check_gr_rows(x, xs, T, C);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(f, fs, T, C);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(g, gs, T, C);
+  int rc = check_gr_rows(x, xs, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(f, fs, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(g, gs, T, C, dtype);
   return rc;
 }
 
@@ -637,6 +639,7 @@ int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dt
   if (T == 0) return ok();
   if (!out) return fail(ATTNRES_EINVAL, "out is NULL");
   const int64_t es = dtype_bytes(dtype), w = d * es;
+  if (!aligned(out, (int)es)) return fail(ATTNRES_EINVAL, "a tensor is not aligned to its elements");
   {
     const Rows in[3] = {{x, T, w, x_stride * es}, {gain, 1, d * 4LL, d * 4LL}, {bias, 1, d * 4LL, d * 4LL}};
     const Rows outs[1] = {{out, T, w, out_stride * es}};
@@ -681,6 +684,7 @@ int attnres_layer_norm_backward(const void* x, int64_t x_stride, int64_t T, int 
   if (!span_ok(T, grad_out_stride) || !span_ok(T, grad_x_stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
   if (!grad_x && !grad_gain && !grad_bias) return ok();
   if (T > 0 && !grad_out) return fail(ATTNRES_EINVAL, "grad_out is NULL");
+  if (!aligned(grad_out, (int)es) || !aligned(grad_x, (int)es)) return fail(ATTNRES_EINVAL, "a tensor is not aligned to its elements");
   {
     const int64_t wsb = workspace && workspace_bytes > 0 ? workspace_bytes : 0;
     const Rows in[3] = {{grad_out, T, w, grad_out_stride * es}, {x, T, w, x_stride * es}, {gain, 1, vec, vec}};
@@ -721,11 +725,11 @@ int attnres_layer_norm_backward(const void* x, int64_t x_stride, int64_t T, int 
 int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
                              int64_t gate_stride, int64_t T, int C, int dtype, const int32_t* cu_seqlens, int num_seqs,
                              const float* initial_state, float* final_state, void* out, int64_t out_stride,
-                             float* chunk_states, void* stream) {
+                             float* chunk_states, int* dev_err, void* stream) {
   int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, T, C, dtype, cu_seqlens, num_seqs);
   if (rc != ATTNRES_OK) return rc;
   if (T > 0 && !out) return fail(ATTNRES_EINVAL, "out is NULL");
-  rc = check_gr_rows(out, out_stride, T, C);
+  rc = check_gr_rows(out, out_stride, T, C, dtype);
   if (rc != ATTNRES_OK) return rc;
   if (T == 0 && !final_state) return ok();
   {
@@ -755,6 +759,7 @@ int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget
   a.out = out;
   a.os = out_stride;
   a.chunk = T > 0 ? chunk_states : nullptr;
+  a.dev_err = dev_err;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_gated_recurrence(a);
   if (e != cudaSuccess) return cuda_fail(e, "attnres_gated_recurrence launch");
@@ -767,17 +772,17 @@ int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const voi
                                       const float* chunk_states, const void* grad_out, int64_t grad_out_stride,
                                       const float* grad_final_state, void* grad_x, int64_t grad_x_stride, void* grad_forget,
                                       int64_t grad_forget_stride, void* grad_gate, int64_t grad_gate_stride,
-                                      float* grad_initial_state, void* stream) {
+                                      float* grad_initial_state, int* dev_err, void* stream) {
   int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, T, C, dtype, cu_seqlens, num_seqs);
   if (rc != ATTNRES_OK) return rc;
   if (grad_gate && !gate) return fail(ATTNRES_EINVAL, "grad_gate without gate");
   if (!grad_x && !grad_forget && !grad_gate && !grad_initial_state) return ok();
   if (T == 0 && !grad_initial_state) return ok();
   if (T > 0 && (!grad_out || !chunk_states)) return fail(ATTNRES_EINVAL, "grad_out/chunk_states is NULL");
-  rc = check_gr_rows(grad_out, grad_out_stride, T, C);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_x, grad_x_stride, T, C);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_forget, grad_forget_stride, T, C);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_gate, grad_gate_stride, T, C);
+  rc = check_gr_rows(grad_out, grad_out_stride, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_x, grad_x_stride, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_forget, grad_forget_stride, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(grad_gate, grad_gate_stride, T, C, dtype);
   if (rc != ATTNRES_OK) return rc;
   {
     const int64_t es = dtype_bytes(dtype), w = C * es, st = (int64_t)num_seqs * C * 4, cub = (num_seqs + 1) * 4LL;
@@ -815,6 +820,7 @@ int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const voi
   a.dg = grad_gate;
   a.dgs = grad_gate_stride;
   a.ds0 = grad_initial_state;
+  a.dev_err = dev_err;
   a.stream = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_gated_recurrence_backward(a);
   if (e != cudaSuccess) return cuda_fail(e, "attnres_gated_recurrence_backward launch");
@@ -827,7 +833,7 @@ int attnres_gated_recurrence_step(const void* x, int64_t x_stride, const void* f
   if (B < 0 || num_slots < 0) return fail(ATTNRES_EINVAL, "B=%d num_slots=%d", B, num_slots);
   if (B > 65535) return fail(ATTNRES_ERANGE, "B=%d", B);
   int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, B, C, dtype, nullptr, 1);
-  if (rc == ATTNRES_OK) rc = check_gr_rows(out, out_stride, B, C);
+  if (rc == ATTNRES_OK) rc = check_gr_rows(out, out_stride, B, C, dtype);
   if (rc != ATTNRES_OK) return rc;
   if (!slots && B > num_slots) return fail(ATTNRES_EINVAL, "B=%d rows for %d slots", B, num_slots);
   if (B == 0 || num_slots == 0) return ok();

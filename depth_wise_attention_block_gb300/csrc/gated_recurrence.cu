@@ -23,6 +23,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "attnres.h"
 #include "body.h"
 #include "device_common.cuh"
@@ -37,22 +39,20 @@ constexpr int kGrChunk = ATTNRES_RECURRENCE_CHUNK;  // rows of a tile
 constexpr int kGrWarps = 8;
 constexpr int kGrRows = kGrChunk / kGrWarps;        // of a warp
 constexpr int kGrThreads = 32 * kGrWarps;
-constexpr int kGrRowBytes = 128;                    // of a slab
-#ifndef GR_FS
-#define GR_FS 2
-#define GR_FB 3
-#define GR_BS 2
-#define GR_BB 2
-#define GR_MAXR 8
-#endif
-constexpr int kGrStages = GR_FS, kGrBwdStages = GR_BS;          // tiles of a warp's ring
-constexpr int kGrBlocksPerSm = GR_FB, kGrBwdBlocksPerSm = GR_BB;  // resident CTAs
-constexpr int kGrMaxCluster = GR_MAXR;
+constexpr int kGrMaxCluster = 8;
+constexpr int kGrBlocksPerSm = 2;                   // resident CTAs
 constexpr int kGsThreads = 256;
+
+// ---------------------------------------------------------- arithmetic ---
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -65,29 +65,161 @@ __device__ __forceinline__ float rcp(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(d) : "f"(x));
   return d;
 }
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2_both(-1.f), a); }
 constexpr float kLog2e = 1.44269504f;
 
-// a = 1 / (1 + e^-f) and rest = 1 - a, neither by a difference.  f below -83
-// counts as -83 (a = 1e-36), where e^-f would leave fp32; NaN stays NaN.  For
-// bf16 tensors the fast exponential and reciprocal (2^-22 each, far below the
-// results' 2^-8), for fp32 ones the full functions.
+// 1 / (1 + e^-z) on both halves, and e^-z.  For bf16 tensors with the fast
+// exponential and reciprocal (2^-22 each, far below the results' 2^-8), for
+// fp32 ones with the full functions.
 template <typename T>
-__device__ __forceinline__ void forget(float f, float* a, float* rest) {
+__device__ __forceinline__ uint64_t f2_sigmoid(uint64_t z, uint64_t* e) {
+  float a, b;
   if constexpr (sizeof(T) == 2) {
-    const float e = ex2(min_nan(-kLog2e * f, 120.f));
-    *a = rcp(1.f + e);
-    *rest = e * *a;
+    f2_unpack(f2_mul(z, f2_both(-kLog2e)), a, b);
+    *e = f2_pack(ex2(a), ex2(b));
+    f2_unpack(f2_add(*e, f2_both(1.f)), a, b);
+    return f2_pack(rcp(a), rcp(b));
   } else {
-    const float e = expf(min_nan(-f, 83.f));
-    *a = 1.f / (1.f + e);
-    *rest = e * *a;
+    f2_unpack(z, a, b);
+    a = expf(-a);
+    b = expf(-b);
+    *e = f2_pack(a, b);
+    return f2_pack(1.f / (1.f + a), 1.f / (1.f + b));
+  }
+}
+
+// One value of it, and the rest to one (not by a difference).  f below -83
+// counts as -83 (a = 1e-36), where e^-f would leave fp32; NaN stays NaN.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float z, float* e) {
+  if constexpr (sizeof(T) == 2) {
+    *e = ex2(-kLog2e * z);
+    return rcp(1.f + *e);
+  } else {
+    *e = expf(-z);
+    return 1.f / (1.f + *e);
   }
 }
 template <typename T>
-__device__ __forceinline__ float sigmoid(float z) {
-  if constexpr (sizeof(T) == 2) return rcp(1.f + ex2(-kLog2e * z));
-  else return 1.f / (1.f + expf(-z));
+__device__ __forceinline__ void forget(float f, float* a, float* rest) {
+  float e;
+  *a = sigmoid<T>(-min_nan(-f, 83.f), &e);
+  *rest = e * *a;
 }
+
+// -------------------------------------------------- the channels of a lane --
+
+// N channels of one row: a lane's 4 or 8 bytes in memory, N / 2 packed pairs
+// of fp32 in registers.
+template <typename T, int N>
+struct Lane {
+  static constexpr int P = N / 2;
+  static constexpr int kBytes = N * (int)sizeof(T);
+  static constexpr int kWords = kBytes / 4;
+  struct Raw {
+    uint32_t w[kWords];
+  };
+  static __device__ __forceinline__ Raw load(uint32_t addr) {
+    Raw r;
+    if constexpr (kWords == 2) asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[1]) : "r"(addr));
+    else asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.w[0]) : "r"(addr));
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const Raw& r, uint64_t (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if constexpr (sizeof(T) == 2) v[i] = f2_pack(bf16lo(r.w[i]), bf16hi(r.w[i]));
+      else v[i] = f2_pack(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+    }
+  }
+  static __device__ __forceinline__ void load(uint32_t addr, uint64_t (&v)[P]) { unpack(load(addr), v); }
+  // the forget gate's a and 1 - a (below -83 as -83)
+  static __device__ __forceinline__ void forgets(uint32_t addr, uint64_t (&a)[P], uint64_t (&rest)[P]) {
+    Raw r = load(addr);
+    uint64_t f[P];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 2) r.w[i] = max_nan_bf16x2(r.w[i], 0xC2A6C2A6u);  // -83
+      else r.w[i] = __float_as_uint(-min_nan(-__uint_as_float(r.w[i]), 83.f));
+    }
+    unpack(r, f);
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      uint64_t e;
+      a[i] = f2_sigmoid<T>(f[i], &e);
+      rest[i] = f2_mul(e, a[i]);
+    }
+  }
+  // whole: all N channels are there, and the row lies on the lane's boundaries
+  static __device__ __forceinline__ void store(T* at, int in, bool whole, const uint64_t (&v)[P]) {
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < P; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
+    if (whole) {
+      uint32_t w[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        if constexpr (sizeof(T) == 2) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+        else w[i] = __float_as_uint(f[i]);
+      }
+      if constexpr (kWords == 2) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(at) = w[0];
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (e < in) store_elem(at + e, f[e]);
+    }
+  }
+  // fp32 states in device memory, and in shared memory (16-byte or 8-byte vectors)
+  static __device__ __forceinline__ void load_state(const float* at, int in, uint64_t (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = f2_pack(2 * i < in ? at[2 * i] : 0.f, 2 * i + 1 < in ? at[2 * i + 1] : 0.f);
+  }
+  static __device__ __forceinline__ void store_state(float* at, int in, const uint64_t (&v)[P]) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      float a, b;
+      f2_unpack(v[i], a, b);
+      if (2 * i < in) at[2 * i] = a;
+      if (2 * i + 1 < in) at[2 * i + 1] = b;
+    }
+  }
+  static __device__ __forceinline__ void get(const uint64_t (&at)[P], uint64_t (&v)[P]) {
+    if constexpr (P == 2) {
+      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&at[0]);
+      v[0] = u.x;
+      v[1] = u.y;
+    } else {
+      v[0] = at[0];
+    }
+  }
+  static __device__ __forceinline__ void put(uint64_t (&at)[P], const uint64_t (&v)[P]) {
+    if constexpr (P == 2) *reinterpret_cast<ulonglong2*>(&at[0]) = make_ulonglong2(v[0], v[1]);
+    else at[0] = v[0];
+  }
+  // into a CTA of the cluster, counted by its mbarrier
+  static __device__ __forceinline__ void put_cluster(uint32_t addr, const uint64_t (&v)[P], uint32_t bar) {
+    if constexpr (P == 2)
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(addr), "l"(v[0]), "l"(v[1]),
+                   "r"(bar)
+                   : "memory");
+    else
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr), "l"(v[0]), "r"(bar) : "memory");
+  }
+};
+
+// ------------------------------------------------------------ rows ahead --
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of 16: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -100,25 +232,11 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
-}
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, const float (&v)[4]) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, const float (&v)[2]) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v[0]), "f"(v[1]) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
 
-// How the rows of a tensor lie: 16-byte vectors, 32-bit words, or elements.
+// How the rows of a tensor lie: on 16-byte vectors, on 32-bit words, or neither.
 enum RowAccess { kVectors = 0, kWords = 1, kElements = 2 };
 
 struct GrParams {
@@ -126,99 +244,83 @@ struct GrParams {
   int ranks;       // CTAs of a cluster
   int groups;      // tiles of a CTA: ceil(tiles / ranks)
   int access[4];   // of x, f, g and (backward) dout
-  int words_out;   // every row tensor written lies on 32-bit words
+  int whole;       // every row tensor written lies on a lane's boundaries
+  unsigned long long wait_ns;  // limit of a wait
+  int withhold;    // the bounded-wait test: the first tile's spans are not sent
 };
 
-// The channels of a lane: one 32-bit word of a row.
-template <typename T>
-struct Word {
-  static constexpr int N = 4 / sizeof(T);
-  static __device__ __forceinline__ void unpack(uint32_t w, float (&v)[N]) {
-    if constexpr (N == 2) {
-      v[0] = bf16lo(w);
-      v[1] = bf16hi(w);
-    } else {
-      v[0] = __uint_as_float(w);
-    }
-  }
-  static __device__ __forceinline__ uint32_t pack(const float (&v)[N]) {
-    if constexpr (N == 2) return pack_bf16x2(v[0], v[1]);
-    else return __float_as_uint(v[0]);
-  }
-  // row: the row's slab; in: how many of the lane's channels there are
-  static __device__ __forceinline__ void store(T* row, int lane, int in, bool words, const float (&v)[N]) {
-    if (in == N && words) {
-      *reinterpret_cast<uint32_t*>(row + lane * N) = pack(v);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (e < in) store_elem(row + lane * N + e, v[e]);
-    }
-  }
-};
-
-// One warp's copy of its 8 rows from t0 on into shared memory, rows of 128
-// bytes; zeros where there is no row or channel.
-template <typename T>
-__device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long long stride, long long t0, long long T_, int c0, int C,
-                                           int access, int lane) {
-  constexpr int N = Word<T>::N;
+// One warp's copy of its 8 rows from t0 on (channels c0 and up, N to a lane)
+// into shared memory; zeros where there is no row or channel.
+template <typename T, int N>
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long long stride, int t0, int T_, int c0, int C, int access,
+                                           int lane) {
+  constexpr int kRow = 32 * Lane<T, N>::kBytes;
   const T* base = static_cast<const T*>(src);
   if (access == kVectors) {
-    constexpr int V = 16 / sizeof(T);
-    const int v = lane & 7, left = C - c0 - v * V;
+    constexpr int V = 16 / sizeof(T), kVecs = kRow / 16, kStep = 32 / kVecs;  // vectors of a row, rows at a time
+    const int v = lane % kVecs, r0 = lane / kVecs, left = C - c0 - v * V;
     const int bytes = left >= V ? 16 : left > 0 ? left * (int)sizeof(T) : 0;
+    const T* at = base + (t0 + r0) * stride + c0 + v * V;
+    dst += r0 * kRow + v * 16;
+    if (t0 + kGrRows <= T_ && bytes == 16) {
 #pragma unroll
-    for (int i = 0; i < kGrRows / 4; ++i) {
-      const int r = (lane >> 3) + 4 * i;
-      const int n = t0 + r < T_ ? bytes : 0;
-      cp_async16(dst + r * kGrRowBytes + v * 16, n > 0 ? base + (t0 + r) * stride + c0 + v * V : base, n);
+      for (int i = 0; i < kGrRows / kStep; ++i) cp_async16(dst + i * kStep * kRow, at + i * kStep * stride, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGrRows / kStep; ++i) {
+        const int n = t0 + r0 + i * kStep < T_ ? bytes : 0;
+        cp_async16(dst + i * kStep * kRow, n > 0 ? at + i * kStep * stride : base, n);
+      }
     }
   } else {
-    const int in = C - c0 - lane * N;
-#pragma unroll
+    constexpr int E = 4 / sizeof(T);  // elements of a word
     for (int r = 0; r < kGrRows; ++r) {
-      const bool row = t0 + r < T_ && in > 0;
-      const T* at = base + (row ? (t0 + r) * stride + c0 + lane * N : 0);
-      const uint32_t to = dst + r * kGrRowBytes + lane * 4;
-      if (access == kWords) {
-        cp_async4(to, row ? at : base, !row ? 0 : in >= N ? 4 : (int)sizeof(T));
-      } else {  // (bf16 off the 32-bit words)
-        uint32_t w = 0;
-        if (row) w = *reinterpret_cast<const uint16_t*>(at);
-        if (row && in >= N) w |= (uint32_t) * reinterpret_cast<const uint16_t*>(at + N - 1) << 16;
-        st_shared_u32(to, w);
+      const T* row = base + (t0 + r < T_ ? (t0 + r) * stride + c0 : 0);
+#pragma unroll
+      for (int i = 0; i < Lane<T, N>::kWords; ++i) {  // (neighbouring lanes, neighbouring words)
+        const int c = (i * 32 + lane) * E, in = t0 + r < T_ ? C - c0 - c : 0;
+        const uint32_t to = dst + r * kRow + (i * 32 + lane) * 4;
+        if (access == kWords) {
+          cp_async4(to, in > 0 ? row + c : base, in >= E ? 4 : in > 0 ? (int)sizeof(T) : 0);
+        } else {  // bf16 off the words
+          uint32_t w = 0;
+          if (in > 0) w = reinterpret_cast<const uint16_t*>(row)[c];
+          if (in > 1) w |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[c + 1] << 16;
+          st_shared_u32(to, w);
+        }
       }
     }
   }
 }
 
+// ------------------------------------------------------------- sequences --
+
 __device__ __forceinline__ int clamp_row(int r, int T_) { return r < 0 ? 0 : r > T_ ? T_ : r; }
 
-// Which of a warp's 8 rows begin and end a sequence, and of which sequence.
-// The offsets are looked through in one direction as the tiles go by: `j` is
-// the first offset not below the rows (forward) or the first one above all
-// earlier-visited rows' lower end (backward starts a new search).
-struct Marks {
-  uint32_t starts, ends;
-};
-// smallest index in [lo, N + 1] whose offset is not below t (N + 1: none), given that offset lo - 1 is below
+// The smallest index in [lo, N + 1] whose offset is not below t (N + 1: none),
+// given that those before lo are below.
 __device__ __forceinline__ int lower_bound(const int* cu, int N, int T_, int t, int lo, int lane) {
   int hi = N + 1;
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32, at = lo + lane * step;
     const bool below = at < hi && clamp_row(__ldg(cu + at), T_) < t;
-    const int k = __popc(__ballot_sync(0xffffffffu, below));  // probes below: the first of them, in order
+    const int k = __popc(__ballot_sync(0xffffffffu, below));  // the first k probes
     if (k == 0) return lo;
-    const int from = lo + (k - 1) * step + 1, to = lo + k * step;
-    lo = from;
+    const int to = lo + k * step;
+    lo += (k - 1) * step + 1;
     hi = to < hi ? to : hi;
   }
   const bool below = lo + lane < hi && clamp_row(__ldg(cu + lo + lane), T_) < t;
   return lo + __popc(__ballot_sync(0xffffffffu, below));
 }
 
-__device__ __forceinline__ Marks find_marks(const int* cu, int N, int T_, int t0, int j, int* seqs, int lane) {
+// Which of a warp's 8 rows begin and end a sequence: bit k for row t0 + k,
+// the sequences in seqs[k] and seqs[8 + k].
+struct Marks {
+  uint32_t starts, ends;
+};
+// j: the first offset not below t0
+__device__ __noinline__ Marks find_marks(const int* cu, int N, int T_, int t0, int j, int* seqs, int lane) {
   Marks m{0, 0};
   for (int base = j; base <= N; base += 32) {
     const int i = base + lane;
@@ -240,32 +342,39 @@ __device__ __forceinline__ Marks find_marks(const int* cu, int N, int T_, int t0
   return m;
 }
 
-// The marks of one warp's rows, tile after tile in either direction.
+// The marks of a warp's rows, tile after tile in either direction: the offsets
+// are searched only when the rows reach the next one.
+template <bool REV>
 struct Boundaries {
-  int j, next;  // forward: the first offset not below the last rows looked at, and its value
-  __device__ __forceinline__ Marks rows(const RecurrenceArgs& a, int t0, int* seqs, int lane, bool descending) {
+  int j, next;  // the first offset not below the rows last looked at, and its value (REV: that of the one before)
+  __device__ __forceinline__ void begin(int first) {
+    j = 0;
+    next = REV ? INT_MAX : first;
+  }
+  __device__ __forceinline__ Marks rows(const RecurrenceArgs& a, int t0, int* seqs, int lane) {
     const int T_ = (int)a.T;
     if (!a.cu) {
-      Marks m{t0 == 0 ? 1u : 0u, t0 < T_ && T_ <= t0 + kGrRows ? 1u << (T_ - 1 - t0) : 0u};
-      if (lane < 2 * kGrRows) seqs[lane] = 0;
-      __syncwarp();
+      const Marks m{t0 == 0 ? 1u : 0u, t0 < T_ && T_ <= t0 + kGrRows ? 1u << (T_ - 1 - t0) : 0u};
+      if (m.starts | m.ends) {
+        if (lane < 2 * kGrRows) seqs[lane] = 0;
+        __syncwarp();
+      }
       return m;
     }
-    if (descending) {
-      // `next`: the largest offset not above the last rows looked at
-      if (next < t0) return {0, 0};
+    if (REV ? next < t0 : next > t0 + kGrRows) return {0, 0};
+    if (REV) {
       j = lower_bound(a.cu, a.N, T_, t0, 0, lane);
       next = j > 0 ? clamp_row(__ldg(a.cu + j - 1), T_) : -1;
     } else if (next < t0) {
       j = lower_bound(a.cu, a.N, T_, t0, j + 1, lane);
       next = j <= a.N ? clamp_row(__ldg(a.cu + j), T_) : INT_MAX;
+      if (next > t0 + kGrRows) return {0, 0};
     }
-    if (!descending && next > t0 + kGrRows) return {0, 0};
     return find_marks(a.cu, a.N, T_, t0, j, seqs, lane);
   }
 };
 
-// the state of every empty sequence goes on unchanged (from: its states or null)
+// the states of empty sequences go on unchanged (from: or null, zeros)
 __device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, const float* from, float* to, int rank, int ranks, int c, int in, int warp,
                                            int lane) {
   if (!to) return;
@@ -280,370 +389,462 @@ __device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, const float*
   }
 }
 
-// (A, B) of a span followed by (A2, B2); a cut span forgets what is behind it
-__device__ __forceinline__ float carry_on(float c, float A, float B, bool cut) { return cut ? B : fmaf(A, c, B); }
+// ---------------------------------------------- spans: h -> A h + B ------
 
-template <typename T>
-struct GrShared {
-  static constexpr int N = Word<T>::N;
-  float warps[2][kGrWarps][32][2 * N];          // (A, B) per channel of the tile's warps; two tiles in turn
-  int warp_cut[2][kGrWarps], rank_cut[2][kGrMaxCluster];
+// What a tile's warps leave for one another, two tiles in turn.  A span that a
+// sequence begins in (REV: ends in) is cut: it forgets the state behind it
+// (by choice and not by A = 0: infinities do not pass).
+template <int P>
+struct alignas(16) GrShared {
+  uint64_t A[2][kGrWarps][32][P], B[2][kGrWarps][32][P];
+  uint64_t state[2][32][P];  // of a CTA alone: ahead of its tile
+  uint64_t arrived[2];  // mbarriers: the spans of a cluster's tiles are here
+  unsigned char cut[2][kGrWarps];
   int seqs[kGrWarps][2 * kGrRows];
 };
+// of a cluster's tiles; A = -1: cut
+template <int P>
+struct RankSpan {
+  uint64_t A[32][P], B[32][P];
+};
 
-// After a tile's warps have left their (A, B) in sh: the state ahead of this
-// CTA's tile, for the lane's channels (state: the one ahead of the cluster's
-// tiles, and then the one behind them).  of_ranks: [2][ranks], the (A, B) of the
-// cluster's tiles, two sets in turn.  REV: spans follow one another from the
-// last row to the first.
-template <typename T, bool REV>
-__device__ __forceinline__ void exchange(GrShared<T>& sh, float (*of_ranks)[32][2 * Word<T>::N], int par, int rank, int ranks, int warp, int lane, float (&state)[Word<T>::N],
-                                         float (&ahead)[Word<T>::N]) {
-  constexpr int N = Word<T>::N;
-  auto nth = [](int i, int n) { return REV ? n - 1 - i : i; };
+template <int P>
+__device__ __forceinline__ void carry_on(uint64_t (&c)[P], const uint64_t (&A)[P], const uint64_t (&B)[P], bool cut) {
+#pragma unroll
+  for (int i = 0; i < P; ++i) c[i] = cut ? B[i] : f2_fma(A[i], c[i], B[i]);
+}
+
+// c through the spans of the warps before this one (REV: behind it)
+template <typename L, bool REV, typename S>
+__device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][L::P], const uint64_t (&B)[kGrWarps][32][L::P], S cuts,
+                                              int warp, int lane, uint64_t (&c)[L::P]) {
+  const int n = REV ? kGrWarps - 1 - warp : warp;
+#pragma unroll
+  for (int i = 0; i < kGrWarps - 1; ++i) {
+    if (i < n) {
+      const int w = REV ? kGrWarps - 1 - i : i;
+      uint64_t a[L::P], b[L::P];
+      L::get(A[w][lane], a);
+      L::get(B[w][lane], b);
+      carry_on(c, a, b, cuts >> (8 * w) & 1);
+    }
+  }
+}
+
+// After a barrier behind the warps' spans: the state at this warp's first row
+// (REV: the gradient behind its last), h, and the one at the CTA's tile, ahead.
+// A, B: the warp's own span.  state: what a cluster's CTAs carry along.  ok:
+// becomes false where the cluster's spans did not arrive in time (and then
+// nothing is waited for any more).
+template <typename L, bool REV>
+__device__ __forceinline__ void exchange(GrShared<L::P>& sh, RankSpan<L::P>* spans, int par, uint32_t phase, int rank, int ranks,
+                                         bool send, unsigned long long limit_ns, bool& ok, int warp, int lane,
+                                         const uint64_t (&A)[L::P], const uint64_t (&B)[L::P], uint64_t (&state)[L::P],
+                                         uint64_t (&ahead)[L::P], uint64_t (&h)[L::P]) {
+  constexpr int P = L::P;
+  const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut[par]);
+  const bool last = REV ? warp == 0 : warp == kGrWarps - 1;
   if (ranks == 1) {
+    L::get(sh.state[par][lane], ahead);
 #pragma unroll
-    for (int e = 0; e < N; ++e) ahead[e] = state[e];
+    for (int i = 0; i < P; ++i) h[i] = ahead[i];
+    through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
+    if (last) {
+      uint64_t c[P];
 #pragma unroll
-    for (int i = 0; i < kGrWarps; ++i) {
-      const int w = nth(i, kGrWarps);
-      const bool cut = sh.warp_cut[par][w];
-#pragma unroll
-      for (int e = 0; e < N; ++e) state[e] = carry_on(state[e], sh.warps[par][w][lane][2 * e], sh.warps[par][w][lane][2 * e + 1], cut);
+      for (int i = 0; i < P; ++i) c[i] = h[i];
+      carry_on(c, A, B, cuts >> (8 * warp) & 1);
+      L::put(sh.state[par ^ 1][lane], c);
     }
     return;
   }
-  if (warp == 0) {  // the tile's own (A, B), to every CTA of the cluster
-    float v[2 * N];
-    bool any = false;
+  if (last) {  // the tile's span, to every CTA of the cluster
+    uint64_t a[P], b[P], ta[P];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      v[2 * e] = 1.f;
-      v[2 * e + 1] = 0.f;
+    for (int i = 0; i < P; ++i) {
+      b[i] = 0;
+      a[i] = A[i];
     }
+    through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, b);
+    carry_on(b, A, B, cuts >> (8 * warp) & 1);
 #pragma unroll
-    for (int i = 0; i < kGrWarps; ++i) {
-      const int w = nth(i, kGrWarps);
-      const bool cut = sh.warp_cut[par][w];
-      any |= cut;
+    for (int w = 0; w < kGrWarps; ++w)
+      if (w != warp) {
+        L::get(sh.A[par][w][lane], ta);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float A = sh.warps[par][w][lane][2 * e], B = sh.warps[par][w][lane][2 * e + 1];
-        v[2 * e + 1] = carry_on(v[2 * e + 1], A, B, cut);
-        v[2 * e] *= A;
+        for (int i = 0; i < P; ++i) a[i] = f2_mul(a[i], ta[i]);
       }
+    if (cuts) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) a[i] = f2_both(-1.f);
     }
-    const uint32_t at = smem_addr(&of_ranks[par * ranks + rank][lane][0]), flag = smem_addr(&sh.rank_cut[par][rank]);
-    for (int r = 0; r < ranks; ++r) {
-      st_cluster(map_shared_rank(at, r), v);
-      if (lane == 0) st_cluster(map_shared_rank(flag, r), (int)any);
-    }
+    const uint32_t at = smem_addr(&spans[par * ranks + rank].A[lane][0]), bt = smem_addr(&spans[par * ranks + rank].B[lane][0]);
+    const uint32_t bar = smem_addr(&sh.arrived[par]);
+    // (after a wait that ran out, the barrier's phase is open without an arrival
+    // to come: a second one there is not allowed, and the spans that the others
+    // still send are few, because they stop in turn when these stay away)
+    if (ok && lane == 0) mbar_arrive_expect_tx(bar, ranks * (uint32_t)sizeof(RankSpan<P>));
+    if (ok && send)
+      for (int r = 0; r < ranks; ++r) {
+        const uint32_t to = map_shared_rank(bar, r);
+        L::put_cluster(map_shared_rank(at, r), a, to);
+        L::put_cluster(map_shared_rank(bt, r), b, to);
+      }
   }
-  cluster_sync_all();
+  // (a tile's spans come after those of the tile two before have been used:
+  // their CTA has seen this one's next tile, sent behind a barrier of its own)
+  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&sh.arrived[par]), phase, limit_ns));
   for (int i = 0; i < ranks; ++i) {
-    const int r = nth(i, ranks);
+    const int r = REV ? ranks - 1 - i : i;
     if (r == rank) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) ahead[e] = state[e];
+      for (int e = 0; e < P; ++e) ahead[e] = state[e];
     }
-    const bool cut = sh.rank_cut[par][r];
-#pragma unroll
-    for (int e = 0; e < N; ++e) state[e] = carry_on(state[e], of_ranks[par * ranks + r][lane][2 * e], of_ranks[par * ranks + r][lane][2 * e + 1], cut);
+    uint64_t a[P], b[P];
+    L::get(spans[par * ranks + r].A[lane], a);
+    L::get(spans[par * ranks + r].B[lane], b);
+    float cut, unused;
+    f2_unpack(a[0], cut, unused);
+    carry_on(state, a, b, cut == -1.f);
   }
+  if (!ok) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) ahead[e] = state[e] = f2_both(__int_as_float(0x7fc00000));
+  }
+#pragma unroll
+  for (int e = 0; e < P; ++e) h[e] = ahead[e];
+  through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
 }
 
-// the state at this warp's first row (REV: behind its last), from the one ahead of the tile
-template <typename T, bool REV>
-__device__ __forceinline__ void through_warps(const GrShared<T>& sh, int par, int warp, int lane, float (&c)[Word<T>::N]) {
-  constexpr int N = Word<T>::N;
-  const int n = REV ? kGrWarps - 1 - warp : warp;
-  for (int i = 0; i < n; ++i) {
-    const int w = REV ? kGrWarps - 1 - i : i;
-    const bool cut = sh.warp_cut[par][w];
-#pragma unroll
-    for (int e = 0; e < N; ++e) c[e] = carry_on(c[e], sh.warps[par][w][lane][2 * e], sh.warps[par][w][lane][2 * e + 1], cut);
-  }
-}
+// --------------------------------------------------------------- forward --
 
 template <typename T, bool GATE>
 __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(const __grid_constant__ GrParams p) {
-  constexpr int N = Word<T>::N, kArrays = GATE ? 3 : 2, kBytes = kArrays * kGrRows * kGrRowBytes;
-  extern __shared__ __align__(128) unsigned char ring_mem[];  // [warp][stage][array][row], then the exchange of a cluster
-  __shared__ __align__(16) GrShared<T> sh;
+  constexpr int N = 8 / sizeof(T);
+  using L = Lane<T, N>;
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGrRows * kRow, kArrays = GATE ? 3 : 2;
+  extern __shared__ __align__(128) unsigned char dyn[];  // [warp][array][row], then the spans of a cluster's tiles
+  __shared__ GrShared<P> sh;
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
-  const int c0 = blockIdx.x / ranks * (kGrRowBytes / (int)sizeof(T)), c = c0 + lane * N;
+  const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;  // channels of this lane
+  const bool whole = p.whole && in == N;
   const int T_ = (int)a.T;
-  const uint32_t ring = smem_addr(ring_mem) + warp * (kGrStages * kBytes);
-  auto of_ranks = reinterpret_cast<float (*)[32][2 * N]>(ring_mem + kGrWarps * kGrStages * kBytes);
-  if (ranks > 1) cluster_sync_all();  // every CTA of the cluster is there
+  const uint32_t ring = smem_addr(dyn) + warp * (kArrays * kArray);
+  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kArrays * kArray);
+  const uint64_t zero[P] = {};
+  if (warp == 0) L::put(sh.state[0][lane], zero);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(smem_addr(&sh.arrived[0]), 1);
+      mbar_init(smem_addr(&sh.arrived[1]), 1);
+      mbar_fence_init();
+    }
+    cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
+  }
+  bool ok = true;
   pdl_wait();
   pdl_trigger();
 
   auto row0 = [&](int i) { return (i * ranks + rank) * kGrChunk + warp * kGrRows; };
-  auto fetch = [&](int i) {
+  auto fetch_xf = [&](int i) {
     if (i < p.groups) {
-      const uint32_t to = ring + i % kGrStages * kBytes;
-      fetch_rows<T>(to, a.x, a.xs, row0(i), a.T, c0, a.C, p.access[0], lane);
-      fetch_rows<T>(to + kGrRows * kGrRowBytes, a.f, a.fs, row0(i), a.T, c0, a.C, p.access[1], lane);
-      if constexpr (GATE) fetch_rows<T>(to + 2 * kGrRows * kGrRowBytes, a.g, a.gs, row0(i), a.T, c0, a.C, p.access[2], lane);
+      fetch_rows<T, N>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
+      fetch_rows<T, N>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
     }
     cp_async_commit();  // a group for every tile, there or not
   };
-  for (int i = 0; i < kGrStages - 1; ++i) fetch(i);
+  auto fetch_g = [&](int i) {
+    if constexpr (GATE) {
+      if (i < p.groups) fetch_rows<T, N>(ring + 2 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
+      cp_async_commit();
+    }
+  };
+  fetch_xf(0);
+  fetch_g(0);
   pass_empty(a, a.s0, a.s1, rank, ranks, c, in, warp, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
-  Boundaries bounds{0, first};
-  float state[N];
+  Boundaries<false> bounds;
+  bounds.begin(first);
+  uint64_t state[P];
 #pragma unroll
-  for (int e = 0; e < N; ++e) state[e] = 0.f;
+  for (int e = 0; e < P; ++e) state[e] = 0;
 
   for (int i = 0; i < p.groups; ++i) {
     const int t0 = row0(i), par = i & 1;
-    __syncwarp();  // the slot that is filled next has been read
-    fetch(i + kGrStages - 1);
-    const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane, false);
-    cp_async_wait<kGrStages - 1>();
+    __syncwarp();  // the last rows' marks have been read
+    const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane);
+    cp_async_wait<GATE ? 1 : 0>();
     __syncwarp();
-    const uint32_t at = ring + i % kGrStages * kBytes + lane * 4;
+    const uint32_t at = ring + lane * L::kBytes;
 
     // the rows from a state of zero: h = hl + pa * (the state ahead), hl alone behind a first token
-    float hl[kGrRows][N], pa[kGrRows][N], A[N], B[N];
+    uint64_t hl[kGrRows][P], pa[kGrRows][P], A[P], B[P];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      A[e] = 1.f;
-      B[e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+      A[e] = f2_both(1.f);
+      B[e] = 0;
     }
 #pragma unroll
     for (int k = 0; k < kGrRows; ++k) {
-      float x[N], f[N], h0[N];
-      Word<T>::unpack(ld_shared_u32(at + k * kGrRowBytes), x);
-      Word<T>::unpack(ld_shared_u32(at + (kGrRows + k) * kGrRowBytes), f);
-      const bool start = m.starts >> k & 1;
-      if (start) {
-        const long long s = (long long)sh.seqs[warp][k] * a.C + c;
+      uint64_t x[P], g[P], rest[P];
+      L::load(at + k * kRow, x);
+      L::forgets(at + kArray + k * kRow, g, rest);
+      if (m.starts >> k & 1) {
+        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, B);
+        else
 #pragma unroll
-        for (int e = 0; e < N; ++e) h0[e] = a.s0 && e < in ? a.s0[s + e] : 0.f;
+          for (int e = 0; e < P; ++e) B[e] = 0;
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        float g, rest;
-        forget<T>(f[e], &g, &rest);
-        B[e] = fmaf(g, start ? h0[e] : B[e], rest * x[e]);
-        A[e] *= g;
+      for (int e = 0; e < P; ++e) {
+        B[e] = f2_fma(g[e], B[e], f2_mul(rest[e], x[e]));
+        A[e] = f2_mul(A[e], g[e]);
         hl[k][e] = B[e];
         pa[k][e] = A[e];
       }
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      sh.warps[par][warp][lane][2 * e] = A[e];
-      sh.warps[par][warp][lane][2 * e + 1] = B[e];
-    }
-    if (lane == 0) sh.warp_cut[par][warp] = m.starts != 0;
+    L::put(sh.A[par][warp][lane], A);
+    L::put(sh.B[par][warp][lane], B);
+    if (lane == 0) sh.cut[par][warp] = m.starts != 0;
+    __syncwarp();  // x and f have been read
+    fetch_xf(i + 1);
     __syncthreads();
-    float h[N];
-    exchange<T, false>(sh, of_ranks, par, rank, ranks, warp, lane, state, h);
-    if (warp == 0 && a.chunk && t0 < T_) {
+    uint64_t h[P], ahead[P];
+    exchange<L, false>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, B, state, ahead, h);
+    if (warp == 0 && a.chunk && t0 < T_) L::store_state(a.chunk + (long long)(t0 / kGrChunk) * a.C + c, in, ahead);
+    if (m.starts == 0) {
 #pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (e < in) a.chunk[(long long)(t0 / kGrChunk) * a.C + c + e] = h[e];
+      for (int k = 0; k < kGrRows; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) hl[k][e] = f2_fma(pa[k][e], h[e], hl[k][e]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kGrRows; ++k)
+        if (!(m.starts & ((2u << k) - 1)))
+#pragma unroll
+          for (int e = 0; e < P; ++e) hl[k][e] = f2_fma(pa[k][e], h[e], hl[k][e]);
     }
-    through_warps<T, false>(sh, par, warp, lane, h);
-
-    T* o = static_cast<T*>(a.out) + (long long)t0 * a.os + c0;
+    if (!ok) {
+#pragma unroll
+      for (int k = 0; k < kGrRows; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) hl[k][e] = f2_both(__int_as_float(0x7fc00000));
+    }
+    if (m.ends && a.s1) {
+#pragma unroll
+      for (int k = 0; k < kGrRows; ++k)
+        if (m.ends >> k & 1) L::store_state(a.s1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, hl[k]);
+    }
+    if constexpr (GATE) {
+      cp_async_wait<1>();
+      __syncwarp();
+    }
+    T* o = static_cast<T*>(a.out) + t0 * a.os + c;
 #pragma unroll
     for (int k = 0; k < kGrRows; ++k) {
-      float v[N], g[N];
-      const bool cut = m.starts & ((2u << k) - 1);
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = cut ? hl[k][e] : fmaf(pa[k][e], h[e], hl[k][e]);
-      if (a.s1 && (m.ends >> k & 1)) {
-        const long long s = (long long)sh.seqs[warp][kGrRows + k] * a.C + c;
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (e < in) a.s1[s + e] = v[e];
-      }
       if constexpr (GATE) {
-        Word<T>::unpack(ld_shared_u32(at + (2 * kGrRows + k) * kGrRowBytes), g);
+        uint64_t g[P], e;
+        L::load(at + 2 * kArray + k * kRow, g);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] *= g[e] * sigmoid<T>(g[e]);
+        for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
       }
-      if (t0 + k >= first && t0 + k < last) Word<T>::store(o + k * a.os, lane, in, p.words_out, v);
+      if (t0 + k >= first && t0 + k < last) L::store(o + k * a.os, in, whole, hl[k]);
+    }
+    if constexpr (GATE) {
+      __syncwarp();  // g has been read
+      fetch_g(i + 1);
     }
   }
+  if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+  if (ranks > 1) cluster_sync_all();  // no CTA leaves while another may write into it
 }
 
+// -------------------------------------------------------------- backward --
+
 template <typename T, bool GATE>
-__global__ void __launch_bounds__(kGrThreads, kGrBwdBlocksPerSm) gr_backward_kernel(const __grid_constant__ GrParams p) {
-  constexpr int N = Word<T>::N, kArrays = GATE ? 4 : 3, kBytes = kArrays * kGrRows * kGrRowBytes, kArray = kGrRows * kGrRowBytes;
-  extern __shared__ __align__(128) unsigned char ring_mem[];  // [warp][stage][array][row], then the exchange of a cluster
-  __shared__ __align__(16) GrShared<T> sh;
-  __shared__ float fwd_b[2][kGrWarps][32][N];  // the forward's B of the tile's warps
-  __shared__ int fwd_cut[2][kGrWarps];
+__global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 1) gr_backward_kernel(const __grid_constant__ GrParams p) {
+  constexpr int N = 2, kStages = 2;
+  using L = Lane<T, N>;
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGrRows * kRow, kArrays = GATE ? 4 : 3, kStage = kArrays * kArray;
+  extern __shared__ __align__(128) unsigned char dyn[];  // [warp][stage][array][row], then the spans of a cluster's tiles
+  __shared__ GrShared<P> sh;
+  __shared__ alignas(16) uint64_t fwd_B[2][kGrWarps][32][P];  // the forward's spans; their A is that of the gradients
+  __shared__ alignas(8) unsigned char fwd_cut[2][kGrWarps];
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
-  const int c0 = blockIdx.x / ranks * (kGrRowBytes / (int)sizeof(T)), c = c0 + lane * N;
+  const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;
+  const bool whole = p.whole && in == N;
   const int T_ = (int)a.T;
-  const uint32_t ring = smem_addr(ring_mem) + warp * (kGrBwdStages * kBytes);
-  auto of_ranks = reinterpret_cast<float (*)[32][2 * N]>(ring_mem + kGrWarps * kGrBwdStages * kBytes);
-  if (ranks > 1) cluster_sync_all();  // every CTA of the cluster is there
+  const uint32_t ring = smem_addr(dyn) + warp * (kStages * kStage);
+  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kStages * kStage);
+  const uint64_t zero[P] = {};
+  if (warp == 0) L::put(sh.state[0][lane], zero);
+  if (ranks > 1) {
+    if (threadIdx.x == 0) {
+      mbar_init(smem_addr(&sh.arrived[0]), 1);
+      mbar_init(smem_addr(&sh.arrived[1]), 1);
+      mbar_fence_init();
+    }
+    cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
+  }
+  bool ok = true;
   pdl_wait();
   pdl_trigger();
 
   auto row0 = [&](int i) { return ((p.groups - 1 - i) * ranks + rank) * kGrChunk + warp * kGrRows; };
   auto fetch = [&](int i) {
     if (i < p.groups) {
-      const uint32_t to = ring + i % kGrBwdStages * kBytes;
-      fetch_rows<T>(to, a.x, a.xs, row0(i), a.T, c0, a.C, p.access[0], lane);
-      fetch_rows<T>(to + kArray, a.f, a.fs, row0(i), a.T, c0, a.C, p.access[1], lane);
-      fetch_rows<T>(to + 2 * kArray, a.dout, a.dos, row0(i), a.T, c0, a.C, p.access[3], lane);
-      if constexpr (GATE) fetch_rows<T>(to + 3 * kArray, a.g, a.gs, row0(i), a.T, c0, a.C, p.access[2], lane);
+      const uint32_t to = ring + i % kStages * kStage;
+      fetch_rows<T, N>(to, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
+      fetch_rows<T, N>(to + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
+      fetch_rows<T, N>(to + 2 * kArray, a.dout, a.dos, row0(i), T_, c0, a.C, p.access[3], lane);
+      if constexpr (GATE) fetch_rows<T, N>(to + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
     }
     cp_async_commit();
   };
-  for (int i = 0; i < kGrBwdStages - 1; ++i) fetch(i);
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
   pass_empty(a, a.ds1, a.ds0, rank, ranks, c, in, warp, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
-  Boundaries bounds{0, INT_MAX};
-  float state[N];  // the gradient at the state behind the rows not yet visited
+  Boundaries<true> bounds;
+  bounds.begin(first);
+  uint64_t state[P];  // the gradient at the state behind the rows not yet visited
 #pragma unroll
-  for (int e = 0; e < N; ++e) state[e] = 0.f;
+  for (int e = 0; e < P; ++e) state[e] = 0;
 
   for (int i = 0; i < p.groups; ++i) {
     const int t0 = row0(i), par = i & 1;
+    __syncwarp();  // the slot that is filled next has been read
+    fetch(i + kStages - 1);
+    uint64_t hf[P];  // the state ahead of the tile
+    L::load_state(a.chunk + (t0 < T_ ? (long long)(t0 / kGrChunk) * a.C + c : 0), t0 < T_ ? in : 0, hf);
+    const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane);
+    cp_async_wait<kStages - 1>();
     __syncwarp();
-    fetch(i + kGrBwdStages - 1);
-    float hf[N];  // the state ahead of the tile
-#pragma unroll
-    for (int e = 0; e < N; ++e) hf[e] = t0 < T_ && e < in ? a.chunk[(long long)(t0 / kGrChunk) * a.C + c + e] : 0.f;
-    const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane, true);
-    cp_async_wait<kGrBwdStages - 1>();
-    __syncwarp();
-    const uint32_t at = ring + i % kGrBwdStages * kBytes + lane * 4;
+    const uint32_t at = ring + i % kStages * kStage + lane * L::kBytes;
 
-    float ga[kGrRows][N], rest[kGrRows][N], d[kGrRows][N], sg[GATE ? kGrRows : 1][N];
-    float A[N], B[N], R[N];
+    uint64_t ga[kGrRows][P], rest[kGrRows][P], d[kGrRows][P], sg[GATE ? kGrRows : 1][P], A[P], B[P], R[P];
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      A[e] = 1.f;
-      B[e] = R[e] = 0.f;
+    for (int e = 0; e < P; ++e) {
+      A[e] = f2_both(1.f);
+      B[e] = R[e] = 0;
     }
 #pragma unroll
     for (int k = 0; k < kGrRows; ++k) {
-      float x[N], f[N], h0[N];
-      Word<T>::unpack(ld_shared_u32(at + k * kGrRowBytes), x);
-      Word<T>::unpack(ld_shared_u32(at + kArray + k * kGrRowBytes), f);
-      Word<T>::unpack(ld_shared_u32(at + 2 * kArray + k * kGrRowBytes), d[k]);
+      uint64_t x[P];
+      L::load(at + k * kRow, x);
+      L::forgets(at + kArray + k * kRow, ga[k], rest[k]);
+      L::load(at + 2 * kArray + k * kRow, d[k]);
       if constexpr (GATE) {
-        float g[N];
-        Word<T>::unpack(ld_shared_u32(at + 3 * kArray + k * kGrRowBytes), g);
+        uint64_t g[P], u;
+        L::load(at + 3 * kArray + k * kRow, g);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          sg[k][e] = sigmoid<T>(g[e]);
-          d[k][e] *= g[e] * sg[k][e];
+        for (int e = 0; e < P; ++e) {
+          sg[k][e] = f2_sigmoid<T>(g[e], &u);
+          d[k][e] = f2_mul(d[k][e], f2_mul(g[e], sg[k][e]));
         }
       }
       if (a.ds1 && (m.ends >> k & 1)) {
-        const long long s = (long long)sh.seqs[warp][kGrRows + k] * a.C + c;
+        uint64_t v[P];
+        L::load_state(a.ds1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, v);
 #pragma unroll
-        for (int e = 0; e < N; ++e) d[k][e] += e < in ? a.ds1[s + e] : 0.f;
+        for (int e = 0; e < P; ++e) d[k][e] = f2_add(d[k][e], v[e]);
       }
-      const bool start = m.starts >> k & 1;
-      if (start) {
-        const long long s = (long long)sh.seqs[warp][k] * a.C + c;
+      if (m.starts >> k & 1) {
+        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, B);
+        else
 #pragma unroll
-        for (int e = 0; e < N; ++e) h0[e] = a.s0 && e < in ? a.s0[s + e] : 0.f;
+          for (int e = 0; e < P; ++e) B[e] = 0;
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        forget<T>(f[e], &ga[k][e], &rest[k][e]);
-        B[e] = fmaf(ga[k][e], start ? h0[e] : B[e], rest[k][e] * x[e]);
-        A[e] *= ga[k][e];
+      for (int e = 0; e < P; ++e) {
+        B[e] = f2_fma(ga[k][e], B[e], f2_mul(rest[k][e], x[e]));
+        A[e] = f2_mul(A[e], ga[k][e]);
       }
     }
 #pragma unroll
     for (int k = kGrRows - 1; k >= 0; --k) {
-      const bool end = m.ends >> k & 1;
 #pragma unroll
-      for (int e = 0; e < N; ++e) R[e] = ga[k][e] * (end ? d[k][e] : d[k][e] + R[e]);
+      for (int e = 0; e < P; ++e) R[e] = f2_mul(ga[k][e], (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], R[e]));
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      sh.warps[par][warp][lane][2 * e] = A[e];
-      sh.warps[par][warp][lane][2 * e + 1] = R[e];
-      fwd_b[par][warp][lane][e] = B[e];
-    }
+    L::put(sh.A[par][warp][lane], A);
+    L::put(sh.B[par][warp][lane], R);
+    L::put(fwd_B[par][warp][lane], B);
     if (lane == 0) {
-      sh.warp_cut[par][warp] = m.ends != 0;
+      sh.cut[par][warp] = m.ends != 0;
       fwd_cut[par][warp] = m.starts != 0;
     }
     __syncthreads();
-    float G[N];
-    exchange<T, true>(sh, of_ranks, par, rank, ranks, warp, lane, state, G);
-    through_warps<T, true>(sh, par, warp, lane, G);
-    for (int w = 0; w < warp; ++w) {
-      const bool cut = fwd_cut[par][w];
+    uint64_t G[P], behind[P];
+    exchange<L, true>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, R, state, behind, G);
+    through_warps<L, false>(sh.A[par], fwd_B[par], *reinterpret_cast<const uint64_t*>(fwd_cut[par]), warp, lane, hf);
+    if (!ok) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) hf[e] = carry_on(hf[e], sh.warps[par][w][lane][2 * e], fwd_b[par][w][lane][e], cut);
+      for (int k = 0; k < kGrRows; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
     }
     // the states ahead of the rows
-    float hp[kGrRows][N];
+    uint64_t hp[kGrRows][P];
 #pragma unroll
     for (int k = 0; k < kGrRows; ++k) {
-      float x[N];
-      Word<T>::unpack(ld_shared_u32(at + k * kGrRowBytes), x);
+      uint64_t x[P];
+      L::load(at + k * kRow, x);
       if (m.starts >> k & 1) {
-        const long long s = (long long)sh.seqs[warp][k] * a.C + c;
+        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, hf);
+        else
 #pragma unroll
-        for (int e = 0; e < N; ++e) hf[e] = a.s0 && e < in ? a.s0[s + e] : 0.f;
+          for (int e = 0; e < P; ++e) hf[e] = 0;
       }
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
+      for (int e = 0; e < P; ++e) {
         hp[k][e] = hf[e];
-        hf[e] = fmaf(ga[k][e], hf[e], rest[k][e] * x[e]);
+        hf[e] = f2_fma(ga[k][e], hf[e], f2_mul(rest[k][e], x[e]));
       }
     }
-    T* dx = static_cast<T*>(a.dx) + (a.dx ? (long long)t0 * a.dxs + c0 : 0);
-    T* df = static_cast<T*>(a.df) + (a.df ? (long long)t0 * a.dfs + c0 : 0);
-    T* dg = static_cast<T*>(a.dg) + (a.dg ? (long long)t0 * a.dgs + c0 : 0);
+    T* dx = static_cast<T*>(a.dx) + (a.dx ? t0 * a.dxs + c : 0);
+    T* df = static_cast<T*>(a.df) + (a.df ? t0 * a.dfs + c : 0);
+    T* dg = static_cast<T*>(a.dg) + (a.dg ? t0 * a.dgs + c : 0);
 #pragma unroll
     for (int k = kGrRows - 1; k >= 0; --k) {
-      const bool end = m.ends >> k & 1, live = t0 + k >= first && t0 + k < last;
-      float x[N], vx[N], vf[N], vg[N];
-      Word<T>::unpack(ld_shared_u32(at + k * kGrRowBytes), x);
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float dh = end ? d[k][e] : d[k][e] + G[e];
-        vx[e] = rest[k][e] * dh;
-        vf[e] = dh * (hp[k][e] - x[e]) * (ga[k][e] * rest[k][e]);
-        G[e] = ga[k][e] * dh;
-      }
+      const bool live = t0 + k >= first && t0 + k < last;
+      uint64_t x[P], v[P];
+      L::load(at + k * kRow, x);
       if constexpr (GATE) {
-        float g[N], dy[N];
-        Word<T>::unpack(ld_shared_u32(at + 3 * kArray + k * kGrRowBytes), g);
-        Word<T>::unpack(ld_shared_u32(at + 2 * kArray + k * kGrRowBytes), dy);
+        uint64_t g[P], dy[P];
+        L::load(at + 3 * kArray + k * kRow, g);
+        L::load(at + 2 * kArray + k * kRow, dy);
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float h = fmaf(ga[k][e], hp[k][e], rest[k][e] * x[e]), s = sg[k][e];
-          vg[e] = dy[e] * h * fmaf(g[e] * s, 1.f - s, s);
+        for (int e = 0; e < P; ++e) {
+          const uint64_t h = f2_fma(ga[k][e], hp[k][e], f2_mul(rest[k][e], x[e])), s = sg[k][e];
+          v[e] = f2_mul(f2_mul(dy[e], h), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
         }
-        if (live && a.dg) Word<T>::store(dg + k * a.dgs, lane, in, p.words_out, vg);
+        if (live && a.dg) L::store(dg + k * a.dgs, in, whole, v);
       }
-      if (live && a.dx) Word<T>::store(dx + k * a.dxs, lane, in, p.words_out, vx);
-      if (live && a.df) Word<T>::store(df + k * a.dfs, lane, in, p.words_out, vf);
-      if (a.ds0 && (m.starts >> k & 1)) {
-        const long long s = (long long)sh.seqs[warp][k] * a.C + c;
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-          if (e < in) a.ds0[s + e] = G[e];
+      for (int e = 0; e < P; ++e) G[e] = (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], G[e]);  // dh
+      if (live && a.dx) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = f2_mul(rest[k][e], G[e]);
+        L::store(dx + k * a.dxs, in, whole, v);
       }
+      if (live && a.df) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = f2_mul(f2_mul(G[e], f2_sub(hp[k][e], x[e])), f2_mul(ga[k][e], rest[k][e]));
+        L::store(df + k * a.dfs, in, whole, v);
+      }
+#pragma unroll
+      for (int e = 0; e < P; ++e) G[e] = f2_mul(ga[k][e], G[e]);
+      if (a.ds0 && (m.starts >> k & 1)) L::store_state(a.ds0 + (long long)sh.seqs[warp][k] * a.C + c, in, G);
     }
   }
+  if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+  if (ranks > 1) cluster_sync_all();  // no CTA leaves while another may write into it
 }
 
 // One token per row: a CTA owns a row's channels, and goes on through the
@@ -673,7 +874,8 @@ __global__ void __launch_bounds__(kGsThreads) gr_step_kernel(const __grid_consta
       float o = h;
       if (p.g) {
         const float g = load_elem(static_cast<const T*>(p.g) + row * p.gs + c);
-        o *= g * sigmoid<T>(g);
+        float e;
+        o *= g * sigmoid<T>(g, &e);
       }
       store_elem(static_cast<T*>(p.out) + row * p.os + c, o);
     }
@@ -695,54 +897,29 @@ __global__ void __launch_bounds__(kGsThreads) gr_step_kernel(const __grid_consta
 
 int row_access(const void* p, int64_t stride, int es) {
   if (!p) return kVectors;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p), step = (uintptr_t)stride * es;
-  return ((at | step) & 15) == 0 ? kVectors : ((at | step) & 3) == 0 ? kWords : kElements;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es);
+  return (at & 15) == 0 ? kVectors : (at & 3) == 0 ? kWords : kElements;
 }
 
-// CTAs to a slab: the GPU's slots filled as evenly as they can be, by as few
-// CTAs as do it (each doubling has to take off a tenth).
-int choose_ranks(int64_t tiles, int64_t slabs, int slots) {
-  int best = 1;
-  double least = 1e300;
-  for (int r = 1; r <= kGrMaxCluster && r <= tiles; r *= 2) {
-    const double cost = (double)((slabs * r + slots - 1) / slots) / r;
-    if (cost < 0.9 * least) {
-      least = cost;
-      best = r;
-    }
-  }
-  return best;
-}
+// A kernel's launch: its channels to a CTA, its shared memory without the
+// cluster's, and how many clusters of each size run at once.
+struct GrKernel {
+  const void* kern;
+  int width, lane_bytes, smem, span_bytes;
+  SmemOptIn opt;
+  std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];
+};
 
-template <typename K>
-cudaError_t launch_gr(K kern, SmemOptIn& opt, const RecurrenceArgs& a, int arrays, int stages, int blocks_per_sm) {
-  DeviceInfo di;
-  cudaError_t e = device_info(&di);
-  if (e != cudaSuccess) return e;
-  const int es = a.dtype == ATTNRES_BF16 ? 2 : 4, ring = kGrWarps * stages * arrays * kGrRows * kGrRowBytes;
-  const int per_rank = 2 * 32 * (8 / es) * (int)sizeof(float);  // of the exchange
-  e = opt.ensure(reinterpret_cast<const void*>(kern), ring + kGrMaxCluster * per_rank);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.T + kGrChunk - 1) / kGrChunk, width = kGrRowBytes / es, slabs = (a.C + width - 1) / width;
-  GrParams p{};
-  p.a = a;
-  p.ranks = choose_ranks(tiles, slabs, di.sm_count * blocks_per_sm);
-  p.groups = (int)((tiles + p.ranks - 1) / p.ranks);
-  const void* in[4] = {a.x, a.f, a.g, a.dout};
-  const int64_t strides[4] = {a.xs, a.fs, a.gs, a.dos};
-  for (int i = 0; i < 4; ++i) p.access[i] = row_access(in[i], strides[i], es);
-  p.words_out = row_access(a.out, a.os, es) <= kWords && row_access(a.dx, a.dxs, es) <= kWords &&
-                row_access(a.df, a.dfs, es) <= kWords && row_access(a.dg, a.dgs, es) <= kWords;
+cudaLaunchConfig_t gr_config(const GrKernel& k, int64_t slabs, int ranks, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(slabs * p.ranks));
+  cfg.gridDim = dim3((unsigned)(slabs * ranks));
   cfg.blockDim = dim3(kGrThreads);
-  cfg.dynamicSmemBytes = ring + (p.ranks > 1 ? p.ranks * per_rank : 0);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute attr[2];
+  cfg.dynamicSmemBytes = k.smem + (ranks > 1 ? 2 * ranks * k.span_bytes : 0);
+  cfg.stream = stream;
   int n = 0;
-  if (p.ranks > 1) {
+  if (ranks > 1) {
     attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = p.ranks;
+    attr[n].val.clusterDim.x = ranks;
     attr[n].val.clusterDim.y = 1;
     attr[n].val.clusterDim.z = 1;
     ++n;
@@ -754,18 +931,85 @@ cudaError_t launch_gr(K kern, SmemOptIn& opt, const RecurrenceArgs& a, int array
   }
   cfg.attrs = attr;
   cfg.numAttrs = n;
+  return cfg;
+}
+
+// clusters of `ranks` CTAs that run at once (clusters do not cross the GPU's
+// groups of SMs, so fewer than CTAs / ranks may fit)
+cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::atomic<int>* slot = dev >= 0 && dev < SmemOptIn::kMaxDevices ? &k.clusters[dev][ranks] : nullptr;
+  if (slot && (*n = slot->load()) > 0) return cudaSuccess;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = gr_config(k, 1, ranks, nullptr, attr);
+  if (ranks > 1) {
+    e = cudaOccupancyMaxActiveClusters(n, k.kern, &cfg);
+  } else {
+    DeviceInfo di;
+    e = device_info(&di);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k.kern, kGrThreads, cfg.dynamicSmemBytes);
+    *n *= di.sm_count;
+  }
+  if (e == cudaSuccess && *n < 1) *n = 1;
+  if (e == cudaSuccess && slot) slot->store(*n);
+  return e;
+}
+
+#ifndef GR_MAXR
+#define GR_MAXR kGrMaxCluster
+#endif
+template <typename... A>
+cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) {
+  cudaError_t e = k.opt.ensure(k.kern, k.smem + 2 * kGrMaxCluster * k.span_bytes);
+  if (e != cudaSuccess) return e;
+  const int es = a.dtype == ATTNRES_BF16 ? 2 : 4;
+  const int64_t tiles = (a.T + kGrChunk - 1) / kGrChunk, slabs = (a.C + k.width - 1) / k.width;
+  // CTAs to a slab: the smallest cluster that takes off a tenth of the time
+  // (rounds of clusters x tiles of a CTA) against each smaller one
+  GrParams p{};
+  double least = 1e300;
+  for (int r = 1; r <= GR_MAXR && r <= (tiles > 1 ? tiles : 1); ++r) {
+    int n = 0;
+    e = clusters_at_once(k, r, &n);
+    if (e != cudaSuccess) return e;
+    const double cost = (double)((slabs + n - 1) / n) * (double)((tiles + r - 1) / r);
+    if (r == 1 || cost < 0.9 * least) {
+      least = cost;
+      p.ranks = r;
+    }
+  }
+  p.a = a;
+  p.wait_ns = wait_limit_ns();
+  p.withhold = debug_withhold_row1() > 0;
+  p.groups = (int)((tiles + p.ranks - 1) / p.ranks);
+  const void* in[4] = {a.x, a.f, a.g, a.dout};
+  const int64_t strides[4] = {a.xs, a.fs, a.gs, a.dos};
+  for (int i = 0; i < 4; ++i) p.access[i] = row_access(in[i], strides[i], es);
+  const void* out[4] = {a.out, a.dx, a.df, a.dg};
+  const int64_t out_strides[4] = {a.os, a.dxs, a.dfs, a.dgs};
+  p.whole = 1;
+  for (int i = 0; i < 4; ++i)
+    if (out[i] && ((reinterpret_cast<uintptr_t>(out[i]) | (uintptr_t)(out_strides[i] * es)) & (uintptr_t)(k.lane_bytes - 1))) p.whole = 0;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = gr_config(k, slabs, p.ranks, a.stream, attr);
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
 template <typename T, bool GATE>
 cudaError_t launch_forward(const RecurrenceArgs& a) {
-  static SmemOptIn opt;
-  return launch_gr(gr_forward_kernel<T, GATE>, opt, a, GATE ? 3 : 2, kGrStages, kGrBlocksPerSm);
+  using L = Lane<T, 8 / sizeof(T)>;
+  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * 2 * L::P, L::kBytes,
+                    kGrChunk * 32 * L::kBytes * (GATE ? 3 : 2), (int)sizeof(RankSpan<L::P>), {}, {}};
+  return launch_gr(k, gr_forward_kernel<T, GATE>, a);
 }
 template <typename T, bool GATE>
 cudaError_t launch_backward(const RecurrenceArgs& a) {
-  static SmemOptIn opt;
-  return launch_gr(gr_backward_kernel<T, GATE>, opt, a, GATE ? 4 : 3, kGrBwdStages, kGrBwdBlocksPerSm);
+  using L = Lane<T, 2>;
+  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * 2 * L::P, L::kBytes,
+                    2 * kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
+  return launch_gr(k, gr_backward_kernel<T, GATE>, a);
 }
 
 }  // namespace

@@ -790,7 +790,7 @@ int64_t attnres_layer_norm_backward_workspace_size(int64_t T, int d);
 int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,
                              int64_t gate_stride, int64_t T, int C, int dtype, const int32_t* cu_seqlens, int num_seqs,
                              const float* initial_state, float* final_state, void* out, int64_t out_stride,
-                             float* chunk_states, void* stream);
+                             float* chunk_states, int* dev_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * attnres_gated_recurrence_backward -- its gradients, from the forward's
@@ -817,7 +817,7 @@ int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const voi
                                       const float* chunk_states, const void* grad_out, int64_t grad_out_stride,
                                       const float* grad_final_state, void* grad_x, int64_t grad_x_stride, void* grad_forget,
                                       int64_t grad_forget_stride, void* grad_gate, int64_t grad_gate_stride,
-                                      float* grad_initial_state, void* stream);
+                                      float* grad_initial_state, int* dev_err, void* stream);
 
 /* ------------------------------------------------------------------------
  * attnres_gated_recurrence_step -- the form for decoding: row b of the batch

@@ -343,6 +343,41 @@ def test_streams_and_graphs(A):
 
 
 @pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,C", [(2000, 40), (700, 300)])
+def test_waits_that_run_out(A, T, C, dt):
+    """The bounded waits of a cluster's CTAs on one another, made to run out on
+    a healthy GPU (attnres_debug_wait_test: the first tiles' spans are not
+    sent): the call reports it, writes NaN and returns, and the same call then
+    gives the same bits as before."""
+    x, f, g, dy, s0, ds1 = _inputs(T, C, 1, dt, True, 80)
+    out, fin, chunk = torch.empty(T, C, dtype=dt, device="cuda"), torch.empty_like(s0), torch.empty(-(-T // 64), C, device="cuda")
+    grads, ds0 = torch.empty(3, T, C, dtype=dt, device="cuda"), torch.empty_like(s0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        A.attnres_gated_recurrence(x, f, out, gate=g, initial_state=s0, final_state=fin, chunk_states=chunk, dev_err=err)
+        A.attnres_gated_recurrence_backward(x, f, chunk, dy, *grads, gate=g, initial_state=s0, grad_final_state=ds1,
+                                            grad_initial_state=ds0, dev_err=err)
+        torch.cuda.synchronize()
+    call()
+    assert int(err.item()) == 0
+    want = [t.clone() for t in (out, fin, grads, ds0)]
+    A.attnres_debug_wait_test(1_000_000, 0)
+    try:
+        call()
+    finally:
+        A.attnres_debug_wait_test(0, -1)
+    assert int(err.item()) & A.ATTNRES_DEVERR_WAIT_TIMEOUT
+    for t in (out, fin, grads, ds0):
+        assert torch.isnan(t).all()
+    err.zero_()
+    call()
+    assert int(err.item()) == 0
+    for t, v in zip((out, fin, grads, ds0), want):
+        assert torch.equal(t, v)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
 def test_autograd(A, dt):
     from depth_wise_attention_block_gb300 import autograd as F
     cu = [2, 70, 70, 150]

@@ -32,7 +32,7 @@ def _ln(N, **kw):
     (dict(eps=-1.0), "EINVAL"), (dict(eps=float("nan")), "EINVAL"), (dict(eps=float("inf")), "EINVAL"), (dict(xs=63), "EINVAL"),
     (dict(os=63), "EINVAL"), (dict(xs=FAR), "EINVAL"), (dict(T=1 << 40, xs=64), "ERANGE"), (dict(T=1 << 40, os=64, xs=64), "ERANGE"),
     (dict(x=None), "EINVAL"), (dict(out=None), "EINVAL"), (dict(out=X + 2), "EINVAL"), (dict(out=X, os=128), "EINVAL"),
-    (dict(out=V), "EINVAL"), (dict(out=V + 4096 + 252), "EINVAL"),
+    (dict(out=V), "EINVAL"), (dict(out=V + 4096 + 252), "EINVAL"), (dict(x=X + 1), "EINVAL"), (dict(dt=0, out=OUT + 2), "EINVAL"),
 ])
 def test_layer_norm_refuses(N, kw, code):
     assert _ln(N, **kw) == getattr(N, "ATTNRES_" + code), N.lib.attnres_last_error()
@@ -49,7 +49,7 @@ def _ln_bwd(N, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(dt=-1), "EDTYPE"), (dict(x=None), "EINVAL"), (dict(dy=None), "EINVAL"), (dict(dys=63), "EINVAL"), (dict(gxs=63), "EINVAL"),
     (dict(ws=None), "EINVAL"), (dict(gx=X), "EINVAL"), (dict(gx=DY + 2), "EINVAL"), (dict(gx=DY, gxs=128), "EINVAL"), (dict(gg=V), "EINVAL"),
-    (dict(gb=OUT), "EINVAL"), (dict(gb=OUT + 0x100000), "EINVAL"), (dict(ws=X - 256), "EINVAL"), (dict(ws=OUT), "EINVAL"),
+    (dict(gb=OUT), "EINVAL"), (dict(gb=OUT + 0x100000), "EINVAL"), (dict(dy=DY + 1), "EINVAL"), (dict(dt=0, gx=OUT + 2), "EINVAL"), (dict(ws=X - 256), "EINVAL"), (dict(ws=OUT), "EINVAL"),
 ])
 def test_layer_norm_backward_refuses(N, kw, code):
     assert _ln_bwd(N, **kw) == getattr(N, "ATTNRES_" + code), N.lib.attnres_last_error()
@@ -68,7 +68,7 @@ def _gr(N, **kw):
     a = dict(x=X, xs=64, f=F, fs=64, g=G, gs=64, T=100, C=64, dt=1, cu=None, n=1, s0=None, s1=None, out=OUT, os=64, ch=None)
     a.update(kw)
     return N.lib.attnres_gated_recurrence(*[a[n] for n in ("x", "xs", "f", "fs", "g", "gs", "T", "C", "dt", "cu", "n", "s0", "s1", "out",
-                                                          "os", "ch")], None)
+                                                          "os", "ch")], None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -77,7 +77,8 @@ def _gr(N, **kw):
     (dict(f=None), "EINVAL"), (dict(out=None), "EINVAL"), (dict(xs=63), "EINVAL"), (dict(fs=63), "EINVAL"), (dict(gs=63), "EINVAL"),
     (dict(os=63), "EINVAL"), (dict(T=1 << 30, xs=1 << 20), "ERANGE"), (dict(out=X), "EINVAL"), (dict(out=F), "EINVAL"),
     (dict(out=G + 2), "EINVAL"), (dict(s0=V, s1=V + 4), "EINVAL"), (dict(s1=OUT), "EINVAL"), (dict(ch=OUT + 64), "EINVAL"),
-    (dict(s1=V, ch=V), "EINVAL"), (dict(cu=V, s1=V), "EINVAL"), (dict(ch=X), "EINVAL"),
+    (dict(s1=V, ch=V), "EINVAL"), (dict(cu=V, s1=V), "EINVAL"), (dict(ch=X), "EINVAL"), (dict(x=X + 1), "EINVAL"), (dict(f=F + 1), "EINVAL"),
+    (dict(g=G + 1), "EINVAL"), (dict(dt=0, out=OUT + 2), "EINVAL"),
 ])
 def test_gated_recurrence_refuses(N, kw, code):
     assert _gr(N, **kw) == getattr(N, "ATTNRES_" + code), N.lib.attnres_last_error()
@@ -89,7 +90,7 @@ def _gr_bwd(N, **kw):
     a.update(kw)
     return N.lib.attnres_gated_recurrence_backward(*[a[n] for n in (
         "x", "xs", "f", "fs", "g", "gs", "T", "C", "dt", "cu", "n", "s0", "ch", "dy", "dys", "ds1", "gx", "gxs", "gf", "gfs", "gg", "ggs",
-        "ds0")], None)
+        "ds0")], None, None)
 
 
 @pytest.mark.parametrize("kw,code", [
