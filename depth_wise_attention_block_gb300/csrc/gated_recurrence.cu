@@ -24,6 +24,7 @@
 #include <math.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "attnres.h"
 #include "body.h"
@@ -400,9 +401,10 @@ struct alignas(16) GrShared {
   uint64_t state[2][32][P];  // of a CTA alone: ahead of its tile
   uint64_t arrived[2];  // mbarriers: the spans of a cluster's tiles are here
   unsigned char cut[2][kGrWarps];
+  uint32_t rank_cut[2][kGrMaxCluster];
   int seqs[kGrWarps][2 * kGrRows];
 };
-// of a cluster's tiles; A = -1: cut
+// of a cluster's tiles
 template <int P>
 struct RankSpan {
   uint64_t A[32][P], B[32][P];
@@ -414,16 +416,26 @@ __device__ __forceinline__ void carry_on(uint64_t (&c)[P], const uint64_t (&A)[P
   for (int i = 0; i < P; ++i) c[i] = cut ? B[i] : f2_fma(A[i], c[i], B[i]);
 }
 
-// c through the spans of the warps before this one (REV: behind it)
-template <typename L, bool REV, typename S>
-__device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][L::P], const uint64_t (&B)[kGrWarps][32][L::P], S cuts,
-                                              int warp, int lane, uint64_t (&c)[L::P]) {
+// c through the spans of the warps before this one (REV: behind it); cuts: a
+// byte for each warp
+template <typename L, bool REV>
+__device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][L::P], const uint64_t (&B)[kGrWarps][32][L::P],
+                                              uint64_t cuts, int warp, int lane, uint64_t (&c)[L::P]) {
   const int n = REV ? kGrWarps - 1 - warp : warp;
+  uint64_t a[L::P], b[L::P];
+  if (cuts == 0) {
 #pragma unroll
-  for (int i = 0; i < kGrWarps - 1; ++i) {
-    if (i < n) {
+    for (int i = 0; i < kGrWarps - 1; ++i) {
+      if (i == n) break;
       const int w = REV ? kGrWarps - 1 - i : i;
-      uint64_t a[L::P], b[L::P];
+      L::get(A[w][lane], a);
+      L::get(B[w][lane], b);
+      carry_on(c, a, b, false);
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int w = REV ? kGrWarps - 1 - i : i;
       L::get(A[w][lane], a);
       L::get(B[w][lane], b);
       carry_on(c, a, b, cuts >> (8 * w) & 1);
@@ -474,38 +486,38 @@ __device__ __forceinline__ void exchange(GrShared<L::P>& sh, RankSpan<L::P>* spa
 #pragma unroll
         for (int i = 0; i < P; ++i) a[i] = f2_mul(a[i], ta[i]);
       }
-    if (cuts) {
-#pragma unroll
-      for (int i = 0; i < P; ++i) a[i] = f2_both(-1.f);
-    }
     const uint32_t at = smem_addr(&spans[par * ranks + rank].A[lane][0]), bt = smem_addr(&spans[par * ranks + rank].B[lane][0]);
-    const uint32_t bar = smem_addr(&sh.arrived[par]);
+    const uint32_t bar = smem_addr(&sh.arrived[par]), flag = smem_addr(&sh.rank_cut[par][rank]);
     // (after a wait that ran out, the barrier's phase is open without an arrival
     // to come: a second one there is not allowed, and the spans that the others
     // still send are few, because they stop in turn when these stay away)
-    if (ok && lane == 0) mbar_arrive_expect_tx(bar, ranks * (uint32_t)sizeof(RankSpan<P>));
+    if (ok && lane == 0) mbar_arrive_expect_tx(bar, ranks * (uint32_t)(sizeof(RankSpan<P>) + 4));
     if (ok && send)
       for (int r = 0; r < ranks; ++r) {
         const uint32_t to = map_shared_rank(bar, r);
         L::put_cluster(map_shared_rank(at, r), a, to);
         L::put_cluster(map_shared_rank(bt, r), b, to);
+        if (lane == 0)
+          asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(map_shared_rank(flag, r)),
+                       "r"((uint32_t)(cuts != 0)), "r"(to)
+                       : "memory");
       }
   }
   // (a tile's spans come after those of the tile two before have been used:
   // their CTA has seen this one's next tile, sent behind a barrier of its own)
   if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&sh.arrived[par]), phase, limit_ns));
-  for (int i = 0; i < ranks; ++i) {
-    const int r = REV ? ranks - 1 - i : i;
+  const uint32_t cut = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_cut[par][lane & (kGrMaxCluster - 1)] != 0);
+  const RankSpan<P>* span = spans + par * ranks + (REV ? ranks - 1 : 0);
+#pragma unroll 1
+  for (int r = REV ? ranks - 1 : 0; REV ? r >= 0 : r < ranks; r += REV ? -1 : 1, span += REV ? -1 : 1) {
     if (r == rank) {
 #pragma unroll
       for (int e = 0; e < P; ++e) ahead[e] = state[e];
     }
     uint64_t a[P], b[P];
-    L::get(spans[par * ranks + r].A[lane], a);
-    L::get(spans[par * ranks + r].B[lane], b);
-    float cut, unused;
-    f2_unpack(a[0], cut, unused);
-    carry_on(state, a, b, cut == -1.f);
+    L::get(span->A[lane], a);
+    L::get(span->B[lane], b);
+    carry_on(state, a, b, cut >> r & 1);
   }
   if (!ok) {
 #pragma unroll
@@ -531,6 +543,7 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;  // channels of this lane
   const bool whole = p.whole && in == N;
+  const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
   const int T_ = (int)a.T;
   const uint32_t ring = smem_addr(dyn) + warp * (kArrays * kArray);
   auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kArrays * kArray);
@@ -587,25 +600,27 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
       A[e] = f2_both(1.f);
       B[e] = 0;
     }
+    // (the rows without a branch where no sequence begins among them)
+    auto scan = [&](auto starts) {
 #pragma unroll
-    for (int k = 0; k < kGrRows; ++k) {
-      uint64_t x[P], g[P], rest[P];
-      L::load(at + k * kRow, x);
-      L::forgets(at + kArray + k * kRow, g, rest);
-      if (m.starts >> k & 1) {
-        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, B);
-        else
+      for (int k = 0; k < kGrRows; ++k) {
+        uint64_t x[P], g[P], rest[P];
+        L::load(at + k * kRow, x);
+        L::forgets(at + kArray + k * kRow, g, rest);
+        if constexpr (starts.value) {
+          if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, B);
+        }
 #pragma unroll
-          for (int e = 0; e < P; ++e) B[e] = 0;
+        for (int e = 0; e < P; ++e) {
+          B[e] = f2_fma(g[e], B[e], f2_mul(rest[e], x[e]));
+          A[e] = f2_mul(A[e], g[e]);
+          hl[k][e] = B[e];
+          pa[k][e] = A[e];
+        }
       }
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        B[e] = f2_fma(g[e], B[e], f2_mul(rest[e], x[e]));
-        A[e] = f2_mul(A[e], g[e]);
-        hl[k][e] = B[e];
-        pa[k][e] = A[e];
-      }
-    }
+    };
+    if (m.starts == 0) scan(std::false_type{});
+    else scan(std::true_type{});
     L::put(sh.A[par][warp][lane], A);
     L::put(sh.B[par][warp][lane], B);
     if (lane == 0) sh.cut[par][warp] = m.starts != 0;
@@ -643,16 +658,24 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
       __syncwarp();
     }
     T* o = static_cast<T*>(a.out) + t0 * a.os + c;
+    auto finish = [&](auto all) {
 #pragma unroll
-    for (int k = 0; k < kGrRows; ++k) {
-      if constexpr (GATE) {
-        uint64_t g[P], e;
-        L::load(at + 2 * kArray + k * kRow, g);
+      for (int k = 0; k < kGrRows; ++k) {
+        if constexpr (GATE) {
+          uint64_t g[P], e;
+          L::load(at + 2 * kArray + k * kRow, g);
 #pragma unroll
-        for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
+          for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
+        }
+        if constexpr (all.value) {
+          if (in) L::store(o + k * a.os, N, true, hl[k]);
+        } else {
+          if (t0 + k >= first && t0 + k < last) L::store(o + k * a.os, in, whole, hl[k]);
+        }
       }
-      if (t0 + k >= first && t0 + k < last) L::store(o + k * a.os, in, whole, hl[k]);
-    }
+    };
+    if (even && t0 >= first && t0 + kGrRows <= last) finish(std::true_type{});
+    else finish(std::false_type{});
     if constexpr (GATE) {
       __syncwarp();  // g has been read
       fetch_g(i + 1);
@@ -679,6 +702,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;
   const bool whole = p.whole && in == N;
+  const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
   const int T_ = (int)a.T;
   const uint32_t ring = smem_addr(dyn) + warp * (kStages * kStage);
   auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kStages * kStage);
@@ -734,6 +758,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
       A[e] = f2_both(1.f);
       B[e] = R[e] = 0;
     }
+    auto scan = [&](auto marks) {
 #pragma unroll
     for (int k = 0; k < kGrRows; ++k) {
       uint64_t x[P];
@@ -749,17 +774,14 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
           d[k][e] = f2_mul(d[k][e], f2_mul(g[e], sg[k][e]));
         }
       }
-      if (a.ds1 && (m.ends >> k & 1)) {
-        uint64_t v[P];
-        L::load_state(a.ds1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, v);
+      if constexpr (marks.value) {
+        if (a.ds1 && (m.ends >> k & 1)) {
+          uint64_t v[P];
+          L::load_state(a.ds1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, v);
 #pragma unroll
-        for (int e = 0; e < P; ++e) d[k][e] = f2_add(d[k][e], v[e]);
-      }
-      if (m.starts >> k & 1) {
-        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, B);
-        else
-#pragma unroll
-          for (int e = 0; e < P; ++e) B[e] = 0;
+          for (int e = 0; e < P; ++e) d[k][e] = f2_add(d[k][e], v[e]);
+        }
+        if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, B);
       }
 #pragma unroll
       for (int e = 0; e < P; ++e) {
@@ -770,8 +792,11 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
 #pragma unroll
     for (int k = kGrRows - 1; k >= 0; --k) {
 #pragma unroll
-      for (int e = 0; e < P; ++e) R[e] = f2_mul(ga[k][e], (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], R[e]));
+      for (int e = 0; e < P; ++e) R[e] = f2_mul(ga[k][e], marks.value && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], R[e]));
     }
+    };
+    if ((m.starts | m.ends) == 0) scan(std::false_type{});
+    else scan(std::true_type{});
     L::put(sh.A[par][warp][lane], A);
     L::put(sh.B[par][warp][lane], R);
     L::put(fwd_B[par][warp][lane], B);
@@ -789,59 +814,60 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
 #pragma unroll
         for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
     }
-    // the states ahead of the rows
-    uint64_t hp[kGrRows][P];
-#pragma unroll
-    for (int k = 0; k < kGrRows; ++k) {
-      uint64_t x[P];
-      L::load(at + k * kRow, x);
-      if (m.starts >> k & 1) {
-        if (a.s0) L::load_state(a.s0 + (long long)sh.seqs[warp][k] * a.C + c, in, hf);
-        else
-#pragma unroll
-          for (int e = 0; e < P; ++e) hf[e] = 0;
-      }
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        hp[k][e] = hf[e];
-        hf[e] = f2_fma(ga[k][e], hf[e], f2_mul(rest[k][e], x[e]));
-      }
-    }
+    uint64_t hp[kGrRows][P];  // the states ahead of the rows
     T* dx = static_cast<T*>(a.dx) + (a.dx ? t0 * a.dxs + c : 0);
     T* df = static_cast<T*>(a.df) + (a.df ? t0 * a.dfs + c : 0);
     T* dg = static_cast<T*>(a.dg) + (a.dg ? t0 * a.dgs + c : 0);
+    // all: no sequence begins or ends among the rows, all of them are of one,
+    // and all gradients are wanted: no branches
+    auto finish = [&](auto all) {
+      constexpr bool kAll = all.value;
 #pragma unroll
-    for (int k = kGrRows - 1; k >= 0; --k) {
-      const bool live = t0 + k >= first && t0 + k < last;
-      uint64_t x[P], v[P];
-      L::load(at + k * kRow, x);
-      if constexpr (GATE) {
-        uint64_t g[P], dy[P];
-        L::load(at + 3 * kArray + k * kRow, g);
-        L::load(at + 2 * kArray + k * kRow, dy);
+      for (int k = 0; k < kGrRows; ++k) {
+        uint64_t x[P];
+        L::load(at + k * kRow, x);
+        if constexpr (!kAll) {
+          if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, hf);
+        }
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          const uint64_t h = f2_fma(ga[k][e], hp[k][e], f2_mul(rest[k][e], x[e])), s = sg[k][e];
-          v[e] = f2_mul(f2_mul(dy[e], h), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
+          hp[k][e] = hf[e];
+          hf[e] = f2_fma(ga[k][e], hf[e], f2_mul(rest[k][e], x[e]));
         }
-        if (live && a.dg) L::store(dg + k * a.dgs, in, whole, v);
       }
 #pragma unroll
-      for (int e = 0; e < P; ++e) G[e] = (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], G[e]);  // dh
-      if (live && a.dx) {
+      for (int k = kGrRows - 1; k >= 0; --k) {
+        const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
+        uint64_t x[P], v[P];
+        L::load(at + k * kRow, x);
+        if constexpr (GATE) {
+          uint64_t g[P], dy[P];
+          L::load(at + 3 * kArray + k * kRow, g);
+          L::load(at + 2 * kArray + k * kRow, dy);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const uint64_t h = f2_fma(ga[k][e], hp[k][e], f2_mul(rest[k][e], x[e])), s = sg[k][e];
+            v[e] = f2_mul(f2_mul(dy[e], h), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
+          }
+          if (live && (kAll || a.dg)) L::store(dg + k * a.dgs, kAll ? N : in, kAll || whole, v);
+        }
+#pragma unroll
+        for (int e = 0; e < P; ++e) G[e] = !kAll && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], G[e]);  // dh
 #pragma unroll
         for (int e = 0; e < P; ++e) v[e] = f2_mul(rest[k][e], G[e]);
-        L::store(dx + k * a.dxs, in, whole, v);
-      }
-      if (live && a.df) {
+        if (live && (kAll || a.dx)) L::store(dx + k * a.dxs, kAll ? N : in, kAll || whole, v);
 #pragma unroll
         for (int e = 0; e < P; ++e) v[e] = f2_mul(f2_mul(G[e], f2_sub(hp[k][e], x[e])), f2_mul(ga[k][e], rest[k][e]));
-        L::store(df + k * a.dfs, in, whole, v);
-      }
+        if (live && (kAll || a.df)) L::store(df + k * a.dfs, kAll ? N : in, kAll || whole, v);
 #pragma unroll
-      for (int e = 0; e < P; ++e) G[e] = f2_mul(ga[k][e], G[e]);
-      if (a.ds0 && (m.starts >> k & 1)) L::store_state(a.ds0 + (long long)sh.seqs[warp][k] * a.C + c, in, G);
-    }
+        for (int e = 0; e < P; ++e) G[e] = f2_mul(ga[k][e], G[e]);
+        if constexpr (!kAll) {
+          if (a.ds0 && (m.starts >> k & 1)) L::store_state(a.ds0 + (long long)sh.seqs[warp][k] * a.C + c, in, G);
+        }
+      }
+    };
+    if (even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGrRows <= last && a.dx && a.df && (!GATE || a.dg)) finish(std::true_type{});
+    else finish(std::false_type{});
   }
   if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
   if (ranks > 1) cluster_sync_all();  // no CTA leaves while another may write into it
