@@ -37,11 +37,7 @@ namespace attnres {
 namespace {
 
 constexpr int kGrChunk = ATTNRES_RECURRENCE_CHUNK;  // rows of a tile
-constexpr int kGrWarps = 8;
-constexpr int kGrRows = kGrChunk / kGrWarps;        // of a warp
-constexpr int kGrThreads = 32 * kGrWarps;
-constexpr int kGrMaxCluster = 8;
-constexpr int kGrBlocksPerSm = 2;                   // resident CTAs
+constexpr int kGrMaxCluster = 16;
 constexpr int kGsThreads = 256;
 
 // ---------------------------------------------------------- arithmetic ---
@@ -250,9 +246,9 @@ struct GrParams {
   int withhold;    // the bounded-wait test: the first tile's spans are not sent
 };
 
-// One warp's copy of its 8 rows from t0 on (channels c0 and up, N to a lane)
+// One warp's copy of its ROWS rows from t0 on (channels c0 and up, N to a lane)
 // into shared memory; zeros where there is no row or channel.
-template <typename T, int N>
+template <typename T, int N, int ROWS>
 __device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long long stride, int t0, int T_, int c0, int C, int access,
                                            int lane) {
   constexpr int kRow = 32 * Lane<T, N>::kBytes;
@@ -263,19 +259,19 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long l
     const int bytes = left >= V ? 16 : left > 0 ? left * (int)sizeof(T) : 0;
     const T* at = base + (t0 + r0) * stride + c0 + v * V;
     dst += r0 * kRow + v * 16;
-    if (t0 + kGrRows <= T_ && bytes == 16) {
+    if (t0 + ROWS <= T_ && bytes == 16) {
 #pragma unroll
-      for (int i = 0; i < kGrRows / kStep; ++i) cp_async16(dst + i * kStep * kRow, at + i * kStep * stride, 16);
+      for (int i = 0; i < ROWS / kStep; ++i) cp_async16(dst + i * kStep * kRow, at + i * kStep * stride, 16);
     } else {
 #pragma unroll
-      for (int i = 0; i < kGrRows / kStep; ++i) {
+      for (int i = 0; i < ROWS / kStep; ++i) {
         const int n = t0 + r0 + i * kStep < T_ ? bytes : 0;
         cp_async16(dst + i * kStep * kRow, n > 0 ? at + i * kStep * stride : base, n);
       }
     }
   } else {
     constexpr int E = 4 / sizeof(T);  // elements of a word
-    for (int r = 0; r < kGrRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
       const T* row = base + (t0 + r < T_ ? (t0 + r) * stride + c0 : 0);
 #pragma unroll
       for (int i = 0; i < Lane<T, N>::kWords; ++i) {  // (neighbouring lanes, neighbouring words)
@@ -315,29 +311,29 @@ __device__ __forceinline__ int lower_bound(const int* cu, int N, int T_, int t, 
   return lo + __popc(__ballot_sync(0xffffffffu, below));
 }
 
-// Which of a warp's 8 rows begin and end a sequence: bit k for row t0 + k,
-// the sequences in seqs[k] and seqs[8 + k].
+// Which of a warp's rows begin and end a sequence: bit k for row t0 + k, the
+// sequences in seqs[k] and seqs[rows + k].
 struct Marks {
   uint32_t starts, ends;
 };
 // j: the first offset not below t0
-__device__ __noinline__ Marks find_marks(const int* cu, int N, int T_, int t0, int j, int* seqs, int lane) {
+__device__ __noinline__ Marks find_marks(const int* cu, int N, int T_, int t0, int rows, int j, int* seqs, int lane) {
   Marks m{0, 0};
   for (int base = j; base <= N; base += 32) {
     const int i = base + lane;
     const int b = i <= N ? clamp_row(__ldg(cu + i), T_) : INT_MAX;
     uint32_t st = 0, en = 0;
-    if (i < N && b >= t0 && b < t0 + kGrRows && clamp_row(__ldg(cu + i + 1), T_) > b) {
+    if (i < N && b >= t0 && b < t0 + rows && clamp_row(__ldg(cu + i + 1), T_) > b) {
       st = 1u << (b - t0);
       seqs[b - t0] = i;
     }
-    if (i >= 1 && b > t0 && b <= t0 + kGrRows && clamp_row(__ldg(cu + i - 1), T_) < b) {
+    if (i >= 1 && b > t0 && b <= t0 + rows && clamp_row(__ldg(cu + i - 1), T_) < b) {
       en = 1u << (b - 1 - t0);
-      seqs[kGrRows + b - 1 - t0] = i - 1;
+      seqs[rows + b - 1 - t0] = i - 1;
     }
     m.starts |= __reduce_or_sync(0xffffffffu, st);
     m.ends |= __reduce_or_sync(0xffffffffu, en);
-    if (__shfl_sync(0xffffffffu, b, 31) > t0 + kGrRows) break;
+    if (__shfl_sync(0xffffffffu, b, 31) > t0 + rows) break;
   }
   __syncwarp();
   return m;
@@ -345,7 +341,7 @@ __device__ __noinline__ Marks find_marks(const int* cu, int N, int T_, int t0, i
 
 // The marks of a warp's rows, tile after tile in either direction: the offsets
 // are searched only when the rows reach the next one.
-template <bool REV>
+template <int ROWS, bool REV>
 struct Boundaries {
   int j, next;  // the first offset not below the rows last looked at, and its value (REV: that of the one before)
   __device__ __forceinline__ void begin(int first) {
@@ -355,32 +351,32 @@ struct Boundaries {
   __device__ __forceinline__ Marks rows(const RecurrenceArgs& a, int t0, int* seqs, int lane) {
     const int T_ = (int)a.T;
     if (!a.cu) {
-      const Marks m{t0 == 0 ? 1u : 0u, t0 < T_ && T_ <= t0 + kGrRows ? 1u << (T_ - 1 - t0) : 0u};
+      const Marks m{t0 == 0 ? 1u : 0u, t0 < T_ && T_ <= t0 + ROWS ? 1u << (T_ - 1 - t0) : 0u};
       if (m.starts | m.ends) {
-        if (lane < 2 * kGrRows) seqs[lane] = 0;
+        if (lane < 2 * ROWS) seqs[lane] = 0;
         __syncwarp();
       }
       return m;
     }
-    if (REV ? next < t0 : next > t0 + kGrRows) return {0, 0};
+    if (REV ? next < t0 : next > t0 + ROWS) return {0, 0};
     if (REV) {
       j = lower_bound(a.cu, a.N, T_, t0, 0, lane);
       next = j > 0 ? clamp_row(__ldg(a.cu + j - 1), T_) : -1;
     } else if (next < t0) {
       j = lower_bound(a.cu, a.N, T_, t0, j + 1, lane);
       next = j <= a.N ? clamp_row(__ldg(a.cu + j), T_) : INT_MAX;
-      if (next > t0 + kGrRows) return {0, 0};
+      if (next > t0 + ROWS) return {0, 0};
     }
-    return find_marks(a.cu, a.N, T_, t0, j, seqs, lane);
+    return find_marks(a.cu, a.N, T_, t0, ROWS, j, seqs, lane);
   }
 };
 
 // the states of empty sequences go on unchanged (from: or null, zeros)
 __device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, const float* from, float* to, int rank, int ranks, int c, int in, int warp,
-                                           int lane) {
+                                           int warps, int lane) {
   if (!to) return;
   const int T_ = (int)a.T;
-  for (int base = (rank * kGrWarps + warp) * 32; base < a.N; base += ranks * kGrWarps * 32) {
+  for (int base = (rank * warps + warp) * 32; base < a.N; base += ranks * warps * 32) {
     const int i = base + lane;
     const bool none = i < a.N && (a.cu ? clamp_row(__ldg(a.cu + i + 1), T_) <= clamp_row(__ldg(a.cu + i), T_) : T_ == 0);
     for (uint32_t left = __ballot_sync(0xffffffffu, none); left; left &= left - 1) {
@@ -395,14 +391,14 @@ __device__ __forceinline__ void pass_empty(const RecurrenceArgs& a, const float*
 // What a tile's warps leave for one another, two tiles in turn.  A span that a
 // sequence begins in (REV: ends in) is cut: it forgets the state behind it
 // (by choice and not by A = 0: infinities do not pass).
-template <int P>
+template <int P, int W, int ROWS>
 struct alignas(16) GrShared {
-  uint64_t A[2][kGrWarps][32][P], B[2][kGrWarps][32][P];
+  uint64_t A[2][W][32][P], B[2][W][32][P];
   uint64_t state[2][32][P];  // of a CTA alone: ahead of its tile
   uint64_t arrived[2];  // mbarriers: the spans of a cluster's tiles are here
-  unsigned char cut[2][kGrWarps];
+  unsigned char cut[2][8];  // a byte for each warp
   uint32_t rank_cut[2][kGrMaxCluster];
-  int seqs[kGrWarps][2 * kGrRows];
+  int seqs[W][2 * ROWS];
 };
 // of a cluster's tiles
 template <int P>
@@ -418,16 +414,16 @@ __device__ __forceinline__ void carry_on(uint64_t (&c)[P], const uint64_t (&A)[P
 
 // c through the spans of the warps before this one (REV: behind it); cuts: a
 // byte for each warp
-template <typename L, bool REV>
-__device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][L::P], const uint64_t (&B)[kGrWarps][32][L::P],
+template <typename L, int W, bool REV>
+__device__ __forceinline__ void through_warps(const uint64_t (&A)[W][32][L::P], const uint64_t (&B)[W][32][L::P],
                                               uint64_t cuts, int warp, int lane, uint64_t (&c)[L::P]) {
-  const int n = REV ? kGrWarps - 1 - warp : warp;
+  const int n = REV ? W - 1 - warp : warp;
   uint64_t a[L::P], b[L::P];
   if (cuts == 0) {
 #pragma unroll
-    for (int i = 0; i < kGrWarps - 1; ++i) {
+    for (int i = 0; i < W - 1; ++i) {
       if (i == n) break;
-      const int w = REV ? kGrWarps - 1 - i : i;
+      const int w = REV ? W - 1 - i : i;
       L::get(A[w][lane], a);
       L::get(B[w][lane], b);
       carry_on(c, a, b, false);
@@ -435,7 +431,7 @@ __device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][
   } else {
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int w = REV ? kGrWarps - 1 - i : i;
+      const int w = REV ? W - 1 - i : i;
       L::get(A[w][lane], a);
       L::get(B[w][lane], b);
       carry_on(c, a, b, cuts >> (8 * w) & 1);
@@ -448,19 +444,19 @@ __device__ __forceinline__ void through_warps(const uint64_t (&A)[kGrWarps][32][
 // A, B: the warp's own span.  state: what a cluster's CTAs carry along.  ok:
 // becomes false where the cluster's spans did not arrive in time (and then
 // nothing is waited for any more).
-template <typename L, bool REV>
-__device__ __forceinline__ void exchange(GrShared<L::P>& sh, RankSpan<L::P>* spans, int par, uint32_t phase, int rank, int ranks,
+template <typename L, int W, int ROWS, bool REV>
+__device__ __forceinline__ void exchange(GrShared<L::P, W, ROWS>& sh, RankSpan<L::P>* spans, int par, uint32_t phase, int rank, int ranks,
                                          bool send, unsigned long long limit_ns, bool& ok, int warp, int lane,
                                          const uint64_t (&A)[L::P], const uint64_t (&B)[L::P], uint64_t (&state)[L::P],
                                          uint64_t (&ahead)[L::P], uint64_t (&h)[L::P]) {
   constexpr int P = L::P;
   const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut[par]);
-  const bool last = REV ? warp == 0 : warp == kGrWarps - 1;
+  const bool last = REV ? warp == 0 : warp == W - 1;
   if (ranks == 1) {
     L::get(sh.state[par][lane], ahead);
 #pragma unroll
     for (int i = 0; i < P; ++i) h[i] = ahead[i];
-    through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
+    through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
     if (last) {
       uint64_t c[P];
 #pragma unroll
@@ -477,10 +473,10 @@ __device__ __forceinline__ void exchange(GrShared<L::P>& sh, RankSpan<L::P>* spa
       b[i] = 0;
       a[i] = A[i];
     }
-    through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, b);
+    through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, b);
     carry_on(b, A, B, cuts >> (8 * warp) & 1);
 #pragma unroll
-    for (int w = 0; w < kGrWarps; ++w)
+    for (int w = 0; w < W; ++w)
       if (w != warp) {
         L::get(sh.A[par][w][lane], ta);
 #pragma unroll
@@ -525,18 +521,20 @@ __device__ __forceinline__ void exchange(GrShared<L::P>& sh, RankSpan<L::P>* spa
   }
 #pragma unroll
   for (int e = 0; e < P; ++e) h[e] = ahead[e];
-  through_warps<L, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
+  through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
 }
 
 // --------------------------------------------------------------- forward --
 
+constexpr int kGfWarps = 4, kGfRows = kGrChunk / kGfWarps;
+
 template <typename T, bool GATE>
-__global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(const __grid_constant__ GrParams p) {
-  constexpr int N = 8 / sizeof(T);
+__global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __grid_constant__ GrParams p) {
+  constexpr int N = 2;
   using L = Lane<T, N>;
-  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGrRows * kRow, kArrays = GATE ? 3 : 2;
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGfRows * kRow, kArrays = GATE ? 3 : 2;
   extern __shared__ __align__(128) unsigned char dyn[];  // [warp][array][row], then the spans of a cluster's tiles
-  __shared__ GrShared<P> sh;
+  __shared__ GrShared<P, kGfWarps, kGfRows> sh;
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
@@ -546,9 +544,11 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
   const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
   const int T_ = (int)a.T;
   const uint32_t ring = smem_addr(dyn) + warp * (kArrays * kArray);
-  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kArrays * kArray);
+  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGfWarps * kArrays * kArray);
   const uint64_t zero[P] = {};
   if (warp == 0) L::put(sh.state[0][lane], zero);
+  if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(sh.cut[threadIdx.x]) = 0;
+  __syncthreads();
   if (ranks > 1) {
     if (threadIdx.x == 0) {
       mbar_init(smem_addr(&sh.arrived[0]), 1);
@@ -561,25 +561,25 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
   pdl_wait();
   pdl_trigger();
 
-  auto row0 = [&](int i) { return (i * ranks + rank) * kGrChunk + warp * kGrRows; };
+  auto row0 = [&](int i) { return (i * ranks + rank) * kGrChunk + warp * kGfRows; };
   auto fetch_xf = [&](int i) {
     if (i < p.groups) {
-      fetch_rows<T, N>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
-      fetch_rows<T, N>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
+      fetch_rows<T, N, kGfRows>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
+      fetch_rows<T, N, kGfRows>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
     }
     cp_async_commit();  // a group for every tile, there or not
   };
   auto fetch_g = [&](int i) {
     if constexpr (GATE) {
-      if (i < p.groups) fetch_rows<T, N>(ring + 2 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
+      if (i < p.groups) fetch_rows<T, N, kGfRows>(ring + 2 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
       cp_async_commit();
     }
   };
   fetch_xf(0);
   fetch_g(0);
-  pass_empty(a, a.s0, a.s1, rank, ranks, c, in, warp, lane);
+  pass_empty(a, a.s0, a.s1, rank, ranks, c, in, warp, kGfWarps, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
-  Boundaries<false> bounds;
+  Boundaries<kGfRows, false> bounds;
   bounds.begin(first);
   uint64_t state[P];
 #pragma unroll
@@ -594,7 +594,7 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
     const uint32_t at = ring + lane * L::kBytes;
 
     // the rows from a state of zero: h = hl + pa * (the state ahead), hl alone behind a first token
-    uint64_t hl[kGrRows][P], pa[kGrRows][P], A[P], B[P];
+    uint64_t hl[kGfRows][P], pa[kGfRows][P], A[P], B[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       A[e] = f2_both(1.f);
@@ -603,7 +603,7 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
     // (the rows without a branch where no sequence begins among them)
     auto scan = [&](auto starts) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k) {
+      for (int k = 0; k < kGfRows; ++k) {
         uint64_t x[P], g[P], rest[P];
         L::load(at + k * kRow, x);
         L::forgets(at + kArray + k * kRow, g, rest);
@@ -628,30 +628,30 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
     fetch_xf(i + 1);
     __syncthreads();
     uint64_t h[P], ahead[P];
-    exchange<L, false>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, B, state, ahead, h);
+    exchange<L, kGfWarps, kGfRows, false>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, B, state, ahead, h);
     if (warp == 0 && a.chunk && t0 < T_) L::store_state(a.chunk + (long long)(t0 / kGrChunk) * a.C + c, in, ahead);
     if (m.starts == 0) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k)
+      for (int k = 0; k < kGfRows; ++k)
 #pragma unroll
         for (int e = 0; e < P; ++e) hl[k][e] = f2_fma(pa[k][e], h[e], hl[k][e]);
     } else {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k)
+      for (int k = 0; k < kGfRows; ++k)
         if (!(m.starts & ((2u << k) - 1)))
 #pragma unroll
           for (int e = 0; e < P; ++e) hl[k][e] = f2_fma(pa[k][e], h[e], hl[k][e]);
     }
     if (!ok) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k)
+      for (int k = 0; k < kGfRows; ++k)
 #pragma unroll
         for (int e = 0; e < P; ++e) hl[k][e] = f2_both(__int_as_float(0x7fc00000));
     }
     if (m.ends && a.s1) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k)
-        if (m.ends >> k & 1) L::store_state(a.s1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, hl[k]);
+      for (int k = 0; k < kGfRows; ++k)
+        if (m.ends >> k & 1) L::store_state(a.s1 + (long long)sh.seqs[warp][kGfRows + k] * a.C + c, in, hl[k]);
     }
     if constexpr (GATE) {
       cp_async_wait<1>();
@@ -660,7 +660,7 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
     T* o = static_cast<T*>(a.out) + t0 * a.os + c;
     auto finish = [&](auto all) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k) {
+      for (int k = 0; k < kGfRows; ++k) {
         if constexpr (GATE) {
           uint64_t g[P], e;
           L::load(at + 2 * kArray + k * kRow, g);
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
         }
       }
     };
-    if (even && t0 >= first && t0 + kGrRows <= last) finish(std::true_type{});
+    if (even && t0 >= first && t0 + kGfRows <= last) finish(std::true_type{});
     else finish(std::false_type{});
     if constexpr (GATE) {
       __syncwarp();  // g has been read
@@ -687,15 +687,17 @@ __global__ void __launch_bounds__(kGrThreads, kGrBlocksPerSm) gr_forward_kernel(
 
 // -------------------------------------------------------------- backward --
 
+constexpr int kGbWarps = 8, kGbRows = kGrChunk / kGbWarps;
+
 template <typename T, bool GATE>
-__global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 1) gr_backward_kernel(const __grid_constant__ GrParams p) {
+__global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_backward_kernel(const __grid_constant__ GrParams p) {
   constexpr int N = 2, kStages = 2;
   using L = Lane<T, N>;
-  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGrRows * kRow, kArrays = GATE ? 4 : 3, kStage = kArrays * kArray;
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGbRows * kRow, kArrays = GATE ? 4 : 3, kStage = kArrays * kArray;
   extern __shared__ __align__(128) unsigned char dyn[];  // [warp][stage][array][row], then the spans of a cluster's tiles
-  __shared__ GrShared<P> sh;
-  __shared__ alignas(16) uint64_t fwd_B[2][kGrWarps][32][P];  // the forward's spans; their A is that of the gradients
-  __shared__ alignas(8) unsigned char fwd_cut[2][kGrWarps];
+  __shared__ GrShared<P, kGbWarps, kGbRows> sh;
+  __shared__ alignas(16) uint64_t fwd_B[2][kGbWarps][32][P];  // the forward's spans; their A is that of the gradients
+  __shared__ alignas(8) unsigned char fwd_cut[2][kGbWarps];
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
@@ -705,9 +707,11 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
   const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
   const int T_ = (int)a.T;
   const uint32_t ring = smem_addr(dyn) + warp * (kStages * kStage);
-  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGrWarps * kStages * kStage);
+  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGbWarps * kStages * kStage);
   const uint64_t zero[P] = {};
   if (warp == 0) L::put(sh.state[0][lane], zero);
+  if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(sh.cut[threadIdx.x]) = 0;
+  __syncthreads();
   if (ranks > 1) {
     if (threadIdx.x == 0) {
       mbar_init(smem_addr(&sh.arrived[0]), 1);
@@ -720,22 +724,22 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
   pdl_wait();
   pdl_trigger();
 
-  auto row0 = [&](int i) { return ((p.groups - 1 - i) * ranks + rank) * kGrChunk + warp * kGrRows; };
+  auto row0 = [&](int i) { return ((p.groups - 1 - i) * ranks + rank) * kGrChunk + warp * kGbRows; };
   auto fetch = [&](int i) {
     if (i < p.groups) {
       const uint32_t to = ring + i % kStages * kStage;
-      fetch_rows<T, N>(to, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
-      fetch_rows<T, N>(to + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
-      fetch_rows<T, N>(to + 2 * kArray, a.dout, a.dos, row0(i), T_, c0, a.C, p.access[3], lane);
-      if constexpr (GATE) fetch_rows<T, N>(to + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
+      fetch_rows<T, N, kGbRows>(to, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
+      fetch_rows<T, N, kGbRows>(to + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
+      fetch_rows<T, N, kGbRows>(to + 2 * kArray, a.dout, a.dos, row0(i), T_, c0, a.C, p.access[3], lane);
+      if constexpr (GATE) fetch_rows<T, N, kGbRows>(to + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
     }
     cp_async_commit();
   };
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
-  pass_empty(a, a.ds1, a.ds0, rank, ranks, c, in, warp, lane);
+  pass_empty(a, a.ds1, a.ds0, rank, ranks, c, in, warp, kGbWarps, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
-  Boundaries<true> bounds;
+  Boundaries<kGbRows, true> bounds;
   bounds.begin(first);
   uint64_t state[P];  // the gradient at the state behind the rows not yet visited
 #pragma unroll
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
     __syncwarp();
     const uint32_t at = ring + i % kStages * kStage + lane * L::kBytes;
 
-    uint64_t ga[kGrRows][P], rest[kGrRows][P], d[kGrRows][P], sg[GATE ? kGrRows : 1][P], A[P], B[P], R[P];
+    uint64_t ga[kGbRows][P], rest[kGbRows][P], d[kGbRows][P], sg[GATE ? kGbRows : 1][P], A[P], B[P], R[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       A[e] = f2_both(1.f);
@@ -760,7 +764,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
     }
     auto scan = [&](auto marks) {
 #pragma unroll
-    for (int k = 0; k < kGrRows; ++k) {
+    for (int k = 0; k < kGbRows; ++k) {
       uint64_t x[P];
       L::load(at + k * kRow, x);
       L::forgets(at + kArray + k * kRow, ga[k], rest[k]);
@@ -777,7 +781,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
       if constexpr (marks.value) {
         if (a.ds1 && (m.ends >> k & 1)) {
           uint64_t v[P];
-          L::load_state(a.ds1 + (long long)sh.seqs[warp][kGrRows + k] * a.C + c, in, v);
+          L::load_state(a.ds1 + (long long)sh.seqs[warp][kGbRows + k] * a.C + c, in, v);
 #pragma unroll
           for (int e = 0; e < P; ++e) d[k][e] = f2_add(d[k][e], v[e]);
         }
@@ -790,7 +794,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
       }
     }
 #pragma unroll
-    for (int k = kGrRows - 1; k >= 0; --k) {
+    for (int k = kGbRows - 1; k >= 0; --k) {
 #pragma unroll
       for (int e = 0; e < P; ++e) R[e] = f2_mul(ga[k][e], marks.value && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], R[e]));
     }
@@ -806,15 +810,15 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
     }
     __syncthreads();
     uint64_t G[P], behind[P];
-    exchange<L, true>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, R, state, behind, G);
-    through_warps<L, false>(sh.A[par], fwd_B[par], *reinterpret_cast<const uint64_t*>(fwd_cut[par]), warp, lane, hf);
+    exchange<L, kGbWarps, kGbRows, true>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, R, state, behind, G);
+    through_warps<L, kGbWarps, false>(sh.A[par], fwd_B[par], *reinterpret_cast<const uint64_t*>(fwd_cut[par]), warp, lane, hf);
     if (!ok) {
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k)
+      for (int k = 0; k < kGbRows; ++k)
 #pragma unroll
         for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
     }
-    uint64_t hp[kGrRows][P];  // the states ahead of the rows
+    uint64_t hp[kGbRows][P];  // the states ahead of the rows
     T* dx = static_cast<T*>(a.dx) + (a.dx ? t0 * a.dxs + c : 0);
     T* df = static_cast<T*>(a.df) + (a.df ? t0 * a.dfs + c : 0);
     T* dg = static_cast<T*>(a.dg) + (a.dg ? t0 * a.dgs + c : 0);
@@ -823,7 +827,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
     auto finish = [&](auto all) {
       constexpr bool kAll = all.value;
 #pragma unroll
-      for (int k = 0; k < kGrRows; ++k) {
+      for (int k = 0; k < kGbRows; ++k) {
         uint64_t x[P];
         L::load(at + k * kRow, x);
         if constexpr (!kAll) {
@@ -836,7 +840,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
         }
       }
 #pragma unroll
-      for (int k = kGrRows - 1; k >= 0; --k) {
+      for (int k = kGbRows - 1; k >= 0; --k) {
         const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
         uint64_t x[P], v[P];
         L::load(at + k * kRow, x);
@@ -866,7 +870,7 @@ __global__ void __launch_bounds__(kGrThreads, sizeof(T) == 2 ? kGrBlocksPerSm : 
         }
       }
     };
-    if (even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGrRows <= last && a.dx && a.df && (!GATE || a.dg)) finish(std::true_type{});
+    if (even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGbRows <= last && a.dx && a.df && (!GATE || a.dg)) finish(std::true_type{});
     else finish(std::false_type{});
   }
   if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
@@ -931,7 +935,7 @@ int row_access(const void* p, int64_t stride, int es) {
 // cluster's, and how many clusters of each size run at once.
 struct GrKernel {
   const void* kern;
-  int width, lane_bytes, smem, span_bytes;
+  int threads, width, lane_bytes, smem, span_bytes;
   SmemOptIn opt;
   std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];
 };
@@ -939,7 +943,7 @@ struct GrKernel {
 cudaLaunchConfig_t gr_config(const GrKernel& k, int64_t slabs, int ranks, cudaStream_t stream, cudaLaunchAttribute* attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(slabs * ranks));
-  cfg.blockDim = dim3(kGrThreads);
+  cfg.blockDim = dim3(k.threads);
   cfg.dynamicSmemBytes = k.smem + (ranks > 1 ? 2 * ranks * k.span_bytes : 0);
   cfg.stream = stream;
   int n = 0;
@@ -960,6 +964,11 @@ cudaLaunchConfig_t gr_config(const GrKernel& k, int64_t slabs, int ranks, cudaSt
   return cfg;
 }
 
+// (clusters of more than 8 CTAs are asked for explicitly)
+cudaError_t allow_cluster(const GrKernel& k, int ranks) {
+  return ranks > 8 ? cudaFuncSetAttribute(k.kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+}
+
 // clusters of `ranks` CTAs that run at once (clusters do not cross the GPU's
 // groups of SMs, so fewer than CTAs / ranks may fit)
 cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
@@ -968,6 +977,8 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
   if (e != cudaSuccess) return e;
   std::atomic<int>* slot = dev >= 0 && dev < SmemOptIn::kMaxDevices ? &k.clusters[dev][ranks] : nullptr;
   if (slot && (*n = slot->load()) > 0) return cudaSuccess;
+  e = allow_cluster(k, ranks);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gr_config(k, 1, ranks, nullptr, attr);
   if (ranks > 1) {
@@ -975,7 +986,7 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
   } else {
     DeviceInfo di;
     e = device_info(&di);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k.kern, kGrThreads, cfg.dynamicSmemBytes);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k.kern, k.threads, cfg.dynamicSmemBytes);
     *n *= di.sm_count;
   }
   if (e == cudaSuccess && *n < 1) *n = 1;
@@ -1018,6 +1029,8 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
   p.whole = 1;
   for (int i = 0; i < 4; ++i)
     if (out[i] && ((reinterpret_cast<uintptr_t>(out[i]) | (uintptr_t)(out_strides[i] * es)) & (uintptr_t)(k.lane_bytes - 1))) p.whole = 0;
+  e = allow_cluster(k, p.ranks);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = gr_config(k, slabs, p.ranks, a.stream, attr);
   return cudaLaunchKernelEx(&cfg, kern, p);
@@ -1025,15 +1038,15 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
 
 template <typename T, bool GATE>
 cudaError_t launch_forward(const RecurrenceArgs& a) {
-  using L = Lane<T, 8 / sizeof(T)>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * 2 * L::P, L::kBytes,
+  using L = Lane<T, 2>;
+  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * kGfWarps, 32 * 2 * L::P, L::kBytes,
                     kGrChunk * 32 * L::kBytes * (GATE ? 3 : 2), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_forward_kernel<T, GATE>, a);
 }
 template <typename T, bool GATE>
 cudaError_t launch_backward(const RecurrenceArgs& a) {
   using L = Lane<T, 2>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * 2 * L::P, L::kBytes,
+  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * kGbWarps, 32 * 2 * L::P, L::kBytes,
                     2 * kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_backward_kernel<T, GATE>, a);
 }
