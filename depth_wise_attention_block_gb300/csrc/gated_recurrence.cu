@@ -72,47 +72,46 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float f2_low(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return lo;
+}
 __device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
 __device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) { return f2_fma(b, f2_both(-1.f), a); }
-constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ uint64_t f2_neg(uint64_t a) { return f2_mul(a, f2_both(-1.f)); }
+// log2 e as the sum of two fp32 numbers
+constexpr float kLog2e = 1.44269504f, kLog2eLow = (float)(1.4426950408889634074 - (double)1.44269504f);
 
-// 1 / (1 + e^-z) on both halves, and e^-z.  For bf16 tensors with the fast
-// exponential and reciprocal (2^-22 each, far below the results' 2^-8), for
-// fp32 ones with the full functions.
+// 1 / (1 + e^-z) on both halves, and e^-z, with the hardware's power of two
+// and reciprocal (2^-22 each).  For fp32 tensors the product z log2 e, whose
+// rounding would cost |z| 2^-24 of e, is the unevaluated sum of two numbers
+// (Dekker's product, by fma), the second entering as a factor 1 + ln 2 * it.
 template <typename T>
 __device__ __forceinline__ uint64_t f2_sigmoid(uint64_t z, uint64_t* e) {
   float a, b;
-  if constexpr (sizeof(T) == 2) {
-    f2_unpack(f2_mul(z, f2_both(-kLog2e)), a, b);
-    *e = f2_pack(ex2(a), ex2(b));
-    f2_unpack(f2_add(*e, f2_both(1.f)), a, b);
-    return f2_pack(rcp(a), rcp(b));
-  } else {
+  if constexpr (sizeof(T) == 4) {  // (of an infinity the product has no second number; at 100 e^-z is 0 already)
     f2_unpack(z, a, b);
-    a = expf(-a);
-    b = expf(-b);
-    *e = f2_pack(a, b);
-    return f2_pack(1.f / (1.f + a), 1.f / (1.f + b));
+    z = f2_pack(min_nan(a, 100.f), min_nan(b, 100.f));
   }
+  const uint64_t hi = f2_mul(z, f2_both(-kLog2e));
+  f2_unpack(hi, a, b);
+  *e = f2_pack(ex2(a), ex2(b));
+  if constexpr (sizeof(T) == 4) {
+    const uint64_t lo = f2_fma(z, f2_both(-kLog2eLow), f2_fma(z, f2_both(-kLog2e), f2_neg(hi)));
+    *e = f2_fma(*e, f2_mul(lo, f2_both(0.69314718f)), *e);
+  }
+  f2_unpack(f2_add(*e, f2_both(1.f)), a, b);
+  return f2_pack(rcp(a), rcp(b));
 }
 
-// One value of it, and the rest to one (not by a difference).  f below -83
-// counts as -83 (a = 1e-36), where e^-f would leave fp32; NaN stays NaN.
+// One value of it: a gate z (below -83 as -83) gives sigma and 1 - sigma.
 template <typename T>
-__device__ __forceinline__ float sigmoid(float z, float* e) {
-  if constexpr (sizeof(T) == 2) {
-    *e = ex2(-kLog2e * z);
-    return rcp(1.f + *e);
-  } else {
-    *e = expf(-z);
-    return 1.f / (1.f + *e);
-  }
-}
-template <typename T>
-__device__ __forceinline__ void forget(float f, float* a, float* rest) {
-  float e;
-  *a = sigmoid<T>(-min_nan(-f, 83.f), &e);
-  *rest = e * *a;
+__device__ __forceinline__ float sigmoid(float z, float* rest) {
+  uint64_t e;
+  const float s = f2_low(f2_sigmoid<T>(f2_both(-min_nan(-z, 83.f)), &e));
+  *rest = f2_low(e) * s;
+  return s;
 }
 
 // -------------------------------------------------- the channels of a lane --
@@ -141,16 +140,20 @@ struct Lane {
     }
   }
   static __device__ __forceinline__ void load(uint32_t addr, uint64_t (&v)[P]) { unpack(load(addr), v); }
-  // the forget gate's a and 1 - a (below -83 as -83)
-  static __device__ __forceinline__ void forgets(uint32_t addr, uint64_t (&a)[P], uint64_t (&rest)[P]) {
+  // a gate: values below -83 count as -83, where e^-z would leave fp32 (NaN stays NaN)
+  static __device__ __forceinline__ void load_gate(uint32_t addr, uint64_t (&v)[P]) {
     Raw r = load(addr);
-    uint64_t f[P];
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       if constexpr (sizeof(T) == 2) r.w[i] = max_nan_bf16x2(r.w[i], 0xC2A6C2A6u);  // -83
       else r.w[i] = __float_as_uint(-min_nan(-__uint_as_float(r.w[i]), 83.f));
     }
-    unpack(r, f);
+    unpack(r, v);
+  }
+  // the forget gate's a and 1 - a (not by a difference)
+  static __device__ __forceinline__ void forgets(uint32_t addr, uint64_t (&a)[P], uint64_t (&rest)[P]) {
+    uint64_t f[P];
+    load_gate(addr, f);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       uint64_t e;
@@ -395,9 +398,9 @@ template <int P, int W, int ROWS>
 struct alignas(16) GrShared {
   uint64_t A[2][W][32][P], B[2][W][32][P];
   uint64_t state[2][32][P];  // of a CTA alone: ahead of its tile
-  uint64_t arrived[2];  // mbarriers: the spans of a cluster's tiles are here
+  uint64_t before[3], after[3];  // mbarriers: a cluster's spans ahead of this CTA's tile are here; the others, its own among them
   unsigned char cut[2][8];  // a byte for each warp
-  uint32_t rank_cut[2][kGrMaxCluster];
+  uint32_t rank_cut[3][kGrMaxCluster];
   int seqs[W][2 * ROWS];
 };
 // of a cluster's tiles
@@ -439,89 +442,127 @@ __device__ __forceinline__ void through_warps(const uint64_t (&A)[W][32][L::P], 
   }
 }
 
-// After a barrier behind the warps' spans: the state at this warp's first row
-// (REV: the gradient behind its last), h, and the one at the CTA's tile, ahead.
-// A, B: the warp's own span.  state: what a cluster's CTAs carry along.  ok:
-// becomes false where the cluster's spans did not arrive in time (and then
-// nothing is waited for any more).
+// A cluster's CTAs in the order of their tiles: `turn` (REV: the last rank
+// first).  Each goes on from the spans ahead of its own tile: those of the
+// earlier turns, and before them those of the tiles that the later turns had
+// before this one.  So a CTA only waits for work that precedes it, and the
+// later turns may fall behind the earlier ones by most of a tile.  The spans
+// lie in three sets, tile i's in set i % 3: a CTA sends tile i + 3's after it
+// has received for tile i + 2, for which every other has sent its tile i + 1's
+// (and those of an earlier turn tile i + 2's), hence used what it got of tile i.
+
+// Behind a barrier after the warps' spans, by one warp: the tile's span to
+// every CTA of the cluster.  (Behind a wait that ran out, ok = false, the
+// barriers' phases are open without an arrival to come; a second one there is
+// not allowed.  The spans that the others still send are few: they stop in
+// turn when these stay away.)
 template <typename L, int W, int ROWS, bool REV>
-__device__ __forceinline__ void exchange(GrShared<L::P, W, ROWS>& sh, RankSpan<L::P>* spans, int par, uint32_t phase, int rank, int ranks,
-                                         bool send, unsigned long long limit_ns, bool& ok, int warp, int lane,
-                                         const uint64_t (&A)[L::P], const uint64_t (&B)[L::P], uint64_t (&state)[L::P],
-                                         uint64_t (&ahead)[L::P], uint64_t (&h)[L::P]) {
+__device__ __forceinline__ void send_span(GrShared<L::P, W, ROWS>& sh, RankSpan<L::P>* spans, int par, int set, int turn, int ranks,
+                                          bool send, int lane) {
   constexpr int P = L::P;
   const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut[par]);
-  const bool last = REV ? warp == 0 : warp == W - 1;
-  if (ranks == 1) {
-    L::get(sh.state[par][lane], ahead);
+  uint64_t a[P], b[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) h[i] = ahead[i];
-    through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
-    if (last) {
-      uint64_t c[P];
-#pragma unroll
-      for (int i = 0; i < P; ++i) c[i] = h[i];
-      carry_on(c, A, B, cuts >> (8 * warp) & 1);
-      L::put(sh.state[par ^ 1][lane], c);
-    }
-    return;
+  for (int e = 0; e < P; ++e) {
+    a[e] = f2_both(1.f);
+    b[e] = 0;
   }
-  if (last) {  // the tile's span, to every CTA of the cluster
-    uint64_t a[P], b[P], ta[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      b[i] = 0;
-      a[i] = A[i];
-    }
-    through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, b);
-    carry_on(b, A, B, cuts >> (8 * warp) & 1);
+  for (int i = 0; i < W; ++i) {
+    const int w = REV ? W - 1 - i : i;
+    uint64_t wa[P], wb[P];
+    L::get(sh.A[par][w][lane], wa);
+    L::get(sh.B[par][w][lane], wb);
+    carry_on(b, wa, wb, cuts >> (8 * w) & 1);
 #pragma unroll
-    for (int w = 0; w < W; ++w)
-      if (w != warp) {
-        L::get(sh.A[par][w][lane], ta);
-#pragma unroll
-        for (int i = 0; i < P; ++i) a[i] = f2_mul(a[i], ta[i]);
-      }
-    const uint32_t at = smem_addr(&spans[par * ranks + rank].A[lane][0]), bt = smem_addr(&spans[par * ranks + rank].B[lane][0]);
-    const uint32_t bar = smem_addr(&sh.arrived[par]), flag = smem_addr(&sh.rank_cut[par][rank]);
-    // (after a wait that ran out, the barrier's phase is open without an arrival
-    // to come: a second one there is not allowed, and the spans that the others
-    // still send are few, because they stop in turn when these stay away)
-    if (ok && lane == 0) mbar_arrive_expect_tx(bar, ranks * (uint32_t)(sizeof(RankSpan<P>) + 4));
-    if (ok && send)
-      for (int r = 0; r < ranks; ++r) {
-        const uint32_t to = map_shared_rank(bar, r);
-        L::put_cluster(map_shared_rank(at, r), a, to);
-        L::put_cluster(map_shared_rank(bt, r), b, to);
-        if (lane == 0)
-          asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(map_shared_rank(flag, r)),
-                       "r"((uint32_t)(cuts != 0)), "r"(to)
-                       : "memory");
-      }
+    for (int e = 0; e < P; ++e) a[e] = f2_mul(a[e], wa[e]);
   }
-  // (a tile's spans come after those of the tile two before have been used:
-  // their CTA has seen this one's next tile, sent behind a barrier of its own)
-  if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&sh.arrived[par]), phase, limit_ns));
-  const uint32_t cut = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_cut[par][lane & (kGrMaxCluster - 1)] != 0);
-  const RankSpan<P>* span = spans + par * ranks + (REV ? ranks - 1 : 0);
+  const uint32_t at = smem_addr(&spans[set * ranks + turn].A[lane][0]), bt = smem_addr(&spans[set * ranks + turn].B[lane][0]);
+  const uint32_t before = smem_addr(&sh.before[set]), after = smem_addr(&sh.after[set]), flag = smem_addr(&sh.rank_cut[set][turn]);
+  if (lane == 0) {
+    constexpr uint32_t kBytes = sizeof(RankSpan<P>) + 4;
+    mbar_arrive_expect_tx(before, turn * kBytes + (send ? 0u : 4u));  // (the bounded-wait test: more than will come)
+    mbar_arrive_expect_tx(after, (ranks - turn) * kBytes);
+  }
+  if (!send) return;
 #pragma unroll 1
-  for (int r = REV ? ranks - 1 : 0; REV ? r >= 0 : r < ranks; r += REV ? -1 : 1, span += REV ? -1 : 1) {
-    if (r == rank) {
-#pragma unroll
-      for (int e = 0; e < P; ++e) ahead[e] = state[e];
-    }
-    uint64_t a[P], b[P];
+  for (int t = 0; t < ranks; ++t) {  // the receiver's turn
+    const int r = REV ? ranks - 1 - t : t;
+    const uint32_t bar = map_shared_rank(turn < t ? before : after, r);
+    L::put_cluster(map_shared_rank(at, r), a, bar);
+    L::put_cluster(map_shared_rank(bt, r), b, bar);
+    if (lane == 0)
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(map_shared_rank(flag, r)),
+                   "r"((uint32_t)(cuts != 0)), "r"(bar)
+                   : "memory");
+  }
+}
+
+// c through the spans of turns from .. to - 1 of a set
+template <typename L, int W, int ROWS>
+__device__ __forceinline__ void through_turns(const GrShared<L::P, W, ROWS>& sh, const RankSpan<L::P>* spans, int set, int from, int to,
+                                              int ranks, int lane, uint64_t (&c)[L::P]) {
+  const uint32_t cut = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_cut[set][lane & (kGrMaxCluster - 1)] != 0);
+  const RankSpan<L::P>* span = spans + set * ranks + from;
+#pragma unroll 1
+  for (int t = from; t < to; ++t, ++span) {
+    uint64_t a[L::P], b[L::P];
     L::get(span->A[lane], a);
     L::get(span->B[lane], b);
-    carry_on(state, a, b, cut >> r & 1);
+    carry_on(c, a, b, cut >> t & 1);
   }
-  if (!ok) {
+}
+
+// The state at this warp's first row (REV: the gradient behind its last), h,
+// and the one at the CTA's tile, ahead.  A, B: the warp's own span.  state: the
+// one that was at the CTA's last tile.  ok: becomes false where the cluster's
+// spans did not arrive in time (and then nothing is waited for any more).
+template <typename L, int W, int ROWS, bool REV>
+__device__ __forceinline__ void receive(GrShared<L::P, W, ROWS>& sh, RankSpan<L::P>* spans, int i, int turn, int ranks,
+                                        unsigned long long limit_ns, bool& ok, int warp, int lane, const uint64_t (&A)[L::P],
+                                        const uint64_t (&B)[L::P], uint64_t (&state)[L::P], uint64_t (&h)[L::P]) {
+  constexpr int P = L::P;
+  const int par = i & 1;
+  const uint64_t cuts = *reinterpret_cast<const uint64_t*>(sh.cut[par]);
+  if (ranks == 1) {
+    L::get(sh.state[par][lane], state);
+  } else {
+    if (i > 0) {
+      const int set = (i - 1) % 3;
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&sh.after[set]), (uint32_t)((i - 1) / 3) & 1u, limit_ns));
+      through_turns<L, W, ROWS>(sh, spans, set, turn, ranks, ranks, lane, state);
+    }
+    const int set = i % 3;
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(smem_addr(&sh.before[set]), (uint32_t)(i / 3) & 1u, limit_ns));
+    through_turns<L, W, ROWS>(sh, spans, set, 0, turn, ranks, lane, state);
+    if (!ok) {
 #pragma unroll
-    for (int e = 0; e < P; ++e) ahead[e] = state[e] = f2_both(__int_as_float(0x7fc00000));
+      for (int e = 0; e < P; ++e) state[e] = f2_both(__int_as_float(0x7fc00000));
+    }
   }
 #pragma unroll
-  for (int e = 0; e < P; ++e) h[e] = ahead[e];
+  for (int e = 0; e < P; ++e) h[e] = state[e];
   through_warps<L, W, REV>(sh.A[par], sh.B[par], cuts, warp, lane, h);
+  if (ranks == 1 && (REV ? warp == 0 : warp == W - 1)) {
+    uint64_t c[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) c[e] = h[e];
+    carry_on(c, A, B, cuts >> (8 * warp) & 1);
+    L::put(sh.state[par ^ 1][lane], c);
+  }
+}
+
+// Ahead of a kernel's end: what others still send to this CTA's last tile has
+// come, and no CTA leaves while another may write into it.
+template <int P, int W, int ROWS>
+__device__ __forceinline__ void leave(GrShared<P, W, ROWS>& sh, int groups, int ranks, unsigned long long limit_ns, bool ok, int* dev_err,
+                                      int lane) {
+  if (ranks == 1) return;
+  if (ok && groups > 0)
+    ok = mbar_wait_cluster_bounded(smem_addr(&sh.after[(groups - 1) % 3]), (uint32_t)((groups - 1) / 3) & 1u, limit_ns);
+  if (!ok && lane == 0) report_error(dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+  __syncwarp();
+  cluster_sync_all();
 }
 
 // --------------------------------------------------------------- forward --
@@ -551,8 +592,11 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
   __syncthreads();
   if (ranks > 1) {
     if (threadIdx.x == 0) {
-      mbar_init(smem_addr(&sh.arrived[0]), 1);
-      mbar_init(smem_addr(&sh.arrived[1]), 1);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        mbar_init(smem_addr(&sh.before[i]), 1);
+        mbar_init(smem_addr(&sh.after[i]), 1);
+      }
       mbar_fence_init();
     }
     cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
@@ -627,9 +671,11 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
     __syncwarp();  // x and f have been read
     fetch_xf(i + 1);
     __syncthreads();
-    uint64_t h[P], ahead[P];
-    exchange<L, kGfWarps, kGfRows, false>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, B, state, ahead, h);
-    if (warp == 0 && a.chunk && t0 < T_) L::store_state(a.chunk + (long long)(t0 / kGrChunk) * a.C + c, in, ahead);
+    if (ranks > 1 && ok && warp == kGfWarps - 1)
+      send_span<L, kGfWarps, kGfRows, false>(sh, spans, par, i % 3, rank, ranks, !(p.withhold && i == 0), lane);
+    uint64_t h[P];
+    receive<L, kGfWarps, kGfRows, false>(sh, spans, i, rank, ranks, p.wait_ns, ok, warp, lane, A, B, state, h);
+    if (warp == 0 && a.chunk && t0 < T_) L::store_state(a.chunk + (long long)(t0 / kGrChunk) * a.C + c, in, state);
     if (m.starts == 0) {
 #pragma unroll
       for (int k = 0; k < kGfRows; ++k)
@@ -663,7 +709,7 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
       for (int k = 0; k < kGfRows; ++k) {
         if constexpr (GATE) {
           uint64_t g[P], e;
-          L::load(at + 2 * kArray + k * kRow, g);
+          L::load_gate(at + 2 * kArray + k * kRow, g);
 #pragma unroll
           for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
         }
@@ -681,8 +727,7 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
       fetch_g(i + 1);
     }
   }
-  if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
-  if (ranks > 1) cluster_sync_all();  // no CTA leaves while another may write into it
+  leave(sh, p.groups, ranks, p.wait_ns, ok, a.dev_err, lane);
 }
 
 // -------------------------------------------------------------- backward --
@@ -714,8 +759,11 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
   __syncthreads();
   if (ranks > 1) {
     if (threadIdx.x == 0) {
-      mbar_init(smem_addr(&sh.arrived[0]), 1);
-      mbar_init(smem_addr(&sh.arrived[1]), 1);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        mbar_init(smem_addr(&sh.before[i]), 1);
+        mbar_init(smem_addr(&sh.after[i]), 1);
+      }
       mbar_fence_init();
     }
     cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
@@ -771,7 +819,7 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
       L::load(at + 2 * kArray + k * kRow, d[k]);
       if constexpr (GATE) {
         uint64_t g[P], u;
-        L::load(at + 3 * kArray + k * kRow, g);
+        L::load_gate(at + 3 * kArray + k * kRow, g);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
           sg[k][e] = f2_sigmoid<T>(g[e], &u);
@@ -809,22 +857,18 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
       fwd_cut[par][warp] = m.starts != 0;
     }
     __syncthreads();
-    uint64_t G[P], behind[P];
-    exchange<L, kGbWarps, kGbRows, true>(sh, spans, par, (uint32_t)(i >> 1) & 1u, rank, ranks, !(p.withhold && i == 0), p.wait_ns, ok, warp, lane, A, R, state, behind, G);
+    if (ranks > 1 && ok && warp == 0)
+      send_span<L, kGbWarps, kGbRows, true>(sh, spans, par, i % 3, ranks - 1 - rank, ranks, !(p.withhold && i == 0), lane);
+    // while the spans are on their way: the states ahead of the rows, and the output gates' gradients
     through_warps<L, kGbWarps, false>(sh.A[par], fwd_B[par], *reinterpret_cast<const uint64_t*>(fwd_cut[par]), warp, lane, hf);
-    if (!ok) {
-#pragma unroll
-      for (int k = 0; k < kGbRows; ++k)
-#pragma unroll
-        for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
-    }
-    uint64_t hp[kGbRows][P];  // the states ahead of the rows
+    uint64_t hp[kGbRows][P];
     T* dx = static_cast<T*>(a.dx) + (a.dx ? t0 * a.dxs + c : 0);
     T* df = static_cast<T*>(a.df) + (a.df ? t0 * a.dfs + c : 0);
     T* dg = static_cast<T*>(a.dg) + (a.dg ? t0 * a.dgs + c : 0);
-    // all: no sequence begins or ends among the rows, all of them are of one,
-    // and all gradients are wanted: no branches
-    auto finish = [&](auto all) {
+    // all: no sequence begins or ends among the rows, and all of them are of
+    // one: no branches (which gradients are wanted must not choose the code, or
+    // their last bits could depend on it)
+    auto states = [&](auto all) {
       constexpr bool kAll = all.value;
 #pragma unroll
       for (int k = 0; k < kGbRows; ++k) {
@@ -838,31 +882,36 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
           hp[k][e] = hf[e];
           hf[e] = f2_fma(ga[k][e], hf[e], f2_mul(rest[k][e], x[e]));
         }
+        if constexpr (GATE) {
+          const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
+          uint64_t g[P], dy[P], v[P];
+          L::load_gate(at + 3 * kArray + k * kRow, g);
+          L::load(at + 2 * kArray + k * kRow, dy);
+#pragma unroll
+          for (int e = 0; e < P; ++e) {
+            const uint64_t s = sg[k][e];
+            v[e] = f2_mul(f2_mul(dy[e], hf[e]), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
+          }
+          if (live && a.dg) L::store(dg + k * a.dgs, kAll ? N : in, kAll || whole, v);
+        }
       }
+    };
+    uint64_t G[P];
+    auto finish = [&](auto all) {
+      constexpr bool kAll = all.value;
 #pragma unroll
       for (int k = kGbRows - 1; k >= 0; --k) {
         const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
         uint64_t x[P], v[P];
         L::load(at + k * kRow, x);
-        if constexpr (GATE) {
-          uint64_t g[P], dy[P];
-          L::load(at + 3 * kArray + k * kRow, g);
-          L::load(at + 2 * kArray + k * kRow, dy);
-#pragma unroll
-          for (int e = 0; e < P; ++e) {
-            const uint64_t h = f2_fma(ga[k][e], hp[k][e], f2_mul(rest[k][e], x[e])), s = sg[k][e];
-            v[e] = f2_mul(f2_mul(dy[e], h), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
-          }
-          if (live && (kAll || a.dg)) L::store(dg + k * a.dgs, kAll ? N : in, kAll || whole, v);
-        }
 #pragma unroll
         for (int e = 0; e < P; ++e) G[e] = !kAll && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], G[e]);  // dh
 #pragma unroll
         for (int e = 0; e < P; ++e) v[e] = f2_mul(rest[k][e], G[e]);
-        if (live && (kAll || a.dx)) L::store(dx + k * a.dxs, kAll ? N : in, kAll || whole, v);
+        if (live && a.dx) L::store(dx + k * a.dxs, kAll ? N : in, kAll || whole, v);
 #pragma unroll
         for (int e = 0; e < P; ++e) v[e] = f2_mul(f2_mul(G[e], f2_sub(hp[k][e], x[e])), f2_mul(ga[k][e], rest[k][e]));
-        if (live && (kAll || a.df)) L::store(df + k * a.dfs, kAll ? N : in, kAll || whole, v);
+        if (live && a.df) L::store(df + k * a.dfs, kAll ? N : in, kAll || whole, v);
 #pragma unroll
         for (int e = 0; e < P; ++e) G[e] = f2_mul(ga[k][e], G[e]);
         if constexpr (!kAll) {
@@ -870,11 +919,22 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
         }
       }
     };
-    if (even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGbRows <= last && a.dx && a.df && (!GATE || a.dg)) finish(std::true_type{});
+    const bool all = even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGbRows <= last;
+    if (all) states(std::true_type{});
+    else states(std::false_type{});
+    receive<L, kGbWarps, kGbRows, true>(sh, spans, i, ranks - 1 - rank, ranks, p.wait_ns, ok, warp, lane, A, R, state, G);
+    if (!ok) {  // every result NaN, the output gates' gradients too
+#pragma unroll
+      for (int k = 0; k < kGbRows; ++k) {
+#pragma unroll
+        for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
+        if (a.dg && t0 + k >= first && t0 + k < last) L::store(dg + k * a.dgs, in, whole, d[k]);
+      }
+    }
+    if (all) finish(std::true_type{});
     else finish(std::false_type{});
   }
-  if (!ok && lane == 0) report_error(a.dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
-  if (ranks > 1) cluster_sync_all();  // no CTA leaves while another may write into it
+  leave(sh, p.groups, ranks, p.wait_ns, ok, a.dev_err, lane);
 }
 
 // One token per row: a CTA owns a row's channels, and goes on through the
@@ -898,14 +958,13 @@ __global__ void __launch_bounds__(kGsThreads) gr_step_kernel(const __grid_consta
   }
   for (;;) {
     if (in) {
-      float a, rest;
-      forget<T>(load_elem(static_cast<const T*>(p.f) + row * p.fs + c), &a, &rest);
+      float rest;
+      const float a = sigmoid<T>(load_elem(static_cast<const T*>(p.f) + row * p.fs + c), &rest);
       h = fmaf(a, h, rest * load_elem(static_cast<const T*>(p.x) + row * p.xs + c));
       float o = h;
       if (p.g) {
-        const float g = load_elem(static_cast<const T*>(p.g) + row * p.gs + c);
-        float e;
-        o *= g * sigmoid<T>(g, &e);
+        const float g = -min_nan(-load_elem(static_cast<const T*>(p.g) + row * p.gs + c), 83.f);
+        o *= g * sigmoid<T>(g, &rest);
       }
       store_elem(static_cast<T*>(p.out) + row * p.os + c, o);
     }
@@ -944,7 +1003,7 @@ cudaLaunchConfig_t gr_config(const GrKernel& k, int64_t slabs, int ranks, cudaSt
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(slabs * ranks));
   cfg.blockDim = dim3(k.threads);
-  cfg.dynamicSmemBytes = k.smem + (ranks > 1 ? 2 * ranks * k.span_bytes : 0);
+  cfg.dynamicSmemBytes = k.smem + (ranks > 1 ? 3 * ranks * k.span_bytes : 0);
   cfg.stream = stream;
   int n = 0;
   if (ranks > 1) {
@@ -999,7 +1058,7 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
 #endif
 template <typename... A>
 cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) {
-  cudaError_t e = k.opt.ensure(k.kern, k.smem + 2 * kGrMaxCluster * k.span_bytes);
+  cudaError_t e = k.opt.ensure(k.kern, k.smem + 3 * kGrMaxCluster * k.span_bytes);
   if (e != cudaSuccess) return e;
   const int es = a.dtype == ATTNRES_BF16 ? 2 : 4;
   const int64_t tiles = (a.T + kGrChunk - 1) / kGrChunk, slabs = (a.C + k.width - 1) / k.width;
