@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kLnThreads = 256;
 constexpr int kLnBlocksPerSm = 4;   // ln_any_kernel
-constexpr int kLnMaxWarps = 16;     // of a row (ln_row_kernel)
+constexpr int kLnMaxWarps = 16;     // of a row in registers
 
 struct LnParams {
   const void* x;
@@ -33,7 +33,7 @@ struct LnParams {
   int d;
   float eps, inv_d;
   float* part;  // backward: [grid][2][d] partial gain and bias gradients, or null
-  int warps;    // ln_row_kernel: warps of a row
+  int warps;    // rows in registers: warps of a row
 };
 
 // sums of N values over the CTA, the same in every thread
@@ -130,251 +130,340 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// rows on their way: as many as shared memory holds at the widest, up to four
-template <int VPT, bool BWD>
-constexpr int kLnAhead = BWD && VPT > 2 ? 3 : 4;
+// What a lane holds of a row: up to VPL vectors' worth of channels, as they lie
+// in memory (16 bits a channel for bf16).  A row's warps own segments of it,
+// `held` vectors to a lane: vector i of a lane is vector lane + 32 i of the
+// segment (VEC), or its channel k of vector i is channel lane + 32 (i V + k).
+// Everything is at a fixed distance from the segment's first address.
+template <typename T, bool VEC>
+struct Segment {
+  static constexpr int V = Vec16<T>::kElems, P = V / 2;  // channels and packed pairs of a vector
+  int at;    // the lane's first channel
+  int left;  // channels of the segment from there on
+  int held;
 
-// What a thread holds of a row: E channels, as packed pairs of fp32.  VEC: VPT
-// 16-byte vectors, vector tid + i G of the row; otherwise single channels,
-// channel tid + j G (G threads to a row).
-template <typename T, int VPT, bool VEC>
-struct Hold {
-  static constexpr int V = Vec16<T>::kElems, E = VPT * V, P = E / 2;
-  static __device__ __forceinline__ int channel(int j, int tid, int G) { return VEC ? (tid + j / V * G) * V + j % V : tid + j * G; }
-  static __device__ __forceinline__ bool has(int j, int tid, int G, int d) { return channel(j, tid, G) < d; }
-  static __device__ __forceinline__ void unpack(const uint4& v, uint64_t* f) {
+  __device__ __forceinline__ Segment(int warp, int warps, int lane, int d) {
+    held = (d + 32 * V * warps - 1) / (32 * V * warps);
+    at = warp * held * 32 * V + lane * (VEC ? V : 1);
+    const int end = (warp + 1) * held * 32 * V;
+    left = (end < d ? end : d) - at;
+  }
+  static __device__ __forceinline__ constexpr int offset(int i, int k) { return VEC ? i * 32 * V + k : (i * V + k) * 32; }
+  __device__ __forceinline__ bool has(int i, int k = 0) const { return offset(i, VEC ? 0 : k) < left; }
+  __device__ __forceinline__ uint4 load(const T* x, int i) const {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if constexpr (VEC) {
+      if (has(i)) v = __ldcs(reinterpret_cast<const uint4*>(x + offset(i, 0)));
+    } else {
+      float f[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = has(i, k) ? load_elem(x + offset(i, k)) : 0.f;
+      v = Vec16<T>::pack(f);  // (exact: the values are of this type)
+    }
+    return v;
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, uint64_t (&f)[P]) {
     float t[V];
     Vec16<T>::unpack(v, t);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) f[i] = f2_pack(t[2 * i], t[2 * i + 1]);
+    for (int k = 0; k < P; ++k) f[k] = f2_pack(t[2 * k], t[2 * k + 1]);
   }
-  // a row of single channels
-  static __device__ __forceinline__ void load(const T* row, int tid, int G, int d, uint64_t (&f)[P]) {
+  __device__ __forceinline__ void store(T* y, int i, const uint64_t (&f)[P]) const {
+    float t[V];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float t[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) t[k] = has(2 * i + k, tid, G, d) ? load_elem(row + channel(2 * i + k, tid, G)) : 0.f;
-      f[i] = f2_pack(t[0], t[1]);
-    }
-  }
-  static __device__ __forceinline__ void store(T* row, int tid, int G, int d, const uint64_t (&f)[P]) {
-    float t[E];
-#pragma unroll
-    for (int i = 0; i < P; ++i) f2_unpack(f[i], t[2 * i], t[2 * i + 1]);
+    for (int k = 0; k < P; ++k) f2_unpack(f[k], t[2 * k], t[2 * k + 1]);
     if constexpr (VEC) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-        if (has(i * V, tid, G, d)) __stcs(reinterpret_cast<uint4*>(row) + tid + i * G, Vec16<T>::pack(t + i * V));
+      __stcs(reinterpret_cast<uint4*>(y + offset(i, 0)), Vec16<T>::pack(t));
     } else {
 #pragma unroll
-      for (int j = 0; j < E; ++j)
-        if (has(j, tid, G, d)) store_elem(row + channel(j, tid, G), t[j]);
+      for (int k = 0; k < V; ++k)
+        if (has(i, k)) store_elem(y + offset(i, k), t[k]);
     }
   }
-  // a vector of fp32 (null: `none`); zero where there is no channel
-  static __device__ __forceinline__ void load_f32(const float* v, float none, int tid, int G, int d, uint64_t (&f)[P]) {
+  // the lane's channels of a vector of fp32 (null: `none`)
+  __device__ __forceinline__ void load_f32(const float* v, float none, int i, uint64_t (&f)[P]) const {
+    if (!v) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      float t[2];
+      for (int k = 0; k < P; ++k) f[k] = f2_both(none);
+    } else if constexpr (VEC) {
+      const ulonglong2* u = reinterpret_cast<const ulonglong2*>(v + offset(i, 0));
 #pragma unroll
-      for (int k = 0; k < 2; ++k) t[k] = !has(2 * i + k, tid, G, d) ? 0.f : v ? __ldg(v + channel(2 * i + k, tid, G)) : none;
-      f[i] = f2_pack(t[0], t[1]);
+      for (int k = 0; k < P / 2; ++k) {
+        const ulonglong2 w = __ldg(u + k);
+        f[2 * k] = w.x;
+        f[2 * k + 1] = w.y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < P; ++k)
+        f[k] = f2_pack(has(i, 2 * k) ? __ldg(v + offset(i, 2 * k)) : 0.f, has(i, 2 * k + 1) ? __ldg(v + offset(i, 2 * k + 1)) : 0.f);
     }
   }
-  // f where there is a channel, else 0
-  static __device__ __forceinline__ void mask(int tid, int G, int d, uint64_t (&f)[P]) {
+  // x - m where there is a channel, else 0
+  __device__ __forceinline__ void center(const uint4& v, uint64_t minus_m, int i, uint64_t (&z)[P]) const {
+    unpack(v, z);
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      if constexpr (VEC) {
-        if (!has(2 * i / V * V, tid, G, d)) f[i] = 0;
-      } else {
+    for (int k = 0; k < P; ++k) {
+      z[k] = f2_add(z[k], minus_m);
+      if constexpr (!VEC) {
         float t[2];
-        f2_unpack(f[i], t[0], t[1]);
-        f[i] = f2_pack(has(2 * i, tid, G, d) ? t[0] : 0.f, has(2 * i + 1, tid, G, d) ? t[1] : 0.f);
+        f2_unpack(z[k], t[0], t[1]);
+        z[k] = f2_pack(has(i, 2 * k) ? t[0] : 0.f, has(i, 2 * k + 1) ? t[1] : 0.f);
       }
     }
   }
 };
 
-// sums of N values over a row's warps, the same in every thread of the row
-// (one barrier: the caller alternates between two buffers)
+// Sums of N values (up to 4) over a row's warps, the same in every thread of
+// the row, in a fixed order.  Several values are summed over a warp by halves:
+// after the first exchanges each lane carries one of them.  One barrier: the
+// caller alternates between two buffers.
 template <int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int warps, int warp, int lane) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) red[warp][i] = v[i];
+  constexpr uint32_t kAll = 0xffffffffu;
+  constexpr int kLanes = N == 1 ? 32 : N == 2 ? 16 : 8;  // that end up with the same value
+  float s;
+  if constexpr (N == 1) {
+    s = v[0];
+  } else if constexpr (N == 2) {
+    const bool hi = lane & 16;
+    s = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], 16);
+  } else {
+    const bool hi = lane & 16, hi2 = lane & 8;
+    const float v3 = N > 3 ? v[N - 1] : 0.f;
+    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[2], 16);
+    const float b = (hi ? v3 : v[1]) + __shfl_xor_sync(kAll, hi ? v[1] : v3, 16);
+    s = (hi2 ? b : a) + __shfl_xor_sync(kAll, hi2 ? a : b, 8);
   }
-  __syncthreads();
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = lane < warps ? red[lane & (kLnMaxWarps - 1)][i] : 0.f;
+  for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  if (warps > 1) {
+    const int which = lane / kLanes, w = lane % kLanes;
+    if (w == 0) red[warp][which] = s;
+    __syncthreads();
+    s = w < warps ? red[w & (kLnMaxWarps - 1)][which] : 0.f;
+    if (kLanes < kLnMaxWarps && w + kLanes < warps) s += red[(w + kLanes) & (kLnMaxWarps - 1)][which];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+    for (int o = (kLanes < kLnMaxWarps ? kLanes : kLnMaxWarps) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, s, i * kLanes);
 }
 
-// Rows that fit the registers of up to 16 warps: read once, with the next ones
-// on their way (VEC: cp.async into shared memory that each thread keeps to
-// itself).  A row belongs to one warp of eight in a CTA, or to a whole CTA.
-template <typename T, int VPT, bool BWD, bool VEC>
-__global__ void __launch_bounds__(32 * kLnMaxWarps, BWD || VPT > 2 ? 1 : 2) ln_row_kernel(const __grid_constant__ LnParams p) {
-  using H = Hold<T, VPT, VEC>;
-  constexpr int P = H::P, kAhead = kLnAhead<VPT, BWD>, kArrays = BWD ? 2 : 1;
-  extern __shared__ __align__(16) unsigned char ring_mem[];  // VEC: [kAhead][kArrays][VPT][threads] vectors; at the end, BWD: sums
+// Rows that fit registers, read once and then taken from there three times.  A
+// row belongs to one warp of a CTA's, or to the whole CTA.
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_constant__ LnParams p) {
+  using S = Segment<T, VEC>;
+  constexpr int P = S::P;
   __shared__ __align__(16) float red[2][kLnMaxWarps][4];
-  const int warps = p.warps, G = 32 * warps, lane = threadIdx.x & 31;
+  const int warps = p.warps, lane = threadIdx.x & 31;
   const int groups = warps == 1 ? (int)blockDim.x >> 5 : 1, group = warps == 1 ? (int)threadIdx.x >> 5 : 0;
-  const int tid = warps == 1 ? lane : (int)threadIdx.x, warp = warps == 1 ? 0 : (int)threadIdx.x >> 5;
-  const int d = p.d;
+  const int warp = warps == 1 ? 0 : (int)threadIdx.x >> 5;
+  const S seg(warp, warps, lane, p.d);
   pdl_wait();
   pdl_trigger();
-  const T* X = static_cast<const T*>(p.x);
-  const T* DY = static_cast<const T*>(p.dy);
-  T* O = static_cast<T*>(p.out);
-  const long long step = (long long)gridDim.x * groups;
-  long long t = (long long)blockIdx.x * groups + group, ahead_t = t;
-  const uint32_t ring = smem_addr(ring_mem) + threadIdx.x * 16;
-  const int slot_bytes = kArrays * VPT * (int)blockDim.x * 16;
-  int ahead_slot = 0, slot = 0;
-  auto fetch = [&] {
-    if constexpr (VEC) {
-      if (ahead_t < p.T) {
-        const uint32_t to = ring + ahead_slot * slot_bytes;
+  const float* gains = p.gain ? p.gain + seg.at : nullptr;
+  const float* biases = p.bias ? p.bias + seg.at : nullptr;
+  for (long long t = (long long)blockIdx.x * groups + group; t < p.T; t += (long long)gridDim.x * groups) {
+    const T* row = static_cast<const T*>(p.x) + t * p.xs + seg.at;
+    uint4 x[VPL];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-          const bool in = H::has(i * H::V, tid, G, d);
-          const int at = in ? H::channel(i * H::V, tid, G) : 0;
-          cp_async16(to + i * blockDim.x * 16, X + ahead_t * p.xs + at, in);
-          if constexpr (BWD) cp_async16(to + (VPT + i) * blockDim.x * 16, DY + ahead_t * p.dys + at, in);
+    for (int i = 0; i < VPL; ++i)
+      if (i < seg.held) x[i] = seg.load(row, i);
+    uint64_t s = 0, f[P];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < seg.held) {
+        S::unpack(x[i], f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) s = f2_add(s, f[k]);
+      }
+    float s1[1] = {f2_hsum(s)};
+    row_sums<1>(s1, red[0], warps, warp, lane);
+    const float m = s1[0] * p.inv_d;
+    uint64_t sz = 0, sq = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < seg.held && (!VEC || seg.has(i))) {
+        seg.center(x[i], f2_both(-m), i, f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          sz = f2_add(sz, f[k]);
+          sq = f2_fma(f[k], f[k], sq);
         }
       }
-      ahead_t += step;
-      ahead_slot = ahead_slot + 1 == kAhead ? 0 : ahead_slot + 1;
-      cp_async_commit();  // a group for every row, there or not
+    float s2[2] = {f2_hsum(sz), f2_hsum(sq)};
+    row_sums<2>(s2, red[1], warps, warp, lane);
+    const float delta = s2[0] * p.inv_d;
+    const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
+    const uint64_t minus_m = f2_both(-m), minus_delta = f2_both(-delta), r2 = f2_both(rstd);
+    T* out = static_cast<T*>(p.out) + t * p.os + seg.at;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (i < seg.held && (!VEC || seg.has(i))) {
+        uint64_t gain[P], bias[P];
+        seg.load_f32(gains, 1.f, i, gain);
+        seg.load_f32(biases, 0.f, i, bias);
+        S::unpack(x[i], f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) f[k] = f2_fma(f2_mul(f2_add(f2_add(f[k], minus_m), minus_delta), r2), gain[k], bias[k]);
+        seg.store(out, i, f);
+      }
+  }
+}
+
+// Its backward: a lane also keeps its channels' sums of dy h and dy over its
+// rows.  VEC: rows ahead by cp.async, in shared memory that each thread keeps to
+// itself.
+#ifndef LN_BV
+#define LN_BV 4
+#endif
+#ifndef LN_AH
+#define LN_AH 3
+#endif
+constexpr int kLnAhead = LN_AH;
+template <typename T, int VPL, bool VEC>
+__global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const __grid_constant__ LnParams p) {
+  using S = Segment<T, VEC>;
+  constexpr int P = S::P;
+  extern __shared__ __align__(16) unsigned char ring_mem[];  // VEC: [kLnAhead][x, dy][VPL][threads] vectors; at the end: sums
+  __shared__ __align__(16) float red[2][kLnMaxWarps][4];
+  const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
+  const int groups = warps == 1 ? nthreads >> 5 : 1, group = warps == 1 ? (int)threadIdx.x >> 5 : 0;
+  const int warp = warps == 1 ? 0 : (int)threadIdx.x >> 5;
+  const S seg(warp, warps, lane, p.d);
+  pdl_wait();
+  pdl_trigger();
+  const T* X = static_cast<const T*>(p.x) + seg.at;
+  const T* DY = static_cast<const T*>(p.dy) + seg.at;
+  const float* gains = p.gain ? p.gain + seg.at : nullptr;
+  const long long step = (long long)gridDim.x * groups;
+  long long t = (long long)blockIdx.x * groups + group, ahead_t = t;
+  const uint32_t vec = nthreads * 16, ring = smem_addr(ring_mem) + threadIdx.x * 16;
+  int ahead_slot = 0, slot = 0;
+  auto fetch = [&] {
+    if (ahead_t < p.T) {
+      const T* xr = X + ahead_t * p.xs;
+      const T* dr = DY + ahead_t * p.dys;
+      uint32_t to = ring + ahead_slot * (2 * VPL * vec);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i, to += 2 * vec) {
+        const bool in = seg.has(i);
+        cp_async16(to, in ? xr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
+        cp_async16(to + vec, in ? dr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
+      }
     }
+    ahead_t += step;
+    ahead_slot = ahead_slot + 1 == kLnAhead ? 0 : ahead_slot + 1;
+    cp_async_commit();  // a group for every row, there or not
   };
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) fetch();
+    for (int i = 0; i < kLnAhead; ++i) fetch();
   }
-  uint64_t gain[P], bias[BWD ? 1 : P], dg[BWD ? P : 1], db[BWD ? P : 1], x[P], dy[BWD ? P : 1], next_x[VEC ? 1 : P], next_dy[!VEC && BWD ? P : 1];
-  H::load_f32(p.gain, 1.f, tid, G, d, gain);
-  if constexpr (!BWD) H::load_f32(p.bias, 0.f, tid, G, d, bias);
-  if constexpr (BWD) {
+  uint64_t dg[VPL][P], db[VPL][P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) dg[i] = db[i] = 0;
-  }
-  if constexpr (!VEC) {
-    if (t < p.T) {
-      H::load(X + t * p.xs, tid, G, d, next_x);
-      if constexpr (BWD) H::load(DY + t * p.dys, tid, G, d, next_dy);
-    }
-  }
+  for (int i = 0; i < VPL; ++i)
+#pragma unroll
+    for (int k = 0; k < P; ++k) dg[i][k] = db[i][k] = 0;
   for (; t < p.T; t += step) {
+    uint4 x[VPL], dy[VPL];
     if constexpr (VEC) {
-      cp_async_wait<kAhead - 1>();
-      const uint32_t at = ring + slot * slot_bytes;
+      cp_async_wait<kLnAhead - 1>();
+      uint32_t at = ring + slot * (2 * VPL * vec);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        H::unpack(ld_shared_v4(at + i * blockDim.x * 16), x + i * H::V / 2);
-        if constexpr (BWD) H::unpack(ld_shared_v4(at + (VPT + i) * blockDim.x * 16), dy + i * H::V / 2);
+      for (int i = 0; i < VPL; ++i, at += 2 * vec) {
+        x[i] = ld_shared_v4(at);
+        dy[i] = ld_shared_v4(at + vec);
       }
-      slot = slot + 1 == kAhead ? 0 : slot + 1;
+      slot = slot + 1 == kLnAhead ? 0 : slot + 1;
       fetch();  // into the slot just read
     } else {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        x[i] = next_x[i];
-        if constexpr (BWD) dy[i] = next_dy[i];
-      }
-      if (t + step < p.T) {
-        H::load(X + (t + step) * p.xs, tid, G, d, next_x);
-        if constexpr (BWD) H::load(DY + (t + step) * p.dys, tid, G, d, next_dy);
+      for (int i = 0; i < VPL; ++i) {
+        x[i] = seg.load(X + t * p.xs, i);
+        dy[i] = seg.load(DY + t * p.dys, i);
       }
     }
-    uint64_t sx = 0, sn = 0;
+    uint64_t sx = 0, sn = 0, f[P], g[P], gain[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      sx = f2_add(sx, x[i]);
-      if constexpr (BWD) sn = f2_fma(dy[i], gain[i], sn);
+    for (int i = 0; i < VPL; ++i) {
+      if (VEC && !seg.has(i)) continue;
+      seg.load_f32(gains, 1.f, i, gain);
+      S::unpack(x[i], f);
+      S::unpack(dy[i], g);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        sx = f2_add(sx, f[k]);
+        sn = f2_fma(g[k], gain[k], sn);
+      }
     }
     float s1[2] = {f2_hsum(sx), f2_hsum(sn)};
-    if constexpr (BWD) {
-      row_sums<2>(s1, red[0], warps, warp, lane);
-    } else {
-      float s[1] = {s1[0]};
-      row_sums<1>(s, red[0], warps, warp, lane);
-      s1[0] = s[0];
-    }
+    row_sums<2>(s1, red[0], warps, warp, lane);
     const float m = s1[0] * p.inv_d;
-    const uint64_t minus_m = f2_both(-m);
-#pragma unroll
-    for (int i = 0; i < P; ++i) x[i] = f2_add(x[i], minus_m);
-    H::mask(tid, G, d, x);
     uint64_t sz = 0, sq = 0, sw = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      sz = f2_add(sz, x[i]);
-      sq = f2_fma(x[i], x[i], sq);
-      if constexpr (BWD) sw = f2_fma(f2_mul(dy[i], gain[i]), x[i], sw);
+    for (int i = 0; i < VPL; ++i) {
+      if (VEC && !seg.has(i)) continue;
+      seg.load_f32(gains, 1.f, i, gain);
+      seg.center(x[i], f2_both(-m), i, f);
+      S::unpack(dy[i], g);
+#pragma unroll
+      for (int k = 0; k < P; ++k) {
+        sz = f2_add(sz, f[k]);
+        sq = f2_fma(f[k], f[k], sq);
+        sw = f2_fma(f2_mul(g[k], gain[k]), f[k], sw);
+      }
     }
     float s2[3] = {f2_hsum(sz), f2_hsum(sq), f2_hsum(sw)};
-    if constexpr (BWD) {
-      row_sums<3>(s2, red[1], warps, warp, lane);
-    } else {
-      float s[2] = {s2[0], s2[1]};
-      row_sums<2>(s, red[1], warps, warp, lane);
-      s2[0] = s[0];
-      s2[1] = s[1];
-    }
+    row_sums<3>(s2, red[1], warps, warp, lane);
     const float delta = s2[0] * p.inv_d;
     const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
-    const uint64_t minus_delta = f2_both(-delta), r2 = f2_both(rstd);
-    if constexpr (!BWD) {
+    const float mn = s1[1] * p.inv_d;
+    const float mh = (s2[2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
+    T* out = static_cast<T*>(p.out) + (p.out ? t * p.os + seg.at : 0);
 #pragma unroll
-      for (int i = 0; i < P; ++i) x[i] = f2_fma(f2_mul(f2_add(x[i], minus_delta), r2), gain[i], bias[i]);
-      H::store(O + t * p.os, tid, G, d, x);
-    } else {
-      const float mn = s1[1] * p.inv_d;
-      const float mh = (s2[2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
-      const uint64_t minus_mh = f2_both(-mh), minus_mn = f2_both(-mn);
+    for (int i = 0; i < VPL; ++i) {
+      if (VEC && !seg.has(i)) continue;
+      seg.load_f32(gains, 1.f, i, gain);
+      S::unpack(x[i], f);
+      S::unpack(dy[i], g);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const uint64_t h = f2_mul(f2_add(x[i], minus_delta), r2);
-        dg[i] = f2_fma(dy[i], h, dg[i]);
-        db[i] = f2_add(db[i], dy[i]);
-        x[i] = f2_mul(f2_add(f2_fma(h, minus_mh, f2_mul(dy[i], gain[i])), minus_mn), r2);
+      for (int k = 0; k < P; ++k) {
+        const uint64_t h = f2_mul(f2_add(f2_add(f[k], f2_both(-m)), f2_both(-delta)), f2_both(rstd));
+        dg[i][k] = f2_fma(g[k], h, dg[i][k]);
+        db[i][k] = f2_add(db[i][k], g[k]);
+        f[k] = f2_mul(f2_add(f2_fma(h, f2_both(-mh), f2_mul(g[k], gain[k])), f2_both(-mn)), f2_both(rstd));
       }
-      if (O) H::store(O + t * p.os, tid, G, d, x);
+      if (p.out) seg.store(out, i, f);
     }
   }
-  if constexpr (BWD) {
-    if (!p.part) return;
-    float* part = p.part + (long long)blockIdx.x * 2 * d;
-    float* sums = reinterpret_cast<float*>(ring_mem);  // [groups][2][d]
-    cp_async_wait<0>();
-    __syncthreads();  // the ring is done with
+  if (!p.part) return;
+  float* part = p.part + (long long)blockIdx.x * 2 * p.d;
+  float* sums = reinterpret_cast<float*>(ring_mem);  // [groups][2][d]
+  if constexpr (VEC) cp_async_wait<0>();
+  __syncthreads();  // the ring is done with
 #pragma unroll
-    for (int j = 0; j < H::E; ++j) {
+  for (int i = 0; i < VPL; ++i)
+#pragma unroll
+    for (int k = 0; k < S::V; ++k) {
       float a[2], b[2];
-      f2_unpack(dg[j / 2], a[0], a[1]);
-      f2_unpack(db[j / 2], b[0], b[1]);
-      if (H::has(j, tid, G, d)) {
-        const int c = H::channel(j, tid, G);
-        float* at = groups > 1 ? sums + group * 2 * d : part;
-        at[c] = a[j & 1];
-        at[d + c] = b[j & 1];
+      f2_unpack(dg[i][k / 2], a[0], a[1]);
+      f2_unpack(db[i][k / 2], b[0], b[1]);
+      if (seg.has(i, k)) {
+        const int c = seg.at + S::offset(i, k);
+        float* at = groups > 1 ? sums + group * 2 * p.d : part;
+        at[c] = a[k & 1];
+        at[p.d + c] = b[k & 1];
       }
     }
-    if (groups > 1) {  // in order: the sums do not depend on timing
-      __syncthreads();
-      for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
-        float s = 0.f;
-        for (int g = 0; g < groups; ++g) s += sums[g * 2 * d + c];
-        part[c] = s;
-      }
+  if (groups > 1) {  // in order: the sums do not depend on timing
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * p.d; c += nthreads) {
+      float s = 0.f;
+      for (int g = 0; g < groups; ++g) s += sums[g * 2 * p.d + c];
+      part[c] = s;
     }
   }
 }
@@ -401,47 +490,59 @@ __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* par
   if (lane == 0 && blockIdx.x * 32 + r < d) out[blockIdx.x * 32 + r] = s;
 }
 
-// How a call's rows are held: vectors or channels to a thread, warps to a row
-// (0: a row does not fit, ln_any_kernel).
+// How a call's rows are held: vectors to a thread, warps to a row (vpl 0: a row
+// does not fit, ln_any_kernel), threads of a CTA.
 struct LnPlan {
-  int vpt, warps, threads;
+  int vpl, warps, threads;
 };
-LnPlan ln_plan(int d, int es, bool vec) {
+LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, int sms) {
   const int V = 16 / es;
-  for (int vpt = vec ? 2 : 1; vpt <= (vec ? 4 : 2); vpt *= 2) {
-    const int per_warp = 32 * vpt * (vec ? 1 : V), items = vec ? d / V : d;
-    const int warps = (items + per_warp - 1) / per_warp;
-    if (warps <= kLnMaxWarps) return {vpt, warps, warps == 1 ? 256 : 32 * warps};
+  // few rows: each over as many warps as it feeds, a thread's channels few
+  const bool few = T <= 2 * sms;
+  constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[2] = {1, LN_BV};
+  const int* vpl = backward ? kBackward : vec ? kForwardVec : kForward;
+  const int n = backward ? 2 : 3;
+  for (int i = 0; i < n; ++i) {
+    const int per_warp = 32 * vpl[i] * V, warps = (d + per_warp - 1) / per_warp;
+    // many rows: a row in as few warps as hold it, so that its sums cross few of them
+    if (warps > kLnMaxWarps || (!few && i + 1 < n && warps > 1)) continue;
+    return {vpl[i], warps, warps > 1 ? 32 * warps : backward ? 256 : 128};
   }
   return {0, 0, 0};
 }
-// CTAs to an SM: the forward's registers allow 32 warps, the backward's 16
+// CTAs to an SM, by the kernels' registers
 int ln_blocks_per_sm(const LnPlan& k, bool backward) {
-  const int n = (backward || k.vpt > 2 ? 512 : 1024) / k.threads;
-  return n < 1 ? 1 : n > 8 ? 8 : n;
+  const int warps = backward ? 16 : k.vpl > 8 ? 16 : 24, n = warps * 32 / k.threads;
+  return n < 1 ? 1 : n > (backward ? 4 : 16) ? (backward ? 4 : 16) : n;
 }
 
-template <typename T, int VPT, bool VEC>
-cudaError_t launch_rows(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid) {
-  const int ring = VEC ? (a.backward ? kLnAhead<VPT, true> : kLnAhead<VPT, false>) * (a.backward ? 2 : 1) * VPT * k.threads * 16 : 0;
-  const int sums = a.backward && k.warps == 1 ? k.threads / 32 * 2 * a.d * 4 : 0;
-  const int smem = ring > sums ? ring : sums;
-  if (a.backward) {
-    static SmemOptIn opt;
-    const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_kernel<T, VPT, true, VEC>), kLnAhead<VPT, true> * 2 * VPT * 32 * kLnMaxWarps * 16);
-    if (e != cudaSuccess) return e;
-    return launch_kernel(ln_row_kernel<T, VPT, true, VEC>, dim3(grid), dim3(k.threads), smem, a.stream, p);
-  }
+template <typename T, int VPL, bool VEC>
+cudaError_t launch_forward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid) {
+  return launch_kernel(ln_row_kernel<T, VPL, VEC>, dim3(grid), dim3(k.threads), 0, a.stream, p);
+}
+template <typename T, int VPL, bool VEC>
+cudaError_t launch_backward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid) {
   static SmemOptIn opt;
-  const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_kernel<T, VPT, false, VEC>), kLnAhead<VPT, false> * VPT * 32 * kLnMaxWarps * 16);
+  const int ring = VEC ? kLnAhead * 2 * VPL * k.threads * 16 : 0, sums = k.warps == 1 ? k.threads / 32 * 2 * a.d * 4 : 0;
+  const int most = kLnAhead * 2 * VPL * 32 * kLnMaxWarps * 16;  // (a warp's rows of up to 32 VPL vectors: the sums need less)
+  const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_backward_kernel<T, VPL, VEC>), most);
   if (e != cudaSuccess) return e;
-  return launch_kernel(ln_row_kernel<T, VPT, false, VEC>, dim3(grid), dim3(k.threads), smem, a.stream, p);
+  return launch_kernel(ln_row_backward_kernel<T, VPL, VEC>, dim3(grid), dim3(k.threads), ring > sums ? ring : sums, a.stream, p);
 }
 
 template <typename T>
 cudaError_t launch_rows(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, bool vec, int grid) {
-  if (vec) return k.vpt == 2 ? launch_rows<T, 2, true>(a, p, k, grid) : launch_rows<T, 4, true>(a, p, k, grid);
-  return k.vpt == 1 ? launch_rows<T, 1, false>(a, p, k, grid) : launch_rows<T, 2, false>(a, p, k, grid);
+  if (a.backward) {
+    if (vec) return k.vpl == 1 ? launch_backward<T, 1, true>(a, p, k, grid) : launch_backward<T, LN_BV, true>(a, p, k, grid);
+    return k.vpl == 1 ? launch_backward<T, 1, false>(a, p, k, grid) : launch_backward<T, LN_BV, false>(a, p, k, grid);
+  }
+  switch (k.vpl) {
+    case 1: return launch_forward<T, 1, false>(a, p, k, grid);
+    case 2: return vec ? launch_forward<T, 2, true>(a, p, k, grid) : launch_forward<T, 2, false>(a, p, k, grid);
+    case 4: return launch_forward<T, 4, false>(a, p, k, grid);
+    case 8: return launch_forward<T, 8, true>(a, p, k, grid);
+    default: return launch_forward<T, 16, true>(a, p, k, grid);
+  }
 }
 
 bool vec_rows(const void* ptr, int64_t stride, int V) { return (reinterpret_cast<uintptr_t>(ptr) & 15) == 0 && stride % V == 0; }
@@ -451,14 +552,15 @@ bool vec_rows(const void* ptr, int64_t stride, int V) { return (reinterpret_cast
 int64_t layer_norm_backward_workspace_bytes(int64_t T, int d) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
-  // the most CTAs that any type or alignment of rows of this width takes
-  int blocks = 0;
+  // the most CTAs that up to T rows of this width take, of any type and alignment
+  int blocks = kLnBlocksPerSm;
   for (int es = 2; es <= 4; es *= 2)
-    for (int vec = 0; vec < 2; ++vec) {
-      const LnPlan k = ln_plan(d, es, vec != 0);
-      const int n = k.vpt ? ln_blocks_per_sm(k, true) : kLnBlocksPerSm;
-      blocks = n > blocks ? n : blocks;
-    }
+    for (int vec = 0; vec < 2; ++vec)
+      for (int few = 0; few < 2; ++few) {
+        const LnPlan k = ln_plan(few ? 1 : INT64_MAX, d, es, vec != 0, true, di.sm_count);
+        const int n = k.vpl ? ln_blocks_per_sm(k, true) : kLnBlocksPerSm;
+        blocks = n > blocks ? n : blocks;
+      }
   int64_t grid = (int64_t)di.sm_count * blocks;
   if (T < grid) grid = T;
   return grid * 2 * d * 4;
@@ -480,10 +582,11 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a) {
   LnParams p{a.x, a.dy, a.out, a.xs, a.dys, a.os, a.gain, a.bias, a.T, a.d, a.eps, 1.f / (float)a.d, dgain ? a.workspace : nullptr, 0};
   const bool bf16 = a.dtype == ATTNRES_BF16;
   const int es = bf16 ? 2 : 4, V = 16 / es;
-  const bool vec = a.d % V == 0 && vec_rows(a.x, a.xs, V) && (!a.out || vec_rows(a.out, a.os, V)) && (!a.backward || vec_rows(a.dy, a.dys, V));
-  const LnPlan k = ln_plan(a.d, es, vec);
+  const bool vec = a.d % V == 0 && vec_rows(a.x, a.xs, V) && (!a.out || vec_rows(a.out, a.os, V)) && (!a.backward || vec_rows(a.dy, a.dys, V)) &&
+                   ((reinterpret_cast<uintptr_t>(a.gain) | reinterpret_cast<uintptr_t>(a.bias)) & 15) == 0;
+  const LnPlan k = ln_plan(a.T, a.d, es, vec, a.backward, di.sm_count);
   int grid;
-  if (k.vpt) {
+  if (k.vpl) {
     p.warps = k.warps;
     const int64_t rows = k.warps == 1 ? k.threads / 32 : 1, need = (a.T + rows - 1) / rows;  // of a CTA at a time
     const int64_t cap = (int64_t)di.sm_count * ln_blocks_per_sm(k, a.backward);
