@@ -180,23 +180,21 @@ struct Segment {
         if (has(i, k)) store_elem(y + offset(i, k), t[k]);
     }
   }
-  // the lane's channels of a vector of fp32 (null: `none`)
-  __device__ __forceinline__ void load_f32(const float* v, float none, int i, uint64_t (&f)[P]) const {
-    if (!v) {
+  // A vector of fp32 in shared memory, as the lanes read it without conflicts:
+  // the first four channels of every vector, then the other four (V = 8).
+  static __device__ __forceinline__ int place(int c, int d) { return VEC && V == 8 ? (c >> 2 & 1) * (d >> 1) + (c >> 3) * 4 + (c & 3) : c; }
+  // the lane's channels of it; `first`: place(at)
+  __device__ __forceinline__ void load_f32(const float* first, int i, int d, uint64_t (&f)[P]) const {
+    if constexpr (VEC) {
 #pragma unroll
-      for (int k = 0; k < P; ++k) f[k] = f2_both(none);
-    } else if constexpr (VEC) {
-      const ulonglong2* u = reinterpret_cast<const ulonglong2*>(v + offset(i, 0));
-#pragma unroll
-      for (int k = 0; k < P / 2; ++k) {
-        const ulonglong2 w = __ldg(u + k);
-        f[2 * k] = w.x;
-        f[2 * k + 1] = w.y;
+      for (int h = 0; h < P / 2; ++h) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(first + i * 128 + (h ? d >> 1 : 0));
+        f[2 * h] = w.x;
+        f[2 * h + 1] = w.y;
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < P; ++k)
-        f[k] = f2_pack(has(i, 2 * k) ? __ldg(v + offset(i, 2 * k)) : 0.f, has(i, 2 * k + 1) ? __ldg(v + offset(i, 2 * k + 1)) : 0.f);
+      for (int k = 0; k < P; ++k) f[k] = f2_pack(has(i, 2 * k) ? first[offset(i, 2 * k)] : 0.f, has(i, 2 * k + 1) ? first[offset(i, 2 * k + 1)] : 0.f);
     }
   }
   // x - m where there is a channel, else 0
@@ -219,7 +217,7 @@ struct Segment {
 // after the first exchanges each lane carries one of them.  One barrier: the
 // caller alternates between two buffers.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int warps, int warp, int lane) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int warps, int group, int warp, int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
   constexpr int kLanes = N == 1 ? 32 : N == 2 ? 16 : 8;  // that end up with the same value
   float s;
@@ -240,7 +238,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int war
   if (warps > 1) {
     const int which = lane / kLanes, w = lane % kLanes;
     if (w == 0) red[warp][which] = s;
-    __syncthreads();
+    named_barrier_sync(1 + group, 32 * warps);
     s = w < warps ? red[w & (kLnMaxWarps - 1)][which] : 0.f;
     if (kLanes < kLnMaxWarps && w + kLanes < warps) s += red[(w + kLanes) & (kLnMaxWarps - 1)][which];
 #pragma unroll
@@ -250,27 +248,62 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int war
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, s, i * kLanes);
 }
 
+// a vector of fp32 into shared memory by the whole CTA (null: `none`)
+template <typename S>
+__device__ __forceinline__ void stage(float* to, const float* v, float none, int d) {
+#pragma unroll 4
+  for (int c = threadIdx.x; c < d; c += blockDim.x) to[S::place(c, d)] = v ? __ldg(v + c) : none;
+}
+
 // Rows that fit registers, read once and then taken from there three times.  A
-// row belongs to one warp of a CTA's, or to the whole CTA.
+// CTA's warps form groups, each with a row at a time; gain and bias lie in
+// shared memory.  VEC: the next rows are on their way by cp.async, in shared
+// memory that each thread keeps to itself.
 template <typename T, int VPL, bool VEC>
-__global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_constant__ LnParams p) {
+__global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kernel(const __grid_constant__ LnParams p) {
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
+  extern __shared__ __align__(16) unsigned char dyn[];  // gain, bias; VEC: [held][threads] vectors
   __shared__ __align__(16) float red[2][kLnMaxWarps][4];
-  const int warps = p.warps, lane = threadIdx.x & 31;
-  const int groups = warps == 1 ? (int)blockDim.x >> 5 : 1, group = warps == 1 ? (int)threadIdx.x >> 5 : 0;
-  const int warp = warps == 1 ? 0 : (int)threadIdx.x >> 5;
+  const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
+  const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
   const S seg(warp, warps, lane, p.d);
+  float* gains = reinterpret_cast<float*>(dyn);
+  float* biases = gains + (p.d + 3 & ~3);
   pdl_wait();
   pdl_trigger();
-  const float* gains = p.gain ? p.gain + seg.at : nullptr;
-  const float* biases = p.bias ? p.bias + seg.at : nullptr;
-  for (long long t = (long long)blockIdx.x * groups + group; t < p.T; t += (long long)gridDim.x * groups) {
-    const T* row = static_cast<const T*>(p.x) + t * p.xs + seg.at;
-    uint4 x[VPL];
+  const T* X = static_cast<const T*>(p.x) + seg.at;
+  const long long step = (long long)gridDim.x * groups;
+  long long t = (long long)blockIdx.x * groups + group;
+  const uint32_t vec = nthreads * 16, ring = smem_addr(biases + (p.d + 3 & ~3)) + threadIdx.x * 16;
+  auto fetch = [&](long long t) {
+    if (t < p.T) {
+      const T* row = X + t * p.xs;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (i < seg.held) x[i] = seg.load(row, i);
+      for (int i = 0; i < VPL; ++i)
+        if (i < seg.held) cp_async16(ring + i * vec, seg.has(i) ? row + S::offset(i, 0) : static_cast<const T*>(p.x), seg.has(i));
+    }
+    cp_async_commit();
+  };
+  if constexpr (VEC) fetch(t);
+  stage<S>(gains, p.gain, 1.f, p.d);
+  stage<S>(biases, p.bias, 0.f, p.d);
+  __syncthreads();
+  gains += S::place(seg.at, p.d);
+  biases += S::place(seg.at, p.d);
+  for (; t < p.T; t += step) {
+    uint4 x[VPL];
+    if constexpr (VEC) {
+      cp_async_wait<0>();
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i < seg.held) x[i] = ld_shared_v4(ring + i * vec);
+      fetch(t + step);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (i < seg.held) x[i] = seg.load(X + t * p.xs, i);
+    }
     uint64_t s = 0, f[P];
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -280,7 +313,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_c
         for (int k = 0; k < P; ++k) s = f2_add(s, f[k]);
       }
     float s1[1] = {f2_hsum(s)};
-    row_sums<1>(s1, red[0], warps, warp, lane);
+    row_sums<1>(s1, red[0] + group * warps, warps, group, warp, lane);
     const float m = s1[0] * p.inv_d;
     uint64_t sz = 0, sq = 0;
 #pragma unroll
@@ -294,7 +327,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_c
         }
       }
     float s2[2] = {f2_hsum(sz), f2_hsum(sq)};
-    row_sums<2>(s2, red[1], warps, warp, lane);
+    row_sums<2>(s2, red[1] + group * warps, warps, group, warp, lane);
     const float delta = s2[0] * p.inv_d;
     const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
     const uint64_t minus_m = f2_both(-m), minus_delta = f2_both(-delta), r2 = f2_both(rstd);
@@ -303,8 +336,8 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_c
     for (int i = 0; i < VPL; ++i)
       if (i < seg.held && (!VEC || seg.has(i))) {
         uint64_t gain[P], bias[P];
-        seg.load_f32(gains, 1.f, i, gain);
-        seg.load_f32(biases, 0.f, i, bias);
+        seg.load_f32(gains, i, p.d, gain);
+        seg.load_f32(biases, i, p.d, bias);
         S::unpack(x[i], f);
 #pragma unroll
         for (int k = 0; k < P; ++k) f[k] = f2_fma(f2_mul(f2_add(f2_add(f[k], minus_m), minus_delta), r2), gain[k], bias[k]);
@@ -314,41 +347,34 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_kernel(const __grid_c
 }
 
 // Its backward: a lane also keeps its channels' sums of dy h and dy over its
-// rows.  VEC: rows ahead by cp.async, in shared memory that each thread keeps to
-// itself.
-#ifndef LN_BV
-#define LN_BV 4
-#endif
-#ifndef LN_AH
-#define LN_AH 3
-#endif
-constexpr int kLnAhead = LN_AH;
+// group's rows.
+constexpr int kLnAhead = 2;  // rows on their way
 template <typename T, int VPL, bool VEC>
 __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const __grid_constant__ LnParams p) {
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
-  extern __shared__ __align__(16) unsigned char ring_mem[];  // VEC: [kLnAhead][x, dy][VPL][threads] vectors; at the end: sums
+  extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [kLnAhead][held][x, dy][threads] vectors; at the end: sums
   __shared__ __align__(16) float red[2][kLnMaxWarps][4];
   const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
-  const int groups = warps == 1 ? nthreads >> 5 : 1, group = warps == 1 ? (int)threadIdx.x >> 5 : 0;
-  const int warp = warps == 1 ? 0 : (int)threadIdx.x >> 5;
+  const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
   const S seg(warp, warps, lane, p.d);
+  float* gains = reinterpret_cast<float*>(dyn);
   pdl_wait();
   pdl_trigger();
   const T* X = static_cast<const T*>(p.x) + seg.at;
   const T* DY = static_cast<const T*>(p.dy) + seg.at;
-  const float* gains = p.gain ? p.gain + seg.at : nullptr;
   const long long step = (long long)gridDim.x * groups;
   long long t = (long long)blockIdx.x * groups + group, ahead_t = t;
-  const uint32_t vec = nthreads * 16, ring = smem_addr(ring_mem) + threadIdx.x * 16;
+  const uint32_t vec = nthreads * 16, ring = smem_addr(gains + (p.d + 3 & ~3)) + threadIdx.x * 16, row_bytes = 2 * seg.held * vec;
   int ahead_slot = 0, slot = 0;
   auto fetch = [&] {
     if (ahead_t < p.T) {
       const T* xr = X + ahead_t * p.xs;
       const T* dr = DY + ahead_t * p.dys;
-      uint32_t to = ring + ahead_slot * (2 * VPL * vec);
+      uint32_t to = ring + ahead_slot * row_bytes;
 #pragma unroll
       for (int i = 0; i < VPL; ++i, to += 2 * vec) {
+        if (i >= seg.held) break;
         const bool in = seg.has(i);
         cp_async16(to, in ? xr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
         cp_async16(to + vec, in ? dr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
@@ -362,6 +388,9 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
     for (int i = 0; i < kLnAhead; ++i) fetch();
   }
+  stage<S>(gains, p.gain, 1.f, p.d);
+  __syncthreads();
+  gains += S::place(seg.at, p.d);
   uint64_t dg[VPL][P], db[VPL][P];
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
@@ -371,9 +400,10 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
     uint4 x[VPL], dy[VPL];
     if constexpr (VEC) {
       cp_async_wait<kLnAhead - 1>();
-      uint32_t at = ring + slot * (2 * VPL * vec);
+      uint32_t at = ring + slot * row_bytes;
 #pragma unroll
       for (int i = 0; i < VPL; ++i, at += 2 * vec) {
+        if (i >= seg.held) break;
         x[i] = ld_shared_v4(at);
         dy[i] = ld_shared_v4(at + vec);
       }
@@ -390,7 +420,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, 1.f, i, gain);
+      seg.load_f32(gains, i, p.d, gain);
       S::unpack(x[i], f);
       S::unpack(dy[i], g);
 #pragma unroll
@@ -400,13 +430,13 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
       }
     }
     float s1[2] = {f2_hsum(sx), f2_hsum(sn)};
-    row_sums<2>(s1, red[0], warps, warp, lane);
+    row_sums<2>(s1, red[0] + group * warps, warps, group, warp, lane);
     const float m = s1[0] * p.inv_d;
     uint64_t sz = 0, sq = 0, sw = 0;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, 1.f, i, gain);
+      seg.load_f32(gains, i, p.d, gain);
       seg.center(x[i], f2_both(-m), i, f);
       S::unpack(dy[i], g);
 #pragma unroll
@@ -417,7 +447,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
       }
     }
     float s2[3] = {f2_hsum(sz), f2_hsum(sq), f2_hsum(sw)};
-    row_sums<3>(s2, red[1], warps, warp, lane);
+    row_sums<3>(s2, red[1] + group * warps, warps, group, warp, lane);
     const float delta = s2[0] * p.inv_d;
     const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
     const float mn = s1[1] * p.inv_d;
@@ -426,7 +456,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, 1.f, i, gain);
+      seg.load_f32(gains, i, p.d, gain);
       S::unpack(x[i], f);
       S::unpack(dy[i], g);
 #pragma unroll
@@ -441,9 +471,9 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   }
   if (!p.part) return;
   float* part = p.part + (long long)blockIdx.x * 2 * p.d;
-  float* sums = reinterpret_cast<float*>(ring_mem);  // [groups][2][d]
+  float* sums = reinterpret_cast<float*>(dyn);  // [groups][2][d]
   if constexpr (VEC) cp_async_wait<0>();
-  __syncthreads();  // the ring is done with
+  __syncthreads();  // gain and ring are done with
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
 #pragma unroll
@@ -490,58 +520,63 @@ __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* par
   if (lane == 0 && blockIdx.x * 32 + r < d) out[blockIdx.x * 32 + r] = s;
 }
 
-// How a call's rows are held: vectors to a thread, warps to a row (vpl 0: a row
-// does not fit, ln_any_kernel), threads of a CTA.
+// How a call's rows are held: vectors to a lane, warps to a row, rows of a CTA
+// at a time, dynamic shared memory, CTAs to an SM (vpl 0: a row does not fit,
+// ln_any_kernel).
 struct LnPlan {
-  int vpl, warps, threads;
+  int vpl, warps, groups, smem, per_sm;
 };
-LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, int sms) {
-  const int V = 16 / es;
-  // few rows: each over as many warps as it feeds, a thread's channels few
-  const bool few = T <= 2 * sms;
-  constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[2] = {1, LN_BV};
+LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceInfo& di) {
+  constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[2] = {1, 4};
+  const int V = 16 / es, n = backward ? 2 : 3;
   const int* vpl = backward ? kBackward : vec ? kForwardVec : kForward;
-  const int n = backward ? 2 : 3;
+  // few rows: each over as many warps as it feeds, a lane's channels few;
+  // many: a row in as few warps as hold it, so that its sums cross few of them
+  const bool few = T <= 2 * di.sm_count;
   for (int i = 0; i < n; ++i) {
     const int per_warp = 32 * vpl[i] * V, warps = (d + per_warp - 1) / per_warp;
-    // many rows: a row in as few warps as hold it, so that its sums cross few of them
     if (warps > kLnMaxWarps || (!few && i + 1 < n && warps > 1)) continue;
-    return {vpl[i], warps, warps > 1 ? 32 * warps : backward ? 256 : 128};
+    const int held = (d + 32 * V * warps - 1) / (32 * V * warps);
+    for (int groups = few ? 1 : kLnMaxWarps / warps; groups >= 1; --groups) {
+      const int64_t vectors = (int64_t)((d + 3) / 4) * 16 * (backward ? 1 : 2);
+      const int64_t ring = vec ? (int64_t)32 * warps * groups * held * 16 * (backward ? 2 * kLnAhead : 1) : 0;
+      const int64_t sums = backward && groups > 1 ? (int64_t)groups * 2 * d * 4 : 0;
+      const int64_t smem = vectors + ring > sums ? vectors + ring : sums;
+      if (smem + 1024 > di.max_smem_optin) continue;
+      const bool one = vpl[i] == (backward ? 4 : 16) || 2 * smem + 4096 > di.max_smem_optin;
+      return {vpl[i], warps, groups, (int)smem, one ? 1 : 2};
+    }
   }
-  return {0, 0, 0};
-}
-// CTAs to an SM, by the kernels' registers
-int ln_blocks_per_sm(const LnPlan& k, bool backward) {
-  const int warps = backward ? 16 : k.vpl > 8 ? 16 : 24, n = warps * 32 / k.threads;
-  return n < 1 ? 1 : n > (backward ? 4 : 16) ? (backward ? 4 : 16) : n;
+  return {0, 0, 0, 0, 0};
 }
 
 template <typename T, int VPL, bool VEC>
-cudaError_t launch_forward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid) {
-  return launch_kernel(ln_row_kernel<T, VPL, VEC>, dim3(grid), dim3(k.threads), 0, a.stream, p);
+cudaError_t launch_forward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid, int most) {
+  static SmemOptIn opt;
+  const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_kernel<T, VPL, VEC>), most);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(ln_row_kernel<T, VPL, VEC>, dim3(grid), dim3(32 * k.warps * k.groups), k.smem, a.stream, p);
 }
 template <typename T, int VPL, bool VEC>
-cudaError_t launch_backward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid) {
+cudaError_t launch_backward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid, int most) {
   static SmemOptIn opt;
-  const int ring = VEC ? kLnAhead * 2 * VPL * k.threads * 16 : 0, sums = k.warps == 1 ? k.threads / 32 * 2 * a.d * 4 : 0;
-  const int most = kLnAhead * 2 * VPL * 32 * kLnMaxWarps * 16;  // (a warp's rows of up to 32 VPL vectors: the sums need less)
   const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_backward_kernel<T, VPL, VEC>), most);
   if (e != cudaSuccess) return e;
-  return launch_kernel(ln_row_backward_kernel<T, VPL, VEC>, dim3(grid), dim3(k.threads), ring > sums ? ring : sums, a.stream, p);
+  return launch_kernel(ln_row_backward_kernel<T, VPL, VEC>, dim3(grid), dim3(32 * k.warps * k.groups), k.smem, a.stream, p);
 }
 
 template <typename T>
-cudaError_t launch_rows(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, bool vec, int grid) {
+cudaError_t launch_rows(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, bool vec, int grid, int most) {
   if (a.backward) {
-    if (vec) return k.vpl == 1 ? launch_backward<T, 1, true>(a, p, k, grid) : launch_backward<T, LN_BV, true>(a, p, k, grid);
-    return k.vpl == 1 ? launch_backward<T, 1, false>(a, p, k, grid) : launch_backward<T, LN_BV, false>(a, p, k, grid);
+    if (vec) return k.vpl == 1 ? launch_backward<T, 1, true>(a, p, k, grid, most) : launch_backward<T, 4, true>(a, p, k, grid, most);
+    return k.vpl == 1 ? launch_backward<T, 1, false>(a, p, k, grid, most) : launch_backward<T, 4, false>(a, p, k, grid, most);
   }
   switch (k.vpl) {
-    case 1: return launch_forward<T, 1, false>(a, p, k, grid);
-    case 2: return vec ? launch_forward<T, 2, true>(a, p, k, grid) : launch_forward<T, 2, false>(a, p, k, grid);
-    case 4: return launch_forward<T, 4, false>(a, p, k, grid);
-    case 8: return launch_forward<T, 8, true>(a, p, k, grid);
-    default: return launch_forward<T, 16, true>(a, p, k, grid);
+    case 1: return launch_forward<T, 1, false>(a, p, k, grid, most);
+    case 2: return vec ? launch_forward<T, 2, true>(a, p, k, grid, most) : launch_forward<T, 2, false>(a, p, k, grid, most);
+    case 4: return launch_forward<T, 4, false>(a, p, k, grid, most);
+    case 8: return launch_forward<T, 8, true>(a, p, k, grid, most);
+    default: return launch_forward<T, 16, true>(a, p, k, grid, most);
   }
 }
 
@@ -553,16 +588,14 @@ int64_t layer_norm_backward_workspace_bytes(int64_t T, int d) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
   // the most CTAs that up to T rows of this width take, of any type and alignment
-  int blocks = kLnBlocksPerSm;
+  int64_t grid = T < 2 * di.sm_count ? T : 2 * di.sm_count;  // few rows: one to a CTA
   for (int es = 2; es <= 4; es *= 2)
-    for (int vec = 0; vec < 2; ++vec)
-      for (int few = 0; few < 2; ++few) {
-        const LnPlan k = ln_plan(few ? 1 : INT64_MAX, d, es, vec != 0, true, di.sm_count);
-        const int n = k.vpl ? ln_blocks_per_sm(k, true) : kLnBlocksPerSm;
-        blocks = n > blocks ? n : blocks;
-      }
-  int64_t grid = (int64_t)di.sm_count * blocks;
-  if (T < grid) grid = T;
+    for (int vec = 0; vec < 2; ++vec) {
+      const LnPlan k = ln_plan(INT64_MAX, d, es, vec != 0, true, di);
+      const int64_t cap = (int64_t)di.sm_count * (k.vpl ? k.per_sm : kLnBlocksPerSm);
+      const int64_t n = T < cap ? T : cap;
+      grid = n > grid ? n : grid;
+    }
   return grid * 2 * d * 4;
 }
 
@@ -584,14 +617,14 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a) {
   const int es = bf16 ? 2 : 4, V = 16 / es;
   const bool vec = a.d % V == 0 && vec_rows(a.x, a.xs, V) && (!a.out || vec_rows(a.out, a.os, V)) && (!a.backward || vec_rows(a.dy, a.dys, V)) &&
                    ((reinterpret_cast<uintptr_t>(a.gain) | reinterpret_cast<uintptr_t>(a.bias)) & 15) == 0;
-  const LnPlan k = ln_plan(a.T, a.d, es, vec, a.backward, di.sm_count);
+  const LnPlan k = ln_plan(a.T, a.d, es, vec, a.backward, di);
   int grid;
   if (k.vpl) {
     p.warps = k.warps;
-    const int64_t rows = k.warps == 1 ? k.threads / 32 : 1, need = (a.T + rows - 1) / rows;  // of a CTA at a time
-    const int64_t cap = (int64_t)di.sm_count * ln_blocks_per_sm(k, a.backward);
+    const int64_t need = (a.T + k.groups - 1) / k.groups, cap = (int64_t)di.sm_count * k.per_sm;
     grid = (int)(need < cap ? need : cap);
-    e = bf16 ? launch_rows<bf16_t>(a, p, k, vec, grid) : launch_rows<float>(a, p, k, vec, grid);
+    const int most = di.max_smem_optin - 1024;  // (beside the sums' buffers)
+    e = bf16 ? launch_rows<bf16_t>(a, p, k, vec, grid, most) : launch_rows<float>(a, p, k, vec, grid, most);
   } else {
     const int64_t cap = (int64_t)di.sm_count * kLnBlocksPerSm;
     grid = (int)(a.T < cap ? a.T : cap);
