@@ -212,35 +212,34 @@ struct Segment {
   }
 };
 
-// Sums of N values (up to 4) over a row's warps, the same in every thread of
+// Sums of N values (up to 8) over a row's warps, the same in every thread of
 // the row, in a fixed order.  Several values are summed over a warp by halves:
 // after the first exchanges each lane carries one of them.  One barrier: the
 // caller alternates between two buffers.
 template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int warps, int group, int warp, int lane) {
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[8], int warps, int group, int warp, int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
-  constexpr int kLanes = N == 1 ? 32 : N == 2 ? 16 : 8;  // that end up with the same value
-  float s;
-  if constexpr (N == 1) {
-    s = v[0];
-  } else if constexpr (N == 2) {
-    const bool hi = lane & 16;
-    s = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], 16);
-  } else {
-    const bool hi = lane & 16, hi2 = lane & 8;
-    const float v3 = N > 3 ? v[N - 1] : 0.f;
-    const float a = (hi ? v[2] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[2], 16);
-    const float b = (hi ? v3 : v[1]) + __shfl_xor_sync(kAll, hi ? v[1] : v3, 16);
-    s = (hi2 ? b : a) + __shfl_xor_sync(kAll, hi2 ? a : b, 8);
+  constexpr int kValues = N == 1 ? 1 : N == 2 ? 2 : N <= 4 ? 4 : 8, kLanes = 32 / kValues;  // lanes that end up with the same value
+  float a[kValues];
+#pragma unroll
+  for (int i = 0; i < kValues; ++i) a[i] = i < N ? v[i < N ? i : 0] : 0.f;
+#pragma unroll
+  for (int n = kValues / 2, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < n; ++i) a[i] = (hi ? a[i + n] : a[i]) + __shfl_xor_sync(kAll, hi ? a[i] : a[i + n], o);
   }
+  float s = a[0];
 #pragma unroll
   for (int o = kLanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   if (warps > 1) {
     const int which = lane / kLanes, w = lane % kLanes;
     if (w == 0) red[warp][which] = s;
     named_barrier_sync(1 + group, 32 * warps);
-    s = w < warps ? red[w & (kLnMaxWarps - 1)][which] : 0.f;
-    if (kLanes < kLnMaxWarps && w + kLanes < warps) s += red[(w + kLanes) & (kLnMaxWarps - 1)][which];
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLnMaxWarps; i += kLanes)
+      if (w + i < warps) s += red[w + i][which];
 #pragma unroll
     for (int o = (kLanes < kLnMaxWarps ? kLanes : kLnMaxWarps) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
   }
@@ -248,11 +247,15 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[4], int war
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kAll, s, i * kLanes);
 }
 
-// a vector of fp32 into shared memory by the whole CTA (null: `none`)
-template <typename S>
+// a vector of fp32 into shared memory by the whole CTA (null: `none`); VEC: on
+// its way, in the caller's next group of copies
+template <typename S, bool VEC>
 __device__ __forceinline__ void stage(float* to, const float* v, float none, int d) {
-#pragma unroll 4
-  for (int c = threadIdx.x; c < d; c += blockDim.x) to[S::place(c, d)] = v ? __ldg(v + c) : none;
+  if (VEC && v) {
+    for (int c = 4 * threadIdx.x; c < d; c += 4 * blockDim.x) cp_async16(smem_addr(to + S::place(c, d)), v + c, true);
+  } else {
+    for (int c = threadIdx.x; c < d; c += blockDim.x) to[S::place(c, d)] = v ? __ldg(v + c) : none;
+  }
 }
 
 // Rows that fit registers, read once and then taken from there three times.  A
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
   extern __shared__ __align__(16) unsigned char dyn[];  // gain, bias; VEC: [held][threads] vectors
-  __shared__ __align__(16) float red[2][kLnMaxWarps][4];
+  __shared__ __align__(16) float red[2][kLnMaxWarps][8];
   const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
   const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
   const S seg(warp, warps, lane, p.d);
@@ -285,9 +288,12 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
     }
     cp_async_commit();
   };
-  if constexpr (VEC) fetch(t);
-  stage<S>(gains, p.gain, 1.f, p.d);
-  stage<S>(biases, p.bias, 0.f, p.d);
+  stage<S, VEC>(gains, p.gain, 1.f, p.d);
+  stage<S, VEC>(biases, p.bias, 0.f, p.d);
+  if constexpr (VEC) {
+    fetch(t);
+    cp_async_wait<0>();
+  }
   __syncthreads();
   gains += S::place(seg.at, p.d);
   biases += S::place(seg.at, p.d);
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
     row_sums<2>(s2, red[1] + group * warps, warps, group, warp, lane);
     const float delta = s2[0] * p.inv_d;
     const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
-    const uint64_t minus_m = f2_both(-m), minus_delta = f2_both(-delta), r2 = f2_both(rstd);
+    const uint64_t minus_m = f2_both(-m), r2 = f2_both(rstd), shift = f2_both(-delta * rstd);
     T* out = static_cast<T*>(p.out) + t * p.os + seg.at;
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
@@ -340,21 +346,22 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
         seg.load_f32(biases, i, p.d, bias);
         S::unpack(x[i], f);
 #pragma unroll
-        for (int k = 0; k < P; ++k) f[k] = f2_fma(f2_mul(f2_add(f2_add(f[k], minus_m), minus_delta), r2), gain[k], bias[k]);
+        for (int k = 0; k < P; ++k) f[k] = f2_fma(f2_fma(f2_add(f[k], minus_m), r2, shift), gain[k], bias[k]);
         seg.store(out, i, f);
       }
   }
 }
 
 // Its backward: a lane also keeps its channels' sums of dy h and dy over its
-// group's rows.
-constexpr int kLnAhead = 2;  // rows on their way
-template <typename T, int VPL, bool VEC>
+// group's rows, which are taken ROWS at a time (their sums cross the warps
+// together).
+constexpr int kLnAhead = 2;  // takes of rows on their way
+template <typename T, int VPL, int ROWS, bool VEC>
 __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const __grid_constant__ LnParams p) {
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
-  extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [kLnAhead][held][x, dy][threads] vectors; at the end: sums
-  __shared__ __align__(16) float red[2][kLnMaxWarps][4];
+  extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [kLnAhead][ROWS][held][x, dy][threads] vectors; at the end: sums
+  __shared__ __align__(16) float red[2][kLnMaxWarps][8];
   const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
   const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
   const S seg(warp, warps, lane, p.d);
@@ -365,30 +372,32 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   const T* DY = static_cast<const T*>(p.dy) + seg.at;
   const long long step = (long long)gridDim.x * groups;
   long long t = (long long)blockIdx.x * groups + group, ahead_t = t;
-  const uint32_t vec = nthreads * 16, ring = smem_addr(gains + (p.d + 3 & ~3)) + threadIdx.x * 16, row_bytes = 2 * seg.held * vec;
+  const uint32_t vec = nthreads * 16, ring = smem_addr(gains + (p.d + 3 & ~3)) + threadIdx.x * 16, take_bytes = ROWS * 2 * seg.held * vec;
   int ahead_slot = 0, slot = 0;
   auto fetch = [&] {
-    if (ahead_t < p.T) {
-      const T* xr = X + ahead_t * p.xs;
-      const T* dr = DY + ahead_t * p.dys;
-      uint32_t to = ring + ahead_slot * row_bytes;
+    uint32_t to = ring + ahead_slot * take_bytes;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r, ahead_t += step) {
+      const bool row = ahead_t < p.T;
+      const T* xr = X + (row ? ahead_t * p.xs : 0);
+      const T* dr = DY + (row ? ahead_t * p.dys : 0);
 #pragma unroll
       for (int i = 0; i < VPL; ++i, to += 2 * vec) {
         if (i >= seg.held) break;
-        const bool in = seg.has(i);
+        const bool in = row && seg.has(i);
         cp_async16(to, in ? xr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
         cp_async16(to + vec, in ? dr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
       }
     }
-    ahead_t += step;
     ahead_slot = ahead_slot + 1 == kLnAhead ? 0 : ahead_slot + 1;
-    cp_async_commit();  // a group for every row, there or not
+    cp_async_commit();
   };
+  stage<S, VEC>(gains, p.gain, 1.f, p.d);
   if constexpr (VEC) {
 #pragma unroll
     for (int i = 0; i < kLnAhead; ++i) fetch();
+    cp_async_wait<kLnAhead - 1>();  // gain and the first rows
   }
-  stage<S>(gains, p.gain, 1.f, p.d);
   __syncthreads();
   gains += S::place(seg.at, p.d);
   uint64_t dg[VPL][P], db[VPL][P];
@@ -396,77 +405,115 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   for (int i = 0; i < VPL; ++i)
 #pragma unroll
     for (int k = 0; k < P; ++k) dg[i][k] = db[i][k] = 0;
-  for (; t < p.T; t += step) {
-    uint4 x[VPL], dy[VPL];
+  for (; t < p.T; t += ROWS * step) {
+    uint4 x[ROWS][VPL], dy[ROWS][VPL];
     if constexpr (VEC) {
       cp_async_wait<kLnAhead - 1>();
-      uint32_t at = ring + slot * row_bytes;
+      uint32_t at = ring + slot * take_bytes;
 #pragma unroll
-      for (int i = 0; i < VPL; ++i, at += 2 * vec) {
-        if (i >= seg.held) break;
-        x[i] = ld_shared_v4(at);
-        dy[i] = ld_shared_v4(at + vec);
-      }
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i, at += 2 * vec) {
+          if (i >= seg.held) break;
+          x[r][i] = ld_shared_v4(at);
+          dy[r][i] = ld_shared_v4(at + vec);
+        }
       slot = slot + 1 == kLnAhead ? 0 : slot + 1;
       fetch();  // into the slot just read
     } else {
 #pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const bool row = ROWS == 1 || t + r * step < p.T;
+          x[r][i] = row ? seg.load(X + (t + r * step) * p.xs, i) : make_uint4(0, 0, 0, 0);
+          dy[r][i] = row ? seg.load(DY + (t + r * step) * p.dys, i) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    uint64_t f[P], g[P], gain[P];
+    float s1[2 * ROWS], s2[3 * ROWS], m[ROWS];
+    {
+      uint64_t sx[ROWS], sn[ROWS];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) sx[r] = sn[r] = 0;
+#pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        x[i] = seg.load(X + t * p.xs, i);
-        dy[i] = seg.load(DY + t * p.dys, i);
+        if (VEC && !seg.has(i)) continue;
+        seg.load_f32(gains, i, p.d, gain);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          S::unpack(x[r][i], f);
+          S::unpack(dy[r][i], g);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            sx[r] = f2_add(sx[r], f[k]);
+            sn[r] = f2_fma(g[k], gain[k], sn[r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        s1[2 * r] = f2_hsum(sx[r]);
+        s1[2 * r + 1] = f2_hsum(sn[r]);
       }
     }
-    uint64_t sx = 0, sn = 0, f[P], g[P], gain[P];
+    row_sums<2 * ROWS>(s1, red[0] + group * warps, warps, group, warp, lane);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, i, p.d, gain);
-      S::unpack(x[i], f);
-      S::unpack(dy[i], g);
+    for (int r = 0; r < ROWS; ++r) m[r] = s1[2 * r] * p.inv_d;
+    {
+      uint64_t sz[ROWS], sq[ROWS], sw[ROWS];
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        sx = f2_add(sx, f[k]);
-        sn = f2_fma(g[k], gain[k], sn);
+      for (int r = 0; r < ROWS; ++r) sz[r] = sq[r] = sw[r] = 0;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        if (VEC && !seg.has(i)) continue;
+        seg.load_f32(gains, i, p.d, gain);
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          seg.center(x[r][i], f2_both(-m[r]), i, f);
+          S::unpack(dy[r][i], g);
+#pragma unroll
+          for (int k = 0; k < P; ++k) {
+            sz[r] = f2_add(sz[r], f[k]);
+            sq[r] = f2_fma(f[k], f[k], sq[r]);
+            sw[r] = f2_fma(f2_mul(g[k], gain[k]), f[k], sw[r]);
+          }
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        s2[3 * r] = f2_hsum(sz[r]);
+        s2[3 * r + 1] = f2_hsum(sq[r]);
+        s2[3 * r + 2] = f2_hsum(sw[r]);
       }
     }
-    float s1[2] = {f2_hsum(sx), f2_hsum(sn)};
-    row_sums<2>(s1, red[0] + group * warps, warps, group, warp, lane);
-    const float m = s1[0] * p.inv_d;
-    uint64_t sz = 0, sq = 0, sw = 0;
+    row_sums<3 * ROWS>(s2, red[1] + group * warps, warps, group, warp, lane);
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, i, p.d, gain);
-      seg.center(x[i], f2_both(-m), i, f);
-      S::unpack(dy[i], g);
+    for (int r = 0; r < ROWS; ++r) {
+      const long long tr = t + r * step;
+      if (r > 0 && tr >= p.T) break;
+      const float delta = s2[3 * r] * p.inv_d;
+      const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[3 * r + 1] * p.inv_d), 0.f) + p.eps);
+      const float mn = s1[2 * r + 1] * p.inv_d;
+      const float mh = (s2[3 * r + 2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
+      // h = (x - m) r - delta r,  dx = (n r - mn r) - h mh r
+      const uint64_t minus_m = f2_both(-m[r]), r2 = f2_both(rstd), shift = f2_both(-delta * rstd), n0 = f2_both(-mn * rstd), h0 = f2_both(-mh * rstd);
+      T* out = static_cast<T*>(p.out) + (p.out ? tr * p.os + seg.at : 0);
 #pragma unroll
-      for (int k = 0; k < P; ++k) {
-        sz = f2_add(sz, f[k]);
-        sq = f2_fma(f[k], f[k], sq);
-        sw = f2_fma(f2_mul(g[k], gain[k]), f[k], sw);
+      for (int i = 0; i < VPL; ++i) {
+        if (VEC && !seg.has(i)) continue;
+        seg.load_f32(gains, i, p.d, gain);
+        S::unpack(x[r][i], f);
+        S::unpack(dy[r][i], g);
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+          const uint64_t h = f2_fma(f2_add(f[k], minus_m), r2, shift);
+          dg[i][k] = f2_fma(g[k], h, dg[i][k]);
+          db[i][k] = f2_add(db[i][k], g[k]);
+          f[k] = f2_fma(h, h0, f2_fma(f2_mul(g[k], gain[k]), r2, n0));
+        }
+        if (p.out) seg.store(out, i, f);
       }
-    }
-    float s2[3] = {f2_hsum(sz), f2_hsum(sq), f2_hsum(sw)};
-    row_sums<3>(s2, red[1] + group * warps, warps, group, warp, lane);
-    const float delta = s2[0] * p.inv_d;
-    const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[1] * p.inv_d), 0.f) + p.eps);
-    const float mn = s1[1] * p.inv_d;
-    const float mh = (s2[2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
-    T* out = static_cast<T*>(p.out) + (p.out ? t * p.os + seg.at : 0);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-      if (VEC && !seg.has(i)) continue;
-      seg.load_f32(gains, i, p.d, gain);
-      S::unpack(x[i], f);
-      S::unpack(dy[i], g);
-#pragma unroll
-      for (int k = 0; k < P; ++k) {
-        const uint64_t h = f2_mul(f2_add(f2_add(f[k], f2_both(-m)), f2_both(-delta)), f2_both(rstd));
-        dg[i][k] = f2_fma(g[k], h, dg[i][k]);
-        db[i][k] = f2_add(db[i][k], g[k]);
-        f[k] = f2_mul(f2_add(f2_fma(h, f2_both(-mh), f2_mul(g[k], gain[k])), f2_both(-mn)), f2_both(rstd));
-      }
-      if (p.out) seg.store(out, i, f);
     }
   }
   if (!p.part) return;
@@ -527,23 +574,23 @@ struct LnPlan {
   int vpl, warps, groups, smem, per_sm;
 };
 LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceInfo& di) {
-  constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[2] = {1, 4};
-  const int V = 16 / es, n = backward ? 2 : 3;
+  constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[3] = {1, 2, 4};
+  const int V = 16 / es, n = 3;
   const int* vpl = backward ? kBackward : vec ? kForwardVec : kForward;
   // few rows: each over as many warps as it feeds, a lane's channels few;
   // many: a row in as few warps as hold it, so that its sums cross few of them
   const bool few = T <= 2 * di.sm_count;
   for (int i = 0; i < n; ++i) {
     const int per_warp = 32 * vpl[i] * V, warps = (d + per_warp - 1) / per_warp;
-    if (warps > kLnMaxWarps || (!few && i + 1 < n && warps > 1)) continue;
+    if (warps > kLnMaxWarps || (!few && i + 1 < n && warps > 1 && !(backward && vpl[i] == 2))) continue;
     const int held = (d + 32 * V * warps - 1) / (32 * V * warps);
     for (int groups = few ? 1 : kLnMaxWarps / warps; groups >= 1; --groups) {
       const int64_t vectors = (int64_t)((d + 3) / 4) * 16 * (backward ? 1 : 2);
-      const int64_t ring = vec ? (int64_t)32 * warps * groups * held * 16 * (backward ? 2 * kLnAhead : 1) : 0;
+      const int64_t ring = vec ? (int64_t)32 * warps * groups * held * 16 * (backward ? (vpl[i] == 2 ? 4 : 2) * kLnAhead : 1) : 0;
       const int64_t sums = backward && groups > 1 ? (int64_t)groups * 2 * d * 4 : 0;
       const int64_t smem = vectors + ring > sums ? vectors + ring : sums;
       if (smem + 1024 > di.max_smem_optin) continue;
-      const bool one = vpl[i] == (backward ? 4 : 16) || 2 * smem + 4096 > di.max_smem_optin;
+      const bool one = vpl[i] >= (backward ? 2 : 16) || 2 * (smem + 512 + 1024) > di.max_smem_optin + 1024;
       return {vpl[i], warps, groups, (int)smem, one ? 1 : 2};
     }
   }
@@ -560,16 +607,21 @@ cudaError_t launch_forward(const LayerNormArgs& a, const LnParams& p, const LnPl
 template <typename T, int VPL, bool VEC>
 cudaError_t launch_backward(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, int grid, int most) {
   static SmemOptIn opt;
-  const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_backward_kernel<T, VPL, VEC>), most);
+  const cudaError_t e = opt.ensure(reinterpret_cast<const void*>(ln_row_backward_kernel<T, VPL, VPL == 2 ? 2 : 1, VEC>), most);
   if (e != cudaSuccess) return e;
-  return launch_kernel(ln_row_backward_kernel<T, VPL, VEC>, dim3(grid), dim3(32 * k.warps * k.groups), k.smem, a.stream, p);
+  return launch_kernel(ln_row_backward_kernel<T, VPL, VPL == 2 ? 2 : 1, VEC>, dim3(grid), dim3(32 * k.warps * k.groups), k.smem, a.stream, p);
 }
 
 template <typename T>
 cudaError_t launch_rows(const LayerNormArgs& a, const LnParams& p, const LnPlan& k, bool vec, int grid, int most) {
   if (a.backward) {
-    if (vec) return k.vpl == 1 ? launch_backward<T, 1, true>(a, p, k, grid, most) : launch_backward<T, 4, true>(a, p, k, grid, most);
-    return k.vpl == 1 ? launch_backward<T, 1, false>(a, p, k, grid, most) : launch_backward<T, 4, false>(a, p, k, grid, most);
+    if (vec)
+      return k.vpl == 1   ? launch_backward<T, 1, true>(a, p, k, grid, most)
+             : k.vpl == 2 ? launch_backward<T, 2, true>(a, p, k, grid, most)
+                          : launch_backward<T, 4, true>(a, p, k, grid, most);
+    return k.vpl == 1   ? launch_backward<T, 1, false>(a, p, k, grid, most)
+           : k.vpl == 2 ? launch_backward<T, 2, false>(a, p, k, grid, most)
+                        : launch_backward<T, 4, false>(a, p, k, grid, most);
   }
   switch (k.vpl) {
     case 1: return launch_forward<T, 1, false>(a, p, k, grid, most);
