@@ -546,9 +546,9 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 }
 
 // gain and bias gradients: the CTAs' partial rows, summed in order (32
-// channels x 32 interleaved runs of rows per CTA, whose loads do not wait for
+// channels x 16 interleaved runs of rows per CTA, whose loads do not wait for
 // one another; blockIdx.y: gain or bias)
-constexpr int kLnRuns = 32;
+constexpr int kLnRuns = 16;
 __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* part, int blocks, int d, float* dgain, float* dbias) {
   __shared__ float sums[kLnRuns][33];
   const int lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane, r = threadIdx.x >> 5;
@@ -558,13 +558,18 @@ __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* par
   if (!out) return;
   float s = 0.f;
   if (c < d) {
-#pragma unroll 8
-    for (int b = r; b < blocks; b += kLnRuns) s += part[((long long)b * 2 + blockIdx.y) * d + c];
+    const float* at = part + blockIdx.y * (long long)d + c;
+#pragma unroll 10
+    for (int b = r; b < blocks; b += kLnRuns) s += at[b * 2LL * d];
   }
   sums[r][lane] = s;
   __syncthreads();
-  s = warp_sum(sums[lane][r]);  // warp r: channel r of the CTA's
-  if (lane == 0 && blockIdx.x * 32 + r < d) out[blockIdx.x * 32 + r] = s;
+  if (r == 0 && c < d) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kLnRuns; ++i) s += sums[i][lane];
+    out[c] = s;
+  }
 }
 
 // How a call's rows are held: vectors to a lane, warps to a row, rows of a CTA
