@@ -120,9 +120,12 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in = true) {
   const int bytes = in ? 16 : 0;  // none: zeros
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void st_shared_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -168,22 +171,24 @@ struct Segment {
 #pragma unroll
     for (int k = 0; k < P; ++k) f[k] = f2_pack(t[2 * k], t[2 * k + 1]);
   }
+  template <bool MASK>
   __device__ __forceinline__ void store(T* y, int i, const uint64_t (&f)[P]) const {
     float t[V];
 #pragma unroll
     for (int k = 0; k < P; ++k) f2_unpack(f[k], t[2 * k], t[2 * k + 1]);
     if constexpr (VEC) {
-      __stcs(reinterpret_cast<uint4*>(y + offset(i, 0)), Vec16<T>::pack(t));
+      if (!MASK || has(i)) __stcs(reinterpret_cast<uint4*>(y + offset(i, 0)), Vec16<T>::pack(t));
     } else {
 #pragma unroll
       for (int k = 0; k < V; ++k)
-        if (has(i, k)) store_elem(y + offset(i, k), t[k]);
+        if (!MASK || has(i, k)) store_elem(y + offset(i, k), t[k]);
     }
   }
   // A vector of fp32 in shared memory, as the lanes read it without conflicts:
   // the first four channels of every vector, then the other four (V = 8).
   static __device__ __forceinline__ int place(int c, int d) { return VEC && V == 8 ? (c >> 2 & 1) * (d >> 1) + (c >> 3) * 4 + (c & 3) : c; }
-  // the lane's channels of it; `first`: place(at)
+  // the lane's channels of it; `first`: at place(at).  (Where a lane has no
+  // channel it reads what lies there, inside the CTA's shared memory.)
   __device__ __forceinline__ void load_f32(const float* first, int i, int d, uint64_t (&f)[P]) const {
     if constexpr (VEC) {
 #pragma unroll
@@ -197,13 +202,14 @@ struct Segment {
       for (int k = 0; k < P; ++k) f[k] = f2_pack(has(i, 2 * k) ? first[offset(i, 2 * k)] : 0.f, has(i, 2 * k + 1) ? first[offset(i, 2 * k + 1)] : 0.f);
     }
   }
-  // x - m where there is a channel, else 0
+  // x - m where there is a channel, else 0 (MASK: some lanes have none here)
+  template <bool MASK>
   __device__ __forceinline__ void center(const uint4& v, uint64_t minus_m, int i, uint64_t (&z)[P]) const {
     unpack(v, z);
 #pragma unroll
     for (int k = 0; k < P; ++k) {
       z[k] = f2_add(z[k], minus_m);
-      if constexpr (!VEC) {
+      if constexpr (MASK) {
         float t[2];
         f2_unpack(z[k], t[0], t[1]);
         z[k] = f2_pack(has(i, 2 * k) ? t[0] : 0.f, has(i, 2 * k + 1) ? t[1] : 0.f);
@@ -252,7 +258,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[8], int war
 template <typename S, bool VEC>
 __device__ __forceinline__ void stage(float* to, const float* v, float none, int d) {
   if (VEC && v) {
-    for (int c = 4 * threadIdx.x; c < d; c += 4 * blockDim.x) cp_async16(smem_addr(to + S::place(c, d)), v + c, true);
+    for (int c = 4 * threadIdx.x; c < d; c += 4 * blockDim.x) cp_async16(smem_addr(to + S::place(c, d)), v + c);
   } else {
     for (int c = threadIdx.x; c < d; c += blockDim.x) to[S::place(c, d)] = v ? __ldg(v + c) : none;
   }
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
       if (i < seg.held && (!VEC || seg.has(i))) {
-        seg.center(x[i], f2_both(-m), i, f);
+        seg.template center<!VEC>(x[i], f2_both(-m), i, f);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           sz = f2_add(sz, f[k]);
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
         S::unpack(x[i], f);
 #pragma unroll
         for (int k = 0; k < P; ++k) f[k] = f2_fma(f2_fma(f2_add(f[k], minus_m), r2, shift), gain[k], bias[k]);
-        seg.store(out, i, f);
+        seg.template store<!VEC>(out, i, f);
       }
   }
 }
@@ -355,12 +361,13 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
 // Its backward: a lane also keeps its channels' sums of dy h and dy over its
 // group's rows, which are taken ROWS at a time (their sums cross the warps
 // together).
-constexpr int kLnAhead = 2;  // takes of rows on their way
+constexpr int kLnTakes = 3;  // of the ring: one at work, two on their way
 template <typename T, int VPL, int ROWS, bool VEC>
 __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const __grid_constant__ LnParams p) {
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
-  extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [kLnAhead][ROWS][held][x, dy][threads] vectors; at the end: sums
+  constexpr uint32_t kRow = 2 * VPL * 512, kTake = ROWS * kRow;  // of a warp's ring
+  extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [warp][kLnTakes][ROWS][x, dy][VPL][lane] vectors; at the end: sums
   __shared__ __align__(16) float red[2][kLnMaxWarps][8];
   const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
   const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
@@ -368,35 +375,47 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   float* gains = reinterpret_cast<float*>(dyn);
   pdl_wait();
   pdl_trigger();
-  const T* X = static_cast<const T*>(p.x) + seg.at;
-  const T* DY = static_cast<const T*>(p.dy) + seg.at;
   const long long step = (long long)gridDim.x * groups;
   long long t = (long long)blockIdx.x * groups + group, ahead_t = t;
-  const uint32_t vec = nthreads * 16, ring = smem_addr(gains + (p.d + 3 & ~3)) + threadIdx.x * 16, take_bytes = ROWS * 2 * seg.held * vec;
-  int ahead_slot = 0, slot = 0;
+  // the next rows to load and to write
+  const T* xr = static_cast<const T*>(p.x) + t * p.xs + seg.at;
+  const T* dr = static_cast<const T*>(p.dy) + t * p.dys + seg.at;
+  T* out = static_cast<T*>(p.out) + (p.out ? t * p.os + seg.at : 0);
+  const long long x_step = step * p.xs, d_step = step * p.dys, out_step = p.out ? step * p.os : 0;
+  const uint32_t ring = smem_addr(gains + (p.d + 3 & ~3)) + (threadIdx.x >> 5) * (kLnTakes * kTake) + lane * 16;
+  uint32_t ahead_slot = 0, slot = 0;
+  if constexpr (VEC) {  // what no copy fills stays zero
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (!seg.has(i))
+        for (int r = 0; r < kLnTakes * ROWS; ++r) {
+          st_shared_zero(ring + r * kRow + i * 512);
+          st_shared_zero(ring + r * kRow + (VPL + i) * 512);
+        }
+  }
   auto fetch = [&] {
-    uint32_t to = ring + ahead_slot * take_bytes;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r, ahead_t += step) {
-      const bool row = ahead_t < p.T;
-      const T* xr = X + (row ? ahead_t * p.xs : 0);
-      const T* dr = DY + (row ? ahead_t * p.dys : 0);
+    for (int r = 0; r < ROWS; ++r) {
+      if (ahead_t < p.T) {
 #pragma unroll
-      for (int i = 0; i < VPL; ++i, to += 2 * vec) {
-        if (i >= seg.held) break;
-        const bool in = row && seg.has(i);
-        cp_async16(to, in ? xr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
-        cp_async16(to + vec, in ? dr + S::offset(i, 0) : static_cast<const T*>(p.x), in);
+        for (int i = 0; i < VPL; ++i)
+          if (seg.has(i)) {
+            cp_async16(ring + ahead_slot + r * kRow + i * 512, xr + S::offset(i, 0));
+            cp_async16(ring + ahead_slot + r * kRow + (VPL + i) * 512, dr + S::offset(i, 0));
+          }
       }
+      ahead_t += step;
+      xr += x_step;
+      dr += d_step;
     }
-    ahead_slot = ahead_slot + 1 == kLnAhead ? 0 : ahead_slot + 1;
+    ahead_slot = ahead_slot + kTake == kLnTakes * kTake ? 0 : ahead_slot + kTake;
     cp_async_commit();
   };
   stage<S, VEC>(gains, p.gain, 1.f, p.d);
   if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < kLnAhead; ++i) fetch();
-    cp_async_wait<kLnAhead - 1>();  // gain and the first rows
+    for (int i = 0; i < kLnTakes - 1; ++i) fetch();
+    cp_async_wait<kLnTakes - 2>();  // gain and the first rows
   }
   __syncthreads();
   gains += S::place(seg.at, p.d);
@@ -406,105 +425,100 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
     for (int k = 0; k < P; ++k) dg[i][k] = db[i][k] = 0;
   for (; t < p.T; t += ROWS * step) {
-    uint4 x[ROWS][VPL], dy[ROWS][VPL];
+    // rows are read from the ring again for every pass (their registers are the sums'); single channels stay in registers
+    uint4 held_x[VEC ? 1 : ROWS][VEC ? 1 : VPL], held_dy[VEC ? 1 : ROWS][VEC ? 1 : VPL];
+    auto x = [&](int r, int i) {
+      if constexpr (VEC) return ld_shared_v4(ring + slot + r * kRow + i * 512);
+      else return held_x[r][i];
+    };
+    auto dy = [&](int r, int i) {
+      if constexpr (VEC) return ld_shared_v4(ring + slot + r * kRow + (VPL + i) * 512);
+      else return held_dy[r][i];
+    };
     if constexpr (VEC) {
-      cp_async_wait<kLnAhead - 1>();
-      uint32_t at = ring + slot * take_bytes;
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-        for (int i = 0; i < VPL; ++i, at += 2 * vec) {
-          if (i >= seg.held) break;
-          x[r][i] = ld_shared_v4(at);
-          dy[r][i] = ld_shared_v4(at + vec);
-        }
-      slot = slot + 1 == kLnAhead ? 0 : slot + 1;
-      fetch();  // into the slot just read
+      fetch();  // into the slot of the last take
+      cp_async_wait<kLnTakes - 1>();
     } else {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
+      for (int r = 0; r < ROWS; ++r) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
           const bool row = ROWS == 1 || t + r * step < p.T;
-          x[r][i] = row ? seg.load(X + (t + r * step) * p.xs, i) : make_uint4(0, 0, 0, 0);
-          dy[r][i] = row ? seg.load(DY + (t + r * step) * p.dys, i) : make_uint4(0, 0, 0, 0);
+          held_x[r][i] = row ? seg.load(xr, i) : make_uint4(0, 0, 0, 0);
+          held_dy[r][i] = row ? seg.load(dr, i) : make_uint4(0, 0, 0, 0);
         }
+        xr += x_step;
+        dr += d_step;
+      }
     }
+    // (behind the last row a take goes through the motions with what its slot held)
     uint64_t f[P], g[P], gain[P];
-    float s1[2 * ROWS], s2[3 * ROWS], m[ROWS];
+    float s1[ROWS], s2[4 * ROWS], m[ROWS];
     {
-      uint64_t sx[ROWS], sn[ROWS];
+      uint64_t sx[ROWS];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) sx[r] = sn[r] = 0;
+      for (int r = 0; r < ROWS; ++r) sx[r] = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (VEC && !seg.has(i)) continue;
-        seg.load_f32(gains, i, p.d, gain);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          S::unpack(x[r][i], f);
-          S::unpack(dy[r][i], g);
+          S::unpack(x(r, i), f);
 #pragma unroll
-          for (int k = 0; k < P; ++k) {
-            sx[r] = f2_add(sx[r], f[k]);
-            sn[r] = f2_fma(g[k], gain[k], sn[r]);
-          }
+          for (int k = 0; k < P; ++k) sx[r] = f2_add(sx[r], f[k]);
         }
       }
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) {
-        s1[2 * r] = f2_hsum(sx[r]);
-        s1[2 * r + 1] = f2_hsum(sn[r]);
-      }
+      for (int r = 0; r < ROWS; ++r) s1[r] = f2_hsum(sx[r]);
     }
-    row_sums<2 * ROWS>(s1, red[0] + group * warps, warps, group, warp, lane);
+    row_sums<ROWS>(s1, red[0] + group * warps, warps, group, warp, lane);
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) m[r] = s1[2 * r] * p.inv_d;
+    for (int r = 0; r < ROWS; ++r) m[r] = s1[r] * p.inv_d;
     {
-      uint64_t sz[ROWS], sq[ROWS], sw[ROWS];
+      uint64_t sz[ROWS], sq[ROWS], sn[ROWS], sw[ROWS];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) sz[r] = sq[r] = sw[r] = 0;
+      for (int r = 0; r < ROWS; ++r) sz[r] = sq[r] = sn[r] = sw[r] = 0;
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (VEC && !seg.has(i)) continue;
+        if (VPL > 1 && i >= seg.held) break;
         seg.load_f32(gains, i, p.d, gain);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          seg.center(x[r][i], f2_both(-m[r]), i, f);
-          S::unpack(dy[r][i], g);
+          seg.template center<true>(x(r, i), f2_both(-m[r]), i, f);
+          S::unpack(dy(r, i), g);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
+            const uint64_t n = f2_mul(g[k], gain[k]);
             sz[r] = f2_add(sz[r], f[k]);
             sq[r] = f2_fma(f[k], f[k], sq[r]);
-            sw[r] = f2_fma(f2_mul(g[k], gain[k]), f[k], sw[r]);
+            sn[r] = f2_add(sn[r], n);
+            sw[r] = f2_fma(n, f[k], sw[r]);
           }
         }
       }
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        s2[3 * r] = f2_hsum(sz[r]);
-        s2[3 * r + 1] = f2_hsum(sq[r]);
-        s2[3 * r + 2] = f2_hsum(sw[r]);
+        s2[4 * r] = f2_hsum(sz[r]);
+        s2[4 * r + 1] = f2_hsum(sq[r]);
+        s2[4 * r + 2] = f2_hsum(sw[r]);
+        s2[4 * r + 3] = f2_hsum(sn[r]);
       }
     }
-    row_sums<3 * ROWS>(s2, red[1] + group * warps, warps, group, warp, lane);
+    row_sums<4 * ROWS>(s2, red[1] + group * warps, warps, group, warp, lane);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const long long tr = t + r * step;
-      if (r > 0 && tr >= p.T) break;
-      const float delta = s2[3 * r] * p.inv_d;
-      const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[3 * r + 1] * p.inv_d), 0.f) + p.eps);
-      const float mn = s1[2 * r + 1] * p.inv_d;
-      const float mh = (s2[3 * r + 2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
+      if (r > 0 && t + r * step >= p.T) break;
+      const float delta = s2[4 * r] * p.inv_d;
+      const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[4 * r + 1] * p.inv_d), 0.f) + p.eps);
+      const float mn = s2[4 * r + 3] * p.inv_d;
+      const float mh = (s2[4 * r + 2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
       // h = (x - m) r - delta r,  dx = (n r - mn r) - h mh r
       const uint64_t minus_m = f2_both(-m[r]), r2 = f2_both(rstd), shift = f2_both(-delta * rstd), n0 = f2_both(-mn * rstd), h0 = f2_both(-mh * rstd);
-      T* out = static_cast<T*>(p.out) + (p.out ? tr * p.os + seg.at : 0);
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
-        if (VEC && !seg.has(i)) continue;
+        if (VPL > 1 && i >= seg.held) break;
         seg.load_f32(gains, i, p.d, gain);
-        S::unpack(x[r][i], f);
-        S::unpack(dy[r][i], g);
+        S::unpack(x(r, i), f);
+        S::unpack(dy(r, i), g);
 #pragma unroll
         for (int k = 0; k < P; ++k) {
           const uint64_t h = f2_fma(f2_add(f[k], minus_m), r2, shift);
@@ -512,9 +526,11 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
           db[i][k] = f2_add(db[i][k], g[k]);
           f[k] = f2_fma(h, h0, f2_fma(f2_mul(g[k], gain[k]), r2, n0));
         }
-        if (p.out) seg.store(out, i, f);
+        if (p.out) seg.template store<true>(out, i, f);
       }
+      out += out_step;
     }
+    slot = slot + kTake == kLnTakes * kTake ? 0 : slot + kTake;
   }
   if (!p.part) return;
   float* part = p.part + (long long)blockIdx.x * 2 * p.d;
@@ -591,7 +607,8 @@ LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceIn
     const int held = (d + 32 * V * warps - 1) / (32 * V * warps);
     for (int groups = few ? 1 : kLnMaxWarps / warps; groups >= 1; --groups) {
       const int64_t vectors = (int64_t)((d + 3) / 4) * 16 * (backward ? 1 : 2);
-      const int64_t ring = vec ? (int64_t)32 * warps * groups * held * 16 * (backward ? (vpl[i] == 2 ? 4 : 2) * kLnAhead : 1) : 0;
+      const int64_t vectors_of_warp = backward ? (vpl[i] == 2 ? 2 : 1) * 2 * vpl[i] * kLnTakes : held;
+      const int64_t ring = vec ? warps * groups * vectors_of_warp * 512 : 0;
       const int64_t sums = backward && groups > 1 ? (int64_t)groups * 2 * d * 4 : 0;
       const int64_t smem = vectors + ring > sums ? vectors + ring : sums;
       if (smem + 1024 > di.max_smem_optin) continue;
