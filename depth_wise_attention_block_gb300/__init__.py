@@ -14,6 +14,7 @@ over the sources [h_0, b_1 .. b_{n-1}, partial sum of the current block].
 from __future__ import annotations
 
 import ctypes
+from array import array
 from typing import Sequence
 
 import torch
@@ -962,16 +963,26 @@ def attnres_grad_clip_workspace_size() -> int:
     return _N.check(_N.lib.attnres_grad_clip_workspace_size(), "attnres_grad_clip_workspace_size")
 
 
-def _flat_ptrs(tensors, name: str, like, cur: int):
-    """Pointers of contiguous tensors on device `cur`, of the dtypes and sizes of `like`."""
-    for i, (t, g) in enumerate(zip(tensors, like)):
-        if not isinstance(t, torch.Tensor) or t.get_device() != cur or t.dtype is not g.dtype:
-            _where(t, f"{name}[{i}]", g.dtype if isinstance(g, torch.Tensor) else None, cur)
-        if not t.is_contiguous():
-            raise ValueError(f"{name}[{i}] must be contiguous")
-        if t is not g and t.numel() != g.numel():
-            raise ValueError(f"{name}[{i}] must hold {g.numel()} elements")
-    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
+_tensor_dtype, _tensor_bytes = torch.Tensor.dtype.__get__, torch.Tensor.nbytes.__get__
+
+
+def _flat_tensors(tensors: list, name: str, cur: int):
+    """(pointers, sizes in bytes, dtypes) of contiguous tensors on device `cur`.
+    A list of hundreds is looked through attribute by attribute, without a
+    Python frame per tensor."""
+    try:
+        ok = (all(map(torch.Tensor.is_contiguous, tensors)) and set(map(torch.Tensor.get_device, tensors)) <= {cur})
+    except TypeError:
+        ok = False
+    if not ok:
+        for i, t in enumerate(tensors):
+            _dev_ptr(t, f"{name}[{i}]")
+    return array("Q", map(torch.Tensor.data_ptr, tensors)), list(map(_tensor_bytes, tensors)), list(map(_tensor_dtype, tensors))
+
+
+def _c_array(a: array, kind):
+    """A C array over an array's own memory."""
+    return (kind * len(a)).from_buffer(a) if len(a) else (kind * 0)()
 
 
 def attnres_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torch.Tensor,
@@ -991,20 +1002,25 @@ def attnres_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torc
     n = len(grads)
     cur = _device_of(norm, "norm")
     max_norm = float(max_norm)
-    gp = _flat_ptrs(grads, "grads", grads, cur)
+    if not max_norm >= 0.0:
+        raise ValueError("max_norm must be >= 0")
+    ptrs, sizes, dts = _flat_tensors(grads, "grads", cur)
+    codes = array("i", map(_DT.__getitem__ if set(dts) <= _DT.keys() else dtype_code, dts))
+    numels = array("q", [size >> (1 if code == ATTNRES_BF16 else 2) for size, code in zip(sizes, codes)])
+    gp = _c_array(ptrs, ctypes.c_void_p)
     if outs is None:
         op = None if max_norm == float("inf") else gp
     else:
         outs = list(outs)
         if len(outs) != n:
             raise ValueError(f"{n} gradients, {len(outs)} outs")
-        op = _flat_ptrs(outs, "outs", grads, cur)
-    numels = (ctypes.c_int64 * n)(*[t.numel() for t in grads])
-    dtypes = (ctypes.c_int * n)(*[dtype_code(t.dtype) for t in grads])
-    if not max_norm >= 0.0:
-        raise ValueError("max_norm must be >= 0")
+        out_ptrs, out_sizes, out_dts = _flat_tensors(outs, "outs", cur)
+        if out_sizes != sizes or out_dts != dts:
+            i = next(i for i in range(n) if out_sizes[i] != sizes[i] or out_dts[i] != dts[i])
+            raise (TypeError if out_dts[i] != dts[i] else ValueError)(f"outs[{i}] must hold {numels[i]} elements of {dts[i]}")
+        op = _c_array(out_ptrs, ctypes.c_void_p)
     need = attnres_grad_clip_workspace_size() if workspace is None else 0
     _keep, ws, nbytes = _workspace(workspace, need, norm.device, stream)
-    rc = _N.lib.attnres_grad_clip(gp, op, numels, dtypes, n, max_norm, _vec(norm, "norm", (1,), torch.float32, cur), ws, nbytes,
-                                  _stream_on(stream, cur))
+    rc = _N.lib.attnres_grad_clip(gp, op, _c_array(numels, ctypes.c_int64), _c_array(codes, ctypes.c_int), n, max_norm,
+                                  _vec(norm, "norm", (1,), torch.float32, cur), ws, nbytes, _stream_on(stream, cur))
     _N.check(rc, "attnres_grad_clip")
