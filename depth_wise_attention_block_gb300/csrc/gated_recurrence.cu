@@ -9,17 +9,39 @@
 // A span of tokens acts on the state as h -> A h + B, and spans compose, so
 // all rows are one scan whatever sequences they belong to: at a sequence's
 // first token the state behind it is cut off (its initial state enters B).
-// Every element is read once and written once: the bound is HBM.
+// Every element is read once and written once: the floor is HBM's.
 //
-// A CTA owns a slab of channels, 128 bytes of a row, and walks over the rows
-// in tiles of 64, 8 rows to a warp, one 32-bit word of a row to a lane.  Each
-// warp copies its own rows ahead (cp.async, a ring of its own), so a tile takes
-// one barrier: the warps' (A, B) meet in shared memory and each warp goes on
-// from the state at its first row.  Where the slabs do not fill the GPU, a
-// cluster of R CTAs shares a slab: they take R neighbouring tiles at a time and
-// exchange the tiles' (A, B) through distributed shared memory.  The backward
-// walks from the last tile to the first; the states ahead of each tile, which
-// the forward kept, let it form h_{t-1} again without a second scan.
+// A CTA owns a slab of 64 channels, two to a lane (one packed pair of fp32),
+// and walks over the rows in tiles of 64.  Forward: 4 warps, 16 rows each, the
+// rows' h from a zero state and the products of their gates in registers; the
+// warps' (A, B) meet in shared memory, and each warp goes on from the state at
+// its first row.  More rows to a warp leave more registers' worth of work
+// between two meetings: 8 warps with 8 rows took 280 us where this takes 187.
+// Backward: 8 warps, 8 rows each, from the last tile to the first; of a row
+// e^-f and the state ahead of it are kept, the rest is formed again, because
+// there the registers decide how many warps there are (80 a thread, 24 warps
+// to an SM; 4 warps of 16 rows at 128: 248 us where forward and backward now
+// take 230).  The states ahead of the tiles, which the forward kept, let it
+// form h_{t-1} without a second scan over the rows.
+//
+// Where the slabs do not fill the GPU, a cluster of R CTAs shares a slab: they
+// take R neighbouring tiles at a time and send the tiles' (A, B) through
+// distributed shared memory.  With one CTA to a slab instead: 441 us where 189
+// (16384 x 7168), 197 where 39 (5003 x 1000).
+//
+// Rows of whole 16-byte vectors move by TMA, a box to a warp, and the results
+// go out the same way; rows on 32-bit words by cp.async (103 us where the
+// boxes take 72, 8192 x 4096 bf16), bf16 rows on single elements by registers
+// (234 us).  The boxes cost a lane no address: the warps' instructions are
+// what bounds the kernels once the traffic is down to one pass.
+//
+// Measured, gate and all gradients, HBM traffic of one pass over each tensor:
+// 16384 x 7168 bf16 forward 187 us, 5.0 TB/s, backward 476 us, 3.5 TB/s;
+// 8192 x 4096 bf16 in 5 sequences 72 us, 3.7 TB/s, and 154 us, 3.0 TB/s; the
+// same of fp32 99 us, 5.4 TB/s, and 210 us, 4.4 TB/s (the copy: 6.8).  What
+// bounds them: for each pair of channels some 75 instructions forward and 135
+// backward, at 41 % and 49 % of the issue slots, the rest lost to the latency
+// of a warp's own chain with 16 and 24 warps to an SM.
 #include <limits.h>
 #include <math.h>
 
@@ -30,6 +52,7 @@
 #include "body.h"
 #include "device_common.cuh"
 #include "launch.h"
+#include "tc_common.cuh"
 #include "vec16.cuh"
 
 namespace attnres {
@@ -105,6 +128,13 @@ __device__ __forceinline__ uint64_t f2_sigmoid(uint64_t z, uint64_t* e) {
   return f2_pack(rcp(a), rcp(b));
 }
 
+// 1 / (1 + e) on both halves: a gate's value again from its e^-z
+__device__ __forceinline__ uint64_t f2_open(uint64_t e) {
+  float a, b;
+  f2_unpack(f2_add(e, f2_both(1.f)), a, b);
+  return f2_pack(rcp(a), rcp(b));
+}
+
 // One value of it: a gate z (below -83 as -83) gives sigma and 1 - sigma.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float z, float* rest) {
@@ -116,8 +146,8 @@ __device__ __forceinline__ float sigmoid(float z, float* rest) {
 
 // -------------------------------------------------- the channels of a lane --
 
-// N channels of one row: a lane's 4 or 8 bytes in memory, N / 2 packed pairs
-// of fp32 in registers.
+// N (two) channels of one row: a lane's 4 or 8 bytes in memory, N / 2 packed
+// pairs of fp32 in registers.
 template <typename T, int N>
 struct Lane {
   static constexpr int P = N / 2;
@@ -181,7 +211,18 @@ struct Lane {
         if (e < in) store_elem(at + e, f[e]);
     }
   }
-  // fp32 states in device memory, and in shared memory (16-byte or 8-byte vectors)
+  static __device__ __forceinline__ void stage(uint32_t addr, const uint64_t (&v)[P]) {
+    float f[N];
+#pragma unroll
+    for (int i = 0; i < P; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
+    if constexpr (sizeof(T) == 2) {
+      static_assert(N == 2, "a word");
+      asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(pack_bf16x2(f[0], f[1])) : "memory");
+    } else {
+      asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(f[0]), "f"(f[1]) : "memory");
+    }
+  }
+  // fp32 states in device memory, and in shared memory
   static __device__ __forceinline__ void load_state(const float* at, int in, uint64_t (&v)[P]) {
 #pragma unroll
     for (int i = 0; i < P; ++i) v[i] = f2_pack(2 * i < in ? at[2 * i] : 0.f, 2 * i + 1 < in ? at[2 * i + 1] : 0.f);
@@ -196,35 +237,25 @@ struct Lane {
     }
   }
   static __device__ __forceinline__ void get(const uint64_t (&at)[P], uint64_t (&v)[P]) {
-    if constexpr (P == 2) {
-      const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(&at[0]);
-      v[0] = u.x;
-      v[1] = u.y;
-    } else {
-      v[0] = at[0];
-    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) v[i] = at[i];
   }
   static __device__ __forceinline__ void put(uint64_t (&at)[P], const uint64_t (&v)[P]) {
-    if constexpr (P == 2) *reinterpret_cast<ulonglong2*>(&at[0]) = make_ulonglong2(v[0], v[1]);
-    else at[0] = v[0];
+#pragma unroll
+    for (int i = 0; i < P; ++i) at[i] = v[i];
   }
   // into a CTA of the cluster, counted by its mbarrier
   static __device__ __forceinline__ void put_cluster(uint32_t addr, const uint64_t (&v)[P], uint32_t bar) {
-    if constexpr (P == 2)
-      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b64 [%0], {%1, %2}, [%3];" ::"r"(addr), "l"(v[0]), "l"(v[1]),
-                   "r"(bar)
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr + 8 * i), "l"(v[i]), "r"(bar)
                    : "memory");
-    else
-      asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr), "l"(v[0]), "r"(bar) : "memory");
   }
 };
 
 // ------------------------------------------------------------ rows ahead --
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {  // the rest of 16: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {  // the rest of 4: zeros
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -235,63 +266,87 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-
-// How the rows of a tensor lie: on 16-byte vectors, on 32-bit words, or neither.
-enum RowAccess { kVectors = 0, kWords = 1, kElements = 2 };
+// a box of shared memory to a tensor (rows and columns outside it are left out)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
+               "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
 struct GrParams {
+  CUtensorMap in[4], out[3];  // x, f, g, dout; out or dx, df, dg (tma): boxes of a warp's rows
   RecurrenceArgs a;
-  int ranks;       // CTAs of a cluster
-  int groups;      // tiles of a CTA: ceil(tiles / ranks)
-  int access[4];   // of x, f, g and (backward) dout
-  int whole;       // every row tensor written lies on a lane's boundaries
+  int ranks;     // CTAs of a cluster
+  int groups;    // tiles of a CTA: ceil(tiles / ranks)
+  int tma;       // every row is whole 16-byte vectors: boxes by TMA
+  int words[4];  // otherwise: x, f, g, dout lie on 32-bit words
+  int aligned;   // and every row tensor written lies on a lane's boundaries
   unsigned long long wait_ns;  // limit of a wait
-  int withhold;    // the bounded-wait test: the first tile's spans are not sent
+  int withhold;  // the bounded-wait test: the first tile's spans are not sent
 };
 
-// One warp's copy of its ROWS rows from t0 on (channels c0 and up, N to a lane)
-// into shared memory; zeros where there is no row or channel.
+constexpr int kBoxAlign = 128;  // of a box in shared memory
+__device__ __forceinline__ unsigned char* aligned_box(unsigned char* dyn) { return dyn + (0u - smem_addr(dyn)) % kBoxAlign; }
+
+// One warp's copy of its rows from t0 on (channels c0 and up, N to a lane)
+// into shared memory where they do not lie on 16-byte vectors; zeros where
+// there is no row or channel.
 template <typename T, int N, int ROWS>
-__device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long long stride, int t0, int T_, int c0, int C, int access,
+__device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long long stride, int t0, int T_, int c0, int C, int words,
                                            int lane) {
-  constexpr int kRow = 32 * Lane<T, N>::kBytes;
+  constexpr int kRow = 32 * Lane<T, N>::kBytes, E = 4 / sizeof(T);  // elements of a word
   const T* base = static_cast<const T*>(src);
-  if (access == kVectors) {
-    constexpr int V = 16 / sizeof(T), kVecs = kRow / 16, kStep = 32 / kVecs;  // vectors of a row, rows at a time
-    const int v = lane % kVecs, r0 = lane / kVecs, left = C - c0 - v * V;
-    const int bytes = left >= V ? 16 : left > 0 ? left * (int)sizeof(T) : 0;
-    const T* at = base + (t0 + r0) * stride + c0 + v * V;
-    dst += r0 * kRow + v * 16;
-    if (t0 + ROWS <= T_ && bytes == 16) {
+  if (words) {
+    const int c = lane * E, e = 32 * E;  // neighbouring lanes, neighbouring words
+    const T* row = base + (long long)t0 * stride + c0 + c;
+    dst += lane * 4;
+    if (t0 + ROWS <= T_ && c0 + 32 * (int)Lane<T, N>::kWords * E <= C) {
 #pragma unroll
-      for (int i = 0; i < ROWS / kStep; ++i) cp_async16(dst + i * kStep * kRow, at + i * kStep * stride, 16);
+      for (int r = 0; r < ROWS; ++r, row += stride)
+#pragma unroll
+        for (int i = 0; i < Lane<T, N>::kWords; ++i) cp_async4(dst + r * kRow + i * 128, row + i * e, 4);
     } else {
+      for (int r = 0; r < ROWS; ++r, row += stride)
 #pragma unroll
-      for (int i = 0; i < ROWS / kStep; ++i) {
-        const int n = t0 + r0 + i * kStep < T_ ? bytes : 0;
-        cp_async16(dst + i * kStep * kRow, n > 0 ? at + i * kStep * stride : base, n);
-      }
-    }
-  } else {
-    constexpr int E = 4 / sizeof(T);  // elements of a word
-    for (int r = 0; r < ROWS; ++r) {
-      const T* row = base + (t0 + r < T_ ? (t0 + r) * stride + c0 : 0);
-#pragma unroll
-      for (int i = 0; i < Lane<T, N>::kWords; ++i) {  // (neighbouring lanes, neighbouring words)
-        const int c = (i * 32 + lane) * E, in = t0 + r < T_ ? C - c0 - c : 0;
-        const uint32_t to = dst + r * kRow + (i * 32 + lane) * 4;
-        if (access == kWords) {
-          cp_async4(to, in > 0 ? row + c : base, in >= E ? 4 : in > 0 ? (int)sizeof(T) : 0);
-        } else {  // bf16 off the words
-          uint32_t w = 0;
-          if (in > 0) w = reinterpret_cast<const uint16_t*>(row)[c];
-          if (in > 1) w |= (uint32_t) reinterpret_cast<const uint16_t*>(row)[c + 1] << 16;
-          st_shared_u32(to, w);
+        for (int i = 0; i < Lane<T, N>::kWords; ++i) {
+          const int in = t0 + r < T_ ? C - c0 - c - i * e : 0;
+          cp_async4(dst + r * kRow + i * 128, in > 0 ? row + i * e : base, in >= E ? 4 : in > 0 ? (int)sizeof(T) : 0);
         }
+    }
+  } else {  // bf16 off the words: by way of registers, some rows at a time
+    constexpr int kBatch = 4;
+    const int left = C - c0 - 2 * lane;
+    const uint16_t* row = reinterpret_cast<const uint16_t*>(base) + (long long)t0 * stride + c0 + 2 * lane;
+    for (int r = 0; r < ROWS; r += kBatch) {
+      uint32_t w[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k, row += stride) {
+        const int in = t0 + r + k < T_ ? left : 0;
+        w[k] = in > 0 ? row[0] : 0;
+        if (in > 1) w[k] |= (uint32_t)row[1] << 16;
       }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) st_shared_u32(dst + (r + k) * kRow + lane * 4, w[k]);
     }
   }
 }
+
+// A warp's boxes on their way, a phase of `bar` for each tile.  A wait that
+// runs out ends the loads (an open phase takes no second arrival).
+struct Boxes {
+  uint32_t bar;
+  bool landed;
+  __device__ __forceinline__ void wait(int i, unsigned long long limit_ns) {
+    if (landed) landed = __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)i & 1u, limit_ns));
+  }
+  // what is still on its way is not to outlive the CTA's memory
+  __device__ __forceinline__ void settle() const {
+    if (!landed)
+      for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait_bounded(bar, parity);
+  }
+};
 
 // ------------------------------------------------------------- sequences --
 
@@ -398,6 +453,7 @@ template <int P, int W, int ROWS>
 struct alignas(16) GrShared {
   uint64_t A[2][W][32][P], B[2][W][32][P];
   uint64_t state[2][32][P];  // of a CTA alone: ahead of its tile
+  uint64_t loads[W][2];  // mbarriers: a warp's boxes have landed
   uint64_t before[3], after[3];  // mbarriers: a cluster's spans ahead of this CTA's tile are here; the others, its own among them
   unsigned char cut[2][8];  // a byte for each warp
   uint32_t rank_cut[3][kGrMaxCluster];
@@ -504,7 +560,7 @@ __device__ __forceinline__ void through_turns(const GrShared<L::P, W, ROWS>& sh,
                                               int ranks, int lane, uint64_t (&c)[L::P]) {
   const uint32_t cut = __ballot_sync(0xffffffffu, lane < ranks && sh.rank_cut[set][lane & (kGrMaxCluster - 1)] != 0);
   const RankSpan<L::P>* span = spans + set * ranks + from;
-#pragma unroll 1
+#pragma unroll 4
   for (int t = from; t < to; ++t, ++span) {
     uint64_t a[L::P], b[L::P];
     L::get(span->A[lane], a);
@@ -557,12 +613,12 @@ __device__ __forceinline__ void receive(GrShared<L::P, W, ROWS>& sh, RankSpan<L:
 template <int P, int W, int ROWS>
 __device__ __forceinline__ void leave(GrShared<P, W, ROWS>& sh, int groups, int ranks, unsigned long long limit_ns, bool ok, int* dev_err,
                                       int lane) {
-  if (ranks == 1) return;
-  if (ok && groups > 0)
+  if (ranks > 1 && ok && groups > 0)
     ok = mbar_wait_cluster_bounded(smem_addr(&sh.after[(groups - 1) % 3]), (uint32_t)((groups - 1) / 3) & 1u, limit_ns);
   if (!ok && lane == 0) report_error(dev_err, ATTNRES_DEVERR_WAIT_TIMEOUT);
+  if (lane == 0) bulk_wait_read();
   __syncwarp();
-  cluster_sync_all();
+  if (ranks > 1) cluster_sync_all();
 }
 
 // --------------------------------------------------------------- forward --
@@ -573,54 +629,76 @@ template <typename T, bool GATE>
 __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __grid_constant__ GrParams p) {
   constexpr int N = 2;
   using L = Lane<T, N>;
-  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGfRows * kRow, kArrays = GATE ? 3 : 2;
-  extern __shared__ __align__(128) unsigned char dyn[];  // [warp][array][row], then the spans of a cluster's tiles
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGfRows * kRow, kArrays = GATE ? 4 : 3;
+  extern __shared__ unsigned char dyn[];  // [warp][x, f, out, g][row], then the spans of a cluster's tiles
   __shared__ GrShared<P, kGfWarps, kGfRows> sh;
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;  // channels of this lane
-  const bool whole = p.whole && in == N;
-  const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
+  const bool whole = p.aligned && in == N;
   const int T_ = (int)a.T;
-  const uint32_t ring = smem_addr(dyn) + warp * (kArrays * kArray);
-  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGfWarps * kArrays * kArray);
+  unsigned char* const arrays = aligned_box(dyn);
+  const uint32_t ring = smem_addr(arrays) + warp * (kArrays * kArray), staged = ring + 2 * kArray;
+  auto spans = reinterpret_cast<RankSpan<P>*>(arrays + kGfWarps * kArrays * kArray);
   const uint64_t zero[P] = {};
   if (warp == 0) L::put(sh.state[0][lane], zero);
   if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(sh.cut[threadIdx.x]) = 0;
-  __syncthreads();
-  if (ranks > 1) {
-    if (threadIdx.x == 0) {
+  if (lane < 2) mbar_init(smem_addr(&sh.loads[warp][lane]), 1);
+  if (threadIdx.x == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        mbar_init(smem_addr(&sh.before[i]), 1);
-        mbar_init(smem_addr(&sh.after[i]), 1);
-      }
-      mbar_fence_init();
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_addr(&sh.before[i]), 1);
+      mbar_init(smem_addr(&sh.after[i]), 1);
     }
-    cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
   }
+  mbar_fence_init();
+  __syncthreads();
+  if (ranks > 1) cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
   bool ok = true;
   pdl_wait();
   pdl_trigger();
 
   auto row0 = [&](int i) { return (i * ranks + rank) * kGrChunk + warp * kGfRows; };
+  Boxes xf{smem_addr(&sh.loads[warp][0]), true}, gs{smem_addr(&sh.loads[warp][1]), true};
   auto fetch_xf = [&](int i) {
-    if (i < p.groups) {
-      fetch_rows<T, N, kGfRows>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
-      fetch_rows<T, N, kGfRows>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
+    if (p.tma) {
+      if (lane == 0 && i < p.groups && xf.landed) {
+        mbar_arrive_expect_tx(xf.bar, 2 * kArray);
+        tma_load_2d(ring, &p.in[0], c0, row0(i), xf.bar);
+        tma_load_2d(ring + kArray, &p.in[1], c0, row0(i), xf.bar);
+      }
+    } else {
+      if (i < p.groups) {
+        fetch_rows<T, N, kGfRows>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.words[0], lane);
+        fetch_rows<T, N, kGfRows>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.words[1], lane);
+      }
+      cp_async_commit();  // a group for every tile, there or not
     }
-    cp_async_commit();  // a group for every tile, there or not
   };
   auto fetch_g = [&](int i) {
-    if constexpr (GATE) {
-      if (i < p.groups) fetch_rows<T, N, kGfRows>(ring + 2 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
+    if (p.tma) {
+      if (lane == 0 && i < p.groups && gs.landed) {
+        mbar_arrive_expect_tx(gs.bar, kArray);
+        tma_load_2d(ring + 3 * kArray, &p.in[2], c0, row0(i), gs.bar);
+      }
+    } else {
+      if (i < p.groups) fetch_rows<T, N, kGfRows>(ring + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.words[2], lane);
       cp_async_commit();
     }
   };
+  auto wait = [&](Boxes& boxes, int i) {
+    if (p.tma) {
+      boxes.wait(i, p.wait_ns);
+      ok = ok && boxes.landed;
+    } else {
+      cp_async_wait<GATE ? 1 : 0>();
+      __syncwarp();
+    }
+  };
   fetch_xf(0);
-  fetch_g(0);
+  if constexpr (GATE) fetch_g(0);
   pass_empty(a, a.s0, a.s1, rank, ranks, c, in, warp, kGfWarps, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
   Boundaries<kGfRows, false> bounds;
@@ -633,8 +711,7 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
     const int t0 = row0(i), par = i & 1;
     __syncwarp();  // the last rows' marks have been read
     const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane);
-    cp_async_wait<GATE ? 1 : 0>();
-    __syncwarp();
+    wait(xf, i);
     const uint32_t at = ring + lane * L::kBytes;
 
     // the rows from a state of zero: h = hl + pa * (the state ahead), hl alone behind a first token
@@ -688,6 +765,7 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
 #pragma unroll
           for (int e = 0; e < P; ++e) hl[k][e] = f2_fma(pa[k][e], h[e], hl[k][e]);
     }
+    if constexpr (GATE) wait(gs, i);
     if (!ok) {
 #pragma unroll
       for (int k = 0; k < kGfRows; ++k)
@@ -699,34 +777,43 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
       for (int k = 0; k < kGfRows; ++k)
         if (m.ends >> k & 1) L::store_state(a.s1 + (long long)sh.seqs[warp][kGfRows + k] * a.C + c, in, hl[k]);
     }
-    if constexpr (GATE) {
-      cp_async_wait<1>();
-      __syncwarp();
-    }
-    T* o = static_cast<T*>(a.out) + t0 * a.os + c;
-    auto finish = [&](auto all) {
+    auto finish = [&](auto box) {
 #pragma unroll
       for (int k = 0; k < kGfRows; ++k) {
         if constexpr (GATE) {
           uint64_t g[P], e;
-          L::load_gate(at + 2 * kArray + k * kRow, g);
+          L::load_gate(at + 3 * kArray + k * kRow, g);
 #pragma unroll
           for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
         }
-        if constexpr (all.value) {
-          if (in) L::store(o + k * a.os, N, true, hl[k]);
+        if constexpr (box.value) {
+          L::stage(staged + lane * L::kBytes + k * kRow, hl[k]);
         } else {
-          if (t0 + k >= first && t0 + k < last) L::store(o + k * a.os, in, whole, hl[k]);
+          if (t0 + k >= first && t0 + k < last) L::store(static_cast<T*>(a.out) + (long long)(t0 + k) * a.os + c, in, whole, hl[k]);
         }
       }
     };
-    if (even && t0 >= first && t0 + kGfRows <= last) finish(std::true_type{});
-    else finish(std::false_type{});
+    // (a box leaves out rows behind the tensor's end, but not those outside every sequence)
+    if (p.tma && t0 >= first && (t0 + kGfRows <= last || last == T_)) {
+      if (lane == 0) bulk_wait_read();  // of the last tile's box
+      __syncwarp();
+      finish(std::true_type{});
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && t0 < T_) {
+        tma_store_2d(&p.out[0], c0, t0, staged);
+        bulk_commit();
+      }
+    } else {
+      finish(std::false_type{});
+    }
     if constexpr (GATE) {
       __syncwarp();  // g has been read
       fetch_g(i + 1);
     }
   }
+  xf.settle();
+  gs.settle();
   leave(sh, p.groups, ranks, p.wait_ns, ok, a.dev_err, lane);
 }
 
@@ -735,56 +822,66 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
 constexpr int kGbWarps = 8, kGbRows = kGrChunk / kGbWarps;
 
 template <typename T, bool GATE>
-__global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_backward_kernel(const __grid_constant__ GrParams p) {
-  constexpr int N = 2, kStages = 2;
+__global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 3 : 2) gr_backward_kernel(const __grid_constant__ GrParams p) {
+  constexpr int N = 2;
   using L = Lane<T, N>;
-  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGbRows * kRow, kArrays = GATE ? 4 : 3, kStage = kArrays * kArray;
-  extern __shared__ __align__(128) unsigned char dyn[];  // [warp][stage][array][row], then the spans of a cluster's tiles
+  constexpr int P = L::P, kRow = 32 * L::kBytes, kArray = kGbRows * kRow, kArrays = GATE ? 4 : 3;
+  // [warp][x, f, dy, g][row], then the spans of a cluster's tiles.  A row's
+  // gradients take its places: dx that of x, df that of f, dg that of g.
+  extern __shared__ unsigned char dyn[];
   __shared__ GrShared<P, kGbWarps, kGbRows> sh;
   __shared__ alignas(16) uint64_t fwd_B[2][kGbWarps][32][P];  // the forward's spans; their A is that of the gradients
-  __shared__ alignas(8) unsigned char fwd_cut[2][kGbWarps];
+  __shared__ alignas(8) unsigned char fwd_cut[2][8];
   const RecurrenceArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;
-  const bool whole = p.whole && in == N;
-  const bool even = __all_sync(0xffffffffu, whole || in == 0);  // no lane holds a part of its channels
+  const bool whole = p.aligned && in == N;
   const int T_ = (int)a.T;
-  const uint32_t ring = smem_addr(dyn) + warp * (kStages * kStage);
-  auto spans = reinterpret_cast<RankSpan<P>*>(dyn + kGbWarps * kStages * kStage);
+  unsigned char* const arrays = aligned_box(dyn);
+  const uint32_t ring = smem_addr(arrays) + warp * (kArrays * kArray);
+  auto spans = reinterpret_cast<RankSpan<P>*>(arrays + kGbWarps * kArrays * kArray);
   const uint64_t zero[P] = {};
+  if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(fwd_cut[threadIdx.x]) = 0;
   if (warp == 0) L::put(sh.state[0][lane], zero);
   if (threadIdx.x < 2) *reinterpret_cast<uint64_t*>(sh.cut[threadIdx.x]) = 0;
-  __syncthreads();
-  if (ranks > 1) {
-    if (threadIdx.x == 0) {
+  if (lane < 2) mbar_init(smem_addr(&sh.loads[warp][lane]), 1);
+  if (threadIdx.x == 0) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        mbar_init(smem_addr(&sh.before[i]), 1);
-        mbar_init(smem_addr(&sh.after[i]), 1);
-      }
-      mbar_fence_init();
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_addr(&sh.before[i]), 1);
+      mbar_init(smem_addr(&sh.after[i]), 1);
     }
-    cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
   }
+  mbar_fence_init();
+  __syncthreads();
+  if (ranks > 1) cluster_sync_all();  // every CTA of the cluster is there, its barriers ready
   bool ok = true;
   pdl_wait();
   pdl_trigger();
 
   auto row0 = [&](int i) { return ((p.groups - 1 - i) * ranks + rank) * kGrChunk + warp * kGbRows; };
+  Boxes boxes{smem_addr(&sh.loads[warp][0]), true};
   auto fetch = [&](int i) {
-    if (i < p.groups) {
-      const uint32_t to = ring + i % kStages * kStage;
-      fetch_rows<T, N, kGbRows>(to, a.x, a.xs, row0(i), T_, c0, a.C, p.access[0], lane);
-      fetch_rows<T, N, kGbRows>(to + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.access[1], lane);
-      fetch_rows<T, N, kGbRows>(to + 2 * kArray, a.dout, a.dos, row0(i), T_, c0, a.C, p.access[3], lane);
-      if constexpr (GATE) fetch_rows<T, N, kGbRows>(to + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.access[2], lane);
+    if (p.tma) {
+      if (lane == 0 && i < p.groups && boxes.landed) {
+        mbar_arrive_expect_tx(boxes.bar, kArrays * kArray);
+        tma_load_2d(ring + 2 * kArray, &p.in[3], c0, row0(i), boxes.bar);
+        bulk_wait_read();  // the gradients of the last tile have left these places
+        tma_load_2d(ring, &p.in[0], c0, row0(i), boxes.bar);
+        tma_load_2d(ring + kArray, &p.in[1], c0, row0(i), boxes.bar);
+        if constexpr (GATE) tma_load_2d(ring + 3 * kArray, &p.in[2], c0, row0(i), boxes.bar);
+      }
+    } else if (i < p.groups) {
+      fetch_rows<T, N, kGbRows>(ring, a.x, a.xs, row0(i), T_, c0, a.C, p.words[0], lane);
+      fetch_rows<T, N, kGbRows>(ring + kArray, a.f, a.fs, row0(i), T_, c0, a.C, p.words[1], lane);
+      fetch_rows<T, N, kGbRows>(ring + 2 * kArray, a.dout, a.dos, row0(i), T_, c0, a.C, p.words[3], lane);
+      if constexpr (GATE) fetch_rows<T, N, kGbRows>(ring + 3 * kArray, a.g, a.gs, row0(i), T_, c0, a.C, p.words[2], lane);
+      cp_async_commit();
     }
-    cp_async_commit();
   };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  fetch(0);
   pass_empty(a, a.ds1, a.ds0, rank, ranks, c, in, warp, kGbWarps, lane);
   const int first = a.cu ? clamp_row(__ldg(a.cu), T_) : 0, last = a.cu ? clamp_row(__ldg(a.cu + a.N), T_) : T_;
   Boundaries<kGbRows, true> bounds;
@@ -795,16 +892,24 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
 
   for (int i = 0; i < p.groups; ++i) {
     const int t0 = row0(i), par = i & 1;
-    __syncwarp();  // the slot that is filled next has been read
-    fetch(i + kStages - 1);
     uint64_t hf[P];  // the state ahead of the tile
     L::load_state(a.chunk + (t0 < T_ ? (long long)(t0 / kGrChunk) * a.C + c : 0), t0 < T_ ? in : 0, hf);
+    __syncwarp();  // the last rows' marks have been read
     const Marks m = bounds.rows(a, t0, sh.seqs[warp], lane);
-    cp_async_wait<kStages - 1>();
-    __syncwarp();
-    const uint32_t at = ring + i % kStages * kStage + lane * L::kBytes;
+    if (p.tma) {
+      boxes.wait(i, p.wait_ns);
+      ok = ok && boxes.landed;
+    } else {
+      cp_async_wait<0>();
+      __syncwarp();
+    }
+    const uint32_t at = ring + lane * L::kBytes;
 
-    uint64_t ga[kGbRows][P], rest[kGbRows][P], d[kGbRows][P], sg[GATE ? kGbRows : 1][P], A[P], B[P], R[P];
+    // The rows' span for the state (A, B) and for the gradients, R = sum of
+    // (a_0 .. a_k) d_k up to the first row that ends a sequence.  Of a row
+    // only e^-f is kept, from which a and 1 - a come back exactly.
+    uint64_t ef[kGbRows][P], A[P], B[P], R[P];
+    uint64_t final[kGbRows][P];  // the gradients at final states (read once: ds0 may lie in their place)
 #pragma unroll
     for (int e = 0; e < P; ++e) {
       A[e] = f2_both(1.f);
@@ -812,40 +917,38 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
     }
     auto scan = [&](auto marks) {
 #pragma unroll
-    for (int k = 0; k < kGbRows; ++k) {
-      uint64_t x[P];
-      L::load(at + k * kRow, x);
-      L::forgets(at + kArray + k * kRow, ga[k], rest[k]);
-      L::load(at + 2 * kArray + k * kRow, d[k]);
-      if constexpr (GATE) {
-        uint64_t g[P], u;
-        L::load_gate(at + 3 * kArray + k * kRow, g);
+      for (int k = 0; k < kGbRows; ++k) {
+        uint64_t x[P], f[P], d[P], ga[P];
+        L::load(at + k * kRow, x);
+        L::load_gate(at + kArray + k * kRow, f);
+        L::load(at + 2 * kArray + k * kRow, d);
+        if constexpr (GATE) {
+          uint64_t g[P], u;
+          L::load_gate(at + 3 * kArray + k * kRow, g);
+#pragma unroll
+          for (int e = 0; e < P; ++e) d[e] = f2_mul(d[e], f2_mul(g[e], f2_sigmoid<T>(g[e], &u)));
+        }
+        if constexpr (marks.value) {
+          if (a.ds1 && (m.ends >> k & 1)) {
+            uint64_t v[P];
+            L::load_state(a.ds1 + (long long)sh.seqs[warp][kGbRows + k] * a.C + c, in, v);
+#pragma unroll
+            for (int e = 0; e < P; ++e) {
+              d[e] = f2_add(d[e], v[e]);
+              final[__popc(m.ends & ((1u << k) - 1))][e] = v[e];
+            }
+          }
+          if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, B);
+        }
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-          sg[k][e] = f2_sigmoid<T>(g[e], &u);
-          d[k][e] = f2_mul(d[k][e], f2_mul(g[e], sg[k][e]));
+          ga[e] = f2_sigmoid<T>(f[e], &ef[k][e]);
+          const uint64_t rest = f2_mul(ef[k][e], ga[e]);
+          B[e] = f2_fma(ga[e], B[e], f2_mul(rest, x[e]));
+          A[e] = f2_mul(A[e], ga[e]);
+          if (!marks.value || !(m.ends & ((1u << k) - 1))) R[e] = f2_fma(A[e], d[e], R[e]);
         }
       }
-      if constexpr (marks.value) {
-        if (a.ds1 && (m.ends >> k & 1)) {
-          uint64_t v[P];
-          L::load_state(a.ds1 + (long long)sh.seqs[warp][kGbRows + k] * a.C + c, in, v);
-#pragma unroll
-          for (int e = 0; e < P; ++e) d[k][e] = f2_add(d[k][e], v[e]);
-        }
-        if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, B);
-      }
-#pragma unroll
-      for (int e = 0; e < P; ++e) {
-        B[e] = f2_fma(ga[k][e], B[e], f2_mul(rest[k][e], x[e]));
-        A[e] = f2_mul(A[e], ga[k][e]);
-      }
-    }
-#pragma unroll
-    for (int k = kGbRows - 1; k >= 0; --k) {
-#pragma unroll
-      for (int e = 0; e < P; ++e) R[e] = f2_mul(ga[k][e], marks.value && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], R[e]));
-    }
     };
     if ((m.starts | m.ends) == 0) scan(std::false_type{});
     else scan(std::true_type{});
@@ -859,81 +962,107 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 2 : 1) gr_back
     __syncthreads();
     if (ranks > 1 && ok && warp == 0)
       send_span<L, kGbWarps, kGbRows, true>(sh, spans, par, i % 3, ranks - 1 - rank, ranks, !(p.withhold && i == 0), lane);
-    // while the spans are on their way: the states ahead of the rows, and the output gates' gradients
+    // while the spans are on their way: the states ahead of the rows
     through_warps<L, kGbWarps, false>(sh.A[par], fwd_B[par], *reinterpret_cast<const uint64_t*>(fwd_cut[par]), warp, lane, hf);
     uint64_t hp[kGbRows][P];
-    T* dx = static_cast<T*>(a.dx) + (a.dx ? t0 * a.dxs + c : 0);
-    T* df = static_cast<T*>(a.df) + (a.df ? t0 * a.dfs + c : 0);
-    T* dg = static_cast<T*>(a.dg) + (a.dg ? t0 * a.dgs + c : 0);
-    // all: no sequence begins or ends among the rows, and all of them are of
-    // one: no branches (which gradients are wanted must not choose the code, or
-    // their last bits could depend on it)
-    auto states = [&](auto all) {
-      constexpr bool kAll = all.value;
+    auto states = [&](auto marks) {
 #pragma unroll
       for (int k = 0; k < kGbRows; ++k) {
         uint64_t x[P];
         L::load(at + k * kRow, x);
-        if constexpr (!kAll) {
+        if constexpr (marks.value) {
           if (m.starts >> k & 1) L::load_state(a.s0 + (a.s0 ? (long long)sh.seqs[warp][k] * a.C + c : 0), a.s0 ? in : 0, hf);
         }
 #pragma unroll
         for (int e = 0; e < P; ++e) {
+          const uint64_t ga = f2_open(ef[k][e]);
           hp[k][e] = hf[e];
-          hf[e] = f2_fma(ga[k][e], hf[e], f2_mul(rest[k][e], x[e]));
-        }
-        if constexpr (GATE) {
-          const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
-          uint64_t g[P], dy[P], v[P];
-          L::load_gate(at + 3 * kArray + k * kRow, g);
-          L::load(at + 2 * kArray + k * kRow, dy);
-#pragma unroll
-          for (int e = 0; e < P; ++e) {
-            const uint64_t s = sg[k][e];
-            v[e] = f2_mul(f2_mul(dy[e], hf[e]), f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));
-          }
-          if (live && a.dg) L::store(dg + k * a.dgs, kAll ? N : in, kAll || whole, v);
+          hf[e] = f2_fma(ga, hf[e], f2_mul(f2_mul(ef[k][e], ga), x[e]));
         }
       }
     };
+    if (m.starts == 0) states(std::false_type{});
+    else states(std::true_type{});
     uint64_t G[P];
-    auto finish = [&](auto all) {
-      constexpr bool kAll = all.value;
+    receive<L, kGbWarps, kGbRows, true>(sh, spans, i, ranks - 1 - rank, ranks, p.wait_ns, ok, warp, lane, A, R, state, G);
+    if (!ok) {  // every result NaN
+#pragma unroll
+      for (int k = 0; k < kGbRows; ++k)
+#pragma unroll
+        for (int e = 0; e < P; ++e) ef[k][e] = hp[k][e] = f2_both(__int_as_float(0x7fc00000));
+    }
+    // marks: a sequence begins or ends among the rows, or some are of none.
+    // (Which gradients are wanted does not choose the code: their last bits
+    // must not depend on it.)
+    auto finish = [&](auto marks) {
+      constexpr bool kMarks = marks.value;
 #pragma unroll
       for (int k = kGbRows - 1; k >= 0; --k) {
-        const bool live = kAll ? in > 0 : t0 + k >= first && t0 + k < last;
-        uint64_t x[P], v[P];
+        uint64_t x[P], d[P], vx[P], vf[P];
+        [[maybe_unused]] uint64_t vg[P];
         L::load(at + k * kRow, x);
+        L::load(at + 2 * kArray + k * kRow, d);
+        if constexpr (GATE) {
+          uint64_t g[P], u;
+          L::load_gate(at + 3 * kArray + k * kRow, g);
 #pragma unroll
-        for (int e = 0; e < P; ++e) G[e] = !kAll && (m.ends >> k & 1) ? d[k][e] : f2_add(d[k][e], G[e]);  // dh
+          for (int e = 0; e < P; ++e) {
+            const uint64_t s = f2_sigmoid<T>(g[e], &u);
+            vg[e] = f2_mul(d[e], f2_fma(f2_mul(g[e], s), f2_sub(f2_both(1.f), s), s));  // dy silu'(g)
+            d[e] = f2_mul(d[e], f2_mul(g[e], s));
+          }
+        }
+        if constexpr (kMarks) {
+          if (a.ds1 && (m.ends >> k & 1)) {
 #pragma unroll
-        for (int e = 0; e < P; ++e) v[e] = f2_mul(rest[k][e], G[e]);
-        if (live && a.dx) L::store(dx + k * a.dxs, kAll ? N : in, kAll || whole, v);
+            for (int e = 0; e < P; ++e) d[e] = f2_add(d[e], final[__popc(m.ends & ((1u << k) - 1))][e]);
+          }
+        }
 #pragma unroll
-        for (int e = 0; e < P; ++e) v[e] = f2_mul(f2_mul(G[e], f2_sub(hp[k][e], x[e])), f2_mul(ga[k][e], rest[k][e]));
-        if (live && a.df) L::store(df + k * a.dfs, kAll ? N : in, kAll || whole, v);
-#pragma unroll
-        for (int e = 0; e < P; ++e) G[e] = f2_mul(ga[k][e], G[e]);
-        if constexpr (!kAll) {
+        for (int e = 0; e < P; ++e) {
+          const uint64_t ga = f2_open(ef[k][e]), rest = f2_mul(ef[k][e], ga);
+          G[e] = kMarks && (m.ends >> k & 1) ? d[e] : f2_add(d[e], G[e]);  // dh
+          vx[e] = f2_mul(rest, G[e]);
+          vf[e] = f2_mul(f2_mul(G[e], f2_sub(hp[k][e], x[e])), f2_mul(ga, rest));
+          if constexpr (GATE) vg[e] = f2_mul(vg[e], f2_fma(ga, hp[k][e], f2_mul(rest, x[e])));
+          G[e] = f2_mul(ga, G[e]);
+        }
+        if (p.tma && !kMarks) {
+          L::stage(at + k * kRow, vx);
+          L::stage(at + kArray + k * kRow, vf);
+          if constexpr (GATE) L::stage(at + 3 * kArray + k * kRow, vg);
+        } else if (t0 + k >= first && t0 + k < last) {
+          const long long t = t0 + k;
+          if (a.dx) L::store(static_cast<T*>(a.dx) + t * a.dxs + c, in, whole, vx);
+          if (a.df) L::store(static_cast<T*>(a.df) + t * a.dfs + c, in, whole, vf);
+          if constexpr (GATE) {
+            if (a.dg) L::store(static_cast<T*>(a.dg) + t * a.dgs + c, in, whole, vg);
+          }
+        }
+        if constexpr (kMarks) {
           if (a.ds0 && (m.starts >> k & 1)) L::store_state(a.ds0 + (long long)sh.seqs[warp][k] * a.C + c, in, G);
         }
       }
     };
-    const bool all = even && (m.starts | m.ends) == 0 && t0 >= first && t0 + kGbRows <= last;
-    if (all) states(std::true_type{});
-    else states(std::false_type{});
-    receive<L, kGbWarps, kGbRows, true>(sh, spans, i, ranks - 1 - rank, ranks, p.wait_ns, ok, warp, lane, A, R, state, G);
-    if (!ok) {  // every result NaN, the output gates' gradients too
-#pragma unroll
-      for (int k = 0; k < kGbRows; ++k) {
-#pragma unroll
-        for (int e = 0; e < P; ++e) d[k][e] = ga[k][e] = f2_both(__int_as_float(0x7fc00000));
-        if (a.dg && t0 + k >= first && t0 + k < last) L::store(dg + k * a.dgs, in, whole, d[k]);
+    if ((m.starts | m.ends) == 0 && t0 >= first && (t0 + kGbRows <= last || last == T_)) {
+      finish(std::false_type{});
+      if (p.tma) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && t0 < T_) {
+          if (a.dx) tma_store_2d(&p.out[0], c0, t0, ring);
+          if (a.df) tma_store_2d(&p.out[1], c0, t0, ring + kArray);
+          if (GATE && a.dg) tma_store_2d(&p.out[2], c0, t0, ring + 3 * kArray);
+          bulk_commit();
+        }
       }
+    } else {
+      finish(std::true_type{});
     }
-    if (all) finish(std::true_type{});
-    else finish(std::false_type{});
+    __syncwarp();  // the rows have been read
+    fetch(i + 1);
   }
+  boxes.settle();
   leave(sh, p.groups, ranks, p.wait_ns, ok, a.dev_err, lane);
 }
 
@@ -984,17 +1113,27 @@ __global__ void __launch_bounds__(kGsThreads) gr_step_kernel(const __grid_consta
   if (in) *st = h;
 }
 
-int row_access(const void* p, int64_t stride, int es) {
-  if (!p) return kVectors;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es);
-  return (at & 15) == 0 ? kVectors : (at & 3) == 0 ? kWords : kElements;
+// whether a row tensor (null: absent) lies on boundaries of `bytes`
+bool rows_on(const void* p, int64_t stride, int es, int bytes) {
+  return !p || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(stride * es)) & (uintptr_t)(bytes - 1)) == 0;
+}
+
+// a row tensor in boxes of a warp's rows and a CTA's channels
+bool make_rows_map(CUtensorMap* map, const void* p, int64_t stride, int64_t T, int C, bool bf16, int width, int rows) {
+  const EncodeTiled enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)T}, strides[1] = {(cuuint64_t)(stride * (bf16 ? 2 : 4))};
+  const cuuint32_t box[2] = {(cuuint32_t)width, (cuuint32_t)rows}, steps[2] = {1, 1};
+  return enc(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(p), dims, strides, box, steps,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A kernel's launch: its channels to a CTA, its shared memory without the
 // cluster's, and how many clusters of each size run at once.
 struct GrKernel {
   const void* kern;
-  int threads, width, lane_bytes, smem, span_bytes;
+  int threads, rows, width, lane_bytes, smem, span_bytes;
   SmemOptIn opt;
   std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];
 };
@@ -1053,9 +1192,6 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
   return e;
 }
 
-#ifndef GR_MAXR
-#define GR_MAXR kGrMaxCluster
-#endif
 template <typename... A>
 cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) {
   cudaError_t e = k.opt.ensure(k.kern, k.smem + 3 * kGrMaxCluster * k.span_bytes);
@@ -1063,10 +1199,12 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
   const int es = a.dtype == ATTNRES_BF16 ? 2 : 4;
   const int64_t tiles = (a.T + kGrChunk - 1) / kGrChunk, slabs = (a.C + k.width - 1) / k.width;
   // CTAs to a slab: the smallest cluster that takes off a tenth of the time
-  // (rounds of clusters x tiles of a CTA) against each smaller one
+  // (rounds of clusters x tiles of a CTA) against each smaller one.  (5003 x
+  // 1000, fp32: 39 us with up to 16 CTAs, 48 with up to 8; 16384 x 7168 takes
+  // few and is the same with either limit.)
   GrParams p{};
   double least = 1e300;
-  for (int r = 1; r <= GR_MAXR && r <= (tiles > 1 ? tiles : 1); ++r) {
+  for (int r = 1; r <= kGrMaxCluster && r <= (tiles > 1 ? tiles : 1); ++r) {
     int n = 0;
     e = clusters_at_once(k, r, &n);
     if (e != cudaSuccess) return e;
@@ -1080,14 +1218,25 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
   p.wait_ns = wait_limit_ns();
   p.withhold = debug_withhold_row1() > 0;
   p.groups = (int)((tiles + p.ranks - 1) / p.ranks);
+  const bool backward = a.dout != nullptr;
   const void* in[4] = {a.x, a.f, a.g, a.dout};
-  const int64_t strides[4] = {a.xs, a.fs, a.gs, a.dos};
-  for (int i = 0; i < 4; ++i) p.access[i] = row_access(in[i], strides[i], es);
-  const void* out[4] = {a.out, a.dx, a.df, a.dg};
-  const int64_t out_strides[4] = {a.os, a.dxs, a.dfs, a.dgs};
-  p.whole = 1;
-  for (int i = 0; i < 4; ++i)
-    if (out[i] && ((reinterpret_cast<uintptr_t>(out[i]) | (uintptr_t)(out_strides[i] * es)) & (uintptr_t)(k.lane_bytes - 1))) p.whole = 0;
+  const int64_t in_strides[4] = {a.xs, a.fs, a.gs, a.dos};
+  void* const out[3] = {backward ? a.dx : a.out, a.df, a.dg};
+  const int64_t out_strides[3] = {backward ? a.dxs : a.os, a.dfs, a.dgs};
+  p.tma = a.T > 0 && (int64_t)a.C * es % 16 == 0;  // (a box is cut off at 16 bytes, not at an element)
+  p.aligned = 1;
+  for (int i = 0; i < 4; ++i) {
+    p.tma = p.tma && rows_on(in[i], in_strides[i], es, 16);
+    p.words[i] = rows_on(in[i], in_strides[i], es, 4);
+  }
+  for (int i = 0; i < 3; ++i) {
+    p.tma = p.tma && rows_on(out[i], out_strides[i], es, 16);
+    p.aligned = p.aligned && rows_on(out[i], out_strides[i], es, k.lane_bytes);
+  }
+  for (int i = 0; i < 4 && p.tma; ++i)
+    if (in[i]) p.tma = make_rows_map(&p.in[i], in[i], in_strides[i], a.T, a.C, es == 2, k.width, k.rows);
+  for (int i = 0; i < 3 && p.tma; ++i)
+    if (out[i]) p.tma = make_rows_map(&p.out[i], out[i], out_strides[i], a.T, a.C, es == 2, k.width, k.rows);
   e = allow_cluster(k, p.ranks);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -1098,15 +1247,15 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
 template <typename T, bool GATE>
 cudaError_t launch_forward(const RecurrenceArgs& a) {
   using L = Lane<T, 2>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * kGfWarps, 32 * 2 * L::P, L::kBytes,
-                    kGrChunk * 32 * L::kBytes * (GATE ? 3 : 2), (int)sizeof(RankSpan<L::P>), {}, {}};
+  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * kGfWarps, kGfRows, 32 * 2 * L::P, L::kBytes,
+                    kBoxAlign + kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_forward_kernel<T, GATE>, a);
 }
 template <typename T, bool GATE>
 cudaError_t launch_backward(const RecurrenceArgs& a) {
   using L = Lane<T, 2>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * kGbWarps, 32 * 2 * L::P, L::kBytes,
-                    2 * kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
+  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * kGbWarps, kGbRows, 32 * 2 * L::P, L::kBytes,
+                    kBoxAlign + kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_backward_kernel<T, GATE>, a);
 }
 

@@ -182,6 +182,39 @@ def test_memories_from_none_to_hundreds_of_tokens(A, dt):
 
 
 @pytest.mark.parametrize("dt", DTYPES)
+@pytest.mark.parametrize("T,C,cu", [(1, 1, None), (15, 7, None), (200, 63, None), (333, 65, [0, 5, 130, 333]), (70, 130, [3, 40, 60]),
+                                    (64, 8, [0, 64]), (1100, 300, [0, 1100]),
+                                    (130, 128, None), (500, 72, [2, 130, 131, 488])])
+def test_rows_on_vectors_and_off_them(A, T, C, cu, dt):
+    """Rows of 16-byte vectors (channels that fill them or not) and the same
+    rows one element off give the same bits, and nothing beside them is written."""
+    cut = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    n = 1 if cu is None else len(cu) - 1
+    x, f, g, dy, s0, ds1 = _inputs(T, C, n, dt, True, 11)
+    pitch = -(-C // 8) * 8 + 8
+    results = []
+    for off in (0, 1):
+        def rows(t):
+            buf = torch.full((T, pitch), 7.0, dtype=dt, device="cuda")
+            buf[:, off:off + C] = t
+            return buf, buf[:, off:off + C]
+        ins = [rows(t)[1] for t in (x, f, g, dy)]
+        outs = [rows(7.0) for _ in range(4)]
+        out, dx, df, dg = (view for _, view in outs)
+        fin, ds0 = torch.full((n, C), 7.0, device="cuda"), torch.full((n, C), 7.0, device="cuda")
+        chunk = torch.empty(-(-T // 64), C, device="cuda")
+        A.attnres_gated_recurrence(ins[0], ins[1], out, gate=ins[2], cu_seqlens=cut, initial_state=s0, final_state=fin, chunk_states=chunk)
+        A.attnres_gated_recurrence_backward(ins[0], ins[1], chunk, ins[3], dx, df, dg, gate=ins[2], cu_seqlens=cut, initial_state=s0,
+                                            grad_final_state=ds1, grad_initial_state=ds0)
+        live = torch.zeros(T, pitch, dtype=torch.bool, device="cuda")
+        live[(cu or [0])[0]:(cu or [T])[-1], off:off + C] = True
+        assert all((buf[~live] == 7).all() for buf, _ in outs)
+        results.append([out.clone(), dx.clone(), df.clone(), dg.clone(), fin, ds0])
+    for one, other in zip(*results):
+        assert torch.equal(one, other)
+
+
+@pytest.mark.parametrize("dt", DTYPES)
 @pytest.mark.parametrize("C", [48, 35])
 def test_states_in_place_and_the_same_bits(A, C, dt):
     cu = [0, 130, 130, 131, 600]
