@@ -4,6 +4,7 @@
 // grad_clip.cu).
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
 #include <memory>
 #include <new>
 
@@ -115,6 +116,13 @@ int check_la(const void* q, int64_t qs, const void* k, int64_t ks, const void* v
   if (!span_ok(T, qs) || !span_ok(T, ks) || !span_ok(T, vs)) return fail(ATTNRES_ERANGE, "T*stride too large");
   if (!log_decay) return fail(ATTNRES_EINVAL, "log_decay is NULL");
   if (T > 0 && (!q || !k || !v)) return fail(ATTNRES_EINVAL, "q/k/v is NULL");
+  return ATTNRES_OK;
+}
+
+// fp32 and int32 arrays (null: absent)
+int check_words(std::initializer_list<const void*> arrays) {
+  for (const void* p : arrays)
+    if (!aligned(p, 4)) return fail(ATTNRES_EINVAL, "a float or int32 array is not 4-byte aligned");
   return ATTNRES_OK;
 }
 
@@ -632,7 +640,8 @@ int attnres_linear_attention_step(const void* q, int64_t q_stride, const void* k
 
 int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, const float* bias,
                        float eps, void* out, int64_t out_stride, void* stream) {
-  const int rc = check_ln(x, x_stride, T, d, dtype, eps);
+  int rc = check_ln(x, x_stride, T, d, dtype, eps);
+  if (rc == ATTNRES_OK) rc = check_words({gain, bias});
   if (rc != ATTNRES_OK) return rc;
   if (!stride_ok(out_stride, d)) return fail(ATTNRES_EINVAL, "a row stride is shorter than its row");
   if (!span_ok(T, out_stride)) return fail(ATTNRES_ERANGE, "T*stride too large");
@@ -677,6 +686,7 @@ int attnres_layer_norm_backward(const void* x, int64_t x_stride, int64_t T, int 
                                 const void* grad_out, int64_t grad_out_stride, void* grad_x, int64_t grad_x_stride,
                                 float* grad_gain, float* grad_bias, void* workspace, int64_t workspace_bytes, void* stream) {
   int rc = check_ln(x, x_stride, T, d, dtype, eps);
+  if (rc == ATTNRES_OK) rc = check_words({gain, grad_gain, grad_bias});
   if (rc != ATTNRES_OK) return rc;
   const int64_t es = dtype_bytes(dtype), w = d * es, vec = d * 4LL;
   if (!stride_ok(grad_out_stride, d) || !stride_ok(grad_x_stride, d))
@@ -730,6 +740,7 @@ int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget
   if (rc != ATTNRES_OK) return rc;
   if (T > 0 && !out) return fail(ATTNRES_EINVAL, "out is NULL");
   rc = check_gr_rows(out, out_stride, T, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_words({cu_seqlens, initial_state, final_state, chunk_states, dev_err});
   if (rc != ATTNRES_OK) return rc;
   if (T == 0 && !final_state) return ok();
   {
@@ -783,6 +794,8 @@ int attnres_gated_recurrence_backward(const void* x, int64_t x_stride, const voi
   if (rc == ATTNRES_OK) rc = check_gr_rows(grad_x, grad_x_stride, T, C, dtype);
   if (rc == ATTNRES_OK) rc = check_gr_rows(grad_forget, grad_forget_stride, T, C, dtype);
   if (rc == ATTNRES_OK) rc = check_gr_rows(grad_gate, grad_gate_stride, T, C, dtype);
+  if (rc == ATTNRES_OK)
+    rc = check_words({cu_seqlens, initial_state, chunk_states, grad_final_state, grad_initial_state, dev_err});
   if (rc != ATTNRES_OK) return rc;
   {
     const int64_t es = dtype_bytes(dtype), w = C * es, st = (int64_t)num_seqs * C * 4, cub = (num_seqs + 1) * 4LL;
@@ -834,6 +847,7 @@ int attnres_gated_recurrence_step(const void* x, int64_t x_stride, const void* f
   if (B > 65535) return fail(ATTNRES_ERANGE, "B=%d", B);
   int rc = check_gr(x, x_stride, forget, forget_stride, gate, gate_stride, B, C, dtype, nullptr, 1);
   if (rc == ATTNRES_OK) rc = check_gr_rows(out, out_stride, B, C, dtype);
+  if (rc == ATTNRES_OK) rc = check_words({state, slots});
   if (rc != ATTNRES_OK) return rc;
   if (!slots && B > num_slots) return fail(ATTNRES_EINVAL, "B=%d rows for %d slots", B, num_slots);
   if (B == 0 || num_slots == 0) return ok();

@@ -7,6 +7,17 @@
 // The mean is held as the sum of two fp32 numbers: m, the rounded mean, and
 // delta, the mean of the differences x - m (exact where m is near x), so rows
 // whose mean is far from zero keep their digits.
+//
+// The floor is HBM's: x once in and once out, backward x and dy in, dx out.
+// A row therefore stays on the SM between its passes (mean, squares, result):
+// forward in registers, backward in shared memory, since there the registers
+// hold a lane's sums of the gain and bias gradients.  Rows wider than that are
+// read once per pass by ln_any_kernel; what this saves, 16384 x 7168 bf16: 228
+// us there, 81 here (5.8 TB/s, the copy runs at 6.8); backward of 8192 x 7168:
+// 426 and 87 us (4.1 TB/s).  What bounds them now: the barriers of the row's
+// sums (two forward, two backward), and backward its issue slots: every pass
+// unpacks x and dy again.  64 rows take the launch and one row's chain of
+// load, sums and store: 6.5 us between the calls of a program.
 #include <math.h>
 
 #include "attnres.h"
@@ -590,7 +601,8 @@ __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* par
 
 // How a call's rows are held: vectors to a lane, warps to a row, rows of a CTA
 // at a time, dynamic shared memory, CTAs to an SM (vpl 0: a row does not fit,
-// ln_any_kernel).
+// ln_any_kernel).  The partial rows of the gain gradients follow the grid that
+// this gives: layer_norm_backward_workspace_bytes asks for the most of any plan.
 struct LnPlan {
   int vpl, warps, groups, smem, per_sm;
 };
@@ -598,11 +610,16 @@ LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceIn
   constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[3] = {1, 2, 4};
   const int V = 16 / es, n = 3;
   const int* vpl = backward ? kBackward : vec ? kForwardVec : kForward;
-  // few rows: each over as many warps as it feeds, a lane's channels few;
-  // many: a row in as few warps as hold it, so that its sums cross few of them
-  const bool few = T <= 2 * di.sm_count;
+  // few rows (one to an SM): each over as many warps as it feeds, a lane's
+  // channels few; many: a row in as few warps as hold it, so that its sums cross
+  // few of them.  Forward of 7168 bf16, with caches cold and the launch: 64 rows
+  // 10.9 us over many warps, 13.0 over few; 304 rows 17.0 and 15.0; 16384 rows
+  // 111 and 87; 2047 rows of 1003 fp32 19.1 and 12.9.
+  const bool few = T <= di.sm_count;
   for (int i = 0; i < n; ++i) {
     const int per_warp = 32 * vpl[i] * V, warps = (d + per_warp - 1) / per_warp;
+    // (backward, two vectors to a lane may take several warps: they take two rows
+    // at a time, 97 us where single rows over fewer warps took 108)
     if (warps > kLnMaxWarps || (!few && i + 1 < n && warps > 1 && !(backward && vpl[i] == 2))) continue;
     const int held = (d + 32 * V * warps - 1) / (32 * V * warps);
     for (int groups = few ? 1 : kLnMaxWarps / warps; groups >= 1; --groups) {
@@ -612,6 +629,7 @@ LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceIn
       const int64_t sums = backward && groups > 1 ? (int64_t)groups * 2 * d * 4 : 0;
       const int64_t smem = vectors + ring > sums ? vectors + ring : sums;
       if (smem + 1024 > di.max_smem_optin) continue;
+      // the variants with most registers to a thread run as one CTA to an SM
       const bool one = vpl[i] >= (backward ? 2 : 16) || 2 * (smem + 512 + 1024) > di.max_smem_optin + 1024;
       return {vpl[i], warps, groups, (int)smem, one ? 1 : 2};
     }
@@ -662,7 +680,7 @@ int64_t layer_norm_backward_workspace_bytes(int64_t T, int d) {
   DeviceInfo di;
   if (device_info(&di) != cudaSuccess) return -1;
   // the most CTAs that up to T rows of this width take, of any type and alignment
-  int64_t grid = T < 2 * di.sm_count ? T : 2 * di.sm_count;  // few rows: one to a CTA
+  int64_t grid = T < di.sm_count ? T : di.sm_count;  // few rows: one to a CTA
   for (int es = 2; es <= 4; es *= 2)
     for (int vec = 0; vec < 2; ++vec) {
       const LnPlan k = ln_plan(INT64_MAX, d, es, vec != 0, true, di);

@@ -782,9 +782,14 @@ int64_t attnres_layer_norm_backward_workspace_size(int64_t T, int d);
  *             the states ahead of every 64th row, which the backward goes on
  *             from (rows of it that lie in no sequence are unspecified)
  * T 0..2^31 - 65537, C 1..2^24, num_seqs 1..65535 (ATTNRES_ERANGE above).
- * The state is held in fp32.  A forget gate below -83 counts as -83 (a_t of
- * 1e-36).  Infinities and NaN reach the tokens of their channel and sequence
- * behind them and no others (an infinite state may become NaN).
+ * dev_err     device int or NULL.  CTAs that share channels wait for one
+ *             another's spans; a wait that runs out (a bound of seconds) ORs
+ *             ATTNRES_DEVERR_WAIT_TIMEOUT into *dev_err, and what depends on it
+ *             is NaN
+ * The state is held in fp32.  Either gate below -83 (minus infinity too)
+ * counts as -83: a_t of 1e-36.  Infinities and NaN reach the tokens of their
+ * channel and sequence behind them and no others (an infinite state may become
+ * NaN).  The last bits of a result do not depend on how the rows lie in memory.
  * ---------------------------------------------------------------------- */
 #define ATTNRES_RECURRENCE_CHUNK 64
 int attnres_gated_recurrence(const void* x, int64_t x_stride, const void* forget, int64_t forget_stride, const void* gate,

@@ -119,6 +119,17 @@ def test_step_refuses(N, kw, code):
     assert _step(N, **kw) == getattr(N, "ATTNRES_" + code), N.lib.attnres_last_error()
 
 
+@pytest.mark.parametrize("call,kw", [
+    (_ln, dict(gain=V + 2)), (_ln, dict(bias=V + 4098)), (_ln_bwd, dict(gain=V + 2)), (_ln_bwd, dict(gg=V + 0x10001)),
+    (_ln_bwd, dict(gb=V + 0x10003)), (_gr, dict(cu=V + 1)), (_gr, dict(s0=V + 2)), (_gr, dict(s1=V + 2)), (_gr, dict(ch=V + 2)),
+    (_gr_bwd, dict(ch=V + 2)), (_gr_bwd, dict(ds1=WS + 2)), (_gr_bwd, dict(ds0=WS + 1)), (_step, dict(st=WS + 2)),
+    (_step, dict(slots=V + 2)),
+])
+def test_float_and_int32_arrays_off_their_words(N, call, kw):
+    assert call(N, **kw) == N.ATTNRES_EINVAL
+    assert b"4-byte" in N.lib.attnres_last_error()
+
+
 def test_recurrence_without_rows(N):
     assert _gr(N, T=0, x=None, f=None, g=None, out=None) == 0
     assert _gr_bwd(N, gx=None, gf=None, gg=None, dy=None, ch=None) == 0
