@@ -20,8 +20,8 @@
 // Backward: 8 warps, 8 rows each, from the last tile to the first; of a row
 // e^-f and the state ahead of it are kept, the rest is formed again, because
 // there the registers decide how many warps there are (80 a thread, 24 warps
-// to an SM; 4 warps of 16 rows at 128: 248 us where forward and backward now
-// take 230).  The states ahead of the tiles, which the forward kept, let it
+// to an SM; 4 warps of 16 rows at 128: 248 us where forward and backward
+// together took 230).  The states ahead of the tiles, which the forward kept, let it
 // form h_{t-1} without a second scan over the rows.
 //
 // Where the slabs do not fill the GPU, a cluster of R CTAs shares a slab: they
@@ -32,16 +32,18 @@
 // Rows of whole 16-byte vectors move by TMA, a box to a warp, and the results
 // go out the same way; rows on 32-bit words by cp.async (103 us where the
 // boxes take 72, 8192 x 4096 bf16), bf16 rows on single elements by registers
-// (234 us).  The boxes cost a lane no address: the warps' instructions are
+// (205 us); these leave through shared memory by words.  The boxes cost a lane no address: the warps' instructions are
 // what bounds the kernels once the traffic is down to one pass.
 //
 // Measured, gate and all gradients, HBM traffic of one pass over each tensor:
-// 16384 x 7168 bf16 forward 187 us, 5.0 TB/s, backward 476 us, 3.5 TB/s;
-// 8192 x 4096 bf16 in 5 sequences 72 us, 3.7 TB/s, and 154 us, 3.0 TB/s; the
-// same of fp32 99 us, 5.4 TB/s, and 210 us, 4.4 TB/s (the copy: 6.8).  What
-// bounds them: for each pair of channels some 75 instructions forward and 135
-// backward, at 41 % and 49 % of the issue slots, the rest lost to the latency
-// of a warp's own chain with 16 and 24 warps to an SM.
+// 16384 x 7168 bf16 forward 187 us, 5.0 TB/s, backward 459 us, 3.6 TB/s;
+// 8192 x 4096 bf16 in 5 sequences 72 us, 3.7 TB/s, and 140 us, 3.4 TB/s; the
+// same of fp32 99 us, 5.4 TB/s, and 190 us, 4.9 TB/s (the copy: 6.8).  What
+// bounds them: for each pair of channels some 75 instructions forward and 130
+// backward, at 41 % and about half of the issue slots, the rest lost to the
+// latency of a warp's own chain with 16 and 24 warps to an SM and to fetching
+// instructions (a second form of the backward's stores beside the boxes cost a
+// tenth without running).
 #include <limits.h>
 #include <math.h>
 
@@ -191,26 +193,7 @@ struct Lane {
       rest[i] = f2_mul(e, a[i]);
     }
   }
-  // whole: all N channels are there, and the row lies on the lane's boundaries
-  static __device__ __forceinline__ void store(T* at, int in, bool whole, const uint64_t (&v)[P]) {
-    float f[N];
-#pragma unroll
-    for (int i = 0; i < P; ++i) f2_unpack(v[i], f[2 * i], f[2 * i + 1]);
-    if (whole) {
-      uint32_t w[kWords];
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        if constexpr (sizeof(T) == 2) w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
-        else w[i] = __float_as_uint(f[i]);
-      }
-      if constexpr (kWords == 2) *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(at) = w[0];
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e)
-        if (e < in) store_elem(at + e, f[e]);
-    }
-  }
+  // results, rounded to T, into shared memory
   static __device__ __forceinline__ void stage(uint32_t addr, const uint64_t (&v)[P]) {
     float f[N];
 #pragma unroll
@@ -266,6 +249,11 @@ __device__ __forceinline__ void cp_async_wait() {
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
 // a box of shared memory to a tensor (rows and columns outside it are left out)
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
@@ -282,7 +270,6 @@ struct GrParams {
   int groups;    // tiles of a CTA: ceil(tiles / ranks)
   int tma;       // every row is whole 16-byte vectors: boxes by TMA
   int words[4];  // otherwise: x, f, g, dout lie on 32-bit words
-  int aligned;   // and every row tensor written lies on a lane's boundaries
   unsigned long long wait_ns;  // limit of a wait
   int withhold;  // the bounded-wait test: the first tile's spans are not sent
 };
@@ -329,6 +316,38 @@ __device__ __forceinline__ void fetch_rows(uint32_t dst, const void* src, long l
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) st_shared_u32(dst + (r + k) * kRow + lane * 4, w[k]);
+    }
+  }
+}
+
+// Rows of results from shared memory to those of from .. to - 1 among t0 ..: by
+// words, whatever boundaries they lie on.  (A function of its own: in line it
+// costs the rows that leave as boxes one part in a hundred.)
+template <typename T, int N, int ROWS>
+__device__ __noinline__ void put_rows(uint32_t src, void* dst, long long stride, int t0, int from, int to, int c0, int C, int lane) {
+  constexpr int kRow = 32 * Lane<T, N>::kBytes;
+  const int r0 = from > t0 ? from - t0 : 0, r1 = to - t0 < ROWS ? to - t0 : ROWS;
+  src += r0 * kRow;
+  T* row = static_cast<T*>(dst) + (long long)(t0 + r0) * stride + c0;
+#pragma unroll 2
+  for (int r = r0; r < r1; ++r, row += stride, src += kRow) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < Lane<T, N>::kWords; ++i)
+        if (c0 + i * 32 + lane < C) reinterpret_cast<uint32_t*>(row)[i * 32 + lane] = ld_shared_u32(src + (i * 32 + lane) * 4);
+    } else {
+      const int left = C - c0 - 2 * lane;
+      uint16_t* to = reinterpret_cast<uint16_t*>(row) + 2 * lane;
+      const uint32_t own = ld_shared_u32(src + lane * 4);
+      if (reinterpret_cast<uintptr_t>(row) & 2) {  // the words lie an element ahead of the lanes'
+        const uint32_t before = __shfl_up_sync(0xffffffffu, own, 1);
+        if (left > 0 && lane > 0) *reinterpret_cast<uint32_t*>(to - 1) = __funnelshift_l(before, own, 16);
+        if (lane == 0) to[0] = (uint16_t)own;
+        if (left > 1 && (lane == 31 || left == 2)) to[1] = (uint16_t)(own >> 16);
+      } else {
+        if (left > 1) *reinterpret_cast<uint32_t*>(to) = own;
+        else if (left > 0) to[0] = (uint16_t)own;
+      }
     }
   }
 }
@@ -637,7 +656,6 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;  // channels of this lane
-  const bool whole = p.aligned && in == N;
   const int T_ = (int)a.T;
   unsigned char* const arrays = aligned_box(dyn);
   const uint32_t ring = smem_addr(arrays) + warp * (kArrays * kArray), staged = ring + 2 * kArray;
@@ -777,7 +795,9 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
       for (int k = 0; k < kGfRows; ++k)
         if (m.ends >> k & 1) L::store_state(a.s1 + (long long)sh.seqs[warp][kGfRows + k] * a.C + c, in, hl[k]);
     }
-    auto finish = [&](auto box) {
+    // (twice in the code: around one copy of it the compiler holds more at once,
+    // 197 us where these take 187)
+    auto finish = [&]() {
 #pragma unroll
       for (int k = 0; k < kGfRows; ++k) {
         if constexpr (GATE) {
@@ -786,18 +806,14 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
 #pragma unroll
           for (int q = 0; q < P; ++q) hl[k][q] = f2_mul(hl[k][q], f2_mul(g[q], f2_sigmoid<T>(g[q], &e)));
         }
-        if constexpr (box.value) {
-          L::stage(staged + lane * L::kBytes + k * kRow, hl[k]);
-        } else {
-          if (t0 + k >= first && t0 + k < last) L::store(static_cast<T*>(a.out) + (long long)(t0 + k) * a.os + c, in, whole, hl[k]);
-        }
+        L::stage(staged + lane * L::kBytes + k * kRow, hl[k]);
       }
     };
     // (a box leaves out rows behind the tensor's end, but not those outside every sequence)
     if (p.tma && t0 >= first && (t0 + kGfRows <= last || last == T_)) {
       if (lane == 0) bulk_wait_read();  // of the last tile's box
       __syncwarp();
-      finish(std::true_type{});
+      finish();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && t0 < T_) {
@@ -805,7 +821,11 @@ __global__ void __launch_bounds__(32 * kGfWarps, 4) gr_forward_kernel(const __gr
         bulk_commit();
       }
     } else {
-      finish(std::false_type{});
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+      finish();
+      __syncwarp();
+      put_rows<T, N, kGfRows>(staged, a.out, a.os, t0, first, last, c0, a.C, lane);
     }
     if constexpr (GATE) {
       __syncwarp();  // g has been read
@@ -837,7 +857,6 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 3 : 2) gr_back
   const int ranks = p.ranks, rank = ranks > 1 ? (int)cluster_ctarank() : 0;
   const int c0 = blockIdx.x / ranks * (32 * N), c = c0 + lane * N;
   const int in = a.C - c < 0 ? 0 : a.C - c < N ? a.C - c : N;
-  const bool whole = p.aligned && in == N;
   const int T_ = (int)a.T;
   unsigned char* const arrays = aligned_box(dyn);
   const uint32_t ring = smem_addr(arrays) + warp * (kArrays * kArray);
@@ -991,7 +1010,7 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 3 : 2) gr_back
 #pragma unroll
         for (int e = 0; e < P; ++e) ef[k][e] = hp[k][e] = f2_both(__int_as_float(0x7fc00000));
     }
-    // marks: a sequence begins or ends among the rows, or some are of none.
+    // marks: a sequence begins or ends among the rows.
     // (Which gradients are wanted does not choose the code: their last bits
     // must not depend on it.)
     auto finish = [&](auto marks) {
@@ -1027,37 +1046,30 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 3 : 2) gr_back
           if constexpr (GATE) vg[e] = f2_mul(vg[e], f2_fma(ga, hp[k][e], f2_mul(rest, x[e])));
           G[e] = f2_mul(ga, G[e]);
         }
-        if (p.tma && !kMarks) {
-          L::stage(at + k * kRow, vx);
-          L::stage(at + kArray + k * kRow, vf);
-          if constexpr (GATE) L::stage(at + 3 * kArray + k * kRow, vg);
-        } else if (t0 + k >= first && t0 + k < last) {
-          const long long t = t0 + k;
-          if (a.dx) L::store(static_cast<T*>(a.dx) + t * a.dxs + c, in, whole, vx);
-          if (a.df) L::store(static_cast<T*>(a.df) + t * a.dfs + c, in, whole, vf);
-          if constexpr (GATE) {
-            if (a.dg) L::store(static_cast<T*>(a.dg) + t * a.dgs + c, in, whole, vg);
-          }
-        }
+        L::stage(at + k * kRow, vx);
+        L::stage(at + kArray + k * kRow, vf);
+        if constexpr (GATE) L::stage(at + 3 * kArray + k * kRow, vg);
         if constexpr (kMarks) {
           if (a.ds0 && (m.starts >> k & 1)) L::store_state(a.ds0 + (long long)sh.seqs[warp][k] * a.C + c, in, G);
         }
       }
     };
-    if ((m.starts | m.ends) == 0 && t0 >= first && (t0 + kGbRows <= last || last == T_)) {
-      finish(std::false_type{});
-      if (p.tma) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && t0 < T_) {
-          if (a.dx) tma_store_2d(&p.out[0], c0, t0, ring);
-          if (a.df) tma_store_2d(&p.out[1], c0, t0, ring + kArray);
-          if (GATE && a.dg) tma_store_2d(&p.out[2], c0, t0, ring + 3 * kArray);
-          bulk_commit();
-        }
+    if ((m.starts | m.ends) == 0) finish(std::false_type{});
+    else finish(std::true_type{});
+    if (p.tma && t0 >= first && (t0 + kGbRows <= last || last == T_)) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && t0 < T_) {
+        if (a.dx) tma_store_2d(&p.out[0], c0, t0, ring);
+        if (a.df) tma_store_2d(&p.out[1], c0, t0, ring + kArray);
+        if (GATE && a.dg) tma_store_2d(&p.out[2], c0, t0, ring + 3 * kArray);
+        bulk_commit();
       }
     } else {
-      finish(std::true_type{});
+      __syncwarp();
+      if (a.dx) put_rows<T, N, kGbRows>(ring, a.dx, a.dxs, t0, first, last, c0, a.C, lane);
+      if (a.df) put_rows<T, N, kGbRows>(ring + kArray, a.df, a.dfs, t0, first, last, c0, a.C, lane);
+      if (GATE && a.dg) put_rows<T, N, kGbRows>(ring + 3 * kArray, a.dg, a.dgs, t0, first, last, c0, a.C, lane);
     }
     __syncwarp();  // the rows have been read
     fetch(i + 1);
@@ -1135,7 +1147,7 @@ bool make_rows_map(CUtensorMap* map, const void* p, int64_t stride, int64_t T, i
 // cluster's, and how many clusters of each size run at once.
 struct GrKernel {
   const void* kern;
-  int threads, rows, width, lane_bytes, smem, span_bytes;
+  int threads, rows, width, smem, span_bytes;
   SmemOptIn opt;
   std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];
 };
@@ -1226,15 +1238,11 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
   void* const out[3] = {backward ? a.dx : a.out, a.df, a.dg};
   const int64_t out_strides[3] = {backward ? a.dxs : a.os, a.dfs, a.dgs};
   p.tma = a.T > 0 && (int64_t)a.C * es % 16 == 0;  // (a box is cut off at 16 bytes, not at an element)
-  p.aligned = 1;
   for (int i = 0; i < 4; ++i) {
     p.tma = p.tma && rows_on(in[i], in_strides[i], es, 16);
     p.words[i] = rows_on(in[i], in_strides[i], es, 4);
   }
-  for (int i = 0; i < 3; ++i) {
-    p.tma = p.tma && rows_on(out[i], out_strides[i], es, 16);
-    p.aligned = p.aligned && rows_on(out[i], out_strides[i], es, k.lane_bytes);
-  }
+  for (int i = 0; i < 3; ++i) p.tma = p.tma && rows_on(out[i], out_strides[i], es, 16);
   for (int i = 0; i < 4 && p.tma; ++i)
     if (in[i]) p.tma = make_rows_map(&p.in[i], in[i], in_strides[i], a.T, a.C, es == 2, k.width, k.rows);
   for (int i = 0; i < 3 && p.tma; ++i)
@@ -1249,14 +1257,14 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
 template <typename T, bool GATE>
 cudaError_t launch_forward(const RecurrenceArgs& a) {
   using L = Lane<T, 2>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * kGfWarps, kGfRows, 32 * 2 * L::P, L::kBytes,
+  static GrKernel k{reinterpret_cast<const void*>(gr_forward_kernel<T, GATE>), 32 * kGfWarps, kGfRows, 32 * 2 * L::P,
                     kBoxAlign + kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_forward_kernel<T, GATE>, a);
 }
 template <typename T, bool GATE>
 cudaError_t launch_backward(const RecurrenceArgs& a) {
   using L = Lane<T, 2>;
-  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * kGbWarps, kGbRows, 32 * 2 * L::P, L::kBytes,
+  static GrKernel k{reinterpret_cast<const void*>(gr_backward_kernel<T, GATE>), 32 * kGbWarps, kGbRows, 32 * 2 * L::P,
                     kBoxAlign + kGrChunk * 32 * L::kBytes * (GATE ? 4 : 3), (int)sizeof(RankSpan<L::P>), {}, {}};
   return launch_gr(k, gr_backward_kernel<T, GATE>, a);
 }
