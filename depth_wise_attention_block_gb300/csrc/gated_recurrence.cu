@@ -21,8 +21,8 @@
 // e^-f and the state ahead of it are kept, the rest is formed again, because
 // there the registers decide how many warps there are (80 a thread, 24 warps
 // to an SM; 4 warps of 16 rows at 128: 248 us where forward and backward
-// together took 230).  The states ahead of the tiles, which the forward kept, let it
-// form h_{t-1} without a second scan over the rows.
+// together took 230).  The states ahead of the tiles, which the forward kept,
+// let it form h_{t-1} without a second scan over the rows.
 //
 // Where the slabs do not fill the GPU, a cluster of R CTAs shares a slab: they
 // take R neighbouring tiles at a time and send the tiles' (A, B) through
@@ -30,10 +30,11 @@
 // (16384 x 7168), 197 where 39 (5003 x 1000).
 //
 // Rows of whole 16-byte vectors move by TMA, a box to a warp, and the results
-// go out the same way; rows on 32-bit words by cp.async (103 us where the
-// boxes take 72, 8192 x 4096 bf16), bf16 rows on single elements by registers
-// (205 us); these leave through shared memory by words.  The boxes cost a lane no address: the warps' instructions are
-// what bounds the kernels once the traffic is down to one pass.
+// go out the same way, which costs a lane no address: the warps' instructions
+// are what bounds the kernels once every tensor passes once.  Rows on 32-bit
+// words come by cp.async (8192 x 4094 bf16: 132 us where 4096 channels take
+// 72), bf16 rows on single elements through registers (4095: 205); both leave
+// by words.
 //
 // Measured, gate and all gradients, HBM traffic of one pass over each tensor:
 // 16384 x 7168 bf16 forward 187 us, 5.0 TB/s, backward 459 us, 3.6 TB/s;
