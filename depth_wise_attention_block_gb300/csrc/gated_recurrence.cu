@@ -1193,7 +1193,7 @@ struct GrKernel {
   const void* kern;
   int threads, rows, width, smem, span_bytes;
   SmemOptIn opt;
-  std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];
+  std::atomic<int> clusters[SmemOptIn::kMaxDevices][kGrMaxCluster + 1];  // and one (0: not asked yet)
 };
 
 cudaLaunchConfig_t gr_config(const GrKernel& k, int64_t slabs, int ranks, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -1232,7 +1232,7 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   std::atomic<int>* slot = dev >= 0 && dev < SmemOptIn::kMaxDevices ? &k.clusters[dev][ranks] : nullptr;
-  if (slot && (*n = slot->load()) > 0) return cudaSuccess;
+  if (slot && (*n = slot->load() - 1) >= 0) return cudaSuccess;
   e = allow_cluster(k, ranks);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
@@ -1245,8 +1245,7 @@ cudaError_t clusters_at_once(GrKernel& k, int ranks, int* n) {
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, k.kern, k.threads, cfg.dynamicSmemBytes);
     *n *= di.sm_count;
   }
-  if (e == cudaSuccess && *n < 1) *n = 1;
-  if (e == cudaSuccess && slot) slot->store(*n);
+  if (e == cudaSuccess && slot) slot->store(*n + 1);
   return e;
 }
 
@@ -1266,6 +1265,8 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
     int n = 0;
     e = clusters_at_once(k, r, &n);
     if (e != cudaSuccess) return e;
+    if (n < 1 && r > 1) continue;  // not to be had here
+    if (n < 1) n = 1;
     const double cost = (double)((slabs + n - 1) / n) * (double)((tiles + r - 1) / r);
     if (r == 1 || cost < 0.9 * least) {
       least = cost;
