@@ -14,10 +14,11 @@
 // hold a lane's sums of the gain and bias gradients.  Rows wider than that are
 // read once per pass by ln_any_kernel; what this saves, 16384 x 7168 bf16: 228
 // us there, 81 here (5.8 TB/s, the copy runs at 6.8); backward of 8192 x 7168:
-// 426 and 87 us (4.1 TB/s).  What bounds them now: the barriers of the row's
-// sums (two forward, two backward), and backward its issue slots: every pass
-// unpacks x and dy again.  64 rows take the launch and one row's chain of
-// load, sums and store: 6.5 us between the calls of a program.
+// 426 and 79 us (4.4 TB/s; 73 without the gain and bias gradients, whose
+// partial rows a second launch adds).  What bounds them now: the barriers of
+// the row's sums (two forward, two backward), and backward its issue slots:
+// every pass unpacks x and dy again.  64 rows take the launch and one row's
+// chain of load, sums and store: 6.5 us between the calls of a program.
 #include <math.h>
 
 #include "attnres.h"
@@ -548,20 +549,33 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   float* sums = reinterpret_cast<float*>(dyn);  // [groups][2][d]
   if constexpr (VEC) cp_async_wait<0>();
   __syncthreads();  // gain and ring are done with
+  float* own = groups > 1 ? sums + group * 2 * p.d : part;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i)
+  for (int i = 0; i < VPL; ++i) {
+    float a[S::V], b[S::V];
 #pragma unroll
-    for (int k = 0; k < S::V; ++k) {
-      float a[2], b[2];
-      f2_unpack(dg[i][k / 2], a[0], a[1]);
-      f2_unpack(db[i][k / 2], b[0], b[1]);
-      if (seg.has(i, k)) {
-        const int c = seg.at + S::offset(i, k);
-        float* at = groups > 1 ? sums + group * 2 * p.d : part;
-        at[c] = a[k & 1];
-        at[p.d + c] = b[k & 1];
-      }
+    for (int k = 0; k < P; ++k) {
+      f2_unpack(dg[i][k], a[2 * k], a[2 * k + 1]);
+      f2_unpack(db[i][k], b[2 * k], b[2 * k + 1]);
     }
+    if constexpr (VEC) {  // (a row of sums is whole vectors too)
+      if (seg.has(i)) {
+        float* at = own + seg.at + S::offset(i, 0);
+#pragma unroll
+        for (int k = 0; k < S::V; k += 4) {
+          *reinterpret_cast<float4*>(at + k) = make_float4(a[k], a[k + 1], a[k + 2], a[k + 3]);
+          *reinterpret_cast<float4*>(at + p.d + k) = make_float4(b[k], b[k + 1], b[k + 2], b[k + 3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < S::V; ++k)
+        if (seg.has(i, k)) {
+          own[seg.at + S::offset(i, k)] = a[k];
+          own[p.d + seg.at + S::offset(i, k)] = b[k];
+        }
+    }
+  }
   if (groups > 1) {  // in order: the sums do not depend on timing
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * p.d; c += nthreads) {
