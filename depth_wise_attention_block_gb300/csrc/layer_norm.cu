@@ -14,10 +14,10 @@
 // hold a lane's sums of the gain and bias gradients.  Rows wider than that are
 // read once per pass by ln_any_kernel; what this saves, 16384 x 7168 bf16: 228
 // us there, 81 here (5.8 TB/s, the copy runs at 6.8); backward of 8192 x 7168:
-// 426 and 79 us (4.4 TB/s; 73 without the gain and bias gradients, whose
+// 426 and 76 us (4.7 TB/s; 69 without the gain and bias gradients, whose
 // partial rows a second launch adds).  What bounds them now: the barriers of
-// the row's sums (two forward, two backward), and backward its issue slots:
-// every pass unpacks x and dy again.  64 rows take the launch and one row's
+// the rows' sums (forward two a row, backward one for two rows), and backward
+// its issue slots: every pass unpacks x and dy again.  64 rows take the launch and one row's
 // chain of load, sums and store: 6.5 us between the calls of a program.
 #include <math.h>
 
@@ -230,14 +230,14 @@ struct Segment {
   }
 };
 
-// Sums of N values (up to 8) over a row's warps, the same in every thread of
+// Sums of N values (up to W) over a row's warps, the same in every thread of
 // the row, in a fixed order.  Several values are summed over a warp by halves:
 // after the first exchanges each lane carries one of them.  One barrier: the
 // caller alternates between two buffers.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[8], int warps, int group, int warp, int lane) {
+template <int N, int W>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*red)[W], int warps, int group, int warp, int lane) {
   constexpr uint32_t kAll = 0xffffffffu;
-  constexpr int kValues = N == 1 ? 1 : N == 2 ? 2 : N <= 4 ? 4 : 8, kLanes = 32 / kValues;  // lanes that end up with the same value
+  constexpr int kValues = N == 1 ? 1 : N == 2 ? 2 : N <= 4 ? 4 : N <= 8 ? 8 : 16, kLanes = 32 / kValues;  // lanes that end up with the same value
   float a[kValues];
 #pragma unroll
   for (int i = 0; i < kValues; ++i) a[i] = i < N ? v[i < N ? i : 0] : 0.f;
@@ -373,14 +373,14 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps, VPL > 8 ? 1 : 2) ln_row_kern
 // Its backward: a lane also keeps its channels' sums of dy h and dy over its
 // group's rows, which are taken ROWS at a time (their sums cross the warps
 // together).
-constexpr int kLnTakes = 3;  // of the ring: one at work, two on their way
+constexpr int kLnTakes = 3;  // of the ring: one at work, the next, and one on its way
 template <typename T, int VPL, int ROWS, bool VEC>
 __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const __grid_constant__ LnParams p) {
   using S = Segment<T, VEC>;
   constexpr int P = S::P;
   constexpr uint32_t kRow = 2 * VPL * 512, kTake = ROWS * kRow;  // of a warp's ring
   extern __shared__ __align__(16) unsigned char dyn[];  // gain; VEC: [warp][kLnTakes][ROWS][x, dy][VPL][lane] vectors; at the end: sums
-  __shared__ __align__(16) float red[2][kLnMaxWarps][8];
+  __shared__ __align__(16) float red[2][kLnMaxWarps][16];
   const int warps = p.warps, lane = threadIdx.x & 31, nthreads = (int)blockDim.x;
   const int group = (threadIdx.x >> 5) / warps, groups = (nthreads >> 5) / warps, warp = (threadIdx.x >> 5) % warps;
   const S seg(warp, warps, lane, p.d);
@@ -436,6 +436,34 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   for (int i = 0; i < VPL; ++i)
 #pragma unroll
     for (int k = 0; k < P; ++k) dg[i][k] = db[i][k] = 0;
+  // sums of a take's x, behind its other sums
+  auto add_x = [&](auto x, float (&s)[5 * ROWS]) {
+    uint64_t f[P], sx[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) sx[r] = 0;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) {
+        S::unpack(x(r, i), f);
+#pragma unroll
+        for (int k = 0; k < P; ++k) sx[r] = f2_add(sx[r], f[k]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s[4 * ROWS + r] = f2_hsum(sx[r]);
+  };
+  float m[ROWS];  // the take's means
+  [[maybe_unused]] int turn = 0;
+  if constexpr (VEC) {
+    float s[5 * ROWS], s1[ROWS];
+    add_x([&](int r, int i) { return ld_shared_v4(ring + r * kRow + i * 512); }, s);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) s1[r] = s[4 * ROWS + r];
+    row_sums<ROWS>(s1, red[1] + group * warps, warps, group, warp, lane);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) m[r] = s1[r] * p.inv_d;
+  }
   for (; t < p.T; t += ROWS * step) {
     // rows are read from the ring again for every pass (their registers are the sums'); single channels stay in registers
     uint4 held_x[VEC ? 1 : ROWS][VEC ? 1 : VPL], held_dy[VEC ? 1 : ROWS][VEC ? 1 : VPL];
@@ -449,7 +477,6 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
     };
     if constexpr (VEC) {
       fetch();  // into the slot of the last take
-      cp_async_wait<kLnTakes - 1>();
     } else {
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
@@ -463,28 +490,17 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
         dr += d_step;
       }
     }
-    // (behind the last row a take goes through the motions with what its slot held)
     uint64_t f[P], g[P], gain[P];
-    float s1[ROWS], s2[4 * ROWS], m[ROWS];
-    {
-      uint64_t sx[ROWS];
+    float s[5 * ROWS];  // of the take (behind the last row it goes through the motions with what its slot held), and sums of the next one's x
+    if constexpr (!VEC) {
+      add_x(x, s);
+      float s1[ROWS];
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) sx[r] = 0;
+      for (int r = 0; r < ROWS; ++r) s1[r] = s[4 * ROWS + r];
+      row_sums<ROWS>(s1, red[1] + group * warps, warps, group, warp, lane);
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-          S::unpack(x(r, i), f);
-#pragma unroll
-          for (int k = 0; k < P; ++k) sx[r] = f2_add(sx[r], f[k]);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < ROWS; ++r) s1[r] = f2_hsum(sx[r]);
+      for (int r = 0; r < ROWS; ++r) m[r] = s1[r] * p.inv_d;
     }
-    row_sums<ROWS>(s1, red[0] + group * warps, warps, group, warp, lane);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) m[r] = s1[r] * p.inv_d;
     {
       uint64_t sz[ROWS], sq[ROWS], sn[ROWS], sw[ROWS];
 #pragma unroll
@@ -509,20 +525,33 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
       }
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        s2[4 * r] = f2_hsum(sz[r]);
-        s2[4 * r + 1] = f2_hsum(sq[r]);
-        s2[4 * r + 2] = f2_hsum(sw[r]);
-        s2[4 * r + 3] = f2_hsum(sn[r]);
+        s[4 * r] = f2_hsum(sz[r]);
+        s[4 * r + 1] = f2_hsum(sq[r]);
+        s[4 * r + 2] = f2_hsum(sw[r]);
+        s[4 * r + 3] = f2_hsum(sn[r]);
       }
     }
-    row_sums<4 * ROWS>(s2, red[1] + group * warps, warps, group, warp, lane);
+    if constexpr (VEC) {  // the next take's means come by the same barrier (by one of their own: 79 us where 76)
+      cp_async_wait<kLnTakes - 2>();
+      const uint32_t next = slot + kTake == kLnTakes * kTake ? 0 : slot + kTake;
+      add_x([&](int r, int i) { return ld_shared_v4(ring + next + r * kRow + i * 512); }, s);
+      row_sums<5 * ROWS>(s, red[turn] + group * warps, warps, group, warp, lane);
+      turn ^= 1;
+    } else {
+      float s2[4 * ROWS];
+#pragma unroll
+      for (int k = 0; k < 4 * ROWS; ++k) s2[k] = s[k];
+      row_sums<4 * ROWS>(s2, red[0] + group * warps, warps, group, warp, lane);
+#pragma unroll
+      for (int k = 0; k < 4 * ROWS; ++k) s[k] = s2[k];
+    }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       if (r > 0 && t + r * step >= p.T) break;
-      const float delta = s2[4 * r] * p.inv_d;
-      const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s2[4 * r + 1] * p.inv_d), 0.f) + p.eps);
-      const float mn = s2[4 * r + 3] * p.inv_d;
-      const float mh = (s2[4 * r + 2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
+      const float delta = s[4 * r] * p.inv_d;
+      const float rstd = rsqrtf(fmaxf(fmaf(-delta, delta, s[4 * r + 1] * p.inv_d), 0.f) + p.eps);
+      const float mn = s[4 * r + 3] * p.inv_d;
+      const float mh = (s[4 * r + 2] * p.inv_d - delta * mn) * rstd;  // mean(n h)
       // h = (x - m) r - delta r,  dx = (n r - mn r) - h mh r
       const uint64_t minus_m = f2_both(-m[r]), r2 = f2_both(rstd), shift = f2_both(-delta * rstd), n0 = f2_both(-mn * rstd), h0 = f2_both(-mh * rstd);
 #pragma unroll
@@ -541,6 +570,10 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
         if (p.out) seg.template store<true>(out, i, f);
       }
       out += out_step;
+    }
+    if constexpr (VEC) {
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) m[r] = s[4 * ROWS + r] * p.inv_d;
     }
     slot = slot + kTake == kLnTakes * kTake ? 0 : slot + kTake;
   }
@@ -620,6 +653,7 @@ __global__ void __launch_bounds__(32 * kLnRuns) ln_dgain_kernel(const float* par
 struct LnPlan {
   int vpl, warps, groups, smem, per_sm;
 };
+int ln_fixed_smem(bool backward) { return backward ? 2048 : 1024; }  // the sums' buffers
 LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceInfo& di) {
   constexpr int kForwardVec[3] = {2, 8, 16}, kForward[3] = {1, 2, 4}, kBackward[3] = {1, 2, 4};
   const int V = 16 / es, n = 3;
@@ -642,9 +676,9 @@ LnPlan ln_plan(int64_t T, int d, int es, bool vec, bool backward, const DeviceIn
       const int64_t ring = vec ? warps * groups * vectors_of_warp * 512 : 0;
       const int64_t sums = backward && groups > 1 ? (int64_t)groups * 2 * d * 4 : 0;
       const int64_t smem = vectors + ring > sums ? vectors + ring : sums;
-      if (smem + 1024 > di.max_smem_optin) continue;
+      if (smem + ln_fixed_smem(backward) > di.max_smem_optin) continue;
       // the variants with most registers to a thread run as one CTA to an SM
-      const bool one = vpl[i] >= (backward ? 2 : 16) || 2 * (smem + 512 + 1024) > di.max_smem_optin + 1024;
+      const bool one = vpl[i] >= (backward ? 2 : 16) || 2 * (smem + 512 + ln_fixed_smem(backward)) > di.max_smem_optin + 1024;
       return {vpl[i], warps, groups, (int)smem, one ? 1 : 2};
     }
   }
@@ -729,7 +763,7 @@ cudaError_t launch_layer_norm(const LayerNormArgs& a) {
     p.warps = k.warps;
     const int64_t need = (a.T + k.groups - 1) / k.groups, cap = (int64_t)di.sm_count * k.per_sm;
     grid = (int)(need < cap ? need : cap);
-    const int most = di.max_smem_optin - 1024;  // (beside the sums' buffers)
+    const int most = di.max_smem_optin - ln_fixed_smem(a.backward);
     e = bf16 ? launch_rows<bf16_t>(a, p, k, vec, grid, most) : launch_rows<float>(a, p, k, vec, grid, most);
   } else {
     const int64_t cap = (int64_t)di.sm_count * kLnBlocksPerSm;
