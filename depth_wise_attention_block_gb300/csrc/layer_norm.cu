@@ -199,8 +199,8 @@ struct Segment {
   // A vector of fp32 in shared memory, as the lanes read it without conflicts:
   // the first four channels of every vector, then the other four (V = 8).
   static __device__ __forceinline__ int place(int c, int d) { return VEC && V == 8 ? (c >> 2 & 1) * (d >> 1) + (c >> 3) * 4 + (c & 3) : c; }
-  // the lane's channels of it; `first`: at place(at).  (Where a lane has no
-  // channel it reads what lies there, inside the CTA's shared memory.)
+  // the lane's channels of it; `first`: at place(at).  (VEC: only where the lane
+  // has channels, something else lies behind them.)
   __device__ __forceinline__ void load_f32(const float* first, int i, int d, uint64_t (&f)[P]) const {
     if constexpr (VEC) {
 #pragma unroll
@@ -508,10 +508,13 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (VPL > 1 && i >= seg.held) break;
+        // (where a lane has no channel there is no gain either: behind the gains
+        // lies another row's x, whose infinities a product with zero would keep)
+        if (VEC && !seg.has(i)) break;
         seg.load_f32(gains, i, p.d, gain);
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          seg.template center<true>(x(r, i), f2_both(-m[r]), i, f);
+          seg.template center<!VEC>(x(r, i), f2_both(-m[r]), i, f);
           S::unpack(dy(r, i), g);
 #pragma unroll
           for (int k = 0; k < P; ++k) {
@@ -557,6 +560,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
 #pragma unroll
       for (int i = 0; i < VPL; ++i) {
         if (VPL > 1 && i >= seg.held) break;
+        if (VEC && !seg.has(i)) break;
         seg.load_f32(gains, i, p.d, gain);
         S::unpack(x(r, i), f);
         S::unpack(dy(r, i), g);
@@ -567,7 +571,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
           db[i][k] = f2_add(db[i][k], g[k]);
           f[k] = f2_fma(h, h0, f2_fma(f2_mul(g[k], gain[k]), r2, n0));
         }
-        if (p.out) seg.template store<true>(out, i, f);
+        if (p.out) seg.template store<!VEC>(out, i, f);
       }
       out += out_step;
     }
