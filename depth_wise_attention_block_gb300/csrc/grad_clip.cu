@@ -169,15 +169,27 @@ __global__ void __launch_bounds__(kClipThreads) clip_total_kernel(const __grid_c
   if (threadIdx.x == 0) *p.norm = (float)norm;
 }
 
+// max_norm / norm as a product of two fp32 numbers. Below 2^-126 one would lose
+// digits, or be zero, although the results are numbers of fp32: the first is
+// then a power of two, by which no value loses anything that its result shows
+// (what is rounded away of it, 2^-150 at most, meets a second one below 2^-26).
+struct Factor {
+  float first, second;
+  __device__ __forceinline__ explicit Factor(double ratio)
+      : first(ratio >= 0x1p-126 ? 1.f : ratio >= 0x1p-226 ? 0x1p-100f : 0x1p-149f), second((float)(ratio / (double)first)) {}
+  __device__ __forceinline__ bool one() const { return second == 1.f; }
+  __device__ __forceinline__ float times(float v) const { return v * first * second; }
+};
+
 template <typename T>
-__device__ __forceinline__ void scale_chunk(const void* in, void* out, long long n, int c, bool scalar, float factor) {
+__device__ __forceinline__ void scale_chunk(const void* in, void* out, long long n, int c, bool scalar, const Factor& factor) {
   constexpr int E = Vec16<T>::kElems;
   const T* x = static_cast<const T*>(in);
   T* y = static_cast<T*>(out);
   if (scalar) {
     for (int i = threadIdx.x; i < kClipChunk * E; i += kClipThreads) {
       const long long at = (long long)c * kClipChunk * E + i;
-      if (at < n) store_elem(y + at, load_elem(x + at) * factor);
+      if (at < n) store_elem(y + at, factor.times(load_elem(x + at)));
     }
     return;
   }
@@ -195,13 +207,13 @@ __device__ __forceinline__ void scale_chunk(const void* in, void* out, long long
       float e[E];
       Vec16<T>::unpack(v[k], e);
 #pragma unroll
-      for (int i = 0; i < E; ++i) e[i] *= factor;
+      for (int i = 0; i < E; ++i) e[i] = factor.times(e[i]);
       yv[v0 + k * kClipThreads] = Vec16<T>::pack(e);
     }
   if (c == 0) {
-    if ((int)threadIdx.x < head) store_elem(y + threadIdx.x, load_elem(x + threadIdx.x) * factor);
+    if ((int)threadIdx.x < head) store_elem(y + threadIdx.x, factor.times(load_elem(x + threadIdx.x)));
     const long long tail = head + nv * E + threadIdx.x;
-    if (tail < n) store_elem(y + tail, load_elem(x + tail) * factor);
+    if (tail < n) store_elem(y + tail, factor.times(load_elem(x + tail)));
   }
 }
 
@@ -213,14 +225,14 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   const double norm = total_norm(p, red);
   if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
   // (a norm that is not finite scales nothing)
-  const float factor = norm > (double)p.max_norm && isfinite(norm) ? (float)((double)p.max_norm / norm) : 1.f;
+  const Factor factor(norm > (double)p.max_norm && isfinite(norm) ? (double)p.max_norm / norm : 1.0);
   const int chunks = l.first[l.count];
   const int c0 = (int)((long long)chunks * blockIdx.x / gridDim.x), c1 = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
   if (c0 >= c1) return;
   int i = find_tensor(l, c1 - 1);
   for (int c = c1 - 1; c >= c0; --c) {  // what was read last may still be in L2
     while (c < l.first[i]) --i;
-    if (factor == 1.f && l.in[i] == l.out[i]) continue;
+    if (factor.one() && l.in[i] == l.out[i]) continue;
     const bool scalar = l.kind[i] & kScalar;
     if (l.kind[i] & kBf16) scale_chunk<bf16_t>(l.in[i], l.out[i], l.n[i], c - l.first[i], scalar, factor);
     else scale_chunk<float>(l.in[i], l.out[i], l.n[i], c - l.first[i], scalar, factor);
