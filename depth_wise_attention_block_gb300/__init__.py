@@ -994,7 +994,8 @@ def attnres_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, norm: torc
     grads: contiguous float32 or bfloat16 tensors on one device; outs: where
     the results go, tensor by tensor (None: in place, and nothing is written
     where nothing is clipped; max_norm infinity: only the norm).  A norm that
-    is not finite scales nothing.  workspace: a device buffer of
+    is not finite scales nothing; a finite one above fp32's numbers is
+    reported as the largest of them.  workspace: a device buffer of
     attnres_grad_clip_workspace_size() bytes (allocated here through torch
     when None).
     """

@@ -16,6 +16,7 @@
 // (four CTAs: 854; twice the vectors to a thread: no faster).  94 rows of 7168
 // in fp32: a few us on the GPU, 8 us in the C call and some 70 in the Python
 // binding, which has to look at 188 tensors.
+#include <float.h>
 #include <math.h>
 
 #include "attnres.h"
@@ -161,12 +162,18 @@ __device__ __forceinline__ double total_norm(const ClipParams& p, double* red) {
   return sqrt(block_sum(s, red));
 }
 
+// what the caller reads: a norm that is finite but above fp32's numbers is the
+// largest of them (an infinity says that nothing was scaled)
+__device__ __forceinline__ void put_norm(float* to, double norm) {
+  *to = isfinite(norm) ? (float)fmin(norm, (double)FLT_MAX) : (float)norm;
+}
+
 __global__ void __launch_bounds__(kClipThreads) clip_total_kernel(const __grid_constant__ ClipParams p) {
   __shared__ double red[kClipThreads / 32];
   pdl_wait();
   pdl_trigger();
   const double norm = total_norm(p, red);
-  if (threadIdx.x == 0) *p.norm = (float)norm;
+  if (threadIdx.x == 0) put_norm(p.norm, norm);
 }
 
 // max_norm / norm as a product of two fp32 numbers. Below 2^-126 one would lose
@@ -223,7 +230,7 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
   const double norm = total_norm(p, red);
-  if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) *p.norm = (float)norm;
+  if (p.norm && blockIdx.x == 0 && threadIdx.x == 0) put_norm(p.norm, norm);
   // (a norm that is not finite scales nothing)
   const Factor factor(norm > (double)p.max_norm && isfinite(norm) ? (double)p.max_norm / norm : 1.0);
   const int chunks = l.first[l.count];

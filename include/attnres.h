@@ -845,7 +845,9 @@ int attnres_gated_recurrence_step(const void* x, int64_t x_stride, const void* f
  * and their clipping:
  *   norm = sqrt(sum over all tensors of g^2)
  *   out = g * (max_norm / norm) where norm > max_norm, else g
- * A norm that is not finite scales nothing: out = g, and out_norm says so.
+ * A norm that is not finite (a gradient is an infinity or NaN) scales nothing:
+ * out = g, and out_norm says so.  A finite norm above fp32's numbers clips like
+ * any other; out_norm is then the largest of them (3.4e38).
  * grads       host array of n device pointers, contiguous tensors
  * outs        host array of n device pointers, or NULL (only the norm).
  *             outs[i] may be grads[i] itself (in place: nothing is written

@@ -1,5 +1,5 @@
-"""attnres_grad_clip where max_norm / norm leaves fp32, against its fp64
-statement.
+"""attnres_grad_clip where max_norm / norm, or the norm itself, leaves fp32,
+against its fp64 statement.
 
 Tolerances, derived before any run: the norm is off by 19 2^-24 of itself and a
 value by that, three fp32 roundings, its own (u: bf16 2^-8, fp32 2^-24) and a
@@ -14,6 +14,7 @@ pytestmark = pytest.mark.gpu
 N_ERR = 19 * 2.0 ** -24
 U = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
 STEP = {torch.bfloat16: 2.0 ** -133, torch.float32: 2.0 ** -149}
+FLT_MAX = float(np.finfo(np.float32).max)
 # single elements ahead of a boundary, whole vectors, several chunks, tails
 SIZES = [1, 7, 4096, 70001, 9]
 
@@ -69,3 +70,22 @@ def test_small_gradients_keep_their_digits(A, dts, scale):
         grads = _grads(dts, scale)
         norm, want = _check(A, grads, max_norm, [torch.empty_like(t) for t in grads])
         assert abs(norm - want) <= N_ERR * want + 2.0 ** -149
+
+
+@pytest.mark.parametrize("dts", DTYPES)
+@pytest.mark.parametrize("max_norm", [1e38, 1.0, 1e-6])
+def test_a_norm_above_fp32(A, dts, max_norm):
+    """Finite gradients whose norm fp32 does not hold are clipped; the norm is
+    reported as fp32's largest number, so infinity and NaN still say that
+    nothing was scaled."""
+    grads = _grads(dts, 1e38)
+    norm, want = _check(A, grads, max_norm, [torch.empty_like(t) for t in grads])
+    assert want > 1e40 and norm == FLT_MAX
+    alone = torch.zeros(1, device="cuda")
+    before = [t.clone() for t in grads]
+    A.attnres_grad_clip(grads, float("inf"), alone)
+    assert float(alone) == FLT_MAX and all(torch.equal(t, b) for t, b in zip(grads, before))
+    grads[2][5] = float("inf")
+    before = [t.clone() for t in grads]
+    A.attnres_grad_clip(grads, max_norm, alone)
+    assert float(alone) == float("inf") and all(torch.equal(t, b) for t, b in zip(grads, before))
