@@ -1071,6 +1071,7 @@ __global__ void __launch_bounds__(32 * kGbWarps, sizeof(T) == 2 ? 3 : 2) gr_back
       if (a.dx) put_rows<T, N, kGbRows>(ring, a.dx, a.dxs, t0, first, last, c0, a.C, lane);
       if (a.df) put_rows<T, N, kGbRows>(ring + kArray, a.df, a.dfs, t0, first, last, c0, a.C, lane);
       if (GATE && a.dg) put_rows<T, N, kGbRows>(ring + 3 * kArray, a.dg, a.dgs, t0, first, last, c0, a.C, lane);
+      if (p.tma) fence_proxy_async_smem();  // the next boxes land where these gradients were written
     }
     __syncwarp();  // the rows have been read
     fetch(i + 1);
