@@ -771,7 +771,7 @@ int attnres_layer_sources(const attnres_state* st, int layer_idx, const void** o
   int rc = check_state(st);
   if (rc) return rc;
   if (!out_ptrs || !out_S) return fail(ATTNRES_EINVAL, "NULL output");
-  const int L = st->num_layers, B = st->block_size;
+  const int L = st->num_layers;
   if (layer_idx < 1 || layer_idx > L + 1) return fail(ATTNRES_EINVAL, "layer_idx %d outside 1..L+1", layer_idx);
   if (st->folded != layer_idx - 1)
     return fail(ATTNRES_ESTATE, "layer %d needs %d folded layer outputs, state has %d", layer_idx, layer_idx - 1,

@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(32 * kLnMaxWarps) ln_row_backward_kernel(const
   }
   for (; t < p.T; t += ROWS * step) {
     // rows are read from the ring again for every pass (their registers are the sums'); single channels stay in registers
-    uint4 held_x[VEC ? 1 : ROWS][VEC ? 1 : VPL], held_dy[VEC ? 1 : ROWS][VEC ? 1 : VPL];
+    uint4 held_x[VEC ? 1 : ROWS][VEC ? 1 : VPL] = {}, held_dy[VEC ? 1 : ROWS][VEC ? 1 : VPL] = {};
     auto x = [&](int r, int i) {
       if constexpr (VEC) return ld_shared_v4(ring + slot + r * kRow + i * 512);
       else return held_x[r][i];
