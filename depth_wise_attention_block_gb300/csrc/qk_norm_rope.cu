@@ -139,27 +139,12 @@ struct Pairs<float, INTER> {
   }
 };
 
-__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
 // each pair (x, y) turned by (c, s)
 __device__ __forceinline__ void rotate2(uint64_t& x, uint64_t& y, uint64_t c, uint64_t s) {
   const uint64_t minus = f2_pack(-1.f, -1.f);
   const uint64_t ys = f2_mul(f2_mul(y, s), minus), xs = f2_mul(x, s);
   x = f2_fma(x, c, ys);
   y = f2_fma(y, c, xs);
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-  const int bytes = in ? 16 : 0;  // none: zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // INTER pairs channels (2i, 2i + 1), otherwise (i, i + rot/2).
