@@ -284,7 +284,11 @@ def clip_grad_norm(leaves, max_norm: float) -> torch.Tensor:
     """The 2-norm [1] float32 of all the gradients that `leaves` hold, which are
     then clipped in place to max_norm (attnres_grad_clip).  Nothing is copied to
     the host.  A gradient that is not contiguous is replaced by a contiguous
-    copy first."""
+    copy first.
+
+    Not as in torch.nn.utils.clip_grad_norm_: the factor is max_norm / norm
+    without an addend, a norm that is not finite leaves the gradients as they
+    are, and leaves without any gradient are a ValueError."""
     leaves = [leaves] if isinstance(leaves, torch.Tensor) else list(leaves)
     grads = []
     for p in {id(p): p for p in leaves}.values():  # a leaf named twice counts once

@@ -26,8 +26,8 @@
 //
 // Where the slabs do not fill the GPU, a cluster of R CTAs shares a slab: they
 // take R neighbouring tiles at a time and send the tiles' (A, B) through
-// distributed shared memory.  With one CTA to a slab instead: 441 us where 189
-// (16384 x 7168), 197 where 39 (5003 x 1000).
+// distributed shared memory.  With one CTA to a slab instead: 427 us where 187
+// (16384 x 7168), 195 where 38 (5003 x 1000).
 //
 // Rows of whole 16-byte vectors move by TMA, a box to a warp, and the results
 // go out the same way, which costs a lane no address: the warps' instructions
@@ -36,15 +36,19 @@
 // 72), bf16 rows on single elements through registers (4095: 205); both leave
 // by words.
 //
-// Measured, gate and all gradients, HBM traffic of one pass over each tensor:
+// All figures here are single calls with cold caches; among other calls the
+// forward of 16384 x 7168 takes 182 us and that of 5003 x 1000 30.  Gate and all
+// gradients, HBM traffic of one pass over each tensor:
 // 16384 x 7168 bf16 forward 187 us, 5.0 TB/s, backward 459 us, 3.6 TB/s;
 // 8192 x 4096 bf16 in 5 sequences 72 us, 3.7 TB/s, and 140 us, 3.4 TB/s; the
-// same of fp32 99 us, 5.4 TB/s, and 190 us, 4.9 TB/s (the copy: 6.8).  What
+// same of fp32 99 us, 5.4 TB/s, and 191 us, 4.9 TB/s (the copy: 6.8).  What
 // bounds them: for each pair of channels some 75 instructions forward and 130
-// backward, at 41 % and about half of the issue slots, the rest lost to the
-// latency of a warp's own chain with 16 and 24 warps to an SM and to fetching
-// instructions (a second form of the backward's stores beside the boxes cost a
-// tenth without running).
+// backward, at 51 % of the issue slots (forward of 8192 x 4096: 39 %), the rest
+// lost to the latency of a warp's own chain with at most 16 and 24 warps to an SM
+// and to fetching instructions (a second form of the backward's stores beside the
+// boxes cost a tenth without running).  And not every place on the SMs is taken:
+// the CTAs of 16384 x 7168 fill 0.92 of them, those of 8192 x 4096 0.84 in both
+// directions, with SMs that hold none beside full ones.
 #include <limits.h>
 #include <math.h>
 
@@ -1091,7 +1095,9 @@ __device__ __forceinline__ void store_channels(void* at, long long i, const floa
 // before the other rows' slots are looked at.  64 rows of 7168 bf16 channels
 // with a gate move 7.3 MB, 1.1 us of HBM; in a graph of such calls one takes 2.4
 // us, which is its launch and one chain of loads (128 rows in fp32: 5.5 us for
-// 22 MB), a call from a program 9.5, most of it the binding's.
+// 22 MB), a call from a program 9.5, most of it the binding's.  (Every CTA reads
+// all B slots to find its row's like: nothing for hundreds of rows, 256 turns of
+// its loop for 65535.)
 template <typename T, int V>
 __global__ void __launch_bounds__(kGsThreads) gr_step_kernel(const __grid_constant__ RecurrenceStepArgs p) {
   __shared__ int next_row;
@@ -1242,7 +1248,7 @@ cudaError_t launch_gr(GrKernel& k, void (*kern)(A...), const RecurrenceArgs& a) 
   const int64_t tiles = (a.T + kGrChunk - 1) / kGrChunk, slabs = (a.C + k.width - 1) / k.width;
   // CTAs to a slab: the smallest cluster that takes off a tenth of the time
   // (rounds of clusters x tiles of a CTA) against each smaller one.  (5003 x
-  // 1000, fp32: 39 us with up to 16 CTAs, 48 with up to 8; 16384 x 7168 takes
+  // 1000, fp32: 38 us with up to 16 CTAs, 48 with up to 8; 16384 x 7168 takes
   // few and is the same with either limit.)
   GrParams p{};
   double least = 1e300;

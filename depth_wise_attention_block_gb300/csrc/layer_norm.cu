@@ -15,10 +15,13 @@
 // read once per pass by ln_any_kernel; what this saves, 16384 x 7168 bf16: 228
 // us there, 81 here (5.8 TB/s, the copy runs at 6.8); backward of 8192 x 7168:
 // 426 and 76 us (4.7 TB/s; 69 without the gain and bias gradients, whose
-// partial rows a second launch adds).  What bounds them now: the barriers of
-// the rows' sums (forward two a row, backward one for two rows), and backward
-// its issue slots: every pass unpacks x and dy again.  64 rows take the launch and one row's
-// chain of load, sums and store: 6.5 us between the calls of a program.
+// partial rows a second launch adds).  What bounds them now is latency at the
+// warps that the registers leave: forward 16 to an SM, 48 % of the issue slots
+// and 64 % of DRAM's cycles, backward 14, 50 % and 55 %.  They wait for their own
+// chains, for one another at the barriers of the rows' sums (forward two a row,
+// backward one for two rows) and for arithmetic that comes in bursts: every pass
+// unpacks x, and backward dy, again.  64 rows take the launch and one row's chain
+// of load, sums and store: 6.5 us between the calls of a program.
 #include <math.h>
 
 #include "attnres.h"

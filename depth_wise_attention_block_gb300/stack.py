@@ -405,7 +405,9 @@ class StackBackward:
         """The 2-norm [1] float32 of dW and the tensors of `others` (gradients of
         the same step, contiguous) taken as one vector, all of which are then
         clipped in place to max_norm (attnres_grad_clip).  dh0, the gradient
-        at the stack's input, flows on as it is unless it is among them."""
+        at the stack's input, flows on as it is unless it is among them.  The
+        norm's buffer and the workspace are this object's: the next call
+        overwrites them, and calls that overlap in time need one each."""
         attnres_grad_clip([self.dW, *others], max_norm, self.norm, workspace=self.clip_ws, stream=stream)
         return self.norm
 

@@ -731,7 +731,9 @@ int attnres_linear_attention_step(const void* q, int64_t q_stride, const void* k
  * eps         finite, >= 0
  * T >= 0 (0 launches nothing and accepts NULL buffers), d 1..2^24
  * (ATTNRES_ERANGE above).  Sums are fp32; the mean is held as two numbers, so
- * rows whose mean is far from zero keep their digits.
+ * rows whose mean is far from zero keep their digits.  Their squares have to
+ * lie within fp32: x - mean up to 1.8e19 / sqrt(d) (beyond it a row comes out as
+ * its bias, or NaN).  Infinities and NaN of a row reach no other row's result.
  * ---------------------------------------------------------------------- */
 int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dtype, const float* gain, const float* bias,
                        float eps, void* out, int64_t out_stride, void* stream);
@@ -742,7 +744,9 @@ int attnres_layer_norm(const void* x, int64_t x_stride, int64_t T, int d, int dt
  *   grad_x = (n - mean_c n - h mean_c(n h)) / sigma
  *   grad_gain[c] = sum_t grad_out h,   grad_bias[c] = sum_t grad_out
  * grad_out    device [T, d] of dtype, row stride given
- * grad_x      the same, or NULL to skip; it may be grad_out itself (same stride)
+ * grad_x      the same, or NULL to skip; it may be grad_out itself (same
+ *             stride).  Infinities and NaN of a row of x or grad_out reach no
+ *             other row of it.
  * grad_gain, grad_bias  device [d] fp32, overwritten, or NULL to skip; summed
  *             in fp32 in a fixed order (bit-reproducible)
  * workspace   device scratch, 256-byte aligned, of at least
@@ -786,7 +790,8 @@ int64_t attnres_layer_norm_backward_workspace_size(int64_t T, int d);
  *             another's spans; a wait that runs out (a bound of seconds) ORs
  *             ATTNRES_DEVERR_WAIT_TIMEOUT into *dev_err, and what depends on it
  *             is NaN
- * The state is held in fp32.  Either gate below -83 (minus infinity too)
+ * The state is held in fp32, and so is a_t (off by some 2^-22 of itself, which a
+ * memory of n tokens sees n times).  Either gate below -83 (minus infinity too)
  * counts as -83: a_t of 1e-36.  Infinities and NaN reach the tokens of their
  * channel and sequence behind them and no others (an infinite state may become
  * NaN).  The last bits of a result do not depend on how the rows lie in memory.

@@ -1,7 +1,7 @@
 """The gated recurrence over batches with padding ahead of the first sequence
 and behind the last, cut inside tiles: whatever the padding holds (NaN and
-infinities too), the sequences' results have the bits of the same rows without
-padding around them, and nothing is written to the padding's rows."""
+infinities too), the sequences' results have the same bits, and nothing is
+written to the padding's rows."""
 import pytest
 import torch
 
